@@ -12,6 +12,9 @@ Functions mirror the C names:
 * ``topk_ef_compress(grad, residual, lr, k)``            -> (idx, val)
 * ``topk_ef_compress_batched(grad, residual, offsets, k, lr)`` -> (idx, val)
 * ``gtopk_merge(in_idx, in_val, k, n)``                  -> (idx, val, count)
+* ``embedding_lookup(weight, ids, scale)``               -> out
+* ``embedding_grad(grad_out, ids, num_rows, scale)``     -> grad_weight
+* ``embedding_grad_rows(grad_out, ids, num_rows, scale)`` -> (rows, val, count)
 * ``topk_ef_workspace_bytes``, ``topk_ef_batched_workspace_bytes``,
   ``gtopk_merge_workspace_bytes``, ``topk_ef_last_device_status``,
   ``topk_ef_path_info``, ``topk_ef_set_test_flags``.
@@ -109,6 +112,20 @@ def lib() -> ctypes.CDLL:
         L.topk_ef_trace_read.restype = ctypes.c_int
         L.topk_ef_trace_only.argtypes = [ctypes.c_char_p, ctypes.c_int]
         L.topk_ef_trace_only.restype = ctypes.c_int
+        L.embedding_lookup_workspace_bytes.argtypes = []
+        L.embedding_lookup_workspace_bytes.restype = _sz
+        L.embedding_lookup.argtypes = [_vp, _i32, _i64, _vp, _i32, _i64, _i64, _i64,
+                                       ctypes.c_float, _vp, _i32, _i64, _vp, _sz, _vp]
+        L.embedding_lookup.restype = ctypes.c_int
+        L.embedding_grad_workspace_bytes.argtypes = [_i64, _i64, _i64]
+        L.embedding_grad_workspace_bytes.restype = _sz
+        L.embedding_grad.argtypes = [_vp, _i32, _i64, _vp, _i32, _i64, _i64, _i64, ctypes.c_float,
+                                     _i64, _vp, _i32, _i64, _i32, _vp, _sz, _vp]
+        L.embedding_grad.restype = ctypes.c_int
+        L.embedding_grad_rows.argtypes = [_vp, _i32, _i64, _vp, _i32, _i64, _i64, _i64,
+                                          ctypes.c_float, _i64, _vp, _vp, _i32, _i64, _vp, _vp,
+                                          _sz, _vp]
+        L.embedding_grad_rows.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -359,6 +376,186 @@ def gtopk_merge(in_idx, in_val, k, n, out_idx=None, out_val=None, out_count=None
                            ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
     _check(rc, "gtopk_merge")
     return out_idx, out_val, out_count
+
+
+# ----------------------------------------------------------------- embedding
+
+_TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _matrix(t, name: str, device=None):
+    """Element type code and row stride of a CUDA matrix whose rows are
+    contiguous (the rows themselves may be apart)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _TYPE:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    ld = t.stride(0) if rows > 1 else cols
+    if ld < cols:
+        raise ValueError(f"the rows of {name} overlap")
+    return _TYPE[t.dtype], ld
+
+
+def _token_ids(ids, device):
+    if not isinstance(ids, torch.Tensor) or not ids.is_cuda or not ids.is_contiguous() \
+            or ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("ids must be a contiguous int32 or int64 CUDA tensor")
+    if ids.device != device:
+        raise ValueError(f"ids is on {ids.device}, not on {device}")
+    return ids.element_size(), ids.numel()
+
+
+class _On:
+    """Makes a tensor's device current for a call and names the stream that
+    the call and what it allocates belong to."""
+
+    def __init__(self, device, stream):
+        self.dev = device
+        self.stream = stream
+        self.guard = None
+
+    def __enter__(self):
+        if self.stream is not None:
+            if self.stream.device != self.dev:
+                raise ValueError(f"the stream is on {self.stream.device}, not on {self.dev}")
+            self.guard = torch.cuda.stream(self.stream)      # its device too
+        elif self.dev.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.dev)
+        if self.guard is not None:
+            self.guard.__enter__()
+        return int((self.stream or torch.cuda.current_stream()).cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _on_device(ws, device):
+    if ws is not None and ws.device != device:
+        raise ValueError(f"ws is on {ws.device}, not on {device}")
+
+
+def embedding_lookup_workspace_bytes() -> int:
+    return int(lib().embedding_lookup_workspace_bytes())
+
+
+def embedding_lookup(weight, ids, scale=1.0, out=None, out_dtype=None, ws=None, stream=None):
+    """out[..., :] = scale * weight[ids[...], :], the product in fp32 and
+    rounded once.  weight: [V, D] float32 / bfloat16 / float16 with contiguous
+    rows; ids: int32 / int64 of any shape; out: [*ids.shape, D] (or [T, D]) in
+    any of the types (default: the weight's).  An id outside [0, V) gives a
+    row of zeros and ERR_BAD_INPUT from topk_ef_last_device_status(ws)."""
+    wt, ldw = _matrix(weight, "weight")
+    dev = weight.device
+    idb, T = _token_ids(ids, dev)
+    V, D = weight.shape
+    _on_device(ws, dev)
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty((*ids.shape, D), dtype=out_dtype or weight.dtype, device=dev)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out and out_dtype differ")
+        o2 = out if out.dim() == 2 else out.view(-1, D) if out.numel() else out.new_empty((T, D))
+        ot, ldo = _matrix(o2, "out", dev)
+        if tuple(o2.shape) != (T, D):
+            raise ValueError(f"out must hold [{T}, {D}] elements")
+        ws = _workspace(embedding_lookup_workspace_bytes(), dev, ws)
+        rc = lib().embedding_lookup(weight.data_ptr(), wt, ldw, ids.data_ptr(), idb, T, V, D,
+                                    float(scale), o2.data_ptr(), ot, ldo, ws.data_ptr(),
+                                    ws.numel() * ws.element_size(), st)
+    _check(rc, "embedding_lookup")
+    return out
+
+
+def embedding_grad_workspace_bytes(T: int, V: int, D: int) -> int:
+    return int(lib().embedding_grad_workspace_bytes(int(T), int(V), int(D)))
+
+
+def _grad_args(grad_out, ids, num_rows):
+    if isinstance(grad_out, torch.Tensor) and grad_out.dim() != 2 and grad_out.dim() > 0:
+        D = grad_out.shape[-1]
+        grad_out = grad_out.view(-1, D) if grad_out.numel() else grad_out.new_empty((ids.numel(), D))
+    gt, ldg = _matrix(grad_out, "grad_out")
+    dev = grad_out.device
+    idb, T = _token_ids(ids, dev)
+    if grad_out.shape[0] != T:
+        raise ValueError("grad_out must hold one row for each id")
+    V, D = int(num_rows), grad_out.shape[1]
+    nb = embedding_grad_workspace_bytes(T, V, D)
+    if nb == 0:
+        raise TopkEfError(ERR_INVALID_ARG, "embedding_grad_workspace_bytes")
+    return grad_out, gt, ldg, dev, idb, T, V, D, nb
+
+
+def embedding_grad(grad_out, ids, num_rows, scale=1.0, padding_idx=-1, accumulate=False, out=None,
+                   out_dtype=None, ws=None, stream=None):
+    """Gradient of embedding_lookup with respect to its weight:
+    out[v] = (out[v] if accumulate else 0) + scale * sum of grad_out[t] over
+    ids[t] == v, summed in fp32 in a fixed order and rounded once.  grad_out:
+    [*ids.shape, D]; out: [num_rows, D] (default float32, the type that
+    topk_ef_compress reads).  Positions whose id is padding_idx contribute
+    nothing; other ids outside [0, num_rows) neither, and they give
+    ERR_BAD_INPUT from topk_ef_last_device_status(ws)."""
+    grad_out, gt, ldg, dev, idb, T, V, D, nb = _grad_args(grad_out, ids, num_rows)
+    _on_device(ws, dev)
+    with _On(dev, stream) as st:
+        if out is None:
+            if accumulate:
+                raise ValueError("accumulate needs out")
+            out = torch.empty((V, D), dtype=out_dtype or torch.float32, device=dev)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out and out_dtype differ")
+        ot, ldo = _matrix(out, "out", dev)
+        if tuple(out.shape) != (V, D):
+            raise ValueError(f"out must be [{V}, {D}]")
+        ws = _workspace(nb, dev, ws)
+        rc = lib().embedding_grad(grad_out.data_ptr(), gt, ldg, ids.data_ptr(), idb, T, V, D,
+                                  float(scale), int(padding_idx), out.data_ptr(), ot, ldo,
+                                  1 if accumulate else 0, ws.data_ptr(),
+                                  ws.numel() * ws.element_size(), st)
+    _check(rc, "embedding_grad")
+    return out
+
+
+def embedding_grad_rows(grad_out, ids, num_rows, scale=1.0, padding_idx=-1, out_rows=None,
+                        out_val=None, out_count=None, out_dtype=None, ws=None, stream=None):
+    """The gradient of embedding_grad as a row-sparse set: the distinct ids in
+    ascending order (padding_idx left out), the gradient row of each, and
+    their number.  Returns (rows int32[m], val [m, D], count int32[1]) with
+    m = min(T, num_rows); slots from the count on are not written."""
+    grad_out, gt, ldg, dev, idb, T, V, D, nb = _grad_args(grad_out, ids, num_rows)
+    _on_device(ws, dev)
+    m = min(T, V)
+    with _On(dev, stream) as st:
+        if out_rows is None:
+            out_rows = torch.empty(m, dtype=torch.int32, device=dev)
+        if out_val is None:
+            out_val = torch.empty((m, D), dtype=out_dtype or torch.float32, device=dev)
+        elif out_dtype is not None and out_val.dtype != out_dtype:
+            raise ValueError("out_val and out_dtype differ")
+        if out_count is None:
+            out_count = torch.empty(1, dtype=torch.int32, device=dev)
+        for t, name, least in ((out_rows, "out_rows", m), (out_count, "out_count", 1)):
+            if not t.is_cuda or t.device != dev or t.dtype != torch.int32 or \
+                    not t.is_contiguous() or t.numel() < least:
+                raise ValueError(f"{name} must be a contiguous int32 tensor of {least} on {dev}")
+        ot, ldo = _matrix(out_val, "out_val", dev)
+        if out_val.shape[0] < m or out_val.shape[1] != D:
+            raise ValueError(f"out_val must be [{m}, {D}]")
+        ws = _workspace(nb, dev, ws)
+        rc = lib().embedding_grad_rows(grad_out.data_ptr(), gt, ldg, ids.data_ptr(), idb, T, V, D,
+                                       float(scale), int(padding_idx), out_rows.data_ptr(),
+                                       out_val.data_ptr(), ot, ldo, out_count.data_ptr(),
+                                       ws.data_ptr(), ws.numel() * ws.element_size(), st)
+    _check(rc, "embedding_grad_rows")
+    return out_rows, out_val, out_count
 
 
 # -------------------------------------------------------------------- status

@@ -11,7 +11,7 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRC = os.path.join(HERE, "csrc", "topk_ef.cu")
+SRCS = [os.path.join(HERE, "csrc", f) for f in ("topk_ef.cu", "embedding.cu")]
 DEPS = sorted(glob.glob(os.path.join(HERE, "csrc", "*.cu*"))) + [
     os.path.join(ROOT, "include", "topk_ef.h")]
 LIB = os.path.join(HERE, "libtopk_ef.so")
@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libtopk_ef.so")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC", "-shared", "--threads", "0",
     "--ftz=false", "--prec-div=true", "--prec-sqrt=true", "--fmad=false",
 ]
 
@@ -41,7 +41,7 @@ def stale() -> bool:
 def build(verbose: bool = False, force: bool = False) -> str:
     if not force and not stale():
         return LIB
-    cmd = [nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", LIB, SRC]
+    cmd = [nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", LIB, *SRCS]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
         print(" ".join(cmd), file=sys.stderr)

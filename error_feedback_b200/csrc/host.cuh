@@ -1,0 +1,41 @@
+// Host helpers shared by the translation units of the C ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace tke {
+
+constexpr int64_t MAX_N = 2147483647LL;
+constexpr size_t ALIGN = 256;
+
+inline size_t align_up(size_t x, size_t a = ALIGN) { return (x + a - 1) / a * a; }
+
+// Records the error for topk_ef_last_cuda_error; returns TOPK_EF_ERR_CUDA.
+int cuda_fail(cudaError_t e);
+
+// Bracket a kernel launch for the tracing calls.
+void trace_before(cudaStream_t st, const char* name);
+void trace_after(cudaStream_t st);
+
+// Launch with programmatic stream serialisation: the kernel may be scheduled
+// while the previous kernel on the stream is still running, and waits for it
+// (griddepcontrol.wait) before touching anything that kernel produces.
+template <typename Kern, typename Arg>
+cudaError_t launch_pdl(Kern kernel, dim3 grid, int block, cudaStream_t st, const Arg& arg,
+                       size_t smem = 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, arg);
+}
+
+}  // namespace tke

@@ -1,0 +1,582 @@
+// Embedding lookup with scaling, and its gradient by sorted tokens.
+//
+//   lookup:  out[t, :] = round(scale * W[id_t, :])
+//   grad:    g[v, :]   = (accumulate ? g[v, :] : 0) + scale * sum_{t: id_t = v} dy[t, :]
+//
+// The gradient sorts the positions by id (stable, so the positions of one id
+// stay in ascending order), cuts the sorted list into tiles of `C` positions
+// and sums runs of equal ids inside each tile; a run that crosses tiles
+// leaves one fp32 partial row per tile, which a last kernel adds in tile
+// order.  The work of a tile does not depend on how often an id occurs, and
+// the order of every sum is a function of the sizes alone: no floating-point
+// atomics, results bit-identical from run to run.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace tke {
+
+// ------------------------------------------------------------ element types
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+
+// One rounding to nearest even: what an fp32 result becomes in the output type.
+template <typename T> __device__ __forceinline__ T from_f32(float x);
+template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
+    return __float2bfloat16_rn(x);
+}
+template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+
+// Eight consecutive elements; p is 16-byte aligned.
+template <typename T>
+struct Vec8 {
+    uint4 q[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Vec8<T> load8(const T* p) {
+    Vec8<T> v;
+    const uint4* s = reinterpret_cast<const uint4*>(p);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) v.q[i] = __ldg(s + i);
+    return v;
+}
+template <typename T>
+__device__ __forceinline__ float elem8(const Vec8<T>& v, int j) {
+    return to_f32(reinterpret_cast<const T*>(&v)[j]);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float* x) {
+    Vec8<T> v;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) reinterpret_cast<T*>(&v)[j] = from_f32<T>(x[j]);
+    uint4* d = reinterpret_cast<uint4*>(p);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) d[i] = v.q[i];
+}
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;"); }
+
+// ------------------------------------------------------------------- lookup
+
+constexpr int LK_THREADS = 128;
+constexpr int LK_COLS = 1024;          // columns of one warp's item
+constexpr int64_t LK_SCAN_T = 8192;    // up to here one block checks every id
+
+struct LookupParams {
+    const void* w;
+    const void* ids;
+    void* out;
+    Ctrl* ctrl;
+    int64_t T, V, D, ldw, ldo;
+    int64_t items;                 // T * ceil(D / LK_COLS)
+    int32_t chunks;                // ceil(D / LK_COLS)
+    int32_t scan;                  // the last block checks the ids and writes the status
+    float scale;
+};
+
+// One warp per (token, LK_COLS columns): bound by the bytes of the rows read
+// and written.  VEC: rows start on 16-byte boundaries on both sides.
+template <typename TW, typename TO, typename TI, bool VEC>
+__global__ void __launch_bounds__(LK_THREADS) lookup_kernel(const LookupParams p) {
+    pdl_launch();
+    pdl_wait();
+    const TI* __restrict__ ids = static_cast<const TI*>(p.ids);
+    int nblocks = (int)gridDim.x;
+    if (p.scan) {
+        --nblocks;
+        if ((int)blockIdx.x == nblocks) {
+            int bad = 0;
+            for (int64_t t = threadIdx.x; t < p.T; t += LK_THREADS) {
+                const int64_t id = (int64_t)ids[t];
+                bad |= (id < 0 || id >= p.V);
+            }
+            bad = __syncthreads_or(bad);
+            if (threadIdx.x == 0) {
+                p.ctrl->path_small = 0;
+                p.ctrl->status = bad ? ST_BAD_INPUT : 0u;
+            }
+            return;
+        }
+    }
+    const TW* __restrict__ w = static_cast<const TW*>(p.w);
+    TO* __restrict__ out = static_cast<TO*>(p.out);
+    const int lane = (int)lane_id();
+    const int64_t stride = (int64_t)nblocks * (LK_THREADS / 32);
+    for (int64_t it = (int64_t)blockIdx.x * (LK_THREADS / 32) + warp_id(); it < p.items;
+         it += stride) {
+        const int64_t t = it / p.chunks;
+        const int64_t c0 = (it - t * p.chunks) * LK_COLS;
+        const int64_t id = (int64_t)ids[t];
+        const bool ok = id >= 0 && id < p.V;
+        if (!ok && !p.scan && lane == 0) atomicOr(&p.ctrl->status, ST_BAD_INPUT);
+        const TW* src = w + (ok ? id : 0) * p.ldw;
+        TO* dst = out + t * p.ldo;
+        if (VEC) {
+            Vec8<TW> v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t c = c0 + j * 256 + lane * 8;
+                if (ok && c + 8 <= p.D) v[j] = load8(src + c);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t c = c0 + j * 256 + lane * 8;
+                if (c + 8 <= p.D) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = ok ? p.scale * elem8(v[j], e) : 0.0f;
+                    store8(dst + c, x);
+                } else {
+                    for (int64_t k = c; k < p.D; ++k)
+                        dst[k] = from_f32<TO>(ok ? p.scale * to_f32(src[k]) : 0.0f);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j0 = 0; j0 < 32; j0 += 8) {
+                TW v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int64_t c = c0 + (j0 + j) * 32 + lane;
+                    if (ok && c < p.D) v[j] = src[c];
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int64_t c = c0 + (j0 + j) * 32 + lane;
+                    if (c < p.D) dst[c] = from_f32<TO>(ok ? p.scale * to_f32(v[j]) : 0.0f);
+                }
+            }
+        }
+    }
+}
+
+// ----------------------------------------------------- sort of the positions
+
+// Least-significant-digit radix sort of (key, position), 9 bits a pass:
+// counting and scattering kernels over tiles of 4,096 keys.  A key is the id,
+// or V (which sorts last) for the padding id and for ids outside [0, V).
+constexpr int ES_BITS = 9;
+constexpr int ES_BINS = 1 << ES_BITS;
+constexpr int ES_THREADS = 512;
+constexpr int ES_WARPS = ES_THREADS / 32;
+constexpr int ES_TILE = 4096;
+constexpr int ES_ROUNDS = ES_TILE / ES_THREADS;     // keys per thread
+constexpr int ES_SCAN_TILES = 32;                   // more tiles: prefixes by their own kernel
+static_assert(ES_BINS == ES_THREADS, "one thread per bin");
+
+struct SortParams {
+    const void* ids;               // first pass
+    const uint32_t* key_in;        // later passes
+    const uint32_t* pos_in;
+    uint32_t* key_out;
+    uint32_t* pos_out;
+    uint32_t* counts;              // [tiles][ES_BINS]
+    uint32_t* totals;              // [ES_BINS], when the prefixes are scanned ahead
+    uint32_t* bitmap;              // ids that occur (first pass), or null
+    uint32_t* word_prefix;         // ids that occur below each bitmap word (first pass), or null
+    int32_t* out_count;            // their number (with word_prefix)
+    Ctrl* ctrl;
+    int64_t T, V, padding;
+    int32_t tiles, shift, scanned;
+};
+
+template <typename TI>
+__device__ __forceinline__ uint32_t sort_key(const TI* ids, int64_t t, int64_t V, int64_t padding,
+                                             bool& bad) {
+    const int64_t id = (int64_t)ids[t];
+    const bool out = id < 0 || id >= V;
+    bad = out && id != padding;
+    return (out || id == padding) ? (uint32_t)V : (uint32_t)id;
+}
+
+template <typename TI, bool FIRST>
+__global__ void __launch_bounds__(ES_THREADS) sort_count_kernel(const SortParams p) {
+    __shared__ uint32_t hist[ES_BINS];
+    pdl_launch();
+    hist[threadIdx.x] = 0;
+    pdl_wait();
+    __syncthreads();
+    const int64_t base = (int64_t)blockIdx.x * ES_TILE;
+#pragma unroll
+    for (int r = 0; r < ES_ROUNDS; ++r) {
+        const int64_t t = base + r * ES_THREADS + threadIdx.x;
+        if (t < p.T) {
+            uint32_t key;
+            if (FIRST) {
+                bool bad;
+                key = sort_key(static_cast<const TI*>(p.ids), t, p.V, p.padding, bad);
+                if (bad) atomicOr(&p.ctrl->status, ST_BAD_INPUT);
+                if (p.bitmap && key < (uint32_t)p.V) {
+                    const uint32_t bit = 1u << (key & 31);
+                    if (!(__ldcg(&p.bitmap[key >> 5]) & bit)) atomicOr(&p.bitmap[key >> 5], bit);
+                }
+            } else {
+                key = p.key_in[t];
+            }
+            atomicAdd(&hist[(key >> p.shift) & (ES_BINS - 1)], 1u);
+        }
+    }
+    __syncthreads();
+    p.counts[(int64_t)blockIdx.x * ES_BINS + threadIdx.x] = hist[threadIdx.x];
+}
+
+// counts -> exclusive prefixes over the tiles (in place) and totals, per bin;
+// one block per 32 bins, its 32 warps over ranges of tiles.
+__global__ void __launch_bounds__(1024) sort_prefix_kernel(const SortParams p) {
+    __shared__ uint32_t part[32][33];
+    pdl_launch();
+    pdl_wait();
+    const int bin = (int)blockIdx.x * 32 + (int)lane_id();
+    const int per = (p.tiles + 31) / 32;
+    const int t0 = min(p.tiles, (int)warp_id() * per), t1 = min(p.tiles, t0 + per);
+    uint32_t s = 0;
+    for (int t = t0; t < t1; ++t) s += p.counts[(int64_t)t * ES_BINS + bin];
+    part[warp_id()][lane_id()] = s;
+    __syncthreads();
+    uint32_t run = 0;
+    for (int w = 0; w < (int)warp_id(); ++w) run += part[w][lane_id()];
+    for (int t = t0; t < t1; ++t) {
+        const uint32_t c = p.counts[(int64_t)t * ES_BINS + bin];
+        p.counts[(int64_t)t * ES_BINS + bin] = run;
+        run += c;
+    }
+    if (warp_id() == 31) p.totals[bin] = run;
+}
+
+// Number of ids that occur below every 32-id word of the bitmap, and in all.
+__device__ __forceinline__ void bitmap_prefix(const SortParams& p, uint32_t* s_red) {
+    const int64_t words = ceil_div64(p.V, 32);
+    uint32_t run = 0;
+    for (int64_t w0 = 0; w0 < words; w0 += ES_THREADS) {
+        const int64_t w = w0 + threadIdx.x;
+        const uint32_t c = w < words ? (uint32_t)__popc(__ldcg(&p.bitmap[w])) : 0u;
+        uint32_t tot;
+        const uint32_t ex = block_excl_scan(c, s_red, &tot);
+        if (w < words) p.word_prefix[w] = run + ex;
+        run += tot;
+    }
+    if (threadIdx.x == 0) *p.out_count = (int32_t)run;
+}
+
+// Stable scatter of one tile: the place of a key is the number of keys with a
+// smaller digit, plus those of the same digit in earlier tiles, in earlier
+// warps (each warp has a contiguous 256 keys) and earlier in this warp.
+template <typename TI, bool FIRST>
+__global__ void __launch_bounds__(ES_THREADS) sort_scatter_kernel(const SortParams p) {
+    __shared__ uint32_t hist[ES_WARPS][ES_BINS];
+    __shared__ uint32_t s_red[33];
+    pdl_launch();
+    const int tid = (int)threadIdx.x, lane = (int)lane_id(), warp = (int)warp_id();
+#pragma unroll
+    for (int w = 0; w < ES_WARPS; ++w) hist[w][tid] = 0;
+    pdl_wait();
+    if (FIRST && (int)blockIdx.x == p.tiles) {
+        bitmap_prefix(p, s_red);
+        return;
+    }
+    __syncthreads();
+    const int64_t base = (int64_t)blockIdx.x * ES_TILE + warp * (ES_TILE / ES_WARPS);
+    uint32_t key[ES_ROUNDS], pos[ES_ROUNDS], rank[ES_ROUNDS];
+#pragma unroll
+    for (int r = 0; r < ES_ROUNDS; ++r) {
+        const int64_t t = base + r * 32 + lane;
+        key[r] = 0;
+        pos[r] = (uint32_t)t;
+        if (t < p.T) {
+            if (FIRST) {
+                bool bad;
+                key[r] = sort_key(static_cast<const TI*>(p.ids), t, p.V, p.padding, bad);
+            } else {
+                key[r] = p.key_in[t];
+                pos[r] = p.pos_in[t];
+            }
+        }
+    }
+    // first place of this thread's bin among this tile's keys
+    uint32_t before = 0, total = 0;
+    if (p.scanned) {
+        before = p.counts[(int64_t)blockIdx.x * ES_BINS + tid];
+        total = p.totals[tid];
+    } else {
+#pragma unroll 8
+        for (int t = 0; t < p.tiles; ++t) {
+            const uint32_t c = p.counts[t * ES_BINS + tid];
+            total += c;
+            before += t < (int)blockIdx.x ? c : 0u;
+        }
+    }
+    uint32_t all;
+    before += block_excl_scan(total, s_red, &all);
+#pragma unroll
+    for (int r = 0; r < ES_ROUNDS; ++r) {
+        const bool live = base + r * 32 + lane < p.T;
+        const uint32_t act = __ballot_sync(0xFFFFFFFFu, live);
+        if (live) {
+            const uint32_t d = (key[r] >> p.shift) & (ES_BINS - 1);
+            const uint32_t peers = __match_any_sync(act, d);
+            const int leader = __ffs(peers) - 1;
+            uint32_t had = 0;
+            if (lane == leader) {
+                had = hist[warp][d];
+                hist[warp][d] = had + (uint32_t)__popc(peers);
+            }
+            had = __shfl_sync(peers, had, leader);
+            rank[r] = had + (uint32_t)__popc(peers & ((1u << lane) - 1u));
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < ES_WARPS; ++w) {
+        const uint32_t c = hist[w][tid];
+        hist[w][tid] = before;
+        before += c;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < ES_ROUNDS; ++r) {
+        if (base + r * 32 + lane < p.T) {
+            const uint32_t at = hist[warp][(key[r] >> p.shift) & (ES_BINS - 1)] + rank[r];
+            p.key_out[at] = key[r];
+            p.pos_out[at] = pos[r];
+        }
+    }
+}
+
+// ------------------------------------------------------------------ the sums
+
+constexpr int EG_THREADS = 128;
+constexpr int EG_COLS = EG_THREADS * 8;    // columns of one block
+constexpr int EG_MAX_C = 128;              // positions of one tile, at most
+constexpr int64_t EG_FILL_BYTES = 32768;   // zeros written by one fill block
+
+struct GradParams {
+    const void* dy;
+    void* out;
+    const uint32_t* key;           // sorted
+    const uint32_t* pos;
+    const uint32_t* bitmap;
+    const uint32_t* word_prefix;   // row-sparse output: ordinals
+    int32_t* out_rows;             // row-sparse output, or null
+    float* head;                   // [tiles][Dp]: run continued from the tile before
+    float* tail;                   // [tiles][Dp]: run begun here that goes on in the next
+    uint32_t* list;                // tiles whose tail goes on
+    uint32_t* list_count;
+    int64_t T, V, D, Dp, ld_dy, ld_out;
+    int64_t tiles;
+    int64_t sum_blocks;            // tiles * slabs; the blocks after them fill with zeros
+    int64_t fill_rows;             // rows of one fill block
+    int32_t slabs, C;
+    int32_t accumulate;
+    float scale;
+};
+
+__device__ __forceinline__ int64_t out_row(const GradParams& p, uint32_t key) {
+    if (!p.out_rows) return (int64_t)key;
+    const uint32_t word = p.bitmap[key >> 5];
+    return (int64_t)p.word_prefix[key >> 5] + __popc(word & ((1u << (key & 31)) - 1u));
+}
+
+template <typename TO, bool VEC>
+__device__ __forceinline__ void fill_block(const GradParams& p, int64_t f) {
+    TO* out = static_cast<TO*>(p.out);
+    const int64_t r0 = f * p.fill_rows, r1 = min(p.V, r0 + p.fill_rows);
+    for (int64_t v = r0 + warp_id(); v < r1; v += EG_THREADS / 32) {
+        if (p.bitmap[v >> 5] >> (v & 31) & 1u) continue;
+        TO* dst = out + v * p.ld_out;
+        if (VEC) {
+            const float z[8] = {};
+            for (int64_t c = lane_id() * 8; c < p.D; c += 256) {
+                if (c + 8 <= p.D) {
+                    store8(dst + c, z);
+                } else {
+                    for (int64_t k = c; k < p.D; ++k) dst[k] = from_f32<TO>(0.0f);
+                }
+            }
+        } else {
+            for (int64_t c = lane_id(); c < p.D; c += 32) dst[c] = from_f32<TO>(0.0f);
+        }
+    }
+}
+
+// One block per (tile of C sorted positions, EG_COLS columns); thread j has 8
+// columns: consecutive ones (VEC: rows on 16-byte boundaries), else one in
+// every EG_THREADS.  Bound by the rows of dy read and the rows written.
+template <typename TD, typename TO, bool VEC>
+__global__ void __launch_bounds__(EG_THREADS) grad_sum_kernel(const GradParams p) {
+    __shared__ uint32_t s_key[EG_MAX_C + 2], s_pos[EG_MAX_C];
+    pdl_launch();
+    pdl_wait();
+    const int tid = (int)threadIdx.x;
+    if ((int64_t)blockIdx.x >= p.sum_blocks) {
+        fill_block<TO, VEC>(p, (int64_t)blockIdx.x - p.sum_blocks);
+        return;
+    }
+    const int64_t tile = (int64_t)blockIdx.x / p.slabs;
+    const int64_t slab = (int64_t)blockIdx.x - tile * p.slabs;
+    const int64_t start = tile * p.C;
+    const int n = (int)min((int64_t)p.C, p.T - start);
+    const uint32_t none = (uint32_t)p.V;       // key of positions that do not count
+    for (int i = tid; i < n + 2; i += EG_THREADS) {
+        const int64_t t = start + i - 1;
+        s_key[i] = (t >= 0 && t < p.T) ? p.key[t] : 0xFFFFFFFFu;
+        if (i < n) s_pos[i] = p.pos[start + i];
+    }
+    __syncthreads();
+    const TD* __restrict__ dy = static_cast<const TD*>(p.dy);
+    const int64_t c0 = slab * EG_COLS + (VEC ? tid * 8 : tid);
+    auto col = [&](int j) { return c0 + (VEC ? j : j * EG_THREADS); };
+    const bool whole = col(7) < p.D;
+    float acc[8] = {};
+
+    auto flush = [&](int i, bool first, bool goes_on) {   // the run that ends at position i
+        const uint32_t k = s_key[i + 1];
+        const bool from_before = first && s_key[0] == k;
+        if (from_before || goes_on) {
+            float* part = (from_before ? p.head : p.tail) + tile * p.Dp;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (whole || col(j) < p.D) part[col(j)] = acc[j];
+            if (!from_before && slab == 0 && tid == 0)
+                p.list[atomicAdd(p.list_count, 1u)] = (uint32_t)tile;
+        } else {
+            const int64_t row = out_row(p, k);
+            TO* dst = static_cast<TO*>(p.out) + row * p.ld_out;
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = p.scale * acc[j];
+            if (VEC && whole) {
+                if (p.accumulate) {
+                    const Vec8<TO> o = load8(dst + c0);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] += elem8(o, j);
+                }
+                store8(dst + c0, y);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (col(j) < p.D)
+                        dst[col(j)] = from_f32<TO>(p.accumulate ? to_f32(dst[col(j)]) + y[j] : y[j]);
+            }
+            if (p.out_rows && slab == 0 && tid == 0) p.out_rows[row] = (int32_t)k;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+    };
+
+    bool first = true;
+    int i = 0;
+    constexpr int U = 4;                       // rows in flight
+    for (; i < n; i += U) {
+        if (s_key[i + 1] == none) break;
+        Vec8<TD> v[U];
+        TD sv[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i + u >= n || s_key[i + u + 1] == none) continue;
+            const TD* src = dy + (int64_t)s_pos[i + u] * p.ld_dy;
+            if (VEC) {
+                if (whole) {
+                    v[u] = load8(src + c0);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        reinterpret_cast<TD*>(&v[u])[j] =
+                            col(j) < p.D ? src[col(j)] : from_f32<TD>(0.0f);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    sv[u][j] = col(j) < p.D ? src[col(j)] : from_f32<TD>(0.0f);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i + u >= n || s_key[i + u + 1] == none) continue;
+            if (i + u > 0 && s_key[i + u + 1] != s_key[i + u]) {
+                flush(i + u - 1, first, false);
+                first = false;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] += VEC ? elem8(v[u], j) : to_f32(sv[u][j]);
+        }
+    }
+    // the last run of positions that count
+    int m = n;
+    while (m > 0 && s_key[m] == none) --m;
+    if (m > 0) flush(m - 1, first, s_key[m] == s_key[m + 1]);
+}
+
+constexpr int EC_THREADS = 256;
+constexpr int EC_COLS = 128;           // columns of one item: 32 lanes x 4
+
+// Adds the partial rows of every run that crosses tiles: tail of the tile it
+// begins in, then the heads of the following tiles.  The warps take
+// contiguous parts of the list in order, and their sums are added in order.
+template <typename TO>
+__global__ void __launch_bounds__(EC_THREADS) grad_combine_kernel(const GradParams p) {
+    __shared__ float4 s_part[EC_THREADS / 32][32];
+    pdl_launch();
+    pdl_wait();
+    const int lane = (int)lane_id(), warp = (int)warp_id();
+    constexpr int W = EC_THREADS / 32;
+    const int64_t slabs = max((int64_t)1, ceil_div64(p.D, EC_COLS));
+    const int64_t items = (int64_t)*p.list_count * slabs;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const int64_t tile = p.list[it / slabs];
+        const int64_t c = (it % slabs) * EC_COLS + lane * 4;
+        const uint32_t k = p.key[(tile + 1) * p.C - 1];
+        // last position of the run: upper bound of its key
+        int64_t lo = (tile + 1) * p.C, hi = p.T;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (p.key[mid] <= k) lo = mid + 1; else hi = mid;
+        }
+        const int64_t parts = (lo - 1) / p.C - tile + 1;
+        const int64_t per = ceil_div64(parts, W);
+        const int64_t j0 = min(parts, warp * per), j1 = min(parts, j0 + per);
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < p.D) {
+#pragma unroll 4
+            for (int64_t j = j0; j < j1; ++j) {
+                const float* part = (j == 0 ? p.tail : p.head) + (tile + j) * p.Dp + c;
+                const float4 x = *reinterpret_cast<const float4*>(part);
+                s.x += x.x;
+                s.y += x.y;
+                s.z += x.z;
+                s.w += x.w;
+            }
+        }
+        s_part[warp][lane] = s;
+        __syncthreads();
+        if (warp == 0 && c < p.D) {
+            const int used = (int)ceil_div64(parts, per);
+            for (int w = 1; w < used; ++w) {
+                const float4 x = s_part[w][lane];
+                s.x += x.x;
+                s.y += x.y;
+                s.z += x.z;
+                s.w += x.w;
+            }
+            const float y[4] = {p.scale * s.x, p.scale * s.y, p.scale * s.z, p.scale * s.w};
+            const int64_t row = out_row(p, k);
+            TO* dst = static_cast<TO*>(p.out) + row * p.ld_out;
+            for (int j = 0; j < 4; ++j)
+                if (c + j < p.D)
+                    dst[c + j] = from_f32<TO>(p.accumulate ? to_f32(dst[c + j]) + y[j] : y[j]);
+            if (p.out_rows && c == 0) p.out_rows[row] = (int32_t)k;
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace tke

@@ -30,6 +30,7 @@
 
 #include "topk_ef.h"
 #include "common.cuh"
+#include "host.cuh"
 #include "kernels_compress.cuh"
 #include "kernels_stream.cuh"
 #include "kernels_merge.cuh"
@@ -46,17 +47,17 @@ namespace {
 thread_local int t_last_cuda_error = 0;
 std::atomic<int> g_test_flags{0};
 
-constexpr int64_t MAX_N = 2147483647LL;
 constexpr int SLOT_MAX = 2048;         // select grid never exceeds this
-constexpr size_t ALIGN = 256;
 constexpr int MAX_MERGE_P = 2 * SEG_MAX;   // pairs per round <= SEG_MAX
 
-size_t align_up(size_t x, size_t a = ALIGN) { return (x + a - 1) / a * a; }
+}  // namespace
 
-int cuda_fail(cudaError_t e) {
+int tke::cuda_fail(cudaError_t e) {
     t_last_cuda_error = (int)e;
     return TOPK_EF_ERR_CUDA;
 }
+
+namespace {
 
 // ------------------------------------------------------------------ tracing
 // When enabled, every kernel launch (or only those of one kernel) is
@@ -79,7 +80,9 @@ struct Trace {
 Trace g_trace;
 std::mutex g_trace_mu;
 
-void trace_before(cudaStream_t st, const char* name) {
+}  // namespace
+
+void tke::trace_before(cudaStream_t st, const char* name) {
     g_trace.open = false;
     if (!g_trace.on || g_trace.n >= TRACE_MAX) return;
     if (!g_trace.only.empty() && g_trace.only != name) return;
@@ -89,12 +92,14 @@ void trace_before(cudaStream_t st, const char* name) {
     g_trace.open = true;
 }
 
-void trace_after(cudaStream_t st) {
+void tke::trace_after(cudaStream_t st) {
     if (!g_trace.open) return;
     g_trace.open = false;
     cudaEventRecord(g_trace.ev[2 * g_trace.n + 1], st);
     ++g_trace.n;
 }
+
+namespace {
 
 // ------------------------------------------------------------ device facts
 
@@ -158,24 +163,6 @@ int device_facts(DevFacts* out) {
     }
     *out = g_facts[dev];
     return TOPK_EF_OK;
-}
-
-// Launch with programmatic stream serialisation: the kernel may be scheduled
-// while the previous kernel on the stream is still running, and waits for it
-// (griddepcontrol.wait) before touching anything that kernel produces.
-template <typename Kern, typename Arg>
-cudaError_t launch_pdl(Kern kernel, int grid, int block, cudaStream_t st, const Arg& arg) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = 0;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, arg);
 }
 
 // ------------------------------------------------------- compress planning
@@ -1358,7 +1345,7 @@ const char* topk_ef_status_string(int status) {
         case TOPK_EF_ERR_WORKSPACE: return "workspace too small";
         case TOPK_EF_ERR_CUDA: return "CUDA error";
         case TOPK_EF_ERR_DEVICE_TIMEOUT: return "device wait timed out";
-        case TOPK_EF_ERR_BAD_INPUT: return "malformed merge input";
+        case TOPK_EF_ERR_BAD_INPUT: return "malformed merge input or embedding ids";
         case TOPK_EF_ERR_INTERNAL: return "internal count mismatch";
         default: return "unknown status";
     }

@@ -69,7 +69,8 @@ extern "C" {
 #define TOPK_EF_ERR_CUDA (-3)
 /* device: a bounded spin-wait gave up (outputs are undefined) */
 #define TOPK_EF_ERR_DEVICE_TIMEOUT (-4)
-/* device: merge input rows not strictly ascending or indices outside [0, n) */
+/* device: merge input rows not strictly ascending or indices outside [0, n),
+   embedding ids outside [0, V) */
 #define TOPK_EF_ERR_BAD_INPUT (-5)
 /* device: an internal count did not add up (outputs are undefined) */
 #define TOPK_EF_ERR_INTERNAL (-6)
@@ -292,6 +293,89 @@ size_t topk_allgather_workspace_bytes(int32_t P, int64_t k_in, int64_t n);
 int topk_allgather_sum(const int32_t* in_idx, const float* in_val, int32_t P,
                        int64_t k_in, int64_t n, float* out, void* ws,
                        size_t ws_bytes, void* stream);
+
+/* -------------------------------------------------------------- embedding */
+
+/* Element types of the calls below (the calls above are fp32 throughout). */
+#define TOPK_EF_F32 0
+#define TOPK_EF_BF16 1
+#define TOPK_EF_F16 2
+
+/* Workspace bytes for embedding_lookup (a status block). */
+size_t embedding_lookup_workspace_bytes(void);
+
+/*
+ * Embedding lookup with scaling, the forward pass of the layer whose gradient
+ * is row-sparse:
+ *     out[t][j] = round(scale * weight[ids[t]][j])     (fp32 product, one
+ *                                                       rounding to out_type)
+ *   weight     device, [V][ld_weight] of weight_type, the first D columns of
+ *              each row are read; rows on 16-byte boundaries take the
+ *              vectorised path (likewise out), others a path with identical
+ *              results
+ *   ids        device, int32[T] (id_bytes = 4) or int64[T] (id_bytes = 8)
+ *   out        device, [T][ld_out] of out_type; columns from D on are not
+ *              written; must not overlap weight
+ *   sizes      0 <= T, V <= 2^31 - 1; 0 <= D <= 2^24; ld_weight, ld_out >= D
+ *   ws         device workspace of >= embedding_lookup_workspace_bytes()
+ * An id outside [0, V) gives a row of zeros and TOPK_EF_ERR_BAD_INPUT through
+ * topk_ef_last_device_status(ws); no memory outside weight is read.
+ * Errors: TOPK_EF_ERR_INVALID_ARG (sizes, types, null or misaligned pointers),
+ * TOPK_EF_ERR_WORKSPACE, TOPK_EF_ERR_CUDA.
+ */
+int embedding_lookup(const void* weight, int32_t weight_type, int64_t ld_weight,
+                     const void* ids, int32_t id_bytes, int64_t T, int64_t V,
+                     int64_t D, float scale, void* out, int32_t out_type,
+                     int64_t ld_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes for embedding_grad and embedding_grad_rows; 0 for invalid
+   sizes. */
+size_t embedding_grad_workspace_bytes(int64_t T, int64_t V, int64_t D);
+
+/*
+ * Gradient of embedding_lookup with respect to weight, by sorted tokens:
+ *     grad_weight[v][j] = (accumulate ? grad_weight[v][j] : 0)
+ *                         + scale * sum over t with ids[t] = v of grad_out[t][j]
+ * The sums are held in fp32 and rounded once to grad_weight_type.  Their
+ * order depends on the sizes and ids alone (no floating-point atomics).
+ * With fp32 output the call writes straight into the bucket that
+ * topk_ef_compress and topk_ef_compress_batched read.
+ *   grad_out     device, [T][ld_grad_out] of grad_out_type
+ *   padding_idx  positions with this id contribute nothing (their row is zero,
+ *                or with accumulate left as it was); any value outside [0, V),
+ *                e.g. -1, for none
+ *   grad_weight  device, [V][ld_grad_weight]; without accumulate every row is
+ *                written, with it only the rows of ids that occur; columns
+ *                from D on are not written; must not overlap grad_out
+ *   ws           device workspace of >= embedding_grad_workspace_bytes(T, V, D)
+ * An id outside [0, V), other than padding_idx, contributes nothing and gives
+ * TOPK_EF_ERR_BAD_INPUT through topk_ef_last_device_status(ws).
+ * Otherwise as embedding_lookup.
+ */
+int embedding_grad(const void* grad_out, int32_t grad_out_type,
+                   int64_t ld_grad_out, const void* ids, int32_t id_bytes,
+                   int64_t T, int64_t V, int64_t D, float scale,
+                   int64_t padding_idx, void* grad_weight,
+                   int32_t grad_weight_type, int64_t ld_grad_weight,
+                   int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The same gradient as a row-sparse set (the row form of the index-sorted
+ * sets that the merge calls take):
+ *   out_rows   device, int32[min(T, V)]: the distinct ids that occur, without
+ *              padding_idx, ascending
+ *   out_val    device, [min(T, V)][ld_out_val] of out_val_type: row j is the
+ *              gradient of weight row out_rows[j]
+ *   out_count  device, int32[1]: their number; slots of out_rows and rows of
+ *              out_val from it on are not written
+ */
+int embedding_grad_rows(const void* grad_out, int32_t grad_out_type,
+                        int64_t ld_grad_out, const void* ids, int32_t id_bytes,
+                        int64_t T, int64_t V, int64_t D, float scale,
+                        int64_t padding_idx, int32_t* out_rows, void* out_val,
+                        int32_t out_val_type, int64_t ld_out_val,
+                        int32_t* out_count, void* ws, size_t ws_bytes,
+                        void* stream);
 
 /* Synchronises `stream` and returns the device-side status of the last call
    that used `ws`: TOPK_EF_OK, TOPK_EF_ERR_DEVICE_TIMEOUT,
