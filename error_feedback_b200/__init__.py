@@ -14,6 +14,7 @@ Functions mirror the C names:
 * ``gtopk_merge(in_idx, in_val, k, n)``                  -> (idx, val, count)
 * ``embedding_lookup(weight, ids, scale)``               -> out
 * ``embedding_grad(grad_out, ids, num_rows, scale)``     -> grad_weight
+* ``muon_update(grad, momentum, mu)``                    -> out
 * ``embedding_grad_rows(grad_out, ids, num_rows, scale)`` -> (rows, val, count)
 * ``topk_ef_workspace_bytes``, ``topk_ef_batched_workspace_bytes``,
   ``gtopk_merge_workspace_bytes``, ``topk_ef_last_device_status``,
@@ -126,6 +127,12 @@ def lib() -> ctypes.CDLL:
                                           ctypes.c_float, _i64, _vp, _vp, _i32, _i64, _vp, _vp,
                                           _sz, _vp]
         L.embedding_grad_rows.restype = ctypes.c_int
+        L.muon_workspace_bytes.argtypes = [_i32, _i64, _i64, _i32]
+        L.muon_workspace_bytes.restype = _sz
+        L.muon_update.argtypes = [_vp, _i32, _i64, _i64, _vp, _i32, _i64, _i64, ctypes.c_float,
+                                  _i32, ctypes.c_float, ctypes.POINTER(ctypes.c_float), _i32,
+                                  ctypes.c_float, _vp, _i32, _i64, _i64, _vp, _sz, _vp]
+        L.muon_update.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -556,6 +563,87 @@ def embedding_grad_rows(grad_out, ids, num_rows, scale=1.0, padding_idx=-1, out_
                                        ws.data_ptr(), ws.numel() * ws.element_size(), st)
     _check(rc, "embedding_grad_rows")
     return out_rows, out_val, out_count
+
+
+# ---------------------------------------------------------------------- muon
+
+MUON_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def _matrices(t, name: str, device=None):
+    """(type code, row stride, matrix stride, (B, rows, cols)) of a CUDA
+    tensor of one matrix or a batch of them with contiguous rows."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _TYPE:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [rows, cols] or [B, rows, cols]")
+    B = t.shape[0] if t.dim() == 3 else 1
+    rows, cols = t.shape[-2:]
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    ld = t.stride(-2) if rows > 1 else cols
+    stride = t.stride(0) if B > 1 else rows * ld
+    if t.numel() and (ld < cols or stride < (rows - 1) * ld + cols):
+        raise ValueError(f"the rows of {name} overlap")
+    return _TYPE[t.dtype], max(ld, cols), stride, (B, rows, cols)
+
+
+def _coefficients(coefficients, steps):
+    """float[3 * steps] of one (a, b, c) for every step, or one for each."""
+    steps = int(steps)
+    flat = list(coefficients)
+    if flat and not hasattr(flat[0], "__len__"):
+        flat = [flat] * steps
+    if len(flat) != steps or any(len(c) != 3 for c in flat):
+        raise ValueError("coefficients must be one (a, b, c), or one for each step")
+    return (ctypes.c_float * max(1, 3 * steps))(*[float(x) for c in flat for x in c]), steps
+
+
+def muon_workspace_bytes(B: int, rows: int, cols: int, out_dtype=torch.float32) -> int:
+    return int(lib().muon_workspace_bytes(int(B), int(rows), int(cols), _TYPE[out_dtype]))
+
+
+def muon_update(grad, momentum=None, mu=0.95, nesterov=True, coefficients=MUON_COEFFICIENTS,
+                steps=5, eps=1e-7, scale=1.0, out=None, out_dtype=None, ws=None, stream=None):
+    """Orthogonalised update of one matrix [rows, cols] or of each of a batch
+    [B, rows, cols]: momentum = mu momentum + grad (in place, contiguous
+    float32; None: u = grad), u = grad + mu momentum (nesterov) or momentum,
+    X = u / (||u||_F + eps), `steps` times X <- a X + (b A + c A A) X with
+    A = X X^T, out = scale X.  out: float32 (default; as exact as plain
+    float32 products) or a 16-bit type (operands of the products rounded to
+    11 bits); may be grad itself."""
+    gt, ldg, sg, (B, rows, cols) = _matrices(grad, "grad")
+    dev = grad.device
+    coef, steps = _coefficients(coefficients, steps)
+    _on_device(ws, dev)
+    mp = None
+    if momentum is not None:
+        _cuda_f32(momentum, "momentum")
+        if momentum.shape != grad.shape or momentum.device != dev:
+            raise ValueError("momentum must have grad's shape and device")
+        mp = momentum.data_ptr()
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty(grad.shape, dtype=out_dtype or torch.float32, device=dev)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out and out_dtype differ")
+        ot, ldo, so, shape = _matrices(out, "out", dev)
+        if out.shape != grad.shape:
+            raise ValueError("out must have grad's shape")
+        nb = int(lib().muon_workspace_bytes(B, rows, cols, ot))
+        if nb == 0:
+            raise TopkEfError(ERR_INVALID_ARG, "muon_workspace_bytes")
+        ws = _workspace(nb, dev, ws)
+        rc = lib().muon_update(grad.data_ptr(), gt, ldg, sg, mp, B, rows, cols, float(mu),
+                               1 if nesterov else 0, float(eps), coef, steps, float(scale),
+                               out.data_ptr(), ot, ldo, so, ws.data_ptr(),
+                               ws.numel() * ws.element_size(), st)
+    _check(rc, "muon_update")
+    return out
 
 
 # -------------------------------------------------------------------- status

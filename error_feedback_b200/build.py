@@ -11,7 +11,7 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRCS = [os.path.join(HERE, "csrc", f) for f in ("topk_ef.cu", "embedding.cu")]
+SRCS = [os.path.join(HERE, "csrc", f) for f in ("topk_ef.cu", "embedding.cu", "muon.cu")]
 DEPS = sorted(glob.glob(os.path.join(HERE, "csrc", "*.cu*"))) + [
     os.path.join(ROOT, "include", "topk_ef.h")]
 LIB = os.path.join(HERE, "libtopk_ef.so")

@@ -12,58 +12,13 @@
 // atomics, results bit-identical from run to run.
 #pragma once
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "common.cuh"
+#include "elements.cuh"
 
 namespace tke {
-
-// ------------------------------------------------------------ element types
-
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
-
-// One rounding to nearest even: what an fp32 result becomes in the output type.
-template <typename T> __device__ __forceinline__ T from_f32(float x);
-template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
-    return __float2bfloat16_rn(x);
-}
-template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
-
-// Eight consecutive elements; p is 16-byte aligned.
-template <typename T>
-struct Vec8 {
-    uint4 q[sizeof(T) / 2];
-};
-template <typename T>
-__device__ __forceinline__ Vec8<T> load8(const T* p) {
-    Vec8<T> v;
-    const uint4* s = reinterpret_cast<const uint4*>(p);
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) v.q[i] = __ldg(s + i);
-    return v;
-}
-template <typename T>
-__device__ __forceinline__ float elem8(const Vec8<T>& v, int j) {
-    return to_f32(reinterpret_cast<const T*>(&v)[j]);
-}
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float* x) {
-    Vec8<T> v;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) reinterpret_cast<T*>(&v)[j] = from_f32<T>(x[j]);
-    uint4* d = reinterpret_cast<uint4*>(p);
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) d[i] = v.q[i];
-}
-
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;"); }
 
 // ------------------------------------------------------------------- lookup
 
@@ -89,7 +44,7 @@ template <typename TW, typename TO, typename TI, bool VEC>
 __global__ void __launch_bounds__(LK_THREADS) lookup_kernel(const LookupParams p) {
     pdl_launch();
     pdl_wait();
-    const TI* __restrict__ ids = static_cast<const TI*>(p.ids);
+    const TI* ids = static_cast<const TI*>(p.ids);
     int nblocks = (int)gridDim.x;
     if (p.scan) {
         --nblocks;
@@ -107,8 +62,8 @@ __global__ void __launch_bounds__(LK_THREADS) lookup_kernel(const LookupParams p
             return;
         }
     }
-    const TW* __restrict__ w = static_cast<const TW*>(p.w);
-    TO* __restrict__ out = static_cast<TO*>(p.out);
+    const TW* w = static_cast<const TW*>(p.w);
+    TO* out = static_cast<TO*>(p.out);
     const int lane = (int)lane_id();
     const int64_t stride = (int64_t)nblocks * (LK_THREADS / 32);
     for (int64_t it = (int64_t)blockIdx.x * (LK_THREADS / 32) + warp_id(); it < p.items;
@@ -432,7 +387,7 @@ __global__ void __launch_bounds__(EG_THREADS) grad_sum_kernel(const GradParams p
         if (i < n) s_pos[i] = p.pos[start + i];
     }
     __syncthreads();
-    const TD* __restrict__ dy = static_cast<const TD*>(p.dy);
+    const TD* dy = static_cast<const TD*>(p.dy);
     const int64_t c0 = slab * EG_COLS + (VEC ? tid * 8 : tid);
     auto col = [&](int j) { return c0 + (VEC ? j : j * EG_THREADS); };
     const bool whole = col(7) < p.D;

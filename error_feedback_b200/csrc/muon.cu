@@ -1,0 +1,358 @@
+// Host side of muon_update (include/topk_ef.h): argument checks, workspace
+// layout, launch sequence.
+//
+//   muon_norm_kernel -> muon_scale_kernel -> steps times: muon_gemm_kernel as
+//   gram, square and update (the last update writes the caller's matrix)
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "topk_ef.h"
+#include "common.cuh"
+#include "host.cuh"
+#include "kernels_muon.cuh"
+
+using namespace tke;
+
+namespace {
+
+constexpr int64_t MU_MAX_SIDE = (int64_t)1 << 20;
+constexpr int32_t MU_MAX_BATCH = 65535;
+constexpr int32_t MU_MAX_STEPS = 64;
+
+size_t type_size(int32_t t) {
+    return t == TOPK_EF_F32 ? 4 : t == TOPK_EF_BF16 || t == TOPK_EF_F16 ? 2 : 0;
+}
+
+bool aligned(const void* p, size_t a) { return (uintptr_t)p % a == 0; }
+
+struct MuLayout {
+    int64_t p, ldx, ldp, stride_x, stride_p, groups, parts;
+    size_t ctrl, part, lift, x[2][2], a[2], b[2], total;
+};
+
+MuLayout muon_layout(int32_t B, int64_t m, int64_t n, bool exact) {
+    MuLayout L;
+    L.p = std::min(m, n);
+    L.ldx = ceil_div64(n, 64) * 64;
+    L.ldp = ceil_div64(L.p, 64) * 64;
+    L.stride_x = m * L.ldx;
+    L.stride_p = L.p * L.ldp;
+    L.groups = m * ceil_div64(n, 8);
+    L.parts = std::max<int64_t>(
+        1, std::min<int64_t>(MN_MAX_PARTS, ceil_div64(L.groups, 2 * MN_THREADS)));
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = o;
+        o = align_up(o + bytes);
+        return at;
+    };
+    L.ctrl = take(sizeof(Ctrl));
+    L.part = take((size_t)B * L.parts * sizeof(double));
+    L.lift = take((size_t)B * sizeof(int32_t));
+    for (int i = 0; i < 2; ++i)
+        for (int h = 0; h < 2; ++h) L.x[i][h] = take((size_t)B * L.stride_x * 2);
+    for (int h = 0; h < 2; ++h) {
+        const bool used = h == 0 || exact;
+        L.a[h] = take(used ? (size_t)B * L.stride_p * 2 : 0);
+        L.b[h] = take(used ? (size_t)B * L.stride_p * 2 : 0);
+    }
+    L.total = o;
+    return L;
+}
+
+bool muon_sizes_ok(int32_t B, int64_t m, int64_t n) {
+    return B >= 0 && B <= MU_MAX_BATCH && m >= 0 && m <= MU_MAX_SIDE && n >= 0 && n <= MU_MAX_SIDE;
+}
+
+// Largest |x (a + b s + c s^2)| (s = x^2), |b s + c s^2| and |a + b s + c s^2|
+// for 0 <= x <= reach.
+void polynomial_reach(const float* k, double reach, double* most_p, double* most_q,
+                      double* growth) {
+    const double a = k[0], b = k[1], c = k[2];
+    *most_p = *most_q = 0.0;
+    *growth = std::fabs(a);
+    auto at = [&](double s) {
+        if (!(s >= 0.0 && s <= reach * reach)) return;
+        *growth = std::max(*growth, std::fabs(a + s * (b + s * c)));
+        *most_p = std::max(*most_p, std::fabs(std::sqrt(s) * (a + s * (b + s * c))));
+        *most_q = std::max(*most_q, std::fabs(s * (b + s * c)));
+    };
+    at(reach * reach);
+    // p' = a + 3 b s + 5 c s^2,  q' = b + 2 c s
+    if (c != 0.0) {
+        at(-b / (2.0 * c));
+        const double d = 9.0 * b * b - 20.0 * a * c;
+        if (d >= 0.0) {
+            at((-3.0 * b + std::sqrt(d)) / (10.0 * c));
+            at((-3.0 * b - std::sqrt(d)) / (10.0 * c));
+        }
+    } else if (b != 0.0) {
+        at(-a / (3.0 * b));
+    }
+}
+
+// The singular values start at 1 at most; X, A and B are held in fp16 under
+// fixed scales, so the polynomials must not take them out of its range.
+// drop[i]: bits that X can have grown by before step i.
+bool coefficients_ok(const float* coef, int32_t steps, int32_t* drop) {
+    double reach = 1.0;
+    drop[0] = 0;
+    for (int i = 0; i < steps; ++i) {
+        const float* k = coef + 3 * i;
+        if (!std::isfinite(k[0]) || !std::isfinite(k[1]) || !std::isfinite(k[2])) return false;
+        double mp, mq, growth;
+        polynomial_reach(k, reach, &mp, &mq, &growth);
+        if (mp > MU_REACH || mq > MU_REACH * MU_REACH) return false;
+        reach = mp;
+        drop[i + 1] = drop[i] + (growth > 1.0 ? (int32_t)std::ceil(std::log2(growth)) : 0);
+    }
+    return true;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn(cudaError_t* e) {
+    static std::atomic<void*> fn{nullptr};
+    void* f = fn.load();
+    if (!f) {
+        cudaDriverEntryPointQueryResult q;
+        *e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                              cudaEnableDefault, &q);
+        if (*e != cudaSuccess) return nullptr;
+        if (!f || q != cudaDriverEntryPointSuccess) {
+            *e = cudaErrorNotSupported;
+            return nullptr;
+        }
+        fn.store(f);
+    }
+    return reinterpret_cast<EncodeFn>(f);
+}
+
+// 64 x 64 boxes of [batch][rows][cols] fp16, 128-byte swizzle; zeros outside.
+bool encode(EncodeFn fn, CUtensorMap* map, void* base, int64_t cols, int64_t rows, int64_t batch,
+            int64_t ld, int64_t stride) {
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, 64, 1}, step[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides, box, step,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Block pairs that the current device runs at once; its kernels' shared memory
+// is set the first time.
+cudaError_t muon_device(int* pairs) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool keep = dev >= 0 && dev < 64;
+    if (keep && (*pairs = known[dev].load()) > 0) return cudaSuccess;
+    if ((e = cudaFuncSetAttribute(muon_gemm_kernel<true>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, GM_SMEM)) !=
+        cudaSuccess)
+        return e;
+    if ((e = cudaFuncSetAttribute(muon_gemm_kernel<false>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, GM_SMEM)) !=
+        cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(GM_THREADS);
+    cfg.dynamicSmemBytes = GM_SMEM;
+    e = cudaOccupancyMaxActiveClusters(pairs, muon_gemm_kernel<false>, &cfg);
+    if (e == cudaSuccess && *pairs < 1) e = cudaErrorNotSupported;
+    if (e == cudaSuccess && keep) known[dev].store(*pairs);
+    return e;
+}
+
+template <typename F>
+cudaError_t with_type(int32_t t, F f) {
+    switch (t) {
+        case TOPK_EF_F32: return f(float{});
+        case TOPK_EF_BF16: return f(__nv_bfloat16{});
+        default: return f(__half{});
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t muon_workspace_bytes(int32_t B, int64_t rows, int64_t cols, int32_t out_type) {
+    if (!muon_sizes_ok(B, rows, cols) || !type_size(out_type)) return 0;
+    return muon_layout(B, rows, cols, out_type == TOPK_EF_F32).total;
+}
+
+int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t stride_grad,
+                float* momentum, int32_t B, int64_t rows, int64_t cols, float mu, int32_t nesterov,
+                float eps, const float* coef, int32_t steps, float scale, void* out,
+                int32_t out_type, int64_t ld_out, int64_t stride_out, void* ws, size_t ws_bytes,
+                void* stream) {
+    const size_t need = muon_workspace_bytes(B, rows, cols, out_type);
+    const size_t sg = type_size(grad_type), so = type_size(out_type);
+    if (need == 0 || !ws || !aligned(ws, ALIGN) || !sg) return TOPK_EF_ERR_INVALID_ARG;
+    if (steps < 1 || steps > MU_MAX_STEPS || !coef || !(eps >= 0.0f))
+        return TOPK_EF_ERR_INVALID_ARG;
+    int32_t drop[MU_MAX_STEPS + 1];
+    if (!coefficients_ok(coef, steps, drop)) return TOPK_EF_ERR_INVALID_ARG;
+    if (ld_grad < cols || ld_out < cols || (B > 1 && rows > 0 && cols > 0 &&
+        (stride_grad < (rows - 1) * ld_grad + cols || stride_out < (rows - 1) * ld_out + cols)))
+        return TOPK_EF_ERR_INVALID_ARG;
+    const bool empty = B == 0 || rows == 0 || cols == 0;
+    if (!empty && (!grad || !out || !aligned(grad, sg) || !aligned(out, so) ||
+                   !aligned(momentum, 4)))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (ws_bytes < need) return TOPK_EF_ERR_WORKSPACE;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (empty) {
+        e = cudaMemsetAsync(ws, 0, sizeof(Ctrl), st);
+        return e == cudaSuccess ? TOPK_EF_OK : cuda_fail(e);
+    }
+    const bool exact = out_type == TOPK_EF_F32, tall = rows > cols;
+    const MuLayout L = muon_layout(B, rows, cols, exact);
+    char* w = static_cast<char*>(ws);
+    __half *x[2][2], *am[2], *bm[2];
+    for (int h = 0; h < 2; ++h) {
+        for (int i = 0; i < 2; ++i) x[i][h] = reinterpret_cast<__half*>(w + L.x[i][h]);
+        am[h] = reinterpret_cast<__half*>(w + L.a[h]);
+        bm[h] = reinterpret_cast<__half*>(w + L.b[h]);
+    }
+    // typical entries of X near 1, the largest below 2^15
+    const double S = std::exp2(std::min(13.0, std::ceil(0.5 * std::log2((double)rows * cols))));
+
+    int pairs = 0;
+    if ((e = muon_device(&pairs)) != cudaSuccess) return cuda_fail(e);
+    EncodeFn fn = encode_fn(&e);
+    if (!fn) return cuda_fail(e);
+    CUtensorMap mx[2][2], ma[2], mb[2];
+    bool ok = true;
+    for (int h = 0; h < (exact ? 2 : 1); ++h) {
+        for (int i = 0; i < 2; ++i)
+            ok = ok && encode(fn, &mx[i][h], x[i][h], cols, rows, B, L.ldx, L.stride_x);
+        ok = ok && encode(fn, &ma[h], am[h], L.p, L.p, B, L.ldp, L.stride_p);
+        ok = ok && encode(fn, &mb[h], bm[h], L.p, L.p, B, L.ldp, L.stride_p);
+    }
+    if (!ok) return cuda_fail(cudaErrorInvalidValue);
+
+    MuonPreParams pp = {};
+    pp.grad = grad;
+    pp.momentum = momentum;
+    pp.part = reinterpret_cast<double*>(w + L.part);
+    pp.hi = x[0][0];
+    pp.lo = x[0][1];
+    pp.lift = reinterpret_cast<int32_t*>(w + L.lift);
+    pp.ctrl = reinterpret_cast<Ctrl*>(w + L.ctrl);
+    pp.rows = rows;
+    pp.cols = cols;
+    pp.ldx = L.ldx;
+    pp.ld_g = ld_grad;
+    pp.stride_g = stride_grad;
+    pp.stride_x = L.stride_x;
+    pp.parts = L.parts;
+    pp.row_groups = ceil_div64(cols, 8);
+    pp.groups = L.groups;
+    pp.mu = mu;
+    pp.nesterov = nesterov;
+    pp.eps = eps;
+    pp.S = S;
+    const dim3 pre((unsigned)L.parts, (unsigned)B);
+    e = with_type(grad_type, [&](auto t) {
+        using TG = decltype(t);
+        trace_before(st, "muon_norm_kernel");
+        cudaError_t r = launch_pdl(muon_norm_kernel<TG>, pre, MN_THREADS, st, pp);
+        trace_after(st);
+        if (r != cudaSuccess) return r;
+        trace_before(st, "muon_scale_kernel");
+        r = launch_pdl(muon_scale_kernel<TG>, pre, MN_THREADS, st, pp);
+        trace_after(st);
+        return r;
+    });
+    if (e != cudaSuccess) return cuda_fail(e);
+
+    const int32_t P = (int32_t)L.p, Q = (int32_t)std::max(rows, cols);
+    auto launch = [&](GemmParams& g, const CUtensorMap* a, const CUtensorMap* b) {
+        for (int h = 0; h < 2; ++h) {
+            g.a[h] = a[exact ? h : 0];
+            g.b[h] = b[exact ? h : 0];
+        }
+        g.batch = B;
+        g.ctrl = pp.ctrl;
+        g.lift = pp.lift;
+        g.tiles_m = (int32_t)ceil_div64(g.M, GM_TILE);
+        g.tiles_n = (int32_t)ceil_div64(g.N, GM_TILE);
+        int64_t tiles = (int64_t)g.tiles_m * g.tiles_n;
+        if (g.mode <= MU_SQUARE) tiles = (int64_t)g.tiles_m * (g.tiles_m + 1) / 2;
+        if (tiles * B > MAX_N) return cudaErrorInvalidValue;
+        g.tiles = (int32_t)tiles;
+        const unsigned grid = 2u * (unsigned)std::min<int64_t>(tiles * B, pairs);
+        trace_before(st, "muon_gemm_kernel");
+        const cudaError_t r =
+            exact ? launch_pdl(muon_gemm_kernel<true>, grid, GM_THREADS, st, g, GM_SMEM)
+                  : launch_pdl(muon_gemm_kernel<false>, grid, GM_THREADS, st, g, GM_SMEM);
+        trace_after(st);
+        return r;
+    };
+    int cur = 0;
+    for (int i = 0; i < steps; ++i) {
+        const float* k = coef + 3 * i;
+        GemmParams g = {};
+        g.drop = drop[i];
+        g.drop_next = drop[i + 1];
+        g.mode = MU_GRAM;
+        g.M = g.N = P;
+        g.K = Q;
+        g.a_mn = g.b_mn = tall;
+        g.alpha = (float)(MU_SA / (S * S));
+        g.dst[0] = am[0];
+        g.dst[1] = am[1];
+        g.ld = L.ldp;
+        g.stride = L.stride_p;
+        if ((e = launch(g, mx[cur], mx[cur])) != cudaSuccess) return cuda_fail(e);
+
+        g.mode = MU_SQUARE;
+        g.K = P;
+        g.a_mn = g.b_mn = 0;
+        g.alpha = k[2] / MU_SA;
+        g.beta = k[1];
+        g.src[0] = am[0];
+        g.src[1] = am[1];
+        g.dst[0] = bm[0];
+        g.dst[1] = bm[1];
+        if ((e = launch(g, ma, ma)) != cudaSuccess) return cuda_fail(e);
+
+        const bool last = i == steps - 1;
+        g.mode = last ? MU_LAST : MU_UPDATE;
+        g.M = (int32_t)rows;
+        g.N = (int32_t)cols;
+        g.K = P;
+        g.b_mn = !tall;
+        g.n_fast = tall;
+        g.alpha = last ? (float)(scale / (S * MU_SA)) : 1.0f / MU_SA;
+        g.beta = last ? (float)(k[0] * (double)scale / S) : k[0];
+        g.src[0] = x[cur][0];
+        g.src[1] = x[cur][1];
+        g.dst[0] = x[cur ^ 1][0];
+        g.dst[1] = x[cur ^ 1][1];
+        g.ld = L.ldx;
+        g.stride = L.stride_x;
+        g.out = out;
+        g.out_type = out_type;
+        g.ld_out = ld_out;
+        g.stride_out = stride_out;
+        e = tall ? launch(g, mx[cur], mb) : launch(g, mb, mx[cur]);
+        if (e != cudaSuccess) return cuda_fail(e);
+        cur ^= 1;
+    }
+    return TOPK_EF_OK;
+}
+
+}  // extern "C"

@@ -377,6 +377,56 @@ int embedding_grad_rows(const void* grad_out, int32_t grad_out_type,
                         int32_t* out_count, void* ws, size_t ws_bytes,
                         void* stream);
 
+/* ------------------------------------------------------------------- muon */
+
+/* Workspace bytes for muon_update; 0 for invalid arguments. */
+size_t muon_workspace_bytes(int32_t B, int64_t rows, int64_t cols,
+                            int32_t out_type);
+
+/*
+ * Momentum and orthogonalisation of the updates of B matrices by
+ * Newton-Schulz products (the Muon optimiser's update), each on its own:
+ *     momentum = fmaf(mu, momentum, grad)
+ *     u        = nesterov ? fmaf(mu, momentum, grad) : momentum
+ *                (without momentum: u = grad)
+ *     X        = u / (||u||_F + eps)
+ *     steps times, with (a, b, c) = coef[3 i .. 3 i + 2]:
+ *         A = X X^T;   X = a X + (b A + c A A) X
+ *     out      = round(scale * X)
+ * (a tall matrix is treated as its transpose.)  Sums are fp32 or wider.  With
+ * fp32 output every product keeps 22 bits of its operands and the result is
+ * as exact as one in plain fp32; with 16-bit output the products' operands
+ * are rounded to 11 bits, which leaves an error near that of the output's own
+ * rounding (relative to the matrix's norm; larger where many entries are
+ * equal).  fp32 output may be part of the flat buffer that topk_ef_compress and
+ * topk_ef_compress_batched read.
+ *   grad       device, [B][rows][cols] of grad_type; rows ld_grad apart,
+ *              matrices stride_grad apart
+ *   momentum   device, fp32[B][rows][cols] contiguous, updated in place; or NULL
+ *   B          0 <= B <= 65535;  0 <= rows, cols <= 2^20
+ *   eps        >= 0
+ *   coef       host, float[3 * steps], read before the call returns.  On the
+ *              singular values that can occur (at most 1 at the start) every
+ *              |x (a + b x^2 + c x^4)| must stay within 4 and every
+ *              |b x^2 + c x^4| within 16
+ *   steps      1 <= steps <= 64
+ *   out        device, [B][rows][cols] of out_type; rows ld_out apart,
+ *              matrices stride_out apart; may be grad itself (same type and
+ *              strides), must not overlap otherwise
+ *   ws         device workspace of >= muon_workspace_bytes(B, rows, cols,
+ *              out_type)
+ * Infinities, NaNs: as the formulas give them (a NaN anywhere makes the whole
+ * of its matrix NaN); the other matrices are not touched by them.
+ * Errors: TOPK_EF_ERR_INVALID_ARG (sizes, types, coefficients, null or
+ * misaligned pointers), TOPK_EF_ERR_WORKSPACE, TOPK_EF_ERR_CUDA.
+ */
+int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad,
+                int64_t stride_grad, float* momentum, int32_t B, int64_t rows,
+                int64_t cols, float mu, int32_t nesterov, float eps,
+                const float* coef, int32_t steps, float scale, void* out,
+                int32_t out_type, int64_t ld_out, int64_t stride_out, void* ws,
+                size_t ws_bytes, void* stream);
+
 /* Synchronises `stream` and returns the device-side status of the last call
    that used `ws`: TOPK_EF_OK, TOPK_EF_ERR_DEVICE_TIMEOUT,
    TOPK_EF_ERR_BAD_INPUT or TOPK_EF_ERR_INTERNAL (or TOPK_EF_ERR_CUDA if the
