@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(MN_THREADS) muon_scale_kernel(const MuonPrePar
 constexpr int GM_EPI_WARPS = 8;
 constexpr int GM_THREADS = 128 + 32 * GM_EPI_WARPS;    // load, product, 2 idle, epilogue
 constexpr int GM_TILE = 256, GM_ROWS = 128, GM_K = 64;
+constexpr int GM_HAND = 2;                             // fp32 output: stages of one handover
 constexpr int GM_BOX = 64 * 64 * 2;                    // bytes of one 64 x 64 fp16 box
 constexpr int GM_OP = GM_ROWS * GM_K * 2;              // one operand of one block and stage
 constexpr int GM_RING = 6 * 2 * GM_OP;                 // 196,608 bytes of stages
@@ -227,8 +228,16 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     return false;
 }
 
-// One 64 x 64 box into this block's shared memory; the bytes are counted on a
-// barrier of either block of the pair.
+// One 64 x 64 box into this block's shared memory, counted on its barrier.
+__device__ __forceinline__ void tma_box1(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                         uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+// The same, counted on a barrier of either block of a pair.
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
                                         uint32_t bar) {
     asm volatile(
@@ -236,6 +245,9 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
         "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -263,12 +275,26 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool mn) {
            (1ull << 46) | (2ull << 61);
 }
 
+// D (+)= A B^T on one SM, and on a pair of SMs.
+__device__ __forceinline__ void mma_f16_1(uint32_t tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                        bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
 __device__ __forceinline__ void mma_f16(uint32_t tmem, uint64_t a, uint64_t b, uint32_t idesc,
                                         bool add) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit1(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
         : "memory");
 }
 // Arrives on the barrier at this place in both blocks once the products so far are done.
@@ -280,12 +306,12 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+// (the registers hold the values after tmem_wait)
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t* r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
           "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
@@ -295,13 +321,33 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_wait() {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+    tmem_load32(addr, r);
+    tmem_wait();
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
 struct TileAt {
     int b, m, n;       // batch, this block's first row, the tile's first column
 };
 
-// The t-th tile of this call, rank: 0 or 1 in the pair.  Symmetric outputs:
-// tiles (i, j) with i >= j, row by row.
-__device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t, int rank) {
+// The t-th size x size tile of this call.  Symmetric outputs: tiles (i, j)
+// with i >= j, row by row.
+__device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t, int size) {
     TileAt r;
     r.b = t / p.tiles;
     t -= r.b * p.tiles;
@@ -318,8 +364,8 @@ __device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t, int rank) 
         j = t / p.tiles_m;
         i = t - j * p.tiles_m;
     }
-    r.m = i * GM_TILE + rank * GM_ROWS;
-    r.n = j * GM_TILE;
+    r.m = i * size;
+    r.n = j * size;
     return r;
 }
 
@@ -391,73 +437,60 @@ __device__ __forceinline__ void store_pair(const GemmParams& p, int64_t o, const
 // What a tile's values are multiplied by besides alpha and beta: X is held
 // times 2^k, k = max(0, lift - drop), and the next X times 2^max(0, lift -
 // drop_next).
+template <int MODE>
 __device__ __forceinline__ void lift_factors(const GemmParams& p, int b, float* sum, float* src) {
     *sum = *src = 1.0f;
     const int lift = p.lift[b];
     if (lift == 0) return;
     const int k = max(0, lift - p.drop), next = max(0, lift - p.drop_next);
-    if (p.mode == MU_GRAM) *sum = exp2f((float)(-2 * k));
-    else if (p.mode == MU_UPDATE) *sum = *src = exp2f((float)(next - k));
-    else if (p.mode == MU_LAST) *sum = *src = exp2f((float)-k);
+    if (MODE == MU_GRAM) *sum = exp2f((float)(-2 * k));
+    else if (MODE == MU_UPDATE) *sum = *src = exp2f((float)(next - k));
+    else if (MODE == MU_LAST) *sum = *src = exp2f((float)-k);
 }
 
-// One row's 32 columns of a finished tile; v: the sums.
-template <bool EXACT>
-__device__ __forceinline__ void epilogue32(const GemmParams& p, const TileAt& at, float alpha,
-                                           float beta, int64_t row, int64_t c0, float* v) {
-    const bool live = row < p.M && c0 < p.N;
-    const int64_t o = at.b * p.stride + row * p.ld + c0;
-    // (rows of src and dst are padded to 64 columns: 32 at a time stay inside)
-    if (p.mode == MU_GRAM) {
+// The elementwise operand of one row's 32 columns: hi, or hi + lo.
+template <bool EXACT, int MODE>
+__device__ __forceinline__ void load_src32(const GemmParams& p, int64_t o, bool live, float* x) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] *= alpha;
-    } else if (live) {
+    for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+    if (MODE != MU_GRAM && live) {
 #pragma unroll
         for (int j = 0; j < 32; j += 16) {
-            float h[16], l[16];
-            load_half16(p.src[0] + o + j, h);
-            if (EXACT || p.mode >= MU_UPDATE) {
+            load_half16(p.src[0] + o + j, x + j);
+            if (EXACT || MODE >= MU_UPDATE) {
+                float l[16];
                 load_half16(p.src[1] + o + j, l);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) h[e] += l[e];
+                for (int e = 0; e < 16; ++e) x[j + e] += l[e];
             }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[j + e] = fmaf(alpha, v[j + e], beta * h[e]);
         }
     }
-    if (p.mode == MU_LAST) {
-        if (!live) return;
+}
+
+// One row's 32 columns of a finished tile; v: the sums, x: the elementwise
+// operand.  (Rows of src and dst are padded to 64 columns: 32 at a time stay
+// inside.)  mirror: the tile lies below the diagonal, and its image above is
+// written too (a warp's 32 rows are 32 consecutive columns there).
+template <bool EXACT, int MODE>
+__device__ __forceinline__ void epilogue32(const GemmParams& p, const TileAt& at, float alpha,
+                                           float beta, int64_t row, int64_t c0, bool mirror,
+                                           float* v, const float* x) {
+    if (row >= p.M || c0 >= p.N) return;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = MODE == MU_GRAM ? alpha * v[j] : fmaf(alpha, v[j], beta * x[j]);
+    if (MODE == MU_LAST) {
         if (p.out_type == 0) store_out<float>(p, at.b, row, c0, v);
         else if (p.out_type == 1) store_out<__nv_bfloat16>(p, at.b, row, c0, v);
         else store_out<__half>(p, at.b, row, c0, v);
         return;
     }
-    if (p.mode == MU_UPDATE) {
-        if (live) store_pair(p, o, v, true);
-        return;
-    }
-    // Symmetric: columns up to the row, and their mirror image (a warp's 32
-    // rows are 32 consecutive columns there).  Each entry is written by one
-    // thread only.
-    const int64_t row0 = row - lane_id();
-    if (c0 > row0 + 31) return;
-    const bool below = c0 + 31 <= row0;
-    if (live && below) store_pair(p, o, v, EXACT);
+    store_pair(p, at.b * p.stride + row * p.ld + c0, v, EXACT || MODE == MU_UPDATE);
+    if (MODE <= MU_SQUARE && mirror) {
+        const int64_t o = at.b * p.stride + c0 * p.ld + row;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        const int64_t c = c0 + j;
-        if (live && c <= row) {
-            const __half h = __float2half_rn(v[j]);
-            const __half l = __float2half_rn(v[j] - __half2float(h));
-            if (!below) {
-                p.dst[0][o + j] = h;
-                if (EXACT) p.dst[1][o + j] = l;
-            }
-            if (c < row) {
-                const int64_t om = at.b * p.stride + c * p.ld + row;
-                p.dst[0][om] = h;
-                if (EXACT) p.dst[1][om] = l;
-            }
+        for (int j = 0; j < 32; ++j) {
+            p.dst[0][o + j * p.ld] = __float2half_rn(v[j]);
+            if (EXACT) p.dst[1][o + j * p.ld] = __float2half_rn(below_half(v[j]));
         }
     }
 }
@@ -469,10 +502,10 @@ __device__ __forceinline__ void epilogue32(const GemmParams& p, const TileAt& at
 //
 // The tensor core's own fp32 accumulation truncates: a sum of K / 16 products
 // of one sign comes out up to K / 16 half-steps low.  With fp32 output the
-// accumulator is therefore handed over after every 64 of K, the small
-// products (hi lo, lo hi) before the large, and added up in registers with
+// accumulator is therefore handed over after every 128 of K, the small
+// products (hi lo, lo hi) before the large of each 64, and added up in registers with
 // rounding to nearest.
-template <bool EXACT>
+template <bool EXACT, int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
     muon_gemm_kernel(const __grid_constant__ GemmParams p) {
     constexpr int PARTS = EXACT ? 2 : 1;
@@ -500,6 +533,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
         mbar_init(smem_u32(&s_drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (warp == 0 && lane < 2 * PARTS) prefetch_map(lane & 1 ? &p.b[lane >> 1] : &p.a[lane >> 1]);
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          smem_u32(&s_tmem))
@@ -515,13 +549,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
     const int total = p.tiles * p.batch, kblocks = (p.K + GM_K - 1) / GM_K;
     pdl_launch();
     pdl_wait();
-    if (EXACT) {
-        // 384 threads start with 168 registers each; the 128 running sums of
-        // an epilogue thread need more: 72 + 216 + 216 = 3 x 168
-        if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    }
 
+    // With fp32 output: 384 threads start with 168 registers each; the 128
+    // running sums of an epilogue thread need more: 72 + 216 + 216 = 3 x 168.
+    const int group = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x / 128, 0);
+    if (group == 0) {
+    if (EXACT) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0 && lane == 0) {
         // ---- loads (of what earlier kernels wrote with ordinary stores)
         asm volatile("fence.proxy.async;" ::: "memory");
@@ -529,7 +562,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
         uint32_t phase = 0, issued = 0;
         bool ok = true;
         for (int t = pair; t < total && ok; t += pairs) {
-            const TileAt at = tile_at(p, t, rank);
+            TileAt at = tile_at(p, t, GM_TILE);
+            at.m += rank * GM_ROWS;
             const int n0 = at.n + rank * GM_ROWS;
             for (int kb = 0; kb < kblocks; ++kb) {
                 if (!(ok = mbar_wait(smem_u32(&s_empty[stage]), phase ^ 1, &s_gave_up, status)))
@@ -578,7 +612,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
         bool ok = true;
         for (int t = pair; t < total && ok; t += pairs) {
             for (int kb = 0; kb < kblocks; ++kb) {
-                const bool begin = EXACT || kb == 0, end = EXACT || kb == kblocks - 1;
+                const bool begin = kb % (EXACT ? GM_HAND : kblocks) == 0;
+                const bool end = kb == kblocks - 1 || (EXACT && kb % GM_HAND == GM_HAND - 1);
                 if (begin) {
                     if (!(ok = mbar_wait(smem_u32(&s_free[slot]), slot_phase ^ 1, &s_gave_up,
                                          status)))
@@ -592,7 +627,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
 #pragma unroll
                     for (int k = 0; k < GM_K / 16; ++k) {
                         mma_f16(d, smem_desc(a0 + k * a_step, p.a_mn),
-                                smem_desc(b0 + GM_OP + k * b_step, p.b_mn), idesc, k > 0);
+                                smem_desc(b0 + GM_OP + k * b_step, p.b_mn), idesc, !begin || k > 0);
                         mma_f16(d, smem_desc(a0 + GM_OP + k * a_step, p.a_mn),
                                 smem_desc(b0 + k * b_step, p.b_mn), idesc, true);
                     }
@@ -600,7 +635,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
 #pragma unroll
                 for (int k = 0; k < GM_K / 16; ++k)
                     mma_f16(d, smem_desc(a0 + k * a_step, p.a_mn),
-                            smem_desc(b0 + k * b_step, p.b_mn), idesc, EXACT || kb > 0 || k > 0);
+                            smem_desc(b0 + k * b_step, p.b_mn), idesc, EXACT || !begin || k > 0);
                 mma_commit(smem_u32(&s_empty[stage]));
                 if (end) {
                     mma_commit(smem_u32(&s_done[slot]));
@@ -615,7 +650,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
                 }
             }
         }
-    } else if (warp >= 4) {
+    }
+    } else {
+        if (EXACT) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         // ---- epilogue: warp w reads TMEM lanes 32 (w mod 4) .., half of the columns
         const int quad = warp & 3, col = warp < 8 ? 0 : HALF;
         const uint32_t src = tmem + col + ((uint32_t)(quad * 32) << 16);
@@ -638,37 +675,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
             return ok;
         };
         for (int t = pair; t < total && ok; t += pairs) {
-            const TileAt at = tile_at(p, t, rank);
+            TileAt at = tile_at(p, t, GM_TILE);
+            at.m += rank * GM_ROWS;
             const int64_t row = at.m + quad * 32 + lane;
             float fs, fx;
-            lift_factors(p, at.b, &fs, &fx);
+            lift_factors<MODE>(p, at.b, &fs, &fx);
             const float alpha = p.alpha * fs, beta = p.beta * fx;
+            const int64_t o = at.b * p.stride + row * p.ld + at.n + col;
+            const bool mirror = at.m >= at.n + GM_TILE;
+            float x[32];
             if (EXACT) {
                 float sum[HALF];
-                for (int kb = 0; kb < kblocks; ++kb) {
+#pragma unroll
+                for (int c = 0; c < HALF; ++c) sum[c] = 0.0f;
+                for (int kb = 0; kb < kblocks; kb += GM_HAND) {
                     if (!wait_done()) break;
 #pragma unroll
-                    for (int c = 0; c < HALF; c += 32) {
-                        float v[32];
-                        tmem_ld32(src + slot * GM_TILE + c, reinterpret_cast<uint32_t*>(v));
+                    for (int c = 0; c < HALF; c += 64) {
+                        float v[64];
+                        tmem_load32(src + slot * GM_TILE + c, reinterpret_cast<uint32_t*>(v));
+                        tmem_load32(src + slot * GM_TILE + c + 32, reinterpret_cast<uint32_t*>(v + 32));
+                        tmem_wait();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) sum[c + j] = kb == 0 ? v[j] : sum[c + j] + v[j];
+                        for (int j = 0; j < 64; ++j) sum[c + j] += v[j];
                     }
-                    drained();
+                    if (kb + GM_HAND < kblocks) drained();
                 }
                 if (!ok) break;
+                // back to where the last sums came from, for the loop below
 #pragma unroll
                 for (int c = 0; c < HALF; c += 32)
-                    epilogue32<EXACT>(p, at, alpha, beta, row, at.n + col + c, sum + c);
+                    tmem_st32(src + slot * GM_TILE + c, reinterpret_cast<uint32_t*>(sum + c));
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                load_src32<EXACT, MODE>(p, o, row < p.M && at.n + col < p.N, x);
             } else {
+                load_src32<EXACT, MODE>(p, o, row < p.M && at.n + col < p.N, x);
                 if (!wait_done()) break;
-                for (int c = 0; c < HALF; c += 32) {
-                    float v[32];
-                    tmem_ld32(src + slot * GM_TILE + c, reinterpret_cast<uint32_t*>(v));
-                    epilogue32<EXACT>(p, at, alpha, beta, row, at.n + col + c, v);
-                }
-                drained();
             }
+#pragma unroll 1
+            for (int c = 0; c < HALF; c += 32) {
+                float v[32], next[32];
+                load_src32<EXACT, MODE>(p, o + c + 32, c + 32 < HALF && row < p.M &&
+                                        at.n + col + c + 32 < p.N, next);
+                tmem_ld32(src + slot * GM_TILE + c, reinterpret_cast<uint32_t*>(v));
+                epilogue32<EXACT, MODE>(p, at, alpha, beta, row, at.n + col + c, mirror, v, x);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[j] = next[j];
+            }
+            drained();
         }
     }
     __syncthreads();
@@ -683,6 +737,293 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
     cluster_sync();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// ------------------------------------- products of few tiles: K over a cluster
+
+// Where there are fewer 256 x 256 tiles than pairs of SMs: one 128 x 128 tile per
+// cluster of 1, 2, 4 or 8 blocks, each of which takes a part of K.  The blocks' sums
+// meet in shared memory: block r adds up the r-th part of the rows over all
+// blocks, in block order, and finishes them.
+constexpr int SP_THREADS = 256;
+constexpr int SP_TILE = 128;
+constexpr int SP_STAGES = 3;
+constexpr int SP_LD = SP_TILE + 4;                     // row of sums, in floats
+constexpr int SP_MAX_SPLIT = 8;
+constexpr int SP_MAX_SUM = 48;     // fp32 output: 64s of K of one block, at most (64 truncated adds)
+constexpr int SP_SUMS = SP_TILE * SP_LD * 4;           // bytes of the sums, then the turned tile
+constexpr int sp_smem(bool exact) {
+    const int ring = SP_STAGES * (exact ? 4 : 2) * GM_OP;
+    const int after = SP_SUMS + (exact ? 2 : 1) * SP_TILE * (SP_TILE + 8) * 2;
+    return (ring > after ? ring : after) + 1024;
+}
+
+// Four columns of one row; v: the sums, h and l: the elementwise operand; v
+// becomes the value.
+template <bool EXACT, int MODE>
+__device__ __forceinline__ void epilogue4(const GemmParams& p, const TileAt& at, float alpha,
+                                          float beta, int64_t row, int64_t c0, uint2 h, uint2 l,
+                                          float* v) {
+    const __half* hh = reinterpret_cast<const __half*>(&h);
+    const __half* ll = reinterpret_cast<const __half*>(&l);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        v[j] = MODE == MU_GRAM
+                   ? alpha * v[j]
+                   : fmaf(alpha, v[j], beta * (__half2float(hh[j]) + __half2float(ll[j])));
+    if (row >= p.M || c0 >= p.N) return;
+    if (MODE == MU_LAST) {
+        auto put = [&](auto type) {
+            using TO = decltype(type);
+            TO* dst = static_cast<TO*>(p.out) + at.b * p.stride_out + row * p.ld_out + c0;
+            if (c0 + 4 <= p.N && (uintptr_t)dst % (4 * sizeof(TO)) == 0) {
+                uint32_t r[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) reinterpret_cast<TO*>(r)[j] = from_f32<TO>(v[j]);
+                if (sizeof(TO) == 4)
+                    *reinterpret_cast<uint4*>(dst) = make_uint4(r[0], r[1], r[2], r[3]);
+                else
+                    *reinterpret_cast<uint2*>(dst) = make_uint2(r[0], r[1]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (c0 + j < p.N) dst[j] = from_f32<TO>(v[j]);
+            }
+        };
+        if (p.out_type == 0) put(float{});
+        else if (p.out_type == 1) put(__nv_bfloat16{});
+        else put(__half{});
+        return;
+    }
+    const int64_t o = at.b * p.stride + row * p.ld + c0;
+    *reinterpret_cast<uint2*>(p.dst[0] + o) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+    if (EXACT || MODE == MU_UPDATE)
+        *reinterpret_cast<uint2*>(p.dst[1] + o) =
+            make_uint2(pack2(below_half(v[0]), below_half(v[1])),
+                       pack2(below_half(v[2]), below_half(v[3])));
+}
+
+// fp32 output: the large products of successive 64 of K go to three
+// accumulators in turn and the small ones to a fourth, which keeps the
+// truncated sums short (see muon_gemm_kernel).
+template <bool EXACT, int MODE>
+__global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_constant__ GemmParams p) {
+    constexpr int PARTS = EXACT ? 2 : 1;
+    constexpr int STAGE = PARTS * 2 * GM_OP;
+    constexpr int BIG = EXACT ? 3 : 1;                 // accumulators of large products
+    constexpr uint32_t COLS = EXACT ? 512 : 128;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t s_full[SP_STAGES], s_empty[SP_STAGES], s_done;
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_gave_up;
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    const int warp = (int)warp_id(), lane = (int)lane_id();
+    const int rank = (int)cluster_rank();
+    uint32_t split;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
+    if (threadIdx.x == 0) {
+        s_gave_up = 0;
+        for (int s = 0; s < SP_STAGES; ++s) {
+            mbar_init(smem_u32(&s_full[s]), 1);
+            mbar_init(smem_u32(&s_empty[s]), 1);
+        }
+        mbar_init(smem_u32(&s_done), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0 && lane < 2 * PARTS) prefetch_map(lane & 1 ? &p.b[lane >> 1] : &p.a[lane >> 1]);
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&s_tmem)), "n"(COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = s_tmem;
+    uint32_t* status = &p.ctrl->status;
+    const TileAt at = tile_at(p, (int)(blockIdx.x / split), SP_TILE);
+    const int kblocks = (p.K + GM_K - 1) / GM_K;
+    const int kb0 = (int)((int64_t)kblocks * rank / split);
+    const int n = (int)((int64_t)kblocks * (rank + 1) / split) - kb0;
+    pdl_launch();
+    pdl_wait();
+
+    if (warp == 0 && lane == 0) {
+        asm volatile("fence.proxy.async;" ::: "memory");
+        int i = 0;
+        for (; i < n; ++i) {
+            const int s = i % SP_STAGES;
+            if (i >= SP_STAGES && !mbar_wait(smem_u32(&s_empty[s]), (i / SP_STAGES - 1) & 1,
+                                             &s_gave_up, status))
+                break;
+            const uint32_t bar = smem_u32(&s_full[s]);
+            mbar_expect(bar, STAGE);
+            uint32_t dst = base + s * STAGE;
+            const int k = (kb0 + i) * GM_K;
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+                for (int h = 0; h < 2; ++h, dst += GM_BOX) {
+                    if (p.a_mn) tma_box1(dst, &p.a[q], at.m + h * 64, k, at.b, bar);
+                    else tma_box1(dst, &p.a[q], k, at.m + h * 64, at.b, bar);
+                }
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+                for (int h = 0; h < 2; ++h, dst += GM_BOX) {
+                    if (p.b_mn) tma_box1(dst, &p.b[q], at.n + h * 64, k, at.b, bar);
+                    else tma_box1(dst, &p.b[q], k, at.n + h * 64, at.b, bar);
+                }
+        }
+        // no copy is in flight when the stages are used for the sums
+        for (int j = max(0, i - SP_STAGES); j < i; ++j) {
+            volatile int never = 0;
+            mbar_wait(smem_u32(&s_full[j % SP_STAGES]), (j / SP_STAGES) & 1, &never, status);
+        }
+    } else if (warp == 1 && lane == 0) {
+        const uint32_t idesc = (1u << 4) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16) |
+                               ((SP_TILE / 8) << 17) | ((SP_TILE / 16) << 24);
+        const uint32_t a_step = p.a_mn ? 2048 : 32, b_step = p.b_mn ? 2048 : 32;
+        for (int i = 0; i < n; ++i) {
+            const int s = i % SP_STAGES;
+            if (!mbar_wait(smem_u32(&s_full[s]), (i / SP_STAGES) & 1, &s_gave_up, status)) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t a0 = base + s * STAGE, b0 = a0 + PARTS * GM_OP;
+            const uint32_t d = tmem + (i % BIG) * SP_TILE, small = tmem + BIG * SP_TILE;
+#pragma unroll
+            for (int k = 0; k < GM_K / 16; ++k) {
+                const uint64_t ah = smem_desc(a0 + k * a_step, p.a_mn);
+                const uint64_t bh = smem_desc(b0 + k * b_step, p.b_mn);
+                mma_f16_1(d, ah, bh, idesc, i >= BIG || k > 0);
+                if (EXACT) {
+                    mma_f16_1(small, ah, smem_desc(b0 + GM_OP + k * b_step, p.b_mn), idesc,
+                              i > 0 || k > 0);
+                    mma_f16_1(small, smem_desc(a0 + GM_OP + k * a_step, p.a_mn), bh, idesc, true);
+                }
+            }
+            mma_commit1(smem_u32(&s_empty[s]));
+        }
+        mma_commit1(smem_u32(&s_done));
+    }
+    __syncwarp();
+    // all warps drain the accumulators: rows 32 (warp mod 4) .., half of the columns
+    {
+        volatile int never = 0;
+        mbar_wait(smem_u32(&s_done), 0, &never, status);
+    }
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const int quad = warp & 3, col = (warp >> 2) * (SP_TILE / 2);
+    float fs, fx;
+    lift_factors<MODE>(p, at.b, &fs, &fx);
+    const float alpha = p.alpha * fs, beta = p.beta * fx;
+    float* sums = reinterpret_cast<float*>(raw + (base - smem_u32(raw)));
+#pragma unroll 1
+    for (int c = col; c < col + SP_TILE / 2; c += 32) {
+        float v[32];
+        const uint32_t src = tmem + c + ((uint32_t)(quad * 32) << 16);
+        tmem_ld32(src, reinterpret_cast<uint32_t*>(v));
+        if (EXACT) {
+            for (int a = 1; a <= BIG; ++a) {
+                if (a < BIG && a >= n) continue;
+                float w[32];
+                tmem_ld32(src + a * SP_TILE, reinterpret_cast<uint32_t*>(w));
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] += w[j];
+            }
+        }
+        float* to = sums + (quad * 32 + lane) * SP_LD + c;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4*>(to + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    }
+    if (split > 1) cluster_sync();
+    else __syncthreads();
+
+    // This block's rows, one per warp at a time (512 contiguous bytes from
+    // each block); the mirror image is turned in shared memory.
+    const int rows = SP_TILE / (int)split, pitch = rows + 8;
+    const bool mirror = MODE <= MU_SQUARE && at.m != at.n;
+    __half* turned = reinterpret_cast<__half*>(sums + SP_TILE * SP_LD);    // [hi, lo][128][pitch]
+    const uint32_t mine = smem_u32(sums);
+    const int64_t c0 = at.n + lane * 4;
+    constexpr int U = 4;
+    for (int r0 = warp; r0 < rows; r0 += U * SP_THREADS / 32) {
+        float4 x[U];
+        uint2 h[U], l[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = rank * rows + r0 + u * (SP_THREADS / 32);
+            const int64_t row = at.m + r, o = at.b * p.stride + row * p.ld + c0;
+            h[u] = l[u] = make_uint2(0, 0);
+            if (MODE != MU_GRAM && r0 + u * (SP_THREADS / 32) < rows && row < p.M && c0 < p.N) {
+                h[u] = *reinterpret_cast<const uint2*>(p.src[0] + o);
+                if (EXACT || MODE >= MU_UPDATE)
+                    l[u] = *reinterpret_cast<const uint2*>(p.src[1] + o);
+            }
+            x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (split == 1) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                x[u] = *reinterpret_cast<const float4*>(
+                    sums + (r0 + u * (SP_THREADS / 32)) * SP_LD + lane * 4);
+        } else {
+#pragma unroll 1
+            for (uint32_t q = 0; q < split; ++q) {
+                const uint32_t from = in_block(
+                    mine + (uint32_t)((rank * rows + r0) * SP_LD + lane * 4) * 4, q);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (r0 + u * (SP_THREADS / 32) >= rows) continue;
+                    float4 y;
+                    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                 : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
+                                 : "r"(from + (uint32_t)(u * (SP_THREADS / 32) * SP_LD * 4)));
+                    x[u].x += y.x;
+                    x[u].y += y.y;
+                    x[u].z += y.z;
+                    x[u].w += y.w;
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * (SP_THREADS / 32);
+            if (r >= rows) continue;
+            float* v = reinterpret_cast<float*>(&x[u]);
+            epilogue4<EXACT, MODE>(p, at, alpha, beta, at.m + rank * rows + r, c0, h[u], l[u], v);
+            if (mirror) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    turned[(lane * 4 + j) * pitch + r] = __float2half_rn(v[j]);
+                    if (EXACT)
+                        turned[(SP_TILE + lane * 4 + j) * pitch + r] = __float2half_rn(below_half(v[j]));
+                }
+            }
+        }
+    }
+    if (mirror) {
+        __syncthreads();
+        const int groups = rows / 8;
+        const int64_t row0 = at.m + rank * rows;
+        for (int g = (int)threadIdx.x; g < groups * SP_TILE; g += SP_THREADS) {
+            const int c = g / groups, r = g % groups * 8;
+            if (row0 + r >= p.M) continue;
+            // (a row of dst is padded to 64 columns)
+            const int64_t o = at.b * p.stride + (at.n + c) * p.ld + row0 + r;
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q)
+                *reinterpret_cast<uint4*>(p.dst[q] + o) =
+                    *reinterpret_cast<const uint4*>(turned + (q * SP_TILE + c) * pitch + r);
+        }
+    }
+    if (split > 1) cluster_sync();     // no block leaves while its sums are read
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(COLS));
 }
 
 }  // namespace tke

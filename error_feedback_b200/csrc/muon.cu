@@ -146,6 +146,23 @@ bool encode(EncodeFn fn, CUtensorMap* map, void* base, int64_t cols, int64_t row
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Calls f with the pair and split kernels of a precision and mode.
+template <bool EXACT, typename F>
+cudaError_t with_mode(int mode, F f) {
+    switch (mode) {
+        case MU_GRAM: return f(muon_gemm_kernel<EXACT, MU_GRAM>, muon_split_kernel<EXACT, MU_GRAM>);
+        case MU_SQUARE:
+            return f(muon_gemm_kernel<EXACT, MU_SQUARE>, muon_split_kernel<EXACT, MU_SQUARE>);
+        case MU_UPDATE:
+            return f(muon_gemm_kernel<EXACT, MU_UPDATE>, muon_split_kernel<EXACT, MU_UPDATE>);
+        default: return f(muon_gemm_kernel<EXACT, MU_LAST>, muon_split_kernel<EXACT, MU_LAST>);
+    }
+}
+template <typename F>
+cudaError_t with_kernel(bool exact, int mode, F f) {
+    return exact ? with_mode<true>(mode, f) : with_mode<false>(mode, f);
+}
+
 // Block pairs that the current device runs at once; its kernels' shared memory
 // is set the first time.
 cudaError_t muon_device(int* pairs) {
@@ -155,22 +172,48 @@ cudaError_t muon_device(int* pairs) {
     if (e != cudaSuccess) return e;
     const bool keep = dev >= 0 && dev < 64;
     if (keep && (*pairs = known[dev].load()) > 0) return cudaSuccess;
-    if ((e = cudaFuncSetAttribute(muon_gemm_kernel<true>,
-                                  cudaFuncAttributeMaxDynamicSharedMemorySize, GM_SMEM)) !=
-        cudaSuccess)
-        return e;
-    if ((e = cudaFuncSetAttribute(muon_gemm_kernel<false>,
-                                  cudaFuncAttributeMaxDynamicSharedMemorySize, GM_SMEM)) !=
-        cudaSuccess)
-        return e;
+    for (int exact = 0; exact < 2; ++exact)
+        for (int mode = MU_GRAM; mode <= MU_LAST; ++mode) {
+            e = with_kernel(exact != 0, mode, [&](auto pair, auto split) {
+                const cudaError_t r = cudaFuncSetAttribute(
+                    pair, cudaFuncAttributeMaxDynamicSharedMemorySize, GM_SMEM);
+                return r != cudaSuccess ? r
+                                        : cudaFuncSetAttribute(
+                                              split, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              sp_smem(exact != 0));
+            });
+            if (e != cudaSuccess) return e;
+        }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(GM_THREADS);
     cfg.dynamicSmemBytes = GM_SMEM;
-    e = cudaOccupancyMaxActiveClusters(pairs, muon_gemm_kernel<false>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(pairs, muon_gemm_kernel<false, MU_UPDATE>, &cfg);
     if (e == cudaSuccess && *pairs < 1) e = cudaErrorNotSupported;
     if (e == cudaSuccess && keep) known[dev].store(*pairs);
     return e;
+}
+
+#ifndef MU_LARGE
+#define MU_LARGE 74
+#endif
+
+cudaError_t launch_split(bool exact, unsigned tiles, unsigned parts, cudaStream_t st,
+                         const GemmParams& g) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(tiles * parts);
+    cfg.blockDim = dim3(SP_THREADS);
+    cfg.dynamicSmemBytes = sp_smem(exact);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {parts, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return with_kernel(exact, g.mode,
+                       [&](auto, auto split) { return cudaLaunchKernelEx(&cfg, split, g); });
 }
 
 template <typename F>
@@ -287,17 +330,34 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
         g.batch = B;
         g.ctrl = pp.ctrl;
         g.lift = pp.lift;
-        g.tiles_m = (int32_t)ceil_div64(g.M, GM_TILE);
-        g.tiles_n = (int32_t)ceil_div64(g.N, GM_TILE);
-        int64_t tiles = (int64_t)g.tiles_m * g.tiles_n;
-        if (g.mode <= MU_SQUARE) tiles = (int64_t)g.tiles_m * (g.tiles_m + 1) / 2;
-        if (tiles * B > MAX_N) return cudaErrorInvalidValue;
-        g.tiles = (int32_t)tiles;
-        const unsigned grid = 2u * (unsigned)std::min<int64_t>(tiles * B, pairs);
-        trace_before(st, "muon_gemm_kernel");
-        const cudaError_t r =
-            exact ? launch_pdl(muon_gemm_kernel<true>, grid, GM_THREADS, st, g, GM_SMEM)
-                  : launch_pdl(muon_gemm_kernel<false>, grid, GM_THREADS, st, g, GM_SMEM);
+        auto cut = [&](int size) {
+            g.tiles_m = (int32_t)ceil_div64(g.M, size);
+            g.tiles_n = (int32_t)ceil_div64(g.N, size);
+            return g.mode <= MU_SQUARE ? (int64_t)g.tiles_m * (g.tiles_m + 1) / 2
+                                       : (int64_t)g.tiles_m * g.tiles_n;
+        };
+        const int64_t kblocks = ceil_div64(g.K, GM_K);
+        int64_t tiles = cut(SP_TILE);
+        if (tiles * B > MAX_N / 8) return cudaErrorInvalidValue;
+        int split = 1;
+        while (split < SP_MAX_SPLIT && tiles * B * split * 2 <= 2 * pairs && kblocks >= split * 4)
+            split *= 2;
+        const bool long_sums = exact && kblocks > (int64_t)split * SP_MAX_SUM;
+        cudaError_t r;
+        if (long_sums || cut(GM_TILE) * B >= MU_LARGE) {
+            tiles = cut(GM_TILE);
+            g.tiles = (int32_t)tiles;
+            const unsigned grid = 2u * (unsigned)std::min<int64_t>(tiles * B, pairs);
+            trace_before(st, "muon_gemm_kernel");
+            r = with_kernel(exact, g.mode, [&](auto pair, auto) {
+                return launch_pdl(pair, grid, GM_THREADS, st, g, GM_SMEM);
+            });
+        } else {
+            cut(SP_TILE);
+            g.tiles = (int32_t)tiles;
+            trace_before(st, "muon_split_kernel");
+            r = launch_split(exact, (unsigned)(tiles * B), (unsigned)split, st, g);
+        }
         trace_after(st);
         return r;
     };
