@@ -28,12 +28,31 @@ template <typename T>
 struct Vec8 {
     uint4 q[sizeof(T) / 2];
 };
+// 32 bytes of one lane in one access where they are aligned to it: two of 16 at
+// a stride of 32 would touch every sector twice (a fill of 2 GB: 4.2 against
+// 6.4 TB/s).
+__device__ __forceinline__ void load32b(const void* p, uint4* q) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(q[0].x), "=r"(q[0].y), "=r"(q[0].z), "=r"(q[0].w), "=r"(q[1].x),
+                   "=r"(q[1].y), "=r"(q[1].z), "=r"(q[1].w)
+                 : "l"(p));
+}
+__device__ __forceinline__ void store32b(void* p, const uint4* q) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(q[0].x),
+                 "r"(q[0].y), "r"(q[0].z), "r"(q[0].w), "r"(q[1].x), "r"(q[1].y), "r"(q[1].z),
+                 "r"(q[1].w)
+                 : "memory");
+}
 template <typename T>
 __device__ __forceinline__ Vec8<T> load8(const T* p) {
     Vec8<T> v;
     const uint4* s = reinterpret_cast<const uint4*>(p);
+    if (sizeof(T) == 4 && (uintptr_t)p % 32 == 0) {
+        load32b(p, v.q);
+    } else {
 #pragma unroll
-    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) v.q[i] = s[i];
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) v.q[i] = s[i];
+    }
     return v;
 }
 template <typename T>
@@ -46,8 +65,12 @@ __device__ __forceinline__ void store8(T* p, const float* x) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) reinterpret_cast<T*>(&v)[j] = from_f32<T>(x[j]);
     uint4* d = reinterpret_cast<uint4*>(p);
+    if (sizeof(T) == 4 && (uintptr_t)p % 32 == 0) {
+        store32b(p, v.q);
+    } else {
 #pragma unroll
-    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) d[i] = v.q[i];
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) d[i] = v.q[i];
+    }
 }
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

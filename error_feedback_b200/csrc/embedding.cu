@@ -2,7 +2,7 @@
 // (include/topk_ef.h): argument checks, workspace layout, launch sequences.
 //
 //   embedding_lookup:     lookup_kernel
-//   embedding_grad*:      per 9-bit digit of the id (sort_count_kernel ->
+//   embedding_grad*:      rank_kernel (short lists), or per 9-bit digit of the id (sort_count_kernel ->
 //                         [sort_prefix_kernel, many tiles] -> sort_scatter_kernel)
 //                         -> grad_sum_kernel -> grad_combine_kernel
 #include <cuda_runtime.h>
@@ -51,7 +51,7 @@ cudaError_t with_type(int32_t t, F f) {
 int32_t tile_positions(int64_t T) { return T <= 4096 ? 8 : T <= 262144 ? 32 : EG_MAX_C; }
 
 struct GLayout {
-    size_t ctrl, list_count, bitmap, zero_end, word_prefix, totals, counts, key[2], pos[2], list,
+    size_t ctrl, list_count, bitmap, zero_end, word_prefix, totals, counts, key[2], pos[2], list[2],
         head, tail, total;
     int64_t sort_tiles, tiles, Dp;
     int32_t C;
@@ -71,7 +71,7 @@ GLayout grad_layout(int64_t T, int64_t V, int64_t D) {
         return at;
     };
     L.ctrl = take(sizeof(Ctrl));
-    L.list_count = take(sizeof(uint32_t));
+    L.list_count = take(2 * sizeof(uint32_t));
     L.bitmap = take(words);
     L.zero_end = o;
     L.word_prefix = take(words);
@@ -81,7 +81,8 @@ GLayout grad_layout(int64_t T, int64_t V, int64_t D) {
         L.key[i] = take((size_t)T * 4);
         L.pos[i] = take((size_t)T * 4);
     }
-    L.list = take((size_t)L.tiles * 4);
+    L.list[0] = take((size_t)L.tiles * 8);
+    L.list[1] = take(((size_t)L.tiles / EC_LONG + 1) * 8);
     L.head = take((size_t)L.tiles * L.Dp * 4);
     L.tail = take((size_t)L.tiles * L.Dp * 4);
     L.total = o;
@@ -130,7 +131,9 @@ int grad_call(const void* dy, int32_t dy_type, int64_t ld_dy, const void* ids, i
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const GLayout L = grad_layout(T, V, D);
     char* w = static_cast<char*>(ws);
-    cudaError_t e = cudaMemsetAsync(w, 0, L.zero_end, st);
+    const bool brief = T > 0 && T <= SR_MAX;
+    cudaError_t e = cudaSuccess;
+    if (!brief) e = cudaMemsetAsync(w, 0, L.zero_end, st);
     if (e == cudaSuccess && rows && T == 0) e = cudaMemsetAsync(out_count, 0, 4, st);
     if (e != cudaSuccess) return cuda_fail(e);
 
@@ -148,7 +151,37 @@ int grad_call(const void* dy, int32_t dy_type, int64_t ld_dy, const void* ids, i
     sp.padding = padding;
     sp.tiles = (int32_t)L.sort_tiles;
     int cur = 0;
-    if (T > 0) {
+    if (brief) {
+        RankParams rp = {};
+        rp.ids = ids;
+        rp.key = reinterpret_cast<uint32_t*>(w + L.key[0]);
+        rp.pos = reinterpret_cast<uint32_t*>(w + L.pos[0]);
+        rp.list_count = reinterpret_cast<uint32_t*>(w + L.list_count);
+        rp.ctrl = sp.ctrl;
+        rp.T = T;
+        rp.V = V;
+        rp.padding = padding;
+        rp.rank_blocks = (int32_t)ceil_div64(T, SR_KEYS);
+        int64_t blocks = rp.rank_blocks;
+        if (fill) {
+            rp.out = out;
+            rp.D = D;
+            rp.ld_out = ld_out;
+            rp.fill_rows = std::max<int64_t>(SR_THREADS / 32, EG_FILL_BYTES / (D * (int64_t)so));
+            blocks += ceil_div64(V, rp.fill_rows);
+        }
+        if (blocks > MAX_N) return TOPK_EF_ERR_INVALID_ARG;
+        trace_before(st, "rank_kernel");
+        e = with_type(out_type, [&](auto to) {
+            using TO = decltype(to);
+            return id_bytes == 8
+                       ? launch_pdl(rank_kernel<int64_t, TO>, (unsigned)blocks, SR_THREADS, st, rp)
+                       : launch_pdl(rank_kernel<int32_t, TO>, (unsigned)blocks, SR_THREADS, st, rp);
+        });
+        trace_after(st);
+        if (e != cudaSuccess) return cuda_fail(e);
+        sp.word_prefix = nullptr;
+    } else if (T > 0) {
         int bits = 1;
         while (bits < 32 && ((uint64_t)V >> bits) != 0) ++bits;
         const int passes = (bits + ES_BITS - 1) / ES_BITS;
@@ -173,9 +206,10 @@ int grad_call(const void* dy, int32_t dy_type, int64_t ld_dy, const void* ids, i
     p.bitmap = reinterpret_cast<uint32_t*>(w + L.bitmap);
     p.word_prefix = sp.word_prefix;
     p.out_rows = rows ? out_rows : nullptr;
+    p.out_count = out_count;
     p.head = reinterpret_cast<float*>(w + L.head);
     p.tail = reinterpret_cast<float*>(w + L.tail);
-    p.list = reinterpret_cast<uint32_t*>(w + L.list);
+    for (int i = 0; i < 2; ++i) p.list[i] = reinterpret_cast<uint2*>(w + L.list[i]);
     p.list_count = reinterpret_cast<uint32_t*>(w + L.list_count);
     p.T = T;
     p.V = V;
@@ -190,7 +224,7 @@ int grad_call(const void* dy, int32_t dy_type, int64_t ld_dy, const void* ids, i
     p.accumulate = accumulate ? 1 : 0;
     p.scale = scale;
     int64_t fill_blocks = 0;
-    if (fill) {
+    if (fill && !brief) {
         p.fill_rows = std::max<int64_t>(EG_THREADS / 32, EG_FILL_BYTES / (D * (int64_t)so));
         fill_blocks = ceil_div64(V, p.fill_rows);
     }
@@ -208,7 +242,8 @@ int grad_call(const void* dy, int32_t dy_type, int64_t ld_dy, const void* ids, i
                     : launch_pdl(grad_sum_kernel<TD, TO, false>, (unsigned)grid, EG_THREADS, st, p);
             trace_after(st);
             if (r != cudaSuccess || L.tiles < 2) return r;
-            const int64_t most = (L.tiles - 1) * std::max<int64_t>(1, ceil_div64(D, EC_COLS));
+            // runs that cross tiles, and the columns of each that a block takes
+            const int64_t most = (L.tiles - 1) * ceil_div64(D, EC_LONG_COLS);
             const int gc = (int)std::min<int64_t>(148 * 8, std::max<int64_t>(1, most));
             trace_before(st, "grad_combine_kernel");
             r = launch_pdl(grad_combine_kernel<TO>, gc, EC_THREADS, st, p);

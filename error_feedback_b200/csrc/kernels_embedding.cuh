@@ -117,15 +117,16 @@ __global__ void __launch_bounds__(LK_THREADS) lookup_kernel(const LookupParams p
 // ----------------------------------------------------- sort of the positions
 
 // Least-significant-digit radix sort of (key, position), 9 bits a pass:
-// counting and scattering kernels over tiles of 4,096 keys.  A key is the id,
+// counting and scattering kernels over tiles of 2,048 keys.  A key is the id,
 // or V (which sorts last) for the padding id and for ids outside [0, V).
 constexpr int ES_BITS = 9;
 constexpr int ES_BINS = 1 << ES_BITS;
 constexpr int ES_THREADS = 512;
 constexpr int ES_WARPS = ES_THREADS / 32;
-constexpr int ES_TILE = 4096;
+constexpr int ES_TILE = 2048;
 constexpr int ES_ROUNDS = ES_TILE / ES_THREADS;     // keys per thread
-constexpr int ES_SCAN_TILES = 32;                   // more tiles: prefixes by their own kernel
+constexpr int ES_WORDS = 256;
+constexpr int ES_SCAN_TILES = 64;                   // more tiles: prefixes by their own kernel
 static_assert(ES_BINS == ES_THREADS, "one thread per bin");
 
 struct SortParams {
@@ -153,34 +154,57 @@ __device__ __forceinline__ uint32_t sort_key(const TI* ids, int64_t t, int64_t V
     return (out || id == padding) ? (uint32_t)V : (uint32_t)id;
 }
 
+__device__ __forceinline__ void set_bits(uint32_t* word, uint32_t bits) {
+    if ((__ldcg(word) & bits) != bits) atomicOr(word, bits);
+}
+
+// Frequent ids would have every block set the same few words at once: each
+// block gathers its bits in shared memory first, one word to a slot (a word
+// whose slot another has taken goes to memory directly).
 template <typename TI, bool FIRST>
 __global__ void __launch_bounds__(ES_THREADS) sort_count_kernel(const SortParams p) {
     __shared__ uint32_t hist[ES_BINS];
+    __shared__ uint32_t s_word[ES_WORDS], s_bits[ES_WORDS];
     pdl_launch();
     hist[threadIdx.x] = 0;
+    if (FIRST && threadIdx.x < ES_WORDS) {
+        s_word[threadIdx.x] = 0xFFFFFFFFu;
+        s_bits[threadIdx.x] = 0;
+    }
     pdl_wait();
     __syncthreads();
     const int64_t base = (int64_t)blockIdx.x * ES_TILE;
 #pragma unroll
     for (int r = 0; r < ES_ROUNDS; ++r) {
         const int64_t t = base + r * ES_THREADS + threadIdx.x;
+        uint32_t key = 0;
         if (t < p.T) {
-            uint32_t key;
             if (FIRST) {
                 bool bad;
                 key = sort_key(static_cast<const TI*>(p.ids), t, p.V, p.padding, bad);
                 if (bad) atomicOr(&p.ctrl->status, ST_BAD_INPUT);
                 if (p.bitmap && key < (uint32_t)p.V) {
-                    const uint32_t bit = 1u << (key & 31);
-                    if (!(__ldcg(&p.bitmap[key >> 5]) & bit)) atomicOr(&p.bitmap[key >> 5], bit);
+                    const uint32_t word = key >> 5, bit = 1u << (key & 31);
+                    volatile uint32_t* slot = &s_word[word % ES_WORDS];
+                    if (*slot == 0xFFFFFFFFu)
+                        atomicCAS(&s_word[word % ES_WORDS], 0xFFFFFFFFu, word);
+                    if (*slot == word) {
+                        volatile uint32_t* bits = &s_bits[word % ES_WORDS];
+                        if (!(*bits & bit)) atomicOr(&s_bits[word % ES_WORDS], bit);
+                    } else {
+                        set_bits(&p.bitmap[word], bit);
+                    }
                 }
             } else {
                 key = p.key_in[t];
             }
-            atomicAdd(&hist[(key >> p.shift) & (ES_BINS - 1)], 1u);
         }
+        // (frequent ids share their digits: one add for the lanes of a bin)
+        warp_agg_inc(hist, (key >> p.shift) & (ES_BINS - 1), t < p.T);
     }
     __syncthreads();
+    if (FIRST && p.bitmap && threadIdx.x < ES_WORDS && s_bits[threadIdx.x])
+        set_bits(&p.bitmap[s_word[threadIdx.x]], s_bits[threadIdx.x]);
     p.counts[(int64_t)blockIdx.x * ES_BINS + threadIdx.x] = hist[threadIdx.x];
 }
 
@@ -210,13 +234,23 @@ __global__ void __launch_bounds__(1024) sort_prefix_kernel(const SortParams p) {
 // Number of ids that occur below every 32-id word of the bitmap, and in all.
 __device__ __forceinline__ void bitmap_prefix(const SortParams& p, uint32_t* s_red) {
     const int64_t words = ceil_div64(p.V, 32);
+    constexpr int PER = 8;
     uint32_t run = 0;
-    for (int64_t w0 = 0; w0 < words; w0 += ES_THREADS) {
-        const int64_t w = w0 + threadIdx.x;
-        const uint32_t c = w < words ? (uint32_t)__popc(__ldcg(&p.bitmap[w])) : 0u;
+    for (int64_t w0 = 0; w0 < words; w0 += ES_THREADS * PER) {
+        const int64_t w = w0 + (int64_t)threadIdx.x * PER;
+        uint32_t c[PER], sum = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            c[j] = w + j < words ? (uint32_t)__popc(__ldcg(&p.bitmap[w + j])) : 0u;
+            sum += c[j];
+        }
         uint32_t tot;
-        const uint32_t ex = block_excl_scan(c, s_red, &tot);
-        if (w < words) p.word_prefix[w] = run + ex;
+        uint32_t ex = run + block_excl_scan(sum, s_red, &tot);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            if (w + j < words) p.word_prefix[w + j] = ex;
+            ex += c[j];
+        }
         run += tot;
     }
     if (threadIdx.x == 0) *p.out_count = (int32_t)run;
@@ -224,21 +258,18 @@ __device__ __forceinline__ void bitmap_prefix(const SortParams& p, uint32_t* s_r
 
 // Stable scatter of one tile: the place of a key is the number of keys with a
 // smaller digit, plus those of the same digit in earlier tiles, in earlier
-// warps (each warp has a contiguous 256 keys) and earlier in this warp.
+// warps (each warp has a contiguous 128 keys) and earlier in this warp.
 template <typename TI, bool FIRST>
 __global__ void __launch_bounds__(ES_THREADS) sort_scatter_kernel(const SortParams p) {
-    __shared__ uint32_t hist[ES_WARPS][ES_BINS];
+    __shared__ __align__(16) uint32_t hist[ES_WARPS][ES_BINS];
     __shared__ uint32_t s_red[33];
     pdl_launch();
     const int tid = (int)threadIdx.x, lane = (int)lane_id(), warp = (int)warp_id();
-#pragma unroll
-    for (int w = 0; w < ES_WARPS; ++w) hist[w][tid] = 0;
     pdl_wait();
     if (FIRST && (int)blockIdx.x == p.tiles) {
         bitmap_prefix(p, s_red);
         return;
     }
-    __syncthreads();
     const int64_t base = (int64_t)blockIdx.x * ES_TILE + warp * (ES_TILE / ES_WARPS);
     uint32_t key[ES_ROUNDS], pos[ES_ROUNDS], rank[ES_ROUNDS];
 #pragma unroll
@@ -262,15 +293,36 @@ __global__ void __launch_bounds__(ES_THREADS) sort_scatter_kernel(const SortPara
         before = p.counts[(int64_t)blockIdx.x * ES_BINS + tid];
         total = p.totals[tid];
     } else {
-#pragma unroll 8
-        for (int t = 0; t < p.tiles; ++t) {
-            const uint32_t c = p.counts[t * ES_BINS + tid];
-            total += c;
-            before += t < (int)blockIdx.x ? c : 0u;
+        // each quarter of the block sums every fourth tile, four bins a thread
+        const int g = tid >> 7, q = tid & 127;
+        uint4 tot = make_uint4(0, 0, 0, 0), bef = tot;
+#pragma unroll 16
+        for (int t = g; t < p.tiles; t += 4) {
+            const uint4 c = *reinterpret_cast<const uint4*>(p.counts + t * ES_BINS + 4 * q);
+            const uint32_t m = t < (int)blockIdx.x ? 0xFFFFFFFFu : 0u;
+            tot.x += c.x;
+            tot.y += c.y;
+            tot.z += c.z;
+            tot.w += c.w;
+            bef.x += c.x & m;
+            bef.y += c.y & m;
+            bef.z += c.z & m;
+            bef.w += c.w & m;
+        }
+        reinterpret_cast<uint4*>(hist[g])[q] = tot;
+        reinterpret_cast<uint4*>(hist[4 + g])[q] = bef;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            total += hist[i][tid];
+            before += hist[4 + i][tid];
         }
     }
     uint32_t all;
     before += block_excl_scan(total, s_red, &all);
+#pragma unroll
+    for (int w = 0; w < ES_WARPS; ++w) hist[w][tid] = 0;
+    __syncthreads();
 #pragma unroll
     for (int r = 0; r < ES_ROUNDS; ++r) {
         const bool live = base + r * 32 + lane < p.T;
@@ -307,11 +359,103 @@ __global__ void __launch_bounds__(ES_THREADS) sort_scatter_kernel(const SortPara
     }
 }
 
+// ------------------------------------------------------------- short lists
+
+// Up to SR_MAX positions are sorted by one kernel: every block counts, for
+// its own keys, the keys that come before them among all (the whole list is
+// read by every block; T^2 comparisons over all SMs).  Blocks after the
+// ranking ones write the zeros of a dense gradient in the meantime.
+constexpr int SR_THREADS = 256;
+constexpr int SR_MAX = 8192;
+constexpr int SR_KEYS = 64;            // keys of one block, 4 threads each
+
+struct RankParams {
+    const void* ids;
+    uint32_t* key;                 // sorted
+    uint32_t* pos;
+    uint32_t* list_count;
+    Ctrl* ctrl;
+    int64_t T, V, padding;
+    int32_t rank_blocks;
+    void* out;                     // dense gradient to clear, or null
+    int64_t D, ld_out, fill_rows;
+};
+
+template <typename TO>
+__device__ __forceinline__ void zero_row(TO* dst, int64_t D, int lane) {
+    if ((uintptr_t)dst % 16 == 0) {
+        constexpr int E = 16 / (int)sizeof(TO);
+        const int64_t whole = D / E;
+        for (int64_t c = lane; c < whole; c += 32)
+            reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
+        for (int64_t c = whole * E + lane; c < D; c += 32) dst[c] = from_f32<TO>(0.0f);
+    } else {
+        for (int64_t c = lane; c < D; c += 32) dst[c] = from_f32<TO>(0.0f);
+    }
+}
+
+template <typename TI, typename TO>
+__global__ void __launch_bounds__(SR_THREADS) rank_kernel(const RankParams p) {
+    __shared__ __align__(16) uint32_t s_key[SR_MAX];
+    pdl_launch();
+    pdl_wait();
+    const int tid = (int)threadIdx.x;
+    if ((int)blockIdx.x >= p.rank_blocks) {
+        const int64_t r0 = ((int64_t)blockIdx.x - p.rank_blocks) * p.fill_rows;
+        const int64_t r1 = min(p.V, r0 + p.fill_rows);
+        for (int64_t v = r0 + warp_id(); v < r1; v += SR_THREADS / 32)
+            zero_row(static_cast<TO*>(p.out) + v * p.ld_out, p.D, (int)lane_id());
+        return;
+    }
+    const int T = (int)p.T, T4 = (T + 3) / 4;
+    int bad_any = 0;
+    for (int t = tid; t < T4 * 4; t += SR_THREADS) {
+        bool bad = false;
+        s_key[t] = t < T ? sort_key(static_cast<const TI*>(p.ids), t, p.V, p.padding, bad)
+                         : 0xFFFFFFFFu;
+        bad_any |= bad;
+    }
+    bad_any = __syncthreads_or(bad_any);
+    if (blockIdx.x == 0 && tid == 0) {
+        p.ctrl->path_small = 0;
+        p.ctrl->status = bad_any ? ST_BAD_INPUT : 0u;
+        p.list_count[0] = p.list_count[1] = 0;
+    }
+    // four neighbouring threads share a key and take every fourth quadruple
+    const int t = (int)blockIdx.x * SR_KEYS + tid / 4;
+    const uint32_t mine = t < T ? s_key[t] : 0;
+    const uint4* all = reinterpret_cast<const uint4*>(s_key);
+    uint32_t before = 0;
+    // earlier positions come first among equals: key <= mine there, key < mine after
+    const int split = min(t, T) / 4;
+#pragma unroll 4
+    for (int j = tid & 3; j < split; j += 4) {
+        const uint4 k = all[j];
+        before += (k.x <= mine) + (k.y <= mine) + (k.z <= mine) + (k.w <= mine);
+    }
+    if ((tid & 3) == 0) {
+        for (int j = split * 4; j < min(split * 4 + 4, T); ++j)
+            before += j < t ? s_key[j] <= mine : s_key[j] < mine;
+    }
+#pragma unroll 4
+    for (int j = split + 1 + (tid & 3); j < T4; j += 4) {
+        const uint4 k = all[j];
+        before += (k.x < mine) + (k.y < mine) + (k.z < mine) + (k.w < mine);
+    }
+    before += __shfl_xor_sync(0xFFFFFFFFu, before, 1);
+    before += __shfl_xor_sync(0xFFFFFFFFu, before, 2);
+    if (t < T && (tid & 3) == 0) {
+        p.key[before] = mine;
+        p.pos[before] = (uint32_t)t;
+    }
+}
+
 // ------------------------------------------------------------------ the sums
 
 constexpr int EG_THREADS = 128;
 constexpr int EG_COLS = EG_THREADS * 8;    // columns of one block
 constexpr int EG_MAX_C = 128;              // positions of one tile, at most
+constexpr int EC_LONG = 16;                // a run over more tiles is added up by a whole block
 constexpr int64_t EG_FILL_BYTES = 32768;   // zeros written by one fill block
 
 struct GradParams {
@@ -324,8 +468,9 @@ struct GradParams {
     int32_t* out_rows;             // row-sparse output, or null
     float* head;                   // [tiles][Dp]: run continued from the tile before
     float* tail;                   // [tiles][Dp]: run begun here that goes on in the next
-    uint32_t* list;                // tiles whose tail goes on
-    uint32_t* list_count;
+    int32_t* out_count;            // (short list)
+    uint2* list[2];                // tiles whose tail goes on, and the tail's row of out:
+    uint32_t* list_count;          //   short runs, long runs (EC_LONG tiles or more after it)
     int64_t T, V, D, Dp, ld_dy, ld_out;
     int64_t tiles;
     int64_t sum_blocks;            // tiles * slabs; the blocks after them fill with zeros
@@ -335,32 +480,18 @@ struct GradParams {
     float scale;
 };
 
-__device__ __forceinline__ int64_t out_row(const GradParams& p, uint32_t key) {
-    if (!p.out_rows) return (int64_t)key;
+// Row of the row-sparse output that holds `key`.
+__device__ __forceinline__ int64_t ordinal(const GradParams& p, uint32_t key) {
     const uint32_t word = p.bitmap[key >> 5];
     return (int64_t)p.word_prefix[key >> 5] + __popc(word & ((1u << (key & 31)) - 1u));
 }
 
-template <typename TO, bool VEC>
+template <typename TO>
 __device__ __forceinline__ void fill_block(const GradParams& p, int64_t f) {
-    TO* out = static_cast<TO*>(p.out);
     const int64_t r0 = f * p.fill_rows, r1 = min(p.V, r0 + p.fill_rows);
-    for (int64_t v = r0 + warp_id(); v < r1; v += EG_THREADS / 32) {
-        if (p.bitmap[v >> 5] >> (v & 31) & 1u) continue;
-        TO* dst = out + v * p.ld_out;
-        if (VEC) {
-            const float z[8] = {};
-            for (int64_t c = lane_id() * 8; c < p.D; c += 256) {
-                if (c + 8 <= p.D) {
-                    store8(dst + c, z);
-                } else {
-                    for (int64_t k = c; k < p.D; ++k) dst[k] = from_f32<TO>(0.0f);
-                }
-            }
-        } else {
-            for (int64_t c = lane_id(); c < p.D; c += 32) dst[c] = from_f32<TO>(0.0f);
-        }
-    }
+    for (int64_t v = r0 + warp_id(); v < r1; v += EG_THREADS / 32)
+        if (!(p.bitmap[v >> 5] >> (v & 31) & 1u))
+            zero_row(static_cast<TO*>(p.out) + v * p.ld_out, p.D, (int)lane_id());
 }
 
 // One block per (tile of C sorted positions, EG_COLS columns); thread j has 8
@@ -369,11 +500,12 @@ __device__ __forceinline__ void fill_block(const GradParams& p, int64_t f) {
 template <typename TD, typename TO, bool VEC>
 __global__ void __launch_bounds__(EG_THREADS) grad_sum_kernel(const GradParams p) {
     __shared__ uint32_t s_key[EG_MAX_C + 2], s_pos[EG_MAX_C];
+    __shared__ uint32_t s_red[33];
     pdl_launch();
     pdl_wait();
     const int tid = (int)threadIdx.x;
     if ((int64_t)blockIdx.x >= p.sum_blocks) {
-        fill_block<TO, VEC>(p, (int64_t)blockIdx.x - p.sum_blocks);
+        fill_block<TO>(p, (int64_t)blockIdx.x - p.sum_blocks);
         return;
     }
     const int64_t tile = (int64_t)blockIdx.x / p.slabs;
@@ -387,6 +519,19 @@ __global__ void __launch_bounds__(EG_THREADS) grad_sum_kernel(const GradParams p
         if (i < n) s_pos[i] = p.pos[start + i];
     }
     __syncthreads();
+    // row-sparse output: the rows of this tile's runs follow one another
+    int64_t row = 0;
+    if (p.out_rows) {
+        if (p.word_prefix) {
+            if (s_key[1] != none) row = ordinal(p, s_key[1]);
+        } else {
+            // short list: runs that begin before this tile, by counting
+            uint32_t heads = 0;
+            for (int64_t t = tid; t <= start; t += EG_THREADS)
+                heads += t == 0 || p.key[t] != p.key[t - 1];
+            row = (int64_t)block_sum(heads, s_red) - 1;
+        }
+    }
     const TD* dy = static_cast<const TD*>(p.dy);
     const int64_t c0 = slab * EG_COLS + (VEC ? tid * 8 : tid);
     auto col = [&](int j) { return c0 + (VEC ? j : j * EG_THREADS); };
@@ -401,10 +546,14 @@ __global__ void __launch_bounds__(EG_THREADS) grad_sum_kernel(const GradParams p
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (whole || col(j) < p.D) part[col(j)] = acc[j];
-            if (!from_before && slab == 0 && tid == 0)
-                p.list[atomicAdd(p.list_count, 1u)] = (uint32_t)tile;
+            if (!from_before && slab == 0 && tid == 0) {
+                const int64_t far = tile + EC_LONG;
+                const int l = far < p.tiles && p.key[far * p.C] == k;
+                p.list[l][atomicAdd(p.list_count + l, 1u)] =
+                    make_uint2((uint32_t)tile, p.out_rows ? (uint32_t)row : k);
+            }
         } else {
-            const int64_t row = out_row(p, k);
+            if (!p.out_rows) row = k;
             TO* dst = static_cast<TO*>(p.out) + row * p.ld_out;
             float y[8];
 #pragma unroll
@@ -422,8 +571,9 @@ __global__ void __launch_bounds__(EG_THREADS) grad_sum_kernel(const GradParams p
                     if (col(j) < p.D)
                         dst[col(j)] = from_f32<TO>(p.accumulate ? to_f32(dst[col(j)]) + y[j] : y[j]);
             }
-            if (p.out_rows && slab == 0 && tid == 0) p.out_rows[row] = (int32_t)k;
         }
+        if (p.out_rows && !from_before && slab == 0 && tid == 0) p.out_rows[row] = (int32_t)k;
+        ++row;
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
     };
@@ -469,68 +619,112 @@ __global__ void __launch_bounds__(EG_THREADS) grad_sum_kernel(const GradParams p
     int m = n;
     while (m > 0 && s_key[m] == none) --m;
     if (m > 0) flush(m - 1, first, s_key[m] == s_key[m + 1]);
+    // short list: the last run's block knows how many there are
+    if (p.out_rows && !p.word_prefix && slab == 0 && tid == 0 &&
+        (m == n ? start + n == p.T : (m > 0 || start == 0 || s_key[0] != none)))
+        *p.out_count = (int32_t)row;
 }
 
 constexpr int EC_THREADS = 256;
-constexpr int EC_COLS = 128;           // columns of one item: 32 lanes x 4
+constexpr int EC_WARPS = EC_THREADS / 32;
+constexpr int EC_COLS = 512;           // columns of a warp with a short run: 32 lanes x 4 x float4
+constexpr int EC_LONG_COLS = 128;      // columns of a block with a long run: 32 lanes x float4
 
-// Adds the partial rows of every run that crosses tiles: tail of the tile it
-// begins in, then the heads of the following tiles.  The warps take
-// contiguous parts of the list in order, and their sums are added in order.
+// The sum of partial rows [j0, j1) of the run that begins in `tile`: its tail,
+// then the heads of the following tiles.
+template <int N>
+__device__ __forceinline__ void add_parts(const GradParams& p, int64_t tile, int64_t j0, int64_t j1,
+                                          int64_t c, float4* s) {
+#pragma unroll
+    for (int u = 0; u < N; ++u) s[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll (N == 1 ? 8 : 2)
+    for (int64_t j = j0; j < j1; ++j) {
+        const float* part = (j == 0 ? p.tail : p.head) + (tile + j) * p.Dp + c;
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            if (c + u * 128 >= p.D) continue;
+            const float4 x = *reinterpret_cast<const float4*>(part + u * 128);
+            s[u].x += x.x;
+            s[u].y += x.y;
+            s[u].z += x.z;
+            s[u].w += x.w;
+        }
+    }
+}
+
+template <typename TO, int N>
+__device__ __forceinline__ void put_row(const GradParams& p, int64_t row, int64_t c, const float4* s) {
+    TO* dst = static_cast<TO*>(p.out) + row * p.ld_out + c;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        const float y[4] = {p.scale * s[u].x, p.scale * s[u].y, p.scale * s[u].z, p.scale * s[u].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = u * 128 + j;
+            if (c + k < p.D) dst[k] = from_f32<TO>(p.accumulate ? to_f32(dst[k]) + y[j] : y[j]);
+        }
+    }
+}
+
+// Number of tiles that the run of the last key of `tile` touches from it on:
+// 32 probes at a time at the first keys of tiles, first of the next 32 tiles,
+// then ever finer between the last hit and the first miss.
+__device__ __forceinline__ int64_t run_tiles(const GradParams& p, int64_t tile) {
+    const uint32_t k = p.key[(tile + 1) * p.C - 1];
+    int64_t hit = tile, miss = p.tiles;
+    for (int64_t step = 1; miss - hit > 1;) {
+        const int64_t at = hit + (lane_id() + 1) * step;
+        const bool in = at < miss && p.key[at * p.C] == k;
+        const int n = __popc(__ballot_sync(0xFFFFFFFFu, in));   // (hits come first)
+        if (n < 32) miss = min(miss, hit + (n + 1) * step);
+        hit += n * step;
+        step = max((int64_t)1, (miss - hit) / 32);
+    }
+    return hit - tile + 1;
+}
+
+// Adds the partial rows of every run that crosses tiles, in tile order.  Long
+// runs (a frequent id): a block takes 128 columns, its warps contiguous parts
+// of the run, and their sums are added in order.  Short ones, two or three
+// partial rows as a rule: a warp takes 512 columns.
 template <typename TO>
 __global__ void __launch_bounds__(EC_THREADS) grad_combine_kernel(const GradParams p) {
-    __shared__ float4 s_part[EC_THREADS / 32][32];
+    __shared__ float4 s_part[EC_WARPS][32];
     pdl_launch();
     pdl_wait();
     const int lane = (int)lane_id(), warp = (int)warp_id();
-    constexpr int W = EC_THREADS / 32;
-    const int64_t slabs = max((int64_t)1, ceil_div64(p.D, EC_COLS));
-    const int64_t items = (int64_t)*p.list_count * slabs;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const int64_t tile = p.list[it / slabs];
-        const int64_t c = (it % slabs) * EC_COLS + lane * 4;
-        const uint32_t k = p.key[(tile + 1) * p.C - 1];
-        // last position of the run: upper bound of its key
-        int64_t lo = (tile + 1) * p.C, hi = p.T;
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) >> 1;
-            if (p.key[mid] <= k) lo = mid + 1; else hi = mid;
-        }
-        const int64_t parts = (lo - 1) / p.C - tile + 1;
-        const int64_t per = ceil_div64(parts, W);
-        const int64_t j0 = min(parts, warp * per), j1 = min(parts, j0 + per);
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c < p.D) {
-#pragma unroll 4
-            for (int64_t j = j0; j < j1; ++j) {
-                const float* part = (j == 0 ? p.tail : p.head) + (tile + j) * p.Dp + c;
-                const float4 x = *reinterpret_cast<const float4*>(part);
-                s.x += x.x;
-                s.y += x.y;
-                s.z += x.z;
-                s.w += x.w;
-            }
-        }
+    const int64_t long_slabs = ceil_div64(p.D, EC_LONG_COLS);
+    const int64_t long_items = (int64_t)p.list_count[1] * long_slabs;
+    for (int64_t it = blockIdx.x; it < long_items; it += gridDim.x) {
+        const int64_t run = it / long_slabs, c = (it - run * long_slabs) * EC_LONG_COLS + lane * 4;
+        const uint2 entry = p.list[1][run];
+        const int64_t parts = run_tiles(p, entry.x), per = ceil_div64(parts, EC_WARPS);
+        float4 s;
+        add_parts<1>(p, entry.x, min(parts, warp * per), min(parts, (warp + 1) * per), c, &s);
         s_part[warp][lane] = s;
         __syncthreads();
-        if (warp == 0 && c < p.D) {
+        if (warp == 0) {
             const int used = (int)ceil_div64(parts, per);
-            for (int w = 1; w < used; ++w) {
-                const float4 x = s_part[w][lane];
+            for (int q = 1; q < used; ++q) {
+                const float4 x = s_part[q][lane];
                 s.x += x.x;
                 s.y += x.y;
                 s.z += x.z;
                 s.w += x.w;
             }
-            const float y[4] = {p.scale * s.x, p.scale * s.y, p.scale * s.z, p.scale * s.w};
-            const int64_t row = out_row(p, k);
-            TO* dst = static_cast<TO*>(p.out) + row * p.ld_out;
-            for (int j = 0; j < 4; ++j)
-                if (c + j < p.D)
-                    dst[c + j] = from_f32<TO>(p.accumulate ? to_f32(dst[c + j]) + y[j] : y[j]);
-            if (p.out_rows && c == 0) p.out_rows[row] = (int32_t)k;
+            put_row<TO, 1>(p, entry.y, c, &s);
         }
         __syncthreads();
+    }
+    const int64_t slabs = ceil_div64(p.D, EC_COLS);
+    const int64_t items = (int64_t)p.list_count[0] * slabs;
+    for (int64_t it = (int64_t)blockIdx.x * EC_WARPS + warp; it < items;
+         it += (int64_t)gridDim.x * EC_WARPS) {
+        const int64_t run = it / slabs, c = (it - run * slabs) * EC_COLS + lane * 4;
+        const uint2 entry = p.list[0][run];
+        float4 s[4];
+        add_parts<4>(p, entry.x, 0, run_tiles(p, entry.x), c, s);
+        put_row<TO, 4>(p, entry.y, c, s);
     }
 }
 

@@ -371,22 +371,15 @@ __device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t, int size) 
 
 // Sixteen fp16 values, 32 bytes: one whole memory sector for each lane.
 __device__ __forceinline__ void load_half16(const __half* p, float* v) {
-    uint32_t r[8];
-    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                   "=r"(r[6]), "=r"(r[7])
-                 : "l"(p));
+    uint4 q[2];
+    load32b(p, q);
+    const __half2* h = reinterpret_cast<const __half2*>(q);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[j]));
+        const float2 f = __half22float2(h[j]);
         v[2 * j] = f.x;
         v[2 * j + 1] = f.y;
     }
-}
-__device__ __forceinline__ void store32b(void* p, const uint32_t* r) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
 }
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
     const __half2 h = __floats2half2_rn(x, y);
@@ -404,7 +397,7 @@ __device__ __forceinline__ void store_out(const GemmParams& p, int64_t b, int64_
         constexpr int E = 32 / (int)sizeof(TO);
 #pragma unroll
         for (int j = 0; j < 32; j += E) {
-            uint32_t r[8];
+            uint4 r[2];
 #pragma unroll
             for (int e = 0; e < E; ++e) reinterpret_cast<TO*>(r)[e] = from_f32<TO>(v[j + e]);
             store32b(dst + j, r);
@@ -421,15 +414,16 @@ __device__ __forceinline__ void store_pair(const GemmParams& p, int64_t o, const
                                            bool want_lo) {
 #pragma unroll
     for (int j = 0; j < 32; j += 16) {
-        uint32_t r[8];
+        uint4 q[2];
+        uint32_t* r = reinterpret_cast<uint32_t*>(q);
 #pragma unroll
         for (int e = 0; e < 8; ++e) r[e] = pack2(v[j + 2 * e], v[j + 2 * e + 1]);
-        store32b(p.dst[0] + o + j, r);
+        store32b(p.dst[0] + o + j, q);
         if (want_lo) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 r[e] = pack2(below_half(v[j + 2 * e]), below_half(v[j + 2 * e + 1]));
-            store32b(p.dst[1] + o + j, r);
+            store32b(p.dst[1] + o + j, q);
         }
     }
 }
