@@ -433,20 +433,30 @@ class _On:
             if self.stream.device != self.dev:
                 raise ValueError(f"the stream is on {self.stream.device}, not on {self.dev}")
             self.guard = torch.cuda.stream(self.stream)      # its device too
-        elif self.dev.index != torch.cuda.current_device():
+        else:
             self.guard = torch.cuda.device(self.dev)
-        if self.guard is not None:
-            self.guard.__enter__()
+        self.guard.__enter__()
         return int((self.stream or torch.cuda.current_stream()).cuda_stream)
 
     def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        self.guard.__exit__(*exc)
+
+
+def _on(device, stream, call):
+    """call(raw stream) with the device current; the usual case (its current
+    stream, on the current device) at once."""
+    if stream is None and device.index == torch._C._cuda_getDevice():
+        return call(torch._C._cuda_getCurrentRawStream(device.index))
+    with _On(device, stream) as st:
+        return call(st)
 
 
 def _on_device(ws, device):
     if ws is not None and ws.device != device:
         raise ValueError(f"ws is on {ws.device}, not on {device}")
+
+
+_LOOKUP_WS = 512                        # at least embedding_lookup_workspace_bytes()
 
 
 def embedding_lookup_workspace_bytes() -> int:
@@ -464,21 +474,26 @@ def embedding_lookup(weight, ids, scale=1.0, out=None, out_dtype=None, ws=None, 
     idb, T = _token_ids(ids, dev)
     V, D = weight.shape
     _on_device(ws, dev)
-    with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty((*ids.shape, D), dtype=out_dtype or weight.dtype, device=dev)
-        elif out_dtype is not None and out.dtype != out_dtype:
+
+    def call(st):
+        o = out
+        if o is None:
+            o = torch.empty((*ids.shape, D), dtype=out_dtype or weight.dtype, device=dev)
+        elif out_dtype is not None and o.dtype != out_dtype:
             raise ValueError("out and out_dtype differ")
-        o2 = out if out.dim() == 2 else out.view(-1, D) if out.numel() else out.new_empty((T, D))
+        o2 = o if o.dim() == 2 else o.view(-1, D) if o.numel() else o.new_empty((T, D))
         ot, ldo = _matrix(o2, "out", dev)
-        if tuple(o2.shape) != (T, D):
+        if o2.shape != (T, D):
             raise ValueError(f"out must hold [{T}, {D}] elements")
-        ws = _workspace(embedding_lookup_workspace_bytes(), dev, ws)
+        w = _workspace(_LOOKUP_WS, dev, ws)
         rc = lib().embedding_lookup(weight.data_ptr(), wt, ldw, ids.data_ptr(), idb, T, V, D,
-                                    float(scale), o2.data_ptr(), ot, ldo, ws.data_ptr(),
-                                    ws.numel() * ws.element_size(), st)
-    _check(rc, "embedding_lookup")
-    return out
+                                    scale, o2.data_ptr(), ot, ldo, w.data_ptr(),
+                                    w.numel() * w.element_size(), st)
+        if rc != OK:
+            _check(rc, "embedding_lookup")
+        return o
+
+    return _on(dev, stream, call)
 
 
 def embedding_grad_workspace_bytes(T: int, V: int, D: int) -> int:
@@ -512,23 +527,28 @@ def embedding_grad(grad_out, ids, num_rows, scale=1.0, padding_idx=-1, accumulat
     ERR_BAD_INPUT from topk_ef_last_device_status(ws)."""
     grad_out, gt, ldg, dev, idb, T, V, D, nb = _grad_args(grad_out, ids, num_rows)
     _on_device(ws, dev)
-    with _On(dev, stream) as st:
-        if out is None:
+
+    def call(st):
+        o = out
+        if o is None:
             if accumulate:
                 raise ValueError("accumulate needs out")
-            out = torch.empty((V, D), dtype=out_dtype or torch.float32, device=dev)
-        elif out_dtype is not None and out.dtype != out_dtype:
+            o = torch.empty((V, D), dtype=out_dtype or torch.float32, device=dev)
+        elif out_dtype is not None and o.dtype != out_dtype:
             raise ValueError("out and out_dtype differ")
-        ot, ldo = _matrix(out, "out", dev)
-        if tuple(out.shape) != (V, D):
+        ot, ldo = _matrix(o, "out", dev)
+        if o.shape != (V, D):
             raise ValueError(f"out must be [{V}, {D}]")
-        ws = _workspace(nb, dev, ws)
+        w = _workspace(nb, dev, ws)
         rc = lib().embedding_grad(grad_out.data_ptr(), gt, ldg, ids.data_ptr(), idb, T, V, D,
-                                  float(scale), int(padding_idx), out.data_ptr(), ot, ldo,
-                                  1 if accumulate else 0, ws.data_ptr(),
-                                  ws.numel() * ws.element_size(), st)
-    _check(rc, "embedding_grad")
-    return out
+                                  scale, int(padding_idx), o.data_ptr(), ot, ldo,
+                                  1 if accumulate else 0, w.data_ptr(),
+                                  w.numel() * w.element_size(), st)
+        if rc != OK:
+            _check(rc, "embedding_grad")
+        return o
+
+    return _on(dev, stream, call)
 
 
 def embedding_grad_rows(grad_out, ids, num_rows, scale=1.0, padding_idx=-1, out_rows=None,
@@ -540,29 +560,34 @@ def embedding_grad_rows(grad_out, ids, num_rows, scale=1.0, padding_idx=-1, out_
     grad_out, gt, ldg, dev, idb, T, V, D, nb = _grad_args(grad_out, ids, num_rows)
     _on_device(ws, dev)
     m = min(T, V)
-    with _On(dev, stream) as st:
-        if out_rows is None:
-            out_rows = torch.empty(m, dtype=torch.int32, device=dev)
-        if out_val is None:
-            out_val = torch.empty((m, D), dtype=out_dtype or torch.float32, device=dev)
-        elif out_dtype is not None and out_val.dtype != out_dtype:
+
+    def call(st):
+        rows, val, count = out_rows, out_val, out_count
+        if rows is None:
+            rows = torch.empty(m, dtype=torch.int32, device=dev)
+        if val is None:
+            val = torch.empty((m, D), dtype=out_dtype or torch.float32, device=dev)
+        elif out_dtype is not None and val.dtype != out_dtype:
             raise ValueError("out_val and out_dtype differ")
-        if out_count is None:
-            out_count = torch.empty(1, dtype=torch.int32, device=dev)
-        for t, name, least in ((out_rows, "out_rows", m), (out_count, "out_count", 1)):
+        if count is None:
+            count = torch.empty(1, dtype=torch.int32, device=dev)
+        for t, name, least in ((rows, "out_rows", m), (count, "out_count", 1)):
             if not t.is_cuda or t.device != dev or t.dtype != torch.int32 or \
                     not t.is_contiguous() or t.numel() < least:
                 raise ValueError(f"{name} must be a contiguous int32 tensor of {least} on {dev}")
-        ot, ldo = _matrix(out_val, "out_val", dev)
-        if out_val.shape[0] < m or out_val.shape[1] != D:
+        ot, ldo = _matrix(val, "out_val", dev)
+        if val.shape[0] < m or val.shape[1] != D:
             raise ValueError(f"out_val must be [{m}, {D}]")
-        ws = _workspace(nb, dev, ws)
+        w = _workspace(nb, dev, ws)
         rc = lib().embedding_grad_rows(grad_out.data_ptr(), gt, ldg, ids.data_ptr(), idb, T, V, D,
-                                       float(scale), int(padding_idx), out_rows.data_ptr(),
-                                       out_val.data_ptr(), ot, ldo, out_count.data_ptr(),
-                                       ws.data_ptr(), ws.numel() * ws.element_size(), st)
-    _check(rc, "embedding_grad_rows")
-    return out_rows, out_val, out_count
+                                       scale, int(padding_idx), rows.data_ptr(), val.data_ptr(),
+                                       ot, ldo, count.data_ptr(), w.data_ptr(),
+                                       w.numel() * w.element_size(), st)
+        if rc != OK:
+            _check(rc, "embedding_grad_rows")
+        return rows, val, count
+
+    return _on(dev, stream, call)
 
 
 # ---------------------------------------------------------------------- muon
@@ -626,24 +651,28 @@ def muon_update(grad, momentum=None, mu=0.95, nesterov=True, coefficients=MUON_C
         if momentum.shape != grad.shape or momentum.device != dev:
             raise ValueError("momentum must have grad's shape and device")
         mp = momentum.data_ptr()
-    with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty(grad.shape, dtype=out_dtype or torch.float32, device=dev)
-        elif out_dtype is not None and out.dtype != out_dtype:
+
+    def call(st):
+        o = out
+        if o is None:
+            o = torch.empty(grad.shape, dtype=out_dtype or torch.float32, device=dev)
+        elif out_dtype is not None and o.dtype != out_dtype:
             raise ValueError("out and out_dtype differ")
-        ot, ldo, so, shape = _matrices(out, "out", dev)
-        if out.shape != grad.shape:
+        ot, ldo, so, _ = _matrices(o, "out", dev)
+        if o.shape != grad.shape:
             raise ValueError("out must have grad's shape")
-        nb = int(lib().muon_workspace_bytes(B, rows, cols, ot))
+        nb = lib().muon_workspace_bytes(B, rows, cols, ot)
         if nb == 0:
             raise TopkEfError(ERR_INVALID_ARG, "muon_workspace_bytes")
-        ws = _workspace(nb, dev, ws)
-        rc = lib().muon_update(grad.data_ptr(), gt, ldg, sg, mp, B, rows, cols, float(mu),
-                               1 if nesterov else 0, float(eps), coef, steps, float(scale),
-                               out.data_ptr(), ot, ldo, so, ws.data_ptr(),
-                               ws.numel() * ws.element_size(), st)
-    _check(rc, "muon_update")
-    return out
+        w = _workspace(nb, dev, ws)
+        rc = lib().muon_update(grad.data_ptr(), gt, ldg, sg, mp, B, rows, cols, mu,
+                               1 if nesterov else 0, eps, coef, steps, scale, o.data_ptr(), ot,
+                               ldo, so, w.data_ptr(), w.numel() * w.element_size(), st)
+        if rc != OK:
+            _check(rc, "muon_update")
+        return o
+
+    return _on(dev, stream, call)
 
 
 # -------------------------------------------------------------------- status

@@ -81,8 +81,8 @@ GLayout grad_layout(int64_t T, int64_t V, int64_t D) {
         L.key[i] = take((size_t)T * 4);
         L.pos[i] = take((size_t)T * 4);
     }
-    L.list[0] = take((size_t)L.tiles * 8);
-    L.list[1] = take(((size_t)L.tiles / EC_LONG + 1) * 8);
+    L.list[0] = take((size_t)L.tiles * 16);
+    L.list[1] = take(((size_t)L.tiles / EC_LONG + 1) * 16);
     L.head = take((size_t)L.tiles * L.Dp * 4);
     L.tail = take((size_t)L.tiles * L.Dp * 4);
     L.total = o;
@@ -209,7 +209,7 @@ int grad_call(const void* dy, int32_t dy_type, int64_t ld_dy, const void* ids, i
     p.out_count = out_count;
     p.head = reinterpret_cast<float*>(w + L.head);
     p.tail = reinterpret_cast<float*>(w + L.tail);
-    for (int i = 0; i < 2; ++i) p.list[i] = reinterpret_cast<uint2*>(w + L.list[i]);
+    for (int i = 0; i < 2; ++i) p.list[i] = reinterpret_cast<uint4*>(w + L.list[i]);
     p.list_count = reinterpret_cast<uint32_t*>(w + L.list_count);
     p.T = T;
     p.V = V;
@@ -244,7 +244,7 @@ int grad_call(const void* dy, int32_t dy_type, int64_t ld_dy, const void* ids, i
             if (r != cudaSuccess || L.tiles < 2) return r;
             // runs that cross tiles, and the columns of each that a block takes
             const int64_t most = (L.tiles - 1) * ceil_div64(D, EC_LONG_COLS);
-            const int gc = (int)std::min<int64_t>(148 * 8, std::max<int64_t>(1, most));
+            const int gc = (int)std::min<int64_t>(148 * 4, std::max<int64_t>(1, most));
             trace_before(st, "grad_combine_kernel");
             r = launch_pdl(grad_combine_kernel<TO>, gc, EC_THREADS, st, p);
             trace_after(st);
@@ -292,7 +292,7 @@ int embedding_lookup(const void* weight, int32_t weight_type, int64_t ld_weight,
         const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(Ctrl), st);
         if (e != cudaSuccess) return cuda_fail(e);
     }
-    const int64_t want = std::min<int64_t>(ceil_div64(p.items, LK_THREADS / 32), 148 * 16);
+    const int64_t want = std::min<int64_t>(ceil_div64(p.items, LK_THREADS / 32), MAX_N / 2);
     const int grid = (int)std::max<int64_t>(1, want) + (p.scan ? 1 : 0);
     const bool vec = rows16(weight, ld_weight, sw) && rows16(out, ld_out, so);
     trace_before(st, "lookup_kernel");

@@ -96,20 +96,31 @@ __global__ void __launch_bounds__(LK_THREADS) lookup_kernel(const LookupParams p
                 }
             }
         } else {
-#pragma unroll
-            for (int j0 = 0; j0 < 32; j0 += 8) {
+            // rows that start anywhere: one element a lane.  (Groups of four, aligned
+            // in the output and shifted into place from aligned loads, take more
+            // instructions than they save: 43 against 28 us for 30,011 rows of 1,001
+            // fp32 to bf16.)
+            const TW* s = src + c0 + lane;
+            TO* d = dst + c0 + lane;
+            const int n = (int)min((int64_t)LK_COLS, p.D - c0);
+            int c = 0;
+            for (; c + 256 <= n; c += 256) {
                 TW v[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int64_t c = c0 + (j0 + j) * 32 + lane;
-                    if (ok && c < p.D) v[j] = src[c];
-                }
+                for (int j = 0; j < 8; ++j)
+                    if (ok) v[j] = s[c + j * 32];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int64_t c = c0 + (j0 + j) * 32 + lane;
-                    if (c < p.D) dst[c] = from_f32<TO>(ok ? p.scale * to_f32(v[j]) : 0.0f);
-                }
+                for (int j = 0; j < 8; ++j)
+                    d[c + j * 32] = from_f32<TO>(ok ? p.scale * to_f32(v[j]) : 0.0f);
             }
+            TW v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (ok && c + j * 32 + lane < n) v[j] = s[c + j * 32];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j * 32 + lane < n)
+                    d[c + j * 32] = from_f32<TO>(ok ? p.scale * to_f32(v[j]) : 0.0f);
         }
     }
 }
@@ -365,9 +376,10 @@ __global__ void __launch_bounds__(ES_THREADS) sort_scatter_kernel(const SortPara
 // its own keys, the keys that come before them among all (the whole list is
 // read by every block; T^2 comparisons over all SMs).  Blocks after the
 // ranking ones write the zeros of a dense gradient in the meantime.
-constexpr int SR_THREADS = 256;
+constexpr int SR_THREADS = 512;
 constexpr int SR_MAX = 8192;
-constexpr int SR_KEYS = 64;            // keys of one block, 4 threads each
+constexpr int SR_SHARE = 16;           // threads of one key
+constexpr int SR_KEYS = SR_THREADS / SR_SHARE;
 
 struct RankParams {
     const void* ids;
@@ -409,6 +421,7 @@ __global__ void __launch_bounds__(SR_THREADS) rank_kernel(const RankParams p) {
     }
     const int T = (int)p.T, T4 = (T + 3) / 4;
     int bad_any = 0;
+#pragma unroll 8
     for (int t = tid; t < T4 * 4; t += SR_THREADS) {
         bool bad = false;
         s_key[t] = t < T ? sort_key(static_cast<const TI*>(p.ids), t, p.V, p.padding, bad)
@@ -421,30 +434,30 @@ __global__ void __launch_bounds__(SR_THREADS) rank_kernel(const RankParams p) {
         p.ctrl->status = bad_any ? ST_BAD_INPUT : 0u;
         p.list_count[0] = p.list_count[1] = 0;
     }
-    // four neighbouring threads share a key and take every fourth quadruple
-    const int t = (int)blockIdx.x * SR_KEYS + tid / 4;
+    // neighbouring threads share a key and take turns at the quadruples
+    const int t = (int)blockIdx.x * SR_KEYS + tid / SR_SHARE, turn = tid % SR_SHARE;
     const uint32_t mine = t < T ? s_key[t] : 0;
     const uint4* all = reinterpret_cast<const uint4*>(s_key);
     uint32_t before = 0;
     // earlier positions come first among equals: key <= mine there, key < mine after
     const int split = min(t, T) / 4;
 #pragma unroll 4
-    for (int j = tid & 3; j < split; j += 4) {
+    for (int j = turn; j < split; j += SR_SHARE) {
         const uint4 k = all[j];
         before += (k.x <= mine) + (k.y <= mine) + (k.z <= mine) + (k.w <= mine);
     }
-    if ((tid & 3) == 0) {
-        for (int j = split * 4; j < min(split * 4 + 4, T); ++j)
-            before += j < t ? s_key[j] <= mine : s_key[j] < mine;
+    if (turn < 4) {
+        const int j = split * 4 + turn;
+        if (j < T) before += j < t ? s_key[j] <= mine : s_key[j] < mine;
     }
 #pragma unroll 4
-    for (int j = split + 1 + (tid & 3); j < T4; j += 4) {
+    for (int j = split + 1 + turn; j < T4; j += SR_SHARE) {
         const uint4 k = all[j];
         before += (k.x < mine) + (k.y < mine) + (k.z < mine) + (k.w < mine);
     }
-    before += __shfl_xor_sync(0xFFFFFFFFu, before, 1);
-    before += __shfl_xor_sync(0xFFFFFFFFu, before, 2);
-    if (t < T && (tid & 3) == 0) {
+#pragma unroll
+    for (int o = 1; o < SR_SHARE; o <<= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+    if (t < T && turn == 0) {
         p.key[before] = mine;
         p.pos[before] = (uint32_t)t;
     }
@@ -469,7 +482,7 @@ struct GradParams {
     float* head;                   // [tiles][Dp]: run continued from the tile before
     float* tail;                   // [tiles][Dp]: run begun here that goes on in the next
     int32_t* out_count;            // (short list)
-    uint2* list[2];                // tiles whose tail goes on, and the tail's row of out:
+    uint4* list[2];                // tile whose tail goes on, the tail's row of out, its key:
     uint32_t* list_count;          //   short runs, long runs (EC_LONG tiles or more after it)
     int64_t T, V, D, Dp, ld_dy, ld_out;
     int64_t tiles;
@@ -498,7 +511,7 @@ __device__ __forceinline__ void fill_block(const GradParams& p, int64_t f) {
 // columns: consecutive ones (VEC: rows on 16-byte boundaries), else one in
 // every EG_THREADS.  Bound by the rows of dy read and the rows written.
 template <typename TD, typename TO, bool VEC>
-__global__ void __launch_bounds__(EG_THREADS) grad_sum_kernel(const GradParams p) {
+__global__ void __launch_bounds__(EG_THREADS, VEC && sizeof(TD) == 2 ? 10 : 8) grad_sum_kernel(const GradParams p) {
     __shared__ uint32_t s_key[EG_MAX_C + 2], s_pos[EG_MAX_C];
     __shared__ uint32_t s_red[33];
     pdl_launch();
@@ -527,7 +540,8 @@ __global__ void __launch_bounds__(EG_THREADS) grad_sum_kernel(const GradParams p
         } else {
             // short list: runs that begin before this tile, by counting
             uint32_t heads = 0;
-            for (int64_t t = tid; t <= start; t += EG_THREADS)
+#pragma unroll 8
+            for (int t = tid; t <= (int)start; t += EG_THREADS)
                 heads += t == 0 || p.key[t] != p.key[t - 1];
             row = (int64_t)block_sum(heads, s_red) - 1;
         }
@@ -550,7 +564,7 @@ __global__ void __launch_bounds__(EG_THREADS) grad_sum_kernel(const GradParams p
                 const int64_t far = tile + EC_LONG;
                 const int l = far < p.tiles && p.key[far * p.C] == k;
                 p.list[l][atomicAdd(p.list_count + l, 1u)] =
-                    make_uint2((uint32_t)tile, p.out_rows ? (uint32_t)row : k);
+                    make_uint4((uint32_t)tile, p.out_rows ? (uint32_t)row : k, k, 0u);
             }
         } else {
             if (!p.out_rows) row = k;
@@ -625,7 +639,7 @@ __global__ void __launch_bounds__(EG_THREADS) grad_sum_kernel(const GradParams p
         *p.out_count = (int32_t)row;
 }
 
-constexpr int EC_THREADS = 256;
+constexpr int EC_THREADS = 512;
 constexpr int EC_WARPS = EC_THREADS / 32;
 constexpr int EC_COLS = 512;           // columns of a warp with a short run: 32 lanes x 4 x float4
 constexpr int EC_LONG_COLS = 128;      // columns of a block with a long run: 32 lanes x float4
@@ -637,7 +651,7 @@ __device__ __forceinline__ void add_parts(const GradParams& p, int64_t tile, int
                                           int64_t c, float4* s) {
 #pragma unroll
     for (int u = 0; u < N; ++u) s[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll (N == 1 ? 8 : 2)
+#pragma unroll (N == 1 ? 8 : 4)
     for (int64_t j = j0; j < j1; ++j) {
         const float* part = (j == 0 ? p.tail : p.head) + (tile + j) * p.Dp + c;
 #pragma unroll
@@ -666,19 +680,23 @@ __device__ __forceinline__ void put_row(const GradParams& p, int64_t row, int64_
     }
 }
 
-// Number of tiles that the run of the last key of `tile` touches from it on:
-// 32 probes at a time at the first keys of tiles, first of the next 32 tiles,
-// then ever finer between the last hit and the first miss.
-__device__ __forceinline__ int64_t run_tiles(const GradParams& p, int64_t tile) {
-    const uint32_t k = p.key[(tile + 1) * p.C - 1];
+// Number of tiles that the run of key k touches from `tile` on, by probes of the
+// first keys of tiles, one per thread at a time: first of the next tiles, then
+// ever finer between the last hit and the first miss.  BLOCK: by the whole
+// block, else by a warp.
+template <bool BLOCK>
+__device__ __forceinline__ int64_t run_tiles(const GradParams& p, int64_t tile, uint32_t k) {
+    constexpr int W = BLOCK ? EC_THREADS : 32;
+    const int id = BLOCK ? (int)threadIdx.x : (int)lane_id();
     int64_t hit = tile, miss = p.tiles;
     for (int64_t step = 1; miss - hit > 1;) {
-        const int64_t at = hit + (lane_id() + 1) * step;
+        const int64_t at = hit + (id + 1) * step;
         const bool in = at < miss && p.key[at * p.C] == k;
-        const int n = __popc(__ballot_sync(0xFFFFFFFFu, in));   // (hits come first)
-        if (n < 32) miss = min(miss, hit + (n + 1) * step);
+        const int n = BLOCK ? __syncthreads_count(in)            // (hits come first)
+                            : __popc(__ballot_sync(0xFFFFFFFFu, in));
+        if (n < W) miss = min(miss, hit + (n + 1) * step);
         hit += n * step;
-        step = max((int64_t)1, (miss - hit) / 32);
+        step = max((int64_t)1, (miss - hit) / W);
     }
     return hit - tile + 1;
 }
@@ -697,8 +715,8 @@ __global__ void __launch_bounds__(EC_THREADS) grad_combine_kernel(const GradPara
     const int64_t long_items = (int64_t)p.list_count[1] * long_slabs;
     for (int64_t it = blockIdx.x; it < long_items; it += gridDim.x) {
         const int64_t run = it / long_slabs, c = (it - run * long_slabs) * EC_LONG_COLS + lane * 4;
-        const uint2 entry = p.list[1][run];
-        const int64_t parts = run_tiles(p, entry.x), per = ceil_div64(parts, EC_WARPS);
+        const uint4 entry = p.list[1][run];
+        const int64_t parts = run_tiles<true>(p, entry.x, entry.z), per = ceil_div64(parts, EC_WARPS);
         float4 s;
         add_parts<1>(p, entry.x, min(parts, warp * per), min(parts, (warp + 1) * per), c, &s);
         s_part[warp][lane] = s;
@@ -718,12 +736,13 @@ __global__ void __launch_bounds__(EC_THREADS) grad_combine_kernel(const GradPara
     }
     const int64_t slabs = ceil_div64(p.D, EC_COLS);
     const int64_t items = (int64_t)p.list_count[0] * slabs;
-    for (int64_t it = (int64_t)blockIdx.x * EC_WARPS + warp; it < items;
+    // (from the last block on: the first ones have had the long runs)
+    for (int64_t it = (int64_t)(gridDim.x - 1 - blockIdx.x) * EC_WARPS + warp; it < items;
          it += (int64_t)gridDim.x * EC_WARPS) {
         const int64_t run = it / slabs, c = (it - run * slabs) * EC_COLS + lane * 4;
-        const uint2 entry = p.list[0][run];
+        const uint4 entry = p.list[0][run];
         float4 s[4];
-        add_parts<4>(p, entry.x, 0, run_tiles(p, entry.x), c, s);
+        add_parts<4>(p, entry.x, 0, run_tiles<false>(p, entry.x, entry.z), c, s);
         put_row<TO, 4>(p, entry.y, c, s);
     }
 }
