@@ -269,8 +269,8 @@ __device__ __forceinline__ void cluster_sync() {
 // Shared-memory matrix descriptor, 128-byte swizzle.  K-major: rows of 64 K
 // values (128 bytes), 8-row groups 1,024 bytes apart.  M/N-major: boxes of 64
 // M/N values x 64 K rows, 8,192 bytes apart, 8-row groups 1,024 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool mn) {
-    const uint64_t lead = mn ? (uint64_t)(GM_BOX >> 4) : 1ull;
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool mn, int box = GM_BOX) {
+    const uint64_t lead = mn ? (uint64_t)(box >> 4) : 1ull;
     return (uint64_t)((addr & 0x3FFFF) >> 4) | (lead << 16) | ((uint64_t)(1024 >> 4) << 32) |
            (1ull << 46) | (2ull << 61);
 }
@@ -1018,6 +1018,224 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
     __syncthreads();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(COLS));
+}
+
+// ------------------------------------------------ small matrices: one kernel
+
+// A matrix of at most 128 x 256 (either way round): one block does the whole
+// call, with X, A and B in shared memory, the sums in TMEM and fp32 output's
+// three products throughout (they cost nothing here: each product waits for the
+// one before).  X is held with the short side as rows: chunks of 64 columns, 128
+// rows of 128 swizzled bytes each, which the gram reads as K-major and the update
+// as N-major operand.  What lies outside the matrix is zero and stays zero.
+constexpr int TN_THREADS = 256;
+constexpr int TN_ROWS = 128, TN_COLS = 256;
+constexpr int TN_CHUNK = TN_ROWS * 128;                // bytes of 64 columns
+constexpr int TN_X = TN_COLS / 64 * TN_CHUNK, TN_A = TN_ROWS / 64 * TN_CHUNK;   // hi (or lo)
+constexpr int TN_SMEM = 2 * TN_X + 2 * TN_A + 1024;
+constexpr int TN_MAX_STEPS = 64;
+
+struct TinyParams {
+    MuonPreParams pre;             // (rows, cols: the caller's; groups unused)
+    float coef[3 * TN_MAX_STEPS];
+    int8_t drop[TN_MAX_STEPS + 1]; // (saturated)
+    int32_t steps, out_type;
+    float scale;
+    void* out;
+    int64_t ld_out, stride_out;
+};
+
+// Byte offset of 16-byte unit u of row r of a chunk.
+__device__ __forceinline__ uint32_t tn_unit(int r, int u) {
+    return (uint32_t)(r * 128 + ((u ^ (r & 7)) << 4));
+}
+
+template <typename TG>
+__global__ void __launch_bounds__(TN_THREADS, 1) muon_tiny_kernel(const __grid_constant__ TinyParams p) {
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t s_done;
+    __shared__ double s_red[33];
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_gave_up;
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    uint8_t* mem = raw + (base - smem_u32(raw));
+    const uint32_t x_at = base, a_at = base + 2 * TN_X;
+    const int tid = (int)threadIdx.x, warp = (int)warp_id(), lane = (int)lane_id();
+    if (tid == 0) {
+        s_gave_up = 0;
+        mbar_init(smem_u32(&s_done), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         smem_u32(&s_tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    for (int i = tid; i < (2 * TN_X + 2 * TN_A) / 16; i += TN_THREADS)
+        reinterpret_cast<uint4*>(mem)[i] = make_uint4(0, 0, 0, 0);
+    pdl_launch();
+    pdl_wait();
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = s_tmem;
+    uint32_t* status = &p.pre.ctrl->status;
+    const int64_t b = blockIdx.x;
+    const int m = (int)p.pre.rows, n = (int)p.pre.cols, total = m * n;
+    const bool tall = m > n;
+    const int P = tall ? n : m, Q = tall ? m : n;
+    if (b == 0 && tid == 0) {
+        p.pre.ctrl->path_small = 0;
+        p.pre.ctrl->status = 0;
+    }
+
+    // ---- momentum, norm, X
+    const TG* g = static_cast<const TG*>(p.pre.grad) + b * p.pre.stride_g;
+    float* mom = p.pre.momentum ? p.pre.momentum + b * total : nullptr;
+    double sum = 0.0;
+#pragma unroll 4
+    for (int i = tid; i < total; i += TN_THREADS) {
+        const int r = i / n, c = i - r * n;
+        float u = to_f32(g[r * p.pre.ld_g + c]);
+        if (mom) {
+            const float v = fmaf(p.pre.mu, mom[i], u);
+            mom[i] = v;
+            u = p.pre.nesterov ? fmaf(p.pre.mu, v, u) : v;
+        }
+        sum = fma((double)u, (double)u, sum);
+    }
+    const double norm = sqrt(block_sum(sum, s_red));
+    int lift = 0;
+    if (norm > 0.0 && norm < p.pre.eps) lift = min(MU_MAX_LIFT, ilogb((norm + p.pre.eps) / norm));
+    const double f = scalbn(p.pre.S, lift) / (norm + p.pre.eps);
+#pragma unroll 4
+    for (int i = tid; i < total; i += TN_THREADS) {
+        const int r = i / n, c = i - r * n;
+        float u = to_f32(g[r * p.pre.ld_g + c]);
+        if (mom) u = p.pre.nesterov ? fmaf(p.pre.mu, mom[i], u) : mom[i];
+        const float y = (float)((double)u * f);
+        const int xr = tall ? c : r, xc = tall ? r : c;
+        const uint32_t o = (uint32_t)(xc >> 6) * TN_CHUNK + tn_unit(xr, (xc & 63) >> 3) + (xc & 7) * 2;
+        const __half h = __float2half_rn(y);
+        *reinterpret_cast<__half*>(mem + o) = h;
+        *reinterpret_cast<__half*>(mem + TN_X + o) = __float2half_rn(y - __half2float(h));
+    }
+
+    // ---- the products
+    const float S = (float)p.pre.S;
+    const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
+    const uint32_t lane_at = tmem + ((uint32_t)(quad * 32) << 16);
+    uint32_t parity = 0;
+    bool ok = true;
+    for (int i = 0; i < 3 * p.steps && ok; ++i) {
+        const int step = i / 3, mode = i - step * 3;   // gram, square, update
+        const bool update = mode == MU_UPDATE, last = i == 3 * p.steps - 1;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncthreads();
+        if (tid == 0) {
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const int N = ((update ? Q : P) + 15) / 16 * 16, K = mode == MU_GRAM ? Q : P;
+            const uint32_t idesc = (1u << 4) | ((uint32_t)update << 16) | ((uint32_t)(N / 8) << 17) |
+                                   ((TN_ROWS / 16) << 24);
+            const uint32_t left = mode == MU_GRAM ? x_at : a_at, left_lo = mode == MU_GRAM ? TN_X : TN_A;
+            const uint32_t right = mode == MU_SQUARE ? a_at : x_at;
+            const uint32_t right_lo = mode == MU_SQUARE ? TN_A : TN_X;
+            for (int k = 0; k * 16 < K; ++k) {
+                const uint32_t along = (uint32_t)(k >> 2) * TN_CHUNK + (k & 3) * 32;
+                const uint32_t la = left + along, ra = right + (update ? (uint32_t)k * 2048 : along);
+                const uint64_t lh = smem_desc(la, false), ll = smem_desc(la + left_lo, false);
+                const uint64_t rh = smem_desc(ra, update, TN_CHUNK);
+                const uint64_t rl = smem_desc(ra + right_lo, update, TN_CHUNK);
+                mma_f16_1(tmem, lh, rh, idesc, k > 0);
+                mma_f16_1(tmem + 256, lh, rl, idesc, k > 0);
+                mma_f16_1(tmem + 256, ll, rh, idesc, true);
+            }
+            mma_commit1(smem_u32(&s_done));
+        }
+        ok = mbar_wait(smem_u32(&s_done), parity, &s_gave_up, status);
+        ok = __syncthreads_and(ok);
+        if (!ok) break;
+        parity ^= 1;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+
+        const float* coef = p.coef + 3 * step;
+        float alpha, beta = 0.0f;
+        const int k = max(0, lift - p.drop[step]), next = max(0, lift - p.drop[step + 1]);
+        if (mode == MU_GRAM) {
+            alpha = MU_SA / (S * S) * exp2f((float)(-2 * k));
+        } else if (mode == MU_SQUARE) {
+            alpha = coef[2] / MU_SA;
+            beta = coef[1];
+        } else {
+            const float by = last ? p.scale / S * exp2f((float)-k) : exp2f((float)(next - k));
+            alpha = by / MU_SA;
+            beta = by * coef[0];
+        }
+        const int chunks = ((update ? Q : P) + 63) / 64;
+        uint8_t* buf = mem + (update ? 0 : 2 * TN_X);
+        const uint32_t lo_at = update ? TN_X : TN_A;
+        for (int ch = half; ch < chunks; ch += 2) {
+#pragma unroll 1
+            for (int c = 0; c < 64; c += 32) {
+                float v[32], w[32];
+                tmem_load32(lane_at + ch * 64 + c, reinterpret_cast<uint32_t*>(v));
+                tmem_load32(lane_at + 256 + ch * 64 + c, reinterpret_cast<uint32_t*>(w));
+                tmem_wait();
+                uint8_t* at = buf + ch * TN_CHUNK;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    uint4* ph = reinterpret_cast<uint4*>(at + tn_unit(row, c / 8 + u));
+                    uint4* pl = reinterpret_cast<uint4*>(at + lo_at + tn_unit(row, c / 8 + u));
+                    float y[8];
+                    if (mode == MU_GRAM) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = alpha * (v[u * 8 + e] + w[u * 8 + e]);
+                    } else {
+                        const uint4 h = *ph, l = *pl;
+                        const __half* hh = reinterpret_cast<const __half*>(&h);
+                        const __half* ll = reinterpret_cast<const __half*>(&l);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            y[e] = fmaf(alpha, v[u * 8 + e] + w[u * 8 + e],
+                                        beta * (__half2float(hh[e]) + __half2float(ll[e])));
+                    }
+                    if (last) {
+                        // fp32 in place: a 16-byte unit of hi and of lo are 8 values
+                        *ph = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]),
+                                         __float_as_uint(y[2]), __float_as_uint(y[3]));
+                        *pl = make_uint4(__float_as_uint(y[4]), __float_as_uint(y[5]),
+                                         __float_as_uint(y[6]), __float_as_uint(y[7]));
+                    } else {
+                        *ph = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]),
+                                         pack2(y[6], y[7]));
+                        *pl = make_uint4(pack2(below_half(y[0]), below_half(y[1])),
+                                         pack2(below_half(y[2]), below_half(y[3])),
+                                         pack2(below_half(y[4]), below_half(y[5])),
+                                         pack2(below_half(y[6]), below_half(y[7])));
+                    }
+                }
+            }
+        }
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (ok) {
+        for (int i = tid; i < total; i += TN_THREADS) {
+            const int r = i / n, c = i - r * n;
+            const int xr = tall ? c : r, xc = tall ? r : c;
+            const uint32_t o = (uint32_t)(xc >> 6) * TN_CHUNK + tn_unit(xr, (xc & 63) >> 3) +
+                               (xc & 3) * 4 + (xc & 4 ? TN_X : 0);
+            const float y = *reinterpret_cast<const float*>(mem + o);
+            const int64_t to = b * p.stride_out + r * p.ld_out + c;
+            if (p.out_type == 0) static_cast<float*>(p.out)[to] = y;
+            else if (p.out_type == 1) static_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(y);
+            else static_cast<__half*>(p.out)[to] = __float2half_rn(y);
+        }
+    }
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 }  // namespace tke

@@ -1,6 +1,7 @@
 // Host side of muon_update (include/topk_ef.h): argument checks, workspace
 // layout, launch sequence.
 //
+//   a small matrix: muon_tiny_kernel alone; else
 //   muon_norm_kernel -> muon_scale_kernel -> steps times: muon_gemm_kernel as
 //   gram, square and update (the last update writes the caller's matrix)
 #include <cuda.h>
@@ -113,6 +114,15 @@ bool coefficients_ok(const float* coef, int32_t steps, int32_t* drop) {
     return true;
 }
 
+template <typename F>
+cudaError_t with_type(int32_t t, F f) {
+    switch (t) {
+        case TOPK_EF_F32: return f(float{});
+        case TOPK_EF_BF16: return f(__nv_bfloat16{});
+        default: return f(__half{});
+    }
+}
+
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                               const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -184,6 +194,13 @@ cudaError_t muon_device(int* pairs) {
             });
             if (e != cudaSuccess) return e;
         }
+    for (int32_t t = TOPK_EF_F32; t <= TOPK_EF_F16; ++t) {
+        e = with_type(t, [&](auto type) {
+            return cudaFuncSetAttribute(muon_tiny_kernel<decltype(type)>,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize, TN_SMEM);
+        });
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(GM_THREADS);
@@ -214,15 +231,6 @@ cudaError_t launch_split(bool exact, unsigned tiles, unsigned parts, cudaStream_
     cfg.numAttrs = 2;
     return with_kernel(exact, g.mode,
                        [&](auto, auto split) { return cudaLaunchKernelEx(&cfg, split, g); });
-}
-
-template <typename F>
-cudaError_t with_type(int32_t t, F f) {
-    switch (t) {
-        case TOPK_EF_F32: return f(float{});
-        case TOPK_EF_BF16: return f(__nv_bfloat16{});
-        default: return f(__half{});
-    }
 }
 
 }  // namespace
@@ -307,6 +315,24 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
     pp.nesterov = nesterov;
     pp.eps = eps;
     pp.S = S;
+    if (std::min(rows, cols) <= TN_ROWS && std::max(rows, cols) <= TN_COLS) {
+        TinyParams tp = {};
+        tp.pre = pp;
+        std::copy(coef, coef + 3 * steps, tp.coef);
+        for (int i = 0; i <= steps; ++i) tp.drop[i] = (int8_t)std::min(drop[i], 127);
+        tp.steps = steps;
+        tp.out_type = out_type;
+        tp.scale = scale;
+        tp.out = out;
+        tp.ld_out = ld_out;
+        tp.stride_out = stride_out;
+        trace_before(st, "muon_tiny_kernel");
+        e = with_type(grad_type, [&](auto t) {
+            return launch_pdl(muon_tiny_kernel<decltype(t)>, (unsigned)B, TN_THREADS, st, tp, TN_SMEM);
+        });
+        trace_after(st);
+        return e == cudaSuccess ? TOPK_EF_OK : cuda_fail(e);
+    }
     const dim3 pre((unsigned)L.parts, (unsigned)B);
     e = with_type(grad_type, [&](auto t) {
         using TG = decltype(t);

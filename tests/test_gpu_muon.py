@@ -71,7 +71,8 @@ def _make(shape, kind, seed):
 
 SHAPES = [(1, 1, 1), (1, 1, 1000), (1, 1000, 1), (1, 64, 27), (1, 27, 64), (1, 128, 256),
           (2, 129, 257), (3, 257, 129), (5, 16, 16), (1, 512, 700), (2, 700, 512), (1, 65, 2049),
-          (1, 300, 300), (40, 130, 70), (1, 1030, 1100)]
+          (1, 300, 300), (40, 130, 70), (1, 1030, 1100), (3, 256, 128), (1, 129, 128), (1, 128, 257),
+          (200, 40, 33), (2, 65, 255)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
