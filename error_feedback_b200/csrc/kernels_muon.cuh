@@ -36,7 +36,7 @@ constexpr uint64_t MU_WAIT_NS = 2000000000ull;
 // ------------------------------------------------------- momentum and norm
 
 constexpr int MN_THREADS = 256;
-constexpr int MN_MAX_PARTS = 512;          // partial sums of one matrix
+constexpr int MN_MAX_PARTS = 1184;         // partial sums of one matrix
 
 struct MuonPreParams {
     const void* grad;
@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(MN_THREADS) muon_norm_kernel(const MuonPrePara
         p.ctrl->status = 0;
     }
     double sum = 0.0;
+#pragma unroll 4
     for (int64_t i = (int64_t)blockIdx.x * MN_THREADS + threadIdx.x; i < p.groups;
          i += (int64_t)gridDim.x * MN_THREADS) {
         const int64_t r = i / p.row_groups;
@@ -139,6 +140,7 @@ __global__ void __launch_bounds__(MN_THREADS) muon_scale_kernel(const MuonPrePar
     if (norm > 0.0 && norm < p.eps) lift = min(MU_MAX_LIFT, ilogb((norm + p.eps) / norm));
     if (blockIdx.x == 0 && threadIdx.x == 0) p.lift[b] = lift;
     const double f = scalbn(p.S, lift) / (norm + p.eps);
+#pragma unroll 4
     for (int64_t i = (int64_t)blockIdx.x * MN_THREADS + threadIdx.x; i < p.groups;
          i += (int64_t)gridDim.x * MN_THREADS) {
         const int64_t r = i / p.row_groups, c = (i - r * p.row_groups) * 8;
@@ -172,8 +174,12 @@ constexpr int GM_SMEM = GM_RING + 1024;                // + alignment
 enum { MU_GRAM = 0, MU_SQUARE = 1, MU_UPDATE = 2, MU_LAST = 3 };
 
 struct GemmParams {
-    CUtensorMap a[2], b[2];        // hi, lo of both operands
+    // hi, lo of both operands: 128 rows (columns) x 64 of K, and 64 of the right
+    // one's.  K contiguous: {K, rows, 1, batch}, zeros outside.  The other way
+    // round: {64, K, columns / 64, batch}: 64 K rows of one or two chunks of 64.
+    CUtensorMap a[2], b[2], b_half[2];
     int32_t M, N, K, batch, tiles_m, tiles_n, tiles;   // tiles: of one matrix
+    int32_t whole;                 // pairs: tiles taken whole, the others in two halves of columns
     int32_t a_mn, b_mn;            // operand's M (N) dimension is the contiguous one
     int32_t n_fast;                // neighbouring tiles differ in N
     int32_t mode, out_type;
@@ -228,22 +234,23 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     return false;
 }
 
-// One 64 x 64 box into this block's shared memory, counted on its barrier.
-__device__ __forceinline__ void tma_box1(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
-                                         uint32_t bar) {
+// One box (128 or 64 rows or columns from `at`, 64 of K from `k`) into this
+// block's shared memory, counted on its barrier.
+__device__ __forceinline__ void tma_box1(uint32_t dst, const CUtensorMap* map, bool mn, int at, int k,
+                                         int b, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(mn ? 0 : k), "r"(mn ? k : at), "r"(mn ? at >> 6 : 0), "r"(b), "r"(bar)
         : "memory");
 }
 // The same, counted on a barrier of either block of a pair.
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
-                                        uint32_t bar) {
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, bool mn, int at, int k,
+                                        int b, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(mn ? 0 : k), "r"(mn ? k : at), "r"(mn ? at >> 6 : 0), "r"(b), "r"(bar)
         : "memory");
 }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
@@ -366,6 +373,24 @@ __device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t, int size) 
     }
     r.m = i * size;
     r.n = j * size;
+    return r;
+}
+
+// The u-th piece of work of a pair kernel: a whole tile, or half the columns
+// of one of the last tiles.
+struct Piece {
+    TileAt at;         // (m: this block's rows; n: the piece's first column)
+    int width;         // columns
+    bool diagonal;     // of a symmetric output
+};
+__device__ __forceinline__ Piece piece_at(const GemmParams& p, int u, int rank) {
+    Piece r;
+    const int h = u - p.whole;
+    r.at = tile_at(p, h < 0 ? u : p.whole + (h >> 1), GM_TILE);
+    r.diagonal = r.at.m == r.at.n;
+    r.width = h < 0 ? GM_TILE : GM_TILE / 2;
+    r.at.m += rank * GM_ROWS;
+    if (h >= 0) r.at.n += (h & 1) * (GM_TILE / 2);
     return r;
 }
 
@@ -527,7 +552,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
         mbar_init(smem_u32(&s_drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0 && lane < 2 * PARTS) prefetch_map(lane & 1 ? &p.b[lane >> 1] : &p.a[lane >> 1]);
+    if (warp == 0 && lane < 3 * PARTS) prefetch_map(lane < 2 * PARTS ? lane < PARTS ? &p.a[lane] : &p.b[lane - PARTS] : &p.b_half[lane - 2 * PARTS]);
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          smem_u32(&s_tmem))
@@ -540,7 +565,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = s_tmem;
     uint32_t* status = &p.ctrl->status;
-    const int total = p.tiles * p.batch, kblocks = (p.K + GM_K - 1) / GM_K;
+    const int total = 2 * p.tiles * p.batch - p.whole;     // pieces
+    const int kblocks = (p.K + GM_K - 1) / GM_K;
     pdl_launch();
     pdl_wait();
 
@@ -556,31 +582,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
         uint32_t phase = 0, issued = 0;
         bool ok = true;
         for (int t = pair; t < total && ok; t += pairs) {
-            TileAt at = tile_at(p, t, GM_TILE);
-            at.m += rank * GM_ROWS;
-            const int n0 = at.n + rank * GM_ROWS;
+            const Piece piece = piece_at(p, t, rank);
+            const TileAt at = piece.at;
+            const int n0 = at.n + rank * (piece.width / 2);
+            const CUtensorMap* right = piece.width == GM_TILE ? p.b : p.b_half;
+            const uint32_t bytes = 2 * PARTS * (GM_OP + piece.width / 2 * GM_K * 2);
             for (int kb = 0; kb < kblocks; ++kb) {
                 if (!(ok = mbar_wait(smem_u32(&s_empty[stage]), phase ^ 1, &s_gave_up, status)))
                     break;
                 const uint32_t bar = in_block(smem_u32(&s_full[stage]), 0);
-                if (rank == 0) mbar_expect(smem_u32(&s_full[stage]), 2 * STAGE);
-                uint32_t dst = base + stage * STAGE;
+                if (rank == 0) mbar_expect(smem_u32(&s_full[stage]), bytes);
+                const uint32_t dst = base + stage * STAGE;
                 const int k = kb * GM_K;
 #pragma unroll
                 for (int q = 0; q < PARTS; ++q) {
-#pragma unroll
-                    for (int i = 0; i < GM_ROWS / 64; ++i, dst += GM_BOX) {
-                        if (p.a_mn) tma_box(dst, &p.a[q], at.m + i * 64, k, at.b, bar);
-                        else tma_box(dst, &p.a[q], k, at.m + i * 64, at.b, bar);
-                    }
-                }
-#pragma unroll
-                for (int q = 0; q < PARTS; ++q) {
-#pragma unroll
-                    for (int i = 0; i < GM_ROWS / 64; ++i, dst += GM_BOX) {
-                        if (p.b_mn) tma_box(dst, &p.b[q], n0 + i * 64, k, at.b, bar);
-                        else tma_box(dst, &p.b[q], k, n0 + i * 64, at.b, bar);
-                    }
+                    tma_box(dst + q * GM_OP, &p.a[q], p.a_mn, at.m, k, at.b, bar);
+                    tma_box(dst + (PARTS + q) * GM_OP, right + q, p.b_mn, n0, k, at.b, bar);
                 }
                 ++issued;
                 if (++stage == STAGES) {
@@ -598,13 +615,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
             }
     } else if (warp == 1 && lane == 0 && rank == 0) {
         // ---- products
-        const uint32_t idesc = (1u << 4) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16) |
-                               ((GM_TILE / 8) << 17) | ((GM_TILE / 16) << 24);
+        const uint32_t shape = (1u << 4) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16) |
+                               ((GM_TILE / 16) << 24);
         const uint32_t a_step = p.a_mn ? 2048 : 32, b_step = p.b_mn ? 2048 : 32;
         int stage = 0, slot = 0;
         uint32_t phase = 0, slot_phase = 0;
         bool ok = true;
         for (int t = pair; t < total && ok; t += pairs) {
+            const uint32_t idesc = shape | ((uint32_t)((t < p.whole ? GM_TILE : GM_TILE / 2) / 8) << 17);
             for (int kb = 0; kb < kblocks; ++kb) {
                 const bool begin = kb % (EXACT ? GM_HAND : kblocks) == 0;
                 const bool end = kb == kblocks - 1 || (EXACT && kb % GM_HAND == GM_HAND - 1);
@@ -648,8 +666,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
     } else {
         if (EXACT) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         // ---- epilogue: warp w reads TMEM lanes 32 (w mod 4) .., half of the columns
-        const int quad = warp & 3, col = warp < 8 ? 0 : HALF;
-        const uint32_t src = tmem + col + ((uint32_t)(quad * 32) << 16);
+        const int quad = warp & 3;
         int slot = 0;
         uint32_t slot_phase = 0;
         bool ok = true;
@@ -669,14 +686,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
             return ok;
         };
         for (int t = pair; t < total && ok; t += pairs) {
-            TileAt at = tile_at(p, t, GM_TILE);
-            at.m += rank * GM_ROWS;
+            const Piece piece = piece_at(p, t, rank);
+            const TileAt at = piece.at;
+            const int cols = piece.width / 2, col = warp < 8 ? 0 : cols;     // this warp's
+            const uint32_t src = tmem + col + ((uint32_t)(quad * 32) << 16);
             const int64_t row = at.m + quad * 32 + lane;
             float fs, fx;
             lift_factors<MODE>(p, at.b, &fs, &fx);
             const float alpha = p.alpha * fs, beta = p.beta * fx;
             const int64_t o = at.b * p.stride + row * p.ld + at.n + col;
-            const bool mirror = at.m >= at.n + GM_TILE;
+            const bool mirror = !piece.diagonal;
             float x[32];
             if (EXACT) {
                 float sum[HALF];
@@ -686,6 +705,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
                     if (!wait_done()) break;
 #pragma unroll
                     for (int c = 0; c < HALF; c += 64) {
+                        if (c >= cols) break;
                         float v[64];
                         tmem_load32(src + slot * GM_TILE + c, reinterpret_cast<uint32_t*>(v));
                         tmem_load32(src + slot * GM_TILE + c + 32, reinterpret_cast<uint32_t*>(v + 32));
@@ -699,7 +719,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
                 // back to where the last sums came from, for the loop below
 #pragma unroll
                 for (int c = 0; c < HALF; c += 32)
-                    tmem_st32(src + slot * GM_TILE + c, reinterpret_cast<uint32_t*>(sum + c));
+                    if (c < cols) tmem_st32(src + slot * GM_TILE + c, reinterpret_cast<uint32_t*>(sum + c));
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 load_src32<EXACT, MODE>(p, o, row < p.M && at.n + col < p.N, x);
             } else {
@@ -707,9 +727,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
                 if (!wait_done()) break;
             }
 #pragma unroll 1
-            for (int c = 0; c < HALF; c += 32) {
+            for (int c = 0; c < cols; c += 32) {
                 float v[32], next[32];
-                load_src32<EXACT, MODE>(p, o + c + 32, c + 32 < HALF && row < p.M &&
+                load_src32<EXACT, MODE>(p, o + c + 32, c + 32 < cols && row < p.M &&
                                         at.n + col + c + 32 < p.N, next);
                 tmem_ld32(src + slot * GM_TILE + c, reinterpret_cast<uint32_t*>(v));
                 epilogue32<EXACT, MODE>(p, at, alpha, beta, row, at.n + col + c, mirror, v, x);
@@ -797,6 +817,38 @@ __device__ __forceinline__ void epilogue4(const GemmParams& p, const TileAt& at,
                        pack2(below_half(v[2]), below_half(v[3])));
 }
 
+// Adds up, in block order, the sums of this block's part of the rows over the
+// S blocks of the cluster, into its own.  Each warp has 16 loads of 512
+// contiguous bytes in flight: it is their latency that costs.
+template <int S>
+__device__ __forceinline__ void add_blocks(float* sums, int rank) {
+    constexpr int R = SP_TILE / S / (SP_THREADS / 32);
+    const int row = rank * (SP_TILE / S) + (int)warp_id();
+    const uint32_t mine = smem_u32(sums) + (uint32_t)(row * SP_LD + (int)lane_id() * 4) * 4;
+    float4 y[S][R];
+#pragma unroll
+    for (int q = 0; q < S; ++q) {
+        const uint32_t from = in_block(mine, q);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                         : "=f"(y[q][r].x), "=f"(y[q][r].y), "=f"(y[q][r].z), "=f"(y[q][r].w)
+                         : "r"(from + (uint32_t)(r * (SP_THREADS / 32) * SP_LD * 4)));
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        float4 x = y[0][r];
+#pragma unroll
+        for (int q = 1; q < S; ++q) {
+            x.x += y[q][r].x;
+            x.y += y[q][r].y;
+            x.z += y[q][r].z;
+            x.w += y[q][r].w;
+        }
+        *reinterpret_cast<float4*>(sums + (row + r * (SP_THREADS / 32)) * SP_LD + lane_id() * 4) = x;
+    }
+}
+
 // fp32 output: the large products of successive 64 of K go to three
 // accumulators in turn and the small ones to a fourth, which keeps the
 // truncated sums short (see muon_gemm_kernel).
@@ -853,22 +905,13 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
                 break;
             const uint32_t bar = smem_u32(&s_full[s]);
             mbar_expect(bar, STAGE);
-            uint32_t dst = base + s * STAGE;
+            const uint32_t dst = base + s * STAGE;
             const int k = (kb0 + i) * GM_K;
 #pragma unroll
-            for (int q = 0; q < PARTS; ++q)
-#pragma unroll
-                for (int h = 0; h < 2; ++h, dst += GM_BOX) {
-                    if (p.a_mn) tma_box1(dst, &p.a[q], at.m + h * 64, k, at.b, bar);
-                    else tma_box1(dst, &p.a[q], k, at.m + h * 64, at.b, bar);
-                }
-#pragma unroll
-            for (int q = 0; q < PARTS; ++q)
-#pragma unroll
-                for (int h = 0; h < 2; ++h, dst += GM_BOX) {
-                    if (p.b_mn) tma_box1(dst, &p.b[q], at.n + h * 64, k, at.b, bar);
-                    else tma_box1(dst, &p.b[q], k, at.n + h * 64, at.b, bar);
-                }
+            for (int q = 0; q < PARTS; ++q) {
+                tma_box1(dst + q * GM_OP, &p.a[q], p.a_mn, at.m, k, at.b, bar);
+                tma_box1(dst + (PARTS + q) * GM_OP, &p.b[q], p.b_mn, at.n, k, at.b, bar);
+            }
         }
         // no copy is in flight when the stages are used for the sums
         for (int j = max(0, i - SP_STAGES); j < i; ++j) {
@@ -934,57 +977,39 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
     }
     if (split > 1) cluster_sync();
     else __syncthreads();
+    if (split == 2) add_blocks<2>(sums, rank);
+    else if (split == 4) add_blocks<4>(sums, rank);
+    else if (split == 8) add_blocks<8>(sums, rank);
 
-    // This block's rows, one per warp at a time (512 contiguous bytes from
-    // each block); the mirror image is turned in shared memory.
+    // This block's rows, one per warp at a time; the mirror image is turned in
+    // shared memory.
+    constexpr int U = 4, WARPS = SP_THREADS / 32;
     const int rows = SP_TILE / (int)split, pitch = rows + 8;
+    const int64_t c0 = at.n + lane * 4;
     const bool mirror = MODE <= MU_SQUARE && at.m != at.n;
     __half* turned = reinterpret_cast<__half*>(sums + SP_TILE * SP_LD);    // [hi, lo][128][pitch]
-    const uint32_t mine = smem_u32(sums);
-    const int64_t c0 = at.n + lane * 4;
-    constexpr int U = 4;
-    for (int r0 = warp; r0 < rows; r0 += U * SP_THREADS / 32) {
+    for (int r0 = warp; r0 < rows; r0 += U * WARPS) {
         float4 x[U];
         uint2 h[U], l[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = rank * rows + r0 + u * (SP_THREADS / 32);
-            const int64_t row = at.m + r, o = at.b * p.stride + row * p.ld + c0;
+            const int r = r0 + u * WARPS;
+            const int64_t row = at.m + rank * rows + r, o = at.b * p.stride + row * p.ld + c0;
             h[u] = l[u] = make_uint2(0, 0);
-            if (MODE != MU_GRAM && r0 + u * (SP_THREADS / 32) < rows && row < p.M && c0 < p.N) {
+            if (MODE != MU_GRAM && r < rows && row < p.M && c0 < p.N) {
                 h[u] = *reinterpret_cast<const uint2*>(p.src[0] + o);
                 if (EXACT || MODE >= MU_UPDATE)
                     l[u] = *reinterpret_cast<const uint2*>(p.src[1] + o);
             }
-            x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        if (split == 1) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                x[u] = *reinterpret_cast<const float4*>(
-                    sums + (r0 + u * (SP_THREADS / 32)) * SP_LD + lane * 4);
-        } else {
-#pragma unroll 1
-            for (uint32_t q = 0; q < split; ++q) {
-                const uint32_t from = in_block(
-                    mine + (uint32_t)((rank * rows + r0) * SP_LD + lane * 4) * 4, q);
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (r0 + u * (SP_THREADS / 32) >= rows) continue;
-                    float4 y;
-                    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                                 : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
-                                 : "r"(from + (uint32_t)(u * (SP_THREADS / 32) * SP_LD * 4)));
-                    x[u].x += y.x;
-                    x[u].y += y.y;
-                    x[u].z += y.z;
-                    x[u].w += y.w;
-                }
-            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = r0 + u * (SP_THREADS / 32);
+            const int r = min(r0 + u * WARPS, rows - 1);
+            x[u] = *reinterpret_cast<const float4*>(sums + (rank * rows + r) * SP_LD + lane * 4);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * WARPS;
             if (r >= rows) continue;
             float* v = reinterpret_cast<float*>(&x[u]);
             epilogue4<EXACT, MODE>(p, at, alpha, beta, at.m + rank * rows + r, c0, h[u], l[u], v);

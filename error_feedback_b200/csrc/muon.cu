@@ -65,6 +65,14 @@ MuLayout muon_layout(int32_t B, int64_t m, int64_t n, bool exact) {
     return L;
 }
 
+// Three products for 22 bits, or one for 11.  Also where the short side is at
+// most 64: there are too few terms for the 11-bit roundings to average out (1 x
+// 1,000 in bf16: 3.9e-3 off, against 1.6e-3), and the products wait for one
+// another more than for the tensor cores.
+bool muon_exact(int64_t m, int64_t n, int32_t out_type) {
+    return out_type == TOPK_EF_F32 || std::min(m, n) <= SP_TILE / 2;
+}
+
 bool muon_sizes_ok(int32_t B, int64_t m, int64_t n) {
     return B >= 0 && B <= MU_MAX_BATCH && m >= 0 && m <= MU_MAX_SIDE && n >= 0 && n <= MU_MAX_SIDE;
 }
@@ -145,13 +153,22 @@ EncodeFn encode_fn(cudaError_t* e) {
     return reinterpret_cast<EncodeFn>(f);
 }
 
-// 64 x 64 boxes of [batch][rows][cols] fp16, 128-byte swizzle; zeros outside.
-bool encode(EncodeFn fn, CUtensorMap* map, void* base, int64_t cols, int64_t rows, int64_t batch,
-            int64_t ld, int64_t stride) {
-    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
-    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)stride * 2};
-    const cuuint32_t box[3] = {64, 64, 1}, step[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides, box, step,
+// Boxes of an operand in [batch][rows][cols] fp16, 128-byte swizzle: `count`
+// rows x 64 columns where the columns are K, else 64 rows x `count` columns
+// (see GemmParams).
+struct Operand {
+    __half* base[2];
+    int64_t rows, cols, ld, stride;
+    bool mn;                       // the rows are K
+};
+bool encode(EncodeFn fn, CUtensorMap* map, const Operand& o, int part, int64_t batch, int count) {
+    const bool mn = o.mn;
+    const cuuint64_t dims[4] = {(cuuint64_t)(mn ? 64 : o.cols), (cuuint64_t)o.rows,
+                                (cuuint64_t)(mn ? ceil_div64(o.cols, 64) : 1), (cuuint64_t)batch};
+    const cuuint64_t strides[3] = {(cuuint64_t)o.ld * 2, 128, (cuuint64_t)o.stride * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)(mn ? 64 : count), (cuuint32_t)(mn ? count / 64 : 1), 1};
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, o.base[part], dims, strides, box, step,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -239,7 +256,7 @@ extern "C" {
 
 size_t muon_workspace_bytes(int32_t B, int64_t rows, int64_t cols, int32_t out_type) {
     if (!muon_sizes_ok(B, rows, cols) || !type_size(out_type)) return 0;
-    return muon_layout(B, rows, cols, out_type == TOPK_EF_F32).total;
+    return muon_layout(B, rows, cols, muon_exact(rows, cols, out_type)).total;
 }
 
 int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t stride_grad,
@@ -268,7 +285,7 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
         e = cudaMemsetAsync(ws, 0, sizeof(Ctrl), st);
         return e == cudaSuccess ? TOPK_EF_OK : cuda_fail(e);
     }
-    const bool exact = out_type == TOPK_EF_F32, tall = rows > cols;
+    const bool exact = muon_exact(rows, cols, out_type), tall = rows > cols;
     const MuLayout L = muon_layout(B, rows, cols, exact);
     char* w = static_cast<char*>(ws);
     __half *x[2][2], *am[2], *bm[2];
@@ -284,16 +301,6 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
     if ((e = muon_device(&pairs)) != cudaSuccess) return cuda_fail(e);
     EncodeFn fn = encode_fn(&e);
     if (!fn) return cuda_fail(e);
-    CUtensorMap mx[2][2], ma[2], mb[2];
-    bool ok = true;
-    for (int h = 0; h < (exact ? 2 : 1); ++h) {
-        for (int i = 0; i < 2; ++i)
-            ok = ok && encode(fn, &mx[i][h], x[i][h], cols, rows, B, L.ldx, L.stride_x);
-        ok = ok && encode(fn, &ma[h], am[h], L.p, L.p, B, L.ldp, L.stride_p);
-        ok = ok && encode(fn, &mb[h], bm[h], L.p, L.p, B, L.ldp, L.stride_p);
-    }
-    if (!ok) return cuda_fail(cudaErrorInvalidValue);
-
     MuonPreParams pp = {};
     pp.grad = grad;
     pp.momentum = momentum;
@@ -348,10 +355,36 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
     if (e != cudaSuccess) return cuda_fail(e);
 
     const int32_t P = (int32_t)L.p, Q = (int32_t)std::max(rows, cols);
-    auto launch = [&](GemmParams& g, const CUtensorMap* a, const CUtensorMap* b) {
-        for (int h = 0; h < 2; ++h) {
-            g.a[h] = a[exact ? h : 0];
-            g.b[h] = b[exact ? h : 0];
+    // operand maps, made once for each use: gram, square and update of both X
+    struct Maps {
+        CUtensorMap a[2], b[2], b_half[2];
+    };
+    Maps maps[5];
+    const int parts = exact ? 2 : 1;
+    auto fill = [&](Maps& to, const Operand& a, const Operand& b) {
+        bool ok = true;
+        for (int h = 0; h < parts; ++h)
+            ok = ok && encode(fn, &to.a[h], a, h, B, 128) && encode(fn, &to.b[h], b, h, B, 128) &&
+                 encode(fn, &to.b_half[h], b, h, B, 64);
+        return ok;
+    };
+    bool ok = true;
+    for (int i = 0; i < 2; ++i) {
+        Operand xo = {{x[i][0], x[i][1]}, rows, cols, L.ldx, L.stride_x, tall};
+        const Operand bo = {{bm[0], bm[1]}, L.p, L.p, L.ldp, L.stride_p, false};
+        ok = ok && fill(maps[i], xo, xo);
+        xo.mn = !tall;
+        ok = ok && (tall ? fill(maps[3 + i], xo, bo) : fill(maps[3 + i], bo, xo));
+    }
+    const Operand ao = {{am[0], am[1]}, L.p, L.p, L.ldp, L.stride_p, false};
+    ok = ok && fill(maps[2], ao, ao);
+    if (!ok) return cuda_fail(cudaErrorInvalidValue);
+
+    auto launch = [&](GemmParams& g, const Maps& from) {
+        for (int h = 0; h < parts; ++h) {
+            g.a[h] = from.a[h];
+            g.b[h] = from.b[h];
+            g.b_half[h] = from.b_half[h];
         }
         g.batch = B;
         g.ctrl = pp.ctrl;
@@ -373,7 +406,12 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
         if (long_sums || cut(GM_TILE) * B >= MU_LARGE) {
             tiles = cut(GM_TILE);
             g.tiles = (int32_t)tiles;
-            const unsigned grid = 2u * (unsigned)std::min<int64_t>(tiles * B, pairs);
+            // where the last round would leave half of the pairs idle, its tiles are
+            // halved (a half takes three quarters of the time of a whole one)
+            const int64_t all = tiles * B, rest = all % pairs;
+            g.whole = (int32_t)(2 * rest <= pairs ? all - rest : all);
+            const int64_t pieces = 2 * all - g.whole;
+            const unsigned grid = 2u * (unsigned)std::min<int64_t>(pieces, pairs);
             trace_before(st, "muon_gemm_kernel");
             r = with_kernel(exact, g.mode, [&](auto pair, auto) {
                 return launch_pdl(pair, grid, GM_THREADS, st, g, GM_SMEM);
@@ -402,7 +440,7 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
         g.dst[1] = am[1];
         g.ld = L.ldp;
         g.stride = L.stride_p;
-        if ((e = launch(g, mx[cur], mx[cur])) != cudaSuccess) return cuda_fail(e);
+        if ((e = launch(g, maps[cur])) != cudaSuccess) return cuda_fail(e);
 
         g.mode = MU_SQUARE;
         g.K = P;
@@ -413,7 +451,7 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
         g.src[1] = am[1];
         g.dst[0] = bm[0];
         g.dst[1] = bm[1];
-        if ((e = launch(g, ma, ma)) != cudaSuccess) return cuda_fail(e);
+        if ((e = launch(g, maps[2])) != cudaSuccess) return cuda_fail(e);
 
         const bool last = i == steps - 1;
         g.mode = last ? MU_LAST : MU_UPDATE;
@@ -434,8 +472,7 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
         g.out_type = out_type;
         g.ld_out = ld_out;
         g.stride_out = stride_out;
-        e = tall ? launch(g, mx[cur], mb) : launch(g, mb, mx[cur]);
-        if (e != cudaSuccess) return cuda_fail(e);
+        if ((e = launch(g, maps[3 + cur])) != cudaSuccess) return cuda_fail(e);
         cur ^= 1;
     }
     return TOPK_EF_OK;
