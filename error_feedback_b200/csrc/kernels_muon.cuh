@@ -179,6 +179,7 @@ struct GemmParams {
     // round: {64, K, columns / 64, batch}: 64 K rows of one or two chunks of 64.
     CUtensorMap a[2], b[2], b_half[2];
     int32_t M, N, K, batch, tiles_m, tiles_n, tiles;   // tiles: of one matrix
+    int32_t stages;                // clusters: stages of the ring
     int32_t whole;                 // pairs: tiles taken whole, the others in two halves of columns
     int32_t a_mn, b_mn;            // operand's M (N) dimension is the contiguous one
     int32_t n_fast;                // neighbouring tiles differ in N
@@ -418,14 +419,24 @@ template <typename TO>
 __device__ __forceinline__ void store_out(const GemmParams& p, int64_t b, int64_t row, int64_t c0,
                                           const float* v) {
     TO* dst = static_cast<TO*>(p.out) + b * p.stride_out + row * p.ld_out + c0;
-    if (c0 + 32 <= p.N && (uintptr_t)dst % 32 == 0) {
-        constexpr int E = 32 / (int)sizeof(TO);
+    constexpr int E = 32 / (int)sizeof(TO);
+    const uint32_t align = (uint32_t)(uintptr_t)dst;
+    if (c0 + 32 <= p.N && align % 4 == 0) {
 #pragma unroll
         for (int j = 0; j < 32; j += E) {
             uint4 r[2];
 #pragma unroll
             for (int e = 0; e < E; ++e) reinterpret_cast<TO*>(r)[e] = from_f32<TO>(v[j + e]);
-            store32b(dst + j, r);
+            if (align % 32 == 0) {
+                store32b(dst + j, r);
+            } else if (align % 16 == 0) {
+                reinterpret_cast<uint4*>(dst + j)[0] = r[0];
+                reinterpret_cast<uint4*>(dst + j)[1] = r[1];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    reinterpret_cast<uint32_t*>(dst + j)[e] = reinterpret_cast<const uint32_t*>(r)[e];
+            }
         }
     } else {
 #pragma unroll
@@ -761,13 +772,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
 // blocks, in block order, and finishes them.
 constexpr int SP_THREADS = 256;
 constexpr int SP_TILE = 128;
-constexpr int SP_STAGES = 3;
+constexpr int SP_MIN_STAGES = 3, SP_MAX_STAGES = 6;    // 16-bit output: 3 leave room for two
+                                                       // blocks an SM, 6 cover the latency of one
 constexpr int SP_LD = SP_TILE + 4;                     // row of sums, in floats
-constexpr int SP_MAX_SPLIT = 8;
 constexpr int SP_MAX_SUM = 48;     // fp32 output: 64s of K of one block, at most (64 truncated adds)
 constexpr int SP_SUMS = SP_TILE * SP_LD * 4;           // bytes of the sums, then the turned tile
-constexpr int sp_smem(bool exact) {
-    const int ring = SP_STAGES * (exact ? 4 : 2) * GM_OP;
+constexpr int sp_smem(bool exact, int stages) {
+    const int ring = stages * (exact ? 4 : 2) * GM_OP;
     const int after = SP_SUMS + (exact ? 2 : 1) * SP_TILE * (SP_TILE + 8) * 2;
     return (ring > after ? ring : after) + 1024;
 }
@@ -859,17 +870,17 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
     constexpr int BIG = EXACT ? 3 : 1;                 // accumulators of large products
     constexpr uint32_t COLS = EXACT ? 512 : 128;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t s_full[SP_STAGES], s_empty[SP_STAGES], s_done;
+    __shared__ __align__(8) uint64_t s_full[SP_MAX_STAGES], s_empty[SP_MAX_STAGES], s_done;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_gave_up;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const int warp = (int)warp_id(), lane = (int)lane_id();
-    const int rank = (int)cluster_rank();
+    const int rank = (int)cluster_rank(), stages = p.stages;
     uint32_t split;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
     if (threadIdx.x == 0) {
         s_gave_up = 0;
-        for (int s = 0; s < SP_STAGES; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(smem_u32(&s_full[s]), 1);
             mbar_init(smem_u32(&s_empty[s]), 1);
         }
@@ -897,12 +908,10 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
 
     if (warp == 0 && lane == 0) {
         asm volatile("fence.proxy.async;" ::: "memory");
-        int i = 0;
+        int i = 0, s = 0;
+        uint32_t phase = 0;
         for (; i < n; ++i) {
-            const int s = i % SP_STAGES;
-            if (i >= SP_STAGES && !mbar_wait(smem_u32(&s_empty[s]), (i / SP_STAGES - 1) & 1,
-                                             &s_gave_up, status))
-                break;
+            if (!mbar_wait(smem_u32(&s_empty[s]), phase ^ 1, &s_gave_up, status)) break;
             const uint32_t bar = smem_u32(&s_full[s]);
             mbar_expect(bar, STAGE);
             const uint32_t dst = base + s * STAGE;
@@ -912,19 +921,24 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
                 tma_box1(dst + q * GM_OP, &p.a[q], p.a_mn, at.m, k, at.b, bar);
                 tma_box1(dst + (PARTS + q) * GM_OP, &p.b[q], p.b_mn, at.n, k, at.b, bar);
             }
+            if (++s == stages) {
+                s = 0;
+                phase ^= 1;
+            }
         }
         // no copy is in flight when the stages are used for the sums
-        for (int j = max(0, i - SP_STAGES); j < i; ++j) {
+        for (int j = max(0, i - stages); j < i; ++j) {
             volatile int never = 0;
-            mbar_wait(smem_u32(&s_full[j % SP_STAGES]), (j / SP_STAGES) & 1, &never, status);
+            mbar_wait(smem_u32(&s_full[j % stages]), (j / stages) & 1, &never, status);
         }
     } else if (warp == 1 && lane == 0) {
         const uint32_t idesc = (1u << 4) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16) |
                                ((SP_TILE / 8) << 17) | ((SP_TILE / 16) << 24);
         const uint32_t a_step = p.a_mn ? 2048 : 32, b_step = p.b_mn ? 2048 : 32;
+        int s = 0;
+        uint32_t phase = 0;
         for (int i = 0; i < n; ++i) {
-            const int s = i % SP_STAGES;
-            if (!mbar_wait(smem_u32(&s_full[s]), (i / SP_STAGES) & 1, &s_gave_up, status)) break;
+            if (!mbar_wait(smem_u32(&s_full[s]), phase, &s_gave_up, status)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t a0 = base + s * STAGE, b0 = a0 + PARTS * GM_OP;
             const uint32_t d = tmem + (i % BIG) * SP_TILE, small = tmem + BIG * SP_TILE;
@@ -940,6 +954,10 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
                 }
             }
             mma_commit1(smem_u32(&s_empty[s]));
+            if (++s == stages) {
+                s = 0;
+                phase ^= 1;
+            }
         }
         mma_commit1(smem_u32(&s_done));
     }

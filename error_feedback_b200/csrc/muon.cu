@@ -10,6 +10,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <mutex>
 
 #include "topk_ef.h"
 #include "common.cuh"
@@ -23,6 +24,13 @@ namespace {
 constexpr int64_t MU_MAX_SIDE = (int64_t)1 << 20;
 constexpr int32_t MU_MAX_BATCH = 65535;
 constexpr int32_t MU_MAX_STEPS = 64;
+// 256 x 256 tiles of a product from which pairs of SMs take them, rather than
+// clusters 128 x 128 tiles with K divided.  Below, the pairs that are left idle
+// cost more than the clusters' exchange.  Five steps, pairs from 12 or from 25
+// tiles on: 1,536 x 4,096 in bf16 (gram of 21 tiles) 375 or 391 us; with fp32
+// output, pairs from 15 or from 37: 1,024 x 1,024 (update of 16) 281 or 247, 2,048
+// x 2,048 (gram of 36) 579 or 573.
+constexpr int64_t MU_PAIR_TILES_11 = 12, MU_PAIR_TILES_22 = 37;
 
 size_t type_size(int32_t t) {
     return t == TOPK_EF_F32 ? 4 : t == TOPK_EF_BF16 || t == TOPK_EF_F16 ? 2 : 0;
@@ -190,15 +198,25 @@ cudaError_t with_kernel(bool exact, int mode, F f) {
     return exact ? with_mode<true>(mode, f) : with_mode<false>(mode, f);
 }
 
-// Block pairs that the current device runs at once; its kernels' shared memory
-// is set the first time.
-cudaError_t muon_device(int* pairs) {
-    static std::atomic<int> known[64];
+struct MuDevice {
+    int pairs;                     // block pairs of muon_gemm_kernel that run at once
+    int clusters[4];               // clusters of 1, 2, 4, 8 blocks of muon_split_kernel, one block an SM
+};
+
+// Facts of the current device; its kernels' shared memory is set the first time.
+cudaError_t muon_device(MuDevice* out) {
+    static std::mutex mu;
+    static MuDevice known[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const bool keep = dev >= 0 && dev < 64;
-    if (keep && (*pairs = known[dev].load()) > 0) return cudaSuccess;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lk(mu);
+    if (known[dev].pairs > 0) {
+        *out = known[dev];
+        return cudaSuccess;
+    }
+    const int split_smem = sp_smem(false, SP_MAX_STAGES);
     for (int exact = 0; exact < 2; ++exact)
         for (int mode = MU_GRAM; mode <= MU_LAST; ++mode) {
             e = with_kernel(exact != 0, mode, [&](auto pair, auto split) {
@@ -207,7 +225,7 @@ cudaError_t muon_device(int* pairs) {
                 return r != cudaSuccess ? r
                                         : cudaFuncSetAttribute(
                                               split, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              sp_smem(exact != 0));
+                                              exact ? sp_smem(true, SP_MIN_STAGES) : split_smem);
             });
             if (e != cudaSuccess) return e;
         }
@@ -218,26 +236,34 @@ cudaError_t muon_device(int* pairs) {
         });
         if (e != cudaSuccess) return e;
     }
+    MuDevice d = {};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(GM_THREADS);
     cfg.dynamicSmemBytes = GM_SMEM;
-    e = cudaOccupancyMaxActiveClusters(pairs, muon_gemm_kernel<false, MU_UPDATE>, &cfg);
-    if (e == cudaSuccess && *pairs < 1) e = cudaErrorNotSupported;
-    if (e == cudaSuccess && keep) known[dev].store(*pairs);
+    e = cudaOccupancyMaxActiveClusters(&d.pairs, muon_gemm_kernel<false, MU_UPDATE>, &cfg);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    cfg.blockDim = dim3(SP_THREADS);
+    cfg.dynamicSmemBytes = split_smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
+        cfg.gridDim = dim3(1u << i);
+        attr[0].val.clusterDim = {1u << i, 1, 1};
+        e = cudaOccupancyMaxActiveClusters(&d.clusters[i], muon_split_kernel<false, MU_UPDATE>, &cfg);
+    }
+    if (e == cudaSuccess && d.pairs < 1) e = cudaErrorNotSupported;
+    if (e == cudaSuccess) *out = known[dev] = d;
     return e;
 }
-
-#ifndef MU_LARGE
-#define MU_LARGE 74
-#endif
 
 cudaError_t launch_split(bool exact, unsigned tiles, unsigned parts, cudaStream_t st,
                          const GemmParams& g) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(tiles * parts);
     cfg.blockDim = dim3(SP_THREADS);
-    cfg.dynamicSmemBytes = sp_smem(exact);
+    cfg.dynamicSmemBytes = sp_smem(exact, g.stages);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -297,8 +323,9 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
     // typical entries of X near 1, the largest below 2^15
     const double S = std::exp2(std::min(13.0, std::ceil(0.5 * std::log2((double)rows * cols))));
 
-    int pairs = 0;
-    if ((e = muon_device(&pairs)) != cudaSuccess) return cuda_fail(e);
+    MuDevice dev;
+    if ((e = muon_device(&dev)) != cudaSuccess) return cuda_fail(e);
+    const int pairs = dev.pairs;
     EncodeFn fn = encode_fn(&e);
     if (!fn) return cuda_fail(e);
     MuonPreParams pp = {};
@@ -398,12 +425,13 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
         const int64_t kblocks = ceil_div64(g.K, GM_K);
         int64_t tiles = cut(SP_TILE);
         if (tiles * B > MAX_N / 8) return cudaErrorInvalidValue;
-        int split = 1;
-        while (split < SP_MAX_SPLIT && tiles * B * split * 2 <= 2 * pairs && kblocks >= split * 4)
-            split *= 2;
+        // as many blocks a tile as run at once, each with two 64s of K at least
+        int lg = 0;
+        while (lg < 3 && tiles * B <= dev.clusters[lg + 1] && kblocks >= 4 << lg) ++lg;
+        const int split = 1 << lg;
         const bool long_sums = exact && kblocks > (int64_t)split * SP_MAX_SUM;
         cudaError_t r;
-        if (long_sums || cut(GM_TILE) * B >= MU_LARGE) {
+        if (long_sums || cut(GM_TILE) * B >= (exact ? MU_PAIR_TILES_22 : MU_PAIR_TILES_11)) {
             tiles = cut(GM_TILE);
             g.tiles = (int32_t)tiles;
             // where the last round would leave half of the pairs idle, its tiles are
@@ -419,6 +447,7 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
         } else {
             cut(SP_TILE);
             g.tiles = (int32_t)tiles;
+            g.stages = !exact && tiles * B <= dev.clusters[lg] ? SP_MAX_STAGES : SP_MIN_STAGES;
             trace_before(st, "muon_split_kernel");
             r = launch_split(exact, (unsigned)(tiles * B), (unsigned)split, st, g);
         }
