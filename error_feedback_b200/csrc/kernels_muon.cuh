@@ -31,6 +31,15 @@ namespace tke {
 constexpr float MU_SA = 2048.0f;           // scale of A and B
 constexpr float MU_REACH = 4.0f;           // |p(x)| the coefficients may reach (host check)
 constexpr int MU_MAX_LIFT = 60;
+// The tensor core truncates where it adds 16 products to an fp32 accumulator: a
+// sum of squares of n such adds comes out low, by 5.4e-8 n of its value on
+// average (measured for n = 2 .. 60: 4.9e-8 n to 7.0e-8 n, with a spread of 5e-8
+// in all; 2^-24 = 6.0e-8).  With fp32 output accumulators are kept short, and
+// what is left is multiplied back in the gram and the square, whose diagonals are
+// sums of squares.  The update's terms have both signs: there the factor makes
+// it worse.  A 100 x 200 matrix is 2.5e-6 off without, 1.5e-6 with it (plain
+// fp32: 1.4e-6), one of 2,048 x 8,192 7.3e-6 and 4.5e-6 (3.6e-6).
+constexpr float MU_LOW = 5.4e-8f;
 constexpr uint64_t MU_WAIT_NS = 2000000000ull;
 
 // ------------------------------------------------------- momentum and norm
@@ -530,11 +539,9 @@ __device__ __forceinline__ void epilogue32(const GemmParams& p, const TileAt& at
 // issues the products into one of two TMEM accumulators (2 x 256 columns)
 // while eight warps of each block drain the other.
 //
-// The tensor core's own fp32 accumulation truncates: a sum of K / 16 products
-// of one sign comes out up to K / 16 half-steps low.  With fp32 output the
-// accumulator is therefore handed over after every 128 of K, the small
-// products (hi lo, lo hi) before the large of each 64, and added up in registers with
-// rounding to nearest.
+// With fp32 output (see MU_LOW) the accumulator is handed over after every 128
+// of K, the small products (hi lo, lo hi) before the large of each 64, and added
+// up in registers with rounding to nearest.
 template <bool EXACT, int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
     muon_gemm_kernel(const __grid_constant__ GemmParams p) {
@@ -704,7 +711,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
             const int64_t row = at.m + quad * 32 + lane;
             float fs, fx;
             lift_factors<MODE>(p, at.b, &fs, &fx);
-            const float alpha = p.alpha * fs, beta = p.beta * fx;
+            // (a hand-over: 4 adds, 8 of the small products at half the sum, 4 adds)
+            const float low = EXACT && MODE <= MU_SQUARE ? MU_LOW * (kblocks == 1 ? 4.0f : 16.0f) : 0.0f;
+            const float alpha = p.alpha * fs * (1.0f + low), beta = p.beta * fx;
             const int64_t o = at.b * p.stride + row * p.ld + at.n + col;
             const bool mirror = !piece.diagonal;
             float x[32];
@@ -973,6 +982,7 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
     float fs, fx;
     lift_factors<MODE>(p, at.b, &fs, &fx);
     const float alpha = p.alpha * fs, beta = p.beta * fx;
+    const float low = MODE > MU_SQUARE ? 0.0f : MU_LOW * (GM_K / 16) * (float)n / (float)min(n, BIG);
     float* sums = reinterpret_cast<float*>(raw + (base - smem_u32(raw)));
 #pragma unroll 1
     for (int c = col; c < col + SP_TILE / 2; c += 32) {
@@ -987,6 +997,8 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] += w[j];
             }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = fmaf(low, v[j], v[j]);
         }
         float* to = sums + (quad * 32 + lane) * SP_LD + c;
 #pragma unroll
@@ -1216,6 +1228,7 @@ __global__ void __launch_bounds__(TN_THREADS, 1) muon_tiny_kernel(const __grid_c
             alpha = by / MU_SA;
             beta = by * coef[0];
         }
+        if (!update) alpha *= 1.0f + MU_LOW * (float)(((mode == MU_GRAM ? Q : P) + 15) / 16);
         const int chunks = ((update ? Q : P) + 63) / 64;
         uint8_t* buf = mem + (update ? 0 : 2 * TN_X);
         const uint32_t lo_at = update ? TN_X : TN_A;
