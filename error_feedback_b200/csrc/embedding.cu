@@ -2,7 +2,8 @@
 // (include/topk_ef.h): argument checks, workspace layout, launch sequences.
 //
 //   embedding_lookup:     lookup_kernel
-//   embedding_grad*:      rank_kernel (short lists), or per 9-bit digit of the id (sort_count_kernel ->
+//   embedding_grad*:      a few tokens: grad_direct_kernel alone; else
+//                         rank_kernel (short lists), or per 9-bit digit of the id (sort_count_kernel ->
 //                         [sort_prefix_kernel, many tiles] -> sort_scatter_kernel)
 //                         -> grad_sum_kernel -> grad_combine_kernel
 #include <cuda_runtime.h>
@@ -131,7 +132,7 @@ int grad_call(const void* dy, int32_t dy_type, int64_t ld_dy, const void* ids, i
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const GLayout L = grad_layout(T, V, D);
     char* w = static_cast<char*>(ws);
-    const bool brief = T > 0 && T <= SR_MAX;
+    const bool direct = T > 0 && T <= DR_MAX, brief = T > 0 && T <= SR_MAX;
     cudaError_t e = cudaSuccess;
     if (!brief) e = cudaMemsetAsync(w, 0, L.zero_end, st);
     if (e == cudaSuccess && rows && T == 0) e = cudaMemsetAsync(out_count, 0, 4, st);
@@ -151,7 +152,9 @@ int grad_call(const void* dy, int32_t dy_type, int64_t ld_dy, const void* ids, i
     sp.padding = padding;
     sp.tiles = (int32_t)L.sort_tiles;
     int cur = 0;
-    if (brief) {
+    if (direct) {
+        // (launched below)
+    } else if (brief) {
         RankParams rp = {};
         rp.ids = ids;
         rp.key = reinterpret_cast<uint32_t*>(w + L.key[0]);
@@ -224,6 +227,37 @@ int grad_call(const void* dy, int32_t dy_type, int64_t ld_dy, const void* ids, i
     p.accumulate = accumulate ? 1 : 0;
     p.scale = scale;
     int64_t fill_blocks = 0;
+    if (direct) {
+        DirectParams dp = {};
+        dp.ids = ids;
+        dp.ctrl = sp.ctrl;
+        dp.padding = padding;
+        dp.id64 = id_bytes == 8;
+        p.slabs = (int32_t)std::max<int64_t>(1, ceil_div64(D, DR_COLS));
+        p.sum_blocks = T * p.slabs;
+        if (fill) {
+            p.fill_rows = std::min<int64_t>(
+                DR_FILL_ROWS, std::max<int64_t>(DR_WARPS, EG_FILL_BYTES / (D * (int64_t)so)));
+            fill_blocks = ceil_div64(V, p.fill_rows);
+        }
+        dp.g = p;
+        const int64_t blocks = p.sum_blocks + fill_blocks;
+        if (blocks > MAX_N) return TOPK_EF_ERR_INVALID_ARG;
+        const bool vec = rows16(dy, ld_dy, sd) && rows16(out, ld_out, so);
+        trace_before(st, "grad_direct_kernel");
+        e = with_type(dy_type, [&](auto td) {
+            return with_type(out_type, [&](auto to) {
+                using TD = decltype(td);
+                using TO = decltype(to);
+                return vec ? launch_pdl(grad_direct_kernel<TD, TO, true>, (unsigned)blocks,
+                                        DR_THREADS, st, dp)
+                           : launch_pdl(grad_direct_kernel<TD, TO, false>, (unsigned)blocks,
+                                        DR_THREADS, st, dp);
+            });
+        });
+        trace_after(st);
+        return e == cudaSuccess ? TOPK_EF_OK : cuda_fail(e);
+    }
     if (fill && !brief) {
         p.fill_rows = std::max<int64_t>(EG_THREADS / 32, EG_FILL_BYTES / (D * (int64_t)so));
         fill_blocks = ceil_div64(V, p.fill_rows);

@@ -747,4 +747,180 @@ __global__ void __launch_bounds__(EC_THREADS) grad_combine_kernel(const GradPara
     }
 }
 
+// -------------------------------------------------- a few tokens: one kernel
+
+// Up to DR_MAX positions: a block per (position, DR_COLS columns).  Every block
+// reads the whole list; the block of an id's first position sums the id's rows:
+// the warps take contiguous parts of them, and their sums are added in order.
+// One launch of independent blocks instead of three chained ones: 500 positions
+// of 1,024 columns in 6.2 us on the GPU against 15.
+constexpr int DR_THREADS = 128;
+constexpr int DR_WARPS = DR_THREADS / 32;
+constexpr int DR_MAX = 512;
+constexpr int DR_COLS = 256;
+constexpr int DR_TABLE = 2 * DR_MAX;       // distinct ids, open addressing
+constexpr int DR_FILL_ROWS = 2048;         // rows of one fill block, at most
+
+struct DirectParams {
+    GradParams g;                  // (dy, out, out_rows, out_count, sizes, strides, scale)
+    const void* ids;
+    Ctrl* ctrl;
+    int64_t padding;
+    int32_t id64;
+};
+
+template <typename TD, typename TO, bool VEC>
+__global__ void __launch_bounds__(DR_THREADS) grad_direct_kernel(const DirectParams p) {
+    __shared__ uint32_t s_key[DR_MAX], s_same[DR_MAX / 32], s_list[DR_MAX], s_red[33];
+    __shared__ uint32_t s_table[DR_TABLE];
+    __shared__ __align__(16) float s_part[DR_WARPS][DR_COLS];
+    __shared__ int s_n;
+    pdl_launch();
+    const int tid = (int)threadIdx.x, lane = (int)lane_id(), warp = (int)warp_id();
+    const GradParams& g = p.g;
+    const int T = (int)g.T;
+    const uint32_t none = (uint32_t)g.V;
+    pdl_wait();
+    int bad_any = 0;
+#pragma unroll
+    for (int j = 0; j < DR_MAX / DR_THREADS; ++j) {
+        const int i = j * DR_THREADS + tid;
+        bool bad = false;
+        uint32_t k = none;
+        if (i < T)
+            k = p.id64 ? sort_key(static_cast<const int64_t*>(p.ids), i, g.V, p.padding, bad)
+                       : sort_key(static_cast<const int32_t*>(p.ids), i, g.V, p.padding, bad);
+        s_key[i] = k;
+        bad_any |= bad;
+    }
+    if (g.out_rows)
+        for (int i = tid; i < DR_TABLE; i += DR_THREADS) s_table[i] = none;
+    bad_any = __syncthreads_or(bad_any);
+
+    if ((int64_t)blockIdx.x >= g.sum_blocks) {
+        // rows of a dense gradient that no position names
+        __shared__ uint32_t s_named[DR_FILL_ROWS / 32];
+        for (int i = tid; i < DR_FILL_ROWS / 32; i += DR_THREADS) s_named[i] = 0;
+        __syncthreads();
+        const int64_t r0 = ((int64_t)blockIdx.x - g.sum_blocks) * g.fill_rows;
+        const int64_t r1 = min(g.V, r0 + g.fill_rows);
+        for (int i = tid; i < T; i += DR_THREADS) {
+            const int64_t k = s_key[i];
+            if (k >= r0 && k < r1) atomicOr(&s_named[(k - r0) >> 5], 1u << ((k - r0) & 31));
+        }
+        __syncthreads();
+        for (int64_t v = r0 + warp; v < r1; v += DR_WARPS)
+            if (!(s_named[(v - r0) >> 5] >> ((v - r0) & 31) & 1u))
+                zero_row(static_cast<TO*>(g.out) + v * g.ld_out, g.D, lane);
+        return;
+    }
+    if (blockIdx.x == 0 && tid == 0) {
+        p.ctrl->path_small = 0;
+        p.ctrl->status = bad_any ? ST_BAD_INPUT : 0u;
+    }
+    const int t = (int)(blockIdx.x / (unsigned)g.slabs);
+    const int slab = (int)(blockIdx.x - (unsigned)t * (unsigned)g.slabs);
+    const uint32_t mine = s_key[t];
+    int earlier = 0;
+#pragma unroll
+    for (int j = 0; j < DR_MAX / DR_THREADS; ++j) {
+        const int i = j * DR_THREADS + tid;
+        const bool same = i < T && s_key[i] == mine;
+        earlier |= same && i < t;
+        const uint32_t word = __ballot_sync(0xFFFFFFFFu, same);
+        if (lane == 0) s_same[i >> 5] = word;
+    }
+    earlier = __syncthreads_or(earlier);
+    const bool counts = g.out_rows && blockIdx.x == 0;     // writes the number of ids
+    const bool sums = !earlier && mine != none;
+    if (!sums && !counts) return;
+
+    // row-sparse output: ids below this one, and in all, by a table of distinct ids
+    int64_t row = mine;
+    if (g.out_rows) {
+        for (int i = tid; i < T; i += DR_THREADS) {
+            const uint32_t k = s_key[i];
+            if (k == none) continue;
+            uint32_t at = (k * 2654435761u) >> 16 & (DR_TABLE - 1);
+            for (;; at = (at + 1) & (DR_TABLE - 1)) {       // (never full)
+                const uint32_t was = atomicCAS(&s_table[at], none, k);
+                if (was == none || was == k) break;
+            }
+        }
+        __syncthreads();
+        uint32_t below = 0, all = 0;
+        for (int i = tid; i < DR_TABLE; i += DR_THREADS) {
+            all += s_table[i] != none;
+            below += s_table[i] < mine;                     // (none is above every id)
+        }
+        row = block_sum(below, s_red);
+        all = block_sum(all, s_red);
+        if (counts && tid == 0) *g.out_count = (int32_t)all;
+        if (!sums) return;
+        if (slab == 0 && tid == 0) g.out_rows[row] = (int32_t)mine;
+    }
+    if (warp == 0) {
+        const uint32_t word = lane < DR_MAX / 32 ? s_same[lane] : 0;
+        uint32_t at = warp_incl_scan((uint32_t)__popc(word));
+        if (lane == 31) s_n = (int)at;
+        at -= __popc(word);
+        for (uint32_t w = word; w; w &= w - 1) s_list[at++] = lane * 32 + __ffs(w) - 1;
+    }
+    __syncthreads();
+    const int n = s_n, per = (n + DR_WARPS - 1) / DR_WARPS;
+    const int i0 = min(n, warp * per), i1 = min(n, i0 + per);
+    const TD* dy = static_cast<const TD*>(g.dy);
+    const int64_t c0 = (int64_t)slab * DR_COLS + (VEC ? lane * 8 : lane);
+    auto col = [&](int j) { return c0 + (VEC ? j : j * 32); };
+    const bool whole = col(7) < g.D;
+    float acc[8] = {};
+    constexpr int U = 4;                                    // rows in flight
+    for (int i = i0; i < i1; i += U) {
+        Vec8<TD> v[U];
+        TD sv[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i + u >= i1) continue;
+            const TD* src = dy + (int64_t)s_list[i + u] * g.ld_dy;
+            if (VEC && whole) {
+                v[u] = load8(src + c0);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sv[u][j] = col(j) < g.D ? src[col(j)] : from_f32<TD>(0.0f);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i + u >= i1) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] += VEC && whole ? elem8(v[u], j) : to_f32(sv[u][j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s_part[warp][VEC ? lane * 8 + j : lane + j * 32] = acc[j];
+    __syncthreads();
+    if (warp != 0) return;
+    const int used = (n + per - 1) / per;
+    for (int w = 1; w < used; ++w)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += s_part[w][VEC ? lane * 8 + j : lane + j * 32];
+    TO* dst = static_cast<TO*>(g.out) + row * g.ld_out;
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = g.scale * acc[j];
+    if (VEC && whole) {
+        if (g.accumulate) {
+            const Vec8<TO> o = load8(dst + c0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] += elem8(o, j);
+        }
+        store8(dst + c0, y);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (col(j) < g.D)
+                dst[col(j)] = from_f32<TO>(g.accumulate ? to_f32(dst[col(j)]) + y[j] : y[j]);
+    }
+}
+
 }  // namespace tke

@@ -158,6 +158,7 @@ def _run_grad(dt, ot, T, V, D, kind, ldd=0, ldo=0, off=0, pad=-1, acc=False, idt
 
 
 @pytest.mark.parametrize("T,V,D,kind", [
+    (512, 100, 520, "zipf"), (513, 100, 520, "zipf"), (512, 40, 72, "same"), (511, 2**18, 260, "uniform"),
     (1, 1, 1, "same"), (1, 40000, 8, "uniform"), (2, 3, 7, "same"), (31, 5, 33, "uniform"),
     (33, 1000, 1024, "uniform"), (500, 513, 100, "zipf"), (500, 3, 1001, "uniform"),
     (4096, 511, 64, "zipf"), (4097, 512, 40, "two"), (5000, 300, 1032, "runs"),
