@@ -90,11 +90,27 @@ GLayout grad_layout(int64_t T, int64_t V, int64_t D) {
     return L;
 }
 
+// Units of zeros that a scattering and a counting kernel write besides: about
+// what memory takes in the time that they need anyway.
+constexpr int64_t ES_SCATTER_UNITS = 1200, ES_COUNT_UNITS = 400;
+
 template <typename TI>
-cudaError_t launch_sort_pass(SortParams& sp, bool first, cudaStream_t st) {
+cudaError_t launch_sort_pass(SortParams& sp, bool first, Fill& zeros, int64_t& units,
+                             cudaStream_t st) {
+    // takes up to `most` units for a launch whose own blocks are the first `blocks`
+    auto with_units = [&](int blocks, int64_t most) {
+        const int64_t n = std::min(units, most);
+        sp.fill = zeros;
+        sp.fill_from = blocks;
+        zeros.first += n;
+        units -= n;
+        return blocks + (int)n;
+    };
+    // (the first count sees to the bitmap that says which rows stay out)
+    int grid = with_units(sp.tiles, first ? 0 : ES_COUNT_UNITS);
     trace_before(st, "sort_count_kernel");
-    cudaError_t e = first ? launch_pdl(sort_count_kernel<TI, true>, sp.tiles, ES_THREADS, st, sp)
-                          : launch_pdl(sort_count_kernel<TI, false>, sp.tiles, ES_THREADS, st, sp);
+    cudaError_t e = first ? launch_pdl(sort_count_kernel<TI, true>, grid, ES_THREADS, st, sp)
+                          : launch_pdl(sort_count_kernel<TI, false>, grid, ES_THREADS, st, sp);
     trace_after(st);
     if (e != cudaSuccess) return e;
     sp.scanned = sp.tiles > ES_SCAN_TILES;
@@ -104,7 +120,7 @@ cudaError_t launch_sort_pass(SortParams& sp, bool first, cudaStream_t st) {
         trace_after(st);
         if (e != cudaSuccess) return e;
     }
-    const int grid = sp.tiles + (first && sp.word_prefix ? 1 : 0);
+    grid = with_units(sp.tiles + (first && sp.word_prefix ? 1 : 0), ES_SCATTER_UNITS);
     trace_before(st, "sort_scatter_kernel");
     e = first ? launch_pdl(sort_scatter_kernel<TI, true>, grid, ES_THREADS, st, sp)
               : launch_pdl(sort_scatter_kernel<TI, false>, grid, ES_THREADS, st, sp);
@@ -151,6 +167,20 @@ int grad_call(const void* dy, int32_t dy_type, int64_t ld_dy, const void* ids, i
     sp.V = V;
     sp.padding = padding;
     sp.tiles = (int32_t)L.sort_tiles;
+    // the dense gradient's zeros, in units
+    Fill zeros = {};
+    int64_t units = 0;
+    if (fill) {
+        zeros.out = static_cast<char*>(out);
+        zeros.bitmap = brief ? nullptr : sp.bitmap;
+        zeros.V = V;
+        zeros.row_bytes = D * (int64_t)so;
+        zeros.stride_bytes = ld_out * (int64_t)so;
+        zeros.size = (int32_t)so;
+        zeros.rows = std::max<int64_t>(EG_THREADS / 32, FILL_BYTES / zeros.row_bytes);
+        if (direct) zeros.rows = std::min<int64_t>(zeros.rows, DR_FILL_ROWS);
+        units = ceil_div64(V, zeros.rows);
+    }
     int cur = 0;
     if (direct) {
         // (launched below)
@@ -165,25 +195,16 @@ int grad_call(const void* dy, int32_t dy_type, int64_t ld_dy, const void* ids, i
         rp.V = V;
         rp.padding = padding;
         rp.rank_blocks = (int32_t)ceil_div64(T, SR_KEYS);
-        int64_t blocks = rp.rank_blocks;
-        if (fill) {
-            rp.out = out;
-            rp.D = D;
-            rp.ld_out = ld_out;
-            rp.fill_rows = std::max<int64_t>(SR_THREADS / 32, EG_FILL_BYTES / (D * (int64_t)so));
-            blocks += ceil_div64(V, rp.fill_rows);
-        }
+        rp.fill = zeros;
+        const int64_t blocks = rp.rank_blocks + units;
         if (blocks > MAX_N) return TOPK_EF_ERR_INVALID_ARG;
         trace_before(st, "rank_kernel");
-        e = with_type(out_type, [&](auto to) {
-            using TO = decltype(to);
-            return id_bytes == 8
-                       ? launch_pdl(rank_kernel<int64_t, TO>, (unsigned)blocks, SR_THREADS, st, rp)
-                       : launch_pdl(rank_kernel<int32_t, TO>, (unsigned)blocks, SR_THREADS, st, rp);
-        });
+        e = id_bytes == 8 ? launch_pdl(rank_kernel<int64_t>, (unsigned)blocks, SR_THREADS, st, rp)
+                          : launch_pdl(rank_kernel<int32_t>, (unsigned)blocks, SR_THREADS, st, rp);
         trace_after(st);
         if (e != cudaSuccess) return cuda_fail(e);
         sp.word_prefix = nullptr;
+        units = 0;
     } else if (T > 0) {
         int bits = 1;
         while (bits < 32 && ((uint64_t)V >> bits) != 0) ++bits;
@@ -195,8 +216,8 @@ int grad_call(const void* dy, int32_t dy_type, int64_t ld_dy, const void* ids, i
             cur = i == 0 ? 0 : cur ^ 1;
             sp.key_out = reinterpret_cast<uint32_t*>(w + L.key[cur]);
             sp.pos_out = reinterpret_cast<uint32_t*>(w + L.pos[cur]);
-            e = id_bytes == 8 ? launch_sort_pass<int64_t>(sp, i == 0, st)
-                              : launch_sort_pass<int32_t>(sp, i == 0, st);
+            e = id_bytes == 8 ? launch_sort_pass<int64_t>(sp, i == 0, zeros, units, st)
+                              : launch_sort_pass<int32_t>(sp, i == 0, zeros, units, st);
             if (e != cudaSuccess) return cuda_fail(e);
         }
     }
@@ -226,7 +247,6 @@ int grad_call(const void* dy, int32_t dy_type, int64_t ld_dy, const void* ids, i
     p.sum_blocks = L.tiles * p.slabs;
     p.accumulate = accumulate ? 1 : 0;
     p.scale = scale;
-    int64_t fill_blocks = 0;
     if (direct) {
         DirectParams dp = {};
         dp.ids = ids;
@@ -235,13 +255,9 @@ int grad_call(const void* dy, int32_t dy_type, int64_t ld_dy, const void* ids, i
         dp.id64 = id_bytes == 8;
         p.slabs = (int32_t)std::max<int64_t>(1, ceil_div64(D, DR_COLS));
         p.sum_blocks = T * p.slabs;
-        if (fill) {
-            p.fill_rows = std::min<int64_t>(
-                DR_FILL_ROWS, std::max<int64_t>(DR_WARPS, EG_FILL_BYTES / (D * (int64_t)so)));
-            fill_blocks = ceil_div64(V, p.fill_rows);
-        }
+        p.fill = zeros;
         dp.g = p;
-        const int64_t blocks = p.sum_blocks + fill_blocks;
+        const int64_t blocks = p.sum_blocks + units;
         if (blocks > MAX_N) return TOPK_EF_ERR_INVALID_ARG;
         const bool vec = rows16(dy, ld_dy, sd) && rows16(out, ld_out, so);
         trace_before(st, "grad_direct_kernel");
@@ -258,11 +274,8 @@ int grad_call(const void* dy, int32_t dy_type, int64_t ld_dy, const void* ids, i
         trace_after(st);
         return e == cudaSuccess ? TOPK_EF_OK : cuda_fail(e);
     }
-    if (fill && !brief) {
-        p.fill_rows = std::max<int64_t>(EG_THREADS / 32, EG_FILL_BYTES / (D * (int64_t)so));
-        fill_blocks = ceil_div64(V, p.fill_rows);
-    }
-    const int64_t grid = p.sum_blocks + fill_blocks;
+    p.fill = zeros;
+    const int64_t grid = p.sum_blocks + units;
     if (grid > MAX_N) return TOPK_EF_ERR_INVALID_ARG;
     if (grid == 0) return TOPK_EF_OK;
     const bool vec = rows16(dy, ld_dy, sd) && rows16(out, ld_out, so);

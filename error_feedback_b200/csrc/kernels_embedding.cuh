@@ -125,6 +125,45 @@ __global__ void __launch_bounds__(LK_THREADS) lookup_kernel(const LookupParams p
     }
 }
 
+// ------------------------------------------------- zeros of a dense gradient
+
+// Rows of a dense gradient that no position names are written as zeros, in
+// units of about 32 KB that any block of a call may take: the blocks of the
+// sort, which leaves memory idle, take the first ones, the sums' the others.
+constexpr int64_t FILL_BYTES = 32768;
+
+struct Fill {
+    char* out;
+    const uint32_t* bitmap;        // ids that occur; null: every row is written
+    int64_t V, row_bytes, stride_bytes;
+    int64_t rows;                  // of one unit
+    int64_t first;                 // unit of this launch's first filling block
+    int32_t size;                  // of an element
+};
+
+__device__ __forceinline__ void zero_row(char* dst, int64_t bytes, int size, int lane) {
+    int64_t done = 0;
+    if ((uintptr_t)dst % 16 == 0) {
+        done = bytes / 16;
+        for (int64_t c = lane; c < done; c += 32)
+            reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
+        done *= 16;
+    }
+    if (size == 4) {
+        for (int64_t c = done / 4 + lane; c < bytes / 4; c += 32) reinterpret_cast<uint32_t*>(dst)[c] = 0;
+    } else {
+        for (int64_t c = done / 2 + lane; c < bytes / 2; c += 32) reinterpret_cast<uint16_t*>(dst)[c] = 0;
+    }
+}
+
+// The unit of the `block`-th filling block of a launch.
+__device__ __forceinline__ void fill_unit(const Fill& f, int64_t block) {
+    const int64_t r0 = (f.first + block) * f.rows, r1 = min(f.V, r0 + f.rows);
+    for (int64_t v = r0 + warp_id(); v < r1; v += blockDim.x / 32)
+        if (!f.bitmap || !(f.bitmap[v >> 5] >> (v & 31) & 1u))
+            zero_row(f.out + v * f.stride_bytes, f.row_bytes, f.size, (int)lane_id());
+}
+
 // ----------------------------------------------------- sort of the positions
 
 // Least-significant-digit radix sort of (key, position), 9 bits a pass:
@@ -154,6 +193,8 @@ struct SortParams {
     Ctrl* ctrl;
     int64_t T, V, padding;
     int32_t tiles, shift, scanned;
+    int32_t fill_from;             // blocks from this one on write zeros
+    Fill fill;
 };
 
 template <typename TI>
@@ -183,6 +224,10 @@ __global__ void __launch_bounds__(ES_THREADS) sort_count_kernel(const SortParams
         s_bits[threadIdx.x] = 0;
     }
     pdl_wait();
+    if (!FIRST && (int)blockIdx.x >= p.fill_from) {
+        fill_unit(p.fill, (int)blockIdx.x - p.fill_from);
+        return;
+    }
     __syncthreads();
     const int64_t base = (int64_t)blockIdx.x * ES_TILE;
 #pragma unroll
@@ -277,6 +322,10 @@ __global__ void __launch_bounds__(ES_THREADS) sort_scatter_kernel(const SortPara
     pdl_launch();
     const int tid = (int)threadIdx.x, lane = (int)lane_id(), warp = (int)warp_id();
     pdl_wait();
+    if ((int)blockIdx.x >= p.fill_from) {
+        fill_unit(p.fill, (int)blockIdx.x - p.fill_from);
+        return;
+    }
     if (FIRST && (int)blockIdx.x == p.tiles) {
         bitmap_prefix(p, s_red);
         return;
@@ -389,34 +438,17 @@ struct RankParams {
     Ctrl* ctrl;
     int64_t T, V, padding;
     int32_t rank_blocks;
-    void* out;                     // dense gradient to clear, or null
-    int64_t D, ld_out, fill_rows;
+    Fill fill;
 };
 
-template <typename TO>
-__device__ __forceinline__ void zero_row(TO* dst, int64_t D, int lane) {
-    if ((uintptr_t)dst % 16 == 0) {
-        constexpr int E = 16 / (int)sizeof(TO);
-        const int64_t whole = D / E;
-        for (int64_t c = lane; c < whole; c += 32)
-            reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
-        for (int64_t c = whole * E + lane; c < D; c += 32) dst[c] = from_f32<TO>(0.0f);
-    } else {
-        for (int64_t c = lane; c < D; c += 32) dst[c] = from_f32<TO>(0.0f);
-    }
-}
-
-template <typename TI, typename TO>
+template <typename TI>
 __global__ void __launch_bounds__(SR_THREADS) rank_kernel(const RankParams p) {
     __shared__ __align__(16) uint32_t s_key[SR_MAX];
     pdl_launch();
     pdl_wait();
     const int tid = (int)threadIdx.x;
     if ((int)blockIdx.x >= p.rank_blocks) {
-        const int64_t r0 = ((int64_t)blockIdx.x - p.rank_blocks) * p.fill_rows;
-        const int64_t r1 = min(p.V, r0 + p.fill_rows);
-        for (int64_t v = r0 + warp_id(); v < r1; v += SR_THREADS / 32)
-            zero_row(static_cast<TO*>(p.out) + v * p.ld_out, p.D, (int)lane_id());
+        fill_unit(p.fill, (int)blockIdx.x - p.rank_blocks);
         return;
     }
     const int T = (int)p.T, T4 = (T + 3) / 4;
@@ -469,7 +501,6 @@ constexpr int EG_THREADS = 128;
 constexpr int EG_COLS = EG_THREADS * 8;    // columns of one block
 constexpr int EG_MAX_C = 128;              // positions of one tile, at most
 constexpr int EC_LONG = 16;                // a run over more tiles is added up by a whole block
-constexpr int64_t EG_FILL_BYTES = 32768;   // zeros written by one fill block
 
 struct GradParams {
     const void* dy;
@@ -487,24 +518,16 @@ struct GradParams {
     int64_t T, V, D, Dp, ld_dy, ld_out;
     int64_t tiles;
     int64_t sum_blocks;            // tiles * slabs; the blocks after them fill with zeros
-    int64_t fill_rows;             // rows of one fill block
     int32_t slabs, C;
     int32_t accumulate;
     float scale;
+    Fill fill;
 };
 
 // Row of the row-sparse output that holds `key`.
 __device__ __forceinline__ int64_t ordinal(const GradParams& p, uint32_t key) {
     const uint32_t word = p.bitmap[key >> 5];
     return (int64_t)p.word_prefix[key >> 5] + __popc(word & ((1u << (key & 31)) - 1u));
-}
-
-template <typename TO>
-__device__ __forceinline__ void fill_block(const GradParams& p, int64_t f) {
-    const int64_t r0 = f * p.fill_rows, r1 = min(p.V, r0 + p.fill_rows);
-    for (int64_t v = r0 + warp_id(); v < r1; v += EG_THREADS / 32)
-        if (!(p.bitmap[v >> 5] >> (v & 31) & 1u))
-            zero_row(static_cast<TO*>(p.out) + v * p.ld_out, p.D, (int)lane_id());
 }
 
 // One block per (tile of C sorted positions, EG_COLS columns); thread j has 8
@@ -518,7 +541,7 @@ __global__ void __launch_bounds__(EG_THREADS, VEC && sizeof(TD) == 2 ? 10 : 8) g
     pdl_wait();
     const int tid = (int)threadIdx.x;
     if ((int64_t)blockIdx.x >= p.sum_blocks) {
-        fill_block<TO>(p, (int64_t)blockIdx.x - p.sum_blocks);
+        fill_unit(p.fill, (int64_t)blockIdx.x - p.sum_blocks);
         return;
     }
     const int64_t tile = (int64_t)blockIdx.x / p.slabs;
@@ -802,8 +825,8 @@ __global__ void __launch_bounds__(DR_THREADS) grad_direct_kernel(const DirectPar
         __shared__ uint32_t s_named[DR_FILL_ROWS / 32];
         for (int i = tid; i < DR_FILL_ROWS / 32; i += DR_THREADS) s_named[i] = 0;
         __syncthreads();
-        const int64_t r0 = ((int64_t)blockIdx.x - g.sum_blocks) * g.fill_rows;
-        const int64_t r1 = min(g.V, r0 + g.fill_rows);
+        const int64_t r0 = ((int64_t)blockIdx.x - g.sum_blocks) * g.fill.rows;
+        const int64_t r1 = min(g.V, r0 + g.fill.rows);
         for (int i = tid; i < T; i += DR_THREADS) {
             const int64_t k = s_key[i];
             if (k >= r0 && k < r1) atomicOr(&s_named[(k - r0) >> 5], 1u << ((k - r0) & 31));
@@ -811,7 +834,7 @@ __global__ void __launch_bounds__(DR_THREADS) grad_direct_kernel(const DirectPar
         __syncthreads();
         for (int64_t v = r0 + warp; v < r1; v += DR_WARPS)
             if (!(s_named[(v - r0) >> 5] >> ((v - r0) & 31) & 1u))
-                zero_row(static_cast<TO*>(g.out) + v * g.ld_out, g.D, lane);
+                zero_row(g.fill.out + v * g.fill.stride_bytes, g.fill.row_bytes, g.fill.size, lane);
         return;
     }
     if (blockIdx.x == 0 && tid == 0) {
