@@ -141,6 +141,7 @@ int grad_call(const void* dy, int32_t dy_type, int64_t ld_dy, const void* ids, i
     if (T > 0 && D > 0 && (!dy || !aligned(dy, sd))) return TOPK_EF_ERR_INVALID_ARG;
     const bool writes = D > 0 && V > 0 && (T > 0 || (!rows && !accumulate));
     if (writes && (!out || !aligned(out, so))) return TOPK_EF_ERR_INVALID_ARG;
+    if (writes && T > 0 && out == dy) return TOPK_EF_ERR_INVALID_ARG;
     if (rows && (!out_count || !aligned(out_count, 4) ||
                  (T > 0 && V > 0 && (!out_rows || !aligned(out_rows, 4)))))
         return TOPK_EF_ERR_INVALID_ARG;
@@ -229,7 +230,8 @@ int grad_call(const void* dy, int32_t dy_type, int64_t ld_dy, const void* ids, i
     p.pos = reinterpret_cast<uint32_t*>(w + L.pos[cur]);
     p.bitmap = reinterpret_cast<uint32_t*>(w + L.bitmap);
     p.word_prefix = sp.word_prefix;
-    p.out_rows = rows ? out_rows : nullptr;
+    p.out_rows = out_rows;
+    p.sparse = rows;
     p.out_count = out_count;
     p.head = reinterpret_cast<float*>(w + L.head);
     p.tail = reinterpret_cast<float*>(w + L.tail);
@@ -317,6 +319,7 @@ int embedding_lookup(const void* weight, int32_t weight_type, int64_t ld_weight,
     if (T > 0 && (!ids || !aligned(ids, id_bytes))) return TOPK_EF_ERR_INVALID_ARG;
     if (T > 0 && D > 0 && (!out || !aligned(out, so) || (V > 0 && (!weight || !aligned(weight, sw)))))
         return TOPK_EF_ERR_INVALID_ARG;
+    if (T > 0 && V > 0 && D > 0 && out == weight) return TOPK_EF_ERR_INVALID_ARG;
     if (ws_bytes < embedding_lookup_workspace_bytes()) return TOPK_EF_ERR_WORKSPACE;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     LookupParams p = {};

@@ -509,7 +509,7 @@ struct GradParams {
     const uint32_t* pos;
     const uint32_t* bitmap;
     const uint32_t* word_prefix;   // row-sparse output: ordinals
-    int32_t* out_rows;             // row-sparse output, or null
+    int32_t* out_rows;             // row-sparse output
     float* head;                   // [tiles][Dp]: run continued from the tile before
     float* tail;                   // [tiles][Dp]: run begun here that goes on in the next
     int32_t* out_count;            // (short list)
@@ -519,7 +519,7 @@ struct GradParams {
     int64_t tiles;
     int64_t sum_blocks;            // tiles * slabs; the blocks after them fill with zeros
     int32_t slabs, C;
-    int32_t accumulate;
+    int32_t accumulate, sparse;
     float scale;
     Fill fill;
 };
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(EG_THREADS, VEC && sizeof(TD) == 2 ? 10 : 8) g
     __syncthreads();
     // row-sparse output: the rows of this tile's runs follow one another
     int64_t row = 0;
-    if (p.out_rows) {
+    if (p.sparse) {
         if (p.word_prefix) {
             if (s_key[1] != none) row = ordinal(p, s_key[1]);
         } else {
@@ -587,10 +587,10 @@ __global__ void __launch_bounds__(EG_THREADS, VEC && sizeof(TD) == 2 ? 10 : 8) g
                 const int64_t far = tile + EC_LONG;
                 const int l = far < p.tiles && p.key[far * p.C] == k;
                 p.list[l][atomicAdd(p.list_count + l, 1u)] =
-                    make_uint4((uint32_t)tile, p.out_rows ? (uint32_t)row : k, k, 0u);
+                    make_uint4((uint32_t)tile, p.sparse ? (uint32_t)row : k, k, 0u);
             }
         } else {
-            if (!p.out_rows) row = k;
+            if (!p.sparse) row = k;
             TO* dst = static_cast<TO*>(p.out) + row * p.ld_out;
             float y[8];
 #pragma unroll
@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(EG_THREADS, VEC && sizeof(TD) == 2 ? 10 : 8) g
                         dst[col(j)] = from_f32<TO>(p.accumulate ? to_f32(dst[col(j)]) + y[j] : y[j]);
             }
         }
-        if (p.out_rows && !from_before && slab == 0 && tid == 0) p.out_rows[row] = (int32_t)k;
+        if (p.sparse && !from_before && slab == 0 && tid == 0) p.out_rows[row] = (int32_t)k;
         ++row;
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(EG_THREADS, VEC && sizeof(TD) == 2 ? 10 : 8) g
     while (m > 0 && s_key[m] == none) --m;
     if (m > 0) flush(m - 1, first, s_key[m] == s_key[m + 1]);
     // short list: the last run's block knows how many there are
-    if (p.out_rows && !p.word_prefix && slab == 0 && tid == 0 &&
+    if (p.sparse && !p.word_prefix && slab == 0 && tid == 0 &&
         (m == n ? start + n == p.T : (m > 0 || start == 0 || s_key[0] != none)))
         *p.out_count = (int32_t)row;
 }
@@ -816,7 +816,7 @@ __global__ void __launch_bounds__(DR_THREADS) grad_direct_kernel(const DirectPar
         s_key[i] = k;
         bad_any |= bad;
     }
-    if (g.out_rows)
+    if (g.sparse)
         for (int i = tid; i < DR_TABLE; i += DR_THREADS) s_table[i] = none;
     bad_any = __syncthreads_or(bad_any);
 
@@ -854,13 +854,13 @@ __global__ void __launch_bounds__(DR_THREADS) grad_direct_kernel(const DirectPar
         if (lane == 0) s_same[i >> 5] = word;
     }
     earlier = __syncthreads_or(earlier);
-    const bool counts = g.out_rows && blockIdx.x == 0;     // writes the number of ids
+    const bool counts = g.sparse && blockIdx.x == 0;     // writes the number of ids
     const bool sums = !earlier && mine != none;
     if (!sums && !counts) return;
 
     // row-sparse output: ids below this one, and in all, by a table of distinct ids
     int64_t row = mine;
-    if (g.out_rows) {
+    if (g.sparse) {
         for (int i = tid; i < T; i += DR_THREADS) {
             const uint32_t k = s_key[i];
             if (k == none) continue;

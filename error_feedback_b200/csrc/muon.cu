@@ -304,6 +304,13 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
     if (!empty && (!grad || !out || !aligned(grad, sg) || !aligned(out, so) ||
                    !aligned(momentum, 4)))
         return TOPK_EF_ERR_INVALID_ARG;
+    // (a small matrix's block writes its output while others still read theirs)
+    if (!empty && (momentum == grad || momentum == out ||
+                   (out == grad && B > 1 && (out_type != grad_type || ld_out != ld_grad ||
+                                             stride_out != stride_grad))))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (!empty && ceil_div64(rows, SP_TILE) * ceil_div64(cols, SP_TILE) * B > MAX_N / 8)
+        return TOPK_EF_ERR_INVALID_ARG;
     if (ws_bytes < need) return TOPK_EF_ERR_WORKSPACE;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
@@ -367,20 +374,6 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
         trace_after(st);
         return e == cudaSuccess ? TOPK_EF_OK : cuda_fail(e);
     }
-    const dim3 pre((unsigned)L.parts, (unsigned)B);
-    e = with_type(grad_type, [&](auto t) {
-        using TG = decltype(t);
-        trace_before(st, "muon_norm_kernel");
-        cudaError_t r = launch_pdl(muon_norm_kernel<TG>, pre, MN_THREADS, st, pp);
-        trace_after(st);
-        if (r != cudaSuccess) return r;
-        trace_before(st, "muon_scale_kernel");
-        r = launch_pdl(muon_scale_kernel<TG>, pre, MN_THREADS, st, pp);
-        trace_after(st);
-        return r;
-    });
-    if (e != cudaSuccess) return cuda_fail(e);
-
     const int32_t P = (int32_t)L.p, Q = (int32_t)std::max(rows, cols);
     // operand maps, made once for each use: gram, square and update of both X
     struct Maps {
@@ -407,6 +400,20 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
     ok = ok && fill(maps[2], ao, ao);
     if (!ok) return cuda_fail(cudaErrorInvalidValue);
 
+    const dim3 pre((unsigned)L.parts, (unsigned)B);
+    e = with_type(grad_type, [&](auto t) {
+        using TG = decltype(t);
+        trace_before(st, "muon_norm_kernel");
+        cudaError_t r = launch_pdl(muon_norm_kernel<TG>, pre, MN_THREADS, st, pp);
+        trace_after(st);
+        if (r != cudaSuccess) return r;
+        trace_before(st, "muon_scale_kernel");
+        r = launch_pdl(muon_scale_kernel<TG>, pre, MN_THREADS, st, pp);
+        trace_after(st);
+        return r;
+    });
+    if (e != cudaSuccess) return cuda_fail(e);
+
     auto launch = [&](GemmParams& g, const Maps& from) {
         for (int h = 0; h < parts; ++h) {
             g.a[h] = from.a[h];
@@ -424,7 +431,6 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
         };
         const int64_t kblocks = ceil_div64(g.K, GM_K);
         int64_t tiles = cut(SP_TILE);
-        if (tiles * B > MAX_N / 8) return cudaErrorInvalidValue;
         // as many blocks a tile as run at once, each with two 64s of K at least
         int lg = 0;
         while (lg < 3 && tiles * B <= dev.clusters[lg + 1] && kblocks >= 4 << lg) ++lg;

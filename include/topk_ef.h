@@ -402,7 +402,8 @@ size_t muon_workspace_bytes(int32_t B, int64_t rows, int64_t cols,
  * topk_ef_compress_batched read.
  *   grad       device, [B][rows][cols] of grad_type; rows ld_grad apart,
  *              matrices stride_grad apart
- *   momentum   device, fp32[B][rows][cols] contiguous, updated in place; or NULL
+ *   momentum   device, fp32[B][rows][cols] contiguous, updated in place; or
+ *              NULL; must not overlap grad or out
  *   B          0 <= B <= 65535;  0 <= rows, cols <= 2^20
  *   eps        >= 0
  *   coef       host, float[3 * steps], read before the call returns.  On the

@@ -48,18 +48,18 @@ COMMON = [dict(T=-1), dict(V=-1), dict(D=-1), dict(T=2**31), dict(D=2**24 + 1), 
           dict(ldo=7), dict(ws=None), dict(ws=WS + 8)]
 
 
-@pytest.mark.parametrize("change", COMMON + [dict(w=None), dict(w=4098), dict(wt=7), dict(ldw=7)])
+@pytest.mark.parametrize("change", COMMON + [dict(out=4096), dict(w=None), dict(w=4098), dict(wt=7), dict(ldw=7)])
 def test_lookup_rejects(lib, change):
     assert _call(lib.embedding_lookup, LOOKUP, **change) == ef.ERR_INVALID_ARG
 
 
-@pytest.mark.parametrize("change", COMMON + [dict(dy=None), dict(dy=4098), dict(dt=9), dict(ldd=7),
+@pytest.mark.parametrize("change", COMMON + [dict(out=4096), dict(dy=None), dict(dy=4098), dict(dt=9), dict(ldd=7),
                                              dict(ids=8196, idb=8)])
 def test_grad_rejects(lib, change):
     assert _call(lib.embedding_grad, GRAD, **change) == ef.ERR_INVALID_ARG
 
 
-@pytest.mark.parametrize("change", COMMON + [dict(rows=None), dict(rows=4097), dict(count=None),
+@pytest.mark.parametrize("change", COMMON + [dict(out=4096), dict(rows=None), dict(rows=4097), dict(count=None),
                                              dict(count=8194)])
 def test_rows_rejects(lib, change):
     assert _call(lib.embedding_grad_rows, ROWS, **change) == ef.ERR_INVALID_ARG

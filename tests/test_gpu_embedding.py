@@ -203,6 +203,35 @@ def test_grad_only_padding_and_empty():
     assert ef.topk_ef_last_device_status(ws) == 0 and (g == 0).all()
 
 
+@pytest.mark.parametrize("T", [3, 700, 9000])
+def test_empty_table(T):
+    """No rows at all: every id is outside."""
+    ids, dy = torch.zeros(T, dtype=torch.int64, device="cuda"), torch.ones(T, 8, device="cuda")
+    ws = torch.empty(ef.embedding_grad_workspace_bytes(T, 0, 8), dtype=torch.uint8, device="cuda")
+    count = torch.full((1,), 7, dtype=torch.int32, device="cuda")
+    rows, val, _ = ef.embedding_grad_rows(dy, ids, 0, out_count=count, ws=ws)
+    assert int(count) == 0 and rows.numel() == 0
+    assert ef.topk_ef_last_device_status(ws) == ef.ERR_BAD_INPUT
+    assert ef.embedding_grad(dy, ids, 0).shape == (0, 8)
+    assert (ef.embedding_lookup(dy[:0], ids) == 0).all()
+
+
+@pytest.mark.parametrize("T", [300, 3000, 9000])
+def test_offsets_past_32_bits(T):
+    """A table of more than 2^31 elements: the last rows, and the first."""
+    V, D = 2_200_000, 1024
+    w = torch.zeros(V, D, dtype=torch.bfloat16, device="cuda")
+    ids = torch.cat([torch.arange(V - T + 5, V), torch.arange(5)]).cuda()
+    w[ids] = torch.randn(T, D, device="cuda").bfloat16()
+    out = ef.embedding_lookup(w, ids)
+    assert torch.equal(out, w[ids])
+    w.fill_(1.0)
+    ef.embedding_grad(out, ids, V, out=w)
+    assert torch.equal(w[ids], out) and float(w[5:V - T + 5].abs().max()) == 0.0
+    ef.embedding_grad(out, ids, V, out=w, accumulate=True, scale=-1.0)
+    assert float(w[ids].abs().max()) == 0.0
+
+
 def test_grad_bad_ids_are_reported_and_contained():
     T, V, D = 50, 20, 33
     dy = torch.randn(T, D, device="cuda")

@@ -47,7 +47,9 @@ def test_workspace_sizes(lib):
     dict(out=16386), dict(mom=8194), dict(ws=None), dict(ws=WS + 8), dict(coef=None),
     dict(steps=0), dict(steps=65), dict(eps=-1.0), dict(eps=float("nan")),
     dict(coef=(float("nan"), 0, 0)), dict(coef=(5.0, 0, 0)), dict(coef=(4.0, -17.0, 0.0)),
-    dict(coef=(1.0, 2.0, 2.0)), dict(coef=(0.0, 0.0, 16.5))])
+    dict(coef=(1.0, 2.0, 2.0)), dict(coef=(0.0, 0.0, 16.5)), dict(mom=4096), dict(mom=16384),
+    dict(out=4096, so=56), dict(out=4096, ot=1), dict(rows=2**20, cols=2**20, B=4, ldg=2**20,
+    ldo=2**20, sg=2**40, so=2**40, wsb=2**62)])
 def test_rejects(lib, change):
     assert _call(lib, **change) == ef.ERR_INVALID_ARG
 
