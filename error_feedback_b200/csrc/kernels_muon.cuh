@@ -42,10 +42,16 @@ constexpr int MU_MAX_LIFT = 60;
 constexpr float MU_LOW = 5.4e-8f;
 constexpr uint64_t MU_WAIT_NS = 2000000000ull;
 
+__device__ __forceinline__ float below_half(float x) {     // what fp16 leaves of x
+    return x - __half2float(__float2half_rn(x));
+}
+
 // ------------------------------------------------------- momentum and norm
 
 constexpr int MN_THREADS = 256;
 constexpr int MN_MAX_PARTS = 1184;         // partial sums of one matrix
+template <typename TG>
+constexpr int MN_FLIGHT = sizeof(TG) == 2 ? 4 : 2;     // groups of 8 elements that a thread loads at once
 
 struct MuonPreParams {
     const void* grad;
@@ -60,6 +66,7 @@ struct MuonPreParams {
     float mu;
     int32_t nesterov;
     double eps, S;
+    int32_t flat;                  // grad, momentum and X are contiguous, in 16-byte steps
 };
 
 // u of up to 8 consecutive elements of one row; FIRST: the momentum is
@@ -109,7 +116,7 @@ __device__ __forceinline__ int muon_u8(const MuonPreParams& p, int64_t b, int64_
 // m <- mu m + g, and the partial sums of u^2 (64 bits, fixed order).  Eight
 // elements per thread at a time; bound by the bytes of g and m.
 template <typename TG>
-__global__ void __launch_bounds__(MN_THREADS) muon_norm_kernel(const MuonPreParams p) {
+__global__ void __launch_bounds__(MN_THREADS, 3) muon_norm_kernel(const MuonPreParams p) {
     __shared__ double s_red[33];
     pdl_launch();
     pdl_wait();
@@ -118,15 +125,57 @@ __global__ void __launch_bounds__(MN_THREADS) muon_norm_kernel(const MuonPrePara
         p.ctrl->path_small = 0;
         p.ctrl->status = 0;
     }
+    // squares of 8 elements in fp32, their sums in 64 bits; in 64 bits throughout
+    // where fp32 would not hold the squares (conversions of every element would set
+    // the pace: 85 us for 25,088 x 4,096 bf16)
     double sum = 0.0;
-#pragma unroll 4
-    for (int64_t i = (int64_t)blockIdx.x * MN_THREADS + threadIdx.x; i < p.groups;
-         i += (int64_t)gridDim.x * MN_THREADS) {
-        const int64_t r = i / p.row_groups;
-        float u[8];
-        muon_u8<TG, true>(p, b, r, (i - r * p.row_groups) * 8, u);
+    auto add8 = [&](const float* u) {
+        float s = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fma((double)u[j], (double)u[j], sum);
+        for (int j = 0; j < 8; ++j) s = fmaf(u[j], u[j], s);
+        if (s > 1e-25f && s < 1e35f) {
+            sum += (double)s;
+        } else {
+            for (int j = 0; j < 8; ++j) sum = fma((double)u[j], (double)u[j], sum);
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * MN_THREADS;
+    if (p.flat) {
+        const TG* g = static_cast<const TG*>(p.grad) + b * p.stride_g;
+        float* mom = p.momentum ? p.momentum + b * p.groups * 8 : nullptr;
+        for (int64_t i = (int64_t)blockIdx.x * MN_THREADS + threadIdx.x; i < p.groups;
+             i += MN_FLIGHT<TG> * step) {
+            Vec8<TG> gv[MN_FLIGHT<TG>];
+            Vec8<float> mv[MN_FLIGHT<TG>];
+#pragma unroll
+            for (int k = 0; k < MN_FLIGHT<TG>; ++k)
+                if (i + k * step < p.groups) {
+                    gv[k] = load8(g + (i + k * step) * 8);
+                    if (mom) mv[k] = load8(mom + (i + k * step) * 8);
+                }
+#pragma unroll
+            for (int k = 0; k < MN_FLIGHT<TG>; ++k) {
+                if (i + k * step >= p.groups) continue;
+                float m[8], u[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    u[j] = elem8(gv[k], j);
+                    if (mom) {
+                        m[j] = fmaf(p.mu, elem8(mv[k], j), u[j]);
+                        u[j] = p.nesterov ? fmaf(p.mu, m[j], u[j]) : m[j];
+                    }
+                }
+                add8(u);
+                if (mom) store8(mom + (i + k * step) * 8, m);
+            }
+        }
+    } else {
+        for (int64_t i = (int64_t)blockIdx.x * MN_THREADS + threadIdx.x; i < p.groups; i += step) {
+            const int64_t r = i / p.row_groups;
+            float u[8];
+            muon_u8<TG, true>(p, b, r, (i - r * p.row_groups) * 8, u);
+            add8(u);
+        }
     }
     const double tot = block_sum(sum, s_red);
     if (threadIdx.x == 0) p.part[b * p.parts + blockIdx.x] = tot;
@@ -136,7 +185,7 @@ __global__ void __launch_bounds__(MN_THREADS) muon_norm_kernel(const MuonPrePara
 // the norm of X below 1: then it brings the entries to where fp16 has all its
 // bits, and the products take it back as fast as X can grow.
 template <typename TG>
-__global__ void __launch_bounds__(MN_THREADS) muon_scale_kernel(const MuonPreParams p) {
+__global__ void __launch_bounds__(MN_THREADS, 3) muon_scale_kernel(const MuonPreParams p) {
     __shared__ double s_red[33];
     pdl_launch();
     pdl_wait();
@@ -149,20 +198,56 @@ __global__ void __launch_bounds__(MN_THREADS) muon_scale_kernel(const MuonPrePar
     if (norm > 0.0 && norm < p.eps) lift = min(MU_MAX_LIFT, ilogb((norm + p.eps) / norm));
     if (blockIdx.x == 0 && threadIdx.x == 0) p.lift[b] = lift;
     const double f = scalbn(p.S, lift) / (norm + p.eps);
-#pragma unroll 4
-    for (int64_t i = (int64_t)blockIdx.x * MN_THREADS + threadIdx.x; i < p.groups;
-         i += (int64_t)gridDim.x * MN_THREADS) {
-        const int64_t r = i / p.row_groups, c = (i - r * p.row_groups) * 8;
-        float u[8], l[8];
-        muon_u8<TG, false>(p, b, r, c, u);
+    const int64_t step = (int64_t)gridDim.x * MN_THREADS;
+    // (the factor of a norm near fp32's ends would not be an fp32 value)
+    const float f32 = (float)f;
+    const bool plain = f > 1e-36 && f < 1e36;
+    auto put = [&](int64_t o, float* u) {
+        float l[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            u[j] = (float)((double)u[j] * f);
-            l[j] = u[j] - __half2float(__float2half_rn(u[j]));
+            u[j] = plain ? u[j] * f32 : (float)((double)u[j] * f);
+            l[j] = below_half(u[j]);
         }
-        // (rows of X are padded to 64 columns)
-        store8(p.hi + b * p.stride_x + r * p.ldx + c, u);
-        store8(p.lo + b * p.stride_x + r * p.ldx + c, l);
+        store8(p.hi + o, u);
+        store8(p.lo + o, l);
+    };
+    if (p.flat) {
+        const TG* g = static_cast<const TG*>(p.grad) + b * p.stride_g;
+        const float* mom = p.momentum ? p.momentum + b * p.groups * 8 : nullptr;
+        for (int64_t i = (int64_t)blockIdx.x * MN_THREADS + threadIdx.x; i < p.groups;
+             i += MN_FLIGHT<TG> * step) {
+            Vec8<TG> gv[MN_FLIGHT<TG>];
+            Vec8<float> mv[MN_FLIGHT<TG>];
+#pragma unroll
+            for (int k = 0; k < MN_FLIGHT<TG>; ++k)
+                if (i + k * step < p.groups) {
+                    gv[k] = load8(g + (i + k * step) * 8);
+                    if (mom) mv[k] = load8(mom + (i + k * step) * 8);
+                }
+#pragma unroll
+            for (int k = 0; k < MN_FLIGHT<TG>; ++k) {
+                if (i + k * step >= p.groups) continue;
+                float u[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    u[j] = elem8(gv[k], j);
+                    if (mom) {
+                        const float m = elem8(mv[k], j);
+                        u[j] = p.nesterov ? fmaf(p.mu, m, u[j]) : m;
+                    }
+                }
+                put(b * p.stride_x + (i + k * step) * 8, u);
+            }
+        }
+    } else {
+        for (int64_t i = (int64_t)blockIdx.x * MN_THREADS + threadIdx.x; i < p.groups; i += step) {
+            const int64_t r = i / p.row_groups, c = (i - r * p.row_groups) * 8;
+            float u[8];
+            muon_u8<TG, false>(p, b, r, c, u);
+            // (rows of X are padded to 64 columns)
+            put(b * p.stride_x + r * p.ldx + c, u);
+        }
     }
 }
 
@@ -419,9 +504,6 @@ __device__ __forceinline__ void load_half16(const __half* p, float* v) {
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
     const __half2 h = __floats2half2_rn(x, y);
     return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float below_half(float x) {     // what fp16 leaves of x
-    return x - __half2float(__float2half_rn(x));
 }
 
 template <typename TO>

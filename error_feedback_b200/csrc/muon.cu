@@ -352,6 +352,8 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
     pp.parts = L.parts;
     pp.row_groups = ceil_div64(cols, 8);
     pp.groups = L.groups;
+    pp.flat = ld_grad == cols && cols % 64 == 0 && aligned(grad, 16) &&
+              stride_grad * (int64_t)sg % 16 == 0 && aligned(momentum, 16);
     pp.mu = mu;
     pp.nesterov = nesterov;
     pp.eps = eps;
