@@ -19,12 +19,6 @@ using namespace tke;
 
 namespace {
 
-size_t type_size(int32_t t) {
-    return t == TOPK_EF_F32 ? 4 : t == TOPK_EF_BF16 || t == TOPK_EF_F16 ? 2 : 0;
-}
-
-bool aligned(const void* p, size_t a) { return (uintptr_t)p % a == 0; }
-
 bool rows16(const void* p, int64_t ld, size_t size) {
     return aligned(p, 16) && (size_t)ld * size % 16 == 0;
 }
@@ -32,16 +26,6 @@ bool rows16(const void* p, int64_t ld, size_t size) {
 // ids, rows and columns that every call accepts
 bool sizes_ok(int64_t T, int64_t V, int64_t D) {
     return T >= 0 && T <= MAX_N && V >= 0 && V <= MAX_N && D >= 0 && D <= (int64_t)1 << 24;
-}
-
-// Calls f with a value of the C++ type of element type t.
-template <typename F>
-cudaError_t with_type(int32_t t, F f) {
-    switch (t) {
-        case TOPK_EF_F32: return f(float{});
-        case TOPK_EF_BF16: return f(__nv_bfloat16{});
-        default: return f(__half{});
-    }
 }
 
 // ------------------------------------------------------------------ gradient

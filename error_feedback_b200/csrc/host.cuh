@@ -1,9 +1,13 @@
 // Host helpers shared by the translation units of the C ABI.
 #pragma once
 
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
+
+#include "topk_ef.h"
 
 namespace tke {
 
@@ -11,6 +15,23 @@ constexpr int64_t MAX_N = 2147483647LL;
 constexpr size_t ALIGN = 256;
 
 inline size_t align_up(size_t x, size_t a = ALIGN) { return (x + a - 1) / a * a; }
+
+inline bool aligned(const void* p, size_t a) { return (uintptr_t)p % a == 0; }
+
+// Bytes of an element of type t (0: no such type).
+inline size_t type_size(int32_t t) {
+    return t == TOPK_EF_F32 ? 4 : t == TOPK_EF_BF16 || t == TOPK_EF_F16 ? 2 : 0;
+}
+
+// Calls f with a value of the C++ type of element type t.
+template <typename F>
+cudaError_t with_type(int32_t t, F f) {
+    switch (t) {
+        case TOPK_EF_F32: return f(float{});
+        case TOPK_EF_BF16: return f(__nv_bfloat16{});
+        default: return f(__half{});
+    }
+}
 
 // Records the error for topk_ef_last_cuda_error; returns TOPK_EF_ERR_CUDA.
 int cuda_fail(cudaError_t e);

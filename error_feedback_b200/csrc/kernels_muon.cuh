@@ -30,7 +30,7 @@ namespace tke {
 
 constexpr float MU_SA = 2048.0f;           // scale of A and B
 constexpr float MU_REACH = 4.0f;           // |p(x)| the coefficients may reach (host check)
-constexpr int MU_MAX_LIFT = 60;
+constexpr int MU_MAX_LIFT = 60;             // (see muon_scale_kernel)
 // The tensor core truncates where it adds 16 products to an fp32 accumulator: a
 // sum of squares of n such adds comes out low, by 5.4e-8 n of its value on
 // average (measured for n = 2 .. 60: 4.9e-8 n to 7.0e-8 n, with a spread of 5e-8
@@ -298,9 +298,6 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -652,7 +649,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
         mbar_init(smem_u32(&s_drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0 && lane < 3 * PARTS) prefetch_map(lane < 2 * PARTS ? lane < PARTS ? &p.a[lane] : &p.b[lane - PARTS] : &p.b_half[lane - 2 * PARTS]);
+    if (warp == 0 && lane < PARTS) {
+        prefetch_map(&p.a[lane]);
+        prefetch_map(&p.b[lane]);
+        prefetch_map(&p.b_half[lane]);
+    }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          smem_u32(&s_tmem))
@@ -674,95 +675,96 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
     // running sums of an epilogue thread need more: 72 + 216 + 216 = 3 x 168.
     const int group = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x / 128, 0);
     if (group == 0) {
-    if (EXACT) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 0 && lane == 0) {
-        // ---- loads (of what earlier kernels wrote with ordinary stores)
-        asm volatile("fence.proxy.async;" ::: "memory");
-        int stage = 0;
-        uint32_t phase = 0, issued = 0;
-        bool ok = true;
-        for (int t = pair; t < total && ok; t += pairs) {
-            const Piece piece = piece_at(p, t, rank);
-            const TileAt at = piece.at;
-            const int n0 = at.n + rank * (piece.width / 2);
-            const CUtensorMap* right = piece.width == GM_TILE ? p.b : p.b_half;
-            const uint32_t bytes = 2 * PARTS * (GM_OP + piece.width / 2 * GM_K * 2);
-            for (int kb = 0; kb < kblocks; ++kb) {
-                if (!(ok = mbar_wait(smem_u32(&s_empty[stage]), phase ^ 1, &s_gave_up, status)))
-                    break;
-                const uint32_t bar = in_block(smem_u32(&s_full[stage]), 0);
-                if (rank == 0) mbar_expect(smem_u32(&s_full[stage]), bytes);
-                const uint32_t dst = base + stage * STAGE;
-                const int k = kb * GM_K;
-#pragma unroll
-                for (int q = 0; q < PARTS; ++q) {
-                    tma_box(dst + q * GM_OP, &p.a[q], p.a_mn, at.m, k, at.b, bar);
-                    tma_box(dst + (PARTS + q) * GM_OP, right + q, p.b_mn, n0, k, at.b, bar);
-                }
-                ++issued;
-                if (++stage == STAGES) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            }
-        }
-        // no copy is in flight when the pair ends (its first block counts both blocks')
-        if (rank == 0)
-            for (uint32_t j = issued < STAGES ? issued : STAGES; j > 0; --j) {
-                const uint32_t n = issued - j;
-                volatile int never = 0;
-                mbar_wait(smem_u32(&s_full[n % STAGES]), (n / STAGES) & 1, &never, status);
-            }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
-        // ---- products
-        const uint32_t shape = (1u << 4) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16) |
-                               ((GM_TILE / 16) << 24);
-        const uint32_t a_step = p.a_mn ? 2048 : 32, b_step = p.b_mn ? 2048 : 32;
-        int stage = 0, slot = 0;
-        uint32_t phase = 0, slot_phase = 0;
-        bool ok = true;
-        for (int t = pair; t < total && ok; t += pairs) {
-            const uint32_t idesc = shape | ((uint32_t)((t < p.whole ? GM_TILE : GM_TILE / 2) / 8) << 17);
-            for (int kb = 0; kb < kblocks; ++kb) {
-                const bool begin = kb % (EXACT ? GM_HAND : kblocks) == 0;
-                const bool end = kb == kblocks - 1 || (EXACT && kb % GM_HAND == GM_HAND - 1);
-                if (begin) {
-                    if (!(ok = mbar_wait(smem_u32(&s_free[slot]), slot_phase ^ 1, &s_gave_up,
-                                         status)))
+        if (EXACT) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 0 && lane == 0) {
+            // ---- loads (of what earlier kernels wrote with ordinary stores)
+            asm volatile("fence.proxy.async;" ::: "memory");
+            int stage = 0;
+            uint32_t phase = 0, issued = 0;
+            bool ok = true;
+            for (int t = pair; t < total && ok; t += pairs) {
+                const Piece piece = piece_at(p, t, rank);
+                const TileAt at = piece.at;
+                const int n0 = at.n + rank * (piece.width / 2);
+                const CUtensorMap* right = piece.width == GM_TILE ? p.b : p.b_half;
+                const uint32_t bytes = 2 * PARTS * (GM_OP + piece.width / 2 * GM_K * 2);
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (!(ok = mbar_wait(smem_u32(&s_empty[stage]), phase ^ 1, &s_gave_up, status)))
                         break;
-                }
-                if (!(ok = mbar_wait(smem_u32(&s_full[stage]), phase, &s_gave_up, status))) break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t d = tmem + slot * GM_TILE;
-                const uint32_t a0 = base + stage * STAGE, b0 = a0 + PARTS * GM_OP;
-                if (EXACT) {
+                    const uint32_t bar = in_block(smem_u32(&s_full[stage]), 0);
+                    if (rank == 0) mbar_expect(smem_u32(&s_full[stage]), bytes);
+                    const uint32_t dst = base + stage * STAGE;
+                    const int k = kb * GM_K;
 #pragma unroll
-                    for (int k = 0; k < GM_K / 16; ++k) {
+                    for (int q = 0; q < PARTS; ++q) {
+                        tma_box(dst + q * GM_OP, &p.a[q], p.a_mn, at.m, k, at.b, bar);
+                        tma_box(dst + (PARTS + q) * GM_OP, right + q, p.b_mn, n0, k, at.b, bar);
+                    }
+                    ++issued;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            // no copy is in flight when the pair ends (its first block counts both blocks')
+            if (rank == 0)
+                for (uint32_t j = issued < STAGES ? issued : STAGES; j > 0; --j) {
+                    const uint32_t n = issued - j;
+                    volatile int never = 0;
+                    mbar_wait(smem_u32(&s_full[n % STAGES]), (n / STAGES) & 1, &never, status);
+                }
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            // ---- products
+            const uint32_t shape = (1u << 4) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16) |
+                                   ((GM_TILE / 16) << 24);
+            const uint32_t a_step = p.a_mn ? 2048 : 32, b_step = p.b_mn ? 2048 : 32;
+            int stage = 0, slot = 0;
+            uint32_t phase = 0, slot_phase = 0;
+            bool ok = true;
+            for (int t = pair; t < total && ok; t += pairs) {
+                const uint32_t width = t < p.whole ? GM_TILE : GM_TILE / 2;
+                const uint32_t idesc = shape | ((width / 8) << 17);
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    const bool begin = kb % (EXACT ? GM_HAND : kblocks) == 0;
+                    const bool end = kb == kblocks - 1 || (EXACT && kb % GM_HAND == GM_HAND - 1);
+                    if (begin) {
+                        if (!(ok = mbar_wait(smem_u32(&s_free[slot]), slot_phase ^ 1, &s_gave_up,
+                                             status)))
+                            break;
+                    }
+                    if (!(ok = mbar_wait(smem_u32(&s_full[stage]), phase, &s_gave_up, status))) break;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t d = tmem + slot * GM_TILE;
+                    const uint32_t a0 = base + stage * STAGE, b0 = a0 + PARTS * GM_OP;
+                    if (EXACT) {
+#pragma unroll
+                        for (int k = 0; k < GM_K / 16; ++k) {
+                            mma_f16(d, smem_desc(a0 + k * a_step, p.a_mn),
+                                    smem_desc(b0 + GM_OP + k * b_step, p.b_mn), idesc, !begin || k > 0);
+                            mma_f16(d, smem_desc(a0 + GM_OP + k * a_step, p.a_mn),
+                                    smem_desc(b0 + k * b_step, p.b_mn), idesc, true);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < GM_K / 16; ++k)
                         mma_f16(d, smem_desc(a0 + k * a_step, p.a_mn),
-                                smem_desc(b0 + GM_OP + k * b_step, p.b_mn), idesc, !begin || k > 0);
-                        mma_f16(d, smem_desc(a0 + GM_OP + k * a_step, p.a_mn),
-                                smem_desc(b0 + k * b_step, p.b_mn), idesc, true);
+                                smem_desc(b0 + k * b_step, p.b_mn), idesc, EXACT || !begin || k > 0);
+                    mma_commit(smem_u32(&s_empty[stage]));
+                    if (end) {
+                        mma_commit(smem_u32(&s_done[slot]));
+                        if (++slot == 2) {
+                            slot = 0;
+                            slot_phase ^= 1;
+                        }
                     }
-                }
-#pragma unroll
-                for (int k = 0; k < GM_K / 16; ++k)
-                    mma_f16(d, smem_desc(a0 + k * a_step, p.a_mn),
-                            smem_desc(b0 + k * b_step, p.b_mn), idesc, EXACT || !begin || k > 0);
-                mma_commit(smem_u32(&s_empty[stage]));
-                if (end) {
-                    mma_commit(smem_u32(&s_done[slot]));
-                    if (++slot == 2) {
-                        slot = 0;
-                        slot_phase ^= 1;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
                     }
-                }
-                if (++stage == STAGES) {
-                    stage = 0;
-                    phase ^= 1;
                 }
             }
         }
-    }
     } else {
         if (EXACT) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         // ---- epilogue: warp w reads TMEM lanes 32 (w mod 4) .., half of the columns
@@ -794,7 +796,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
             float fs, fx;
             lift_factors<MODE>(p, at.b, &fs, &fx);
             // (a hand-over: 4 adds, 8 of the small products at half the sum, 4 adds)
-            const float low = EXACT && MODE <= MU_SQUARE ? MU_LOW * (kblocks == 1 ? 4.0f : 16.0f) : 0.0f;
+            const float low =
+                EXACT && MODE <= MU_SQUARE ? MU_LOW * (kblocks == 1 ? 4.0f : 16.0f) : 0.0f;
             const float alpha = p.alpha * fs * (1.0f + low), beta = p.beta * fx;
             const int64_t o = at.b * p.stride + row * p.ld + at.n + col;
             const bool mirror = !piece.diagonal;
@@ -978,7 +981,10 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
         mbar_init(smem_u32(&s_done), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0 && lane < 2 * PARTS) prefetch_map(lane & 1 ? &p.b[lane >> 1] : &p.a[lane >> 1]);
+    if (warp == 0 && lane < PARTS) {
+        prefetch_map(&p.a[lane]);
+        prefetch_map(&p.b[lane]);
+    }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&s_tmem)), "n"(COLS)

@@ -32,12 +32,6 @@ constexpr int32_t MU_MAX_STEPS = 64;
 // x 2,048 (gram of 36) 579 or 573.
 constexpr int64_t MU_PAIR_TILES_11 = 12, MU_PAIR_TILES_22 = 37;
 
-size_t type_size(int32_t t) {
-    return t == TOPK_EF_F32 ? 4 : t == TOPK_EF_BF16 || t == TOPK_EF_F16 ? 2 : 0;
-}
-
-bool aligned(const void* p, size_t a) { return (uintptr_t)p % a == 0; }
-
 struct MuLayout {
     int64_t p, ldx, ldp, stride_x, stride_p, groups, parts;
     size_t ctrl, part, lift, x[2][2], a[2], b[2], total;
@@ -128,15 +122,6 @@ bool coefficients_ok(const float* coef, int32_t steps, int32_t* drop) {
         drop[i + 1] = drop[i] + (growth > 1.0 ? (int32_t)std::ceil(std::log2(growth)) : 0);
     }
     return true;
-}
-
-template <typename F>
-cudaError_t with_type(int32_t t, F f) {
-    switch (t) {
-        case TOPK_EF_F32: return f(float{});
-        case TOPK_EF_BF16: return f(__nv_bfloat16{});
-        default: return f(__half{});
-    }
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
