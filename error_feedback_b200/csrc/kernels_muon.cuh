@@ -273,7 +273,7 @@ struct GemmParams {
     // round: {64, K, columns / 64, batch}: 64 K rows of one or two chunks of 64.
     CUtensorMap a[2], b[2], b_half[2];
     int32_t M, N, K, batch, tiles_m, tiles_n, tiles;   // tiles: of one matrix
-    int32_t stages;                // clusters: stages of the ring
+    int32_t stages, width;         // clusters: stages of the ring, columns of an update's tile
     int32_t whole;                 // pairs: tiles taken whole, the others in two halves of columns
     int32_t a_mn, b_mn;            // operand's M (N) dimension is the contiguous one
     int32_t n_fast;                // neighbouring tiles differ in N
@@ -444,9 +444,9 @@ struct TileAt {
     int b, m, n;       // batch, this block's first row, the tile's first column
 };
 
-// The t-th size x size tile of this call.  Symmetric outputs: tiles (i, j)
-// with i >= j, row by row.
-__device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t, int size) {
+// The t-th size x width tile of this call.  Symmetric outputs (width = size):
+// tiles (i, j) with i >= j, row by row.
+__device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t, int size, int width) {
     TileAt r;
     r.b = t / p.tiles;
     t -= r.b * p.tiles;
@@ -464,7 +464,7 @@ __device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t, int size) 
         i = t - j * p.tiles_m;
     }
     r.m = i * size;
-    r.n = j * size;
+    r.n = j * width;
     return r;
 }
 
@@ -478,7 +478,7 @@ struct Piece {
 __device__ __forceinline__ Piece piece_at(const GemmParams& p, int u, int rank) {
     Piece r;
     const int h = u - p.whole;
-    r.at = tile_at(p, h < 0 ? u : p.whole + (h >> 1), GM_TILE);
+    r.at = tile_at(p, h < 0 ? u : p.whole + (h >> 1), GM_TILE, GM_TILE);
     r.diagonal = r.at.m == r.at.n;
     r.width = h < 0 ? GM_TILE : GM_TILE / 2;
     r.at.m += rank * GM_ROWS;
@@ -996,7 +996,9 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = s_tmem;
     uint32_t* status = &p.ctrl->status;
-    const TileAt at = tile_at(p, (int)(blockIdx.x / split), SP_TILE);
+    // (an update that leaves SMs idle takes 64 columns at a time)
+    const int width = MODE <= MU_SQUARE ? SP_TILE : p.width;
+    const TileAt at = tile_at(p, (int)(blockIdx.x / split), SP_TILE, width);
     const int kblocks = (p.K + GM_K - 1) / GM_K;
     const int kb0 = (int)((int64_t)kblocks * rank / split);
     const int n = (int)((int64_t)kblocks * (rank + 1) / split) - kb0;
@@ -1005,18 +1007,19 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
 
     if (warp == 0 && lane == 0) {
         asm volatile("fence.proxy.async;" ::: "memory");
+        const CUtensorMap* right = width == SP_TILE ? p.b : p.b_half;
         int i = 0, s = 0;
         uint32_t phase = 0;
         for (; i < n; ++i) {
             if (!mbar_wait(smem_u32(&s_empty[s]), phase ^ 1, &s_gave_up, status)) break;
             const uint32_t bar = smem_u32(&s_full[s]);
-            mbar_expect(bar, STAGE);
+            mbar_expect(bar, PARTS * (GM_OP + width * GM_K * 2));
             const uint32_t dst = base + s * STAGE;
             const int k = (kb0 + i) * GM_K;
 #pragma unroll
             for (int q = 0; q < PARTS; ++q) {
                 tma_box1(dst + q * GM_OP, &p.a[q], p.a_mn, at.m, k, at.b, bar);
-                tma_box1(dst + (PARTS + q) * GM_OP, &p.b[q], p.b_mn, at.n, k, at.b, bar);
+                tma_box1(dst + (PARTS + q) * GM_OP, right + q, p.b_mn, at.n, k, at.b, bar);
             }
             if (++s == stages) {
                 s = 0;
@@ -1030,7 +1033,7 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
         }
     } else if (warp == 1 && lane == 0) {
         const uint32_t idesc = (1u << 4) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16) |
-                               ((SP_TILE / 8) << 17) | ((SP_TILE / 16) << 24);
+                               ((uint32_t)(width / 8) << 17) | ((SP_TILE / 16) << 24);
         const uint32_t a_step = p.a_mn ? 2048 : 32, b_step = p.b_mn ? 2048 : 32;
         int s = 0;
         uint32_t phase = 0;
@@ -1066,14 +1069,14 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
     }
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    const int quad = warp & 3, col = (warp >> 2) * (SP_TILE / 2);
+    const int quad = warp & 3;
     float fs, fx;
     lift_factors<MODE>(p, at.b, &fs, &fx);
     const float alpha = p.alpha * fs, beta = p.beta * fx;
     const float low = MODE > MU_SQUARE ? 0.0f : MU_LOW * (GM_K / 16) * (float)n / (float)min(n, BIG);
     float* sums = reinterpret_cast<float*>(raw + (base - smem_u32(raw)));
 #pragma unroll 1
-    for (int c = col; c < col + SP_TILE / 2; c += 32) {
+    for (int c = (warp >> 2) * 32; c < width; c += 64) {
         float v[32];
         const uint32_t src = tmem + c + ((uint32_t)(quad * 32) << 16);
         tmem_ld32(src, reinterpret_cast<uint32_t*>(v));
@@ -1099,19 +1102,21 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
     else if (split == 4) add_blocks<4>(sums, rank);
     else if (split == 8) add_blocks<8>(sums, rank);
 
-    // This block's rows, one per warp at a time; the mirror image is turned in
-    // shared memory.
-    constexpr int U = 4, WARPS = SP_THREADS / 32;
+    // This block's rows, one (two of 64 columns) per warp at a time; the mirror
+    // image is turned in shared memory.
+    constexpr int U = 4;
     const int rows = SP_TILE / (int)split, pitch = rows + 8;
-    const int64_t c0 = at.n + lane * 4;
+    const int lanes = width / 4, col = lane % lanes * 4;       // lanes of a row, first column
+    const int step = SP_THREADS / lanes;                       // rows at a time
+    const int64_t c0 = at.n + col;
     const bool mirror = MODE <= MU_SQUARE && at.m != at.n;
     __half* turned = reinterpret_cast<__half*>(sums + SP_TILE * SP_LD);    // [hi, lo][128][pitch]
-    for (int r0 = warp; r0 < rows; r0 += U * WARPS) {
+    for (int r0 = (int)threadIdx.x / lanes; r0 < rows; r0 += U * step) {
         float4 x[U];
         uint2 h[U], l[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = r0 + u * WARPS;
+            const int r = r0 + u * step;
             const int64_t row = at.m + rank * rows + r, o = at.b * p.stride + row * p.ld + c0;
             h[u] = l[u] = make_uint2(0, 0);
             if (MODE != MU_GRAM && r < rows && row < p.M && c0 < p.N) {
@@ -1122,21 +1127,21 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = min(r0 + u * WARPS, rows - 1);
-            x[u] = *reinterpret_cast<const float4*>(sums + (rank * rows + r) * SP_LD + lane * 4);
+            const int r = min(r0 + u * step, rows - 1);
+            x[u] = *reinterpret_cast<const float4*>(sums + (rank * rows + r) * SP_LD + col);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = r0 + u * WARPS;
+            const int r = r0 + u * step;
             if (r >= rows) continue;
             float* v = reinterpret_cast<float*>(&x[u]);
             epilogue4<EXACT, MODE>(p, at, alpha, beta, at.m + rank * rows + r, c0, h[u], l[u], v);
             if (mirror) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    turned[(lane * 4 + j) * pitch + r] = __float2half_rn(v[j]);
+                    turned[(col + j) * pitch + r] = __float2half_rn(v[j]);
                     if (EXACT)
-                        turned[(SP_TILE + lane * 4 + j) * pitch + r] = __float2half_rn(below_half(v[j]));
+                        turned[(SP_TILE + col + j) * pitch + r] = __float2half_rn(below_half(v[j]));
                 }
             }
         }
