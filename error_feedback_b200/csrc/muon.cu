@@ -67,12 +67,12 @@ MuLayout muon_layout(int32_t B, int64_t m, int64_t n, bool exact) {
     return L;
 }
 
-// Three products for 22 bits, or one for 11.  Also where the short side is at
-// most 64: there are too few terms for the 11-bit roundings to average out (1 x
-// 1,000 in bf16: 3.9e-3 off, against 1.6e-3), and the products wait for one
-// another more than for the tensor cores.
+// Three products for 22 bits, or one for 11.  Also where the short side fits one
+// tile: there are too few terms for the 11-bit roundings to average out (70 x 6,000
+// in bf16: 2.9e-3 off, against the 1.65e-3 of the output's own rounding), and the
+// products wait for one another more than for the tensor cores.
 bool muon_exact(int64_t m, int64_t n, int32_t out_type) {
-    return out_type == TOPK_EF_F32 || std::min(m, n) <= SP_TILE / 2;
+    return out_type == TOPK_EF_F32 || std::min(m, n) <= SP_TILE;
 }
 
 bool muon_sizes_ok(int32_t B, int64_t m, int64_t n) {
