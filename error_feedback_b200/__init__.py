@@ -485,7 +485,7 @@ def embedding_lookup(weight, ids, scale=1.0, out=None, out_dtype=None, ws=None, 
         ot, ldo = _matrix(o2, "out", dev)
         if o2.shape != (T, D):
             raise ValueError(f"out must hold [{T}, {D}] elements")
-        w = _workspace(_LOOKUP_WS, dev, ws)
+        w = ws if ws is not None else _workspace(_LOOKUP_WS, dev, None)
         rc = lib().embedding_lookup(weight.data_ptr(), wt, ldw, ids.data_ptr(), idb, T, V, D,
                                     scale, o2.data_ptr(), ot, ldo, w.data_ptr(),
                                     w.numel() * w.element_size(), st)
@@ -509,11 +509,14 @@ def _grad_args(grad_out, ids, num_rows):
     idb, T = _token_ids(ids, dev)
     if grad_out.shape[0] != T:
         raise ValueError("grad_out must hold one row for each id")
-    V, D = int(num_rows), grad_out.shape[1]
-    nb = embedding_grad_workspace_bytes(T, V, D)
-    if nb == 0:
-        raise TopkEfError(ERR_INVALID_ARG, "embedding_grad_workspace_bytes")
-    return grad_out, gt, ldg, dev, idb, T, V, D, nb
+    return grad_out, gt, ldg, dev, idb, T, int(num_rows), grad_out.shape[1]
+
+
+def _own_workspace(nbytes: int, device, what: str):
+    """A workspace for one call that was given none."""
+    if nbytes == 0:
+        raise TopkEfError(ERR_INVALID_ARG, what)
+    return _workspace(nbytes, device, None)
 
 
 def embedding_grad(grad_out, ids, num_rows, scale=1.0, padding_idx=-1, accumulate=False, out=None,
@@ -525,7 +528,9 @@ def embedding_grad(grad_out, ids, num_rows, scale=1.0, padding_idx=-1, accumulat
     topk_ef_compress reads).  Positions whose id is padding_idx contribute
     nothing; other ids outside [0, num_rows) neither, and they give
     ERR_BAD_INPUT from topk_ef_last_device_status(ws)."""
-    grad_out, gt, ldg, dev, idb, T, V, D, nb = _grad_args(grad_out, ids, num_rows)
+    grad_out, gt, ldg, dev, idb, T, V, D = _grad_args(grad_out, ids, num_rows)
+    if V < 0:
+        raise ValueError("num_rows must not be negative")
     _on_device(ws, dev)
 
     def call(st):
@@ -539,7 +544,9 @@ def embedding_grad(grad_out, ids, num_rows, scale=1.0, padding_idx=-1, accumulat
         ot, ldo = _matrix(o, "out", dev)
         if o.shape != (V, D):
             raise ValueError(f"out must be [{V}, {D}]")
-        w = _workspace(nb, dev, ws)
+        # (a workspace that is given is checked by the call)
+        w = ws if ws is not None else _own_workspace(
+            embedding_grad_workspace_bytes(T, V, D), dev, "embedding_grad_workspace_bytes")
         rc = lib().embedding_grad(grad_out.data_ptr(), gt, ldg, ids.data_ptr(), idb, T, V, D,
                                   scale, int(padding_idx), o.data_ptr(), ot, ldo,
                                   1 if accumulate else 0, w.data_ptr(),
@@ -557,7 +564,9 @@ def embedding_grad_rows(grad_out, ids, num_rows, scale=1.0, padding_idx=-1, out_
     ascending order (padding_idx left out), the gradient row of each, and
     their number.  Returns (rows int32[m], val [m, D], count int32[1]) with
     m = min(T, num_rows); slots from the count on are not written."""
-    grad_out, gt, ldg, dev, idb, T, V, D, nb = _grad_args(grad_out, ids, num_rows)
+    grad_out, gt, ldg, dev, idb, T, V, D = _grad_args(grad_out, ids, num_rows)
+    if V < 0:
+        raise ValueError("num_rows must not be negative")
     _on_device(ws, dev)
     m = min(T, V)
 
@@ -578,7 +587,8 @@ def embedding_grad_rows(grad_out, ids, num_rows, scale=1.0, padding_idx=-1, out_
         ot, ldo = _matrix(val, "out_val", dev)
         if val.shape[0] < m or val.shape[1] != D:
             raise ValueError(f"out_val must be [{m}, {D}]")
-        w = _workspace(nb, dev, ws)
+        w = ws if ws is not None else _own_workspace(
+            embedding_grad_workspace_bytes(T, V, D), dev, "embedding_grad_workspace_bytes")
         rc = lib().embedding_grad_rows(grad_out.data_ptr(), gt, ldg, ids.data_ptr(), idb, T, V, D,
                                        scale, int(padding_idx), rows.data_ptr(), val.data_ptr(),
                                        ot, ldo, count.data_ptr(), w.data_ptr(),
@@ -661,10 +671,8 @@ def muon_update(grad, momentum=None, mu=0.95, nesterov=True, coefficients=MUON_C
         ot, ldo, so, _ = _matrices(o, "out", dev)
         if o.shape != grad.shape:
             raise ValueError("out must have grad's shape")
-        nb = lib().muon_workspace_bytes(B, rows, cols, ot)
-        if nb == 0:
-            raise TopkEfError(ERR_INVALID_ARG, "muon_workspace_bytes")
-        w = _workspace(nb, dev, ws)
+        w = ws if ws is not None else _own_workspace(
+            lib().muon_workspace_bytes(B, rows, cols, ot), dev, "muon_workspace_bytes")
         rc = lib().muon_update(grad.data_ptr(), gt, ldg, sg, mp, B, rows, cols, mu,
                                1 if nesterov else 0, eps, coef, steps, scale, o.data_ptr(), ot,
                                ldo, so, w.data_ptr(), w.numel() * w.element_size(), st)
