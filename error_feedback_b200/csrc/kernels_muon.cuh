@@ -1178,18 +1178,25 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
 
 // ------------------------------------------------ small matrices: one kernel
 
-// A matrix of at most 128 x 256 (either way round): one block does the whole
-// call, with X, A and B in shared memory, the sums in TMEM and fp32 output's
-// three products throughout (they cost nothing here: each product waits for the
-// one before).  X is held with the short side as rows: chunks of 64 columns, 128
+// A matrix whose short side is at most 128 and whose long side at most 2,048: a
+// cluster of up to 8 blocks does the whole call, each with up to 256 columns of X
+// (the short side as rows), with X, A and B in shared memory, the sums in TMEM and
+// fp32 output's three products throughout (they cost nothing here: each product
+// waits for the one before).  Only the gram needs the other blocks: each adds up
+// its part of the rows over all of them, in block order, and hands them out.  X is held with the short side as rows: chunks of 64 columns, 128
 // rows of 128 swizzled bytes each, which the gram reads as K-major and the update
-// as N-major operand.  64 x 27, five steps: 31 us, against 107 in 17 launches.  What lies outside the matrix is zero and stays zero.
+// as N-major operand.  Bound by latency, and with a wide short side by the exchange
+// (64 KB into each block, and out of it): five steps of 64 x 27 take 31 us against
+// 107 in 17 launches, 64 x 600 66 against 123, two of 2,000 x 128 130 against 150.  What lies outside the matrix is zero and stays zero.
 constexpr int TN_THREADS = 256;
-constexpr int TN_ROWS = 128, TN_COLS = 256;
+constexpr int TN_ROWS = 128, TN_COLS = 256;            // of one block
+constexpr int TN_MAX_BLOCKS = 8;                       // of a matrix
 constexpr int TN_CHUNK = TN_ROWS * 128;                // bytes of 64 columns
 constexpr int TN_X = TN_COLS / 64 * TN_CHUNK, TN_A = TN_ROWS / 64 * TN_CHUNK;   // hi (or lo)
 constexpr int TN_SMEM = 2 * TN_X + 2 * TN_A + 1024;
 constexpr int TN_MAX_STEPS = 64;
+// groups of 8 columns that a thread adds up, at most: two blocks share 128 rows of 16
+constexpr int TN_GROUPS = TN_ROWS / 2 * (TN_ROWS / 8) / TN_THREADS;
 
 struct TinyParams {
     MuonPreParams pre;             // (rows, cols: the caller's; groups unused)
@@ -1206,11 +1213,16 @@ __device__ __forceinline__ uint32_t tn_unit(int r, int u) {
     return (uint32_t)(r * 128 + ((u ^ (r & 7)) << 4));
 }
 
+// ... and of an fp32 value in the place of X's entry (r, c).
+__device__ __forceinline__ uint32_t tn_f32(int r, int c) {
+    return (uint32_t)(c >> 6) * TN_CHUNK + tn_unit(r, (c & 63) >> 3) + (c & 3) * 4 + (c & 4 ? TN_X : 0);
+}
+
 template <typename TG>
 __global__ void __launch_bounds__(TN_THREADS, 1) muon_tiny_kernel(const __grid_constant__ TinyParams p) {
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t s_done;
-    __shared__ double s_red[33];
+    __shared__ double s_red[33], s_norm;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_gave_up;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
@@ -1237,45 +1249,73 @@ __global__ void __launch_bounds__(TN_THREADS, 1) muon_tiny_kernel(const __grid_c
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = s_tmem;
     uint32_t* status = &p.pre.ctrl->status;
-    const int64_t b = blockIdx.x;
-    const int m = (int)p.pre.rows, n = (int)p.pre.cols, total = m * n;
-    const bool tall = m > n;
-    const int P = tall ? n : m, Q = tall ? m : n;
-    if (b == 0 && tid == 0) {
+    // this block's columns of X: [q0, q0 + Q) of the long side
+    uint32_t blocks;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(blocks));
+    const int rank = (int)cluster_rank(), cl = (int)blocks;
+    const int64_t b = blockIdx.x / blocks;
+    const bool tall = p.pre.rows > p.pre.cols;
+    const int P = (int)(tall ? p.pre.cols : p.pre.rows), all = (int)(tall ? p.pre.rows : p.pre.cols);
+    const int share = ((all + cl - 1) / cl + 15) / 16 * 16;
+    const int q0 = rank * share, Q = min(all - q0, share);
+    const int n = tall ? P : Q, total = P * Q;             // this block's part: rows of n
+    const int64_t first = tall ? (int64_t)q0 * p.pre.cols : q0;
+    if (blockIdx.x == 0 && tid == 0) {
         p.pre.ctrl->path_small = 0;
         p.pre.ctrl->status = 0;
     }
 
     // ---- momentum, norm, X
-    const TG* g = static_cast<const TG*>(p.pre.grad) + b * p.pre.stride_g;
-    float* mom = p.pre.momentum ? p.pre.momentum + b * total : nullptr;
+    const TG* g = static_cast<const TG*>(p.pre.grad) + b * p.pre.stride_g +
+                  (tall ? q0 * p.pre.ld_g : q0);
+    float* mom =
+        p.pre.momentum ? p.pre.momentum + b * p.pre.rows * p.pre.cols + first : nullptr;
+    // (u waits in X's place as fp32: a 16-byte unit of hi and of lo are 8 values)
     double sum = 0.0;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = tid; i < total; i += TN_THREADS) {
         const int r = i / n, c = i - r * n;
         float u = to_f32(g[r * p.pre.ld_g + c]);
         if (mom) {
-            const float v = fmaf(p.pre.mu, mom[i], u);
-            mom[i] = v;
+            const int64_t o = (int64_t)r * p.pre.cols + c;
+            const float v = fmaf(p.pre.mu, mom[o], u);
+            mom[o] = v;
             u = p.pre.nesterov ? fmaf(p.pre.mu, v, u) : v;
         }
         sum = fma((double)u, (double)u, sum);
+        *reinterpret_cast<float*>(mem + (tall ? tn_f32(c, r) : tn_f32(r, c))) = u;
     }
-    const double norm = sqrt(block_sum(sum, s_red));
+    sum = block_sum(sum, s_red);
+    if (cl > 1) {
+        if (tid == 0) s_norm = sum;
+        cluster_sync();
+        double part = 0.0;
+        for (int q = 0; q < cl; ++q) {
+            double x;
+            asm volatile("ld.shared::cluster.f64 %0, [%1];"
+                         : "=d"(x) : "r"(in_block(smem_u32(&s_norm), q)));
+            part += x;
+        }
+        sum = part;
+    }
+    const double norm = sqrt(sum);
     int lift = 0;
     if (norm > 0.0 && norm < p.pre.eps) lift = min(MU_MAX_LIFT, ilogb((norm + p.pre.eps) / norm));
     const double f = scalbn(p.pre.S, lift) / (norm + p.pre.eps);
-#pragma unroll 4
-    for (int i = tid; i < total; i += TN_THREADS) {
-        const int r = i / n, c = i - r * n;
-        float u = to_f32(g[r * p.pre.ld_g + c]);
-        if (mom) u = p.pre.nesterov ? fmaf(p.pre.mu, mom[i], u) : mom[i];
-        const float y = (float)((double)u * f);
-        const int xr = tall ? c : r, xc = tall ? r : c;
-        const uint32_t o = (uint32_t)(xc >> 6) * TN_CHUNK + tn_unit(xr, (xc & 63) >> 3) + (xc & 7) * 2;
-        const __half h = __float2half_rn(y);
-        *reinterpret_cast<__half*>(mem + o) = h;
-        *reinterpret_cast<__half*>(mem + TN_X + o) = __float2half_rn(y - __half2float(h));
+    for (int i = tid; i < P * ((Q + 7) / 8); i += TN_THREADS) {
+        const int r = i / ((Q + 7) / 8), c = i - r * ((Q + 7) / 8);
+        const uint32_t o = (uint32_t)(c >> 3) * TN_CHUNK + tn_unit(r, c & 7);
+        float4* ph = reinterpret_cast<float4*>(mem + o);
+        float4* pl = reinterpret_cast<float4*>(mem + TN_X + o);
+        const float4 u0 = *ph, u1 = *pl;
+        float y[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = (float)((double)y[e] * f);
+        *reinterpret_cast<uint4*>(ph) =
+            make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
+        *reinterpret_cast<uint4*>(pl) =
+            make_uint4(pack2(below_half(y[0]), below_half(y[1])), pack2(below_half(y[2]), below_half(y[3])),
+                       pack2(below_half(y[4]), below_half(y[5])), pack2(below_half(y[6]), below_half(y[7])));
     }
 
     // ---- the products
@@ -1284,7 +1324,7 @@ __global__ void __launch_bounds__(TN_THREADS, 1) muon_tiny_kernel(const __grid_c
     const uint32_t lane_at = tmem + ((uint32_t)(quad * 32) << 16);
     uint32_t parity = 0;
     bool ok = true;
-    for (int i = 0; i < 3 * p.steps && ok; ++i) {
+    for (int i = 0; i < 3 * p.steps; ++i) {
         const int step = i / 3, mode = i - step * 3;   // gram, square, update
         const bool update = mode == MU_UPDATE, last = i == 3 * p.steps - 1;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1310,9 +1350,10 @@ __global__ void __launch_bounds__(TN_THREADS, 1) muon_tiny_kernel(const __grid_c
             }
             mma_commit1(smem_u32(&s_done));
         }
-        ok = mbar_wait(smem_u32(&s_done), parity, &s_gave_up, status);
-        ok = __syncthreads_and(ok);
-        if (!ok) break;
+        // (once a wait has given up the next ones do so at once; the block goes on, since
+        // the others of its cluster wait for it and read its memory)
+        const bool done = mbar_wait(smem_u32(&s_done), parity, &s_gave_up, status);
+        ok = __syncthreads_and(done) && ok;
         parity ^= 1;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 
@@ -1330,6 +1371,7 @@ __global__ void __launch_bounds__(TN_THREADS, 1) muon_tiny_kernel(const __grid_c
             beta = by * coef[0];
         }
         if (!update) alpha *= 1.0f + MU_LOW * (float)(((mode == MU_GRAM ? Q : P) + 15) / 16);
+        const bool exchange = mode == MU_GRAM && cl > 1;
         const int chunks = ((update ? Q : P) + 63) / 64;
         uint8_t* buf = mem + (update ? 0 : 2 * TN_X);
         const uint32_t lo_at = update ? TN_X : TN_A;
@@ -1358,7 +1400,7 @@ __global__ void __launch_bounds__(TN_THREADS, 1) muon_tiny_kernel(const __grid_c
                             y[e] = fmaf(alpha, v[u * 8 + e] + w[u * 8 + e],
                                         beta * (__half2float(hh[e]) + __half2float(ll[e])));
                     }
-                    if (last) {
+                    if (last || exchange) {
                         // fp32 in place: a 16-byte unit of hi and of lo are 8 values
                         *ph = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]),
                                          __float_as_uint(y[2]), __float_as_uint(y[3]));
@@ -1375,17 +1417,64 @@ __global__ void __launch_bounds__(TN_THREADS, 1) muon_tiny_kernel(const __grid_c
                 }
             }
         }
+        if (exchange) {
+            cluster_sync();
+            const int rows = (P + cl - 1) / cl, groups = (P + 7) / 8;
+            const int r0 = rank * rows, mine = max(0, min(P - r0, rows)) * groups;
+            uint4 h[TN_GROUPS], l[TN_GROUPS];
+#pragma unroll
+            for (int it = 0; it < TN_GROUPS; ++it) {
+                const int g = it * TN_THREADS + tid;
+                if (g >= mine) continue;
+                const int r = r0 + g / groups, c = g % groups;
+                const uint32_t at = a_at + (uint32_t)(c >> 3) * TN_CHUNK + tn_unit(r, c & 7);
+                float y[8] = {};
+#pragma unroll 4
+                for (int q = 0; q < cl; ++q) {
+                    const uint32_t from = in_block(at, q);
+                    float x[8];
+                    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(from));
+                    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                 : "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                                 : "r"(from + TN_A));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] += x[e];
+                }
+                h[it] = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]),
+                                   pack2(y[6], y[7]));
+                l[it] = make_uint4(pack2(below_half(y[0]), below_half(y[1])),
+                                   pack2(below_half(y[2]), below_half(y[3])),
+                                   pack2(below_half(y[4]), below_half(y[5])),
+                                   pack2(below_half(y[6]), below_half(y[7])));
+            }
+            cluster_sync();                                // every sum is read
+#pragma unroll
+            for (int it = 0; it < TN_GROUPS; ++it) {
+                const int g = it * TN_THREADS + tid;
+                if (g >= mine) continue;
+                const int r = r0 + g / groups, c = g % groups;
+                const uint32_t at = a_at + (uint32_t)(c >> 3) * TN_CHUNK + tn_unit(r, c & 7);
+                for (int q = 0; q < cl; ++q) {
+                    const uint32_t to = in_block(at, q);
+                    asm volatile("st.shared::cluster.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to),
+                                 "r"(h[it].x), "r"(h[it].y), "r"(h[it].z), "r"(h[it].w)
+                                 : "memory");
+                    asm volatile("st.shared::cluster.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + TN_A),
+                                 "r"(l[it].x), "r"(l[it].y), "r"(l[it].z), "r"(l[it].w)
+                                 : "memory");
+                }
+            }
+            cluster_sync();
+        }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     if (ok) {
         for (int i = tid; i < total; i += TN_THREADS) {
             const int r = i / n, c = i - r * n;
-            const int xr = tall ? c : r, xc = tall ? r : c;
-            const uint32_t o = (uint32_t)(xc >> 6) * TN_CHUNK + tn_unit(xr, (xc & 63) >> 3) +
-                               (xc & 3) * 4 + (xc & 4 ? TN_X : 0);
-            const float y = *reinterpret_cast<const float*>(mem + o);
-            const int64_t to = b * p.stride_out + r * p.ld_out + c;
+            const float y = *reinterpret_cast<const float*>(mem + (tall ? tn_f32(c, r) : tn_f32(r, c)));
+            const int64_t to = b * p.stride_out + (tall ? q0 + r : r) * p.ld_out + (tall ? c : q0 + c);
             if (p.out_type == 0) static_cast<float*>(p.out)[to] = y;
             else if (p.out_type == 1) static_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(y);
             else static_cast<__half*>(p.out)[to] = __float2half_rn(y);

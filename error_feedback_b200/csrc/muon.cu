@@ -243,22 +243,23 @@ cudaError_t muon_device(MuDevice* out) {
     return e;
 }
 
-cudaError_t launch_split(bool exact, unsigned tiles, unsigned parts, cudaStream_t st,
-                         const GemmParams& g) {
+// As launch_pdl, with clusters of `cluster` blocks.
+template <typename Kern, typename Arg>
+cudaError_t launch_clusters(Kern kernel, unsigned grid, unsigned cluster, int block, size_t smem,
+                            cudaStream_t st, const Arg& arg) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(tiles * parts);
-    cfg.blockDim = dim3(SP_THREADS);
-    cfg.dynamicSmemBytes = sp_smem(exact, g.stages);
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {parts, 1, 1};
+    attr[1].val.clusterDim = {cluster, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return with_kernel(exact, g.mode,
-                       [&](auto, auto split) { return cudaLaunchKernelEx(&cfg, split, g); });
+    return cudaLaunchKernelEx(&cfg, kernel, arg);
 }
 
 }  // namespace
@@ -343,7 +344,9 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
     pp.nesterov = nesterov;
     pp.eps = eps;
     pp.S = S;
-    if (std::min(rows, cols) <= TN_ROWS && std::max(rows, cols) <= TN_COLS) {
+    if (std::min(rows, cols) <= TN_ROWS && std::max(rows, cols) <= TN_MAX_BLOCKS * TN_COLS) {
+        unsigned blocks = 1;
+        while (blocks * TN_COLS < std::max(rows, cols)) blocks *= 2;
         TinyParams tp = {};
         tp.pre = pp;
         std::copy(coef, coef + 3 * steps, tp.coef);
@@ -356,7 +359,8 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
         tp.stride_out = stride_out;
         trace_before(st, "muon_tiny_kernel");
         e = with_type(grad_type, [&](auto t) {
-            return launch_pdl(muon_tiny_kernel<decltype(t)>, (unsigned)B, TN_THREADS, st, tp, TN_SMEM);
+            return launch_clusters(muon_tiny_kernel<decltype(t)>, (unsigned)B * blocks, blocks,
+                                   TN_THREADS, TN_SMEM, st, tp);
         });
         trace_after(st);
         return e == cudaSuccess ? TOPK_EF_OK : cuda_fail(e);
@@ -450,7 +454,10 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
             g.tiles = (int32_t)tiles;
             g.stages = !exact && tiles * B <= dev.clusters[lg] ? SP_MAX_STAGES : SP_MIN_STAGES;
             trace_before(st, "muon_split_kernel");
-            r = launch_split(exact, (unsigned)(tiles * B), (unsigned)split, st, g);
+            r = with_kernel(exact, g.mode, [&](auto, auto kernel) {
+                return launch_clusters(kernel, (unsigned)(tiles * B * split), (unsigned)split,
+                                       SP_THREADS, sp_smem(exact, g.stages), st, g);
+            });
         }
         trace_after(st);
         return r;

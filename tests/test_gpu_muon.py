@@ -72,7 +72,8 @@ def _make(shape, kind, seed):
 SHAPES = [(1, 1, 1), (1, 1, 1000), (1, 1000, 1), (1, 64, 27), (1, 27, 64), (1, 128, 256),
           (2, 129, 257), (3, 257, 129), (5, 16, 16), (1, 512, 700), (2, 700, 512), (1, 65, 2049),
           (1, 300, 300), (40, 130, 70), (1, 1030, 1100), (3, 256, 128), (1, 129, 128), (1, 128, 257),
-          (200, 40, 33), (2, 65, 255)]
+          (200, 40, 33), (2, 65, 255), (1, 100, 2000), (2, 1999, 100), (2, 17, 1025), (1, 128, 2048),
+          (3, 2048, 128), (1, 90, 513), (60, 50, 700), (1, 128, 2049)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
@@ -101,7 +102,7 @@ def test_spectra(kind, ot, shape):
 
 @pytest.mark.parametrize("nesterov", [False, True])
 @pytest.mark.parametrize("gt", ["f32", "bf16"])
-@pytest.mark.parametrize("shape", [(1, 40, 100), (2, 77, 33)])
+@pytest.mark.parametrize("shape", [(1, 40, 100), (2, 77, 33), (2, 30, 1500), (1, 900, 77), (1, 200, 300)])
 def test_momentum(nesterov, gt, shape):
     mom = _make(shape, "strong", 1)
     mu = 0.9
@@ -139,7 +140,8 @@ def test_result_is_orthogonal():
 
 @pytest.mark.parametrize("gt,ot", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f32")])
 @pytest.mark.parametrize("B,m,n,ldg,ldo,off", [(1, 50, 70, 72, 80, 8), (2, 70, 50, 51, 53, 1),
-                                               (3, 33, 64, 64, 64, 4)])
+                                               (3, 33, 64, 64, 64, 4), (2, 700, 90, 91, 93, 1),
+                                               (2, 90, 700, 704, 703, 3), (1, 300, 310, 312, 311, 1)])
 def test_strides(gt, ot, B, m, n, ldg, ldo, off):
     g = torch.Generator(device="cuda").manual_seed(1)
     sg, so = m * ldg + 16, m * ldo + 24
@@ -153,6 +155,15 @@ def test_strides(gt, ot, B, m, n, ldg, ldo, off):
     assert (obuf == 7.0).all()
 
 
+@pytest.mark.parametrize("shape", [(40, 60), (50, 900), (900, 50), (300, 200)])
+def test_out_may_be_grad_in_another_type(shape):
+    """One matrix: the same memory, rows at the same place, half the bytes."""
+    x = torch.randn(*shape, device="cuda")
+    want = ef.muon_update(x.clone(), out_dtype=torch.bfloat16)
+    out = x.view(torch.bfloat16)[:, :shape[1]]
+    assert torch.equal(ef.muon_update(x, out=out), want)
+
+
 def test_out_may_be_grad_and_part_of_a_bucket():
     bucket = torch.randn(10_000, device="cuda")
     keep = bucket.clone()
@@ -164,11 +175,12 @@ def test_out_may_be_grad_and_part_of_a_bucket():
 
 
 @pytest.mark.parametrize("ot", ["f32", "bf16"])
-def test_zero_tiny_huge_nan(ot):
+@pytest.mark.parametrize("n", [50, 600, 2500])
+def test_zero_tiny_huge_nan(ot, n):
     """Each matrix of the batch on its own: zeros stay zero, a tiny one is held
     by eps, a huge one (whose squares pass fp32's range) is normalised, NaN and
     infinity stay in theirs."""
-    x = _make((6, 40, 50), "strong", 3)
+    x = _make((6, 40, n), "strong", 3)
     x[0] = 0
     x[1] *= 1e-20
     x[2] *= 1e25
