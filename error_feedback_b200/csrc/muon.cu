@@ -509,6 +509,11 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
         g.out_type = out_type;
         g.ld_out = ld_out;
         g.stride_out = stride_out;
+        auto starts_on = [&](int64_t a) {
+            return aligned(out, (size_t)a) && ld_out * (int64_t)so % a == 0 &&
+                   (B == 1 || stride_out * (int64_t)so % a == 0);
+        };
+        g.out_align = starts_on(16) ? 16 : starts_on(4) ? 4 : 2;
         if ((e = launch(g, maps[3 + cur])) != cudaSuccess) return cuda_fail(e);
         cur ^= 1;
     }

@@ -141,7 +141,8 @@ def test_result_is_orthogonal():
 @pytest.mark.parametrize("gt,ot", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f32")])
 @pytest.mark.parametrize("B,m,n,ldg,ldo,off", [(1, 50, 70, 72, 80, 8), (2, 70, 50, 51, 53, 1),
                                                (3, 33, 64, 64, 64, 4), (2, 700, 90, 91, 93, 1),
-                                               (2, 90, 700, 704, 703, 3), (1, 300, 310, 312, 311, 1)])
+                                               (2, 90, 700, 704, 703, 3), (1, 300, 310, 312, 311, 1), (1, 1500, 1301, 1304, 1303, 1),
+                                               (1, 1300, 1500, 1500, 1501, 0), (1, 1100, 1288, 1288, 1296, 8)])
 def test_strides(gt, ot, B, m, n, ldg, ldo, off):
     g = torch.Generator(device="cuda").manual_seed(1)
     sg, so = m * ldg + 16, m * ldo + 24
