@@ -395,28 +395,31 @@ def _matrix(t, name: str, device=None):
     contiguous (the rows themselves may be apart)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _TYPE:
+    code = _TYPE.get(t.dtype)
+    if code is None:
         raise ValueError(f"{name} must be float32, bfloat16 or float16")
-    if device is not None and t.device != device:
+    if device is not None and t.get_device() != device.index:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    ld = t.stride(0) if rows > 1 else cols
-    if ld < cols:
+    if rows <= 1:
+        ld = cols
+    elif ld < cols:
         raise ValueError(f"the rows of {name} overlap")
-    return _TYPE[t.dtype], ld
+    return code, ld
 
 
 def _token_ids(ids, device):
     if not isinstance(ids, torch.Tensor) or not ids.is_cuda or not ids.is_contiguous() \
             or ids.dtype not in (torch.int32, torch.int64):
         raise ValueError("ids must be a contiguous int32 or int64 CUDA tensor")
-    if ids.device != device:
+    if ids.get_device() != device.index:
         raise ValueError(f"ids is on {ids.device}, not on {device}")
-    return ids.element_size(), ids.numel()
+    return 8 if ids.dtype == torch.int64 else 4, ids.numel()
 
 
 class _On:
@@ -452,7 +455,7 @@ def _on(device, stream, call):
 
 
 def _on_device(ws, device):
-    if ws is not None and ws.device != device:
+    if ws is not None and ws.get_device() != device.index:
         raise ValueError(f"ws is on {ws.device}, not on {device}")
 
 
@@ -488,7 +491,7 @@ def embedding_lookup(weight, ids, scale=1.0, out=None, out_dtype=None, ws=None, 
         w = ws if ws is not None else _workspace(_LOOKUP_WS, dev, None)
         rc = lib().embedding_lookup(weight.data_ptr(), wt, ldw, ids.data_ptr(), idb, T, V, D,
                                     scale, o2.data_ptr(), ot, ldo, w.data_ptr(),
-                                    w.numel() * w.element_size(), st)
+                                    w.nbytes, st)
         if rc != OK:
             _check(rc, "embedding_lookup")
         return o
@@ -550,7 +553,7 @@ def embedding_grad(grad_out, ids, num_rows, scale=1.0, padding_idx=-1, accumulat
         rc = lib().embedding_grad(grad_out.data_ptr(), gt, ldg, ids.data_ptr(), idb, T, V, D,
                                   scale, int(padding_idx), o.data_ptr(), ot, ldo,
                                   1 if accumulate else 0, w.data_ptr(),
-                                  w.numel() * w.element_size(), st)
+                                  w.nbytes, st)
         if rc != OK:
             _check(rc, "embedding_grad")
         return o
@@ -592,7 +595,7 @@ def embedding_grad_rows(grad_out, ids, num_rows, scale=1.0, padding_idx=-1, out_
         rc = lib().embedding_grad_rows(grad_out.data_ptr(), gt, ldg, ids.data_ptr(), idb, T, V, D,
                                        scale, int(padding_idx), rows.data_ptr(), val.data_ptr(),
                                        ot, ldo, count.data_ptr(), w.data_ptr(),
-                                       w.numel() * w.element_size(), st)
+                                       w.nbytes, st)
         if rc != OK:
             _check(rc, "embedding_grad_rows")
         return rows, val, count
@@ -675,7 +678,7 @@ def muon_update(grad, momentum=None, mu=0.95, nesterov=True, coefficients=MUON_C
             lib().muon_workspace_bytes(B, rows, cols, ot), dev, "muon_workspace_bytes")
         rc = lib().muon_update(grad.data_ptr(), gt, ldg, sg, mp, B, rows, cols, mu,
                                1 if nesterov else 0, eps, coef, steps, scale, o.data_ptr(), ot,
-                               ldo, so, w.data_ptr(), w.numel() * w.element_size(), st)
+                               ldo, so, w.data_ptr(), w.nbytes, st)
         if rc != OK:
             _check(rc, "muon_update")
         return o
