@@ -651,7 +651,7 @@ def muon_update(grad, momentum=None, mu=0.95, nesterov=True, coefficients=MUON_C
     [B, rows, cols]: momentum = mu momentum + grad (in place, contiguous
     float32; None: u = grad), u = grad + mu momentum (nesterov) or momentum,
     X = u / (||u||_F + eps), `steps` times X <- a X + (b A + c A A) X with
-    A = X X^T, out = scale X.  out: float32 (default; as exact as plain
+    A = X X^T, out = scale X.  out: float32 (default; about as exact as plain
     float32 products) or a 16-bit type (operands of the products rounded to
     11 bits); may be grad itself."""
     gt, ldg, sg, (B, rows, cols) = _matrices(grad, "grad")
