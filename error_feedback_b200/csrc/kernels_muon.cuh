@@ -1201,8 +1201,8 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
 
 // ------------------------------------------------ small matrices: one kernel
 
-// A matrix whose short side is at most 128 and whose long side at most 2,048: a
-// cluster of up to 8 blocks does the whole call, each with up to 256 columns of X
+// A matrix whose short side is at most 128 and whose long side at most 4,096: a
+// cluster of up to 16 blocks does the whole call, each with up to 256 columns of X
 // (the short side as rows), with X, A and B in shared memory, the sums in TMEM and
 // fp32 output's three products throughout (they cost nothing here: each product
 // waits for the one before).  Only the gram needs the other blocks: each adds up
@@ -1213,7 +1213,7 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
 // 107 in 17 launches, 64 x 600 66 against 123, two of 2,000 x 128 130 against 150.  What lies outside the matrix is zero and stays zero.
 constexpr int TN_THREADS = 256;
 constexpr int TN_ROWS = 128, TN_COLS = 256;            // of one block
-constexpr int TN_MAX_BLOCKS = 8;                       // of a matrix
+constexpr int TN_MAX_BLOCKS = 16;                      // of a matrix
 constexpr int TN_CHUNK = TN_ROWS * 128;                // bytes of 64 columns
 constexpr int TN_X = TN_COLS / 64 * TN_CHUNK, TN_A = TN_ROWS / 64 * TN_CHUNK;   // hi (or lo)
 constexpr int TN_SMEM = 2 * TN_X + 2 * TN_A + 1024;
@@ -1279,7 +1279,7 @@ __global__ void __launch_bounds__(TN_THREADS, 1) muon_tiny_kernel(const __grid_c
     const int64_t b = blockIdx.x / blocks;
     const bool tall = p.pre.rows > p.pre.cols;
     const int P = (int)(tall ? p.pre.cols : p.pre.rows), all = (int)(tall ? p.pre.rows : p.pre.cols);
-    const int share = ((all + cl - 1) / cl + 15) / 16 * 16;
+    const int share = (all + cl - 1) / cl;
     const int q0 = rank * share, Q = min(all - q0, share);
     const int n = tall ? P : Q, total = P * Q;             // this block's part: rows of n
     const int64_t first = tall ? (int64_t)q0 * p.pre.cols : q0;

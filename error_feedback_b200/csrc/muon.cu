@@ -185,6 +185,7 @@ cudaError_t with_kernel(bool exact, int mode, F f) {
 
 struct MuDevice {
     int pairs;                     // block pairs of muon_gemm_kernel that run at once
+    int tiny_blocks;               // blocks of the largest cluster of muon_tiny_kernel
     int clusters[4];               // clusters of 1, 2, 4, 8 blocks of muon_split_kernel, one block an SM
 };
 
@@ -216,8 +217,13 @@ cudaError_t muon_device(MuDevice* out) {
         }
     for (int32_t t = TOPK_EF_F32; t <= TOPK_EF_F16; ++t) {
         e = with_type(t, [&](auto type) {
-            return cudaFuncSetAttribute(muon_tiny_kernel<decltype(type)>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, TN_SMEM);
+            const cudaError_t r =
+                cudaFuncSetAttribute(muon_tiny_kernel<decltype(type)>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, TN_SMEM);
+            return r != cudaSuccess
+                       ? r
+                       : cudaFuncSetAttribute(muon_tiny_kernel<decltype(type)>,
+                                              cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         });
         if (e != cudaSuccess) return e;
     }
@@ -238,6 +244,16 @@ cudaError_t muon_device(MuDevice* out) {
         attr[0].val.clusterDim = {1u << i, 1, 1};
         e = cudaOccupancyMaxActiveClusters(&d.clusters[i], muon_split_kernel<false, MU_UPDATE>, &cfg);
     }
+    // clusters of more than 8 blocks run where enough SMs of a cluster's size lie together
+    int sixteen = 0;
+    if (e == cudaSuccess) {
+        cfg.gridDim = dim3(TN_MAX_BLOCKS);
+        cfg.blockDim = dim3(TN_THREADS);
+        cfg.dynamicSmemBytes = TN_SMEM;
+        attr[0].val.clusterDim = {TN_MAX_BLOCKS, 1, 1};
+        e = cudaOccupancyMaxActiveClusters(&sixteen, muon_tiny_kernel<float>, &cfg);
+    }
+    d.tiny_blocks = sixteen > 0 ? TN_MAX_BLOCKS : 8;
     if (e == cudaSuccess && d.pairs < 1) e = cudaErrorNotSupported;
     if (e == cudaSuccess) *out = known[dev] = d;
     return e;
@@ -344,7 +360,7 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
     pp.nesterov = nesterov;
     pp.eps = eps;
     pp.S = S;
-    if (std::min(rows, cols) <= TN_ROWS && std::max(rows, cols) <= TN_MAX_BLOCKS * TN_COLS) {
+    if (std::min(rows, cols) <= TN_ROWS && std::max(rows, cols) <= dev.tiny_blocks * TN_COLS) {
         unsigned blocks = 1;
         while (blocks * TN_COLS < std::max(rows, cols)) blocks *= 2;
         TinyParams tp = {};

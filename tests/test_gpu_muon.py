@@ -73,7 +73,8 @@ SHAPES = [(1, 1, 1), (1, 1, 1000), (1, 1000, 1), (1, 64, 27), (1, 27, 64), (1, 1
           (2, 129, 257), (3, 257, 129), (5, 16, 16), (1, 512, 700), (2, 700, 512), (1, 65, 2049),
           (1, 300, 300), (40, 130, 70), (1, 1030, 1100), (3, 256, 128), (1, 129, 128), (1, 128, 257),
           (200, 40, 33), (2, 65, 255), (1, 100, 2000), (2, 1999, 100), (2, 17, 1025), (1, 128, 2048),
-          (3, 2048, 128), (1, 90, 513), (60, 50, 700), (1, 128, 2049)]
+          (3, 2048, 128), (1, 90, 513), (60, 50, 700), (1, 128, 2049), (2, 20, 4096),
+          (1, 3000, 128), (9, 40, 2100), (1, 100, 4097)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
