@@ -1210,7 +1210,8 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
 // rows of 128 swizzled bytes each, which the gram reads as K-major and the update
 // as N-major operand.  Bound by latency, and with a wide short side by the exchange
 // (64 KB into each block, and out of it): five steps of 64 x 27 take 31 us against
-// 107 in 17 launches, 64 x 600 66 against 123, two of 2,000 x 128 130 against 150.  What lies outside the matrix is zero and stays zero.
+// 107 in 17 launches, 64 x 600 54 against 123, two of 2,000 x 128 104 against 150.
+// What lies outside the matrix is zero and stays zero.
 constexpr int TN_THREADS = 256;
 constexpr int TN_ROWS = 128, TN_COLS = 256;            // of one block
 constexpr int TN_MAX_BLOCKS = 16;                      // of a matrix

@@ -185,7 +185,7 @@ cudaError_t with_kernel(bool exact, int mode, F f) {
 
 struct MuDevice {
     int pairs;                     // block pairs of muon_gemm_kernel that run at once
-    int tiny_blocks;               // blocks of the largest cluster of muon_tiny_kernel
+    int tiny[5];                   // clusters of 1, 2, .. 16 blocks of muon_tiny_kernel
     int clusters[4];               // clusters of 1, 2, 4, 8 blocks of muon_split_kernel, one block an SM
 };
 
@@ -244,16 +244,13 @@ cudaError_t muon_device(MuDevice* out) {
         attr[0].val.clusterDim = {1u << i, 1, 1};
         e = cudaOccupancyMaxActiveClusters(&d.clusters[i], muon_split_kernel<false, MU_UPDATE>, &cfg);
     }
-    // clusters of more than 8 blocks run where enough SMs of a cluster's size lie together
-    int sixteen = 0;
-    if (e == cudaSuccess) {
-        cfg.gridDim = dim3(TN_MAX_BLOCKS);
-        cfg.blockDim = dim3(TN_THREADS);
-        cfg.dynamicSmemBytes = TN_SMEM;
-        attr[0].val.clusterDim = {TN_MAX_BLOCKS, 1, 1};
-        e = cudaOccupancyMaxActiveClusters(&sixteen, muon_tiny_kernel<float>, &cfg);
+    cfg.blockDim = dim3(TN_THREADS);
+    cfg.dynamicSmemBytes = TN_SMEM;
+    for (int i = 0; i < 5 && e == cudaSuccess; ++i) {
+        cfg.gridDim = dim3(1u << i);
+        attr[0].val.clusterDim = {1u << i, 1, 1};
+        e = cudaOccupancyMaxActiveClusters(&d.tiny[i], muon_tiny_kernel<float>, &cfg);
     }
-    d.tiny_blocks = sixteen > 0 ? TN_MAX_BLOCKS : 8;
     if (e == cudaSuccess && d.pairs < 1) e = cudaErrorNotSupported;
     if (e == cudaSuccess) *out = known[dev] = d;
     return e;
@@ -360,9 +357,17 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
     pp.nesterov = nesterov;
     pp.eps = eps;
     pp.S = S;
-    if (std::min(rows, cols) <= TN_ROWS && std::max(rows, cols) <= dev.tiny_blocks * TN_COLS) {
-        unsigned blocks = 1;
-        while (blocks * TN_COLS < std::max(rows, cols)) blocks *= 2;
+    // (clusters of 16 run only where so many SMs lie together)
+    const int64_t longest = std::max(rows, cols);
+    if (std::min(rows, cols) <= TN_ROWS &&
+        longest <= (dev.tiny[4] > 0 ? TN_MAX_BLOCKS : TN_MAX_BLOCKS / 2) * TN_COLS) {
+        // as few blocks as hold it, or more down to 64 columns each while all matrices
+        // still run at once (64 x 600: 68 us with 4 blocks, 54 with 16; twenty of 100 x
+        // 600 88 with 4, 220 with 16)
+        int lg = 0;
+        while ((TN_COLS << lg) < longest) ++lg;
+        while (lg < 4 && (64 << lg) < longest && B <= dev.tiny[lg + 1]) ++lg;
+        const unsigned blocks = 1u << lg;
         TinyParams tp = {};
         tp.pre = pp;
         std::copy(coef, coef + 3 * steps, tp.coef);
