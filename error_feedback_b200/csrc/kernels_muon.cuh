@@ -9,13 +9,16 @@
 // update (X' = a X + B X).  A and B are symmetric: only tiles that touch the
 // lower triangle are computed, and the epilogue writes them to both sides.
 //
-// Numbers: X is held as a pair of fp16 values, hi + lo (22 bits), times a power of
-// two that keeps typical entries near 1; A and B likewise times MU_SA.  A step
+// Numbers: X is held as a pair of fp16 values, hi + lo / MU_LO (22 bits), times a
+// power of two that keeps typical entries near 1; A and B likewise times MU_SA.  A step
 // multiplies small singular values by a (3.4 five times in a row), so a
 // rounding of X itself would be amplified 485 times: the term a X is taken
 // from hi + lo.  For 16-bit outputs the products read hi alone (11 bits; bf16
 // operands would leave an error six times a bf16 output's own rounding); for
-// fp32 outputs each product is hi hi + hi lo + lo hi.  All sums are fp32.
+// fp32 outputs each product is hi hi + (hi lo + lo hi) / MU_LO.  All sums are fp32.
+// lo is held times MU_LO because fp16's range ends 2^-24 below the typical entry:
+// a row of 1e-5 of the others would keep 7 bits of its 22, and be 3e-4 off in the
+// result, one of 1e-6 4e-3 (plain fp32: 2e-6; so held 2e-6, and 1e-4 at 1e-8).
 #pragma once
 
 #include <cuda.h>
@@ -29,6 +32,8 @@
 namespace tke {
 
 constexpr float MU_SA = 2048.0f;           // scale of A and B
+constexpr int MU_LO_BITS = 11;             // what fp16 leaves of 2^15 at most is 2^3: no overflow
+constexpr float MU_LO = 1 << MU_LO_BITS;   // scale of what fp16 leaves of X, A and B
 constexpr float MU_REACH = 4.0f;           // |p(x)| the coefficients may reach (host check)
 constexpr int MU_MAX_LIFT = 60;             // (see muon_scale_kernel)
 // The tensor core truncates where it adds 16 products to an fp32 accumulator: a
@@ -42,9 +47,10 @@ constexpr int MU_MAX_LIFT = 60;             // (see muon_scale_kernel)
 constexpr float MU_LOW = 5.4e-8f;
 constexpr uint64_t MU_WAIT_NS = 2000000000ull;
 
-__device__ __forceinline__ float below_half(float x) {     // what fp16 leaves of x
-    return x - __half2float(__float2half_rn(x));
+__device__ __forceinline__ float below_half(float x) {     // what fp16 leaves of x, as it is held
+    return MU_LO * (x - __half2float(__float2half_rn(x)));
 }
+__device__ __forceinline__ float of_pair(float hi, float lo) { return fmaf(lo, 1.0f / MU_LO, hi); }
 
 // ------------------------------------------------------- momentum and norm
 
@@ -182,7 +188,7 @@ __global__ void __launch_bounds__(MN_THREADS, 3) muon_norm_kernel(const MuonPreP
     if (threadIdx.x == 0) p.part[b * p.parts + blockIdx.x] = tot;
 }
 
-// X = u * S * 2^lift / (||u|| + eps) as hi + lo.  lift is 0 unless eps holds
+// X = u * S * 2^lift / (||u|| + eps) as a pair.  lift is 0 unless eps holds
 // the norm of X below 1: then it brings the entries to where fp16 has all its
 // bits, and the products take it back as fast as X can grow.
 template <typename TG>
@@ -260,7 +266,7 @@ __global__ void __launch_bounds__(MN_THREADS, 3) muon_scale_kernel(const MuonPre
 constexpr int GM_EPI_WARPS = 8;
 constexpr int GM_THREADS = 128 + 32 * GM_EPI_WARPS;    // load, product, 2 idle, epilogue
 constexpr int GM_TILE = 256, GM_ROWS = 128, GM_K = 64;
-constexpr int GM_HAND = 2;                             // fp32 output: stages of one handover
+constexpr int GM_HAND = 2;                             // fp32 output: stages of one hand-over
 constexpr int GM_BOX = 64 * 64 * 2;                    // bytes of one 64 x 64 fp16 box
 constexpr int GM_OP = GM_ROWS * GM_K * 2;              // one operand of one block and stage
 constexpr int GM_RING = 6 * 2 * GM_OP;                 // 196,608 bytes of stages
@@ -279,7 +285,7 @@ struct GemmParams {
     int32_t a_mn, b_mn;            // operand's M (N) dimension is the contiguous one
     int32_t n_fast;                // neighbouring tiles differ in N
     int32_t mode, out_type;
-    float alpha, beta;             // value = alpha * sum + beta * (src_hi + src_lo)
+    float alpha, beta;             // value = alpha * sum + beta * src
     const int32_t* lift;           // [batch]
     int32_t drop, drop_next;       // what earlier steps have taken off lift, and this one
     const __half* src[2];          // elementwise operand (square: A, update: X)
@@ -391,6 +397,14 @@ __device__ __forceinline__ void mma_f16(uint32_t tmem, uint64_t a, uint64_t b, u
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+// D = A B^T + D / MU_LO
+__device__ __forceinline__ void mma_f16_lower(uint32_t tmem, uint64_t a, uint64_t b, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p, %4;\n\t}" ::"r"(tmem),
+        "l"(a), "l"(b), "r"(idesc), "n"(MU_LO_BITS)
         : "memory");
 }
 __device__ __forceinline__ void mma_commit1(uint32_t bar) {
@@ -585,7 +599,7 @@ __device__ __forceinline__ void lift_factors(const GemmParams& p, int b, float* 
     else if (MODE == MU_LAST) *sum = *src = exp2f((float)-k);
 }
 
-// The elementwise operand of one row's 32 columns: hi, or hi + lo.
+// The elementwise operand of one row's 32 columns: hi, or both.
 template <bool EXACT, int MODE>
 __device__ __forceinline__ void load_src32(const GemmParams& p, int64_t o, bool live, float* x) {
 #pragma unroll
@@ -598,7 +612,7 @@ __device__ __forceinline__ void load_src32(const GemmParams& p, int64_t o, bool 
                 float l[16];
                 load_half16(p.src[1] + o + j, l);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) x[j + e] += l[e];
+                for (int e = 0; e < 16; ++e) x[j + e] = of_pair(x[j + e], l[e]);
             }
         }
     }
@@ -642,9 +656,12 @@ __device__ __forceinline__ void epilogue32(const GemmParams& p, const TileAt& at
 // update of 4,096 x 4,096 in 59, 60 and 112 us (1.15 to 1.2 PFLOP/s, symmetric
 // products by half), of 25,088 x 4,096 the update in 675 us (1.25 PFLOP/s).
 //
-// With fp32 output (see MU_LOW) the accumulator is handed over after every 128
-// of K, the small products (hi lo, lo hi) before the large of each 64, and added
-// up in registers with rounding to nearest.
+// With fp32 output (see MU_LOW) the accumulator is handed over after every 128 of K
+// and added up in registers with rounding to nearest: first the small products (hi
+// lo, lo hi) of both stages, which the first of the large ones divides by MU_LO.
+// The lo parts of a stage are free, and loaded again, before its hi parts.  (A
+// hand-over of every 64, which needs no two stages at once, keeps the epilogue's
+// warps busier than the tensor cores: 4,096 x 4,096 3.73 ms by 128, 4.59 by 64.)
 template <bool EXACT, int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
     muon_gemm_kernel(const __grid_constant__ GemmParams p) {
@@ -653,7 +670,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
     constexpr int STAGES = GM_RING / STAGE;
     constexpr int HALF = GM_TILE / 2;                  // columns of one epilogue warp
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t s_full[STAGES], s_empty[STAGES], s_done[2], s_free[2], s_drain;
+    __shared__ __align__(8) uint64_t s_full[STAGES], s_empty[STAGES], s_empty_lo[STAGES];
+    __shared__ __align__(8) uint64_t s_done[2], s_free[2], s_drain;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_gave_up;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
@@ -665,6 +683,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&s_full[s]), 1);
             mbar_init(smem_u32(&s_empty[s]), 1);
+            mbar_init(smem_u32(&s_empty_lo[s]), 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&s_done[s]), 1);
@@ -713,18 +732,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
                 const CUtensorMap* right = piece.width == GM_TILE ? p.b : p.b_half;
                 const uint32_t bytes = 2 * PARTS * (GM_OP + piece.width / 2 * GM_K * 2);
                 for (int kb = 0; kb < kblocks; ++kb) {
-                    if (!(ok = mbar_wait(smem_u32(&s_empty[stage]), phase ^ 1, &s_gave_up, status)))
-                        break;
                     const uint32_t bar = in_block(smem_u32(&s_full[stage]), 0);
-                    if (rank == 0) mbar_expect(smem_u32(&s_full[stage]), bytes);
                     const uint32_t dst = base + stage * STAGE;
                     const int k = kb * GM_K;
+                    // (lo before hi: the order in which they become free)
 #pragma unroll
-                    for (int q = 0; q < PARTS; ++q) {
+                    for (int q = PARTS - 1; q >= 0; --q) {
+                        if (!(ok = mbar_wait(smem_u32(q ? &s_empty_lo[stage] : &s_empty[stage]),
+                                             phase ^ 1, &s_gave_up, status)))
+                            break;
+                        if (q == PARTS - 1) {
+                            if (rank == 0) mbar_expect(smem_u32(&s_full[stage]), bytes);
+                            ++issued;
+                        }
                         tma_box(dst + q * GM_OP, &p.a[q], p.a_mn, at.m, k, at.b, bar);
                         tma_box(dst + (PARTS + q) * GM_OP, right + q, p.b_mn, n0, k, at.b, bar);
                     }
-                    ++issued;
+                    if (!ok) break;
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1;
@@ -743,48 +767,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
             const uint32_t shape = (1u << 4) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16) |
                                    ((GM_TILE / 16) << 24);
             const uint32_t a_step = p.a_mn ? 2048 : 32, b_step = p.b_mn ? 2048 : 32;
+            const int chunk = EXACT ? GM_HAND : kblocks;
             int stage = 0, slot = 0;
             uint32_t phase = 0, slot_phase = 0;
             bool ok = true;
             for (int t = pair; t < total && ok; t += pairs) {
                 const uint32_t width = t < p.whole ? GM_TILE : GM_TILE / 2;
                 const uint32_t idesc = shape | ((width / 8) << 17);
-                for (int kb = 0; kb < kblocks; ++kb) {
-                    const bool begin = kb % (EXACT ? GM_HAND : kblocks) == 0;
-                    const bool end = kb == kblocks - 1 || (EXACT && kb % GM_HAND == GM_HAND - 1);
-                    if (begin) {
-                        if (!(ok = mbar_wait(smem_u32(&s_free[slot]), slot_phase ^ 1, &s_gave_up,
-                                             status)))
-                            break;
-                    }
-                    if (!(ok = mbar_wait(smem_u32(&s_full[stage]), phase, &s_gave_up, status))) break;
-                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                for (int kb = 0; kb < kblocks && ok; kb += chunk) {
+                    if (!(ok = mbar_wait(smem_u32(&s_free[slot]), slot_phase ^ 1, &s_gave_up, status)))
+                        break;
                     const uint32_t d = tmem + slot * GM_TILE;
-                    const uint32_t a0 = base + stage * STAGE, b0 = a0 + PARTS * GM_OP;
+                    const int n = min(chunk, kblocks - kb);
                     if (EXACT) {
+                        int s = stage;
+                        uint32_t ph = phase;
+                        for (int j = 0; j < n; ++j) {
+                            if (!(ok = mbar_wait(smem_u32(&s_full[s]), ph, &s_gave_up, status))) break;
+                            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                            const uint32_t a0 = base + s * STAGE, b0 = a0 + PARTS * GM_OP;
+#pragma unroll
+                            for (int k = 0; k < GM_K / 16; ++k) {
+                                mma_f16(d, smem_desc(a0 + k * a_step, p.a_mn),
+                                        smem_desc(b0 + GM_OP + k * b_step, p.b_mn), idesc,
+                                        j > 0 || k > 0);
+                                mma_f16(d, smem_desc(a0 + GM_OP + k * a_step, p.a_mn),
+                                        smem_desc(b0 + k * b_step, p.b_mn), idesc, true);
+                            }
+                            mma_commit(smem_u32(&s_empty_lo[s]));
+                            if (++s == STAGES) {
+                                s = 0;
+                                ph ^= 1;
+                            }
+                        }
+                        if (!ok) break;
+                    }
+                    for (int j = 0; j < n; ++j) {
+                        if (!EXACT) {
+                            if (!(ok = mbar_wait(smem_u32(&s_full[stage]), phase, &s_gave_up, status)))
+                                break;
+                            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        }
+                        const uint32_t a0 = base + stage * STAGE, b0 = a0 + PARTS * GM_OP;
 #pragma unroll
                         for (int k = 0; k < GM_K / 16; ++k) {
-                            mma_f16(d, smem_desc(a0 + k * a_step, p.a_mn),
-                                    smem_desc(b0 + GM_OP + k * b_step, p.b_mn), idesc, !begin || k > 0);
-                            mma_f16(d, smem_desc(a0 + GM_OP + k * a_step, p.a_mn),
-                                    smem_desc(b0 + k * b_step, p.b_mn), idesc, true);
+                            const uint64_t ah = smem_desc(a0 + k * a_step, p.a_mn);
+                            const uint64_t bh = smem_desc(b0 + k * b_step, p.b_mn);
+                            if (EXACT && j == 0 && k == 0) mma_f16_lower(d, ah, bh, idesc);
+                            else mma_f16(d, ah, bh, idesc, j > 0 || k > 0);
+                        }
+                        mma_commit(smem_u32(&s_empty[stage]));
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1;
                         }
                     }
-#pragma unroll
-                    for (int k = 0; k < GM_K / 16; ++k)
-                        mma_f16(d, smem_desc(a0 + k * a_step, p.a_mn),
-                                smem_desc(b0 + k * b_step, p.b_mn), idesc, EXACT || !begin || k > 0);
-                    mma_commit(smem_u32(&s_empty[stage]));
-                    if (end) {
-                        mma_commit(smem_u32(&s_done[slot]));
-                        if (++slot == 2) {
-                            slot = 0;
-                            slot_phase ^= 1;
-                        }
-                    }
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1;
+                    if (!ok) break;
+                    mma_commit(smem_u32(&s_done[slot]));
+                    if (++slot == 2) {
+                        slot = 0;
+                        slot_phase ^= 1;
                     }
                 }
             }
@@ -819,9 +861,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
             const int64_t row = at.m + quad * 32 + lane;
             float fs, fx;
             lift_factors<MODE>(p, at.b, &fs, &fx);
-            // (a hand-over: 4 adds, 8 of the small products at half the sum, 4 adds)
-            const float low =
-                EXACT && MODE <= MU_SQUARE ? MU_LOW * (kblocks == 1 ? 4.0f : 16.0f) : 0.0f;
+            const float low = EXACT && MODE <= MU_SQUARE
+                                  ? MU_LOW * (GM_K / 16) * (float)min(kblocks, GM_HAND)
+                                  : 0.0f;
             const float alpha = p.alpha * fs * (1.0f + low), beta = p.beta * fx;
             const int64_t o = at.b * p.stride + row * p.ld + at.n + col;
             const bool mirror = !piece.diagonal;
@@ -915,7 +957,7 @@ __device__ __forceinline__ void epilogue4(const GemmParams& p, const TileAt& at,
     for (int j = 0; j < 4; ++j)
         v[j] = MODE == MU_GRAM
                    ? alpha * v[j]
-                   : fmaf(alpha, v[j], beta * (__half2float(hh[j]) + __half2float(ll[j])));
+                   : fmaf(alpha, v[j], beta * of_pair(__half2float(hh[j]), __half2float(ll[j])));
     if (row >= p.M || c0 >= p.N) return;
     if (MODE == MU_LAST) return;
     const int64_t o = at.b * p.stride + row * p.ld + c0;
@@ -1108,8 +1150,9 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
                 if (a < BIG && a >= n) continue;
                 float w[32];
                 tmem_ld32(src + a * SP_TILE, reinterpret_cast<uint32_t*>(w));
+                const float by = a < BIG ? 1.0f : 1.0f / MU_LO;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] += w[j];
+                for (int j = 0; j < 32; ++j) v[j] = fmaf(by, w[j], v[j]);
             }
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = fmaf(low, v[j], v[j]);
@@ -1414,15 +1457,15 @@ __global__ void __launch_bounds__(TN_THREADS, 1) muon_tiny_kernel(const __grid_c
                     float y[8];
                     if (mode == MU_GRAM) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = alpha * (v[u * 8 + e] + w[u * 8 + e]);
+                        for (int e = 0; e < 8; ++e) y[e] = alpha * of_pair(v[u * 8 + e], w[u * 8 + e]);
                     } else {
                         const uint4 h = *ph, l = *pl;
                         const __half* hh = reinterpret_cast<const __half*>(&h);
                         const __half* ll = reinterpret_cast<const __half*>(&l);
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            y[e] = fmaf(alpha, v[u * 8 + e] + w[u * 8 + e],
-                                        beta * (__half2float(hh[e]) + __half2float(ll[e])));
+                            y[e] = fmaf(alpha, of_pair(v[u * 8 + e], w[u * 8 + e]),
+                                        beta * of_pair(__half2float(hh[e]), __half2float(ll[e])));
                     }
                     if (last || exchange) {
                         // fp32 in place: a 16-byte unit of hi and of lo are 8 values

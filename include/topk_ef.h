@@ -395,7 +395,8 @@ size_t muon_workspace_bytes(int32_t B, int64_t rows, int64_t cols,
  *     out      = round(scale * X)
  * (a tall matrix is treated as its transpose.)  Sums are fp32 or wider.  With
  * fp32 output every product keeps 22 bits of its operands and the result is
- * about as exact as one in plain fp32; with 16-bit output and a short side above
+ * about as exact as one in plain fp32, in rows and columns of 1e-6 of the
+ * largest ones too (below that they lose bits: 1e-4 off at 1e-8); with 16-bit output and a short side above
  * 128 the products' operands are rounded to 11 bits, which leaves an error
  * near that of the output's own rounding (relative to the matrix's norm;
  * larger where many entries are equal).  fp32 output may be part of the flat

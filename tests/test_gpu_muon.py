@@ -248,3 +248,41 @@ def test_two_streams_at_once():
 def test_binding_refuses(bad):
     with pytest.raises((ValueError, ef.TopkEfError)):
         bad(torch.zeros(4, 6, device="cuda"))
+
+
+def _pair(t, s):
+    """What a pair of fp16 values (hi, and the rest times 2^11) holds of t."""
+    y = t.double() * s
+    hi = y.to(torch.float16).double()
+    lo = ((y - hi) * 2048).to(torch.float16).double() / 2048
+    return ((hi + lo) / s).to(t.dtype)
+
+
+def _worst(x, y, dim):
+    """The largest relative error of a row (dim 1) or column (dim 0)."""
+    n = torch.linalg.norm(y.double(), dim=dim)
+    return float((torch.linalg.norm(x.double() - y.double(), dim=dim) / n).max())
+
+
+@pytest.mark.parametrize("kind", ["one large row", "graded rows", "graded columns"])
+@pytest.mark.parametrize("m,n", [(64, 64), (100, 1500), (300, 1500), (1500, 300), (1100, 1280),
+                                 (2100, 2304), (2304, 2100)])
+def test_rows_of_different_size(kind, m, n):
+    """fp32 output, row by row and column by column: small rows keep their bits.
+    Allowed: four times the error of plain fp32 products, twice that of a 64-bit
+    model in which X, A and B are held as pairs, and 2^-22 for the operands of
+    the last product."""
+    x = _make((1, m, n), "plain", m + n)[0]
+    if kind == "one large row":
+        x[1:] *= 1e-5
+    elif kind == "graded rows":
+        x *= torch.logspace(0, -6, m, device="cuda")[:, None]
+    else:
+        x *= torch.logspace(0, -6, n, device="cuda")
+    want = _iterate(x, [COEF] * 5, 1e-7, torch.float64)
+    plain = _iterate(x, [COEF] * 5, 1e-7, torch.float32)
+    model = _iterate(x, [COEF] * 5, 1e-7, torch.float64, _pair)
+    out = ef.muon_update(x)
+    for dim in (0, 1):
+        tol = 4 * _worst(plain, want, dim) + 2 * _worst(model, want, dim) + 2.0**-22
+        assert _worst(out, want, dim) <= tol
