@@ -651,9 +651,11 @@ def muon_update(grad, momentum=None, mu=0.95, nesterov=True, coefficients=MUON_C
     [B, rows, cols]: momentum = mu momentum + grad (in place, contiguous
     float32; None: u = grad), u = grad + mu momentum (nesterov) or momentum,
     X = u / (||u||_F + eps), `steps` times X <- a X + (b A + c A A) X with
-    A = X X^T, out = scale X.  out: float32 (default; about as exact as plain
-    float32 products) or a 16-bit type (operands of the products rounded to
-    11 bits); may be grad itself."""
+    A = X X^T, out = scale X.  out: float32 (default) or float16, about as
+    exact as plain float32 products, rounded once; or bfloat16, where the
+    products read 11 bits of their operands if both sides are above 128 (2e-3
+    to 4e-3 of the norm off; the rounding alone is 1.65e-3); may be grad
+    itself."""
     gt, ldg, sg, (B, rows, cols) = _matrices(grad, "grad")
     dev = grad.device
     coef, steps = _coefficients(coefficients, steps)

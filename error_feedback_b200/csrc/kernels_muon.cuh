@@ -13,9 +13,9 @@
 // power of two that keeps typical entries near 1; A and B likewise times MU_SA.  A step
 // multiplies small singular values by a (3.4 five times in a row), so a
 // rounding of X itself would be amplified 485 times: the term a X is taken
-// from hi + lo.  For 16-bit outputs the products read hi alone (11 bits; bf16
+// from hi + lo.  For bf16 outputs the products read hi alone (11 bits; bf16
 // operands would leave an error six times a bf16 output's own rounding); for
-// fp32 outputs each product is hi hi + (hi lo + lo hi) / MU_LO.  All sums are fp32.
+// fp32 and fp16 outputs each product is hi hi + (hi lo + lo hi) / MU_LO.  All sums are fp32.
 // lo is held times MU_LO because fp16's range ends 2^-24 below the typical entry:
 // a row of 1e-5 of the others would keep 7 bits of its 22, and be 3e-4 off in the
 // result, one of 1e-6 4e-3 (plain fp32: 2e-6; so held 2e-6, and 1e-4 at 1e-8).
@@ -39,7 +39,7 @@ constexpr int MU_MAX_LIFT = 60;             // (see muon_scale_kernel)
 // The tensor core truncates where it adds 16 products to an fp32 accumulator: a
 // sum of squares of n such adds comes out low, by 5.4e-8 n of its value on
 // average (measured for n = 2 .. 60: 4.9e-8 n to 7.0e-8 n, with a spread of 5e-8
-// in all; 2^-24 = 6.0e-8).  With fp32 output accumulators are kept short, and
+// in all; 2^-24 = 6.0e-8).  With 22 bits accumulators are kept short, and
 // what is left is multiplied back in the gram and the square, whose diagonals are
 // sums of squares.  The update's terms have both signs: there the factor makes
 // it worse.  A 100 x 200 matrix is 2.5e-6 off without, 1.5e-6 with it (plain
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(MN_THREADS, 3) muon_scale_kernel(const MuonPre
 constexpr int GM_EPI_WARPS = 8;
 constexpr int GM_THREADS = 128 + 32 * GM_EPI_WARPS;    // load, product, 2 idle, epilogue
 constexpr int GM_TILE = 256, GM_ROWS = 128, GM_K = 64;
-constexpr int GM_HAND = 2;                             // fp32 output: stages of one hand-over
+constexpr int GM_HAND = 2;                             // 22 bits: stages of one hand-over
 constexpr int GM_BOX = 64 * 64 * 2;                    // bytes of one 64 x 64 fp16 box
 constexpr int GM_OP = GM_ROWS * GM_K * 2;              // one operand of one block and stage
 constexpr int GM_RING = 6 * 2 * GM_OP;                 // 196,608 bytes of stages
@@ -656,7 +656,7 @@ __device__ __forceinline__ void epilogue32(const GemmParams& p, const TileAt& at
 // update of 4,096 x 4,096 in 59, 60 and 112 us (1.15 to 1.2 PFLOP/s, symmetric
 // products by half), of 25,088 x 4,096 the update in 675 us (1.25 PFLOP/s).
 //
-// With fp32 output (see MU_LOW) the accumulator is handed over after every 128 of K
+// With 22 bits (see MU_LOW) the accumulator is handed over after every 128 of K
 // and added up in registers with rounding to nearest: first the small products (hi
 // lo, lo hi) of both stages, which the first of the large ones divides by MU_LO.
 // The lo parts of a stage are free, and loaded again, before its hi parts.  (A
@@ -714,7 +714,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
     pdl_launch();
     pdl_wait();
 
-    // With fp32 output: 384 threads start with 168 registers each; the 128
+    // With 22 bits: 384 threads start with 168 registers each; the 128
     // running sums of an epilogue thread need more: 72 + 216 + 216 = 3 x 168.
     const int group = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x / 128, 0);
     if (group == 0) {
@@ -934,10 +934,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
 // products, 2 to 3 in the exchange (64 KB into each SM) and 1 to 3 in the epilogue.
 constexpr int SP_THREADS = 256;
 constexpr int SP_TILE = 128;
-constexpr int SP_MIN_STAGES = 3, SP_MAX_STAGES = 6;    // 16-bit output: 3 leave room for two
+constexpr int SP_MIN_STAGES = 3, SP_MAX_STAGES = 6;    // 11 bits: 3 leave room for two
                                                        // blocks an SM, 6 cover the latency of one
 constexpr int SP_LD = SP_TILE + 4;                     // row of sums, in floats
-constexpr int SP_MAX_SUM = 48;     // fp32 output: 64s of K of one block, at most (64 truncated adds)
+constexpr int SP_MAX_SUM = 48;     // 22 bits: 64s of K of one block, at most (64 truncated adds)
 constexpr int SP_SUMS = SP_TILE * SP_LD * 4;           // bytes of the sums, then the turned tile
 constexpr int sp_smem(bool exact, int stages) {
     const int ring = stages * (exact ? 4 : 2) * GM_OP;
@@ -1019,7 +1019,7 @@ __device__ __forceinline__ void add_blocks(float* sums, int rank) {
     }
 }
 
-// fp32 output: the large products of successive 64 of K go to three
+// 22 bits: the large products of successive 64 of K go to three
 // accumulators in turn and the small ones to a fourth, which keeps the
 // truncated sums short (see muon_gemm_kernel).
 template <bool EXACT, int MODE>
@@ -1247,11 +1247,12 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
 // A matrix whose short side is at most 128 and whose long side at most 4,096: a
 // cluster of up to 16 blocks does the whole call, each with up to 256 columns of X
 // (the short side as rows), with X, A and B in shared memory, the sums in TMEM and
-// fp32 output's three products throughout (they cost nothing here: each product
+// the three products of 22 bits throughout (they cost nothing here: each product
 // waits for the one before).  Only the gram needs the other blocks: each adds up
-// its part of the rows over all of them, in block order, and hands them out.  X is held with the short side as rows: chunks of 64 columns, 128
-// rows of 128 swizzled bytes each, which the gram reads as K-major and the update
-// as N-major operand.  Bound by latency, and with a wide short side by the exchange
+// its part of the rows over all of them, in block order, and hands them out.  X is
+// held with the short side as rows: chunks of 64 columns, 128 rows of 128 swizzled
+// bytes each, which the gram reads as K-major and the update as N-major operand.
+// Bound by latency, and with a wide short side by the exchange
 // (64 KB into each block, and out of it): five steps of 64 x 27 take 31 us against
 // 107 in 17 launches, 64 x 600 54 against 123, two of 2,000 x 128 104 against 150.
 // What lies outside the matrix is zero and stays zero.

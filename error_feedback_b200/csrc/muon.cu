@@ -67,12 +67,13 @@ MuLayout muon_layout(int32_t B, int64_t m, int64_t n, bool exact) {
     return L;
 }
 
-// Three products for 22 bits, or one for 11.  Also where the short side fits one
-// tile: there are too few terms for the 11-bit roundings to average out (70 x 6,000
-// in bf16: 2.9e-3 off, against the 1.65e-3 of the output's own rounding), and the
+// Three products for 22 bits, or one for 11, which only bf16 output has: 300 x 300
+// comes out 1.64e-3 off before the output's rounding, which is 1.65e-3 for bf16 but
+// 2.1e-4 for fp16.  Not where the short side fits one tile: there are too few terms
+// for the roundings to average out (70 x 6,000 in bf16: 2.9e-3 off in all), and the
 // products wait for one another more than for the tensor cores.
 bool muon_exact(int64_t m, int64_t n, int32_t out_type) {
-    return out_type == TOPK_EF_F32 || std::min(m, n) <= SP_TILE;
+    return out_type != TOPK_EF_BF16 || std::min(m, n) <= SP_TILE;
 }
 
 bool muon_sizes_ok(int32_t B, int64_t m, int64_t n) {

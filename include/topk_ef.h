@@ -394,13 +394,17 @@ size_t muon_workspace_bytes(int32_t B, int64_t rows, int64_t cols,
  *         A = X X^T;   X = a X + (b A + c A A) X
  *     out      = round(scale * X)
  * (a tall matrix is treated as its transpose.)  Sums are fp32 or wider.  With
- * fp32 output every product keeps 22 bits of its operands and the result is
- * about as exact as one in plain fp32, in rows and columns of 1e-6 of the
- * largest ones too (below that they lose bits: 1e-4 off at 1e-8); with 16-bit output and a short side above
- * 128 the products' operands are rounded to 11 bits, which leaves an error
- * near that of the output's own rounding (relative to the matrix's norm;
- * larger where many entries are equal).  fp32 output may be part of the flat
- * buffer that topk_ef_compress and topk_ef_compress_batched read.
+ * fp32 and fp16 output every product keeps 22 bits of its operands, and the
+ * result is about as exact as one in plain fp32 before its one rounding to the
+ * output type, in rows and columns of 1e-6 of the largest ones too (below that
+ * they lose bits: 1e-4 off at 1e-8).  With bf16 output and a short side above 128
+ * the products' operands are rounded to 11 bits.  That leaves the result 1.8e-3
+ * to 2.4e-3 of its norm off for dense matrices and up to 4e-3 for sparse ones,
+ * ones of equal entries and ones with one large row (the rounding to bf16 alone:
+ * 1.65e-3), and single rows of sparse ones up to 1.5e-2 (rounding: 4e-3).  Ask
+ * for fp32 output and round it where that is too much: three times the products'
+ * time.  fp32 output may be part of the flat buffer that topk_ef_compress and
+ * topk_ef_compress_batched read.
  *   grad       device, [B][rows][cols] of grad_type; rows ld_grad apart,
  *              matrices stride_grad apart
  *   momentum   device, fp32[B][rows][cols] contiguous, updated in place; or

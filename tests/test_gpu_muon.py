@@ -286,3 +286,15 @@ def test_rows_of_different_size(kind, m, n):
     for dim in (0, 1):
         tol = 4 * _worst(plain, want, dim) + 2 * _worst(model, want, dim) + 2.0**-22
         assert _worst(out, want, dim) <= tol
+
+
+@pytest.mark.parametrize("kind", ["plain", "strong", "ones"])
+@pytest.mark.parametrize("m,n", [(300, 300), (512, 700), (1500, 200), (1100, 1300)])
+def test_fp16_output_is_rounded_once(kind, m, n):
+    """Off by half a step of fp16 (and half its smallest subnormal), besides what
+    fp32 output may be off by."""
+    x = _make((1, m, n), kind, m + n)[0]
+    want, tol = _tolerance(x, [COEF] * 5, 1e-7, torch.float32)
+    out = ef.muon_update(x, out_dtype=torch.float16)
+    small = 2.0**-25 * math.sqrt(m * n) / float(torch.linalg.norm(want))
+    assert _rel(out, want) <= tol + torch.finfo(torch.float16).eps / 2 + small
