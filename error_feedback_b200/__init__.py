@@ -169,6 +169,8 @@ def _workspace(nbytes: int, device, ws):
     if ws is not None:
         if ws.numel() * ws.element_size() < nbytes:
             raise ValueError("workspace too small")
+        if not ws.is_contiguous():
+            raise ValueError("the workspace must be contiguous")
         return ws
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
@@ -457,6 +459,8 @@ def _on(device, stream, call):
 def _on_device(ws, device):
     if ws is not None and ws.get_device() != device.index:
         raise ValueError(f"ws is on {ws.device}, not on {device}")
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")       # (else it may hold less than its nbytes)
 
 
 _LOOKUP_WS = 512                        # at least embedding_lookup_workspace_bytes()

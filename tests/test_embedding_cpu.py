@@ -79,3 +79,13 @@ def test_binding_rejects_cpu_tensors(lib):
         ef.embedding_grad(torch.zeros(3, 8), ids, 4)
     with pytest.raises(ValueError):
         ef.embedding_grad_rows(torch.zeros(3, 8), ids, 4)
+
+
+def test_binding_rejects_workspaces_that_are_not_contiguous():
+    """An expanded tensor reports more bytes than it holds."""
+    from types import SimpleNamespace
+    ws = torch.empty(1, dtype=torch.uint8).expand(1 << 20)
+    with pytest.raises(ValueError, match="contiguous"):
+        ef._workspace(1024, ws.device, ws)
+    with pytest.raises(ValueError, match="contiguous"):
+        ef._on_device(ws, SimpleNamespace(index=ws.get_device()))
