@@ -332,9 +332,6 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
 
     MuDevice dev;
     if ((e = muon_device(&dev)) != cudaSuccess) return cuda_fail(e);
-    const int pairs = dev.pairs;
-    EncodeFn fn = encode_fn(&e);
-    if (!fn) return cuda_fail(e);
     MuonPreParams pp = {};
     pp.grad = grad;
     pp.momentum = momentum;
@@ -387,6 +384,9 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
         trace_after(st);
         return e == cudaSuccess ? TOPK_EF_OK : cuda_fail(e);
     }
+    EncodeFn fn = encode_fn(&e);
+    if (!fn) return cuda_fail(e);
+    const int pairs = dev.pairs;
     const int32_t P = (int32_t)L.p, Q = (int32_t)std::max(rows, cols);
     // operand maps, made once for each use: gram, square and update of both X
     struct Maps {
