@@ -36,6 +36,9 @@ cudaError_t with_type(int32_t t, F f) {
 // Records the error for topk_ef_last_cuda_error; returns TOPK_EF_ERR_CUDA.
 int cuda_fail(cudaError_t e);
 
+// What topk_ef_set_test_flags has set.
+int test_flags();
+
 // Bracket a kernel launch for the tracing calls.
 void trace_before(cudaStream_t st, const char* name);
 void trace_after(cudaStream_t st);

@@ -294,6 +294,7 @@ struct GemmParams {
     void* out;                     // last update: the user's matrix
     int64_t ld_out, stride_out;
     int32_t out_align;             // its rows start on 16, 4 or 2-byte boundaries
+    int32_t stall;                 // test hook: the products wait for what never comes
     Ctrl* ctrl;
 };
 
@@ -410,6 +411,12 @@ __device__ __forceinline__ void mma_f16_lower(uint32_t tmem, uint64_t a, uint64_
 __device__ __forceinline__ void mma_commit1(uint32_t bar) {
     asm volatile(
         "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+}
+// ... of both blocks, from the pair's first one.
+__device__ __forceinline__ void mma_commit_here(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
         : "memory");
 }
 // Arrives on the barrier at this place in both blocks once the products so far are done.
@@ -770,7 +777,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
             const int chunk = EXACT ? GM_HAND : kblocks;
             int stage = 0, slot = 0;
             uint32_t phase = 0, slot_phase = 0;
-            bool ok = true;
+            bool ok = !p.stall || mbar_wait(smem_u32(&s_done[0]), 0, &s_gave_up, status);
             for (int t = pair; t < total && ok; t += pairs) {
                 const uint32_t width = t < p.whole ? GM_TILE : GM_TILE / 2;
                 const uint32_t idesc = shape | ((width / 8) << 17);
@@ -915,7 +922,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
     // their accumulators are freed
     if (s_gave_up && threadIdx.x == 32 && rank == 0) {
         volatile int never = 0;
-        mma_commit(smem_u32(&s_drain));
+        mma_commit_here(smem_u32(&s_drain));
         mbar_wait(smem_u32(&s_drain), 0, &never, status);
     }
     __syncthreads();
@@ -1102,7 +1109,8 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
         const uint32_t a_step = p.a_mn ? 2048 : 32, b_step = p.b_mn ? 2048 : 32;
         int s = 0;
         uint32_t phase = 0;
-        for (int i = 0; i < n; ++i) {
+        const bool stalled = p.stall && !mbar_wait(smem_u32(&s_done), 0, &s_gave_up, status);
+        for (int i = 0; i < n && !stalled; ++i) {
             if (!mbar_wait(smem_u32(&s_full[s]), phase, &s_gave_up, status)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t a0 = base + s * STAGE, b0 = a0 + PARTS * GM_OP;
@@ -1271,6 +1279,7 @@ struct TinyParams {
     float coef[3 * TN_MAX_STEPS];
     int8_t drop[TN_MAX_STEPS + 1]; // (saturated)
     int32_t steps, out_type;
+    int32_t stall;                 // test hook: as in GemmParams
     float scale;
     void* out;
     int64_t ld_out, stride_out;
@@ -1289,7 +1298,7 @@ __device__ __forceinline__ uint32_t tn_f32(int r, int c) {
 template <typename TG>
 __global__ void __launch_bounds__(TN_THREADS, 1) muon_tiny_kernel(const __grid_constant__ TinyParams p) {
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t s_done;
+    __shared__ __align__(8) uint64_t s_done, s_drain;
     __shared__ double s_red[33], s_norm;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_gave_up;
@@ -1300,6 +1309,7 @@ __global__ void __launch_bounds__(TN_THREADS, 1) muon_tiny_kernel(const __grid_c
     if (tid == 0) {
         s_gave_up = 0;
         mbar_init(smem_u32(&s_done), 1);
+        mbar_init(smem_u32(&s_drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -1398,7 +1408,7 @@ __global__ void __launch_bounds__(TN_THREADS, 1) muon_tiny_kernel(const __grid_c
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncthreads();
-        if (tid == 0) {
+        if (tid == 0 && !s_gave_up && !p.stall) {
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const int N = ((update ? Q : P) + 15) / 16 * 16, K = mode == MU_GRAM ? Q : P;
             const uint32_t idesc = (1u << 4) | ((uint32_t)update << 16) | ((uint32_t)(N / 8) << 17) |
@@ -1418,8 +1428,9 @@ __global__ void __launch_bounds__(TN_THREADS, 1) muon_tiny_kernel(const __grid_c
             }
             mma_commit1(smem_u32(&s_done));
         }
-        // (once a wait has given up the next ones do so at once; the block goes on, since
-        // the others of its cluster wait for it and read its memory)
+        // (once a wait has given up there are no more products and the next waits give up
+        // at once; the block goes on, since the others of its cluster wait for it and read
+        // its memory)
         const bool done = mbar_wait(smem_u32(&s_done), parity, &s_gave_up, status);
         ok = __syncthreads_and(done) && ok;
         parity ^= 1;
@@ -1547,7 +1558,13 @@ __global__ void __launch_bounds__(TN_THREADS, 1) muon_tiny_kernel(const __grid_c
             else if (p.out_type == 1) static_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(y);
             else static_cast<__half*>(p.out)[to] = __float2half_rn(y);
         }
+    } else if (tid == 0) {
+        // products may still be running: let them end before their accumulators are freed
+        volatile int never = 0;
+        mma_commit1(smem_u32(&s_drain));
+        mbar_wait(smem_u32(&s_drain), 0, &never, status);
     }
+    __syncthreads();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }

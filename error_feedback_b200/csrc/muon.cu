@@ -332,6 +332,7 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
 
     MuDevice dev;
     if ((e = muon_device(&dev)) != cudaSuccess) return cuda_fail(e);
+    const int32_t stall = (test_flags() & 4) != 0;
     MuonPreParams pp = {};
     pp.grad = grad;
     pp.momentum = momentum;
@@ -372,6 +373,7 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
         for (int i = 0; i <= steps; ++i) tp.drop[i] = (int8_t)std::min(drop[i], 127);
         tp.steps = steps;
         tp.out_type = out_type;
+        tp.stall = stall;
         tp.scale = scale;
         tp.out = out;
         tp.ld_out = ld_out;
@@ -435,6 +437,7 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
         }
         g.batch = B;
         g.ctrl = pp.ctrl;
+        g.stall = stall;
         g.lift = pp.lift;
         auto cut = [&](int size) {
             g.tiles_m = (int32_t)ceil_div64(g.M, size);

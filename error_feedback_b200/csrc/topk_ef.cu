@@ -57,6 +57,8 @@ int tke::cuda_fail(cudaError_t e) {
     return TOPK_EF_ERR_CUDA;
 }
 
+int tke::test_flags() { return g_test_flags.load(); }
+
 namespace {
 
 // ------------------------------------------------------------------ tracing

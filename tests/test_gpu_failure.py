@@ -41,3 +41,23 @@ def test_bounded_wait_runs_out_then_next_call_is_exact(n, k):
     paths = []
     run_compress_steps(grads, LR, k, ws=ws, paths=paths, zero_between=True)
     assert paths[-1]["fallback"] == 0, paths
+
+
+@pytest.mark.parametrize("m,n,out", [(40, 60, "float32"), (100, 700, "float32"),      # one block, a cluster
+                                     (200, 300, "bfloat16"), (200, 300, "float32"),   # tiles by clusters
+                                     (1100, 1280, "bfloat16"), (1664, 1600, "float32")])   # pairs
+def test_muon_wait_runs_out_then_next_call_is_right(m, n, out):
+    """The products wait for a completion that nothing signals: every kernel of
+    the call gives up by itself, and the next call on the workspace is right."""
+    out = getattr(torch, out)
+    g = torch.randn(m, n, device="cuda")
+    want = ef.muon_update(g, steps=1, out_dtype=out)
+    ws = torch.empty(ef.muon_workspace_bytes(1, m, n, out), dtype=torch.uint8, device="cuda")
+    old = ef.topk_ef_set_test_flags(4)
+    try:
+        ef.muon_update(g, steps=1, out_dtype=out, ws=ws)
+        assert ef.topk_ef_last_device_status(ws) == ef.ERR_DEVICE_TIMEOUT
+    finally:
+        ef.topk_ef_set_test_flags(old)
+    assert torch.equal(ef.muon_update(g, steps=1, out_dtype=out, ws=ws), want)
+    assert ef.topk_ef_last_device_status(ws) == ef.OK
