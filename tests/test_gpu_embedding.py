@@ -347,3 +347,11 @@ def test_binding_refuses(bad):
     w, ids = torch.zeros(10, 8, device="cuda"), torch.zeros(5, dtype=torch.int64, device="cuda")
     with pytest.raises((ValueError, ef.TopkEfError)):
         bad(w, ids, torch.zeros(5, 8, device="cuda"))
+
+
+@pytest.mark.parametrize("T", [600, 5000, 20000])
+@pytest.mark.parametrize("dt,ot,ldo", [("bf16", "f32", 1504), ("f32", "bf16", 1501)])
+def test_grad_accumulates_over_several_slabs(T, dt, ot, ldo):
+    """Added to what is there, by each way to sort, with rows of more columns than
+    one block takes."""
+    _run_grad(dt, ot, T, 3000, 1500, "zipf", ldo=ldo, acc=True)

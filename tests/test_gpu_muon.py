@@ -298,3 +298,118 @@ def test_fp16_output_is_rounded_once(kind, m, n):
     out = ef.muon_update(x, out_dtype=torch.float16)
     small = 2.0**-25 * math.sqrt(m * n) / float(torch.linalg.norm(want))
     assert _rel(out, want) <= tol + torch.finfo(torch.float16).eps / 2 + small
+
+
+# Shapes by the kernels that take them: pairs' 256 x 256 tiles, whole and halved, in
+# one and in several rounds; one tile with a long K; tiles of 64 columns.
+LARGE = [(1, 2300, 2600), (1, 2600, 2300), (1, 3000, 3100), (3, 1100, 1200), (2, 1664, 1600)]
+LONG = [(1, 128, 24640), (1, 28672, 100), (1, 1, 30000), (1, 300, 30000)]
+NARROW = [(1, 64, 5000), (2, 5000, 50), (1, 32, 6001)]
+
+
+@pytest.mark.parametrize("shape", LARGE + LONG + NARROW)
+@pytest.mark.parametrize("gt,ot", [("f32", "f32"), ("bf16", "bf16"), ("f32", "f16")])
+def test_shapes_by_kernel(shape, gt, ot):
+    x = _make(shape, "strong", sum(shape)).to(TYPES[gt])
+    ws = torch.full((ef.muon_workspace_bytes(*shape, TYPES[ot]),), 0x7F, dtype=torch.uint8, device="cuda")
+    out = ef.muon_update(x, out_dtype=TYPES[ot], ws=ws)
+    assert ef.topk_ef_last_device_status(ws) == 0
+    for b in range(shape[0]):
+        want, tol = _tolerance(x[b], [COEF] * 5, 1e-7, TYPES[ot])
+        assert _rel(out[b], want) <= tol
+    assert torch.equal(out, ef.muon_update(x, out_dtype=TYPES[ot]))
+
+
+@pytest.mark.parametrize("nesterov", [False, True])
+@pytest.mark.parametrize("gt", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 200, 320), (2, 320, 192), (2, 1100, 1280), (1, 100, 4224)])
+def test_momentum_of_whole_rows_of_64(nesterov, gt, shape):
+    """Contiguous matrices whose rows are multiples of 64 take a path of their own."""
+    mom = _make(shape, "strong", 1)
+    mu = float(torch.tensor(0.9, dtype=torch.float32))
+    for step in range(2):
+        g = _make(shape, "strong", 2 + step).to(TYPES[gt])
+        want_m = (mom.double() * mu + g.double()).float()
+        out = ef.muon_update(g, momentum=mom, mu=0.9, nesterov=nesterov)
+        assert torch.equal(mom, want_m)
+        u = (mom.double() * mu + g.double()).float() if nesterov else mom
+        for b in range(shape[0]):
+            want, tol = _tolerance(u[b], [COEF] * 5, 1e-7, torch.float32)
+            assert _rel(out[b], want) <= tol
+
+
+@pytest.mark.parametrize("steps", [1, 2, 9])
+@pytest.mark.parametrize("m,n,ot", [(200, 300, "f32"), (300, 200, "bf16"), (1100, 1280, "bf16"),
+                                    (1280, 1100, "bf16"), (1664, 1600, "f32")])
+def test_steps_and_coefficients_by_kernel(steps, m, n, ot):
+    x = _make((1, m, n), "strong", 8)
+    each = [(1.5, -0.5, 0.0), (2.0, -1.5, 0.5), (15 / 8, -10 / 8, 3 / 8)]
+    coefs = [each[i % 3] for i in range(steps)]
+    out = ef.muon_update(x, coefficients=coefs, steps=steps, out_dtype=TYPES[ot])
+    want, tol = _tolerance(x[0], [tuple(float(torch.tensor(v)) for v in c) for c in coefs], 1e-7, TYPES[ot])
+    assert _rel(out[0], want) <= tol
+
+
+@pytest.mark.parametrize("m,n,ot", [(100, 90, "f32"), (200, 300, "f32"), (300, 200, "bf16"), (128, 4200, "f32"),
+                                    (320, 192, "f32"), (1100, 1280, "bf16"), (1664, 1600, "f32")])
+def test_zero_tiny_huge_nan_by_kernel(m, n, ot):
+    """As test_zero_tiny_huge_nan, with a matrix whose norm is near fp32's end.  The
+    tiny one's products vanish beside a X: five steps that each round a pair
+    (2^-22) and an fp32 product and sum (2^-23), and the scaling at both ends."""
+    x = _make((7, m, n), "strong", 3)
+    x[0] = 0
+    x[1] *= 1e-20
+    x[2] *= 1e25
+    x[3, 5, 7] = float("nan")
+    x[4, 5, 7] = float("inf")
+    x[6] = x[6] / x[6].abs().max() * 1e38
+    out = ef.muon_update(x, out_dtype=TYPES[ot])
+    assert (out[0] == 0).all() and out[3].isnan().all() and out[4].isnan().any()
+    tol = _tolerance(x[5], [COEF] * 5, 1e-7, TYPES[ot])[1]
+    for b in (2, 5, 6):
+        assert _rel(out[b], _iterate(x[b].double(), [COEF] * 5, 1e-7, torch.float64)) <= tol
+    tiny = 5 * (2.0**-22 + 2.0**-23) + 2 * 2.0**-22 + (0 if ot == "f32" else torch.finfo(TYPES[ot]).eps / 2)
+    assert _rel(out[1], _iterate(x[1].double(), [COEF] * 5, 1e-7, torch.float64)) <= tiny
+
+
+@pytest.mark.parametrize("m,n", [(60, 70), (200, 300), (320, 192)])
+def test_norm_near_the_smallest_values(m, n):
+    """eps = 0: the factor that brings X to its scale is no fp32 value."""
+    x = _make((1, m, n), "strong", 4)[0] * 1e-34
+    want, tol = _tolerance(x.double(), [COEF] * 5, 0.0, torch.float32)
+    tol = _tolerance(_make((1, m, n), "strong", 4)[0], [COEF] * 5, 0.0, torch.float32)[1]
+    assert _rel(ef.muon_update(x, eps=0.0), want) <= tol
+
+
+@pytest.mark.parametrize("shape,ot", [((1, 200, 300), "f32"), ((1, 1100, 1280), "bf16"), ((1, 1664, 1600), "f32")])
+def test_captured_call_replays_by_kernel(shape, ot):
+    g, mom = _make(shape, "strong", 1), torch.zeros(shape, device="cuda")
+    out = torch.empty(shape, dtype=TYPES[ot], device="cuda")
+    ws = torch.empty(ef.muon_workspace_bytes(*shape, TYPES[ot]), dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        ef.muon_update(g, momentum=mom, out=out, ws=ws)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ef.muon_update(g, momentum=mom, out=out, ws=ws)
+    for k in range(3):
+        g.copy_(_make(shape, "plain", 10 + k))
+        m2 = mom.clone()
+        graph.replay()
+        want = ef.muon_update(g, momentum=m2, out_dtype=TYPES[ot])
+        assert torch.equal(out, want) and torch.equal(mom, m2)
+    assert ef.topk_ef_last_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("shape,ot", [((1, 1100, 1280), "bf16"), ((1, 1664, 1600), "f32"), ((30, 100, 600), "f32")])
+def test_two_streams_at_once_by_kernel(shape, ot):
+    x = [_make(shape, "strong", k) for k in range(2)]
+    want = [ef.muon_update(t, out_dtype=TYPES[ot]) for t in x]
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = [ef.muon_update(t, out_dtype=TYPES[ot], stream=q) for t, q in zip(x, s)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
