@@ -281,6 +281,8 @@ struct GemmParams {
     CUtensorMap a[2], b[2], b_half[2];
     int32_t M, N, K, batch, tiles_m, tiles_n, tiles;   // tiles: of one matrix
     int32_t stages, width;         // clusters: stages of the ring, columns of an update's tile
+    int32_t k_first, k_blocks;     // clusters: the 64s of K of this launch
+    int32_t add;                   // clusters: the gram's sums are added to what dst holds
     int32_t whole;                 // pairs: tiles taken whole, the others in two halves of columns
     int32_t a_mn, b_mn;            // operand's M (N) dimension is the contiguous one
     int32_t n_fast;                // neighbouring tiles differ in N
@@ -944,7 +946,7 @@ constexpr int SP_TILE = 128;
 constexpr int SP_MIN_STAGES = 3, SP_MAX_STAGES = 6;    // 11 bits: 3 leave room for two
                                                        // blocks an SM, 6 cover the latency of one
 constexpr int SP_LD = SP_TILE + 4;                     // row of sums, in floats
-constexpr int SP_MAX_SUM = 48;     // 22 bits: 64s of K of one block, at most (64 truncated adds)
+constexpr int SP_MAX_SUM = 48;     // 22 bits: 64s of K of one block and launch (64 truncated adds)
 constexpr int SP_SUMS = SP_TILE * SP_LD * 4;           // bytes of the sums, then the turned tile
 constexpr int sp_smem(bool exact, int stages) {
     const int ring = stages * (exact ? 4 : 2) * GM_OP;
@@ -952,8 +954,8 @@ constexpr int sp_smem(bool exact, int stages) {
     return (ring > after ? ring : after) + 1024;
 }
 
-// Four columns of one row; v: the sums, h and l: the elementwise operand; v
-// becomes the value.  (The last update's values are stored by store_rows.)
+// Four columns of one row; v: the sums, h and l: the elementwise operand (of a gram:
+// the sums of the K before); v becomes the value.  (The last update's values are stored by store_rows.)
 template <bool EXACT, int MODE>
 __device__ __forceinline__ void epilogue4(const GemmParams& p, const TileAt& at, float alpha,
                                           float beta, int64_t row, int64_t c0, uint2 h, uint2 l,
@@ -962,9 +964,10 @@ __device__ __forceinline__ void epilogue4(const GemmParams& p, const TileAt& at,
     const __half* ll = reinterpret_cast<const __half*>(&l);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        v[j] = MODE == MU_GRAM
+        v[j] = MODE == MU_GRAM && !EXACT
                    ? alpha * v[j]
-                   : fmaf(alpha, v[j], beta * of_pair(__half2float(hh[j]), __half2float(ll[j])));
+                   : fmaf(alpha, v[j], (MODE == MU_GRAM ? 1.0f : beta) *
+                                           of_pair(__half2float(hh[j]), __half2float(ll[j])));
     if (row >= p.M || c0 >= p.N) return;
     if (MODE == MU_LAST) return;
     const int64_t o = at.b * p.stride + row * p.ld + c0;
@@ -1071,9 +1074,8 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
     // (an update that leaves SMs idle takes 64 columns at a time)
     const int width = MODE <= MU_SQUARE ? SP_TILE : p.width;
     const TileAt at = tile_at(p, (int)(blockIdx.x / split), SP_TILE, width);
-    const int kblocks = (p.K + GM_K - 1) / GM_K;
-    const int kb0 = (int)((int64_t)kblocks * rank / split);
-    const int n = (int)((int64_t)kblocks * (rank + 1) / split) - kb0;
+    const int before = (int)((int64_t)p.k_blocks * rank / split), kb0 = p.k_first + before;
+    const int n = (int)((int64_t)p.k_blocks * (rank + 1) / split) - before;
     pdl_launch();
     pdl_wait();
 
@@ -1193,10 +1195,12 @@ __global__ void __launch_bounds__(SP_THREADS) muon_split_kernel(const __grid_con
             const int r = r0 + u * step;
             const int64_t row = at.m + rank * rows + r, o = at.b * p.stride + row * p.ld + c0;
             h[u] = l[u] = make_uint2(0, 0);
-            if (MODE != MU_GRAM && r < rows && row < p.M && c0 < p.N) {
-                h[u] = *reinterpret_cast<const uint2*>(p.src[0] + o);
+            if (MODE == MU_GRAM ? EXACT && p.add : true) {
+                if (r >= rows || row >= p.M || c0 >= p.N) continue;
+                const __half* const* src = MODE == MU_GRAM ? p.dst : p.src;
+                h[u] = *reinterpret_cast<const uint2*>(src[0] + o);
                 if (EXACT || MODE >= MU_UPDATE)
-                    l[u] = *reinterpret_cast<const uint2*>(p.src[1] + o);
+                    l[u] = *reinterpret_cast<const uint2*>(src[1] + o);
             }
         }
 #pragma unroll

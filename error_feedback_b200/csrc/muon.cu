@@ -26,11 +26,15 @@ constexpr int32_t MU_MAX_BATCH = 65535;
 constexpr int32_t MU_MAX_STEPS = 64;
 // 256 x 256 tiles of a product from which pairs of SMs take them, rather than
 // clusters 128 x 128 tiles with K divided.  Below, the pairs that are left idle
-// cost more than the clusters' exchange.  Five steps, pairs from 12 or from 25
-// tiles on: 1,536 x 4,096 in bf16 (gram of 21 tiles) 375 or 391 us; with fp32
-// output, pairs from 15 or from 37: 1,024 x 1,024 (update of 16) 281 or 247, 2,048
-// x 2,048 (gram of 36) 579 or 573.
-constexpr int64_t MU_PAIR_TILES_11 = 12, MU_PAIR_TILES_22 = 37;
+// cost more than the clusters' exchange.  Five steps, 11 bits, pairs from 6, 12 or
+// 25 tiles on: 800 x 3,000 (gram of 10 tiles) 247, 202 or 202 us, 768 x 1,024
+// (update of 12) 166, 154 or 157, 1,500 x 1,500 (gram of 21) 241, 241 or 270.  22
+// bits, from 25, 37 or 70: 2,048 x 2,048 (gram of 36) 633, 585 or 638, 1,100 x 2,500
+// (update of 50) 384, 384 or 412, 2,304 x 2,304 (gram of 45) 945, 946 or 1,147.
+// LONG: of 22 bits, where K is too long for one launch of the clusters (see
+// SP_MAX_SUM); from 11 or 20 tiles on: 1,280 x 8,000 (gram of 15) 1,126 or 850 us, from
+// 20 or 22: 1,500 x 4,000 (gram of 21) 806 or 842.
+constexpr int64_t MU_PAIR_TILES_11 = 12, MU_PAIR_TILES_22 = 37, MU_PAIR_TILES_LONG = 20;
 
 struct MuLayout {
     int64_t p, ldx, ldp, stride_x, stride_p, groups, parts;
@@ -452,9 +456,14 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
         int lg = 0;
         while (lg < 3 && tiles * B <= dev.clusters[lg + 1] && kblocks >= 2 << lg) ++lg;
         const int split = 1 << lg;
-        const bool long_sums = exact && kblocks > (int64_t)split * SP_MAX_SUM;
-        cudaError_t r;
-        if (long_sums || cut(GM_TILE) * B >= (exact ? MU_PAIR_TILES_22 : MU_PAIR_TILES_11)) {
+        // launches over parts of K that keep the truncated sums short (128 x 28,672 in two
+        // parts 417 us; the one pair of blocks that its tile would have 2,090)
+        const int64_t parts_k = exact ? ceil_div64(kblocks, (int64_t)split * SP_MAX_SUM) : 1;
+        const int64_t pairs_from = !exact        ? MU_PAIR_TILES_11
+                                   : parts_k > 1 ? MU_PAIR_TILES_LONG
+                                                 : MU_PAIR_TILES_22;
+        cudaError_t r = cudaSuccess;
+        if (cut(GM_TILE) * B >= pairs_from) {
             tiles = cut(GM_TILE);
             g.tiles = (int32_t)tiles;
             // where the last round would leave half of the pairs idle, its tiles are
@@ -467,6 +476,7 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
             r = with_kernel(exact, g.mode, [&](auto pair, auto) {
                 return launch_pdl(pair, grid, GM_THREADS, st, g, GM_SMEM);
             });
+            trace_after(st);
         } else {
             cut(SP_TILE);
             g.width = SP_TILE;
@@ -478,13 +488,19 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
             }
             g.tiles = (int32_t)tiles;
             g.stages = !exact && tiles * B <= dev.clusters[lg] ? SP_MAX_STAGES : SP_MIN_STAGES;
-            trace_before(st, "muon_split_kernel");
-            r = with_kernel(exact, g.mode, [&](auto, auto kernel) {
-                return launch_clusters(kernel, (unsigned)(tiles * B * split), (unsigned)split,
-                                       SP_THREADS, sp_smem(exact, g.stages), st, g);
-            });
+            const int64_t per = ceil_div64(kblocks, parts_k);
+            for (int64_t k = 0; k < kblocks && r == cudaSuccess; k += per) {
+                g.k_first = (int32_t)k;
+                g.k_blocks = (int32_t)std::min(per, kblocks - k);
+                g.add = k > 0;
+                trace_before(st, "muon_split_kernel");
+                r = with_kernel(exact, g.mode, [&](auto, auto kernel) {
+                    return launch_clusters(kernel, (unsigned)(tiles * B * split), (unsigned)split,
+                                           SP_THREADS, sp_smem(exact, g.stages), st, g);
+                });
+                trace_after(st);
+            }
         }
-        trace_after(st);
         return r;
     };
     int cur = 0;

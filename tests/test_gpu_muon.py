@@ -303,7 +303,8 @@ def test_fp16_output_is_rounded_once(kind, m, n):
 # Shapes by the kernels that take them: pairs' 256 x 256 tiles, whole and halved, in
 # one and in several rounds; one tile with a long K; tiles of 64 columns.
 LARGE = [(1, 2300, 2600), (1, 2600, 2300), (1, 3000, 3100), (3, 1100, 1200), (2, 1664, 1600)]
-LONG = [(1, 128, 24640), (1, 28672, 100), (1, 1, 30000), (1, 300, 30000)]
+LONG = [(1, 128, 24640), (1, 28672, 100), (1, 1, 30000), (1, 300, 30000), (1, 1200, 8000), (1, 8000, 1200),
+        (1, 1500, 4000), (2, 60, 60000)]
 NARROW = [(1, 64, 5000), (2, 5000, 50), (1, 32, 6001)]
 
 
