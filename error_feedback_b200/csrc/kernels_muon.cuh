@@ -1412,7 +1412,7 @@ __global__ void __launch_bounds__(TN_THREADS, 1) muon_tiny_kernel(const __grid_c
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncthreads();
-        if (tid == 0 && !s_gave_up && !p.stall) {
+        if (tid == 0 && ok && !p.stall) {
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const int N = ((update ? Q : P) + 15) / 16 * 16, K = mode == MU_GRAM ? Q : P;
             const uint32_t idesc = (1u << 4) | ((uint32_t)update << 16) | ((uint32_t)(N / 8) << 17) |
@@ -1562,13 +1562,15 @@ __global__ void __launch_bounds__(TN_THREADS, 1) muon_tiny_kernel(const __grid_c
             else if (p.out_type == 1) static_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(y);
             else static_cast<__half*>(p.out)[to] = __float2half_rn(y);
         }
-    } else if (tid == 0) {
+    } else {
         // products may still be running: let them end before their accumulators are freed
         volatile int never = 0;
-        mma_commit1(smem_u32(&s_drain));
-        mbar_wait(smem_u32(&s_drain), 0, &never, status);
+        if (tid == 0) {
+            mma_commit1(smem_u32(&s_drain));
+            mbar_wait(smem_u32(&s_drain), 0, &never, status);
+        }
+        __syncthreads();
     }
-    __syncthreads();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
