@@ -475,7 +475,9 @@ def embedding_lookup(weight, ids, scale=1.0, out=None, out_dtype=None, ws=None, 
     rounded once.  weight: [V, D] float32 / bfloat16 / float16 with contiguous
     rows; ids: int32 / int64 of any shape; out: [*ids.shape, D] (or [T, D]) in
     any of the types (default: the weight's).  An id outside [0, V) gives a
-    row of zeros and ERR_BAD_INPUT from topk_ef_last_device_status(ws)."""
+    row of zeros and ERR_BAD_INPUT from topk_ef_last_device_status(ws) (pass a
+    ws to be able to ask).  The call works on the tensors' memory: autograd
+    records nothing, and the gradient is embedding_grad's."""
     wt, ldw = _matrix(weight, "weight")
     dev = weight.device
     idb, T = _token_ids(ids, dev)
@@ -658,8 +660,9 @@ def muon_update(grad, momentum=None, mu=0.95, nesterov=True, coefficients=MUON_C
     A = X X^T, out = scale X.  out: float32 (default) or float16, about as
     exact as plain float32 products, rounded once; or bfloat16, where the
     products read 11 bits of their operands if both sides are above 128 (2e-3
-    to 4e-3 of the norm off; the rounding alone is 1.65e-3); may be grad
-    itself."""
+    to 4e-3 of the norm off, equal entries up to 7e-3; the rounding alone is
+    1.65e-3).  out may be grad itself.  The call works on the tensors' memory:
+    autograd records nothing."""
     gt, ldg, sg, (B, rows, cols) = _matrices(grad, "grad")
     dev = grad.device
     coef, steps = _coefficients(coefficients, steps)

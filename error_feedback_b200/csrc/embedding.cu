@@ -75,7 +75,9 @@ GLayout grad_layout(int64_t T, int64_t V, int64_t D) {
 }
 
 // Units of zeros that a scattering and a counting kernel write besides: about
-// what memory takes in the time that they need anyway.
+// what memory takes in the time that they need anyway.  (None: 30,011 x 1,001 fp32 99
+// us instead of 93, 32,768 x 4,096 into 131,072 rows 390 instead of 383; half as
+// many: 98 and 388; twice as many: 94 and 380.)
 constexpr int64_t ES_SCATTER_UNITS = 1200, ES_COUNT_UNITS = 400;
 
 template <typename TI>

@@ -427,8 +427,10 @@ __global__ void __launch_bounds__(ES_THREADS) sort_scatter_kernel(const SortPara
 // Up to SR_MAX positions are sorted by one kernel: every block counts, for
 // its own keys, the keys that come before them among all (the whole list is
 // read by every block; T^2 comparisons over all SMs; 2,048 positions in 4 us,
-// where the radix sort's four launches take 20).  Blocks after the ranking ones
-// write the zeros of a dense gradient in the meantime.
+// where the radix sort's four launches take 20).  Whole calls by ranking and by
+// radix, row-sparse, 768 columns: 18 and 37 us for 2,048 positions, 23 and 40 for
+// 4,096, 42 and 50 for 8,192, where the list fills a block's static shared memory.
+// Blocks after the ranking ones write the zeros of a dense gradient in the meantime.
 constexpr int SR_THREADS = 512;
 constexpr int SR_MAX = 8192;
 constexpr int SR_SHARE = 16;           // threads of one key
@@ -782,7 +784,11 @@ __global__ void __launch_bounds__(EC_THREADS) grad_combine_kernel(const GradPara
 // reads the whole list; the block of an id's first position sums the id's rows:
 // the warps take contiguous parts of them, and their sums are added in order.
 // One launch of independent blocks instead of three chained ones: 500 positions
-// of 1,024 columns in 6.2 us on the GPU against 15.
+// of 1,024 columns in 6.2 us on the GPU against 15.  Whole calls by one kernel (with
+// room for 1,024 positions) and by three, at 512, 768 and 1,024 positions: added to
+// rows of 1,024 columns 8, 11 and 14 us against 15, 16 and 17, to rows of 4,096 23,
+// 33 and 43 against 17, 18 and 19, row-sparse with 768 columns 12, 18 and 25 against
+// 13, 14 and 14.
 constexpr int DR_THREADS = 128;
 constexpr int DR_WARPS = DR_THREADS / 32;
 constexpr int DR_MAX = 512;

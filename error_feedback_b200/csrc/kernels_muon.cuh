@@ -42,8 +42,8 @@ constexpr int MU_MAX_LIFT = 60;             // (see muon_scale_kernel)
 // in all; 2^-24 = 6.0e-8).  With 22 bits accumulators are kept short, and
 // what is left is multiplied back in the gram and the square, whose diagonals are
 // sums of squares.  The update's terms have both signs: there the factor makes
-// it worse.  A 100 x 200 matrix is 2.5e-6 off without, 1.5e-6 with it (plain
-// fp32: 1.4e-6), one of 2,048 x 8,192 7.3e-6 and 4.5e-6 (3.6e-6).
+// it worse.  A 128 x 24,576 matrix is 8.1e-6 off without, 3.5e-6 with it (plain
+// fp32: 1.4e-6), one of 2,048 x 8,192 1.2e-5 and 7.5e-6 (5.2e-6).
 constexpr float MU_LOW = 5.4e-8f;
 constexpr uint64_t MU_WAIT_NS = 2000000000ull;
 
@@ -660,17 +660,20 @@ __device__ __forceinline__ void epilogue32(const GemmParams& p, const TileAt& at
 // issues the products into one of two TMEM accumulators (2 x 256 columns)
 // while eight warps of each block drain the other.
 //
-// Bound by the tensor cores at the clock that the power cap leaves, and by shared
-// memory, which takes in 32 KB a stage and gives out as much: gram, square and
-// update of 4,096 x 4,096 in 59, 60 and 112 us (1.15 to 1.2 PFLOP/s, symmetric
-// products by half), of 25,088 x 4,096 the update in 675 us (1.25 PFLOP/s).
+// Bound by the tensor cores at the clock that the power cap leaves (the pipe is
+// active 59 to 62% of a launch, 64 to 69% with 22 bits), by the rounds that leave
+// pairs idle and by the last round's epilogue: gram, square and
+// update of 4,096 x 4,096 in 61, 61 and 111 us at 1.6 GHz (1.1 to 1.25 PFLOP/s,
+// symmetric products by half; with 22 bits 167, 172 and 315), of 25,088 x 4,096 in
+// 356, 76 and 674.  (Five steps and the two passes before them: 1.23 ms; 1.34 to 1.5
+// in calls that follow one another, at the 1.3 to 1.4 GHz of the power cap.)
 //
 // With 22 bits (see MU_LOW) the accumulator is handed over after every 128 of K
 // and added up in registers with rounding to nearest: first the small products (hi
 // lo, lo hi) of both stages, which the first of the large ones divides by MU_LO.
 // The lo parts of a stage are free, and loaded again, before its hi parts.  (A
 // hand-over of every 64, which needs no two stages at once, keeps the epilogue's
-// warps busier than the tensor cores: 4,096 x 4,096 3.73 ms by 128, 4.59 by 64.)
+// warps busier than the tensor cores: 4,096 x 4,096 3.87 ms by 128, 4.61 by 64.)
 template <bool EXACT, int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GM_THREADS, 1)
     muon_gemm_kernel(const __grid_constant__ GemmParams p) {

@@ -2,8 +2,9 @@
 // layout, launch sequence.
 //
 //   a small matrix: muon_tiny_kernel alone; else
-//   muon_norm_kernel -> muon_scale_kernel -> steps times: muon_gemm_kernel as
-//   gram, square and update (the last update writes the caller's matrix)
+//   muon_norm_kernel -> muon_scale_kernel -> steps times: gram, square and update
+//   (the last update writes the caller's matrix), each by muon_gemm_kernel (many
+//   tiles) or muon_split_kernel (few; once for every part of a long K)
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -480,7 +481,8 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
         } else {
             cut(SP_TILE);
             g.width = SP_TILE;
-            // (3 x 150 x 700 in bf16: 152 us with tiles of 128 columns, 140 of 64)
+            // (a short side of at most 64, whose products have one 64 of K and so no split:
+            // 64 x 5,000 153 us with tiles of 128 columns, 143 of 64; 64 x 8,192 168 and 159)
             if (g.mode >= MU_UPDATE && split == 1 && 2 * tiles * B <= dev.clusters[0]) {
                 g.width = SP_TILE / 2;
                 g.tiles_n = (int32_t)ceil_div64(g.N, g.width);

@@ -395,16 +395,16 @@ size_t muon_workspace_bytes(int32_t B, int64_t rows, int64_t cols,
  *     out      = round(scale * X)
  * (a tall matrix is treated as its transpose.)  Sums are fp32 or wider.  With
  * fp32 and fp16 output every product keeps 22 bits of its operands, and the
- * result is about as exact as one in plain fp32 before its one rounding to the
- * output type, in rows and columns of 1e-6 of the largest ones too (below that
- * they lose bits: 1e-4 off at 1e-8).  With bf16 output and a short side above 128
- * the products' operands are rounded to 11 bits.  That leaves the result 1.8e-3
- * to 2.4e-3 of its norm off for dense matrices and up to 4e-3 for sparse ones,
- * ones of equal entries and ones with one large row (the rounding to bf16 alone:
- * 1.65e-3), and single rows of sparse ones up to 1.5e-2 (rounding: 4e-3).  Ask
- * for fp32 output and round it where that is too much: three times the products'
- * time.  fp32 output may be part of the flat buffer that topk_ef_compress and
- * topk_ef_compress_batched read.
+ * result is about as exact as one in plain fp32 (1e-6 to 1e-5 of its norm off)
+ * before its one rounding to the output type, in rows and columns of 1e-6 of the
+ * largest ones too (below that they lose bits: 1e-4 off at 1e-8).  With bf16 output and a short side above 128
+ * the products' operands are rounded to 11 bits.  That leaves the result 1.7e-3
+ * to 2.5e-3 of its norm off for dense matrices, up to 4e-3 for sparse ones and
+ * ones with one large row and up to 7e-3 for equal entries (the rounding to bf16
+ * alone: 1.65e-3, equal entries 0.4e-3 to 3e-3), and single rows of sparse ones
+ * up to 1.5e-2 (rounding: 4e-3).  Ask for fp32 output and round it where that
+ * is too much: three times the products' time.  fp32 output may be part of the
+ * flat buffer that topk_ef_compress and topk_ef_compress_batched read.
  *   grad       device, [B][rows][cols] of grad_type; rows ld_grad apart,
  *              matrices stride_grad apart
  *   momentum   device, fp32[B][rows][cols] contiguous, updated in place; or
@@ -417,8 +417,9 @@ size_t muon_workspace_bytes(int32_t B, int64_t rows, int64_t cols,
  *              |b x^2 + c x^4| within 16
  *   steps      1 <= steps <= 64
  *   out        device, [B][rows][cols] of out_type; rows ld_out apart,
- *              matrices stride_out apart; may be grad itself (same type and
- *              strides), must not overlap otherwise
+ *              matrices stride_out apart; may start where grad does (B > 1:
+ *              with the same type and strides only), must not overlap it
+ *              otherwise
  *   ws         device workspace of >= muon_workspace_bytes(B, rows, cols,
  *              out_type)
  * Infinities, NaNs: as the formulas give them (a NaN anywhere makes the whole
