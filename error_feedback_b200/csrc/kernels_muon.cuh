@@ -662,8 +662,8 @@ __device__ __forceinline__ void epilogue32(const GemmParams& p, const TileAt& at
 //
 // Bound by the tensor cores at the clock that the power cap leaves (the pipe is
 // active 59 to 62% of a launch, 64 to 69% with 22 bits), by the rounds that leave
-// pairs idle and by the last round's epilogue: gram, square and
-// update of 4,096 x 4,096 in 61, 61 and 111 us at 1.6 GHz (1.1 to 1.25 PFLOP/s,
+// pairs idle and by the last round's epilogue: gram, square and update of
+// 4,096 x 4,096 in 61, 61 and 111 us at 1.6 GHz (1.1 to 1.25 PFLOP/s,
 // symmetric products by half; with 22 bits 167, 172 and 315), of 25,088 x 4,096 in
 // 356, 76 and 674.  (Five steps and the two passes before them: 1.23 ms; 1.34 to 1.5
 // in calls that follow one another, at the 1.3 to 1.4 GHz of the power cap.)
@@ -958,7 +958,8 @@ constexpr int sp_smem(bool exact, int stages) {
 }
 
 // Four columns of one row; v: the sums, h and l: the elementwise operand (of a gram:
-// the sums of the K before); v becomes the value.  (The last update's values are stored by store_rows.)
+// the sums of the K before); v becomes the value.  (The last update's values are
+// stored by store_rows.)
 template <bool EXACT, int MODE>
 __device__ __forceinline__ void epilogue4(const GemmParams& p, const TileAt& at, float alpha,
                                           float beta, int64_t row, int64_t c0, uint2 h, uint2 l,

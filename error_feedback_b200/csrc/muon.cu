@@ -490,11 +490,11 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad, int64_t st
             }
             g.tiles = (int32_t)tiles;
             g.stages = !exact && tiles * B <= dev.clusters[lg] ? SP_MAX_STAGES : SP_MIN_STAGES;
-            const int64_t per = ceil_div64(kblocks, parts_k);
-            for (int64_t k = 0; k < kblocks && r == cudaSuccess; k += per) {
-                g.k_first = (int32_t)k;
-                g.k_blocks = (int32_t)std::min(per, kblocks - k);
-                g.add = k > 0;
+            // (even parts: each has far more than one 64 for every block of a cluster)
+            for (int64_t i = 0; i < parts_k && r == cudaSuccess; ++i) {
+                g.k_first = (int32_t)(kblocks * i / parts_k);
+                g.k_blocks = (int32_t)(kblocks * (i + 1) / parts_k) - g.k_first;
+                g.add = i > 0;
                 trace_before(st, "muon_split_kernel");
                 r = with_kernel(exact, g.mode, [&](auto, auto kernel) {
                     return launch_clusters(kernel, (unsigned)(tiles * B * split), (unsigned)split,
