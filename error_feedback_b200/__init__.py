@@ -16,6 +16,8 @@ Functions mirror the C names:
 * ``embedding_grad(grad_out, ids, num_rows, scale)``     -> grad_weight
 * ``muon_update(grad, momentum, mu)``                    -> out
 * ``embedding_grad_rows(grad_out, ids, num_rows, scale)`` -> (rows, val, count)
+* ``layer_norm(x, weight, bias)``                        -> (out, mean, rstd)
+* ``layer_norm_grad(grad_out, x, mean, rstd, weight)``   -> (grad_x, grad_weight, grad_bias)
 * ``topk_ef_workspace_bytes``, ``topk_ef_batched_workspace_bytes``,
   ``gtopk_merge_workspace_bytes``, ``topk_ef_last_device_status``,
   ``topk_ef_path_info``, ``topk_ef_set_test_flags``.
@@ -133,6 +135,14 @@ def lib() -> ctypes.CDLL:
                                   _i32, ctypes.c_float, ctypes.POINTER(ctypes.c_float), _i32,
                                   ctypes.c_float, _vp, _i32, _i64, _i64, _vp, _sz, _vp]
         L.muon_update.restype = ctypes.c_int
+        L.layer_norm.argtypes = [_vp, _i32, _i64, _vp, _i32, _vp, _i32, _i64, _i64, ctypes.c_float,
+                                 _vp, _i32, _i64, _vp, _vp, _vp]
+        L.layer_norm.restype = ctypes.c_int
+        L.layer_norm_grad_workspace_bytes.argtypes = [_i64, _i64]
+        L.layer_norm_grad_workspace_bytes.restype = _sz
+        L.layer_norm_grad.argtypes = [_vp, _i32, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _i32, _i64,
+                                      _i64, _vp, _i64, _vp, _i32, _vp, _i32, _i32, _vp, _sz, _vp]
+        L.layer_norm_grad.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -691,6 +701,132 @@ def muon_update(grad, momentum=None, mu=0.95, nesterov=True, coefficients=MUON_C
         if rc != OK:
             _check(rc, "muon_update")
         return o
+
+    return _on(dev, stream, call)
+
+
+# ---------------------------------------------------------------- layer norm
+
+def _rows(t, name: str, D=None, device=None):
+    """_matrix of [..., D] rows: (2-d view, type code, row stride)."""
+    if isinstance(t, torch.Tensor) and t.dim() != 2 and t.dim() > 0:
+        n = t.shape[-1]
+        t = t.view(-1, n) if t.numel() else t.new_empty((t.shape[:-1].numel(), n))
+    code, ld = _matrix(t, name, device)
+    if D is not None and t.shape[1] != D:
+        raise ValueError(f"{name} must have rows of {D}")
+    return t, code, ld
+
+
+def _vector(t, name: str, n: int, device, dtype=None):
+    """Address and type code of a contiguous [n] tensor on the device; (None, 0)
+    for None."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor) or t.get_device() != device.index or t.numel() != n \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {n} on {device}")
+    code = _TYPE.get(t.dtype)
+    if code is None or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype or 'float32, bfloat16 or float16'}")
+    return t.data_ptr(), code
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=None, mean=None, rstd=None,
+               stats=True, stream=None):
+    """out = (x - mean) rstd weight + bias over the last dimension of x
+    ([..., D] with contiguous rows), mean and rstd = (variance + eps)^-1/2 of
+    each row in fp32, the result rounded once.  Types: float32, bfloat16 or
+    float16 each (out: x's by default).  out may be x.  Returns (out, mean,
+    rstd), mean and rstd float32 [rows] for layer_norm_grad (None with
+    stats=False and none given).  Autograd records nothing: the gradient is
+    layer_norm_grad's."""
+    x2, xt, ldx = _rows(x, "x")
+    dev = x.device
+    T, D = x2.shape
+    wp, wt = _vector(weight, "weight", D, dev)
+    bp, bt = _vector(bias, "bias", D, dev)
+    _vector(mean, "mean", T, dev, torch.float32)
+    _vector(rstd, "rstd", T, dev, torch.float32)
+
+    def call(st):
+        o, m, r = out, mean, rstd
+        if o is None:
+            o = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=dev)
+        elif out_dtype is not None and o.dtype != out_dtype:
+            raise ValueError("out and out_dtype differ")
+        o2, ot, ldo = _rows(o, "out", D, dev)
+        if o2.shape[0] != T:
+            raise ValueError(f"out must hold [{T}, {D}] elements")
+        if stats:
+            if m is None:
+                m = torch.empty(T, dtype=torch.float32, device=dev)
+            if r is None:
+                r = torch.empty(T, dtype=torch.float32, device=dev)
+        rc = lib().layer_norm(x2.data_ptr(), xt, ldx, wp, wt, bp, bt, T, D, eps, o2.data_ptr(), ot,
+                              ldo, None if m is None else m.data_ptr(),
+                              None if r is None else r.data_ptr(), st)
+        if rc != OK:
+            _check(rc, "layer_norm")
+        return o, m, r
+
+    return _on(dev, stream, call)
+
+
+def layer_norm_grad_workspace_bytes(T: int, D: int) -> int:
+    return int(lib().layer_norm_grad_workspace_bytes(int(T), int(D)))
+
+
+def layer_norm_grad(grad_out, x, mean, rstd, weight=None, affine=True, accumulate=False,
+                    grad_x=None, grad_weight=None, grad_bias=None, out_dtype=None, ws=None,
+                    stream=None):
+    """Gradient of layer_norm: (grad_x, grad_weight, grad_bias).  grad_out and x:
+    [..., D]; mean, rstd: layer_norm's; grad_x: x's type, may be x or grad_out
+    itself; grad_weight, grad_bias: [D] (out_dtype, default float32, the type
+    that topk_ef_compress reads), added to what they hold with accumulate; both
+    None with affine=False."""
+    x2, xt, ldx = _rows(x, "x")
+    dev = x.device
+    T, D = x2.shape
+    g2, gt, ldg = _rows(grad_out, "grad_out", D, dev)
+    if g2.shape[0] != T:
+        raise ValueError("grad_out must have x's rows")
+    wp, wt = _vector(weight, "weight", D, dev)
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd are needed")
+    mp = _vector(mean, "mean", T, dev, torch.float32)[0]
+    rp = _vector(rstd, "rstd", T, dev, torch.float32)[0]
+    if affine and accumulate and (grad_weight is None or grad_bias is None):
+        raise ValueError("accumulate needs grad_weight and grad_bias")
+    _on_device(ws, dev)
+
+    def call(st):
+        gx, gw, gb = grad_x, grad_weight, grad_bias
+        if gx is None:
+            gx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        gx2, gxt, ldgx = _rows(gx, "grad_x", D, dev)
+        if gx2.shape[0] != T or gxt != xt:
+            raise ValueError("grad_x must have x's rows and type")
+        w = ws
+        if affine:
+            if gw is None:
+                gw = torch.empty(D, dtype=out_dtype or torch.float32, device=dev)
+            if gb is None:
+                gb = torch.empty(D, dtype=out_dtype or torch.float32, device=dev)
+            if w is None:
+                w = _own_workspace(layer_norm_grad_workspace_bytes(T, D), dev,
+                                   "layer_norm_grad_workspace_bytes")
+        elif gw is not None or gb is not None:
+            raise ValueError("affine=False has no grad_weight and grad_bias")
+        gwp, gwt = _vector(gw, "grad_weight", D, dev)
+        gbp, gbt = _vector(gb, "grad_bias", D, dev)
+        rc = lib().layer_norm_grad(g2.data_ptr(), gt, ldg, x2.data_ptr(), xt, ldx, mp, rp, wp, wt,
+                                   T, D, gx2.data_ptr(), ldgx, gwp, gwt, gbp, gbt,
+                                   1 if accumulate else 0, None if w is None else w.data_ptr(),
+                                   0 if w is None else w.nbytes, st)
+        if rc != OK:
+            _check(rc, "layer_norm_grad")
+        return gx, gw, gb
 
     return _on(dev, stream, call)
 

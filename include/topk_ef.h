@@ -434,6 +434,68 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad,
                 int32_t out_type, int64_t ld_out, int64_t stride_out, void* ws,
                 size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------- layer norm */
+
+/*
+ * Layer norm of T rows:
+ *     mean = 1/D sum x;  rstd = 1 / sqrt(1/D sum (x - mean)^2 + eps)
+ *     out  = round((x - mean) rstd weight + bias)
+ * Sums are fp32, the variance a sum of squared differences (an offset common to
+ * a row costs no bits), one rounding to out_type.
+ *   x          device, [T][ld_x] of x_type
+ *   weight     device, [D] of weight_type, or NULL for 1
+ *   bias       device, [D] of bias_type, or NULL for 0
+ *   sizes      0 <= T <= 2^31 - 1; 1 <= D <= 2^24; ld_x, ld_out >= D
+ *   eps        >= 0
+ *   out        device, [T][ld_out] of out_type; columns from D on are not
+ *              written; may be x itself (same type size and stride), must not
+ *              overlap it otherwise
+ *   mean, rstd device, fp32[T], or NULL: what layer_norm_grad needs
+ * Rows on 16-byte boundaries with D a multiple of 8 take the vectorised path,
+ * others an elementwise one (same formulas; sums in another order).
+ * Infinities and NaNs make their row NaN, no other row.  There is no device
+ * status and no workspace.
+ * Errors: TOPK_EF_ERR_INVALID_ARG (sizes, types, null or misaligned pointers),
+ * TOPK_EF_ERR_CUDA.
+ */
+int layer_norm(const void* x, int32_t x_type, int64_t ld_x, const void* weight,
+               int32_t weight_type, const void* bias, int32_t bias_type,
+               int64_t T, int64_t D, float eps, void* out, int32_t out_type,
+               int64_t ld_out, float* mean, float* rstd, void* stream);
+
+/* Workspace bytes for layer_norm_grad; 0 for invalid sizes. */
+size_t layer_norm_grad_workspace_bytes(int64_t T, int64_t D);
+
+/*
+ * Gradient of layer_norm.  With xh = (x - mean) rstd and g = grad_out weight:
+ *     grad_x      = round(rstd (g - 1/D sum g - xh 1/D sum (g xh)))
+ *     grad_weight = (accumulate ? grad_weight : 0) + sum over rows of grad_out xh
+ *     grad_bias   = (accumulate ? grad_bias : 0) + sum over rows of grad_out
+ * Sums are fp32 in an order that depends on the sizes and alignment alone (no
+ * floating-point atomics), rounded once.  fp32 weight gradients may be part of
+ * the flat buffer that topk_ef_compress and topk_ef_compress_batched read.
+ *   grad_out   device, [T][ld_grad_out] of grad_out_type
+ *   x          device, [T][ld_x] of x_type: layer_norm's input
+ *   mean, rstd device, fp32[T]: layer_norm's
+ *   weight     as in layer_norm
+ *   grad_x     device, [T][ld_grad_x] of x_type; may be x or grad_out itself
+ *              (same type size and stride), must not overlap them otherwise
+ *   grad_weight, grad_bias  device, [D] of their types; either or both may be
+ *              NULL
+ *   ws         device workspace of >= layer_norm_grad_workspace_bytes(T, D);
+ *              not used (may be NULL) if grad_weight and grad_bias are NULL
+ * Otherwise as layer_norm.
+ */
+int layer_norm_grad(const void* grad_out, int32_t grad_out_type,
+                    int64_t ld_grad_out, const void* x, int32_t x_type,
+                    int64_t ld_x, const float* mean, const float* rstd,
+                    const void* weight, int32_t weight_type, int64_t T,
+                    int64_t D, void* grad_x, int64_t ld_grad_x,
+                    void* grad_weight, int32_t grad_weight_type,
+                    void* grad_bias, int32_t grad_bias_type,
+                    int32_t accumulate, void* ws, size_t ws_bytes,
+                    void* stream);
+
 /* Synchronises `stream` and returns the device-side status of the last call
    that used `ws`: TOPK_EF_OK, TOPK_EF_ERR_DEVICE_TIMEOUT,
    TOPK_EF_ERR_BAD_INPUT or TOPK_EF_ERR_INTERNAL (or TOPK_EF_ERR_CUDA if the
