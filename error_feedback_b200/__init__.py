@@ -18,6 +18,9 @@ Functions mirror the C names:
 * ``embedding_grad_rows(grad_out, ids, num_rows, scale)`` -> (rows, val, count)
 * ``layer_norm(x, weight, bias)``                        -> (out, mean, rstd)
 * ``layer_norm_grad(grad_out, x, mean, rstd, weight)``   -> (grad_x, grad_weight, grad_bias)
+* ``token_logprobs(logits, ids, scale, top)``            -> (logprob, entropy, lse, top_ids, top_logprobs)
+* ``token_logprobs_grad(logits, ids, lse, ...)``         -> grad_logits
+* ``distill_loss(logits, teacher_ids, teacher_logits)``  -> (loss, grad_logits)
 * ``topk_ef_workspace_bytes``, ``topk_ef_batched_workspace_bytes``,
   ``gtopk_merge_workspace_bytes``, ``topk_ef_last_device_status``,
   ``topk_ef_path_info``, ``topk_ef_set_test_flags``.
@@ -143,6 +146,19 @@ def lib() -> ctypes.CDLL:
         L.layer_norm_grad.argtypes = [_vp, _i32, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _i32, _i64,
                                       _i64, _vp, _i64, _vp, _i32, _vp, _i32, _i32, _vp, _sz, _vp]
         L.layer_norm_grad.restype = ctypes.c_int
+        L.token_logprobs_workspace_bytes.argtypes = []
+        L.token_logprobs_workspace_bytes.restype = _sz
+        L.token_logprobs.argtypes = [_vp, _i32, _i64, _vp, _i32, _i64, _i64, ctypes.c_float, _i64,
+                                     _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+        L.token_logprobs.restype = ctypes.c_int
+        L.token_logprobs_grad.argtypes = [_vp, _i32, _i64, _vp, _i32, _i64, _i64, ctypes.c_float,
+                                          _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _vp, _sz, _vp]
+        L.token_logprobs_grad.restype = ctypes.c_int
+        L.distill_loss_workspace_bytes.argtypes = []
+        L.distill_loss_workspace_bytes.restype = _sz
+        L.distill_loss.argtypes = [_vp, _i32, _i64, _vp, _i32, _vp, _i32, _i64, _i64, _i32,
+                                   ctypes.c_float, _vp, _vp, _vp, _i32, _i64, _vp, _sz, _vp]
+        L.distill_loss.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -827,6 +843,176 @@ def layer_norm_grad(grad_out, x, mean, rstd, weight=None, affine=True, accumulat
         if rc != OK:
             _check(rc, "layer_norm_grad")
         return gx, gw, gb
+
+    return _on(dev, stream, call)
+
+
+# ------------------------------------------------- losses over a vocabulary
+
+_STATUS_WS = 512        # at least token_logprobs_workspace_bytes(), distill_loss_workspace_bytes()
+
+
+def token_logprobs_workspace_bytes() -> int:
+    return int(lib().token_logprobs_workspace_bytes())
+
+
+def _ids_of(ids, T, device):
+    """Address and size of the T ids of a call, or (None, 8)."""
+    if ids is None:
+        return None, 8
+    idb, n = _token_ids(ids, device)
+    if n != T:
+        raise ValueError("ids must hold one id for each row")
+    return ids.data_ptr(), idb
+
+
+def _table(t, name: str, rows: int, cols: int, device, dtype):
+    if not isinstance(t, torch.Tensor) or t.get_device() != device.index or t.dtype != dtype \
+            or not t.is_contiguous() or t.numel() != rows * cols:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of [{rows}, {cols}] on {device}")
+
+
+def token_logprobs(logits, ids=None, scale=1.0, top=0, padding_idx=-1, logprob=None, entropy=None,
+                   lse=None, top_ids=None, top_logprobs=None, ws=None, stream=None):
+    """Of each row of logits ([..., V], contiguous rows), with
+    p = softmax(scale logits): (log p[ids], the entropy, the log of the sum, the ids
+    of the `top` largest logits in descending order, the lower first among
+    equal ones, and their log-probabilities).  The outputs are float32 [rows]
+    and int32 / float32 [rows, top]; the first is None without ids, the last two
+    with top=0.  Rows whose id is padding_idx are not read: 0, and ids of -1 at
+    -inf.  Another id outside [0, V) gives 0 and ERR_BAD_INPUT from
+    topk_ef_last_device_status(ws).  Autograd records nothing: the gradient is
+    token_logprobs_grad's."""
+    z, zt, ldz = _rows(logits, "logits")
+    dev = z.device
+    T, V = z.shape
+    ip, idb = _ids_of(ids, T, dev)
+    top = int(top)
+    if ids is None and logprob is not None:
+        raise ValueError("logprob needs ids")
+    if top == 0 and (top_ids is not None and top_ids.numel()
+                     or top_logprobs is not None and top_logprobs.numel()):
+        raise ValueError("top_ids and top_logprobs need top")
+    for t, name in ((logprob, "logprob"), (entropy, "entropy"), (lse, "lse")):
+        _vector(t, name, T, dev, torch.float32)
+    _on_device(ws, dev)
+
+    def call(st):
+        lp, en, ls, ti, tp = logprob, entropy, lse, top_ids, top_logprobs
+        if lp is None and ids is not None:
+            lp = torch.empty(T, dtype=torch.float32, device=dev)
+        if en is None:
+            en = torch.empty(T, dtype=torch.float32, device=dev)
+        if ls is None:
+            ls = torch.empty(T, dtype=torch.float32, device=dev)
+        if top > 0:
+            if ti is None:
+                ti = torch.empty((T, top), dtype=torch.int32, device=dev)
+            if tp is None:
+                tp = torch.empty((T, top), dtype=torch.float32, device=dev)
+            _table(ti, "top_ids", T, top, dev, torch.int32)
+            _table(tp, "top_logprobs", T, top, dev, torch.float32)
+        w = ws if ws is not None else _workspace(_STATUS_WS, dev, None)
+        rc = lib().token_logprobs(z.data_ptr(), zt, ldz, ip, idb, T, V, scale, int(padding_idx), top,
+                                  None if lp is None else lp.data_ptr(), en.data_ptr(),
+                                  ls.data_ptr(), ti.data_ptr() if top > 0 else None,
+                                  tp.data_ptr() if top > 0 else None, w.data_ptr(), w.nbytes, st)
+        if rc != OK:
+            _check(rc, "token_logprobs")
+        return lp, en, ls, ti, tp
+
+    return _on(dev, stream, call)
+
+
+def _grad_rows(out, z, dtype, device):
+    """(the tensor, 2-d view, type code, row stride) of a gradient of the logits."""
+    if out is None:
+        out = torch.empty(z.shape, dtype=dtype or z.dtype, device=device)
+    elif dtype is not None and out.dtype != dtype:
+        raise ValueError("out and out_dtype differ")
+    o2, ot, ldo = _rows(out, "the logits' gradient", z.shape[-1], device)
+    if o2.numel() != z.numel():
+        raise ValueError("the logits' gradient must have their shape")
+    return out, o2, ot, ldo
+
+
+def token_logprobs_grad(logits, ids, lse, grad_logprob=None, entropy=None, grad_entropy=None,
+                        scale=1.0, padding_idx=-1, out=None, out_dtype=None, ws=None, stream=None):
+    """Gradient of token_logprobs in the logits: scale (grad_logprob (1[i = id] - p_i)
+    - grad_entropy p_i (log p_i + entropy)) of each row, in the logits' type by
+    default.  lse, entropy: token_logprobs'; grad_logprob, grad_entropy: float32
+    [rows] or None for 0 (entropy is needed with the latter).  out may be the
+    logits.  Rows that are padding or whose gradients are 0 are not read and
+    give zeros."""
+    z, zt, ldz = _rows(logits, "logits")
+    dev = z.device
+    T, V = z.shape
+    ip, idb = _ids_of(ids, T, dev)
+    if lse is None or (grad_entropy is not None and entropy is None) or \
+            (grad_logprob is not None and ids is None):
+        raise ValueError("lse, ids for grad_logprob and entropy for grad_entropy are needed")
+    sp = _vector(lse, "lse", T, dev, torch.float32)[0]
+    ep = _vector(entropy, "entropy", T, dev, torch.float32)[0]
+    gp = _vector(grad_logprob, "grad_logprob", T, dev, torch.float32)[0]
+    hp = _vector(grad_entropy, "grad_entropy", T, dev, torch.float32)[0]
+    _on_device(ws, dev)
+
+    def call(st):
+        o, o2, ot, ldo = _grad_rows(out, logits, out_dtype, dev)
+        w = ws if ws is not None else _workspace(_STATUS_WS, dev, None)
+        rc = lib().token_logprobs_grad(z.data_ptr(), zt, ldz, ip, idb, T, V, scale,
+                                       int(padding_idx), sp, ep, gp, hp, o2.data_ptr(), ot, ldo,
+                                       w.data_ptr(), w.nbytes, st)
+        if rc != OK:
+            _check(rc, "token_logprobs_grad")
+        return o
+
+    return _on(dev, stream, call)
+
+
+def distill_loss_workspace_bytes() -> int:
+    return int(lib().distill_loss_workspace_bytes())
+
+
+def distill_loss(logits, teacher_ids, teacher_logits, weight=None, scale=1.0, grad=False, loss=None,
+                 grad_logits=None, out_dtype=None, ws=None, stream=None):
+    """Distillation from a teacher's top logits: (loss, grad_logits), with
+    q = softmax(scale teacher_logits) over the K entries of a row and
+    p = softmax(scale logits) over all tokens,
+    loss = weight sum_k q_k (log q_k - log p[teacher_ids_k]), float32 [rows], and the
+    gradient of its sum, weight scale (p - q), in the logits' type by default:
+    with grad or a grad_logits to write (which may be the logits), else None.
+    teacher_ids: int32 / int64 [rows, K] (token_logprobs' top_ids; negative: no
+    entry); teacher_logits: [rows, K]; weight: float32 [rows] or None for 1.  An id
+    past V gives ERR_BAD_INPUT from topk_ef_last_device_status(ws) and counts
+    nowhere."""
+    z, zt, ldz = _rows(logits, "logits")
+    dev = z.device
+    T, V = z.shape
+    idb, n = _token_ids(teacher_ids, dev)
+    K = int(teacher_ids.shape[-1]) if teacher_ids.dim() else 1
+    if n != T * K:
+        raise ValueError("teacher_ids must be [rows, K]")
+    tp, tt = _vector(teacher_logits, "teacher_logits", T * K, dev)
+    if tp is None:
+        raise ValueError("teacher_logits are needed")
+    wp = _vector(weight, "weight", T, dev, torch.float32)[0]
+    _vector(loss, "loss", T, dev, torch.float32)
+    _on_device(ws, dev)
+
+    def call(st):
+        lo, o, op, ot, ldo = loss, grad_logits, None, 0, V
+        if lo is None:
+            lo = torch.empty(T, dtype=torch.float32, device=dev)
+        if grad or o is not None:
+            o, o2, ot, ldo = _grad_rows(o, logits, out_dtype, dev)
+            op = o2.data_ptr()
+        w = ws if ws is not None else _workspace(_STATUS_WS, dev, None)
+        rc = lib().distill_loss(z.data_ptr(), zt, ldz, teacher_ids.data_ptr(), idb, tp, tt, T, V, K,
+                                scale, wp, lo.data_ptr(), op, ot, ldo, w.data_ptr(), w.nbytes, st)
+        if rc != OK:
+            _check(rc, "distill_loss")
+        return lo, o
 
     return _on(dev, stream, call)
 

@@ -62,4 +62,23 @@ cudaError_t launch_pdl(Kern kernel, dim3 grid, int block, cudaStream_t st, const
     return cudaLaunchKernelEx(&cfg, kernel, arg);
 }
 
+// As launch_pdl, with clusters of `cluster` blocks.
+template <typename Kern, typename Arg>
+cudaError_t launch_clusters(Kern kernel, unsigned grid, unsigned cluster, int block, size_t smem,
+                            cudaStream_t st, const Arg& arg) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {cluster, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, arg);
+}
+
 }  // namespace tke

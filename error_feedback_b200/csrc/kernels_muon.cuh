@@ -26,6 +26,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "async.cuh"
 #include "common.cuh"
 #include "elements.cuh"
 
@@ -45,7 +46,6 @@ constexpr int MU_MAX_LIFT = 60;             // (see muon_scale_kernel)
 // it worse.  A 128 x 24,576 matrix is 8.1e-6 off without, 3.5e-6 with it (plain
 // fp32: 1.4e-6), one of 2,048 x 8,192 1.2e-5 and 7.5e-6 (5.2e-6).
 constexpr float MU_LOW = 5.4e-8f;
-constexpr uint64_t MU_WAIT_NS = 2000000000ull;
 
 __device__ __forceinline__ float below_half(float x) {     // what fp16 leaves of x, as it is held
     return MU_LO * (x - __half2float(__float2half_rn(x)));
@@ -300,43 +300,6 @@ struct GemmParams {
     Ctrl* ctrl;
 };
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
-}
-__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// Waits for a phase; gives up after MU_WAIT_NS, or once another warp has.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
-                                          uint32_t* status) {
-    if (mbar_try(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-    for (uint32_t it = 0; it < SPIN_LIMIT * 16u; ++it) {
-        if (mbar_try(bar, parity)) return true;
-        if (*gave_up) return false;
-        if ((it & 63u) == 63u && global_ns() - t0 > MU_WAIT_NS) break;
-    }
-    *gave_up = 1;
-    atomicOr(status, ST_TIMEOUT);
-    return false;
-}
-
 // One box (128 or 64 rows or columns from `at`, 64 of K from `k`) into this
 // block's shared memory, counted on its barrier.
 __device__ __forceinline__ void tma_box1(uint32_t dst, const CUtensorMap* map, bool mn, int at, int k,
@@ -359,23 +322,9 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, bo
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t in_block(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-
 // Shared-memory matrix descriptor, 128-byte swizzle.  K-major: rows of 64 K
 // values (128 bytes), 8-row groups 1,024 bytes apart.  M/N-major: boxes of 64
 // M/N values x 64 K rows, 8,192 bytes apart, 8-row groups 1,024 bytes apart.

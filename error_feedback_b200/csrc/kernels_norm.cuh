@@ -412,6 +412,7 @@ __global__ void __launch_bounds__(NL_COLS) norm_cols_kernel(const NormGradParams
 
 struct NormSumParams {
     const float* part;             // [parts][2][D]
+    Ctrl* ctrl;
     void* out[2];                  // dw, db (either or both)
     int64_t D;
     int32_t parts, type[2], accumulate;
@@ -424,6 +425,10 @@ __global__ void __launch_bounds__(32 * NS_WARPS) norm_sum_kernel(const NormSumPa
     __shared__ float s[NS_WARPS][32];
     pdl_wait();
     const int k = (int)blockIdx.y, lane = (int)lane_id(), w = (int)warp_id();
+    if (blockIdx.x == 0 && k == 0 && threadIdx.x == 0) {
+        p.ctrl->path_small = 0;
+        p.ctrl->status = 0;
+    }
     if (!p.out[k]) return;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float v = 0.0f;

@@ -145,7 +145,7 @@ int layer_norm(const void* x, int32_t x_type, int64_t ld_x, const void* weight,
 
 size_t layer_norm_grad_workspace_bytes(int64_t T, int64_t D) {
     if (!sizes_ok(T, D)) return 0;
-    return align_up((size_t)grad_parts(T) * 2 * (size_t)D * 4);
+    return align_up(sizeof(Ctrl)) + align_up((size_t)grad_parts(T) * 2 * (size_t)D * 4);
 }
 
 int layer_norm_grad(const void* grad_out, int32_t grad_out_type, int64_t ld_grad_out,
@@ -183,7 +183,7 @@ int layer_norm_grad(const void* grad_out, int32_t grad_out_type, int64_t ld_grad
     p.rstd = rstd;
     p.w = weight;
     p.dx = grad_x;
-    p.part = cols ? static_cast<float*>(ws) : nullptr;
+    p.part = cols ? reinterpret_cast<float*>(static_cast<char*>(ws) + align_up(sizeof(Ctrl))) : nullptr;
     p.T = T;
     p.D = D;
     p.ldy = ld_grad_out;
@@ -222,9 +222,10 @@ int layer_norm_grad(const void* grad_out, int32_t grad_out_type, int64_t ld_grad
         });
         if (e != cudaSuccess) return cuda_fail(e);
     }
-    if (!cols || (T == 0 && accumulate)) return TOPK_EF_OK;
+    if (!cols) return TOPK_EF_OK;
     NormSumParams s = {};
     s.part = p.part;
+    s.ctrl = static_cast<Ctrl*>(ws);
     s.out[0] = grad_weight;
     s.out[1] = grad_bias;
     s.type[0] = grad_weight_type;

@@ -1,0 +1,266 @@
+// Host side of token_logprobs, token_logprobs_grad and distill_loss
+// (include/topk_ef.h): argument checks, the blocks of a row.  One kernel a
+// call; the status word is written by a block that checks the ids of a short list,
+// or cleared before the kernel whose blocks check a long one.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "topk_ef.h"
+#include "common.cuh"
+#include "host.cuh"
+#include "kernels_logits.cuh"
+
+using namespace tke;
+
+namespace {
+
+constexpr int64_t SCAN_IDS = 8192;         // ids that one block checks
+constexpr int64_t WANT_BLOCKS = 148 * 3;   // blocks that a call should have at least
+constexpr int64_t LEAST_LINES = 32;        // lines of a block of a cluster
+
+bool sizes_ok(int64_t T, int64_t V) {
+    return T >= 0 && T <= MAX_N && V >= 1 && V <= (int64_t)1 << 24;
+}
+bool pointer_ok(const void* p, size_t size) { return p && aligned(p, size); }
+bool scale_ok(float s) { return s >= 1e-30f && s <= 1e30f; }
+
+// Most 128-byte lines that a row of V elements can touch.
+int64_t most_lines(int64_t V, size_t size) { return (V * (int64_t)size + LG_LINE - 2) / LG_LINE + 1; }
+
+// Blocks of a row's cluster: more while the call has too few.
+int row_blocks(int64_t T, int64_t lines) {
+    int c = 1;
+    while (c < 16 && T * c < WANT_BLOCKS && lines / (2 * c) >= LEAST_LINES) c *= 2;
+    return c;
+}
+
+// Lets a kernel have clusters of 16 and `smem` bytes, once for each device.
+template <typename K>
+cudaError_t allow(K kernel, std::atomic<uint64_t>& done, size_t smem) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev >= 64 || (done.load() >> dev & 1)) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && smem)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) done.fetch_or(1ull << dev);
+    return e;
+}
+
+// Rows of z and of out that start alike within their 128-byte lines.
+bool same_lines(const void* a, int64_t lda, const void* b, int64_t ldb, size_t size) {
+    return (uintptr_t)a % LG_LINE == (uintptr_t)b % LG_LINE &&
+           (size_t)(lda - ldb) * size % LG_LINE == 0;
+}
+
+template <typename T, bool ENTROPY, bool TOP>
+cudaError_t launch_logprob(const LogprobParams& p, size_t smem, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    const auto kernel = logprob_kernel<T, ENTROPY, TOP>;
+    cudaError_t e = allow(kernel, done, TOP ? TL_MAX_LINES * 4 : 0);
+    if (e != cudaSuccess) return e;
+    trace_before(st, "logprob_kernel");
+    e = launch_clusters(kernel, (unsigned)((p.T + p.scan) * p.blocks), (unsigned)p.blocks, LG_THREADS,
+                        smem, st, p);
+    trace_after(st);
+    return e;
+}
+
+template <typename T, typename TO, bool SAME>
+cudaError_t launch_distill(const DistillParams& p, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    const auto kernel = distill_kernel<T, TO, SAME>;
+    cudaError_t e = allow(kernel, done, 0);
+    if (e != cudaSuccess) return e;
+    trace_before(st, "distill_kernel");
+    e = launch_clusters(kernel, (unsigned)((p.T + p.scan) * p.blocks), (unsigned)p.blocks, LG_THREADS, 0,
+                        st, p);
+    trace_after(st);
+    return e;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t token_logprobs_workspace_bytes(void) { return align_up(sizeof(Ctrl)); }
+
+int token_logprobs(const void* logits, int32_t logits_type, int64_t ld_logits, const void* ids,
+                   int32_t id_bytes, int64_t T, int64_t V, float scale, int64_t padding_idx,
+                   int32_t top, float* logprob, float* entropy, float* lse, int32_t* top_ids,
+                   float* top_logprobs, void* ws, size_t ws_bytes, void* stream) {
+    const size_t sz = type_size(logits_type);
+    if (!sizes_ok(T, V) || !sz || ld_logits < V || !scale_ok(scale) || top < 0 || top > TL_MAX_TOP ||
+        !ws || !aligned(ws, ALIGN))
+        return TOPK_EF_ERR_INVALID_ARG;
+    const int64_t lines = most_lines(V, sz);
+    if (top > 0 && lines > TL_MAX_LINES) return TOPK_EF_ERR_INVALID_ARG;
+    if (ids && ((id_bytes != 4 && id_bytes != 8) || !aligned(ids, id_bytes)))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (!ids && logprob) return TOPK_EF_ERR_INVALID_ARG;
+    if (!aligned(logprob, 4) || !aligned(entropy, 4) || !aligned(lse, 4) || !aligned(top_ids, 4) ||
+        !aligned(top_logprobs, 4))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (T > 0 && !pointer_ok(logits, sz)) return TOPK_EF_ERR_INVALID_ARG;
+    if (ws_bytes < token_logprobs_workspace_bytes()) return TOPK_EF_ERR_WORKSPACE;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    LogprobParams p = {};
+    p.z = logits;
+    p.ids = ids;
+    p.logprob = logprob;
+    p.entropy = entropy;
+    p.lse = lse;
+    p.top_ids = top_ids;
+    p.top_logprobs = top_logprobs;
+    p.ctrl = static_cast<Ctrl*>(ws);
+    p.T = T;
+    p.V = V;
+    p.ldz = ld_logits;
+    p.padding = padding_idx;
+    p.id64 = id_bytes == 8;
+    p.top = top_ids || top_logprobs ? top : 0;
+    p.blocks = row_blocks(T, lines);
+    p.scan = T <= SCAN_IDS;
+    p.scale = scale;
+    p.c = (float)((double)scale * 1.4426950408889634);
+    if (!p.scan) {
+        const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(Ctrl), st);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    const size_t smem = p.top ? (size_t)lines * 4 : 0;
+    const cudaError_t e = with_type(logits_type, [&](auto t) {
+        using TZ = decltype(t);
+        if (p.top)
+            return entropy ? launch_logprob<TZ, true, true>(p, smem, st)
+                           : launch_logprob<TZ, false, true>(p, smem, st);
+        return entropy ? launch_logprob<TZ, true, false>(p, smem, st)
+                       : launch_logprob<TZ, false, false>(p, smem, st);
+    });
+    return e == cudaSuccess ? TOPK_EF_OK : cuda_fail(e);
+}
+
+int token_logprobs_grad(const void* logits, int32_t logits_type, int64_t ld_logits,
+                        const void* ids, int32_t id_bytes, int64_t T, int64_t V, float scale,
+                        int64_t padding_idx, const float* lse, const float* entropy,
+                        const float* grad_logprob, const float* grad_entropy, void* grad_logits,
+                        int32_t grad_logits_type, int64_t ld_grad_logits, void* ws,
+                        size_t ws_bytes, void* stream) {
+    const size_t sz = type_size(logits_type), so = type_size(grad_logits_type);
+    if (!sizes_ok(T, V) || !sz || !so || ld_logits < V || ld_grad_logits < V || !scale_ok(scale) ||
+        !ws || !aligned(ws, ALIGN))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (ids && ((id_bytes != 4 && id_bytes != 8) || !aligned(ids, id_bytes)))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (!ids && grad_logprob) return TOPK_EF_ERR_INVALID_ARG;
+    if (!aligned(entropy, 4) || !aligned(grad_logprob, 4) || !aligned(grad_entropy, 4) ||
+        (grad_entropy && !entropy))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (T > 0 && (!pointer_ok(logits, sz) || !pointer_ok(grad_logits, so) || !pointer_ok(lse, 4)))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (T > 0 && grad_logits == logits && (sz != so || ld_logits != ld_grad_logits))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (ws_bytes < token_logprobs_workspace_bytes()) return TOPK_EF_ERR_WORKSPACE;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    LogprobGradParams p = {};
+    p.z = logits;
+    p.ids = ids;
+    p.lse = lse;
+    p.entropy = entropy;
+    p.g = grad_logprob;
+    p.h = grad_entropy;
+    p.dz = grad_logits;
+    p.ctrl = static_cast<Ctrl*>(ws);
+    p.T = T;
+    p.V = V;
+    p.ldz = ld_logits;
+    p.lddz = ld_grad_logits;
+    p.padding = padding_idx;
+    p.id64 = id_bytes == 8;
+    p.scan = T <= SCAN_IDS;
+    p.scale = scale;
+    const int64_t chunks = most_lines(V, sz) * 4;
+    p.parts = (int32_t)std::min(ceil_div64(chunks, LD_THREADS * LG_FLIGHT),
+                                std::max<int64_t>(1, MAX_N / (T + 1)));
+    if (!p.scan) {
+        const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(Ctrl), st);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    const unsigned grid = (unsigned)(T * p.parts + p.scan);
+    const bool same = sz == so && same_lines(logits, ld_logits, grad_logits, ld_grad_logits, sz);
+    trace_before(st, "logprob_grad_kernel");
+    const cudaError_t e = with_type(logits_type, [&](auto t) {
+        return with_type(grad_logits_type, [&](auto to) {
+            using TZ = decltype(t);
+            using TO = decltype(to);
+            if constexpr (sizeof(TZ) == sizeof(TO))
+                if (same) return launch_pdl(logprob_grad_kernel<TZ, TO, true>, grid, LD_THREADS, st, p);
+            return launch_pdl(logprob_grad_kernel<TZ, TO, false>, grid, LD_THREADS, st, p);
+        });
+    });
+    trace_after(st);
+    return e == cudaSuccess ? TOPK_EF_OK : cuda_fail(e);
+}
+
+size_t distill_loss_workspace_bytes(void) { return align_up(sizeof(Ctrl)); }
+
+int distill_loss(const void* logits, int32_t logits_type, int64_t ld_logits,
+                 const void* teacher_ids, int32_t id_bytes, const void* teacher_logits,
+                 int32_t teacher_type, int64_t T, int64_t V, int32_t K, float scale,
+                 const float* weight, float* loss, void* grad_logits, int32_t grad_logits_type,
+                 int64_t ld_grad_logits, void* ws, size_t ws_bytes, void* stream) {
+    const size_t sz = type_size(logits_type), so = type_size(grad_logits_type);
+    const size_t st_ = type_size(teacher_type);
+    if (!sizes_ok(T, V) || !sz || !st_ || ld_logits < V || !scale_ok(scale) || K < 0 ||
+        K > DL_MAX_K || !ws || !aligned(ws, ALIGN))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (grad_logits && (!so || ld_grad_logits < V || !aligned(grad_logits, so)))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if ((id_bytes != 4 && id_bytes != 8) || !aligned(weight, 4) || !aligned(loss, 4))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (T > 0 && !pointer_ok(logits, sz)) return TOPK_EF_ERR_INVALID_ARG;
+    if (T > 0 && K > 0 && (!pointer_ok(teacher_ids, id_bytes) || !pointer_ok(teacher_logits, st_)))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (T > 0 && grad_logits == logits && (sz != so || ld_logits != ld_grad_logits))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (ws_bytes < distill_loss_workspace_bytes()) return TOPK_EF_ERR_WORKSPACE;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    DistillParams p = {};
+    p.z = logits;
+    p.ids = teacher_ids;
+    p.teacher = teacher_logits;
+    p.weight = weight;
+    p.loss = loss;
+    p.dz = grad_logits;
+    p.ctrl = static_cast<Ctrl*>(ws);
+    p.T = T;
+    p.V = V;
+    p.ldz = ld_logits;
+    p.lddz = ld_grad_logits;
+    p.id64 = id_bytes == 8;
+    p.teacher_type = teacher_type;
+    p.K = K;
+    p.blocks = row_blocks(T, most_lines(V, sz));
+    p.scan = T * std::max(K, 1) <= SCAN_IDS;
+    p.scale = scale;
+    p.c = (float)((double)scale * 1.4426950408889634);
+    if (!p.scan) {
+        const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(Ctrl), st);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    const bool same = grad_logits && sz == so &&
+                      same_lines(logits, ld_logits, grad_logits, ld_grad_logits, sz);
+    const cudaError_t e = with_type(logits_type, [&](auto t) {
+        return with_type(grad_logits ? grad_logits_type : logits_type, [&](auto to) {
+            using TZ = decltype(t);
+            using TO = decltype(to);
+            if constexpr (sizeof(TZ) == sizeof(TO))
+                if (same) return launch_distill<TZ, TO, true>(p, st);
+            return launch_distill<TZ, TO, false>(p, st);
+        });
+    });
+    return e == cudaSuccess ? TOPK_EF_OK : cuda_fail(e);
+}
+
+}  // extern "C"

@@ -70,7 +70,7 @@ extern "C" {
 /* device: a bounded spin-wait gave up (outputs are undefined) */
 #define TOPK_EF_ERR_DEVICE_TIMEOUT (-4)
 /* device: merge input rows not strictly ascending or indices outside [0, n),
-   embedding ids outside [0, V) */
+   embedding, token or teacher ids outside [0, V) */
 #define TOPK_EF_ERR_BAD_INPUT (-5)
 /* device: an internal count did not add up (outputs are undefined) */
 #define TOPK_EF_ERR_INTERNAL (-6)
@@ -453,8 +453,7 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad,
  *   mean, rstd device, fp32[T], or NULL: what layer_norm_grad needs
  * Rows on 16-byte boundaries with D a multiple of 8 take the vectorised path,
  * others an elementwise one (same formulas; sums in another order).
- * Infinities and NaNs make their row NaN, no other row.  There is no device
- * status and no workspace.
+ * Infinities and NaNs make their row NaN, no other row.  There is no workspace.
  * Errors: TOPK_EF_ERR_INVALID_ARG (sizes, types, null or misaligned pointers),
  * TOPK_EF_ERR_CUDA.
  */
@@ -463,7 +462,8 @@ int layer_norm(const void* x, int32_t x_type, int64_t ld_x, const void* weight,
                int64_t T, int64_t D, float eps, void* out, int32_t out_type,
                int64_t ld_out, float* mean, float* rstd, void* stream);
 
-/* Workspace bytes for layer_norm_grad; 0 for invalid sizes. */
+/* Workspace bytes for layer_norm_grad (a status block, always OK after a call, and
+   partial sums); 0 for invalid sizes. */
 size_t layer_norm_grad_workspace_bytes(int64_t T, int64_t D);
 
 /*
@@ -495,6 +495,108 @@ int layer_norm_grad(const void* grad_out, int32_t grad_out_type,
                     void* grad_bias, int32_t grad_bias_type,
                     int32_t accumulate, void* ws, size_t ws_bytes,
                     void* stream);
+
+/* ----------------------------------------------- losses over a vocabulary */
+
+/* Workspace bytes for token_logprobs and token_logprobs_grad (a status block). */
+size_t token_logprobs_workspace_bytes(void);
+
+/*
+ * Log-probabilities of given tokens, entropies and the largest alternatives of T
+ * rows of logits.  With p = softmax(scale * logits[t]) (sums in fp32):
+ *     lse[t]     = log sum_i exp(scale * logits[t][i])
+ *     logprob[t] = scale * logits[t][ids[t]] - lse[t]
+ *     entropy[t] = -sum_i p_i log p_i                  (0 log 0 = 0)
+ *     top_ids[t][0 .. top - 1]  the ids of the largest logits, descending, the lower
+ *                id first among equal ones (-0 equals +0; NaN above +Inf)
+ *     top_logprobs[t][j]        their log-probabilities
+ *   logits     device, [T][ld_logits] of logits_type; rows may start anywhere
+ *   ids        device, int32[T] or int64[T] (id_bytes 4 or 8); or NULL (then logprob
+ *              too): no row is padding
+ *   scale      1e-30 .. 1e30 (1 / temperature)
+ *   padding_idx  rows with this id are not read: their logprob, entropy and lse
+ *              are 0, their top_ids -1 and top_logprobs -Inf.  Any value, e.g. -1
+ *   top        0 .. 128.  With top > 0: V <= 2^20 (16-bit logits) or 2^19 (fp32), less
+ *              64.  Slots past V get -1 and -Inf
+ *   logprob, entropy, lse  device, fp32[T], each may be NULL
+ *   top_ids, top_logprobs  device, int32 and fp32[T][top], each may be NULL
+ *   sizes      0 <= T <= 2^31 - 1; 1 <= V <= 2^24; ld_logits >= V
+ *   ws         device workspace of >= token_logprobs_workspace_bytes()
+ * -Inf (a forbidden token) has probability 0.  A row of nothing else has lse and
+ * logprob -Inf and entropy 0.  NaN or +Inf makes a row's logprob, entropy, lse
+ * and top_logprobs NaN (a token at -Inf keeps -Inf under +Inf), its top_ids
+ * follow the order above.  An id outside
+ * [0, V), other than padding_idx, gives logprob 0 and TOPK_EF_ERR_BAD_INPUT through
+ * topk_ef_last_device_status(ws); nothing outside logits is read.
+ * Errors: TOPK_EF_ERR_INVALID_ARG (sizes, types, null or misaligned pointers),
+ * TOPK_EF_ERR_WORKSPACE, TOPK_EF_ERR_CUDA.
+ */
+int token_logprobs(const void* logits, int32_t logits_type, int64_t ld_logits,
+                   const void* ids, int32_t id_bytes, int64_t T, int64_t V,
+                   float scale, int64_t padding_idx, int32_t top,
+                   float* logprob, float* entropy, float* lse,
+                   int32_t* top_ids, float* top_logprobs, void* ws,
+                   size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of token_logprobs' log-probabilities and entropies in the logits:
+ *     grad_logits[t][i] = scale * (grad_logprob[t] * ((i == ids[t]) - p_i)
+ *                                  - grad_entropy[t] * p_i (log p_i + entropy[t]))
+ * in fp32, one rounding to grad_logits_type.
+ *   lse        device, fp32[T], token_logprobs'
+ *   entropy    device, fp32[T], token_logprobs'; needed with grad_entropy
+ *   grad_logprob, grad_entropy  device, fp32[T]; NULL for 0
+ *   grad_logits  device, [T][ld_grad_logits] of grad_logits_type; columns from V on are
+ *              not written; may be logits itself (same type size and stride),
+ *              must not overlap it otherwise.  Rows that lie in their
+ *              128-byte lines as logits' do take the vectorised path
+ * Rows that are padding, whose gradients are both 0 (an id outside [0, V) makes
+ * grad_logprob 0) or whose lse is -Inf are not read and give zeros.
+ * Otherwise as token_logprobs.
+ */
+int token_logprobs_grad(const void* logits, int32_t logits_type,
+                        int64_t ld_logits, const void* ids, int32_t id_bytes,
+                        int64_t T, int64_t V, float scale, int64_t padding_idx,
+                        const float* lse, const float* entropy,
+                        const float* grad_logprob, const float* grad_entropy,
+                        void* grad_logits, int32_t grad_logits_type,
+                        int64_t ld_grad_logits, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/* Workspace bytes for distill_loss (a status block). */
+size_t distill_loss_workspace_bytes(void);
+
+/*
+ * Distillation from a teacher's top logits: a (ids, logits) set for each row, as
+ * token_logprobs' top_ids and top_logprobs give it.  With
+ * q = softmax(scale * teacher_logits[t]) over its K entries and
+ * p = softmax(scale * logits[t]) over all V tokens (sums in fp32):
+ *     loss[t]           = weight[t] * sum_k q_k (log q_k - log p_{teacher_ids[t][k]})
+ *     grad_logits[t][i] = weight[t] * scale * (p_i - sum of q_k with id i)
+ * (the gradient of the sum of loss: a temperature's square and a mean's divisor
+ * belong into weight).
+ *   teacher_ids     device, int32 or int64 [T][K]; a negative id is an empty entry; an
+ *                   id may occur more than once
+ *   teacher_logits  device, [T][K] of teacher_type; -Inf has q = 0
+ *   K               0 .. 256
+ *   weight          device, fp32[T], or NULL for 1
+ *   loss            device, fp32[T], or NULL
+ *   grad_logits     device, [T][ld_grad_logits] of grad_logits_type, or NULL; as in
+ *                   token_logprobs_grad
+ *   ws              device workspace of >= distill_loss_workspace_bytes()
+ * Rows whose weight is 0 or that have no entry above -Inf give loss 0 and zeros;
+ * those of weight 0 are not read.  An id >= V is an empty entry and gives
+ * TOPK_EF_ERR_BAD_INPUT through topk_ef_last_device_status(ws).
+ * Infinite and NaN logits, sizes, scale and errors as in token_logprobs; a teacher's
+ * token at -Inf makes the loss +Inf.
+ */
+int distill_loss(const void* logits, int32_t logits_type, int64_t ld_logits,
+                 const void* teacher_ids, int32_t id_bytes,
+                 const void* teacher_logits, int32_t teacher_type, int64_t T,
+                 int64_t V, int32_t K, float scale, const float* weight,
+                 float* loss, void* grad_logits, int32_t grad_logits_type,
+                 int64_t ld_grad_logits, void* ws, size_t ws_bytes,
+                 void* stream);
 
 /* Synchronises `stream` and returns the device-side status of the last call
    that used `ws`: TOPK_EF_OK, TOPK_EF_ERR_DEVICE_TIMEOUT,

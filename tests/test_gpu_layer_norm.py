@@ -201,6 +201,7 @@ def _run_gradient(T, D, xt, dt, wt, gt, acc=False):
     old = (gw.clone(), gb.clone()) if acc else None
     ws = torch.full((ef.layer_norm_grad_workspace_bytes(T, D),), 0xFF, dtype=torch.uint8, device="cuda")
     got = ef.layer_norm_grad(dy, x, mean, rstd, w, accumulate=acc, grad_weight=gw, grad_bias=gb, ws=ws)
+    assert ef.topk_ef_last_device_status(ws) == 0
     _check_gradient(dy, x, mean, rstd, w, got, old)
     if not acc:
         again = ef.layer_norm_grad(dy, x, mean, rstd, w, out_dtype=TYPES[gt])
