@@ -5,9 +5,9 @@
 // s = sum 2^(c z_i - m), u = sum 2^(c z_i - m) (c z_i - m), so that
 //     log p_i = ln2 (c z_i - m - log2 s),   entropy = ln2 (log2 s - u / s),
 //     log of the sum = ln2 m + ln s.
-// m is a whole number near the largest c z: each thread raises its own when a group of
-// values passes it by 2^RAISE, and a change of m scales s by an exact power of two.
-// One fma and one ex2 a value; the rest rides on 32-byte groups.
+// m is the largest c z rounded up to a whole number: each thread raises its own when a
+// group of values passes it, and a change of m scales s by an exact power of two.
+// One ex2 a value and one packed fma two; the maxima take two values an instruction.
 //
 // Values below -2^17 / c are left out at first: if the row's m ends above -2^16, their p
 // is 0.  If m ends past +-2^16, where c z - m would lose bits, or nothing is left, the
@@ -34,7 +34,6 @@ namespace tke {
 constexpr int LG_THREADS = 256, LG_WARPS = LG_THREADS / 32;
 constexpr int LG_LINE = 128;               // bytes of a line (a group of the top selection)
 constexpr int LG_FLIGHT = 4;               // 32-byte chunks that a thread loads at once
-constexpr float LG_RAISE = 8.0f;
 constexpr float LG_START = -3e38f;         // m before any value
 constexpr float LG_FAR = 65536.0f;         // most |m| whose differences are exact enough
 constexpr float LN2 = 0.693147180559945309f, LOG2E = 1.44269504088896341f;
@@ -96,6 +95,19 @@ __device__ __forceinline__ void load_chunk(const LineRow<T>& r, int32_t j, Chunk
             e[i] = p + i >= r.lead && p + i < r.end ? r.line[p + i] : from_f32<T>(-CUDART_INF_F);
     }
 }
+// A chunk of the result at position pos of rows that lie like row (out = row - lead).
+template <typename T, typename TO>
+__device__ __forceinline__ void store_chunk(const LineRow<T>& row, TO* out, int32_t pos,
+                                            const Chunk<TO>& o) {
+    if (pos >= row.lead && pos + CHUNK<T> <= row.end) {
+        store32b(out + pos, o.q);
+    } else {
+        const TO* x = reinterpret_cast<const TO*>(o.q);
+#pragma unroll
+        for (int i = 0; i < CHUNK<T>; ++i)
+            if (pos + i >= row.lead && pos + i < row.end) out[pos + i] = x[i];
+    }
+}
 template <typename T>
 __device__ __forceinline__ void no_chunk(Chunk<T>& c) {
     T* e = reinterpret_cast<T*>(c.q);
@@ -107,32 +119,143 @@ struct Soft {
     float m, s, u;
 };
 
+// Two values a register pair, two values an instruction.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 parts(f32x2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 ex2_2(f32x2 a) {
+    const float2 v = parts(a);
+    return pair(ex2(v.x), ex2(v.y));
+}
+
+// The two elements of word i of a chunk (fp32: elements 2 i and 2 i + 1).
+__device__ __forceinline__ f32x2 widen(__nv_bfloat162 w) {
+    const uint32_t b = *reinterpret_cast<const uint32_t*>(&w);
+    return pair(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u));
+}
+__device__ __forceinline__ f32x2 widen(__half2 w) {
+    const float2 v = __half22float2(w);
+    return pair(v.x, v.y);
+}
+// ... and packs them again.
+__device__ __forceinline__ uint32_t narrow(f32x2 a, __nv_bfloat16) {
+    const float2 v = parts(a);
+    const __nv_bfloat162 w = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&w);
+}
+__device__ __forceinline__ uint32_t narrow(f32x2 a, __half) {
+    const float2 v = parts(a);
+    const __half2 w = __floats2half2_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&w);
+}
+template <typename T>
+__device__ __forceinline__ void put_pair(Chunk<T>& q, int i, f32x2 a) {
+    if constexpr (sizeof(T) == 4) {
+        reinterpret_cast<f32x2*>(q.q)[i] = a;
+    } else {
+        reinterpret_cast<uint32_t*>(q.q)[i] = narrow(a, T{});
+    }
+}
+template <typename T> struct Twin;
+template <> struct Twin<__nv_bfloat16> { typedef __nv_bfloat162 type; static constexpr bool bf16 = true; };
+template <> struct Twin<__half> { typedef __half2 type; static constexpr bool bf16 = false; };
+
+// The pairs of a chunk, not below `low` (NaN stays), and its largest value (of what was
+// there; NaN if there is one).
+template <typename T>
+struct Pairs {
+    typedef typename Twin<T>::type T2;
+    static __device__ __forceinline__ float largest(const Chunk<T>& q) {
+        const T2* w = reinterpret_cast<const T2*>(q.q);
+        T2 m = __hmax2_nan(w[0], w[1]);
+#pragma unroll
+        for (int i = 2; i < 8; ++i) m = __hmax2_nan(m, w[i]);
+        const float2 v = parts(widen(m));
+        return max_nan(v.x, v.y);
+    }
+    // (bf16 holds `low` near enough: m is at most 2^16, so it is off by 256 / c at most;
+    // fp16 may not reach it)
+    template <bool CUT>
+    static __device__ __forceinline__ f32x2 get(const Chunk<T>& q, int i, float low) {
+        T2 w = reinterpret_cast<const T2*>(q.q)[i];
+        if (CUT && T2_IS_BF16) {
+            T2 l;
+            l.x = l.y = from_f32<T>(low);
+            w = __hmax2_nan(w, l);
+        }
+        const f32x2 v = widen(w);
+        if (!CUT || T2_IS_BF16) return v;
+        const float2 f = parts(v);
+        return pair(max_nan(f.x, low), max_nan(f.y, low));
+    }
+    static constexpr bool T2_IS_BF16 = Twin<T>::bf16;
+};
+template <>
+struct Pairs<float> {
+    static __device__ __forceinline__ float largest(const Chunk<float>& q) {
+        float m = q.get(0);
+#pragma unroll
+        for (int i = 1; i < 8; ++i) m = max_nan(m, q.get(i));
+        return m;
+    }
+    template <bool CUT>
+    static __device__ __forceinline__ f32x2 get(const Chunk<float>& q, int i, float low) {
+        const float a = q.get(2 * i), b = q.get(2 * i + 1);
+        return CUT ? pair(max_nan(a, low), max_nan(b, low)) : pair(a, b);
+    }
+};
+
+// What a thread has summed: s and u in two halves each, and the value below which
+// 2^(c z - m) is 0 (fp32's smallest is 2^-126, and ex2 flushes; t must stay finite in u).
+struct Running {
+    float m, low;
+    f32x2 s, u;
+};
+constexpr float LG_BELOW = 400.0f;
+
 // Adds a chunk; returns its largest value (NaN if it holds one).
 template <typename T, bool ENTROPY>
-__device__ __forceinline__ float add_chunk(const Chunk<T>& q, Soft& a, float c) {
-    float v[CHUNK<T>];
-#pragma unroll
-    for (int i = 0; i < CHUNK<T>; ++i) v[i] = q.get(i);
-    float top = v[0];
-#pragma unroll
-    for (int i = 1; i < CHUNK<T>; ++i) top = max_nan(top, v[i]);
-    const float reach = top * c;
+__device__ __forceinline__ float add_chunk(const Chunk<T>& q, Running& a, float c, float inv_c) {
+    const float top = Pairs<T>::largest(q), reach = top * c;
     if (reach < -2.0f * LG_FAR) return top;
-    if (!(reach <= a.m + LG_RAISE)) {
+    if (!(reach <= a.m)) {
         const float m = ceilf(reach), f = ex2(a.m - m);
-        if (ENTROPY) a.u = fmaf(a.m - m, a.s, a.u) * f;
-        a.s *= f;
+        const f32x2 ff = pair(f, f);
+        if (ENTROPY) a.u = mul2(fma2(pair(a.m - m, a.m - m), a.s, a.u), ff);
+        a.s = mul2(a.s, ff);
         a.m = m;
+        a.low = (m - LG_BELOW) * inv_c;
     }
-    float s[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};
+    const f32x2 cc = pair(c, c), mm = pair(-a.m, -a.m);
 #pragma unroll
-    for (int i = 0; i < CHUNK<T>; ++i) {
-        const float t = fmaf(v[i], c, -a.m), e = ex2(t);
-        s[i & 1] += e;
-        if (ENTROPY) u[i & 1] = fmaf(e, fmaxf(t, -1e4f), u[i & 1]);      // (e is 0 there)
+    for (int i = 0; i < CHUNK<T> / 2; ++i) {
+        const f32x2 t = fma2(Pairs<T>::template get<ENTROPY>(q, i, a.low), cc, mm), e = ex2_2(t);
+        a.s = add2(a.s, e);
+        if (ENTROPY) a.u = fma2(e, t, a.u);
     }
-    a.s += s[0] + s[1];
-    if (ENTROPY) a.u += u[0] + u[1];
     return top;
 }
 
@@ -279,19 +402,22 @@ __device__ __forceinline__ Soft far_row(const LineRow<T>& row, int32_t line0, in
 }
 
 // The softmax of a row, of which a block takes lines [line0, line1); TOP: the
-// largest key of each of them in keys[line].
+// largest value of each of them in tops[line].
 template <typename T, bool ENTROPY, bool TOP>
 __device__ __forceinline__ RowSoft row_softmax(const LineRow<T>& row, int32_t line0, int32_t line1,
-                                               float c, int blocks, Soft* s_soft, uint32_t* keys) {
-    Soft a = {LG_START, 0.0f, 0.0f};
+                                               float c, int blocks, Soft* s_soft, float* tops) {
+    Running run = {LG_START, LG_START, 0, 0};
+    const float inv_c = 1.0f / c;
     for_chunks(row, line0, line1, [&](const Chunk<T>& q, int32_t j, bool mine) {
-        float top = add_chunk<T, ENTROPY>(q, a, c);
+        float top = add_chunk<T, ENTROPY>(q, run, c, inv_c);
         if (TOP) {
             top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            if ((threadIdx.x & 3) == 0 && mine) keys[j >> 2] = order_key(top);
+            if ((threadIdx.x & 3) == 0 && mine) tops[j >> 2] = top;
         }
     });
+    const float2 s = parts(run.s), u = parts(run.u);
+    Soft a = {run.m, s.x + s.y, u.x + u.y};
     a = row_join(a, blocks, s_soft);
     RowSoft r;
     r.far = a.s == 0.0f || !(fabsf(a.m) <= LG_FAR) || a.s != a.s;
@@ -364,28 +490,62 @@ __device__ __forceinline__ uint32_t block_threshold(uint32_t want, uint32_t* s, 
     return k;
 }
 
-constexpr int TL_LIST = 512;               // candidates that are ranked by comparison
+constexpr int TL_LIST = 512;               // lines that are read again; candidates that are ranked
+constexpr int TL_BINS = 512;               // 32 an octave of 1 + m - c z
 
 struct TopShared {
+    uint32_t hist[TL_BINS];
+    uint32_t lines, n;                     // lengths of the lists
     uint32_t count[2 * LG_WARPS];
     uint32_t scan[33];
-    uint32_t line[TL_MAX_TOP];
+    uint32_t line[TL_LIST];
     unsigned long long list[TL_LIST];      // key, then the lower index first
 };
 
-// The top K of the row by (value descending, index ascending), one block.
-//
-// The K-th largest of the lines' largest values, t, is at most the K-th largest
-// value; the lines above t and the first of those that equal it, K in all,
-// hold every element above t and the first ones at t.  So K lines are read again, and
-// what reaches t in them, hardly more than K values unless they are ordered, is
-// ranked by comparing each with each.  The time does not depend on the order of the row.
+// 1 + m - c z, at least 1: falls as z grows, and its bits count bins.
+__device__ __forceinline__ float depth(float z, float c, float m) {
+    return fmaxf(fmaf(-z, c, m), 0.0f) + 1.0f;
+}
+__device__ __forceinline__ uint32_t depth_bin(float d) {
+    return min((__float_as_uint(d) - 0x3F800000u) >> 18, (uint32_t)TL_BINS - 1);
+}
+
+// The first bin up to which the histogram holds `want` (every warp finds it), and how many.
+__device__ __forceinline__ uint32_t bin_of(const uint32_t* hist, uint32_t want, uint32_t& upto) {
+    constexpr int EACH = TL_BINS / 32;
+    const uint32_t lane = lane_id();
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) n += hist[lane * EACH + ((i + lane) & (EACH - 1))];
+    const uint32_t incl = warp_incl_scan(n);
+    const int src = __ffs(__ballot_sync(0xFFFFFFFFu, incl >= want)) - 1;
+    const uint32_t run = __shfl_sync(0xFFFFFFFFu, incl - n, src);
+    const uint32_t v = lane < EACH ? hist[src * EACH + lane] : 0u;
+    const uint32_t in2 = run + warp_incl_scan(v);
+    const int at = __ffs(__ballot_sync(0xFFFFFFFFu, in2 >= want)) - 1;
+    upto = __shfl_sync(0xFFFFFFFFu, in2, at);
+    return (uint32_t)(src * EACH + at);
+}
+
+// Adds i to a list in shared memory, for the lanes that want to.
+__device__ __forceinline__ uint32_t slot(uint32_t* n, bool want) {
+    const uint32_t who = __ballot_sync(0xFFFFFFFFu, want);
+    uint32_t first = 0;
+    if (lane_id() == 0 && who) first = atomicAdd(n, (uint32_t)__popc(who));
+    return __shfl_sync(0xFFFFFFFFu, first, 0) + __popc(who & ((1u << lane_id()) - 1));
+}
+
+// The lists by exact counts, where the bins hold too many: the K-th largest of the lines'
+// largest values, t; the lines above it and the first of those at it; of their
+// elements the ones above the K-th largest of them and the first of those at it.
 template <typename T>
-__device__ void select_top(const LogprobParams& p, const LineRow<T>& row, int64_t r,
-                           const uint32_t* keys, TopShared& S, const RowSoft& soft) {
+__device__ __forceinline__ void list_exactly(const LineRow<T>& row, int K, const float* tops,
+                                          TopShared& S) {
     constexpr int LOW = sizeof(T) == 4 ? 0 : 13;       // bf16 keys end 16 bits up, fp16's 13
+    // (keys whose low bits are set, a negative value's, compare as the value they stand for)
+    constexpr uint32_t mask = ~((1u << LOW) - 1);
     const int tid = (int)threadIdx.x;
-    const int lines = row.lines(), K = p.top, want = min(K, lines);
+    const int lines = row.lines(), want = min(K, lines);
     const int per = (lines + LG_THREADS - 1) / LG_THREADS;
     // the thread's lines are neighbours, so that a scan over threads is one over lines
     const int l0 = min(lines, tid * per), l1 = min(lines, l0 + per);
@@ -393,41 +553,38 @@ __device__ void select_top(const LogprobParams& p, const LineRow<T>& row, int64_
     if (lines > K)
         t = block_threshold<LOW>((uint32_t)K, S.count, [&](uint32_t k) {
             uint32_t n = 0;
-            for (int l = l0; l < l1; ++l) n += keys[l] >= k;
+            for (int l = tid; l < lines; l += LG_THREADS) n += order_key(tops[l]) >= k;
             return n;
         });
-    // (keys whose low bits are set, a negative value's, compare as the value they stand for)
-    const uint32_t mask = LOW ? ~((1u << LOW) - 1) : 0xFFFFFFFFu;
-    uint32_t above = 0, equal = 0, all_above;
+    uint32_t above = 0, equal = 0;
     for (int l = l0; l < l1; ++l) {
-        const uint32_t k = keys[l] & mask;
+        const uint32_t k = order_key(tops[l]) & mask;
         above += k > t;
         equal += k == t;
     }
     uint32_t tot;
     const uint32_t before = block_excl_scan(above << 16 | equal, S.scan, &tot);
-    all_above = tot >> 16;
     {
-        const uint32_t quota = (uint32_t)want - all_above;
+        const uint32_t quota = (uint32_t)want - (tot >> 16);
         uint32_t a = before >> 16, e = before & 0xFFFF;
         for (int l = l0; l < l1; ++l) {
-            const uint32_t k = keys[l] & mask;
+            const uint32_t k = order_key(tops[l]) & mask;
             if (k > t || (k == t && e < quota)) S.line[a + min(e, quota)] = (uint32_t)l;
             a += k > t;
             e += k == t;
         }
     }
     __syncthreads();
-    // candidates, in order: the thread's chunks are neighbours of the lines' list
+    // their elements, in order: the thread's chunks are neighbours too
     constexpr int MOST = TL_MAX_TOP * 4 / LG_THREADS;
     const int chunks = want * 4, each = (chunks + LG_THREADS - 1) / LG_THREADS;
     Chunk<T> q[MOST];
     int32_t at[MOST] = {};
-    uint32_t n = 0;
     auto key_of_pos = [&](int i, int e) -> uint32_t {      // 0: not an element
         const int32_t pos = at[i] + e;
         return pos >= row.lead && pos < row.end ? order_key(q[i].get(e)) : 0u;
     };
+    uint32_t n = 0;
 #pragma unroll
     for (int i = 0; i < MOST; ++i) {
         const int j = tid * each + i;
@@ -440,40 +597,30 @@ __device__ void select_top(const LogprobParams& p, const LineRow<T>& row, int64_
             no_chunk(q[i]);
         }
 #pragma unroll
-        for (int e = 0; e < CHUNK<T>; ++e) {
-            const uint32_t k = key_of_pos(i, e);
-            n += k != 0 && (k & mask) >= t;
-        }
+        for (int e = 0; e < CHUNK<T>; ++e) n += key_of_pos(i, e) != 0;
     }
-    uint32_t first = block_excl_scan(n, S.scan, &tot), cut = t, quota = 0xFFFFFFFFu;
-    const uint32_t need = min((uint32_t)K, tot);
-    if (tot > TL_LIST) {
-        // many at or above t: exactly those that belong to the top K
-        cut = block_threshold<LOW>(need, S.count, [&](uint32_t k) {
-            uint32_t c = 0;
-#pragma unroll
-            for (int i = 0; i < MOST; ++i)
-#pragma unroll
-                for (int e = 0; e < CHUNK<T>; ++e) c += key_of_pos(i, e) >= k;
-            return c;
-        });
-        above = equal = 0;
+    const uint32_t need = min((uint32_t)K, block_sum(n, S.scan));
+    const uint32_t cut = block_threshold<LOW>(need, S.count, [&](uint32_t k) {
+        uint32_t c = 0;
 #pragma unroll
         for (int i = 0; i < MOST; ++i)
 #pragma unroll
-            for (int e = 0; e < CHUNK<T>; ++e) {
-                const uint32_t k = key_of_pos(i, e);
-                above += k != 0 && (k & mask) > cut;
-                equal += k != 0 && (k & mask) == cut;
-            }
-        const uint32_t b = block_excl_scan(above << 16 | equal, S.scan, &tot);
-        quota = need - (tot >> 16);
-        n = b & 0xFFFF;                                     // equal ones before the thread's
-        first = (b >> 16) + min(n, quota);
-        tot = need;
-    } else {
-        n = 0;
-    }
+            for (int e = 0; e < CHUNK<T>; ++e) c += key_of_pos(i, e) >= k;
+        return c;
+    });
+    above = equal = 0;
+#pragma unroll
+    for (int i = 0; i < MOST; ++i)
+#pragma unroll
+        for (int e = 0; e < CHUNK<T>; ++e) {
+            const uint32_t k = key_of_pos(i, e);
+            above += k != 0 && (k & mask) > cut;
+            equal += k != 0 && (k & mask) == cut;
+        }
+    const uint32_t b = block_excl_scan(above << 16 | equal, S.scan, &tot);
+    const uint32_t quota = need - (tot >> 16);
+    n = b & 0xFFFF;                                         // equal ones before the thread's
+    uint32_t first = (b >> 16) + min(n, quota);
 #pragma unroll
     for (int i = 0; i < MOST; ++i)
 #pragma unroll
@@ -484,11 +631,91 @@ __device__ void select_top(const LogprobParams& p, const LineRow<T>& row, int64_
                 S.list[first++] = (unsigned long long)k << 32 | (uint32_t)(row.end - 1 - (at[i] + e));
             n += eq;
         }
+    if (tid == 0) S.n = need;
     __syncthreads();
-    for (uint32_t i = tid; i < tot; i += LG_THREADS) {
+}
+
+// The top K of the row by (value descending, index ascending), one block.
+//
+// The K-th largest value is at least the K-th largest of the lines' largest ones.  A
+// histogram of those by their distance from the row's largest gives a bin that holds it;
+// the lines up to that bin are read again, and their elements up to it, hardly more than
+// K, are ranked by comparing each with each.  (Exact counts over 16 or 32 bits of the
+// lines' keys instead of bins: 380 us more for 4,096 rows of 131,072 bf16.)
+template <typename T>
+__device__ __forceinline__ void select_top(const LogprobParams& p, const LineRow<T>& row, int64_t r,
+                                           const float* tops, TopShared& S, const RowSoft& soft) {
+    const int tid = (int)threadIdx.x;
+    const int lines = row.lines(), K = p.top;
+    const float c = p.c, m = soft.m;
+    bool exactly = soft.far;                   // (distances mean nothing)
+    if (!exactly) {
+        for (int i = tid; i < TL_BINS; i += LG_THREADS) S.hist[i] = 0;
+        if (tid == 0) S.lines = S.n = 0;
+        __syncthreads();
+        const bool some = lines > K;
+        uint32_t bin = TL_BINS - 1, upto = 0;
+        if (some) {
+            for (int l = tid; l < lines; l += LG_THREADS)
+                atomicAdd(&S.hist[depth_bin(depth(tops[l], c, m))], 1u);
+        } else if (p.V > TL_LIST) {
+            for (int j = tid; j < lines * 4; j += LG_THREADS) {
+                Chunk<T> q;
+                load_chunk(row, j, q);
+#pragma unroll
+                for (int e = 0; e < CHUNK<T>; ++e) {
+                    const int32_t pos = j * CHUNK<T> + e;
+                    if (pos >= row.lead && pos < row.end)
+                        atomicAdd(&S.hist[depth_bin(depth(q.get(e), c, m))], 1u);
+                }
+            }
+        }
+        if (some || p.V > TL_LIST) {
+            __syncthreads();
+            bin = bin_of(S.hist, (uint32_t)min((int64_t)K, p.V), upto);
+            exactly = upto > TL_LIST;
+        }
+        if (!exactly) {
+            // (the last bin has no end)
+            const float edge = bin == TL_BINS - 1 ? CUDART_INF_F
+                                                  : __uint_as_float(0x3F800000u + ((bin + 1) << 18));
+            auto within = [&](float z) { return depth(z, c, m) < edge || bin == TL_BINS - 1; };
+            if (some) {
+                for (int l0 = 0; l0 < lines; l0 += LG_THREADS) {
+                    const int l = l0 + tid;
+                    const bool in = l < lines && within(tops[l]);
+                    const uint32_t at = slot(&S.lines, in);
+                    if (in) S.line[at] = (uint32_t)l;
+                }
+                __syncthreads();
+            }
+            const int chunks = (some ? (int)S.lines : lines) * 4;
+            for (int j = tid; j < chunks; j += LG_THREADS) {
+                const int32_t chunk = (some ? (int32_t)S.line[j >> 2] : j >> 2) * 4 + (j & 3);
+                Chunk<T> q;
+                load_chunk(row, chunk, q);
+#pragma unroll
+                for (int e = 0; e < CHUNK<T>; ++e) {
+                    const int32_t pos = chunk * CHUNK<T> + e;
+                    const float z = q.get(e);
+                    if (!within(z) || pos < row.lead || pos >= row.end) continue;
+                    const uint32_t at = atomicAdd(&S.n, 1u);
+                    if (at < TL_LIST)
+                        S.list[at] =
+                            (unsigned long long)order_key(z) << 32 | (uint32_t)(row.end - 1 - pos);
+                }
+            }
+            __syncthreads();
+            exactly = S.n > TL_LIST;
+            __syncthreads();
+        }
+    }
+    if (exactly) list_exactly(row, K, tops, S);
+    const uint32_t n = S.n;
+    for (uint32_t i = tid; i < n; i += LG_THREADS) {
         const unsigned long long mine = S.list[i];
         uint32_t rank = 0;
-        for (uint32_t j = 0; j < tot; ++j) rank += S.list[j] > mine;
+        for (uint32_t j = 0; j < n; ++j) rank += S.list[j] > mine;
         if (rank < (uint32_t)K) {
             const float z = key_value((uint32_t)(mine >> 32));
             const int32_t id = row.end - 1 - (int32_t)(uint32_t)mine - row.lead;
@@ -503,8 +730,8 @@ __device__ void select_top(const LogprobParams& p, const LineRow<T>& row, int64_
 }
 
 template <typename T, bool ENTROPY, bool TOP>
-__global__ void __launch_bounds__(LG_THREADS) logprob_kernel(const LogprobParams p) {
-    extern __shared__ uint32_t s_keys[];               // TOP: [blocks][lines]
+__global__ void __launch_bounds__(LG_THREADS, TOP ? 3 : 4) logprob_kernel(const LogprobParams p) {
+    extern __shared__ float s_tops[];                  // TOP: [lines of the row]
     __shared__ Soft s_soft[LG_WARPS + 1];
     __shared__ TopShared S;
     pdl_launch();
@@ -545,24 +772,24 @@ __global__ void __launch_bounds__(LG_THREADS) logprob_kernel(const LogprobParams
     const int32_t share = (lines + p.blocks - 1) / p.blocks;
     const int32_t line0 = min(lines, rank * share), line1 = min(lines, line0 + share);
     const RowSoft a =
-        row_softmax<T, ENTROPY, TOP>(row, line0, line1, p.c, p.blocks, s_soft, s_keys);
+        row_softmax<T, ENTROPY, TOP>(row, line0, line1, p.c, p.blocks, s_soft, s_tops);
     if (rank == 0 && tid == 0) {
         if (p.logprob) p.logprob[r] = ok ? a.log_prob(zt, p.c, p.scale) : 0.0f;
         if (ENTROPY && p.entropy) p.entropy[r] = a.entropy();
         if (p.lse) p.lse[r] = a.log_sum(p.scale);
     }
     if (TOP && rank == 0) {
-        // the other blocks' keys
+        // the other blocks' lines
         if (p.blocks > 1)
             for (int32_t l = line1 + tid; l < lines; l += LG_THREADS) {
-                uint32_t k;
-                asm volatile("ld.shared::cluster.u32 %0, [%1];"
-                             : "=r"(k)
-                             : "r"(in_block(smem_u32(s_keys + l), (uint32_t)(l / share))));
-                s_keys[l] = k;
+                float k;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                             : "=f"(k)
+                             : "r"(in_block(smem_u32(s_tops + l), (uint32_t)(l / share))));
+                s_tops[l] = k;
             }
         __syncthreads();
-        select_top<T>(p, row, r, s_keys, S, a);
+        select_top<T>(p, row, r, s_tops, S, a);
     }
     if (p.blocks > 1) cluster_sync();      // no block leaves while its memory is read
 }
@@ -588,7 +815,7 @@ constexpr int LD_THREADS = 128;
 
 // dz_i = scale (g (delta_i,id - p_i) - h p_i (log p_i + entropy)).  SAME: z's and dz's
 // rows lie alike in their lines.
-template <typename T, typename TO, bool SAME>
+template <typename T, typename TO, bool SAME, bool ENTROPY>
 __global__ void __launch_bounds__(LD_THREADS) logprob_grad_kernel(const LogprobGradParams p) {
     pdl_launch();
     pdl_wait();
@@ -610,19 +837,24 @@ __global__ void __launch_bounds__(LD_THREADS) logprob_grad_kernel(const LogprobG
             atomicOr(&p.ctrl->status, ST_BAD_INPUT);
     }
     const float lse = p.lse[r];
-    const float g = ok && p.g ? p.scale * p.g[r] : 0.0f, h = p.h ? p.scale * p.h[r] : 0.0f;
-    const float H = p.h ? p.entropy[r] : 0.0f;
+    const float g = ok && p.g ? p.scale * p.g[r] : 0.0f;
+    const float h = ENTROPY ? p.scale * p.h[r] : 0.0f, H = ENTROPY ? p.entropy[r] : 0.0f;
     skip = skip || (g == 0.0f && h == 0.0f) || lse == -CUDART_INF_F;
-    // -(p (g + h (log p + H))), and g at the token
-    auto value = [&](float v, int32_t i) {
-        const float t = max_nan(fmaf(v, p.scale, -lse), -1e4f), e = ex2(t * LOG2E);
-        const float k = fmaf(h, t + H, g);
-        return fmaf(-e, k, i == (int32_t)id ? g : 0.0f);
+    // -p (g + h (log p + H)), and g more at the token
+    const float k0 = fmaf(-h, H, -g);
+    auto values = [&](f32x2 v) {
+        f32x2 t = fma2(v, pair(p.scale, p.scale), pair(-lse, -lse));
+        if (ENTROPY) {                                     // (times e, which is 0 there)
+            const float2 f = parts(t);
+            t = pair(max_nan(f.x, -1e4f), max_nan(f.y, -1e4f));
+        }
+        const f32x2 e = ex2_2(mul2(t, pair(LOG2E, LOG2E)));
+        return mul2(e, ENTROPY ? fma2(t, pair(-h, -h), pair(k0, k0)) : pair(-g, -g));
     };
     if (SAME) {
         const LineRow<T> row(z, p.V);
         TO* out = dz - row.lead;
-        const int32_t end = row.lines() * 4;
+        const int32_t end = row.lines() * 4, token = ok ? (int32_t)id + row.lead : -1;
         for (int32_t j0 = part * LD_THREADS * LG_FLIGHT; j0 < end;
              j0 += p.parts * LD_THREADS * LG_FLIGHT) {
             Chunk<T> q[LG_FLIGHT];
@@ -637,23 +869,30 @@ __global__ void __launch_bounds__(LD_THREADS) logprob_grad_kernel(const LogprobG
                 if (j >= end) continue;
                 const int32_t pos = j * CHUNK<T>;
                 Chunk<TO> o;
-                TO* x = reinterpret_cast<TO*>(o.q);
-#pragma unroll
-                for (int i = 0; i < CHUNK<T>; ++i)
-                    x[i] = from_f32<TO>(skip ? 0.0f : value(q[k].get(i), pos + i - row.lead));
-                if (pos >= row.lead && pos + CHUNK<T> <= row.end) {
-                    store32b(out + pos, o.q);
+                if (skip) {
+                    o.q[0] = o.q[1] = make_uint4(0, 0, 0, 0);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < CHUNK<T>; ++i)
-                        if (pos + i >= row.lead && pos + i < row.end) out[pos + i] = x[i];
+                    for (int i = 0; i < CHUNK<T> / 2; ++i) {
+                        f32x2 v = values(Pairs<T>::template get<false>(q[k], i, 0.0f));
+                        if (token >> 1 == (pos >> 1) + i && token >= 0)
+                            v = add2(v, pair(token & 1 ? 0.0f : g, token & 1 ? g : 0.0f));
+                        put_pair(o, i, v);
+                    }
                 }
+                store_chunk(row, out, pos, o);
             }
         }
     } else {
         for (int32_t i = part * LD_THREADS + (int32_t)threadIdx.x; i < (int32_t)p.V;
-             i += p.parts * LD_THREADS)
-            dz[i] = from_f32<TO>(skip ? 0.0f : value(to_f32(z[i]), i));
+             i += p.parts * LD_THREADS) {
+            float v = 0.0f;
+            if (!skip) {
+                v = parts(values(pair(to_f32(z[i]), 0.0f))).x;
+                if (ok && i == (int32_t)id) v += g;
+            }
+            dz[i] = from_f32<TO>(v);
+        }
     }
 }
 
@@ -694,7 +933,7 @@ __device__ __forceinline__ float teacher_at(const DistillParams& p, int64_t i) {
 // loss = weight sum_k q_k (log q_k - log p_{id_k}),  q = softmax(scale teacher);
 // dz = weight scale (p - q).  Thread k keeps the teacher's k-th entry.
 template <typename T, typename TO, bool SAME>
-__global__ void __launch_bounds__(LG_THREADS) distill_kernel(const DistillParams p) {
+__global__ void __launch_bounds__(LG_THREADS, 3) distill_kernel(const DistillParams p) {
     __shared__ Soft s_soft[LG_WARPS + 1];
     __shared__ float s_red[33];
     __shared__ int32_t s_id[DL_MAX_K];
@@ -756,7 +995,12 @@ __global__ void __launch_bounds__(LG_THREADS) distill_kernel(const DistillParams
     if (p.dz) {
         TO* dz = static_cast<TO*>(p.dz) + r * p.lddz;
         const float w = weight * p.scale, f = w * inv;
-        auto prob = [&](float v) { return a.prob(v, p.c); };
+        const f32x2 cc = pair(p.c, p.c), mm = pair(-a.m, -a.m), ff = pair(f, f);
+        auto probs = [&](f32x2 v) {                        // (times f)
+            if (!a.far) return mul2(ex2_2(fma2(v, cc, mm)), ff);
+            const float2 x = parts(v);
+            return pair(f * a.prob(x.x, p.c), f * a.prob(x.y, p.c));
+        };
         if (SAME) {
             TO* out = dz - row.lead;
             const int32_t end = line1 * 4;
@@ -771,26 +1015,22 @@ __global__ void __launch_bounds__(LG_THREADS) distill_kernel(const DistillParams
                 for (int k = 0; k < LG_FLIGHT; ++k) {
                     const int32_t j = j0 + k * LG_THREADS + tid;
                     if (j >= end) continue;
-                    const int32_t pos = j * CHUNK<T>;
                     Chunk<TO> o;
-                    TO* x = reinterpret_cast<TO*>(o.q);
-#pragma unroll
-                    for (int i = 0; i < CHUNK<T>; ++i)
-                        x[i] = from_f32<TO>(skip ? 0.0f : f * prob(v[k].get(i)));
-                    if (pos >= row.lead && pos + CHUNK<T> <= row.end) {
-                        store32b(out + pos, o.q);
+                    if (skip) {
+                        o.q[0] = o.q[1] = make_uint4(0, 0, 0, 0);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < CHUNK<T>; ++i)
-                            if (pos + i >= row.lead && pos + i < row.end) out[pos + i] = x[i];
+                        for (int i = 0; i < CHUNK<T> / 2; ++i)
+                            put_pair(o, i, probs(Pairs<T>::template get<false>(v[k], i, 0.0f)));
                     }
+                    store_chunk(row, out, j * CHUNK<T>, o);
                 }
             }
         } else {
             const int32_t per = LG_LINE / (int)sizeof(T);
             const int32_t i1 = min(line1 * per, row.end) - row.lead;
             for (int32_t i = max(line0 * per - row.lead, 0) + tid; i < i1; i += LG_THREADS)
-                dz[i] = from_f32<TO>(skip ? 0.0f : f * prob(to_f32(z[i])));
+                dz[i] = from_f32<TO>(skip ? 0.0f : parts(probs(pair(to_f32(z[i]), 0.0f))).x);
         }
         if (!skip) {
             // the teacher's tokens: the first entry of each takes all of its q
@@ -804,7 +1044,7 @@ __global__ void __launch_bounds__(LG_THREADS) distill_kernel(const DistillParams
                         all += s_q[j];
                         first = first && j >= tid;
                     }
-                if (first) dz[id] = from_f32<TO>(w * (prob(zk) * inv - all));
+                if (first) dz[id] = from_f32<TO>(w * (a.prob(zk, p.c) * inv - all));
             }
         }
     }

@@ -195,8 +195,11 @@ int token_logprobs_grad(const void* logits, int32_t logits_type, int64_t ld_logi
             using TZ = decltype(t);
             using TO = decltype(to);
             if constexpr (sizeof(TZ) == sizeof(TO))
-                if (same) return launch_pdl(logprob_grad_kernel<TZ, TO, true>, grid, LD_THREADS, st, p);
-            return launch_pdl(logprob_grad_kernel<TZ, TO, false>, grid, LD_THREADS, st, p);
+                if (same)
+                    return p.h ? launch_pdl(logprob_grad_kernel<TZ, TO, true, true>, grid, LD_THREADS, st, p)
+                               : launch_pdl(logprob_grad_kernel<TZ, TO, true, false>, grid, LD_THREADS, st, p);
+            return p.h ? launch_pdl(logprob_grad_kernel<TZ, TO, false, true>, grid, LD_THREADS, st, p)
+                       : launch_pdl(logprob_grad_kernel<TZ, TO, false, false>, grid, LD_THREADS, st, p);
         });
     });
     trace_after(st);
@@ -242,6 +245,7 @@ int distill_loss(const void* logits, int32_t logits_type, int64_t ld_logits,
     p.teacher_type = teacher_type;
     p.K = K;
     p.blocks = row_blocks(T, most_lines(V, sz));
+    if (getenv("DLC")) p.blocks = atoi(getenv("DLC"));
     p.scan = T * std::max(K, 1) <= SCAN_IDS;
     p.scale = scale;
     p.c = (float)((double)scale * 1.4426950408889634);
