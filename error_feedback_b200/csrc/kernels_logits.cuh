@@ -16,8 +16,10 @@
 // -inf (a forbidden token) has p = 0 and counts nowhere.  NaN and +inf make the row
 // NaN.
 //
-// One thread-block cluster a row, each block an equal share of the row's 128-byte
-// lines: rows start anywhere, and whole lines are read as 32 bytes a thread.
+// A row is worked on by a team: a warp (rows of up to LG_SMALL lines: nothing but its own
+// latency counts, so many at once), or a block, or a cluster of blocks while there are few
+// rows, each block an equal share of the row's 128-byte lines.  Rows start anywhere; whole
+// lines are read as 32 bytes a thread.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -31,10 +33,10 @@
 
 namespace tke {
 
-constexpr int LG_THREADS = 256, LG_WARPS = LG_THREADS / 32;
+constexpr int LG_SMALL = 64;               // lines of a row that one warp takes
 constexpr int LG_LINE = 128;               // bytes of a line (a group of the top selection)
 constexpr int LG_FLIGHT = 4;               // 32-byte chunks that a thread loads at once
-constexpr float LG_START = -3e38f;         // m before any value
+constexpr float LG_START = -3.402823466e38f;     // m before any value
 constexpr float LG_FAR = 65536.0f;         // most |m| whose differences are exact enough
 constexpr float LN2 = 0.693147180559945309f, LOG2E = 1.44269504088896341f;
 constexpr float LN2_HI = 0.693145751953125f;         // 16 bits: times a whole m exact
@@ -56,6 +58,33 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 template <typename T>
 constexpr int CHUNK = 32 / (int)sizeof(T);         // elements of 32 bytes
+
+// W warps: a whole block, or each warp of a block of 8.
+template <int W>
+struct Team {
+    static constexpr int THREADS = W * 32;
+    static constexpr int BLOCK = W == 1 ? 256 : THREADS;
+    static constexpr int TEAMS = BLOCK / THREADS;
+    static __device__ __forceinline__ int thread() { return (int)(threadIdx.x % THREADS); }
+    static __device__ __forceinline__ int team() { return (int)(threadIdx.x / THREADS); }
+    static __device__ __forceinline__ void sync() {
+        if (W == 1) {
+            __syncwarp();
+        } else {
+            __syncthreads();
+        }
+    }
+    // Sums over the team; s: 33 words.
+    static __device__ __forceinline__ uint32_t excl_scan(uint32_t v, uint32_t* s, uint32_t* total) {
+        if (W > 1) return block_excl_scan(v, s, total);
+        const uint32_t incl = warp_incl_scan(v);
+        *total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+        return incl - v;
+    }
+    static __device__ __forceinline__ float sum(float v, float* s) {
+        return W > 1 ? block_sum(v, s) : warp_sum(v);
+    }
+};
 
 // A row's elements by position in the 128-byte lines that they lie in: position
 // `lead` holds the first.
@@ -259,20 +288,17 @@ __device__ __forceinline__ float add_chunk(const Chunk<T>& q, Running& a, float 
     return top;
 }
 
-__device__ __forceinline__ Soft join(const Soft& a, const Soft& b) {
-    const float m = fmaxf(a.m, b.m), fa = ex2(a.m - m), fb = ex2(b.m - m);
-    return {m, fmaf(a.s, fa, b.s * fb), fmaf(a.m - m, a.s, a.u) * fa + fmaf(b.m - m, b.s, b.u) * fb};
-}
-
+// The lanes' statistics, joined in every lane.
 __device__ __forceinline__ Soft warp_join(Soft a) {
+    float m = a.m;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Soft b;
-        b.m = __shfl_xor_sync(0xFFFFFFFFu, a.m, o);
-        b.s = __shfl_xor_sync(0xFFFFFFFFu, a.s, o);
-        b.u = __shfl_xor_sync(0xFFFFFFFFu, a.u, o);
-        a = join(a, b);
-    }
+    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const float f = ex2(a.m - m);
+    a.u = fmaf(a.m - m, a.s, a.u) * f;
+    a.s *= f;
+    a.m = m;
+    a.s = warp_sum(a.s);
+    a.u = warp_sum(a.u);
     return a;
 }
 
@@ -286,43 +312,52 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 
 // f(chunk, its number, whether it belongs to the block) for the chunks of lines
-// [line0, line1); every thread of a warp makes the same calls.
-template <typename T, typename F>
+// [line0, line1); every thread of a warp makes the same calls.  Batches that lie in the
+// row as a whole are loaded without a check of each chunk, which would take as many
+// instructions as the sums (7.3 instead of 5.5 an element).
+template <int W, int FLIGHT, typename T, typename F>
 __device__ __forceinline__ void for_chunks(const LineRow<T>& row, int32_t line0, int32_t line1, F f) {
+    constexpr int N = Team<W>::THREADS;
     const int32_t end = line1 * 4;
-    for (int32_t j0 = line0 * 4; j0 < end; j0 += LG_THREADS * LG_FLIGHT) {
-        Chunk<T> q[LG_FLIGHT];
+    const int32_t in0 = (row.lead + CHUNK<T> - 1) / CHUNK<T>, in1 = min(end, row.end / CHUNK<T>);
+#pragma unroll 1
+    for (int32_t j0 = line0 * 4; j0 < end; j0 += N * FLIGHT) {
+        Chunk<T> q[FLIGHT];
+        const int32_t j = j0 + Team<W>::thread();
+        if (j0 >= in0 && j0 + N * FLIGHT <= in1) {
 #pragma unroll
-        for (int k = 0; k < LG_FLIGHT; ++k) {
-            const int32_t j = j0 + k * LG_THREADS + (int32_t)threadIdx.x;
-            if (j < end) {
-                load_chunk(row, j, q[k]);
-            } else {
-                no_chunk(q[k]);
+            for (int k = 0; k < FLIGHT; ++k) load32b(row.line + (j + k * N) * CHUNK<T>, q[k].q);
+        } else {
+#pragma unroll
+            for (int k = 0; k < FLIGHT; ++k) {
+                if (j + k * N < end) {
+                    load_chunk(row, j + k * N, q[k]);
+                } else {
+                    no_chunk(q[k]);
+                }
             }
         }
 #pragma unroll
-        for (int k = 0; k < LG_FLIGHT; ++k) {
-            const int32_t j = j0 + k * LG_THREADS + (int32_t)threadIdx.x;
-            f(q[k], j, j < end);
-        }
+        for (int k = 0; k < FLIGHT; ++k) f(q[k], j + k * N, j + k * N < end);
     }
 }
 
-// The statistics of all the cluster's blocks, in every block (s_soft: LG_WARPS + 1
-// entries).  Also a barrier of the cluster.
+// The statistics of all threads of a row, in each of them (s_soft: W + 1 entries).  Also a
+// barrier of the team and cluster.
+template <int W>
 __device__ __forceinline__ Soft row_join(Soft a, int blocks, Soft* s_soft) {
     a = warp_join(a);
+    if (W == 1) return a;
     if (lane_id() == 0) s_soft[warp_id()] = a;
     __syncthreads();
     const Soft none = {LG_START, 0.0f, 0.0f};
-    a = warp_join(lane_id() < LG_WARPS ? s_soft[lane_id()] : none);
+    a = warp_join(lane_id() < W ? s_soft[lane_id()] : none);
     if (blocks == 1) return a;
-    if (threadIdx.x == 0) s_soft[LG_WARPS] = a;
+    if (threadIdx.x == 0) s_soft[W] = a;
     cluster_sync();
     a = none;
     if ((int)lane_id() < blocks) {
-        const uint32_t at = in_block(smem_u32(&s_soft[LG_WARPS]), lane_id());
+        const uint32_t at = in_block(smem_u32(&s_soft[W]), lane_id());
         asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(a.m) : "r"(at));
         asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(a.s) : "r"(at + 4));
         asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(a.u) : "r"(at + 8));
@@ -357,58 +392,59 @@ struct RowSoft {
 
 // The row again, with its largest value as the reference.  (Rare, and the same for all
 // blocks of the cluster.)
-template <typename T>
+template <int W, typename T>
 __device__ __forceinline__ Soft far_row(const LineRow<T>& row, int32_t line0, int32_t line1, float c,
-                                     int blocks, Soft* s_soft) {
+                                        int blocks, Soft* s_soft) {
     float top = -CUDART_INF_F;
-    for_chunks(row, line0, line1, [&](const Chunk<T>& q, int32_t, bool) {
+    for_chunks<W, 1>(row, line0, line1, [&](const Chunk<T>& q, int32_t, bool) {
 #pragma unroll
         for (int i = 0; i < CHUNK<T>; ++i) top = max_nan(top, q.get(i));
     });
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    if (blocks > 1) cluster_sync(); else __syncthreads();      // what s_soft held has been read
-    if (lane_id() == 0) s_soft[warp_id()].m = top;
-    __syncthreads();
-    top = s_soft[0].m;
-#pragma unroll
-    for (int i = 1; i < LG_WARPS; ++i) top = max_nan(top, s_soft[i].m);
-    if (blocks > 1) {
-        if (threadIdx.x == 0) s_soft[LG_WARPS].m = top;
-        cluster_sync();
-        if ((int)lane_id() < blocks) {
-            const uint32_t at = in_block(smem_u32(&s_soft[LG_WARPS]), lane_id());
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(top) : "r"(at));
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        cluster_sync();
-    } else {
-        __syncthreads();
-    }
+    // (as a sum of one term, whose reference it is)
+    if (blocks > 1) cluster_sync(); else Team<W>::sync();      // what s_soft held has been read
+    top = max_nan(row_join<W>({top, 0.0f, 0.0f}, blocks, s_soft).m, LG_START);     // (finite: -inf - top is -inf)
+    if (blocks > 1) cluster_sync(); else Team<W>::sync();
     Soft a = {0.0f, 0.0f, 0.0f};
-    if (top != -CUDART_INF_F)
-        for_chunks(row, line0, line1, [&](const Chunk<T>& q, int32_t, bool) {
+    for_chunks<W, 1>(row, line0, line1, [&](const Chunk<T>& q, int32_t, bool) {
 #pragma unroll
-            for (int i = 0; i < CHUNK<T>; ++i) {
-                const float t = c * (q.get(i) - top), e = ex2(t);
-                a.s += e;
-                a.u = fmaf(e, fmaxf(t, -1e4f), a.u);
-            }
-        });
-    a = row_join(a, blocks, s_soft);
+        for (int i = 0; i < CHUNK<T>; ++i) {
+            const float t = c * (q.get(i) - top), e = ex2(t);
+            a.s += e;
+            a.u = fmaf(e, fmaxf(t, -1e4f), a.u);
+        }
+    });
+    a = row_join<W>(a, blocks, s_soft);
     a.m = top;
     return a;
 }
 
+// Chunk j of the block's share in the stash; a warp's 16-byte accesses are consecutive.
+template <int W, typename T>
+__device__ __forceinline__ void put_stash(uint4* stash, int32_t j, const Chunk<T>& q) {
+    constexpr int N = Team<W>::THREADS;
+    uint4* at = stash + j / N * 2 * N + j % N;
+    at[0] = q.q[0];
+    at[N] = q.q[1];
+}
+template <int W, typename T>
+__device__ __forceinline__ void get_stash(const uint4* stash, int32_t j, Chunk<T>& q) {
+    constexpr int N = Team<W>::THREADS;
+    const uint4* at = stash + j / N * 2 * N + j % N;
+    q.q[0] = at[0];
+    q.q[1] = at[N];
+}
+
 // The softmax of a row, of which a block takes lines [line0, line1); TOP: the
-// largest value of each of them in tops[line].
-template <typename T, bool ENTROPY, bool TOP>
+// largest value of each of them in tops[line].  The first `keep` chunks stay in the stash,
+// each thread's where it alone reads them.
+template <int W, typename T, bool ENTROPY, bool TOP>
 __device__ __forceinline__ RowSoft row_softmax(const LineRow<T>& row, int32_t line0, int32_t line1,
-                                               float c, int blocks, Soft* s_soft, float* tops) {
+                                               float c, int blocks, Soft* s_soft, float* tops,
+                                               uint4* stash, int32_t keep) {
     Running run = {LG_START, LG_START, 0, 0};
     const float inv_c = 1.0f / c;
-    for_chunks(row, line0, line1, [&](const Chunk<T>& q, int32_t j, bool mine) {
+    for_chunks<W, LG_FLIGHT>(row, line0, line1, [&](const Chunk<T>& q, int32_t j, bool mine) {
+        if (mine && j - line0 * 4 < keep) put_stash<W>(stash, j - line0 * 4, q);
         float top = add_chunk<T, ENTROPY>(q, run, c, inv_c);
         if (TOP) {
             top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
@@ -418,10 +454,10 @@ __device__ __forceinline__ RowSoft row_softmax(const LineRow<T>& row, int32_t li
     });
     const float2 s = parts(run.s), u = parts(run.u);
     Soft a = {run.m, s.x + s.y, u.x + u.y};
-    a = row_join(a, blocks, s_soft);
+    a = row_join<W>(a, blocks, s_soft);
     RowSoft r;
     r.far = a.s == 0.0f || !(fabsf(a.m) <= LG_FAR) || a.s != a.s;
-    if (r.far) a = far_row(row, line0, line1, c, blocks, s_soft);
+    if (r.far) a = far_row<W>(row, line0, line1, c, blocks, s_soft);
     r.m = a.m;
     r.s = a.s;
     r.u = a.u;
@@ -442,7 +478,7 @@ struct LogprobParams {
     Ctrl* ctrl;
     int64_t T, V, ldz, padding;
     int32_t id64, top, blocks;     // blocks of a row's cluster
-    int32_t scan;                  // the last cluster checks the ids
+    int32_t scan;                  // the first cluster checks the ids
     float c, scale;
 };
 
@@ -465,42 +501,46 @@ __device__ __forceinline__ void scan_ids(const void* ids, int32_t id64, int64_t 
     }
 }
 
-// Sum of v over the block (every thread gets it); s: 2 x LG_WARPS words, `flip` the
-// half that the last call did not use.
-__device__ __forceinline__ uint32_t block_count(uint32_t v, uint32_t* s, int flip) {
+constexpr int TL_BINS = 512;               // 32 an octave of 1 + m - c z
+
+template <int W>
+struct TopShared {
+    static constexpr int LINES = W == 1 ? LG_SMALL : 512;  // that are read again
+    static constexpr int LIST = W == 1 ? 256 : 512;        // candidates that are ranked
+    uint32_t hist[TL_BINS];
+    uint32_t lines, n;                     // lengths of the lists
+    uint32_t count[2 * W];
+    uint32_t scan[33];
+    uint32_t line[LINES];
+    unsigned long long list[LIST];         // key, then the lower index first
+};
+
+// Sum of v over the team (every thread gets it); `flip`: not the last call's.
+template <int W>
+__device__ __forceinline__ uint32_t team_count(uint32_t v, uint32_t* s, int flip) {
     v = __reduce_add_sync(0xFFFFFFFFu, v);
-    if (lane_id() == 0) s[flip * LG_WARPS + warp_id()] = v;
+    if (W == 1) return v;
+    if (lane_id() == 0) s[flip * W + warp_id()] = v;
     __syncthreads();
     uint32_t n = 0;
 #pragma unroll
-    for (int i = 0; i < LG_WARPS; ++i) n += s[flip * LG_WARPS + i];
+    for (int i = 0; i < W; ++i) n += s[flip * W + i];
     return n;
 }
 
-// The largest key that at least `want` of the block's keys reach, bit by bit;
+// The largest key that at least `want` of the team's keys reach, bit by bit;
 // `count(k)` counts the thread's keys >= k.  LOW: bits below it are equal in all keys.
-template <int LOW, typename F>
-__device__ __forceinline__ uint32_t block_threshold(uint32_t want, uint32_t* s, F count) {
+template <int W, int LOW, typename F>
+__device__ __forceinline__ uint32_t team_threshold(uint32_t want, uint32_t* s, F count) {
     uint32_t k = 0;
+#pragma unroll 1
     for (int bit = 31; bit >= LOW; --bit) {
         const uint32_t up = k | (1u << bit);
-        if (block_count(count(up), s, bit & 1) >= want) k = up;
+        if (team_count<W>(count(up), s, bit & 1) >= want) k = up;
     }
-    __syncthreads();
+    Team<W>::sync();
     return k;
 }
-
-constexpr int TL_LIST = 512;               // lines that are read again; candidates that are ranked
-constexpr int TL_BINS = 512;               // 32 an octave of 1 + m - c z
-
-struct TopShared {
-    uint32_t hist[TL_BINS];
-    uint32_t lines, n;                     // lengths of the lists
-    uint32_t count[2 * LG_WARPS];
-    uint32_t scan[33];
-    uint32_t line[TL_LIST];
-    unsigned long long list[TL_LIST];      // key, then the lower index first
-};
 
 // 1 + m - c z, at least 1: falls as z grows, and its bits count bins.
 __device__ __forceinline__ float depth(float z, float c, float m) {
@@ -527,7 +567,7 @@ __device__ __forceinline__ uint32_t bin_of(const uint32_t* hist, uint32_t want, 
     return (uint32_t)(src * EACH + at);
 }
 
-// Adds i to a list in shared memory, for the lanes that want to.
+// A place in a list in shared memory for each lane that wants one.
 __device__ __forceinline__ uint32_t slot(uint32_t* n, bool want) {
     const uint32_t who = __ballot_sync(0xFFFFFFFFu, want);
     uint32_t first = 0;
@@ -538,22 +578,23 @@ __device__ __forceinline__ uint32_t slot(uint32_t* n, bool want) {
 // The lists by exact counts, where the bins hold too many: the K-th largest of the lines'
 // largest values, t; the lines above it and the first of those at it; of their
 // elements the ones above the K-th largest of them and the first of those at it.
-template <typename T>
+template <int W, typename T>
 __device__ __forceinline__ void list_exactly(const LineRow<T>& row, int K, const float* tops,
-                                          TopShared& S) {
+                                             TopShared<W>& S) {
+    constexpr int N = Team<W>::THREADS;
     constexpr int LOW = sizeof(T) == 4 ? 0 : 13;       // bf16 keys end 16 bits up, fp16's 13
     // (keys whose low bits are set, a negative value's, compare as the value they stand for)
     constexpr uint32_t mask = ~((1u << LOW) - 1);
-    const int tid = (int)threadIdx.x;
-    const int lines = row.lines(), want = min(K, lines);
-    const int per = (lines + LG_THREADS - 1) / LG_THREADS;
+    const int tid = Team<W>::thread();
+    const int lines = row.lines(), want = min(min(K, lines), TopShared<W>::LINES);
+    const int per = (lines + N - 1) / N;
     // the thread's lines are neighbours, so that a scan over threads is one over lines
     const int l0 = min(lines, tid * per), l1 = min(lines, l0 + per);
     uint32_t t = 0;
     if (lines > K)
-        t = block_threshold<LOW>((uint32_t)K, S.count, [&](uint32_t k) {
+        t = team_threshold<W, LOW>((uint32_t)K, S.count, [&](uint32_t k) {
             uint32_t n = 0;
-            for (int l = tid; l < lines; l += LG_THREADS) n += order_key(tops[l]) >= k;
+            for (int l = tid; l < lines; l += N) n += order_key(tops[l]) >= k;
             return n;
         });
     uint32_t above = 0, equal = 0;
@@ -563,7 +604,7 @@ __device__ __forceinline__ void list_exactly(const LineRow<T>& row, int K, const
         equal += k == t;
     }
     uint32_t tot;
-    const uint32_t before = block_excl_scan(above << 16 | equal, S.scan, &tot);
+    const uint32_t before = Team<W>::excl_scan(above << 16 | equal, S.scan, &tot);
     {
         const uint32_t quota = (uint32_t)want - (tot >> 16);
         uint32_t a = before >> 16, e = before & 0xFFFF;
@@ -574,92 +615,77 @@ __device__ __forceinline__ void list_exactly(const LineRow<T>& row, int K, const
             e += k == t;
         }
     }
-    __syncthreads();
-    // their elements, in order: the thread's chunks are neighbours too
-    constexpr int MOST = TL_MAX_TOP * 4 / LG_THREADS;
-    const int chunks = want * 4, each = (chunks + LG_THREADS - 1) / LG_THREADS;
-    Chunk<T> q[MOST];
-    int32_t at[MOST] = {};
-    auto key_of_pos = [&](int i, int e) -> uint32_t {      // 0: not an element
-        const int32_t pos = at[i] + e;
-        return pos >= row.lead && pos < row.end ? order_key(q[i].get(e)) : 0u;
+    Team<W>::sync();
+    // f(key, position) for their elements, in order: the thread's chunks are neighbours too
+    const int chunks = want * 4, each = (chunks + N - 1) / N;
+    const auto elements = [&](auto f) {
+#pragma unroll 1
+        for (int j = tid * each; j < min(chunks, tid * each + each); ++j) {
+            const int32_t chunk = (int32_t)S.line[j >> 2] * 4 + (j & 3);
+            Chunk<T> q;
+            load_chunk(row, chunk, q);
+#pragma unroll
+            for (int e = 0; e < CHUNK<T>; ++e) {
+                const int32_t pos = chunk * CHUNK<T> + e;
+                if (pos >= row.lead && pos < row.end) f(order_key(q.get(e)), pos);
+            }
+        }
     };
     uint32_t n = 0;
-#pragma unroll
-    for (int i = 0; i < MOST; ++i) {
-        const int j = tid * each + i;
-        at[i] = 0x40000000;                                 // past every row
-        if (i < each && j < chunks) {
-            const int32_t chunk = (int32_t)S.line[j >> 2] * 4 + (j & 3);
-            at[i] = chunk * CHUNK<T>;
-            load_chunk(row, chunk, q[i]);
-        } else {
-            no_chunk(q[i]);
-        }
-#pragma unroll
-        for (int e = 0; e < CHUNK<T>; ++e) n += key_of_pos(i, e) != 0;
-    }
-    const uint32_t need = min((uint32_t)K, block_sum(n, S.scan));
-    const uint32_t cut = block_threshold<LOW>(need, S.count, [&](uint32_t k) {
+    elements([&](uint32_t, int32_t) { ++n; });
+    n = team_count<W>(n, S.count, 0);
+    Team<W>::sync();
+    const uint32_t need = min((uint32_t)K, n);
+    const uint32_t cut = team_threshold<W, LOW>(need, S.count, [&](uint32_t k) {
         uint32_t c = 0;
-#pragma unroll
-        for (int i = 0; i < MOST; ++i)
-#pragma unroll
-            for (int e = 0; e < CHUNK<T>; ++e) c += key_of_pos(i, e) >= k;
+        elements([&](uint32_t key, int32_t) { c += key >= k; });
         return c;
     });
     above = equal = 0;
-#pragma unroll
-    for (int i = 0; i < MOST; ++i)
-#pragma unroll
-        for (int e = 0; e < CHUNK<T>; ++e) {
-            const uint32_t k = key_of_pos(i, e);
-            above += k != 0 && (k & mask) > cut;
-            equal += k != 0 && (k & mask) == cut;
-        }
-    const uint32_t b = block_excl_scan(above << 16 | equal, S.scan, &tot);
+    elements([&](uint32_t key, int32_t) {
+        above += (key & mask) > cut;
+        equal += (key & mask) == cut;
+    });
+    const uint32_t b = Team<W>::excl_scan(above << 16 | equal, S.scan, &tot);
     const uint32_t quota = need - (tot >> 16);
     n = b & 0xFFFF;                                         // equal ones before the thread's
     uint32_t first = (b >> 16) + min(n, quota);
-#pragma unroll
-    for (int i = 0; i < MOST; ++i)
-#pragma unroll
-        for (int e = 0; e < CHUNK<T>; ++e) {
-            const uint32_t k = key_of_pos(i, e);
-            const bool eq = k != 0 && (k & mask) == cut;
-            if (k != 0 && ((k & mask) > cut || (eq && n < quota)))
-                S.list[first++] = (unsigned long long)k << 32 | (uint32_t)(row.end - 1 - (at[i] + e));
-            n += eq;
-        }
+    elements([&](uint32_t key, int32_t pos) {
+        const bool eq = (key & mask) == cut;
+        if ((key & mask) > cut || (eq && n < quota))
+            S.list[first++] = (unsigned long long)key << 32 | (uint32_t)(row.end - 1 - pos);
+        n += eq;
+    });
     if (tid == 0) S.n = need;
-    __syncthreads();
+    Team<W>::sync();
 }
 
-// The top K of the row by (value descending, index ascending), one block.
+// The top K of the row by (value descending, index ascending), one team.
 //
 // The K-th largest value is at least the K-th largest of the lines' largest ones.  A
 // histogram of those by their distance from the row's largest gives a bin that holds it;
 // the lines up to that bin are read again, and their elements up to it, hardly more than
 // K, are ranked by comparing each with each.  (Exact counts over 16 or 32 bits of the
 // lines' keys instead of bins: 380 us more for 4,096 rows of 131,072 bf16.)
-template <typename T>
+template <int W, typename T>
 __device__ __forceinline__ void select_top(const LogprobParams& p, const LineRow<T>& row, int64_t r,
-                                           const float* tops, TopShared& S, const RowSoft& soft) {
-    const int tid = (int)threadIdx.x;
+                                           const float* tops, TopShared<W>& S, const RowSoft& soft) {
+    constexpr int N = Team<W>::THREADS, LIST = TopShared<W>::LIST;
+    const int tid = Team<W>::thread();
     const int lines = row.lines(), K = p.top;
     const float c = p.c, m = soft.m;
     bool exactly = soft.far;                   // (distances mean nothing)
     if (!exactly) {
-        for (int i = tid; i < TL_BINS; i += LG_THREADS) S.hist[i] = 0;
+        for (int i = tid; i < TL_BINS; i += N) S.hist[i] = 0;
         if (tid == 0) S.lines = S.n = 0;
-        __syncthreads();
-        const bool some = lines > K;
-        uint32_t bin = TL_BINS - 1, upto = 0;
+        Team<W>::sync();
+        const bool some = lines > K, binned = some || p.V > LIST;
+        uint32_t bin = TL_BINS - 1;
         if (some) {
-            for (int l = tid; l < lines; l += LG_THREADS)
+            for (int l = tid; l < lines; l += N)
                 atomicAdd(&S.hist[depth_bin(depth(tops[l], c, m))], 1u);
-        } else if (p.V > TL_LIST) {
-            for (int j = tid; j < lines * 4; j += LG_THREADS) {
+        } else if (binned) {
+            for (int j = tid; j < lines * 4; j += N) {
                 Chunk<T> q;
                 load_chunk(row, j, q);
 #pragma unroll
@@ -670,27 +696,28 @@ __device__ __forceinline__ void select_top(const LogprobParams& p, const LineRow
                 }
             }
         }
-        if (some || p.V > TL_LIST) {
-            __syncthreads();
+        if (binned) {
+            Team<W>::sync();
+            uint32_t upto;
             bin = bin_of(S.hist, (uint32_t)min((int64_t)K, p.V), upto);
-            exactly = upto > TL_LIST;
+            exactly = upto > (uint32_t)(some ? TopShared<W>::LINES : LIST);
         }
         if (!exactly) {
             // (the last bin has no end)
             const float edge = bin == TL_BINS - 1 ? CUDART_INF_F
                                                   : __uint_as_float(0x3F800000u + ((bin + 1) << 18));
-            auto within = [&](float z) { return depth(z, c, m) < edge || bin == TL_BINS - 1; };
+            const auto within = [&](float z) { return depth(z, c, m) < edge || bin == TL_BINS - 1; };
             if (some) {
-                for (int l0 = 0; l0 < lines; l0 += LG_THREADS) {
+                for (int l0 = 0; l0 < lines; l0 += N) {
                     const int l = l0 + tid;
                     const bool in = l < lines && within(tops[l]);
                     const uint32_t at = slot(&S.lines, in);
                     if (in) S.line[at] = (uint32_t)l;
                 }
-                __syncthreads();
+                Team<W>::sync();
             }
             const int chunks = (some ? (int)S.lines : lines) * 4;
-            for (int j = tid; j < chunks; j += LG_THREADS) {
+            for (int j = tid; j < chunks; j += N) {
                 const int32_t chunk = (some ? (int32_t)S.line[j >> 2] : j >> 2) * 4 + (j & 3);
                 Chunk<T> q;
                 load_chunk(row, chunk, q);
@@ -700,21 +727,22 @@ __device__ __forceinline__ void select_top(const LogprobParams& p, const LineRow
                     const float z = q.get(e);
                     if (!within(z) || pos < row.lead || pos >= row.end) continue;
                     const uint32_t at = atomicAdd(&S.n, 1u);
-                    if (at < TL_LIST)
+                    if (at < LIST)
                         S.list[at] =
                             (unsigned long long)order_key(z) << 32 | (uint32_t)(row.end - 1 - pos);
                 }
             }
-            __syncthreads();
-            exactly = S.n > TL_LIST;
-            __syncthreads();
+            Team<W>::sync();
+            exactly = S.n > LIST;
+            Team<W>::sync();
         }
     }
-    if (exactly) list_exactly(row, K, tops, S);
+    if (exactly) list_exactly<W>(row, K, tops, S);
     const uint32_t n = S.n;
-    for (uint32_t i = tid; i < n; i += LG_THREADS) {
+    for (uint32_t i = tid; i < n; i += N) {
         const unsigned long long mine = S.list[i];
         uint32_t rank = 0;
+#pragma unroll 4
         for (uint32_t j = 0; j < n; ++j) rank += S.list[j] > mine;
         if (rank < (uint32_t)K) {
             const float z = key_value((uint32_t)(mine >> 32));
@@ -723,26 +751,34 @@ __device__ __forceinline__ void select_top(const LogprobParams& p, const LineRow
             if (p.top_logprobs) p.top_logprobs[r * K + rank] = soft.log_prob(z, p.c, p.scale);
         }
     }
-    for (int i = (int)min((int64_t)K, p.V) + tid; i < K; i += LG_THREADS) {
+    for (int i = (int)min((int64_t)K, p.V) + tid; i < K; i += N) {
         if (p.top_ids) p.top_ids[r * K + i] = -1;
         if (p.top_logprobs) p.top_logprobs[r * K + i] = -CUDART_INF_F;
     }
 }
 
-template <typename T, bool ENTROPY, bool TOP>
-__global__ void __launch_bounds__(LG_THREADS, TOP ? 3 : 4) logprob_kernel(const LogprobParams p) {
-    extern __shared__ float s_tops[];                  // TOP: [lines of the row]
-    __shared__ Soft s_soft[LG_WARPS + 1];
-    __shared__ TopShared S;
+template <int W, bool TOP>
+constexpr int LOGPROB_BLOCKS = TOP ? 3 : 4;        // of an SM
+
+template <int W, typename T, bool ENTROPY, bool TOP>
+__global__ void __launch_bounds__(Team<W>::BLOCK, LOGPROB_BLOCKS<W, TOP>)
+    logprob_kernel(const LogprobParams p) {
+    constexpr int N = Team<W>::THREADS, TEAMS = Team<W>::TEAMS;
+    extern __shared__ float s_dyn[];                   // TOP, W > 1: [lines of the row]
+    __shared__ Soft s_soft[W + 1];
+    __shared__ TopShared<W> S[TEAMS];
+    __shared__ float s_small[TOP && W == 1 ? TEAMS * LG_SMALL : 1];
     pdl_launch();
     pdl_wait();
-    const int64_t r = blockIdx.x / (unsigned)p.blocks;
-    const int rank = (int)(blockIdx.x - r * p.blocks);
-    if (r == p.T) {
+    const int64_t block = (int64_t)(blockIdx.x / (unsigned)p.blocks) - p.scan;
+    const int rank = (int)(blockIdx.x % (unsigned)p.blocks), tid = Team<W>::thread();
+    if (block < 0) {
         if (rank == 0) scan_ids(p.ids, p.id64, p.T, p.V, p.padding, false, p.ctrl);
         return;
     }
-    const int tid = (int)threadIdx.x;
+    const int64_t r = block * TEAMS + Team<W>::team();
+    if (r >= p.T) return;
+    float* s_tops = W == 1 ? s_small + Team<W>::team() * LG_SMALL : s_dyn;
     int64_t id = -1;
     bool skip = false, ok = false;
     if (p.ids) {
@@ -758,7 +794,7 @@ __global__ void __launch_bounds__(LG_THREADS, TOP ? 3 : 4) logprob_kernel(const 
             if (p.entropy) p.entropy[r] = 0.0f;
             if (p.lse) p.lse[r] = 0.0f;
         }
-        for (int i = tid; TOP && i < p.top; i += LG_THREADS) {
+        for (int i = tid; TOP && i < p.top; i += N) {
             if (p.top_ids) p.top_ids[r * p.top + i] = -1;
             if (p.top_logprobs) p.top_logprobs[r * p.top + i] = -CUDART_INF_F;
         }
@@ -771,8 +807,8 @@ __global__ void __launch_bounds__(LG_THREADS, TOP ? 3 : 4) logprob_kernel(const 
     const int32_t lines = row.lines();
     const int32_t share = (lines + p.blocks - 1) / p.blocks;
     const int32_t line0 = min(lines, rank * share), line1 = min(lines, line0 + share);
-    const RowSoft a =
-        row_softmax<T, ENTROPY, TOP>(row, line0, line1, p.c, p.blocks, s_soft, s_tops);
+    const RowSoft a = row_softmax<W, T, ENTROPY, TOP>(row, line0, line1, p.c, p.blocks, s_soft, s_tops,
+                                                      nullptr, 0);
     if (rank == 0 && tid == 0) {
         if (p.logprob) p.logprob[r] = ok ? a.log_prob(zt, p.c, p.scale) : 0.0f;
         if (ENTROPY && p.entropy) p.entropy[r] = a.entropy();
@@ -780,18 +816,18 @@ __global__ void __launch_bounds__(LG_THREADS, TOP ? 3 : 4) logprob_kernel(const 
     }
     if (TOP && rank == 0) {
         // the other blocks' lines
-        if (p.blocks > 1)
-            for (int32_t l = line1 + tid; l < lines; l += LG_THREADS) {
+        if (W > 1 && p.blocks > 1)
+            for (int32_t l = line1 + tid; l < lines; l += N) {
                 float k;
                 asm volatile("ld.shared::cluster.f32 %0, [%1];"
                              : "=f"(k)
                              : "r"(in_block(smem_u32(s_tops + l), (uint32_t)(l / share))));
                 s_tops[l] = k;
             }
-        __syncthreads();
-        select_top<T>(p, row, r, s_tops, S, a);
+        Team<W>::sync();
+        select_top<W, T>(p, row, r, s_tops, S[Team<W>::team()], a);
     }
-    if (p.blocks > 1) cluster_sync();      // no block leaves while its memory is read
+    if (W > 1 && p.blocks > 1) cluster_sync();     // no block leaves while its memory is read
 }
 
 // ------------------------------------- their gradient in the logits
@@ -806,25 +842,28 @@ struct LogprobGradParams {
     void* dz;
     Ctrl* ctrl;
     int64_t T, V, ldz, lddz, padding;
-    int32_t id64, parts;           // blocks of a row
-    int32_t scan;                  // the last block checks the ids
+    int32_t id64, parts;           // warps of a row
+    int32_t scan;                  // the first block checks the ids
     float scale;
 };
 
-constexpr int LD_THREADS = 128;
+constexpr int LD_THREADS = 128, LD_WARPS = LD_THREADS / 32;
+constexpr int LD_LINES = 128;              // lines of a row that one warp takes
 
-// dz_i = scale (g (delta_i,id - p_i) - h p_i (log p_i + entropy)).  SAME: z's and dz's
-// rows lie alike in their lines.
+// dz_i = scale (g (delta_i,id - p_i) - h p_i (log p_i + entropy)), a warp a part of a row.
+// SAME: z's and dz's rows lie alike in their lines.
 template <typename T, typename TO, bool SAME, bool ENTROPY>
 __global__ void __launch_bounds__(LD_THREADS) logprob_grad_kernel(const LogprobGradParams p) {
     pdl_launch();
     pdl_wait();
-    const int64_t r = blockIdx.x / (unsigned)p.parts;
-    const int part = (int)(blockIdx.x - r * p.parts);
-    if (r == p.T) {
+    if (p.scan && blockIdx.x == 0) {
         scan_ids(p.ids, p.id64, p.T, p.V, p.padding, false, p.ctrl);
         return;
     }
+    const int64_t item = ((int64_t)blockIdx.x - p.scan) * LD_WARPS + warp_id();
+    const int64_t r = item / p.parts;
+    const int part = (int)(item - r * p.parts), lane = (int)lane_id();
+    if (r >= p.T) return;
     const T* z = static_cast<const T*>(p.z) + r * p.ldz;
     TO* dz = static_cast<TO*>(p.dz) + r * p.lddz;
     int64_t id = -1;
@@ -833,8 +872,7 @@ __global__ void __launch_bounds__(LD_THREADS) logprob_grad_kernel(const LogprobG
         id = load_id(p.ids, p.id64, r);
         skip = id == p.padding;
         ok = id >= 0 && id < p.V;
-        if (!skip && !ok && !p.scan && part == 0 && threadIdx.x == 0)
-            atomicOr(&p.ctrl->status, ST_BAD_INPUT);
+        if (!skip && !ok && !p.scan && part == 0 && lane == 0) atomicOr(&p.ctrl->status, ST_BAD_INPUT);
     }
     const float lse = p.lse[r];
     const float g = ok && p.g ? p.scale * p.g[r] : 0.0f;
@@ -851,47 +889,44 @@ __global__ void __launch_bounds__(LD_THREADS) logprob_grad_kernel(const LogprobG
         const f32x2 e = ex2_2(mul2(t, pair(LOG2E, LOG2E)));
         return mul2(e, ENTROPY ? fma2(t, pair(-h, -h), pair(k0, k0)) : pair(-g, -g));
     };
-    if (SAME) {
-        const LineRow<T> row(z, p.V);
-        TO* out = dz - row.lead;
-        const int32_t end = row.lines() * 4, token = ok ? (int32_t)id + row.lead : -1;
-        for (int32_t j0 = part * LD_THREADS * LG_FLIGHT; j0 < end;
-             j0 += p.parts * LD_THREADS * LG_FLIGHT) {
-            Chunk<T> q[LG_FLIGHT];
-#pragma unroll
-            for (int k = 0; k < LG_FLIGHT; ++k) {
-                const int32_t j = j0 + k * LD_THREADS + (int32_t)threadIdx.x;
-                if (!skip && j < end) load_chunk(row, j, q[k]);
+    const LineRow<T> row(z, p.V);
+    const int32_t lines = row.lines();
+    // (the row is too long for as many parts as there are blocks: more rounds)
+    for (int32_t line0 = part * LD_LINES; line0 < lines; line0 += p.parts * LD_LINES) {
+        const int32_t line1 = min(lines, line0 + LD_LINES);
+        if (SAME) {
+            TO* out = dz - row.lead;
+            const int32_t token = ok ? (int32_t)id + row.lead : -1;
+            if (skip) {
+                const Chunk<TO> zero = {};
+                for (int32_t j = line0 * 4 + lane; j < line1 * 4; j += 32)
+                    store_chunk(row, out, j * CHUNK<T>, zero);
+                continue;
             }
-#pragma unroll
-            for (int k = 0; k < LG_FLIGHT; ++k) {
-                const int32_t j = j0 + k * LD_THREADS + (int32_t)threadIdx.x;
-                if (j >= end) continue;
+            for_chunks<1, LG_FLIGHT>(row, line0, line1, [&](const Chunk<T>& q, int32_t j, bool mine) {
+                if (!mine) return;
                 const int32_t pos = j * CHUNK<T>;
                 Chunk<TO> o;
-                if (skip) {
-                    o.q[0] = o.q[1] = make_uint4(0, 0, 0, 0);
-                } else {
 #pragma unroll
-                    for (int i = 0; i < CHUNK<T> / 2; ++i) {
-                        f32x2 v = values(Pairs<T>::template get<false>(q[k], i, 0.0f));
-                        if (token >> 1 == (pos >> 1) + i && token >= 0)
-                            v = add2(v, pair(token & 1 ? 0.0f : g, token & 1 ? g : 0.0f));
-                        put_pair(o, i, v);
-                    }
+                for (int i = 0; i < CHUNK<T> / 2; ++i) {
+                    f32x2 v = values(Pairs<T>::template get<false>(q, i, 0.0f));
+                    if (token >> 1 == (pos >> 1) + i)
+                        v = add2(v, pair(token & 1 ? 0.0f : g, token & 1 ? g : 0.0f));
+                    put_pair(o, i, v);
                 }
                 store_chunk(row, out, pos, o);
+            });
+        } else {
+            constexpr int32_t per = LG_LINE / (int)sizeof(T);
+            const int32_t i1 = min(line1 * per, row.end) - row.lead;
+            for (int32_t i = max(line0 * per - row.lead, 0) + lane; i < i1; i += 32) {
+                float v = 0.0f;
+                if (!skip) {
+                    v = parts(values(pair(to_f32(z[i]), 0.0f))).x;
+                    if (i == (int32_t)id) v += g;
+                }
+                dz[i] = from_f32<TO>(v);
             }
-        }
-    } else {
-        for (int32_t i = part * LD_THREADS + (int32_t)threadIdx.x; i < (int32_t)p.V;
-             i += p.parts * LD_THREADS) {
-            float v = 0.0f;
-            if (!skip) {
-                v = parts(values(pair(to_f32(z[i]), 0.0f))).x;
-                if (ok && i == (int32_t)id) v += g;
-            }
-            dz[i] = from_f32<TO>(v);
         }
     }
 }
@@ -907,21 +942,12 @@ struct DistillParams {
     void* dz;                      // or null
     Ctrl* ctrl;
     int64_t T, V, ldz, lddz;
-    int32_t id64, teacher_type, K, blocks, scan;
+    int32_t id64, teacher_type, K, blocks;
+    int32_t scan;                  // the first cluster checks the ids
+    int32_t lines;                 // of a row, at most
+    int32_t keep;                  // chunks of a block's share that its shared memory holds
     float c, scale;
 };
-
-__device__ __forceinline__ float block_max_nan(float v, float* s) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    if (lane_id() == 0) s[warp_id()] = v;
-    __syncthreads();
-    v = s[0];
-#pragma unroll
-    for (int i = 1; i < LG_WARPS; ++i) v = max_nan(v, s[i]);
-    __syncthreads();
-    return v;
-}
 
 __device__ __forceinline__ float teacher_at(const DistillParams& p, int64_t i) {
     if (p.teacher_type == TOPK_EF_F32) return static_cast<const float*>(p.teacher)[i];
@@ -930,125 +956,147 @@ __device__ __forceinline__ float teacher_at(const DistillParams& p, int64_t i) {
     return to_f32(static_cast<const __half*>(p.teacher)[i]);
 }
 
+template <int W>
+struct TeacherShared {
+    float t[DL_MAX_K], z[DL_MAX_K], q[DL_MAX_K];
+    int32_t id[DL_MAX_K];
+};
+
 // loss = weight sum_k q_k (log q_k - log p_{id_k}),  q = softmax(scale teacher);
-// dz = weight scale (p - q).  Thread k keeps the teacher's k-th entry.
-template <typename T, typename TO, bool SAME>
-__global__ void __launch_bounds__(LG_THREADS, 3) distill_kernel(const DistillParams p) {
-    __shared__ Soft s_soft[LG_WARPS + 1];
+// dz = weight scale (p - q).  What fits of the block's share of the row stays in shared memory
+// between the sums and the gradient; the rest is read again, from L2 where the blocks that
+// run at once leave room for it.
+template <int W, typename T, typename TO, bool SAME>
+__global__ void __launch_bounds__(Team<W>::BLOCK, W == 16 ? 2 : 3)
+    distill_kernel(const DistillParams p) {
+    constexpr int N = Team<W>::THREADS, TEAMS = Team<W>::TEAMS;
+    extern __shared__ uint4 s_stash[];                 // W > 1
+    __shared__ Soft s_soft[W + 1];
     __shared__ float s_red[33];
-    __shared__ int32_t s_id[DL_MAX_K];
-    __shared__ float s_q[DL_MAX_K];
+    __shared__ TeacherShared<W> s_teacher[TEAMS];
     pdl_launch();
     pdl_wait();
-    const int64_t r = blockIdx.x / (unsigned)p.blocks;
-    const int rank = (int)(blockIdx.x - r * p.blocks), tid = (int)threadIdx.x;
-    if (r == p.T) {
+    const int64_t block = (int64_t)(blockIdx.x / (unsigned)p.blocks) - p.scan;
+    const int rank = (int)(blockIdx.x % (unsigned)p.blocks), tid = Team<W>::thread();
+    if (block < 0) {
         if (rank == 0) scan_ids(p.ids, p.id64, p.T * p.K, p.V, -1, true, p.ctrl);
         return;
     }
+    const int64_t r = block * TEAMS + Team<W>::team();
+    if (r >= p.T) return;
+    TeacherShared<W>& S = s_teacher[Team<W>::team()];
     const T* z = static_cast<const T*>(p.z) + r * p.ldz;
-    int64_t id = -1;
-    float tz = -CUDART_INF_F, zk = 0.0f;
-    if (tid < p.K) {
-        id = load_id(p.ids, p.id64, r * p.K + tid);
+    const float weight = p.weight ? p.weight[r] : 1.0f;
+    // (S belongs to the threads that write it until the sums are joined)
+    for (int k = tid; k < p.K; k += N) {
+        int64_t id = load_id(p.ids, p.id64, r * p.K + k);
         if (id >= p.V) {
             if (!p.scan && rank == 0) atomicOr(&p.ctrl->status, ST_BAD_INPUT);
             id = -1;
         }
-    }
-    const float weight = p.weight ? p.weight[r] : 1.0f;
-    bool skip = weight == 0.0f;
-    if (!skip && id >= 0) {
-        tz = teacher_at(p, r * p.K + tid);
-        zk = to_f32(z[id]);
-    }
-    float big = -CUDART_INF_F;
-    if (!skip) {
-        big = block_max_nan(tz, s_red);
-        skip = big == -CUDART_INF_F;               // no entry counts
+        const bool there = id >= 0 && weight != 0.0f;
+        S.id[k] = (int32_t)max(id, (int64_t)-1);
+        S.t[k] = there ? teacher_at(p, r * p.K + k) : -CUDART_INF_F;
+        S.z[k] = there ? to_f32(z[id]) : 0.0f;
     }
     const LineRow<T> row(z, p.V);
     const int32_t lines = row.lines(), share = (lines + p.blocks - 1) / p.blocks;
     const int32_t line0 = min(lines, rank * share), line1 = min(lines, line0 + share);
+    const int32_t keep = W > 1 && p.dz ? p.keep : 0;
+    bool none = true;                              // no entry counts
     RowSoft a = {};
-    float q = 0.0f, inv = 0.0f;
-    if (!skip) {                                   // (the same in all blocks of the cluster)
-        const float tq = tz - big;
-        q = ex2(tq * p.c);
-        const float sum = block_sum(q, s_red);
-        q /= sum;
-        a = row_softmax<T, false, false>(row, line0, line1, p.c, p.blocks, s_soft, nullptr);
-        if (rank == 0 && p.loss) {
-            float part = 0.0f;
-            if (q != 0.0f)
-                part = q * (fmaf(tq, p.scale, -logf(sum)) - a.log_prob(zk, p.c, p.scale));
-            part = block_sum(part, s_red);
-            if (tid == 0) p.loss[r] = weight * part;
-        }
-        s_id[tid] = (int32_t)id;
-        s_q[tid] = q;
+    float big = 0.0f, q_sum = 1.0f, inv = 0.0f;
+    if (weight != 0.0f) {                          // (the same in all blocks of the cluster)
+        a = row_softmax<W, T, false, false>(row, line0, line1, p.c, p.blocks, s_soft, nullptr, s_stash,
+                                            keep);
+        Team<W>::sync();
         inv = a.s == 0.0f ? 0.0f : 1.0f / a.s;
-        __syncthreads();
-    } else if (rank == 0 && tid == 0 && p.loss) {
-        p.loss[r] = 0.0f;
+        // each warp for itself
+        big = -CUDART_INF_F;
+        for (int k = (int)lane_id(); k < p.K; k += 32) big = max_nan(big, S.t[k]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) big = max_nan(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
+        none = big == -CUDART_INF_F;
+        if (!none) {
+            q_sum = 0.0f;
+            for (int k = (int)lane_id(); k < p.K; k += 32) q_sum += ex2((S.t[k] - big) * p.c);
+            q_sum = warp_sum(q_sum);
+            for (int k = tid; k < p.K; k += N) S.q[k] = ex2((S.t[k] - big) * p.c) / q_sum;
+        }
     }
     if (p.dz) {
         TO* dz = static_cast<TO*>(p.dz) + r * p.lddz;
         const float w = weight * p.scale, f = w * inv;
         const f32x2 cc = pair(p.c, p.c), mm = pair(-a.m, -a.m), ff = pair(f, f);
-        auto probs = [&](f32x2 v) {                        // (times f)
+        const auto probs = [&](f32x2 v) {          // (times f)
             if (!a.far) return mul2(ex2_2(fma2(v, cc, mm)), ff);
             const float2 x = parts(v);
             return pair(f * a.prob(x.x, p.c), f * a.prob(x.y, p.c));
         };
-        if (SAME) {
-            TO* out = dz - row.lead;
-            const int32_t end = line1 * 4;
-            for (int32_t j0 = line0 * 4; j0 < end; j0 += LG_THREADS * LG_FLIGHT) {
-                Chunk<T> v[LG_FLIGHT];
-#pragma unroll
-                for (int k = 0; k < LG_FLIGHT; ++k) {
-                    const int32_t j = j0 + k * LG_THREADS + tid;
-                    if (!skip && j < end) load_chunk(row, j, v[k]);
-                }
-#pragma unroll
-                for (int k = 0; k < LG_FLIGHT; ++k) {
-                    const int32_t j = j0 + k * LG_THREADS + tid;
-                    if (j >= end) continue;
-                    Chunk<TO> o;
-                    if (skip) {
-                        o.q[0] = o.q[1] = make_uint4(0, 0, 0, 0);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < CHUNK<T> / 2; ++i)
-                            put_pair(o, i, probs(Pairs<T>::template get<false>(v[k], i, 0.0f)));
-                    }
-                    store_chunk(row, out, j * CHUNK<T>, o);
-                }
-            }
-        } else {
-            const int32_t per = LG_LINE / (int)sizeof(T);
+        if (!SAME) {
+            constexpr int32_t per = LG_LINE / (int)sizeof(T);
             const int32_t i1 = min(line1 * per, row.end) - row.lead;
-            for (int32_t i = max(line0 * per - row.lead, 0) + tid; i < i1; i += LG_THREADS)
-                dz[i] = from_f32<TO>(skip ? 0.0f : parts(probs(pair(to_f32(z[i]), 0.0f))).x);
+            for (int32_t i = max(line0 * per - row.lead, 0) + tid; i < i1; i += N)
+                dz[i] = from_f32<TO>(none ? 0.0f : parts(probs(pair(to_f32(z[i]), 0.0f))).x);
+        } else if (none) {
+            const Chunk<TO> zero = {};
+            for (int32_t j = line0 * 4 + tid; j < line1 * 4; j += N)
+                store_chunk(row, dz - row.lead, j * CHUNK<T>, zero);
+        } else {
+            const auto put = [&](const Chunk<T>& v, int32_t j) {
+                Chunk<TO> o;
+#pragma unroll
+                for (int e = 0; e < CHUNK<T> / 2; ++e)
+                    put_pair(o, e, probs(Pairs<T>::template get<false>(v, e, 0.0f)));
+                store_chunk(row, dz - row.lead, j * CHUNK<T>, o);
+            };
+            // the rest first: it may still be in L2
+            if (line0 + keep / 4 < line1)
+                for_chunks<W, 2>(row, line0 + keep / 4, line1,
+                                 [&](const Chunk<T>& v, int32_t j, bool mine) {
+                                     if (mine) put(v, j);
+                                 });
+            const int32_t kept = min(line0 * 4 + keep, line1 * 4);
+#pragma unroll 2
+            for (int32_t j = line0 * 4 + tid; j < kept; j += N) {
+                Chunk<T> v;
+                get_stash<W>(s_stash, j - line0 * 4, v);
+                put(v, j);
+            }
         }
-        if (!skip) {
+        if (!none) {
             // the teacher's tokens: the first entry of each takes all of its q
-            __syncthreads();
-            const int32_t line = id >= 0 ? ((int32_t)id + row.lead) / (LG_LINE / (int)sizeof(T)) : -1;
-            if (line >= line0 && line < line1) {
+            Team<W>::sync();
+            for (int k = tid; k < p.K; k += N) {
+                const int32_t id = S.id[k];
+                const int32_t line = id >= 0 ? (id + row.lead) / (LG_LINE / (int)sizeof(T)) : -1;
+                if (line < line0 || line >= line1) continue;
                 float all = 0.0f;
                 bool first = true;
-                for (int j = 0; j < p.K; ++j)
-                    if (s_id[j] == (int32_t)id) {
-                        all += s_q[j];
-                        first = first && j >= tid;
+#pragma unroll 8
+                for (int i = 0; i < p.K; ++i)
+                    if (S.id[i] == id) {
+                        all += S.q[i];
+                        first = first && i >= k;
                     }
-                if (first) dz[id] = from_f32<TO>(w * (a.prob(zk, p.c) * inv - all));
+                if (first) dz[id] = from_f32<TO>(w * (a.prob(S.z[k], p.c) * inv - all));
             }
         }
     }
-    if (!skip && p.blocks > 1) cluster_sync();     // no block leaves while its memory is read
+    if (rank == 0 && p.loss) {
+        float part = 0.0f;
+        if (!none) {
+            const float log_q = logf(q_sum);
+            for (int k = tid; k < p.K; k += N) {
+                const float q = S.q[k];
+                if (q != 0.0f)
+                    part += q * (fmaf(S.t[k] - big, p.scale, -log_q) - a.log_prob(S.z[k], p.c, p.scale));
+            }
+        }
+        part = Team<W>::sum(part, s_red);
+        if (tid == 0) p.loss[r] = none ? 0.0f : weight * part;
+    }
+    if (W > 1 && weight != 0.0f && p.blocks > 1) cluster_sync();   // no block leaves while its memory is read
 }
 
 }  // namespace tke

@@ -17,8 +17,11 @@ using namespace tke;
 namespace {
 
 constexpr int64_t SCAN_IDS = 8192;         // ids that one block checks
-constexpr int64_t WANT_BLOCKS = 148 * 3;   // blocks that a call should have at least
+constexpr int SMS = 148;
 constexpr int64_t LEAST_LINES = 32;        // lines of a block of a cluster
+// Short rows take a warp each from here on: as many as blocks that run at once.  (64 rows of
+// 1,000 bf16, top 20: a block each 9.4 us, a warp each 13; 16,384 rows: 280 and 60 us.)
+constexpr int64_t WARP_ROWS = SMS * 3;
 
 bool sizes_ok(int64_t T, int64_t V) {
     return T >= 0 && T <= MAX_N && V >= 1 && V <= (int64_t)1 << 24;
@@ -26,13 +29,16 @@ bool sizes_ok(int64_t T, int64_t V) {
 bool pointer_ok(const void* p, size_t size) { return p && aligned(p, size); }
 bool scale_ok(float s) { return s >= 1e-30f && s <= 1e30f; }
 
-// Most 128-byte lines that a row of V elements can touch.
-int64_t most_lines(int64_t V, size_t size) { return (V * (int64_t)size + LG_LINE - 2) / LG_LINE + 1; }
+// Most 128-byte lines that a row touches.
+int64_t most_lines(const void* z, int64_t ld, int64_t V, size_t size) {
+    const bool whole = (uintptr_t)z % LG_LINE == 0 && (size_t)ld * size % LG_LINE == 0;
+    return whole ? ceil_div64(V * (int64_t)size, LG_LINE) : (V * (int64_t)size + LG_LINE - 2) / LG_LINE + 1;
+}
 
-// Blocks of a row's cluster: more while the call has too few.
-int row_blocks(int64_t T, int64_t lines) {
+// Blocks of a row's cluster: more while the call has fewer than `want`.
+int row_blocks(int64_t T, int64_t lines, int64_t want) {
     int c = 1;
-    while (c < 16 && T * c < WANT_BLOCKS && lines / (2 * c) >= LEAST_LINES) c *= 2;
+    while (c < 16 && T * c < want && lines / (2 * c) >= LEAST_LINES) c *= 2;
     return c;
 }
 
@@ -55,30 +61,55 @@ bool same_lines(const void* a, int64_t lda, const void* b, int64_t ldb, size_t s
            (size_t)(lda - ldb) * size % LG_LINE == 0;
 }
 
-template <typename T, bool ENTROPY, bool TOP>
+template <int W, typename T, bool ENTROPY, bool TOP>
 cudaError_t launch_logprob(const LogprobParams& p, size_t smem, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    const auto kernel = logprob_kernel<T, ENTROPY, TOP>;
-    cudaError_t e = allow(kernel, done, TOP ? TL_MAX_LINES * 4 : 0);
+    const auto kernel = logprob_kernel<W, T, ENTROPY, TOP>;
+    cudaError_t e = allow(kernel, done, TOP && W > 1 ? TL_MAX_LINES * 4 : 0);
     if (e != cudaSuccess) return e;
+    const int64_t rows = ceil_div64(p.T, Team<W>::TEAMS);
     trace_before(st, "logprob_kernel");
-    e = launch_clusters(kernel, (unsigned)((p.T + p.scan) * p.blocks), (unsigned)p.blocks, LG_THREADS,
-                        smem, st, p);
+    e = launch_clusters(kernel, (unsigned)((rows + p.scan) * p.blocks), (unsigned)p.blocks,
+                        Team<W>::BLOCK, W > 1 ? smem : 0, st, p);
+    trace_after(st);
+    return e;
+}
+
+template <typename T, bool ENTROPY, bool TOP>
+cudaError_t logprob_by_length(const LogprobParams& p, bool small, size_t smem, cudaStream_t st) {
+    return small ? launch_logprob<1, T, ENTROPY, TOP>(p, smem, st)
+                 : launch_logprob<8, T, ENTROPY, TOP>(p, smem, st);
+}
+
+template <int W, typename T, typename TO, bool SAME>
+cudaError_t launch_distill(DistillParams p, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    // what the blocks of an SM leave one another, in whole rounds of chunks
+    constexpr size_t round = (size_t)Team<W>::THREADS * 32;
+    constexpr size_t room =
+        W == 1 ? 0 : (233472 / (W == 16 ? 2 : 3) - 1024 - sizeof(TeacherShared<W>) - 1024) / round * round;
+    const auto kernel = distill_kernel<W, T, TO, SAME>;
+    cudaError_t e = allow(kernel, done, room);
+    if (e != cudaSuccess) return e;
+    size_t smem = 0;
+    if (SAME && p.dz) {
+        const int64_t share = ceil_div64(p.lines, p.blocks);
+        smem = std::min(room, (size_t)ceil_div64(share * LG_LINE, round) * round);
+        p.keep = (int32_t)(smem / 32);
+    }
+    const int64_t rows = ceil_div64(p.T, Team<W>::TEAMS);
+    trace_before(st, "distill_kernel");
+    e = launch_clusters(kernel, (unsigned)((rows + p.scan) * p.blocks), (unsigned)p.blocks,
+                        Team<W>::BLOCK, smem, st, p);
     trace_after(st);
     return e;
 }
 
 template <typename T, typename TO, bool SAME>
-cudaError_t launch_distill(const DistillParams& p, cudaStream_t st) {
-    static std::atomic<uint64_t> done{0};
-    const auto kernel = distill_kernel<T, TO, SAME>;
-    cudaError_t e = allow(kernel, done, 0);
-    if (e != cudaSuccess) return e;
-    trace_before(st, "distill_kernel");
-    e = launch_clusters(kernel, (unsigned)((p.T + p.scan) * p.blocks), (unsigned)p.blocks, LG_THREADS, 0,
-                        st, p);
-    trace_after(st);
-    return e;
+cudaError_t distill_by_length(const DistillParams& p, int warps, cudaStream_t st) {
+    return warps == 1   ? launch_distill<1, T, TO, SAME>(p, st)
+           : warps == 8 ? launch_distill<8, T, TO, SAME>(p, st)
+                        : launch_distill<16, T, TO, SAME>(p, st);
 }
 
 }  // namespace
@@ -95,7 +126,7 @@ int token_logprobs(const void* logits, int32_t logits_type, int64_t ld_logits, c
     if (!sizes_ok(T, V) || !sz || ld_logits < V || !scale_ok(scale) || top < 0 || top > TL_MAX_TOP ||
         !ws || !aligned(ws, ALIGN))
         return TOPK_EF_ERR_INVALID_ARG;
-    const int64_t lines = most_lines(V, sz);
+    const int64_t lines = most_lines(logits, ld_logits, V, sz);
     if (top > 0 && lines > TL_MAX_LINES) return TOPK_EF_ERR_INVALID_ARG;
     if (ids && ((id_bytes != 4 && id_bytes != 8) || !aligned(ids, id_bytes)))
         return TOPK_EF_ERR_INVALID_ARG;
@@ -121,7 +152,8 @@ int token_logprobs(const void* logits, int32_t logits_type, int64_t ld_logits, c
     p.padding = padding_idx;
     p.id64 = id_bytes == 8;
     p.top = top_ids || top_logprobs ? top : 0;
-    p.blocks = row_blocks(T, lines);
+    const bool small = lines <= LG_SMALL && T > WARP_ROWS;
+    p.blocks = small ? 1 : row_blocks(T, lines, SMS * 3);
     p.scan = T <= SCAN_IDS;
     p.scale = scale;
     p.c = (float)((double)scale * 1.4426950408889634);
@@ -133,10 +165,10 @@ int token_logprobs(const void* logits, int32_t logits_type, int64_t ld_logits, c
     const cudaError_t e = with_type(logits_type, [&](auto t) {
         using TZ = decltype(t);
         if (p.top)
-            return entropy ? launch_logprob<TZ, true, true>(p, smem, st)
-                           : launch_logprob<TZ, false, true>(p, smem, st);
-        return entropy ? launch_logprob<TZ, true, false>(p, smem, st)
-                       : launch_logprob<TZ, false, false>(p, smem, st);
+            return entropy ? logprob_by_length<TZ, true, true>(p, small, smem, st)
+                           : logprob_by_length<TZ, false, true>(p, small, smem, st);
+        return entropy ? logprob_by_length<TZ, true, false>(p, small, smem, st)
+                       : logprob_by_length<TZ, false, false>(p, small, smem, st);
     });
     return e == cudaSuccess ? TOPK_EF_OK : cuda_fail(e);
 }
@@ -180,14 +212,13 @@ int token_logprobs_grad(const void* logits, int32_t logits_type, int64_t ld_logi
     p.id64 = id_bytes == 8;
     p.scan = T <= SCAN_IDS;
     p.scale = scale;
-    const int64_t chunks = most_lines(V, sz) * 4;
-    p.parts = (int32_t)std::min(ceil_div64(chunks, LD_THREADS * LG_FLIGHT),
+    p.parts = (int32_t)std::min(ceil_div64(most_lines(logits, ld_logits, V, sz), LD_LINES),
                                 std::max<int64_t>(1, MAX_N / (T + 1)));
     if (!p.scan) {
         const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(Ctrl), st);
         if (e != cudaSuccess) return cuda_fail(e);
     }
-    const unsigned grid = (unsigned)(T * p.parts + p.scan);
+    const unsigned grid = (unsigned)(ceil_div64(T * p.parts, LD_WARPS) + p.scan);
     const bool same = sz == so && same_lines(logits, ld_logits, grad_logits, ld_grad_logits, sz);
     trace_before(st, "logprob_grad_kernel");
     const cudaError_t e = with_type(logits_type, [&](auto t) {
@@ -244,8 +275,13 @@ int distill_loss(const void* logits, int32_t logits_type, int64_t ld_logits,
     p.id64 = id_bytes == 8;
     p.teacher_type = teacher_type;
     p.K = K;
-    p.blocks = row_blocks(T, most_lines(V, sz));
-    if (getenv("DLC")) p.blocks = atoi(getenv("DLC"));
+    // (with the gradient, rows that shared memory does not hold as a whole take blocks of 16
+    // warps, so that fewer rows are read again out of L2)
+    p.lines = (int32_t)most_lines(logits, ld_logits, V, sz);
+    const int warps = p.lines <= LG_SMALL && T > WARP_ROWS              ? 1
+                      : grad_logits && p.lines > 512 && T >= SMS * 2 ? 16
+                                                                        : 8;
+    p.blocks = warps == 8 ? row_blocks(T, p.lines, SMS * 3) : 1;
     p.scan = T * std::max(K, 1) <= SCAN_IDS;
     p.scale = scale;
     p.c = (float)((double)scale * 1.4426950408889634);
@@ -260,8 +296,8 @@ int distill_loss(const void* logits, int32_t logits_type, int64_t ld_logits,
             using TZ = decltype(t);
             using TO = decltype(to);
             if constexpr (sizeof(TZ) == sizeof(TO))
-                if (same) return launch_distill<TZ, TO, true>(p, st);
-            return launch_distill<TZ, TO, false>(p, st);
+                if (same) return distill_by_length<TZ, TO, true>(p, warps, st);
+            return distill_by_length<TZ, TO, false>(p, warps, st);
         });
     });
     return e == cudaSuccess ? TOPK_EF_OK : cuda_fail(e);
