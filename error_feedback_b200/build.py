@@ -12,7 +12,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRCS = [os.path.join(HERE, "csrc", f) for f in ("topk_ef.cu", "embedding.cu", "muon.cu", "layer_norm.cu",
-                                              "token_loss.cu")]
+                                                "layer_norm_grad.cu", "token_loss.cu")]
 DEPS = sorted(glob.glob(os.path.join(HERE, "csrc", "*.cu*"))) + [
     os.path.join(ROOT, "include", "topk_ef.h")]
 LIB = os.path.join(HERE, "libtopk_ef.so")

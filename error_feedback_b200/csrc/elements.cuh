@@ -1,5 +1,5 @@
-// Element types of the embedding and Muon kernels: conversions, 16-byte
-// accesses of eight elements, and the waits of chained launches.
+// Element types of the calls beside compress and merge: conversions, 16-byte accesses of
+// eight elements, arithmetic on pairs, and the waits of chained launches.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -72,6 +72,58 @@ __device__ __forceinline__ void store8(T* p, const float* x) {
         for (int i = 0; i < (int)(sizeof(T) / 2); ++i) d[i] = v.q[i];
     }
 }
+
+// Two values a register pair, two values an instruction.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 parts(f32x2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// Two 16-bit elements as such a pair ...
+__device__ __forceinline__ f32x2 widen(__nv_bfloat162 w) {
+    const uint32_t b = *reinterpret_cast<const uint32_t*>(&w);
+    return pair(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u));
+}
+__device__ __forceinline__ f32x2 widen(__half2 w) {
+    const float2 v = __half22float2(w);
+    return pair(v.x, v.y);
+}
+// ... and packs them again.
+__device__ __forceinline__ uint32_t narrow(f32x2 a, __nv_bfloat16) {
+    const float2 v = parts(a);
+    const __nv_bfloat162 w = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&w);
+}
+__device__ __forceinline__ uint32_t narrow(f32x2 a, __half) {
+    const float2 v = parts(a);
+    const __half2 w = __floats2half2_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&w);
+}
+
+template <typename T> struct Twin;
+template <> struct Twin<__nv_bfloat16> { typedef __nv_bfloat162 type; static constexpr bool bf16 = true; };
+template <> struct Twin<__half> { typedef __half2 type; static constexpr bool bf16 = false; };
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;"); }

@@ -148,58 +148,11 @@ struct Soft {
     float m, s, u;
 };
 
-// Two values a register pair, two values an instruction.
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pair(float lo, float hi) {
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 parts(f32x2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-    return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ f32x2 ex2_2(f32x2 a) {
     const float2 v = parts(a);
     return pair(ex2(v.x), ex2(v.y));
 }
 
-// The two elements of word i of a chunk (fp32: elements 2 i and 2 i + 1).
-__device__ __forceinline__ f32x2 widen(__nv_bfloat162 w) {
-    const uint32_t b = *reinterpret_cast<const uint32_t*>(&w);
-    return pair(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u));
-}
-__device__ __forceinline__ f32x2 widen(__half2 w) {
-    const float2 v = __half22float2(w);
-    return pair(v.x, v.y);
-}
-// ... and packs them again.
-__device__ __forceinline__ uint32_t narrow(f32x2 a, __nv_bfloat16) {
-    const float2 v = parts(a);
-    const __nv_bfloat162 w = __floats2bfloat162_rn(v.x, v.y);
-    return *reinterpret_cast<const uint32_t*>(&w);
-}
-__device__ __forceinline__ uint32_t narrow(f32x2 a, __half) {
-    const float2 v = parts(a);
-    const __half2 w = __floats2half2_rn(v.x, v.y);
-    return *reinterpret_cast<const uint32_t*>(&w);
-}
 template <typename T>
 __device__ __forceinline__ void put_pair(Chunk<T>& q, int i, f32x2 a) {
     if constexpr (sizeof(T) == 4) {
@@ -208,10 +161,6 @@ __device__ __forceinline__ void put_pair(Chunk<T>& q, int i, f32x2 a) {
         reinterpret_cast<uint32_t*>(q.q)[i] = narrow(a, T{});
     }
 }
-template <typename T> struct Twin;
-template <> struct Twin<__nv_bfloat16> { typedef __nv_bfloat162 type; static constexpr bool bf16 = true; };
-template <> struct Twin<__half> { typedef __half2 type; static constexpr bool bf16 = false; };
-
 // The pairs of a chunk, not below `low` (NaN stays), and its largest value (of what was
 // there; NaN if there is one).
 template <typename T>

@@ -1,9 +1,6 @@
-// Layer norm over the rows of a matrix, and its gradient.
+// Layer norm over the rows of a matrix.
 //
-//   mean = 1/D sum x,  rstd = (1/D sum (x - mean)^2 + eps)^(-1/2)
-//   y    = (x - mean) rstd w + b
-//   with xh = (x - mean) rstd and g = dy w:
-//   dx   = rstd (g - 1/D sum g - xh 1/D sum (g xh)),  dw = sum_t dy xh,  db = sum_t dy
+//   mean = 1/D sum x,  rstd = (1/D sum (x - mean)^2 + eps)^(-1/2),  y = (x - mean) rstd w + b
 //
 // All sums are fp32, of the row less its first element c: at most sqrt(D) deviations
 // from the mean, so an offset common to a row costs no bits.  The variance
@@ -11,11 +8,11 @@
 // squares of the differences from its own elements' mean, and the warps' (count,
 // sum, squares) are joined by sum n (mean_w - mean)^2.
 //
-// Rows of up to NM_MAX_D (forward) and NM_MAX_GRAD_D (gradient) columns are read
-// once and held in registers between the statistics and the result; longer
-// ones are read again.  A block keeps to its columns over all of its rows, so w, b and
-// the gradient's column sums stay in registers too.  Column sums leave one fp32 row per
-// block, added in block order by a second kernel: no floating-point atomics.
+// A row is held in registers by 8 to 512 threads between the statistics and the result, 8 to
+// 64 elements each (32 of fp32): the fewer threads, the less joining, and what is in flight
+// is the warps' rows.  (16 elements a thread with the next row loaded ahead took 33
+// instructions an element, most of them for joining, and 108 us for 16,384 x 4,096 bf16.)
+// Rows past NM_MAX_D columns are read again instead.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -28,7 +25,6 @@
 namespace tke {
 
 constexpr int NM_MAX_D = 16384;
-constexpr int NM_MAX_GRAD_D = 8192;
 
 struct NormParams {
     const void* x;
@@ -48,11 +44,11 @@ __device__ __forceinline__ float load_as(const void* p, int32_t type, int64_t i)
     return to_f32(static_cast<const __half*>(p)[i]);
 }
 
-// The thread's elements of one row: groups of 8 columns (VEC; 16-byte aligned), or
+// The thread's elements of a row of G threads: groups of 8 columns (VEC; 16-byte aligned), or
 // columns G apart (rows that start anywhere).  Element e of thread t:
 template <int G, bool VEC>
-__device__ __forceinline__ int64_t norm_col(int t, int e) {
-    return VEC ? ((int64_t)(e / 8) * G + t) * 8 + e % 8 : (int64_t)e * G + t;
+__device__ __forceinline__ int norm_col(int t, int e) {
+    return VEC ? ((e / 8) * G + t) * 8 + e % 8 : e * G + t;
 }
 
 template <typename T, int N, bool VEC>
@@ -60,6 +56,21 @@ struct RowRegs {
     Vec8<T> v[N];                  // 8 N elements
     __device__ __forceinline__ float get(int e) const {
         return to_f32(reinterpret_cast<const T*>(v)[e]);
+    }
+    // elements 2 i and 2 i + 1
+    __device__ __forceinline__ f32x2 two(int i) const {
+        if constexpr (sizeof(T) == 4) {
+            return reinterpret_cast<const f32x2*>(v)[i];
+        } else {
+            return widen(reinterpret_cast<const typename Twin<T>::type*>(v)[i]);
+        }
+    }
+    __device__ __forceinline__ void put_two(int i, f32x2 a) {
+        if constexpr (sizeof(T) == 4) {
+            reinterpret_cast<f32x2*>(v)[i] = a;
+        } else {
+            reinterpret_cast<uint32_t*>(v)[i] = narrow(a, T{});
+        }
     }
 };
 
@@ -88,124 +99,190 @@ __device__ __forceinline__ void load_row(const T* row, int t, int D, RowRegs<T, 
 }
 
 template <typename T, int G, int N, bool VEC>
-__device__ __forceinline__ void store_row(T* row, int t, int D, const float* x) {
+__device__ __forceinline__ void store_row(T* row, int t, int D, const RowRegs<T, N, VEC>& r) {
     if (VEC) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int c = (j * G + t) * 8;
-            if (c < D) store8(row + c, x + j * 8);
+            if (c >= D) continue;
+            if (sizeof(T) == 4 && (uintptr_t)(row + c) % 32 == 0) {
+                store32b(row + c, r.v[j].q);
+            } else {
+#pragma unroll
+                for (int k = 0; k < (int)(sizeof(T) / 2); ++k)
+                    reinterpret_cast<uint4*>(row + c)[k] = r.v[j].q[k];
+            }
         }
     } else {
+        const T* e = reinterpret_cast<const T*>(r.v);
 #pragma unroll
         for (int j = 0; j < 8 * N; ++j) {
             const int c = j * G + t;
-            if (c < D) row[c] = from_f32<T>(x[j]);
+            if (c < D) row[c] = e[j];
         }
     }
 }
 
-// Elements of the warp that starts at thread t0 of its row's G threads, of D.
+// Eight consecutive weights from c on (c and p 16-byte aligned steps), as pairs.
+__device__ __forceinline__ void load8_as(const void* p, int32_t type, int c, f32x2* o) {
+    if (type == TOPK_EF_F32) {
+        RowRegs<float, 1, true> r;
+        r.v[0] = load8(static_cast<const float*>(p) + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = r.two(i);
+    } else if (type == TOPK_EF_BF16) {
+        RowRegs<__nv_bfloat16, 1, true> r;
+        r.v[0] = load8(static_cast<const __nv_bfloat16*>(p) + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = r.two(i);
+    } else {
+        RowRegs<__half, 1, true> r;
+        r.v[0] = load8(static_cast<const __half*>(p) + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = r.two(i);
+    }
+}
+
+// Elements that the lanes of one warp (VEC: or part of it) hold of a row; t0: the row's
+// thread that the lanes start at.
 template <int G, int N, bool VEC>
 __device__ __forceinline__ int warp_count(int t0, int D) {
+    constexpr int L = G < 32 ? G : 32;
     int n = 0;
     if (VEC) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) n += min(max(D - (j * G + t0) * 8, 0), 256);
+        for (int j = 0; j < N; ++j) n += min(max(D - (j * G + t0) * 8, 0), L * 8);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8 * N; ++j) n += min(max(D - (j * G + t0), 0), 32);
+        for (int j = 0; j < 8 * N; ++j) n += min(max(D - (j * G + t0), 0), L);
     }
     return n;
 }
 
-// Mean and reciprocal deviation of what G threads hold of a row; n elements (columns
-// in(e)) belong to the warp.  s: 3 G / 32 floats that the previous row's call has
-// not used.
-template <int G, int E, typename I>
-__device__ __forceinline__ float2 row_statistics(const float* x, I in, int n, float D, float inv_d,
-                                                 float eps, float* s) {
-    float sum = 0.0f;
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) sum += in(e) ? x[e] : 0.0f;
-    sum = warp_sum(sum);
-    const float m = n > 0 ? sum / (float)n : 0.0f;
-    float sq = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const float d = in(e) ? x[e] - m : 0.0f;
-        sq = fmaf(d, d, sq);
-    }
-    sq = warp_sum(sq);
-    if (G == 32) return make_float2(m, rsqrtf(fmaf(sq, inv_d, eps)));
-    constexpr int W = G / 32;
-    const int w = (int)(threadIdx.x % G) / 32;
-    if (lane_id() == 0) {
-        s[w] = sum;
-        s[W + w] = sq;
-        s[2 * W + w] = (float)n;
-    }
-    __syncthreads();
-    float tot = 0.0f;
-#pragma unroll
-    for (int i = 0; i < W; ++i) tot += s[i];
-    const float mean = tot / D;
-    float var = 0.0f;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-        const float k = s[2 * W + i];
-        const float d = k > 0.0f ? s[i] / k - mean : 0.0f;
-        var += fmaf(k * d, d, s[W + i]);
-    }
-    return make_float2(mean, rsqrtf(fmaf(var, inv_d, eps)));
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
 }
+__device__ __forceinline__ f32x2 both(float x) { return pair(x, x); }
 
 template <int G>
-constexpr int NORM_BLOCK = G < 256 ? (G == 32 ? 256 : G) : G;
+constexpr int NORM_BLOCK = G <= 32 ? 128 : G;
+// Blocks of an SM: registers for 128 bytes of a row in each thread.
+template <typename TX, int G, int N, bool VEC>
+constexpr int NORM_RESIDENT =
+    (N * (int)sizeof(TX) >= 16 || (!VEC && N >= 4) ? 640 : 1024) / NORM_BLOCK<G>;
 
-// G threads a row, 8 N elements a thread.
+// G threads a row, 8 N elements a thread; a block of G threads, or of four warps that
+// each hold one row or several.  Bound by the bytes of x and y.
 template <typename TX, typename TY, int G, int N, bool VEC>
-__global__ void __launch_bounds__(NORM_BLOCK<G>) norm_kernel(const NormParams p) {
-    constexpr int E = 8 * N, ROWS = NORM_BLOCK<G> / G;
-    __shared__ float s_red[2][3 * G / 32];
+__global__ void __launch_bounds__(NORM_BLOCK<G>, NORM_RESIDENT<TX, G, N, VEC>) norm_kernel(const NormParams p) {
+    constexpr int E = 8 * N, ROWS = NORM_BLOCK<G> / G, L = G < 32 ? G : 32, W = G / 32;
+    __shared__ float2 s_part[2][W > 1 ? W : 1];
     pdl_launch();
     const int t = (int)(threadIdx.x % G), D = (int)p.D;
     const TX* x = static_cast<const TX*>(p.x);
     TY* y = static_cast<TY*>(p.y);
     pdl_wait();
-    float w[E], b[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int64_t c = norm_col<G, VEC>(t, e);
-        w[e] = p.w && c < D ? load_as(p.w, p.w_type, c) : 1.0f;
-        b[e] = p.b && c < D ? load_as(p.b, p.b_type, c) : 0.0f;
-    }
-    const int n = warp_count<G, N, VEC>(t & ~31, D);
+    // elements of this warp's lanes, and of the warp that a lane joins for
+    const float n = (float)warp_count<G, N, VEC>(t - t % L, D);
+    const float inv_n = n > 0.0f ? 1.0f / n : 0.0f;
+    const int lane = (int)lane_id();
+    const float k = W > 1 && lane < W ? (float)warp_count<G, N, VEC>(lane * 32, D) : 0.0f;
     const int64_t step = (int64_t)gridDim.x * ROWS;
-    int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / G;
     int flip = 0;
-    RowRegs<TX, N, VEC> next;
-    float next_c = 0.0f;
-    if (r < p.T) {
-        load_row<TX, G, N, VEC>(x + r * p.ldx, t, D, next);
-        next_c = to_f32(x[r * p.ldx]);
-    }
-    for (; r < p.T; r += step) {
-        const RowRegs<TX, N, VEC> v = next;
-        if (r + step < p.T) load_row<TX, G, N, VEC>(x + (r + step) * p.ldx, t, D, next);
-        const float c = next_c;
-        if (r + step < p.T) next_c = to_f32(x[(r + step) * p.ldx]);
-        auto in = [&](int e) { return norm_col<G, VEC>(t, e) < D; };
-        float o[E];
+    // (the lanes of a warp go on together: a warp's last rows may not exist)
+    for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < p.T; r0 += step) {
+        const int64_t r = r0 + (G <= 32 ? threadIdx.x / G : 0);
+        const bool here = r < p.T;
+        const TX* row = x + (here ? r : 0) * p.ldx;
+        RowRegs<TX, N, VEC> v;
+        load_row<TX, G, N, VEC>(row, t, D, v);
+        const float c = to_f32(row[0]);
+        const auto in = [&](int e) { return norm_col<G, VEC>(t, VEC ? e / 8 * 8 : e) < D; };
+        f32x2 sum2 = 0;
+        float sum = 0.0f;
+        if (VEC) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = v.get(e) - c;
-        const float2 m = row_statistics<G, E>(o, in, n, (float)D, p.inv_d, p.eps, s_red[flip]);
-        flip ^= 1;
+            for (int j = 0; j < N; ++j)
+                if (in(8 * j)) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf((o[e] - m.x) * m.y, w[e], b[e]);
-        store_row<TY, G, N, VEC>(y + r * p.ldy, t, D, o);
-        if (t == 0) {
-            if (p.mean) p.mean[r] = c + m.x;
-            if (p.rstd) p.rstd[r] = m.y;
+                    for (int i = 4 * j; i < 4 * j + 4; ++i) sum2 = add2(sum2, add2(v.two(i), both(-c)));
+                }
+            const float2 s = parts(sum2);
+            sum = s.x + s.y;
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) sum += in(e) ? v.get(e) - c : 0.0f;
+        }
+        // the mean of the warp's elements, less c, and the squares of the distances from it
+        float m = lanes_sum<L>(sum) * inv_n;
+        f32x2 sq2 = 0;
+        float sq = 0.0f;
+        if (VEC) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (in(8 * j)) {
+#pragma unroll
+                    for (int i = 4 * j; i < 4 * j + 4; ++i) {
+                        const f32x2 d = add2(add2(v.two(i), both(-c)), both(-m));
+                        sq2 = fma2(d, d, sq2);
+                    }
+                }
+            const float2 s = parts(sq2);
+            sq = s.x + s.y;
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float d = in(e) ? (v.get(e) - c) - m : 0.0f;
+                sq = fmaf(d, d, sq);
+            }
+        }
+        sq = lanes_sum<L>(sq);
+        if (W > 1) {
+            if (lane == 0) s_part[flip][t / 32] = make_float2(m, sq);
+            __syncthreads();
+            const float2 o = lane < W ? s_part[flip][lane] : make_float2(0.0f, 0.0f);
+            flip ^= 1;
+            m = warp_sum(k * o.x) * p.inv_d;
+            const float d = o.x - m;
+            sq = warp_sum(fmaf(k * d, d, o.y));
+        }
+        const float rstd = rsqrtf(fmaf(sq, p.inv_d, p.eps));
+        if (here) {
+            RowRegs<TY, N, VEC> o;
+            if (VEC) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    if (!in(8 * j)) continue;
+                    f32x2 w[4], b[4];
+                    const int col = norm_col<G, VEC>(t, 8 * j);
+                    if (p.w) load8_as(p.w, p.w_type, col, w);
+                    if (p.b) load8_as(p.b, p.b_type, col, b);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const f32x2 d = add2(add2(v.two(4 * j + i), both(-c)), both(-m));
+                        const f32x2 xh = mul2(d, both(rstd));
+                        o.put_two(4 * j + i, p.w ? fma2(xh, w[i], p.b ? b[i] : 0ull)
+                                                 : p.b ? add2(xh, b[i]) : xh);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int col = norm_col<G, VEC>(t, e);
+                    const float w = p.w && col < D ? load_as(p.w, p.w_type, col) : 1.0f;
+                    const float b = p.b && col < D ? load_as(p.b, p.b_type, col) : 0.0f;
+                    reinterpret_cast<TY*>(o.v)[e] =
+                        from_f32<TY>(fmaf(((v.get(e) - c) - m) * rstd, w, b));
+                }
+            }
+            store_row<TY, G, N, VEC>(y + r * p.ldy, t, D, o);
+            if (t == 0) {
+                if (p.mean) p.mean[r] = c + m;
+                if (p.rstd) p.rstd[r] = rstd;
+            }
         }
     }
 }
@@ -239,223 +316,6 @@ __global__ void __launch_bounds__(NL_THREADS) norm_long_kernel(const NormParams 
         if (threadIdx.x == 0) {
             if (p.mean) p.mean[r] = first + mean;
             if (p.rstd) p.rstd[r] = rstd;
-        }
-    }
-}
-
-// ----------------------------------------------------------------- gradient
-
-struct NormGradParams {
-    const void* dy;
-    const void* x;
-    const float* mean;
-    const float* rstd;
-    const void* w;                 // or null
-    void* dx;                      // x's type
-    float* part;                   // [parts][2][D]: column sums of dy xh and of dy; or null
-    int64_t T, D, ldy, ldx, lddx;
-    int32_t w_type;
-    float inv_d;
-};
-
-template <typename TX, typename TD, int G, int N, bool VEC>
-__global__ void __launch_bounds__(NORM_BLOCK<G>) norm_grad_kernel(const NormGradParams p) {
-    constexpr int E = 8 * N, BLOCK = NORM_BLOCK<G>, ROWS = BLOCK / G, W = G / 32;
-    __shared__ float s_red[2][2 * W];
-    __shared__ float s_col[ROWS > 1 ? G * E : 1];
-    pdl_launch();
-    const int t = (int)(threadIdx.x % G), D = (int)p.D;
-    const TX* x = static_cast<const TX*>(p.x);
-    const TD* dy = static_cast<const TD*>(p.dy);
-    TX* dx = static_cast<TX*>(p.dx);
-    pdl_wait();
-    float w[E], dw[E], db[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int64_t c = norm_col<G, VEC>(t, e);
-        w[e] = p.w && c < D ? load_as(p.w, p.w_type, c) : 1.0f;
-        dw[e] = db[e] = 0.0f;
-    }
-    const int64_t step = (int64_t)gridDim.x * ROWS;
-    int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / G;
-    int flip = 0;
-    RowRegs<TX, N, VEC> nx;
-    RowRegs<TD, N, VEC> nd;
-    float nm = 0.0f, nr = 0.0f;
-    auto fetch = [&](int64_t row) {
-        load_row<TX, G, N, VEC>(x + row * p.ldx, t, D, nx);
-        load_row<TD, G, N, VEC>(dy + row * p.ldy, t, D, nd);
-        nm = p.mean[row];
-        nr = p.rstd[row];
-    };
-    if (r < p.T) fetch(r);
-    for (; r < p.T; r += step) {
-        const RowRegs<TX, N, VEC> vx = nx;
-        const RowRegs<TD, N, VEC> vd = nd;
-        const float mean = nm, rstd = nr;
-        if (r + step < p.T) fetch(r + step);
-        // (dy is 0 past the end, so nothing there counts)
-        float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float d = vd.get(e), xh = (vx.get(e) - mean) * rstd, g = d * w[e];
-            s1 += g;
-            s2 = fmaf(g, xh, s2);
-            dw[e] = fmaf(d, xh, dw[e]);
-            db[e] += d;
-        }
-        s1 = warp_sum(s1);
-        s2 = warp_sum(s2);
-        if (G > 32) {
-            const int wi = t / 32;
-            if (lane_id() == 0) {
-                s_red[flip][wi] = s1;
-                s_red[flip][W + wi] = s2;
-            }
-            __syncthreads();
-            s1 = s2 = 0.0f;
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                s1 += s_red[flip][i];
-                s2 += s_red[flip][W + i];
-            }
-            flip ^= 1;
-        }
-        s1 *= p.inv_d;
-        s2 *= p.inv_d;
-        float o[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float xh = (vx.get(e) - mean) * rstd;
-            o[e] = rstd * (fmaf(vd.get(e), w[e], -s1) - xh * s2);
-        }
-        store_row<TX, G, N, VEC>(dx + r * p.lddx, t, D, o);
-    }
-    if (!p.part) return;
-    float* part = p.part + (int64_t)blockIdx.x * 2 * p.D;
-#pragma unroll
-    for (int k = 0; k < 2; ++k, part += p.D) {
-        float* v = k ? db : dw;
-        // the block's rows, in order
-        for (int i = ROWS - 1; i > 0; --i) {
-            if ((int)threadIdx.x / G == i) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) s_col[e * G + t] = v[e];
-            }
-            __syncthreads();
-            if ((int)threadIdx.x / G == i - 1) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) v[e] += s_col[e * G + t];
-            }
-            __syncthreads();
-        }
-        if ((int)threadIdx.x < G) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int64_t c = norm_col<G, VEC>(t, e);
-                if (c < D) part[c] = v[e];
-            }
-        }
-    }
-}
-
-// Rows of any length: dx by one block a row, two passes over it.
-template <typename TX, typename TD>
-__global__ void __launch_bounds__(NL_THREADS) norm_grad_long_kernel(const NormGradParams p) {
-    __shared__ float s_red[33];
-    pdl_launch();
-    pdl_wait();
-    for (int64_t r = blockIdx.x; r < p.T; r += gridDim.x) {
-        const TX* x = static_cast<const TX*>(p.x) + r * p.ldx;
-        const TD* dy = static_cast<const TD*>(p.dy) + r * p.ldy;
-        TX* dx = static_cast<TX*>(p.dx) + r * p.lddx;
-        const float mean = p.mean[r], rstd = p.rstd[r];
-        float s1 = 0.0f, s2 = 0.0f;
-        for (int64_t c = threadIdx.x; c < p.D; c += NL_THREADS) {
-            const float g = to_f32(dy[c]) * (p.w ? load_as(p.w, p.w_type, c) : 1.0f);
-            s1 += g;
-            s2 = fmaf(g, (to_f32(x[c]) - mean) * rstd, s2);
-        }
-        s1 = block_sum(s1, s_red) * p.inv_d;
-        s2 = block_sum(s2, s_red) * p.inv_d;
-        for (int64_t c = threadIdx.x; c < p.D; c += NL_THREADS) {
-            const float w = p.w ? load_as(p.w, p.w_type, c) : 1.0f;
-            const float xh = (to_f32(x[c]) - mean) * rstd;
-            dx[c] = from_f32<TX>(rstd * (fmaf(to_f32(dy[c]), w, -s1) - xh * s2));
-        }
-    }
-}
-
-// ... and their column sums, 32 rows of blocks by NL_COLS columns.
-constexpr int NL_COLS = 256, NL_PARTS = 32;
-
-template <typename TX, typename TD>
-__global__ void __launch_bounds__(NL_COLS) norm_cols_kernel(const NormGradParams p) {
-    pdl_launch();
-    pdl_wait();
-    const int64_t c = (int64_t)blockIdx.x * NL_COLS + threadIdx.x;
-    if (c >= p.D) return;
-    const TX* x = static_cast<const TX*>(p.x) + c;
-    const TD* dy = static_cast<const TD*>(p.dy) + c;
-    float dw = 0.0f, db = 0.0f;
-    for (int64_t r = blockIdx.y; r < p.T; r += gridDim.y) {
-        const float d = to_f32(dy[r * p.ldy]);
-        dw = fmaf(d, (to_f32(x[r * p.ldx]) - p.mean[r]) * p.rstd[r], dw);
-        db += d;
-    }
-    float* part = p.part + (int64_t)blockIdx.y * 2 * p.D;
-    part[c] = dw;
-    part[p.D + c] = db;
-}
-
-// ------------------------------------------------- the blocks' column sums
-
-struct NormSumParams {
-    const float* part;             // [parts][2][D]
-    Ctrl* ctrl;
-    void* out[2];                  // dw, db (either or both)
-    int64_t D;
-    int32_t parts, type[2], accumulate;
-};
-
-// 32 columns a block; its 8 warps take every eighth part each, in order.
-constexpr int NS_WARPS = 8;
-
-__global__ void __launch_bounds__(32 * NS_WARPS) norm_sum_kernel(const NormSumParams p) {
-    __shared__ float s[NS_WARPS][32];
-    pdl_wait();
-    const int k = (int)blockIdx.y, lane = (int)lane_id(), w = (int)warp_id();
-    if (blockIdx.x == 0 && k == 0 && threadIdx.x == 0) {
-        p.ctrl->path_small = 0;
-        p.ctrl->status = 0;
-    }
-    if (!p.out[k]) return;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-    float v = 0.0f;
-    if (c < p.D) {
-        const float* q = p.part + k * p.D + c;
-#pragma unroll 4
-        for (int i = w; i < p.parts; i += NS_WARPS) v += q[(int64_t)i * 2 * p.D];
-    }
-    s[w][lane] = v;
-    __syncthreads();
-    if (w != 0 || c >= p.D) return;
-#pragma unroll
-    for (int i = 1; i < NS_WARPS; ++i) v += s[i][lane];
-    switch (p.type[k]) {
-        case TOPK_EF_F32: {
-            float* o = static_cast<float*>(p.out[k]) + c;
-            *o = p.accumulate ? *o + v : v;
-            break;
-        }
-        case TOPK_EF_BF16: {
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out[k]) + c;
-            *o = from_f32<__nv_bfloat16>(p.accumulate ? to_f32(*o) + v : v);
-            break;
-        }
-        default: {
-            __half* o = static_cast<__half*>(p.out[k]) + c;
-            *o = from_f32<__half>(p.accumulate ? to_f32(*o) + v : v);
         }
     }
 }

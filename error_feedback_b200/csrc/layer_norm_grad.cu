@@ -1,0 +1,151 @@
+// Host side of layer_norm_grad (include/topk_ef.h): argument checks, workspace layout,
+// choice of kernel by row length: norm_grad_kernel -> norm_sum_kernel, for rows past
+// NM_MAX_GRAD_D norm_cols_kernel -> norm_grad_long_kernel -> norm_sum_kernel.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "topk_ef.h"
+#include "common.cuh"
+#include "kernels_norm_grad.cuh"
+#include "norm_host.cuh"
+
+using namespace tke;
+
+namespace {
+
+// Most blocks (partial rows of the column sums) of a gradient, and the least rows of each.
+constexpr int64_t NG_MAX_PARTS = SMS * 16, NG_ROWS = 4;
+
+int64_t grad_parts(int64_t T) {
+    return std::min<int64_t>(NG_MAX_PARTS, std::max<int64_t>(1, ceil_div64(T, NG_ROWS)));
+}
+
+template <typename TX, typename TD, int G, int N, bool VEC>
+cudaError_t launch_grad(const NormGradParams& p, int32_t& parts, cudaStream_t st) {
+    constexpr int block = GRAD_BLOCK<G>;
+    static const int most = resident(norm_grad_kernel<TX, TD, G, N, VEC>, block);
+    const int64_t rows = ceil_div64(p.T, block / G);
+    parts = (int32_t)std::min(std::min<int64_t>(most, rows), grad_parts(p.T));
+    trace_before(st, "norm_grad_kernel");
+    const cudaError_t e =
+        launch_pdl(norm_grad_kernel<TX, TD, G, N, VEC>, (unsigned)parts, block, st, p);
+    trace_after(st);
+    return e;
+}
+
+template <typename TX, typename TD, bool VEC>
+cudaError_t grad_by_length(const NormGradParams& p, int32_t& parts, cudaStream_t st) {
+    if (p.D <= 64) return launch_grad<TX, TD, 8, 1, VEC>(p, parts, st);
+    if (p.D <= 128) return launch_grad<TX, TD, 16, 1, VEC>(p, parts, st);
+    if (p.D <= 256) return launch_grad<TX, TD, 32, 1, VEC>(p, parts, st);
+    constexpr int N = sizeof(TX) == 4 || sizeof(TD) == 4 ? 1 : 2, F = 2 / N;
+    if (p.D <= 512) return launch_grad<TX, TD, 32 * F, N, VEC>(p, parts, st);
+    if (p.D <= 1024) return launch_grad<TX, TD, 64 * F, N, VEC>(p, parts, st);
+    if (p.D <= 2048) return launch_grad<TX, TD, 128 * F, N, VEC>(p, parts, st);
+    if (p.D <= 4096) return launch_grad<TX, TD, 256 * F, N, VEC>(p, parts, st);
+    if (p.D <= 8192) return launch_grad<TX, TD, 512 * F, N, VEC>(p, parts, st);
+    return launch_grad<TX, TD, 1024, 2, VEC>(p, parts, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t layer_norm_grad_workspace_bytes(int64_t T, int64_t D) {
+    if (!norm_sizes_ok(T, D)) return 0;
+    return align_up(sizeof(Ctrl)) + align_up((size_t)grad_parts(T) * 2 * (size_t)D * 4);
+}
+
+int layer_norm_grad(const void* grad_out, int32_t grad_out_type, int64_t ld_grad_out,
+                    const void* x, int32_t x_type, int64_t ld_x, const float* mean,
+                    const float* rstd, const void* weight, int32_t weight_type, int64_t T,
+                    int64_t D, void* grad_x, int64_t ld_grad_x, void* grad_weight,
+                    int32_t grad_weight_type, void* grad_bias, int32_t grad_bias_type,
+                    int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+    const size_t need = layer_norm_grad_workspace_bytes(T, D);
+    const size_t sx = type_size(x_type), sd = type_size(grad_out_type);
+    const bool cols = grad_weight || grad_bias;
+    if (!need || !sx || !sd || ld_x < D || ld_grad_out < D || ld_grad_x < D)
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (weight && (!type_size(weight_type) || !pointer_ok(weight, weight_type)))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (grad_weight && (!type_size(grad_weight_type) || !pointer_ok(grad_weight, grad_weight_type)))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (grad_bias && (!type_size(grad_bias_type) || !pointer_ok(grad_bias, grad_bias_type)))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (cols && (grad_weight == grad_bias || !ws || !aligned(ws, ALIGN)))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (T > 0 && (!pointer_ok(grad_out, grad_out_type) || !pointer_ok(x, x_type) ||
+                  !pointer_ok(grad_x, x_type) || !pointer_ok(mean, TOPK_EF_F32) ||
+                  !pointer_ok(rstd, TOPK_EF_F32)))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (T > 0 && ((grad_x == x && ld_grad_x != ld_x) ||
+                  (grad_x == grad_out && (sx != sd || ld_grad_x != ld_grad_out))))
+        return TOPK_EF_ERR_INVALID_ARG;
+    if (cols && ws_bytes < need) return TOPK_EF_ERR_WORKSPACE;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    NormGradParams p = {};
+    p.dy = grad_out;
+    p.x = x;
+    p.mean = mean;
+    p.rstd = rstd;
+    p.w = weight;
+    p.dx = grad_x;
+    p.part = cols ? reinterpret_cast<float*>(static_cast<char*>(ws) + align_up(sizeof(Ctrl))) : nullptr;
+    p.T = T;
+    p.D = D;
+    p.ldy = ld_grad_out;
+    p.ldx = ld_x;
+    p.lddx = ld_grad_x;
+    p.w_type = weight_type;
+    p.inv_d = 1.0f / (float)D;
+    int32_t parts = 0;
+    cudaError_t e = cudaSuccess;
+    if (T > 0) {
+        const bool vec = D % 8 == 0 && rows16(x, ld_x, sx) && rows16(grad_x, ld_grad_x, sx) &&
+                         rows16(grad_out, ld_grad_out, sd);
+        e = with_type(x_type, [&](auto tx) {
+            return with_type(grad_out_type, [&](auto td) {
+                using TX = decltype(tx);
+                using TD = decltype(td);
+                if (D <= NM_MAX_GRAD_D)
+                    return vec ? grad_by_length<TX, TD, true>(p, parts, st)
+                               : grad_by_length<TX, TD, false>(p, parts, st);
+                cudaError_t r = cudaSuccess;
+                if (cols) {      // first: grad_x may be x or grad_out
+                    parts = (int32_t)std::min<int64_t>(grad_parts(T), NL_PARTS);
+                    trace_before(st, "norm_cols_kernel");
+                    r = launch_pdl(norm_cols_kernel<TX, TD>,
+                                   dim3((unsigned)ceil_div64(D, NL_COLS), (unsigned)parts), NL_COLS,
+                                   st, p);
+                    trace_after(st);
+                    if (r != cudaSuccess) return r;
+                }
+                trace_before(st, "norm_grad_long_kernel");
+                r = launch_pdl(norm_grad_long_kernel<TX, TD>, (unsigned)std::min<int64_t>(T, SMS * 4),
+                               NL_THREADS, st, p);
+                trace_after(st);
+                return r;
+            });
+        });
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    if (!cols) return TOPK_EF_OK;
+    NormSumParams s = {};
+    s.part = p.part;
+    s.ctrl = static_cast<Ctrl*>(ws);
+    s.out[0] = grad_weight;
+    s.out[1] = grad_bias;
+    s.type[0] = grad_weight_type;
+    s.type[1] = grad_bias_type;
+    s.D = D;
+    s.parts = parts;
+    s.accumulate = accumulate ? 1 : 0;
+    trace_before(st, "norm_sum_kernel");
+    e = launch_pdl(norm_sum_kernel, dim3((unsigned)ceil_div64(D, 32), 2), 32 * NS_WARPS, st, s);
+    trace_after(st);
+    return e == cudaSuccess ? TOPK_EF_OK : cuda_fail(e);
+}
+
+}  // extern "C"
