@@ -8,16 +8,18 @@
 // squares of the differences from its own elements' mean, and the warps' (count,
 // sum, squares) are joined by sum n (mean_w - mean)^2.
 //
-// A row is held in registers by 8 to 512 threads between the statistics and the result, 8 to
-// 64 elements each (32 of fp32): the fewer threads, the less joining, and what is in flight
-// is the warps' rows.  (16 elements a thread with the next row loaded ahead took 33
-// instructions an element, most of them for joining, and 108 us for 16,384 x 4,096 bf16.)
-// Rows past NM_MAX_D columns are read again instead.
+// A row is held in registers by 8 to 1,024 threads, 16 elements each, between the statistics
+// and the result; w and b stay in registers over all rows of a block.  The rows that follow
+// are on their way into a ring of shared memory (NR_SLOTS rows, asynchronous copies), so
+// what is in flight takes no registers.  (Loads into registers one row ahead: 108 us
+// instead of NN for 16,384 x 4,096 bf16; 64 elements a thread, w and b converted for every
+// row, nothing ahead: 74.)  Rows past NM_MAX_D columns are read again instead.
 #pragma once
 
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "async.cuh"
 #include "common.cuh"
 #include "elements.cuh"
 #include "topk_ef.h"
@@ -44,118 +46,125 @@ __device__ __forceinline__ float load_as(const void* p, int32_t type, int64_t i)
     return to_f32(static_cast<const __half*>(p)[i]);
 }
 
-// The thread's elements of a row of G threads: groups of 8 columns (VEC; 16-byte aligned), or
-// columns G apart (rows that start anywhere).  Element e of thread t:
-template <int G, bool VEC>
+constexpr int NR_ELEMS = 16;               // of a thread and row
+
+// Columns of a group that a thread takes as a whole: 16 bytes of the wider type, so that a
+// warp's accesses are consecutive.  (Two accesses of 16 bytes at a stride of 32 touch every
+// sector twice: 102 us for 16,384 x 4,096 fp32 to bf16 instead of NN.)
+template <typename TA, typename TB>
+constexpr int NORM_GROUP = sizeof(TA) + sizeof(TB) == 4 ? 8 : 4;
+
+// Column of element e of thread t of a row of G threads: groups of V columns, or V = 1 (rows
+// that start anywhere).
+template <int G, int V>
 __device__ __forceinline__ int norm_col(int t, int e) {
-    return VEC ? ((e / 8) * G + t) * 8 + e % 8 : e * G + t;
+    return ((e / V) * G + t) * V + e % V;
 }
 
-template <typename T, int N, bool VEC>
+template <typename T>
 struct RowRegs {
-    Vec8<T> v[N];                  // 8 N elements
-    __device__ __forceinline__ float get(int e) const {
-        return to_f32(reinterpret_cast<const T*>(v)[e]);
-    }
+    uint32_t q[NR_ELEMS * sizeof(T) / 4];
     // elements 2 i and 2 i + 1
     __device__ __forceinline__ f32x2 two(int i) const {
         if constexpr (sizeof(T) == 4) {
-            return reinterpret_cast<const f32x2*>(v)[i];
+            return pair(__uint_as_float(q[2 * i]), __uint_as_float(q[2 * i + 1]));
         } else {
-            return widen(reinterpret_cast<const typename Twin<T>::type*>(v)[i]);
+            return widen(reinterpret_cast<const typename Twin<T>::type*>(q)[i]);
         }
     }
     __device__ __forceinline__ void put_two(int i, f32x2 a) {
         if constexpr (sizeof(T) == 4) {
-            reinterpret_cast<f32x2*>(v)[i] = a;
+            const float2 f = parts(a);
+            q[2 * i] = __float_as_uint(f.x);
+            q[2 * i + 1] = __float_as_uint(f.y);
         } else {
-            reinterpret_cast<uint32_t*>(v)[i] = narrow(a, T{});
+            q[i] = narrow(a, T{});
         }
     }
 };
 
-// Loads the thread's elements; those past the row's end are zero.
-template <typename T, int G, int N, bool VEC>
-__device__ __forceinline__ void load_row(const T* row, int t, int D, RowRegs<T, N, VEC>& r) {
-    if (VEC) {
+// Stores the thread's elements of a row.
+template <typename T, int G, int V>
+__device__ __forceinline__ void store_row(T* row, int t, int D, const RowRegs<T>& r) {
+    constexpr int WORDS = V * (int)sizeof(T) / 4;
+    if (V > 1) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int c = (j * G + t) * 8;
-            if (c < D) {
-                r.v[j] = load8(row + c);
-            } else {
-#pragma unroll
-                for (int k = 0; k < (int)(sizeof(T) / 2); ++k) r.v[j].q[k] = make_uint4(0, 0, 0, 0);
-            }
-        }
-    } else {
-        T* e = reinterpret_cast<T*>(r.v);
-#pragma unroll
-        for (int j = 0; j < 8 * N; ++j) {
-            const int c = j * G + t;
-            e[j] = c < D ? row[c] : from_f32<T>(0.0f);
-        }
-    }
-}
-
-template <typename T, int G, int N, bool VEC>
-__device__ __forceinline__ void store_row(T* row, int t, int D, const RowRegs<T, N, VEC>& r) {
-    if (VEC) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int c = (j * G + t) * 8;
+        for (int j = 0; j < NR_ELEMS / V; ++j) {
+            const int c = (j * G + t) * V;
+            const uint32_t* q = r.q + j * WORDS;
             if (c >= D) continue;
-            if (sizeof(T) == 4 && (uintptr_t)(row + c) % 32 == 0) {
-                store32b(row + c, r.v[j].q);
+            if (WORDS == 4) {
+                *reinterpret_cast<uint4*>(row + c) = make_uint4(q[0], q[1], q[2], q[WORDS - 1]);
             } else {
-#pragma unroll
-                for (int k = 0; k < (int)(sizeof(T) / 2); ++k)
-                    reinterpret_cast<uint4*>(row + c)[k] = r.v[j].q[k];
+                *reinterpret_cast<uint2*>(row + c) = make_uint2(q[0], q[1]);
             }
         }
     } else {
-        const T* e = reinterpret_cast<const T*>(r.v);
+        const T* e = reinterpret_cast<const T*>(r.q);
 #pragma unroll
-        for (int j = 0; j < 8 * N; ++j) {
+        for (int j = 0; j < NR_ELEMS; ++j) {
             const int c = j * G + t;
             if (c < D) row[c] = e[j];
         }
     }
 }
 
-// Eight consecutive weights from c on (c and p 16-byte aligned steps), as pairs.
-__device__ __forceinline__ void load8_as(const void* p, int32_t type, int c, f32x2* o) {
-    if (type == TOPK_EF_F32) {
-        RowRegs<float, 1, true> r;
-        r.v[0] = load8(static_cast<const float*>(p) + c);
+// V consecutive weights from c on (p and c in steps of 16 bytes), as pairs; without p each is
+// `none`.
+template <typename T, int V>
+__device__ __forceinline__ void load_group(const T* p, f32x2* o) {
+    RowRegs<T> r;
+    constexpr int WORDS = V * (int)sizeof(T) / 4;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = r.two(i);
+    for (int k = 0; k < WORDS / 2; ++k) {
+        const uint2 v = reinterpret_cast<const uint2*>(p)[k];
+        r.q[2 * k] = v.x;
+        r.q[2 * k + 1] = v.y;
+    }
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) o[i] = r.two(i);
+}
+template <int V>
+__device__ __forceinline__ void load_as(const void* p, int32_t type, int c, float none, f32x2* o) {
+    if (!p) {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) o[i] = pair(none, none);
+    } else if (type == TOPK_EF_F32) {
+        load_group<float, V>(static_cast<const float*>(p) + c, o);
     } else if (type == TOPK_EF_BF16) {
-        RowRegs<__nv_bfloat16, 1, true> r;
-        r.v[0] = load8(static_cast<const __nv_bfloat16*>(p) + c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = r.two(i);
+        load_group<__nv_bfloat16, V>(static_cast<const __nv_bfloat16*>(p) + c, o);
     } else {
-        RowRegs<__half, 1, true> r;
-        r.v[0] = load8(static_cast<const __half*>(p) + c);
+        load_group<__half, V>(static_cast<const __half*>(p) + c, o);
+    }
+}
+// The thread's weights of a row, as load_as.
+template <int G, int V>
+__device__ __forceinline__ void row_weights(const void* p, int32_t type, int t, int D, float none,
+                                            f32x2* o) {
+    if constexpr (V > 1) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = r.two(i);
+        for (int j = 0; j < NR_ELEMS / V; ++j) {
+            const int c = norm_col<G, V>(t, j * V);
+            load_as<V>(c < D ? p : nullptr, type, c, none, o + j * V / 2);
+        }
+    } else {
+        const auto at = [&](int e) {
+            const int c = norm_col<G, V>(t, e);
+            return p && c < D ? load_as(p, type, c) : none;
+        };
+#pragma unroll
+        for (int i = 0; i < NR_ELEMS / 2; ++i) o[i] = pair(at(2 * i), at(2 * i + 1));
     }
 }
 
-// Elements that the lanes of one warp (VEC: or part of it) hold of a row; t0: the row's
-// thread that the lanes start at.
-template <int G, int N, bool VEC>
+// Elements that the lanes of one warp (or part of it) hold of a row; t0: the row's thread that
+// the lanes start at.
+template <int G, int V>
 __device__ __forceinline__ int warp_count(int t0, int D) {
     constexpr int L = G < 32 ? G : 32;
     int n = 0;
-    if (VEC) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) n += min(max(D - (j * G + t0) * 8, 0), L * 8);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8 * N; ++j) n += min(max(D - (j * G + t0), 0), L);
-    }
+    for (int j = 0; j < NR_ELEMS / V; ++j) n += min(max(D - (j * G + t0) * V, 0), L * V);
     return n;
 }
 
@@ -167,120 +176,228 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }
 __device__ __forceinline__ f32x2 both(float x) { return pair(x, x); }
 
+// Threads of a block: rows of fewer threads share one.
 template <int G>
-constexpr int NORM_BLOCK = G <= 32 ? 128 : G;
-// Blocks of an SM: registers for 128 bytes of a row in each thread.
-template <typename TX, int G, int N, bool VEC>
-constexpr int NORM_RESIDENT =
-    (N * (int)sizeof(TX) >= 16 || (!VEC && N >= 4) ? 640 : 1024) / NORM_BLOCK<G>;
+constexpr int NORM_BLOCK = G < 256 ? 256 : G;
 
-// G threads a row, 8 N elements a thread; a block of G threads, or of four warps that
-// each hold one row or several.  Bound by the bytes of x and y.
-template <typename TX, typename TY, int G, int N, bool VEC>
-__global__ void __launch_bounds__(NORM_BLOCK<G>, NORM_RESIDENT<TX, G, N, VEC>) norm_kernel(const NormParams p) {
-    constexpr int E = 8 * N, ROWS = NORM_BLOCK<G> / G, L = G < 32 ? G : 32, W = G / 32;
-    __shared__ float2 s_part[2][W > 1 ? W : 1];
+// Waits for the G threads of a row (32 < G < 256: a barrier of its own for each row of the block).
+template <int G>
+__device__ __forceinline__ void row_sync() {
+    if (G <= 32) {
+        __syncwarp();
+    } else if (G >= 256) {
+        __syncthreads();
+    } else {
+        asm volatile("bar.sync %0, %1;" ::"r"((int)threadIdx.x / G + 1), "n"(G) : "memory");
+    }
+}
+
+// ------------------------------------------------------ rows through a ring
+
+// Rows of the ring: what 227 KB leave of an SM's three blocks (768 threads).
+template <typename T, int G>
+constexpr int NR_SLOTS = sizeof(T) == 2 ? 4 : G >= 1024 ? 2 : 3;
+
+// Bytes of one row of G threads in it.  (Rows that start anywhere: in their 16-byte granules.)
+template <typename T, int G, int V>
+constexpr int NR_BYTES = G * NR_ELEMS * (int)sizeof(T) + (V > 1 ? 0 : 32);
+
+__device__ __forceinline__ void copy_async16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_async8(uint32_t to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+}
+// `bytes` (2 or 4) of a word; zero after them.
+__device__ __forceinline__ void copy_async4(uint32_t to, const void* from, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most N groups of the thread's copies are on their way.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Begins to copy a row of D elements.  Of a row that starts within a 4-byte word the first
+// element is left out (read_row takes it from the caller).
+template <typename T, int G, int V>
+__device__ __forceinline__ void copy_row(uint32_t slot, const T* row, int t, int D) {
+    if (V > 1) {
+        constexpr int BYTES = V * (int)sizeof(T);
+#pragma unroll
+        for (int j = 0; j < NR_ELEMS / V; ++j) {
+            const int c = (j * G + t) * V;
+            if (c >= D) continue;
+            const uint32_t to = slot + (uint32_t)(j * G + t) * BYTES;
+            if (BYTES == 16) {
+                copy_async16(to, row + c);
+            } else {
+                copy_async8(to, row + c);
+            }
+        }
+    } else {
+        const int lead = (int)((uintptr_t)row & 15), end = lead + D * (int)sizeof(T);
+        const char* from = reinterpret_cast<const char*>(row) - lead;
+#pragma unroll
+        for (int i = 0; i < NR_ELEMS * (int)sizeof(T) / 16 + 1; ++i) {
+            const int at = (i * G + t) * 16;
+            if (at >= lead && at + 16 <= end) {
+                copy_async16(slot + at, from + at);
+            } else if (at < end) {
+                // the row's ragged ends
+                for (int w = at; w < at + 16; w += 4)
+                    if (w >= lead && w < end) copy_async4(slot + w, from + w, min(4, end - w));
+            }
+        }
+    }
+}
+
+// Bit e: element e of the thread is in the row.
+template <int G, int V>
+__device__ __forceinline__ uint32_t elems_mask(int t, int D) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < NR_ELEMS; ++e) m |= (uint32_t)(norm_col<G, V>(t, e) < D) << e;
+    return m;
+}
+
+// The thread's elements of a copied row; zero where it has none.  `first`: the row's first.
+template <typename T, int G, int V>
+__device__ __forceinline__ void read_row(const char* slot, const T* row, int t, uint32_t mask, T first,
+                                         RowRegs<T>& r) {
+    if (V > 1) {
+        constexpr int WORDS = V * (int)sizeof(T) / 4;
+#pragma unroll
+        for (int j = 0; j < NR_ELEMS / V; ++j) {
+            const bool in = mask >> V * j & 1;
+            uint32_t* q = r.q + j * WORDS;
+            if (WORDS == 4) {
+                const uint4 v = in ? reinterpret_cast<const uint4*>(slot)[j * G + t] : make_uint4(0, 0, 0, 0);
+                q[0] = v.x;
+                q[1] = v.y;
+                q[2] = v.z;
+                q[WORDS - 1] = v.w;
+            } else {
+                const uint2 v = in ? reinterpret_cast<const uint2*>(slot)[j * G + t] : make_uint2(0, 0);
+                q[0] = v.x;
+                q[1] = v.y;
+            }
+        }
+    } else {
+        const int lead = (int)((uintptr_t)row & 15);
+        const T* at = reinterpret_cast<const T*>(slot + lead) + t;
+        T* e = reinterpret_cast<T*>(r.q);
+#pragma unroll
+        for (int j = 0; j < NR_ELEMS; ++j) e[j] = mask >> j & 1 ? at[j * G] : from_f32<T>(0.0f);
+        if (sizeof(T) == 2 && t == 0 && (lead & 2)) e[0] = first;
+    }
+}
+
+// Sums over the G threads of a row of (a, b), which each of a warp's lanes holds already summed
+// over its warp; s: two places a warp, `flip` the ones that the last call did not use.
+// Also a barrier of the row.
+template <int G, typename F>
+__device__ __forceinline__ float2 row_parts(float2 v, float2 (*s)[NORM_BLOCK<G> / 32], int& flip, F f) {
+    constexpr int W = G < 64 ? 1 : G / 32;
+    if (W == 1) {
+        __syncwarp();
+        return v;
+    }
+    const int warp = (int)warp_id(), lane = (int)lane_id();
+    if (lane == 0) s[flip][warp] = v;
+    row_sync<G>();
+    const float2 o = s[flip][warp / W * W + lane % W];     // (lanes W apart hold the same)
+    flip ^= 1;
+    return f(o);
+}
+
+// The pair of elements 2 e and 2 e + 1, 0 where the thread has none.
+template <int V>
+__device__ __forceinline__ f32x2 masked(f32x2 a, uint32_t mask, int e) {
+    if (V > 1) return mask >> 2 * e & 1 ? a : 0;
+    const float2 f = parts(a);
+    return pair(mask >> 2 * e & 1 ? f.x : 0.0f, mask >> (2 * e + 1) & 1 ? f.y : 0.0f);
+}
+
+// G threads a row.  Bound by the bytes of x and y.
+template <typename TX, typename TY, int G, int V>
+__global__ void __launch_bounds__(NORM_BLOCK<G>, G <= 256 ? 3 : 1) norm_kernel(const NormParams p) {
+    constexpr int E = NR_ELEMS, ROWS = NORM_BLOCK<G> / G, L = G < 32 ? G : 32, W = G < 64 ? 1 : G / 32;
+    constexpr int S = NR_SLOTS<TX, G>, BYTES = NR_BYTES<TX, G, V>;
+    extern __shared__ __align__(16) char s_ring[];     // [row of the block][S][BYTES]
+    __shared__ float2 s_part[2][NORM_BLOCK<G> / 32];
     pdl_launch();
-    const int t = (int)(threadIdx.x % G), D = (int)p.D;
+    const int t = (int)(threadIdx.x % G), D = (int)p.D, lane = (int)lane_id();
     const TX* x = static_cast<const TX*>(p.x);
     TY* y = static_cast<TY*>(p.y);
+    char* ring = s_ring + threadIdx.x / G * (S * BYTES);
+    const uint32_t ring_at = smem_u32(ring);
     pdl_wait();
-    // elements of this warp's lanes, and of the warp that a lane joins for
-    const float n = (float)warp_count<G, N, VEC>(t - t % L, D);
-    const float inv_n = n > 0.0f ? 1.0f / n : 0.0f;
-    const int lane = (int)lane_id();
-    const float k = W > 1 && lane < W ? (float)warp_count<G, N, VEC>(lane * 32, D) : 0.0f;
     const int64_t step = (int64_t)gridDim.x * ROWS;
-    int flip = 0;
+    int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / G;
     // (the lanes of a warp go on together: a warp's last rows may not exist)
-    for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < p.T; r0 += step) {
-        const int64_t r = r0 + (G <= 32 ? threadIdx.x / G : 0);
-        const bool here = r < p.T;
-        const TX* row = x + (here ? r : 0) * p.ldx;
-        RowRegs<TX, N, VEC> v;
-        load_row<TX, G, N, VEC>(row, t, D, v);
-        const float c = to_f32(row[0]);
-        const auto in = [&](int e) { return norm_col<G, VEC>(t, VEC ? e / 8 * 8 : e) < D; };
-        f32x2 sum2 = 0;
-        float sum = 0.0f;
-        if (VEC) {
+    const int64_t first = r - (G < 32 ? lane / G : 0);
+    const int64_t rounds = first < p.T ? ceil_div64(p.T - first, step) : 0;
 #pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (in(8 * j)) {
+    for (int i = 0; i < S - 1; ++i) {
+        if (r + i * step < p.T) copy_row<TX, G, V>(ring_at + i * BYTES, x + (r + i * step) * p.ldx, t, D);
+        copies_commit();
+    }
+    TX next_c = r < p.T ? x[r * p.ldx] : from_f32<TX>(0.0f);
+    // elements of this warp's lanes, and of the warp that a lane joins for
+    const float n = (float)warp_count<G, V>(t - t % L, D), inv_n = n > 0.0f ? 1.0f / n : 0.0f;
+    const float k = W > 1 ? (float)warp_count<G, V>(lane % W * 32, D) : 0.0f;
+    const uint32_t mask = elems_mask<G, V>(t, D);
+    f32x2 w[E / 2], b[E / 2];
+    row_weights<G, V>(p.w, p.w_type, t, D, 1.0f, w);
+    row_weights<G, V>(p.b, p.b_type, t, D, 0.0f, b);
+    copies_wait<S - 2>();
+    row_sync<G>();
+    int flip = 0, slot = 0, free_slot = S - 1;
+    for (int64_t i = 0; i < rounds; ++i, r += step) {
+        const TX* row = x + r * p.ldx;
+        if (r + (S - 1) * step < p.T)
+            copy_row<TX, G, V>(ring_at + free_slot * BYTES, row + (S - 1) * step * p.ldx, t, D);
+        copies_commit();
+        RowRegs<TX> v;
+        read_row<TX, G, V>(ring + slot * BYTES, row, t, mask, next_c, v);
+        const f32x2 c = both(-to_f32(next_c));
+        if (r + step < p.T) next_c = row[step * p.ldx];
+        free_slot = slot;
+        slot = slot + 1 == S ? 0 : slot + 1;
+        // d = x - c, 0 past the row's end
+        f32x2 d[E / 2], sum = 0;
 #pragma unroll
-                    for (int i = 4 * j; i < 4 * j + 4; ++i) sum2 = add2(sum2, add2(v.two(i), both(-c)));
-                }
-            const float2 s = parts(sum2);
-            sum = s.x + s.y;
-        } else {
+        for (int e = 0; e < E / 2; ++e) d[e] = masked<V>(add2(v.two(e), c), mask, e);
 #pragma unroll
-            for (int e = 0; e < E; ++e) sum += in(e) ? v.get(e) - c : 0.0f;
-        }
+        for (int e = 0; e < E / 2; ++e) sum = add2(sum, d[e]);
+        const float2 s = parts(sum);
         // the mean of the warp's elements, less c, and the squares of the distances from it
-        float m = lanes_sum<L>(sum) * inv_n;
+        const float m0 = lanes_sum<L>(s.x + s.y) * inv_n;
         f32x2 sq2 = 0;
-        float sq = 0.0f;
-        if (VEC) {
 #pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (in(8 * j)) {
-#pragma unroll
-                    for (int i = 4 * j; i < 4 * j + 4; ++i) {
-                        const f32x2 d = add2(add2(v.two(i), both(-c)), both(-m));
-                        sq2 = fma2(d, d, sq2);
-                    }
-                }
-            const float2 s = parts(sq2);
-            sq = s.x + s.y;
-        } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float d = in(e) ? (v.get(e) - c) - m : 0.0f;
-                sq = fmaf(d, d, sq);
-            }
+        for (int e = 0; e < E / 2; ++e) {
+            const f32x2 q = masked<V>(add2(d[e], both(-m0)), mask, e);
+            sq2 = fma2(q, q, sq2);
         }
-        sq = lanes_sum<L>(sq);
-        if (W > 1) {
-            if (lane == 0) s_part[flip][t / 32] = make_float2(m, sq);
-            __syncthreads();
-            const float2 o = lane < W ? s_part[flip][lane] : make_float2(0.0f, 0.0f);
-            flip ^= 1;
-            m = warp_sum(k * o.x) * p.inv_d;
-            const float d = o.x - m;
-            sq = warp_sum(fmaf(k * d, d, o.y));
-        }
-        const float rstd = rsqrtf(fmaf(sq, p.inv_d, p.eps));
-        if (here) {
-            RowRegs<TY, N, VEC> o;
-            if (VEC) {
+        const float2 q = parts(sq2);
+        copies_wait<S - 2>();                          // (the next row, before the barrier)
+        const float2 tot = row_parts<G>(
+            make_float2(m0, lanes_sum<L>(q.x + q.y)), s_part, flip, [&](float2 o) {
+                const float m = lanes_sum<W>(k * o.x) * p.inv_d, far = o.x - m;
+                return make_float2(m, lanes_sum<W>(fmaf(k * far, far, o.y)));
+            });
+        const float rstd = rsqrtf(fmaf(tot.y, p.inv_d, p.eps));
+        if (r < p.T) {
+            RowRegs<TY> o;
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    if (!in(8 * j)) continue;
-                    f32x2 w[4], b[4];
-                    const int col = norm_col<G, VEC>(t, 8 * j);
-                    if (p.w) load8_as(p.w, p.w_type, col, w);
-                    if (p.b) load8_as(p.b, p.b_type, col, b);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const f32x2 d = add2(add2(v.two(4 * j + i), both(-c)), both(-m));
-                        const f32x2 xh = mul2(d, both(rstd));
-                        o.put_two(4 * j + i, p.w ? fma2(xh, w[i], p.b ? b[i] : 0ull)
-                                                 : p.b ? add2(xh, b[i]) : xh);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int col = norm_col<G, VEC>(t, e);
-                    const float w = p.w && col < D ? load_as(p.w, p.w_type, col) : 1.0f;
-                    const float b = p.b && col < D ? load_as(p.b, p.b_type, col) : 0.0f;
-                    reinterpret_cast<TY*>(o.v)[e] =
-                        from_f32<TY>(fmaf(((v.get(e) - c) - m) * rstd, w, b));
-                }
-            }
-            store_row<TY, G, N, VEC>(y + r * p.ldy, t, D, o);
+            for (int e = 0; e < E / 2; ++e)
+                o.put_two(e, fma2(mul2(add2(d[e], both(-tot.x)), both(rstd)), w[e], b[e]));
+            store_row<TY, G, V>(y + r * p.ldy, t, D, o);
             if (t == 0) {
-                if (p.mean) p.mean[r] = c + m;
+                if (p.mean) p.mean[r] = tot.x - parts(c).x;
                 if (p.rstd) p.rstd[r] = rstd;
             }
         }

@@ -5,7 +5,7 @@
 // A row is held in registers by 8 to 1,024 threads, 16 elements each (8 of fp32), which keep to
 // their columns over all of a block's rows, so w and the column sums stay in registers.
 // Column sums leave one fp32 row per block, added in a fixed order by a second kernel: no
-// floating-point atomics.  Rows past NM_MAX_GRAD_D columns are read again instead.
+// floating-point atomics.  Rows past norm_max_grad_d() columns are read again instead.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -17,7 +17,12 @@
 
 namespace tke {
 
-constexpr int NM_MAX_GRAD_D = 16384;
+// Longest rows that the ring holds, by the bytes of an element of x and one of dy.
+constexpr int norm_max_grad_d(size_t bytes) { return bytes < 8 ? 16384 : 8192; }
+
+// Rows of the rings of x and dy.
+template <typename TX, typename TD, int G>
+constexpr int NG_SLOTS = G >= 1024 ? (sizeof(TX) + sizeof(TD) == 4 ? 3 : 2) : 3;
 
 struct NormGradParams {
     const void* dy;
@@ -32,113 +37,105 @@ struct NormGradParams {
     float inv_d;
 };
 
-// Threads of a gradient's block: rows of fewer threads share one.
-template <int G>
-constexpr int GRAD_BLOCK = G < 256 ? 256 : G;
-
-// Waits for the G threads of a row (G > 32: a barrier of its own for each row of the block).
-template <int G>
-__device__ __forceinline__ void row_sync() {
-    if (G == GRAD_BLOCK<G>) {
-        __syncthreads();
-    } else {
-        asm volatile("bar.sync %0, %1;" ::"r"((int)threadIdx.x / G + 1), "n"(G) : "memory");
-    }
-}
-
-// G threads a row, 8 N elements a thread.  Bound by the bytes of x, dy and dx; 32 registers of
-// column sums, and the next row's x and dy on their way, leave an SM 16 warps.
-template <typename TX, typename TD, int G, int N, bool VEC>
-__global__ void __launch_bounds__(GRAD_BLOCK<G>) norm_grad_kernel(const NormGradParams p) {
-    constexpr int E = 8 * N, BLOCK = GRAD_BLOCK<G>, ROWS = BLOCK / G, L = G < 32 ? G : 32, W = G < 32 ? 1 : G / 32;
-    // (1,024 threads have 64 registers each: no next row, w from memory)
-    constexpr bool AHEAD = G < 1024;
-    __shared__ float2 s_part[2][BLOCK / 32];
-    __shared__ float s_col[ROWS > 1 ? G * E : 1];
+// G threads a row.  Bound by the bytes of x, dy and dx.
+template <typename TX, typename TD, int G, int V>
+__global__ void __launch_bounds__(NORM_BLOCK<G>, G <= 256 ? 2 : 1)
+    norm_grad_kernel(const NormGradParams p) {
+    constexpr int E = NR_ELEMS, ROWS = NORM_BLOCK<G> / G, L = G < 32 ? G : 32, W = G < 64 ? 1 : G / 32;
+    constexpr int S = NG_SLOTS<TX, TD, G>, BX = NR_BYTES<TX, G, V>, BD = NR_BYTES<TD, G, V>;
+    constexpr int BYTES = BX + BD;
+    // (1,024 threads have 64 registers each: w from memory)
+    constexpr bool HOLD = G < 1024;
+    extern __shared__ __align__(16) char s_ring[];     // [row of the block][S][x, dy]
+    __shared__ float2 s_part[2][NORM_BLOCK<G> / 32];
     pdl_launch();
     const int t = (int)(threadIdx.x % G), D = (int)p.D;
     const TX* x = static_cast<const TX*>(p.x);
     const TD* dy = static_cast<const TD*>(p.dy);
     TX* dx = static_cast<TX*>(p.dx);
+    char* ring = s_ring + threadIdx.x / G * (S * BYTES);
+    const uint32_t ring_at = smem_u32(ring);
     pdl_wait();
-    const auto weight = [&](int e) {
-        const int c = norm_col<G, VEC>(t, e);
-        return p.w && c < D ? load_as(p.w, p.w_type, c) : 1.0f;
-    };
-    f32x2 w[AHEAD ? E / 2 : 1], dw[E / 2], db[E / 2];
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-        if (AHEAD) w[i] = pair(weight(2 * i), weight(2 * i + 1));
-        dw[i] = db[i] = 0;
-    }
     const int64_t step = (int64_t)gridDim.x * ROWS;
     int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / G;
-    int flip = 0;
-    RowRegs<TX, N, VEC> nx;
-    RowRegs<TD, N, VEC> nd;
-    float nm = 0.0f, nr = 0.0f;
-    const auto fetch = [&](int64_t row) {
-        load_row<TX, G, N, VEC>(x + row * p.ldx, t, D, nx);
-        load_row<TD, G, N, VEC>(dy + row * p.ldy, t, D, nd);
-        nm = p.mean[row];
-        nr = p.rstd[row];
-    };
-    // (the lanes of a warp go on together: a warp's last rows may not exist; they count as rows
-    // of dy = 0)
+    // (the lanes of a warp go on together: a warp's last rows may not exist)
     const int64_t first = r - (G < 32 ? lane_id() / G : 0);
     const int64_t rounds = first < p.T ? ceil_div64(p.T - first, step) : 0;
-    if (AHEAD && r < p.T) fetch(r);
-    for (int64_t i0 = 0; i0 < rounds; ++i0, r += step) {
-        const bool here = r < p.T;
-        if (!AHEAD) fetch(r);
-        if (!here) {
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                nx.v[j] = Vec8<TX>{};
-                nd.v[j] = Vec8<TD>{};
-            }
+    const auto copy = [&](int slot, int64_t row) {
+        if (row < p.T) {
+            copy_row<TX, G, V>(ring_at + slot * BYTES, x + row * p.ldx, t, D);
+            copy_row<TD, G, V>(ring_at + slot * BYTES + BX, dy + row * p.ldy, t, D);
         }
-        const RowRegs<TX, N, VEC> vx = nx;
-        const RowRegs<TD, N, VEC> vd = nd;
-        const float mean = here ? nm : 0.0f, rstd = here ? nr : 0.0f;
-        if (AHEAD && r + step < p.T) fetch(r + step);
+        copies_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) copy(i, r + i * step);
+    // what is not copied of the next row: its statistics, and the first elements of rows that
+    // start within a word
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    TX next_x = from_f32<TX>(0.0f);
+    TD next_d = from_f32<TD>(0.0f);
+    const auto fetch = [&](int64_t row) {
+        if (row >= p.T) return;
+        next_mean = p.mean[row];
+        next_rstd = p.rstd[row];
+        if (V == 1 && sizeof(TX) == 2) next_x = x[row * p.ldx];
+        if (V == 1 && sizeof(TD) == 2) next_d = dy[row * p.ldy];
+    };
+    fetch(r);
+    const uint32_t mask = elems_mask<G, V>(t, D);
+    f32x2 w[E / 2], dw[E / 2], db[E / 2];
+    if (HOLD) row_weights<G, V>(p.w, p.w_type, t, D, 1.0f, w);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) dw[i] = db[i] = 0;
+    copies_wait<S - 2>();
+    row_sync<G>();
+    int flip = 0, slot = 0, free_slot = S - 1;
+    for (int64_t i = 0; i < rounds; ++i, r += step) {
+        copy(free_slot, r + (S - 1) * step);
+        RowRegs<TX> vx;
+        RowRegs<TD> vd;
+        // (a row that does not exist has dy = 0 and leaves the sums as they are)
+        const uint32_t in = r < p.T ? mask : 0;
+        read_row<TX, G, V>(ring + slot * BYTES, x + r * p.ldx, t, in, next_x, vx);
+        read_row<TD, G, V>(ring + slot * BYTES + BX, dy + r * p.ldy, t, in, next_d, vd);
+        const float mean = r < p.T ? next_mean : 0.0f, rstd = r < p.T ? next_rstd : 0.0f;
+        fetch(r + step);
+        free_slot = slot;
+        slot = slot + 1 == S ? 0 : slot + 1;
         // (dy is 0 past the end, so nothing there counts)
         f32x2 s1 = 0, s2 = 0;
+        if (!HOLD) row_weights<G, V>(p.w, p.w_type, t, D, 1.0f, w);
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-            const f32x2 d = vd.two(i), xh = mul2(add2(vx.two(i), both(-mean)), both(rstd));
-            const f32x2 g = mul2(d, AHEAD ? w[i] : pair(weight(2 * i), weight(2 * i + 1)));
+        for (int e = 0; e < E / 2; ++e) {
+            const f32x2 d = vd.two(e), xh = mul2(add2(vx.two(e), both(-mean)), both(rstd));
+            const f32x2 g = mul2(d, w[e]);
             s1 = add2(s1, g);
             s2 = fma2(g, xh, s2);
-            dw[i] = fma2(d, xh, dw[i]);
-            db[i] = add2(db[i], d);
+            dw[e] = fma2(d, xh, dw[e]);
+            db[e] = add2(db[e], d);
         }
         const float2 a = parts(s1), b = parts(s2);
-        float g1 = lanes_sum<L>(a.x + a.y), g2 = lanes_sum<L>(b.x + b.y);
-        if (W > 1) {
-            const int warp = (int)warp_id(), lane = (int)lane_id();
-            if (lane == 0) s_part[flip][warp] = make_float2(g1, g2);
-            row_sync<G>();
-            const float2 o = lane < W ? s_part[flip][warp / W * W + lane] : make_float2(0.0f, 0.0f);
-            flip ^= 1;
-            g1 = warp_sum(o.x);
-            g2 = warp_sum(o.y);
-        }
-        g1 *= p.inv_d * rstd;
-        g2 *= p.inv_d * rstd;
-        if (here) {
-            RowRegs<TX, N, VEC> o;
+        copies_wait<S - 2>();                          // (the next row, before the barrier)
+        const float2 tot = row_parts<G>(
+            make_float2(lanes_sum<L>(a.x + a.y), lanes_sum<L>(b.x + b.y)), s_part, flip, [](float2 o) {
+                return make_float2(lanes_sum<W>(o.x), lanes_sum<W>(o.y));
+            });
+        const float g1 = tot.x * p.inv_d * rstd, g2 = tot.y * p.inv_d * rstd;
+        if (r < p.T) {
+            if (!HOLD) row_weights<G, V>(p.w, p.w_type, t, D, 1.0f, w);
+            RowRegs<TX> o;
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i) {
-                const f32x2 xh = mul2(add2(vx.two(i), both(-mean)), both(rstd));
-                const f32x2 g =
-                    mul2(vd.two(i), AHEAD ? w[i] : pair(weight(2 * i), weight(2 * i + 1)));
-                o.put_two(i, fma2(xh, both(-g2), fma2(g, both(rstd), both(-g1))));
+            for (int e = 0; e < E / 2; ++e) {
+                const f32x2 xh = mul2(add2(vx.two(e), both(-mean)), both(rstd));
+                const f32x2 g = mul2(vd.two(e), w[e]);
+                o.put_two(e, fma2(xh, both(-g2), fma2(g, both(rstd), both(-g1))));
             }
-            store_row<TX, G, N, VEC>(dx + r * p.lddx, t, D, o);
+            store_row<TX, G, V>(dx + r * p.lddx, t, D, o);
         }
     }
     if (!p.part) return;
+    float* s_col = reinterpret_cast<float*>(s_ring);   // (all copies have landed and been read)
     float* part = p.part + (int64_t)blockIdx.x * 2 * p.D;
     const int mine = (int)threadIdx.x / G;
 #pragma unroll
@@ -166,7 +163,7 @@ __global__ void __launch_bounds__(GRAD_BLOCK<G>) norm_grad_kernel(const NormGrad
 #pragma unroll
             for (int e = 0; e < E / 2; ++e) {
                 const float2 f = parts(v[e]);
-                const int c0 = norm_col<G, VEC>(t, 2 * e), c1 = norm_col<G, VEC>(t, 2 * e + 1);
+                const int c0 = norm_col<G, V>(t, 2 * e), c1 = norm_col<G, V>(t, 2 * e + 1);
                 if (c0 < D) part[c0] = f.x;
                 if (c1 < D) part[c1] = f.y;
             }

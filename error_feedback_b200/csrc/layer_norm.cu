@@ -12,31 +12,31 @@ using namespace tke;
 
 namespace {
 
-template <typename TX, typename TY, int G, int N, bool VEC>
+template <typename TX, typename TY, int G, int V>
 cudaError_t launch_norm(const NormParams& p, cudaStream_t st) {
     constexpr int block = NORM_BLOCK<G>;
-    static const int most = resident(norm_kernel<TX, TY, G, N, VEC>, block);
+    constexpr size_t smem = (size_t)block / G * NR_SLOTS<TX, G> * NR_BYTES<TX, G, V>;
+    static Resident resident;
+    const int most = resident.get(norm_kernel<TX, TY, G, V>, block, smem);
+    if (!most) return cudaErrorLaunchOutOfResources;
     const int64_t rows = ceil_div64(p.T, block / G);
     trace_before(st, "norm_kernel");
-    const cudaError_t e = launch_pdl(norm_kernel<TX, TY, G, N, VEC>,
-                                     (unsigned)std::min<int64_t>(most, rows), block, st, p);
+    const cudaError_t e = launch_pdl(norm_kernel<TX, TY, G, V>,
+                                     (unsigned)std::min<int64_t>(most, rows), block, st, p, smem);
     trace_after(st);
     return e;
 }
 
-// Threads of a row and groups of 8 elements of a thread (see kernels_norm.cuh).
-template <typename TX, typename TY, bool VEC>
+template <typename TX, typename TY, int V>
 cudaError_t norm_by_length(const NormParams& p, cudaStream_t st) {
-    if (p.D <= 64) return launch_norm<TX, TY, 8, 1, VEC>(p, st);
-    if (p.D <= 128) return launch_norm<TX, TY, 16, 1, VEC>(p, st);
-    if (p.D <= 256) return launch_norm<TX, TY, 32, 1, VEC>(p, st);
-    if (p.D <= 512) return launch_norm<TX, TY, 32, 2, VEC>(p, st);
-    if (p.D <= 1024) return launch_norm<TX, TY, 32, 4, VEC>(p, st);
-    constexpr int N = sizeof(TX) == 4 || !VEC ? 4 : 8, F = 8 / N;
-    if (p.D <= 2048) return launch_norm<TX, TY, 32 * F, N, VEC>(p, st);
-    if (p.D <= 4096) return launch_norm<TX, TY, 64 * F, N, VEC>(p, st);
-    if (p.D <= 8192) return launch_norm<TX, TY, 128 * F, N, VEC>(p, st);
-    return launch_norm<TX, TY, 256 * F, N, VEC>(p, st);
+    if (p.D <= 128) return launch_norm<TX, TY, 8, V>(p, st);
+    if (p.D <= 256) return launch_norm<TX, TY, 16, V>(p, st);
+    if (p.D <= 512) return launch_norm<TX, TY, 32, V>(p, st);
+    if (p.D <= 1024) return launch_norm<TX, TY, 64, V>(p, st);
+    if (p.D <= 2048) return launch_norm<TX, TY, 128, V>(p, st);
+    if (p.D <= 4096) return launch_norm<TX, TY, 256, V>(p, st);
+    if (p.D <= 8192) return launch_norm<TX, TY, 512, V>(p, st);
+    return launch_norm<TX, TY, 1024, V>(p, st);
 }
 
 }  // namespace
@@ -82,7 +82,8 @@ int layer_norm(const void* x, int32_t x_type, int64_t ld_x, const void* weight,
             using TX = decltype(tx);
             using TO = decltype(to);
             if (D <= NM_MAX_D)
-                return vec ? norm_by_length<TX, TO, true>(p, st) : norm_by_length<TX, TO, false>(p, st);
+                return vec ? norm_by_length<TX, TO, NORM_GROUP<TX, TO>>(p, st)
+                           : norm_by_length<TX, TO, 1>(p, st);
             trace_before(st, "norm_long_kernel");
             const cudaError_t r = launch_pdl(norm_long_kernel<TX, TO>,
                                              (unsigned)std::min<int64_t>(T, SMS * 4), NL_THREADS, st, p);

@@ -1,6 +1,6 @@
 // Host side of layer_norm_grad (include/topk_ef.h): argument checks, workspace layout,
 // choice of kernel by row length: norm_grad_kernel -> norm_sum_kernel, for rows past
-// NM_MAX_GRAD_D norm_cols_kernel -> norm_grad_long_kernel -> norm_sum_kernel.
+// norm_max_grad_d() norm_cols_kernel -> norm_grad_long_kernel -> norm_sum_kernel.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -21,31 +21,36 @@ int64_t grad_parts(int64_t T) {
     return std::min<int64_t>(NG_MAX_PARTS, std::max<int64_t>(1, ceil_div64(T, NG_ROWS)));
 }
 
-template <typename TX, typename TD, int G, int N, bool VEC>
+template <typename TX, typename TD, int G, int V>
 cudaError_t launch_grad(const NormGradParams& p, int32_t& parts, cudaStream_t st) {
-    constexpr int block = GRAD_BLOCK<G>;
-    static const int most = resident(norm_grad_kernel<TX, TD, G, N, VEC>, block);
+    constexpr int block = NORM_BLOCK<G>;
+    constexpr size_t ring = (size_t)block / G * NG_SLOTS<TX, TD, G> *
+                            (NR_BYTES<TX, G, V> + NR_BYTES<TD, G, V>);
+    constexpr size_t smem = std::max(ring, (size_t)G * NR_ELEMS * 4);
+    static Resident resident;
+    const int most = resident.get(norm_grad_kernel<TX, TD, G, V>, block, smem);
+    if (!most) return cudaErrorLaunchOutOfResources;
     const int64_t rows = ceil_div64(p.T, block / G);
     parts = (int32_t)std::min(std::min<int64_t>(most, rows), grad_parts(p.T));
     trace_before(st, "norm_grad_kernel");
     const cudaError_t e =
-        launch_pdl(norm_grad_kernel<TX, TD, G, N, VEC>, (unsigned)parts, block, st, p);
+        launch_pdl(norm_grad_kernel<TX, TD, G, V>, (unsigned)parts, block, st, p, smem);
     trace_after(st);
     return e;
 }
 
-template <typename TX, typename TD, bool VEC>
+template <typename TX, typename TD, int V>
 cudaError_t grad_by_length(const NormGradParams& p, int32_t& parts, cudaStream_t st) {
-    if (p.D <= 64) return launch_grad<TX, TD, 8, 1, VEC>(p, parts, st);
-    if (p.D <= 128) return launch_grad<TX, TD, 16, 1, VEC>(p, parts, st);
-    if (p.D <= 256) return launch_grad<TX, TD, 32, 1, VEC>(p, parts, st);
-    constexpr int N = sizeof(TX) == 4 || sizeof(TD) == 4 ? 1 : 2, F = 2 / N;
-    if (p.D <= 512) return launch_grad<TX, TD, 32 * F, N, VEC>(p, parts, st);
-    if (p.D <= 1024) return launch_grad<TX, TD, 64 * F, N, VEC>(p, parts, st);
-    if (p.D <= 2048) return launch_grad<TX, TD, 128 * F, N, VEC>(p, parts, st);
-    if (p.D <= 4096) return launch_grad<TX, TD, 256 * F, N, VEC>(p, parts, st);
-    if (p.D <= 8192) return launch_grad<TX, TD, 512 * F, N, VEC>(p, parts, st);
-    return launch_grad<TX, TD, 1024, 2, VEC>(p, parts, st);
+    if (p.D <= 128) return launch_grad<TX, TD, 8, V>(p, parts, st);
+    if (p.D <= 256) return launch_grad<TX, TD, 16, V>(p, parts, st);
+    if (p.D <= 512) return launch_grad<TX, TD, 32, V>(p, parts, st);
+    if (p.D <= 1024) return launch_grad<TX, TD, 64, V>(p, parts, st);
+    if (p.D <= 2048) return launch_grad<TX, TD, 128, V>(p, parts, st);
+    if (p.D <= 4096) return launch_grad<TX, TD, 256, V>(p, parts, st);
+    if (p.D <= 8192) return launch_grad<TX, TD, 512, V>(p, parts, st);
+    if constexpr (norm_max_grad_d(sizeof(TX) + sizeof(TD)) > 8192)
+        return launch_grad<TX, TD, 1024, V>(p, parts, st);
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -104,14 +109,14 @@ int layer_norm_grad(const void* grad_out, int32_t grad_out_type, int64_t ld_grad
     cudaError_t e = cudaSuccess;
     if (T > 0) {
         const bool vec = D % 8 == 0 && rows16(x, ld_x, sx) && rows16(grad_x, ld_grad_x, sx) &&
-                         rows16(grad_out, ld_grad_out, sd);
+                         rows16(grad_out, ld_grad_out, sd) && aligned(weight, 16);
         e = with_type(x_type, [&](auto tx) {
             return with_type(grad_out_type, [&](auto td) {
                 using TX = decltype(tx);
                 using TD = decltype(td);
-                if (D <= NM_MAX_GRAD_D)
-                    return vec ? grad_by_length<TX, TD, true>(p, parts, st)
-                               : grad_by_length<TX, TD, false>(p, parts, st);
+                if (D <= norm_max_grad_d(sx + sd))
+                    return vec ? grad_by_length<TX, TD, NORM_GROUP<TX, TD>>(p, parts, st)
+                               : grad_by_length<TX, TD, 1>(p, parts, st);
                 cudaError_t r = cudaSuccess;
                 if (cols) {      // first: grad_x may be x or grad_out
                     parts = (int32_t)std::min<int64_t>(grad_parts(T), NL_PARTS);

@@ -3,6 +3,8 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "topk_ef.h"
 #include "host.cuh"
 #include "kernels_norm.cuh"
@@ -21,13 +23,28 @@ inline bool rows16(const void* p, int64_t ld, size_t size) {
     return aligned(p, 16) && (size_t)ld * size % 16 == 0;
 }
 
-// Blocks of a kernel that run at once.
+// Blocks of a kernel that run at once, with `smem` bytes each (which it is allowed to have).
 template <typename K>
-int resident(K kernel, int threads) {
+int resident(K kernel, int threads, size_t smem) {
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1)
-        n = 1;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess)
+        return 0;
     return n * SMS;
 }
+
+// The same, found once for each device; 0: the launch cannot work.
+struct Resident {
+    std::atomic<int> n[64];
+    template <typename K>
+    int get(K kernel, int threads, size_t smem) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return resident(kernel, threads, smem);
+        int v = n[dev].load();
+        if (!v) n[dev].store(v = resident(kernel, threads, smem));
+        return v;
+    }
+};
 
 }  // namespace tke
