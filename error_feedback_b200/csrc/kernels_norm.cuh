@@ -61,6 +61,10 @@ __device__ __forceinline__ int norm_col(int t, int e) {
     return ((e / V) * G + t) * V + e % V;
 }
 
+// Elements of a thread that every row has: rows take the fewest threads that hold them.
+template <int G>
+constexpr int NORM_FULL = G > 8 ? NR_ELEMS / 2 : 0;
+
 template <typename T>
 struct RowRegs {
     uint32_t q[NR_ELEMS * sizeof(T) / 4];
@@ -92,7 +96,7 @@ __device__ __forceinline__ void store_row(T* row, int t, int D, const RowRegs<T>
         for (int j = 0; j < NR_ELEMS / V; ++j) {
             const int c = (j * G + t) * V;
             const uint32_t* q = r.q + j * WORDS;
-            if (c >= D) continue;
+            if (j * V >= NORM_FULL<G> && c >= D) continue;
             if (WORDS == 4) {
                 *reinterpret_cast<uint4*>(row + c) = make_uint4(q[0], q[1], q[2], q[WORDS - 1]);
             } else {
@@ -104,7 +108,7 @@ __device__ __forceinline__ void store_row(T* row, int t, int D, const RowRegs<T>
 #pragma unroll
         for (int j = 0; j < NR_ELEMS; ++j) {
             const int c = j * G + t;
-            if (c < D) row[c] = e[j];
+            if (j < NORM_FULL<G> || c < D) row[c] = e[j];
         }
     }
 }
@@ -229,7 +233,7 @@ __device__ __forceinline__ void copy_row(uint32_t slot, const T* row, int t, int
 #pragma unroll
         for (int j = 0; j < NR_ELEMS / V; ++j) {
             const int c = (j * G + t) * V;
-            if (c >= D) continue;
+            if (j * V >= NORM_FULL<G> && c >= D) continue;
             const uint32_t to = slot + (uint32_t)(j * G + t) * BYTES;
             if (BYTES == 16) {
                 copy_async16(to, row + c);
@@ -271,7 +275,7 @@ __device__ __forceinline__ void read_row(const char* slot, const T* row, int t, 
         constexpr int WORDS = V * (int)sizeof(T) / 4;
 #pragma unroll
         for (int j = 0; j < NR_ELEMS / V; ++j) {
-            const bool in = mask >> V * j & 1;
+            const bool in = j * V < NORM_FULL<G> || (mask >> V * j & 1);
             uint32_t* q = r.q + j * WORDS;
             if (WORDS == 4) {
                 const uint4 v = in ? reinterpret_cast<const uint4*>(slot)[j * G + t] : make_uint4(0, 0, 0, 0);
@@ -290,7 +294,7 @@ __device__ __forceinline__ void read_row(const char* slot, const T* row, int t, 
         const T* at = reinterpret_cast<const T*>(slot + lead) + t;
         T* e = reinterpret_cast<T*>(r.q);
 #pragma unroll
-        for (int j = 0; j < NR_ELEMS; ++j) e[j] = mask >> j & 1 ? at[j * G] : from_f32<T>(0.0f);
+        for (int j = 0; j < NR_ELEMS; ++j) e[j] = j < NORM_FULL<G> || (mask >> j & 1) ? at[j * G] : from_f32<T>(0.0f);
         if (sizeof(T) == 2 && t == 0 && (lead & 2)) e[0] = first;
     }
 }
@@ -314,8 +318,9 @@ __device__ __forceinline__ float2 row_parts(float2 v, float2 (*s)[NORM_BLOCK<G> 
 }
 
 // The pair of elements 2 e and 2 e + 1, 0 where the thread has none.
-template <int V>
+template <int G, int V>
 __device__ __forceinline__ f32x2 masked(f32x2 a, uint32_t mask, int e) {
+    if (2 * e < NORM_FULL<G>) return a;
     if (V > 1) return mask >> 2 * e & 1 ? a : 0;
     const float2 f = parts(a);
     return pair(mask >> 2 * e & 1 ? f.x : 0.0f, mask >> (2 * e + 1) & 1 ? f.y : 0.0f);
@@ -370,7 +375,7 @@ __global__ void __launch_bounds__(NORM_BLOCK<G>, G <= 256 ? 3 : 1) norm_kernel(c
         // d = x - c, 0 past the row's end
         f32x2 d[E / 2], sum = 0;
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) d[e] = masked<V>(add2(v.two(e), c), mask, e);
+        for (int e = 0; e < E / 2; ++e) d[e] = masked<G, V>(add2(v.two(e), c), mask, e);
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) sum = add2(sum, d[e]);
         const float2 s = parts(sum);
@@ -379,7 +384,7 @@ __global__ void __launch_bounds__(NORM_BLOCK<G>, G <= 256 ? 3 : 1) norm_kernel(c
         f32x2 sq2 = 0;
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) {
-            const f32x2 q = masked<V>(add2(d[e], both(-m0)), mask, e);
+            const f32x2 q = masked<G, V>(add2(d[e], both(-m0)), mask, e);
             sq2 = fma2(q, q, sq2);
         }
         const float2 q = parts(sq2);

@@ -95,10 +95,13 @@ __global__ void __launch_bounds__(NORM_BLOCK<G>, G <= 256 ? 2 : 1)
         copy(free_slot, r + (S - 1) * step);
         RowRegs<TX> vx;
         RowRegs<TD> vd;
-        // (a row that does not exist has dy = 0 and leaves the sums as they are)
-        const uint32_t in = r < p.T ? mask : 0;
-        read_row<TX, G, V>(ring + slot * BYTES, x + r * p.ldx, t, in, next_x, vx);
-        read_row<TD, G, V>(ring + slot * BYTES + BX, dy + r * p.ldy, t, in, next_d, vd);
+        read_row<TX, G, V>(ring + slot * BYTES, x + r * p.ldx, t, mask, next_x, vx);
+        read_row<TD, G, V>(ring + slot * BYTES + BX, dy + r * p.ldy, t, mask, next_d, vd);
+        if (G < 32 && r >= p.T) {
+            // (a row that does not exist leaves the sums as they are)
+            vx = RowRegs<TX>{};
+            vd = RowRegs<TD>{};
+        }
         const float mean = r < p.T ? next_mean : 0.0f, rstd = r < p.T ? next_rstd : 0.0f;
         fetch(r + step);
         free_slot = slot;
