@@ -214,11 +214,15 @@ struct Running {
 };
 constexpr float LG_BELOW = 400.0f;
 
-// Adds a chunk; returns its largest value (NaN if it holds one).
-template <typename T, bool ENTROPY>
-__device__ __forceinline__ float add_chunk(const Chunk<T>& q, Running& a, float c, float inv_c) {
-    const float top = Pairs<T>::largest(q), reach = top * c;
-    if (reach < -2.0f * LG_FAR) return top;
+// Adds chunks; `top` gets the largest value of each (NaN if it holds one).
+template <typename T, bool ENTROPY, int N>
+__device__ __forceinline__ void add_chunks(const Chunk<T>* q, float* top, Running& a, float c,
+                                           float inv_c) {
+    float all = -CUDART_INF_F;
+#pragma unroll
+    for (int k = 0; k < N; ++k) all = max_nan(all, top[k] = Pairs<T>::largest(q[k]));
+    const float reach = all * c;
+    if (reach < -2.0f * LG_FAR) return;
     if (!(reach <= a.m)) {
         const float m = ceilf(reach), f = ex2(a.m - m);
         const f32x2 ff = pair(f, f);
@@ -229,12 +233,13 @@ __device__ __forceinline__ float add_chunk(const Chunk<T>& q, Running& a, float 
     }
     const f32x2 cc = pair(c, c), mm = pair(-a.m, -a.m);
 #pragma unroll
-    for (int i = 0; i < CHUNK<T> / 2; ++i) {
-        const f32x2 t = fma2(Pairs<T>::template get<ENTROPY>(q, i, a.low), cc, mm), e = ex2_2(t);
-        a.s = add2(a.s, e);
-        if (ENTROPY) a.u = fma2(e, t, a.u);
-    }
-    return top;
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int i = 0; i < CHUNK<T> / 2; ++i) {
+            const f32x2 t = fma2(Pairs<T>::template get<ENTROPY>(q[k], i, a.low), cc, mm), e = ex2_2(t);
+            a.s = add2(a.s, e);
+            if (ENTROPY) a.u = fma2(e, t, a.u);
+        }
 }
 
 // The lanes' statistics, joined in every lane.
@@ -260,8 +265,9 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
-// f(chunk, its number, whether it belongs to the block) for the chunks of lines
-// [line0, line1); every thread of a warp makes the same calls.  Batches that lie in the
+// f(FLIGHT chunks, the number of the first, those of the others THREADS apart, end) for the
+// chunks of lines [line0, line1); a chunk from `end` on holds nothing but -inf.  Every thread
+// of a warp makes the same calls.  Batches that lie in the
 // row as a whole are loaded without a check of each chunk, which would take as many
 // instructions as the sums (7.3 instead of 5.5 an element).
 template <int W, int FLIGHT, typename T, typename F>
@@ -286,8 +292,7 @@ __device__ __forceinline__ void for_chunks(const LineRow<T>& row, int32_t line0,
                 }
             }
         }
-#pragma unroll
-        for (int k = 0; k < FLIGHT; ++k) f(q[k], j + k * N, j + k * N < end);
+        f(q, j, end);
     }
 }
 
@@ -345,19 +350,19 @@ template <int W, typename T>
 __device__ __forceinline__ Soft far_row(const LineRow<T>& row, int32_t line0, int32_t line1, float c,
                                         int blocks, Soft* s_soft) {
     float top = -CUDART_INF_F;
-    for_chunks<W, 1>(row, line0, line1, [&](const Chunk<T>& q, int32_t, bool) {
+    for_chunks<W, 1>(row, line0, line1, [&](const Chunk<T>* q, int32_t, int32_t) {
 #pragma unroll
-        for (int i = 0; i < CHUNK<T>; ++i) top = max_nan(top, q.get(i));
+        for (int i = 0; i < CHUNK<T>; ++i) top = max_nan(top, q->get(i));
     });
     // (as a sum of one term, whose reference it is)
     if (blocks > 1) cluster_sync(); else Team<W>::sync();      // what s_soft held has been read
     top = max_nan(row_join<W>({top, 0.0f, 0.0f}, blocks, s_soft).m, LG_START);     // (finite: -inf - top is -inf)
     if (blocks > 1) cluster_sync(); else Team<W>::sync();
     Soft a = {0.0f, 0.0f, 0.0f};
-    for_chunks<W, 1>(row, line0, line1, [&](const Chunk<T>& q, int32_t, bool) {
+    for_chunks<W, 1>(row, line0, line1, [&](const Chunk<T>* q, int32_t, int32_t) {
 #pragma unroll
         for (int i = 0; i < CHUNK<T>; ++i) {
-            const float t = c * (q.get(i) - top), e = ex2(t);
+            const float t = c * (q->get(i) - top), e = ex2(t);
             a.s += e;
             a.u = fmaf(e, fmaxf(t, -1e4f), a.u);
         }
@@ -386,19 +391,29 @@ __device__ __forceinline__ void get_stash(const uint4* stash, int32_t j, Chunk<T
 // The softmax of a row, of which a block takes lines [line0, line1); TOP: the
 // largest value of each of them in tops[line].  The first `keep` chunks stay in the stash,
 // each thread's where it alone reads them.
-template <int W, typename T, bool ENTROPY, bool TOP>
+template <int W, typename T, bool ENTROPY, bool TOP, bool KEEP>
 __device__ __forceinline__ RowSoft row_softmax(const LineRow<T>& row, int32_t line0, int32_t line1,
                                                float c, int blocks, Soft* s_soft, float* tops,
                                                uint4* stash, int32_t keep) {
     Running run = {LG_START, LG_START, 0, 0};
     const float inv_c = 1.0f / c;
-    for_chunks<W, LG_FLIGHT>(row, line0, line1, [&](const Chunk<T>& q, int32_t j, bool mine) {
-        if (mine && j - line0 * 4 < keep) put_stash<W>(stash, j - line0 * 4, q);
-        float top = add_chunk<T, ENTROPY>(q, run, c, inv_c);
+    constexpr int N = Team<W>::THREADS;
+    for_chunks<W, LG_FLIGHT>(row, line0, line1, [&](const Chunk<T>* q, int32_t j, int32_t end) {
+        if (KEEP) {
+            const int32_t last = min(end, line0 * 4 + keep);
+#pragma unroll
+            for (int k = 0; k < LG_FLIGHT; ++k)
+                if (j + k * N < last) put_stash<W>(stash, j + k * N - line0 * 4, q[k]);
+        }
+        float top[LG_FLIGHT];
+        add_chunks<T, ENTROPY, LG_FLIGHT>(q, top, run, c, inv_c);
         if (TOP) {
-            top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-            top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            if ((threadIdx.x & 3) == 0 && mine) tops[j >> 2] = top;
+#pragma unroll
+            for (int k = 0; k < LG_FLIGHT; ++k) {
+                float line = max_nan(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], 1));
+                line = max_nan(line, __shfl_xor_sync(0xFFFFFFFFu, line, 2));
+                if ((threadIdx.x & 3) == 0 && j + k * N < end) tops[(j + k * N) >> 2] = line;
+            }
         }
     });
     const float2 s = parts(run.s), u = parts(run.u);
@@ -756,8 +771,8 @@ __global__ void __launch_bounds__(Team<W>::BLOCK, LOGPROB_BLOCKS<W, TOP>)
     const int32_t lines = row.lines();
     const int32_t share = (lines + p.blocks - 1) / p.blocks;
     const int32_t line0 = min(lines, rank * share), line1 = min(lines, line0 + share);
-    const RowSoft a = row_softmax<W, T, ENTROPY, TOP>(row, line0, line1, p.c, p.blocks, s_soft, s_tops,
-                                                      nullptr, 0);
+    const RowSoft a = row_softmax<W, T, ENTROPY, TOP, false>(row, line0, line1, p.c, p.blocks, s_soft,
+                                                             s_tops, nullptr, 0);
     if (rank == 0 && tid == 0) {
         if (p.logprob) p.logprob[r] = ok ? a.log_prob(zt, p.c, p.scale) : 0.0f;
         if (ENTROPY && p.entropy) p.entropy[r] = a.entropy();
@@ -852,18 +867,21 @@ __global__ void __launch_bounds__(LD_THREADS) logprob_grad_kernel(const LogprobG
                     store_chunk(row, out, j * CHUNK<T>, zero);
                 continue;
             }
-            for_chunks<1, LG_FLIGHT>(row, line0, line1, [&](const Chunk<T>& q, int32_t j, bool mine) {
-                if (!mine) return;
-                const int32_t pos = j * CHUNK<T>;
-                Chunk<TO> o;
+            for_chunks<1, LG_FLIGHT>(row, line0, line1, [&](const Chunk<T>* q, int32_t j, int32_t end) {
 #pragma unroll
-                for (int i = 0; i < CHUNK<T> / 2; ++i) {
-                    f32x2 v = values(Pairs<T>::template get<false>(q, i, 0.0f));
-                    if (token >> 1 == (pos >> 1) + i)
-                        v = add2(v, pair(token & 1 ? 0.0f : g, token & 1 ? g : 0.0f));
-                    put_pair(o, i, v);
+                for (int k = 0; k < LG_FLIGHT; ++k, j += 32) {
+                    if (j >= end) continue;
+                    const int32_t pos = j * CHUNK<T>;
+                    Chunk<TO> o;
+#pragma unroll
+                    for (int i = 0; i < CHUNK<T> / 2; ++i) {
+                        f32x2 v = values(Pairs<T>::template get<false>(q[k], i, 0.0f));
+                        if (token >> 1 == (pos >> 1) + i)
+                            v = add2(v, pair(token & 1 ? 0.0f : g, token & 1 ? g : 0.0f));
+                        put_pair(o, i, v);
+                    }
+                    store_chunk(row, out, pos, o);
                 }
-                store_chunk(row, out, pos, o);
             });
         } else {
             constexpr int32_t per = LG_LINE / (int)sizeof(T);
@@ -956,8 +974,8 @@ __global__ void __launch_bounds__(Team<W>::BLOCK, W == 16 ? 2 : 3)
     RowSoft a = {};
     float big = 0.0f, q_sum = 1.0f, inv = 0.0f;
     if (weight != 0.0f) {                          // (the same in all blocks of the cluster)
-        a = row_softmax<W, T, false, false>(row, line0, line1, p.c, p.blocks, s_soft, nullptr, s_stash,
-                                            keep);
+        a = row_softmax<W, T, false, false, (W > 1 && SAME)>(row, line0, line1, p.c, p.blocks, s_soft,
+                                                             nullptr, s_stash, keep);
         Team<W>::sync();
         inv = a.s == 0.0f ? 0.0f : 1.0f / a.s;
         // each warp for itself
@@ -1002,8 +1020,9 @@ __global__ void __launch_bounds__(Team<W>::BLOCK, W == 16 ? 2 : 3)
             // the rest first: it may still be in L2
             if (line0 + keep / 4 < line1)
                 for_chunks<W, 2>(row, line0 + keep / 4, line1,
-                                 [&](const Chunk<T>& v, int32_t j, bool mine) {
-                                     if (mine) put(v, j);
+                                 [&](const Chunk<T>* v, int32_t j, int32_t end) {
+                                     if (j < end) put(v[0], j);
+                                     if (j + N < end) put(v[1], j + N);
                                  });
             const int32_t kept = min(line0 * 4 + keep, line1 * 4);
 #pragma unroll 2
