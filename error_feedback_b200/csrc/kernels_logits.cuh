@@ -16,9 +16,9 @@
 // -inf (a forbidden token) has p = 0 and counts nowhere.  NaN and +inf make the row
 // NaN.
 //
-// A row is worked on by a team: a warp (rows of up to LG_SMALL lines: nothing but its own
-// latency counts, so many at once), or a block, or a cluster of blocks while there are few
-// rows, each block an equal share of the row's 128-byte lines.  Rows start anywhere; whole
+// A row is worked on by a team: a warp or four (rows of up to LG_SMALL and LG_MIDDLE lines, where
+// the chain of a row's steps counts: many at once), a block of eight, or a cluster of blocks
+// while there are few rows, each block an equal share of the row's 128-byte lines.  Rows start anywhere; whole
 // lines are read as 32 bytes a thread.
 #pragma once
 
@@ -34,6 +34,7 @@
 namespace tke {
 
 constexpr int LG_SMALL = 64;               // lines of a row that one warp takes
+constexpr int LG_MIDDLE = 256;             // ... and that four take
 constexpr int LG_LINE = 128;               // bytes of a line (a group of the top selection)
 constexpr int LG_FLIGHT = 4;               // 32-byte chunks that a thread loads at once
 constexpr float LG_START = -3.402823466e38f;     // m before any value
@@ -372,50 +373,10 @@ __device__ __forceinline__ Soft far_row(const LineRow<T>& row, int32_t line0, in
     return a;
 }
 
-// Chunk j of the block's share in the stash; a warp's 16-byte accesses are consecutive.
+// A row's softmax from what its threads have summed.
 template <int W, typename T>
-__device__ __forceinline__ void put_stash(uint4* stash, int32_t j, const Chunk<T>& q) {
-    constexpr int N = Team<W>::THREADS;
-    uint4* at = stash + j / N * 2 * N + j % N;
-    at[0] = q.q[0];
-    at[N] = q.q[1];
-}
-template <int W, typename T>
-__device__ __forceinline__ void get_stash(const uint4* stash, int32_t j, Chunk<T>& q) {
-    constexpr int N = Team<W>::THREADS;
-    const uint4* at = stash + j / N * 2 * N + j % N;
-    q.q[0] = at[0];
-    q.q[1] = at[N];
-}
-
-// The softmax of a row, of which a block takes lines [line0, line1); TOP: the
-// largest value of each of them in tops[line].  The first `keep` chunks stay in the stash,
-// each thread's where it alone reads them.
-template <int W, typename T, bool ENTROPY, bool TOP, bool KEEP>
-__device__ __forceinline__ RowSoft row_softmax(const LineRow<T>& row, int32_t line0, int32_t line1,
-                                               float c, int blocks, Soft* s_soft, float* tops,
-                                               uint4* stash, int32_t keep) {
-    Running run = {LG_START, LG_START, 0, 0};
-    const float inv_c = 1.0f / c;
-    constexpr int N = Team<W>::THREADS;
-    for_chunks<W, LG_FLIGHT>(row, line0, line1, [&](const Chunk<T>* q, int32_t j, int32_t end) {
-        if (KEEP) {
-            const int32_t last = min(end, line0 * 4 + keep);
-#pragma unroll
-            for (int k = 0; k < LG_FLIGHT; ++k)
-                if (j + k * N < last) put_stash<W>(stash, j + k * N - line0 * 4, q[k]);
-        }
-        float top[LG_FLIGHT];
-        add_chunks<T, ENTROPY, LG_FLIGHT>(q, top, run, c, inv_c);
-        if (TOP) {
-#pragma unroll
-            for (int k = 0; k < LG_FLIGHT; ++k) {
-                float line = max_nan(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], 1));
-                line = max_nan(line, __shfl_xor_sync(0xFFFFFFFFu, line, 2));
-                if ((threadIdx.x & 3) == 0 && j + k * N < end) tops[(j + k * N) >> 2] = line;
-            }
-        }
-    });
+__device__ __forceinline__ RowSoft join_softmax(const LineRow<T>& row, int32_t line0, int32_t line1,
+                                                float c, int blocks, Soft* s_soft, const Running& run) {
     const float2 s = parts(run.s), u = parts(run.u);
     Soft a = {run.m, s.x + s.y, u.x + u.y};
     a = row_join<W>(a, blocks, s_soft);
@@ -427,6 +388,29 @@ __device__ __forceinline__ RowSoft row_softmax(const LineRow<T>& row, int32_t li
     r.u = a.u;
     r.log2s = log2f(a.s);
     return r;
+}
+
+// The thread's part of the sums of a row, of which a block takes lines [line0, line1); TOP:
+// the largest value of each line in tops[line].
+template <int W, typename T, bool ENTROPY, bool TOP>
+__device__ __forceinline__ Running row_sums(const LineRow<T>& row, int32_t line0, int32_t line1,
+                                            float c, float* tops) {
+    constexpr int N = Team<W>::THREADS;
+    Running run = {LG_START, LG_START, 0, 0};
+    const float inv_c = 1.0f / c;
+    for_chunks<W, LG_FLIGHT>(row, line0, line1, [&](const Chunk<T>* q, int32_t j, int32_t end) {
+        float top[LG_FLIGHT];
+        add_chunks<T, ENTROPY, LG_FLIGHT>(q, top, run, c, inv_c);
+        if (TOP) {
+#pragma unroll
+            for (int k = 0; k < LG_FLIGHT; ++k) {
+                float line = max_nan(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], 1));
+                line = max_nan(line, __shfl_xor_sync(0xFFFFFFFFu, line, 2));
+                if ((threadIdx.x & 3) == 0 && j + k * N < end) tops[(j + k * N) >> 2] = line;
+            }
+        }
+    });
+    return run;
 }
 
 // ------------------------------------------- log-probabilities of given tokens
@@ -722,7 +706,7 @@ __device__ __forceinline__ void select_top(const LogprobParams& p, const LineRow
 }
 
 template <int W, bool TOP>
-constexpr int LOGPROB_BLOCKS = TOP ? 3 : 4;        // of an SM
+constexpr int LOGPROB_BLOCKS = (TOP ? 3 : 4) * 256 / Team<W>::BLOCK;       // of an SM
 
 template <int W, typename T, bool ENTROPY, bool TOP>
 __global__ void __launch_bounds__(Team<W>::BLOCK, LOGPROB_BLOCKS<W, TOP>)
@@ -771,8 +755,8 @@ __global__ void __launch_bounds__(Team<W>::BLOCK, LOGPROB_BLOCKS<W, TOP>)
     const int32_t lines = row.lines();
     const int32_t share = (lines + p.blocks - 1) / p.blocks;
     const int32_t line0 = min(lines, rank * share), line1 = min(lines, line0 + share);
-    const RowSoft a = row_softmax<W, T, ENTROPY, TOP, false>(row, line0, line1, p.c, p.blocks, s_soft,
-                                                             s_tops, nullptr, 0);
+    const Running run = row_sums<W, T, ENTROPY, TOP>(row, line0, line1, p.c, s_tops);
+    const RowSoft a = join_softmax<W>(row, line0, line1, p.c, p.blocks, s_soft, run);
     if (rank == 0 && tid == 0) {
         if (p.logprob) p.logprob[r] = ok ? a.log_prob(zt, p.c, p.scale) : 0.0f;
         if (ENTROPY && p.entropy) p.entropy[r] = a.entropy();
@@ -911,8 +895,6 @@ struct DistillParams {
     int64_t T, V, ldz, lddz;
     int32_t id64, teacher_type, K, blocks;
     int32_t scan;                  // the first cluster checks the ids
-    int32_t lines;                 // of a row, at most
-    int32_t keep;                  // chunks of a block's share that its shared memory holds
     float c, scale;
 };
 
@@ -923,23 +905,55 @@ __device__ __forceinline__ float teacher_at(const DistillParams& p, int64_t i) {
     return to_f32(static_cast<const __half*>(p.teacher)[i]);
 }
 
+// f times the probabilities of a chunk.
+template <typename T, typename TO>
+__device__ __forceinline__ Chunk<TO> grad_chunk(const Chunk<T>& v, const RowSoft& a, float c, float f) {
+    Chunk<TO> o;
+    if (!a.far) {
+        const f32x2 cc = pair(c, c), mm = pair(-a.m, -a.m), ff = pair(f, f);
+#pragma unroll
+        for (int e = 0; e < CHUNK<T> / 2; ++e)
+            put_pair(o, e, mul2(ex2_2(fma2(Pairs<T>::template get<false>(v, e, 0.0f), cc, mm)), ff));
+    } else {
+        TO* x = reinterpret_cast<TO*>(o.q);
+#pragma unroll
+        for (int e = 0; e < CHUNK<T>; ++e) x[e] = from_f32<TO>(f * a.prob(v.get(e), c));
+    }
+    return o;
+}
+
+// The teacher's entries, and what each warp has found of its own: their largest logit, the sum
+// of their powers over it, and its part of the loss.
 template <int W>
 struct TeacherShared {
-    float t[DL_MAX_K], z[DL_MAX_K], q[DL_MAX_K];
-    int32_t id[DL_MAX_K];
+    float t[DL_MAX_K];
+    __align__(16) int32_t id[DL_MAX_K];
+    float2 soft[W];
+    float gap[W];
 };
 
+// Largest logit and sum of powers over it, of two sets.
+__device__ __forceinline__ float2 join_powers(float2 a, float2 b, float c) {
+    const float m = max_nan(a.x, b.x);
+    if (m == -CUDART_INF_F) return make_float2(m, 0.0f);
+    return make_float2(m, fmaf(a.y, ex2((a.x - m) * c), b.y * ex2((b.x - m) * c)));
+}
+
 // loss = weight sum_k q_k (log q_k - log p_{id_k}),  q = softmax(scale teacher);
-// dz = weight scale (p - q).  What fits of the block's share of the row stays in shared memory
-// between the sums and the gradient; the rest is read again, from L2 where the blocks that
-// run at once leave room for it.
+// dz = weight scale (p - q).  SAME: z's and dz's rows lie alike in their lines.
+//
+// Bound by the bytes of z and dz, and for short rows by the chain of a row's steps: so
+// thread k keeps the teacher's k-th entry in registers, its softmax and the loss ride on the
+// barriers that the row's sums and the gradient need anyway (a barrier for each step: 70 us
+// instead of NN for 4,096 rows of 8,192 bf16).  For the gradient the row is read again, out of
+// L2.  (Kept in shared memory instead, with the next row copied behind it, by blocks of 8, 16
+// or 32 warps: 255 to 290 us for 2,048 x 131,072 bf16, 148 for 4,096 x 32,768; read again: 240
+// and 122.  Fewer blocks fit, and they all read or all write at the same time.)
 template <int W, typename T, typename TO, bool SAME>
-__global__ void __launch_bounds__(Team<W>::BLOCK, W == 16 ? 2 : 3)
-    distill_kernel(const DistillParams p) {
+__global__ void __launch_bounds__(Team<W>::BLOCK, 3 * 256 / Team<W>::BLOCK) distill_kernel(const DistillParams p) {
     constexpr int N = Team<W>::THREADS, TEAMS = Team<W>::TEAMS;
-    extern __shared__ uint4 s_stash[];                 // W > 1
+    constexpr int OWN = DL_MAX_K / N;                  // entries of a thread
     __shared__ Soft s_soft[W + 1];
-    __shared__ float s_red[33];
     __shared__ TeacherShared<W> s_teacher[TEAMS];
     pdl_launch();
     pdl_wait();
@@ -953,116 +967,144 @@ __global__ void __launch_bounds__(Team<W>::BLOCK, W == 16 ? 2 : 3)
     if (r >= p.T) return;
     TeacherShared<W>& S = s_teacher[Team<W>::team()];
     const T* z = static_cast<const T*>(p.z) + r * p.ldz;
+    TO* dz = static_cast<TO*>(p.dz) + r * p.lddz;
     const float weight = p.weight ? p.weight[r] : 1.0f;
-    // (S belongs to the threads that write it until the sums are joined)
-    for (int k = tid; k < p.K; k += N) {
-        int64_t id = load_id(p.ids, p.id64, r * p.K + k);
-        if (id >= p.V) {
-            if (!p.scan && rank == 0) atomicOr(&p.ctrl->status, ST_BAD_INPUT);
-            id = -1;
+    int32_t id[OWN];
+    float t[OWN], zk[OWN];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+        const int k = i * N + tid;
+        int64_t v = -1;
+        t[i] = -CUDART_INF_F;
+        if (k < p.K) {
+            v = load_id(p.ids, p.id64, r * p.K + k);
+            t[i] = teacher_at(p, r * p.K + k);
         }
-        const bool there = id >= 0 && weight != 0.0f;
-        S.id[k] = (int32_t)max(id, (int64_t)-1);
-        S.t[k] = there ? teacher_at(p, r * p.K + k) : -CUDART_INF_F;
-        S.z[k] = there ? to_f32(z[id]) : 0.0f;
+        bad |= v >= p.V;
+        id[i] = v < 0 || v >= p.V ? -1 : (int32_t)v;
     }
     const LineRow<T> row(z, p.V);
     const int32_t lines = row.lines(), share = (lines + p.blocks - 1) / p.blocks;
     const int32_t line0 = min(lines, rank * share), line1 = min(lines, line0 + share);
-    const int32_t keep = W > 1 && p.dz ? p.keep : 0;
-    bool none = true;                              // no entry counts
+    if (bad && !p.scan && rank == 0) atomicOr(&p.ctrl->status, ST_BAD_INPUT);
     RowSoft a = {};
-    float big = 0.0f, q_sum = 1.0f, inv = 0.0f;
+    float2 teacher = make_float2(-CUDART_INF_F, 1.0f);
+    float inv = 0.0f;
     if (weight != 0.0f) {                          // (the same in all blocks of the cluster)
-        a = row_softmax<W, T, false, false, (W > 1 && SAME)>(row, line0, line1, p.c, p.blocks, s_soft,
-                                                             nullptr, s_stash, keep);
-        Team<W>::sync();
-        inv = a.s == 0.0f ? 0.0f : 1.0f / a.s;
-        // each warp for itself
-        big = -CUDART_INF_F;
-        for (int k = (int)lane_id(); k < p.K; k += 32) big = max_nan(big, S.t[k]);
+        const Running run = row_sums<W, T, false, false>(row, line0, line1, p.c, nullptr);
+        // the warp's part of the teacher's softmax, joined after the row's barrier
+        float2 own = make_float2(-CUDART_INF_F, 0.0f);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) big = max_nan(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
-        none = big == -CUDART_INF_F;
-        if (!none) {
-            q_sum = 0.0f;
-            for (int k = (int)lane_id(); k < p.K; k += 32) q_sum += ex2((S.t[k] - big) * p.c);
-            q_sum = warp_sum(q_sum);
-            for (int k = tid; k < p.K; k += N) S.q[k] = ex2((S.t[k] - big) * p.c) / q_sum;
+        for (int i = 0; i < OWN; ++i) {
+            if (i * N >= p.K) break;
+            if (id[i] < 0) t[i] = -CUDART_INF_F;
+            own.x = max_nan(own.x, t[i]);
+            if (i * N + tid < p.K) {
+                S.t[i * N + tid] = t[i];
+                S.id[i * N + tid] = id[i];
+            }
+            zk[i] = id[i] >= 0 ? to_f32(z[id[i]]) : 0.0f;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) own.x = max_nan(own.x, __shfl_xor_sync(0xFFFFFFFFu, own.x, o));
+        if (own.x != -CUDART_INF_F) {
+#pragma unroll
+            for (int i = 0; i < OWN; ++i) {
+                if (i * N >= p.K) break;
+                own.y += ex2((t[i] - own.x) * p.c);
+            }
+            own.y = warp_sum(own.y);
+        }
+        if (W > 1 && lane_id() == 0) S.soft[warp_id()] = own;
+        a = join_softmax<W>(row, line0, line1, p.c, p.blocks, s_soft, run);
+        inv = a.s == 0.0f ? 0.0f : 1.0f / a.s;
+        if (W == 1) {
+            __syncwarp();
+            teacher = own;
+        } else {
+            teacher = S.soft[0];
+#pragma unroll
+            for (int i = 1; i < W; ++i) teacher = join_powers(teacher, S.soft[i], p.c);
         }
     }
+    const bool none = teacher.x == -CUDART_INF_F;      // no entry counts
+    const float w = weight * p.scale, f = w * inv;
+    // the loss, and the gradient at the thread's tokens: the first entry of a token takes all of
+    // its q
+    float gap = 0.0f, at[OWN];
+    bool first[OWN];
+    if (!none) {
+        const float log_sum = logf(teacher.y), inv_sum = 1.0f / teacher.y;
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            const int k = i * N + tid;
+            first[i] = false;
+            if (i * N >= p.K) continue;
+            const float q = ex2((t[i] - teacher.x) * p.c) * inv_sum;
+            if (rank == 0 && id[i] >= 0 && q != 0.0f)
+                gap += q * (fmaf(t[i] - teacher.x, p.scale, -log_sum) - a.log_prob(zk[i], p.c, p.scale));
+            const int32_t line = id[i] >= 0 ? (id[i] + row.lead) / (LG_LINE / (int)sizeof(T)) : -1;
+            first[i] = p.dz && line >= line0 && line < line1;
+            if (!first[i]) continue;
+            // (entries of the same token are rare; a branch for each equal pair would be taken
+            // by one lane at a time)
+            int same = 0, before = 0;
+#pragma unroll 4
+            for (int j = 0; j < p.K; j += 4) {
+                const int4 v = *reinterpret_cast<const int4*>(S.id + j);
+                const int e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int l = 0; l < 4; ++l) {
+                    const int is = e[l] == id[i] && j + l < p.K;
+                    same += is;
+                    before += is & (j + l < k);
+                }
+            }
+            first[i] = before == 0;
+            float all = q;
+            if (same > 1 && first[i]) {
+                all = 0.0f;
+                for (int j = k; j < p.K; ++j)
+                    if (S.id[j] == id[i]) all = fmaf(ex2((S.t[j] - teacher.x) * p.c), inv_sum, all);
+            }
+            at[i] = w * fmaf(a.prob(zk[i], p.c), inv, -all);
+        }
+        gap = warp_sum(gap);
+        if (W > 1 && lane_id() == 0) S.gap[warp_id()] = gap;
+    }
     if (p.dz) {
-        TO* dz = static_cast<TO*>(p.dz) + r * p.lddz;
-        const float w = weight * p.scale, f = w * inv;
-        const f32x2 cc = pair(p.c, p.c), mm = pair(-a.m, -a.m), ff = pair(f, f);
-        const auto probs = [&](f32x2 v) {          // (times f)
-            if (!a.far) return mul2(ex2_2(fma2(v, cc, mm)), ff);
-            const float2 x = parts(v);
-            return pair(f * a.prob(x.x, p.c), f * a.prob(x.y, p.c));
-        };
         if (!SAME) {
             constexpr int32_t per = LG_LINE / (int)sizeof(T);
             const int32_t i1 = min(line1 * per, row.end) - row.lead;
             for (int32_t i = max(line0 * per - row.lead, 0) + tid; i < i1; i += N)
-                dz[i] = from_f32<TO>(none ? 0.0f : parts(probs(pair(to_f32(z[i]), 0.0f))).x);
+                dz[i] = from_f32<TO>(none ? 0.0f : f * a.prob(to_f32(z[i]), p.c));
         } else if (none) {
             const Chunk<TO> zero = {};
             for (int32_t j = line0 * 4 + tid; j < line1 * 4; j += N)
                 store_chunk(row, dz - row.lead, j * CHUNK<T>, zero);
         } else {
-            const auto put = [&](const Chunk<T>& v, int32_t j) {
-                Chunk<TO> o;
+            for_chunks<W, 2>(row, line0, line1, [&](const Chunk<T>* v, int32_t j, int32_t end) {
 #pragma unroll
-                for (int e = 0; e < CHUNK<T> / 2; ++e)
-                    put_pair(o, e, probs(Pairs<T>::template get<false>(v, e, 0.0f)));
-                store_chunk(row, dz - row.lead, j * CHUNK<T>, o);
-            };
-            // the rest first: it may still be in L2
-            if (line0 + keep / 4 < line1)
-                for_chunks<W, 2>(row, line0 + keep / 4, line1,
-                                 [&](const Chunk<T>* v, int32_t j, int32_t end) {
-                                     if (j < end) put(v[0], j);
-                                     if (j + N < end) put(v[1], j + N);
-                                 });
-            const int32_t kept = min(line0 * 4 + keep, line1 * 4);
-#pragma unroll 2
-            for (int32_t j = line0 * 4 + tid; j < kept; j += N) {
-                Chunk<T> v;
-                get_stash<W>(s_stash, j - line0 * 4, v);
-                put(v, j);
-            }
-        }
-        if (!none) {
-            // the teacher's tokens: the first entry of each takes all of its q
-            Team<W>::sync();
-            for (int k = tid; k < p.K; k += N) {
-                const int32_t id = S.id[k];
-                const int32_t line = id >= 0 ? (id + row.lead) / (LG_LINE / (int)sizeof(T)) : -1;
-                if (line < line0 || line >= line1) continue;
-                float all = 0.0f;
-                bool first = true;
-#pragma unroll 8
-                for (int i = 0; i < p.K; ++i)
-                    if (S.id[i] == id) {
-                        all += S.q[i];
-                        first = first && i >= k;
-                    }
-                if (first) dz[id] = from_f32<TO>(w * (a.prob(S.z[k], p.c) * inv - all));
-            }
+                for (int k = 0; k < 2; ++k, j += N)
+                    if (j < end)
+                        store_chunk(row, dz - row.lead, j * CHUNK<T>, grad_chunk<T, TO>(v[k], a, p.c, f));
+            });
         }
     }
-    if (rank == 0 && p.loss) {
-        float part = 0.0f;
-        if (!none) {
-            const float log_q = logf(q_sum);
-            for (int k = tid; k < p.K; k += N) {
-                const float q = S.q[k];
-                if (q != 0.0f)
-                    part += q * (fmaf(S.t[k] - big, p.scale, -log_q) - a.log_prob(S.z[k], p.c, p.scale));
-            }
+    Team<W>::sync();
+    if (!none) {
+#pragma unroll
+        for (int i = 0; i < OWN; ++i)
+            if (first[i]) dz[id[i]] = from_f32<TO>(at[i]);
+    }
+    if (rank == 0 && tid == 0 && p.loss) {
+        if (W > 1 && !none) {
+            gap = 0.0f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) gap += S.gap[i];
         }
-        part = Team<W>::sum(part, s_red);
-        if (tid == 0) p.loss[r] = none ? 0.0f : weight * part;
+        p.loss[r] = none ? 0.0f : weight * gap;
     }
     if (W > 1 && weight != 0.0f && p.blocks > 1) cluster_sync();   // no block leaves while its memory is read
 }

@@ -19,9 +19,16 @@ namespace {
 constexpr int64_t SCAN_IDS = 8192;         // ids that one block checks
 constexpr int SMS = 148;
 constexpr int64_t LEAST_LINES = 32;        // lines of a block of a cluster
-// Short rows take a warp each from here on: as many as blocks that run at once.  (64 rows of
-// 1,000 bf16, top 20: a block each 9.4 us, a warp each 13; 16,384 rows: 280 and 60 us.)
-constexpr int64_t WARP_ROWS = SMS * 3;
+// Bytes of logits that L2 holds besides what is written (2,048 x 131,072 bf16, 114 MB: 255 us
+// one block a row, 239 two).
+constexpr int64_t GRAD_L2 = (int64_t)80 << 20;
+// Warps of a row: fewer for short rows once there are more of them than blocks that run at
+// once.  (64 rows of 1,000 bf16, top 20: eight warps each 9.4 us, one 13; 16,384 rows: 280 and
+// 72 us.)
+int row_warps(int64_t T, int64_t lines) {
+    if (T <= SMS * 3) return 8;
+    return lines <= LG_SMALL ? 1 : lines <= LG_MIDDLE ? 4 : 8;
+}
 
 bool sizes_ok(int64_t T, int64_t V) {
     return T >= 0 && T <= MAX_N && V >= 1 && V <= (int64_t)1 << 24;
@@ -76,31 +83,22 @@ cudaError_t launch_logprob(const LogprobParams& p, size_t smem, cudaStream_t st)
 }
 
 template <typename T, bool ENTROPY, bool TOP>
-cudaError_t logprob_by_length(const LogprobParams& p, bool small, size_t smem, cudaStream_t st) {
-    return small ? launch_logprob<1, T, ENTROPY, TOP>(p, smem, st)
-                 : launch_logprob<8, T, ENTROPY, TOP>(p, smem, st);
+cudaError_t logprob_by_length(const LogprobParams& p, int warps, size_t smem, cudaStream_t st) {
+    return warps == 1   ? launch_logprob<1, T, ENTROPY, TOP>(p, smem, st)
+           : warps == 4 ? launch_logprob<4, T, ENTROPY, TOP>(p, smem, st)
+                        : launch_logprob<8, T, ENTROPY, TOP>(p, smem, st);
 }
 
 template <int W, typename T, typename TO, bool SAME>
-cudaError_t launch_distill(DistillParams p, cudaStream_t st) {
+cudaError_t launch_distill(const DistillParams& p, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    // what the blocks of an SM leave one another, in whole rounds of chunks
-    constexpr size_t round = (size_t)Team<W>::THREADS * 32;
-    constexpr size_t room =
-        W == 1 ? 0 : (233472 / (W == 16 ? 2 : 3) - 1024 - sizeof(TeacherShared<W>) - 1024) / round * round;
     const auto kernel = distill_kernel<W, T, TO, SAME>;
-    cudaError_t e = allow(kernel, done, room);
+    cudaError_t e = allow(kernel, done, 0);
     if (e != cudaSuccess) return e;
-    size_t smem = 0;
-    if (SAME && p.dz) {
-        const int64_t share = ceil_div64(p.lines, p.blocks);
-        smem = std::min(room, (size_t)ceil_div64(share * LG_LINE, round) * round);
-        p.keep = (int32_t)(smem / 32);
-    }
     const int64_t rows = ceil_div64(p.T, Team<W>::TEAMS);
     trace_before(st, "distill_kernel");
     e = launch_clusters(kernel, (unsigned)((rows + p.scan) * p.blocks), (unsigned)p.blocks,
-                        Team<W>::BLOCK, smem, st, p);
+                        Team<W>::BLOCK, 0, st, p);
     trace_after(st);
     return e;
 }
@@ -108,8 +106,8 @@ cudaError_t launch_distill(DistillParams p, cudaStream_t st) {
 template <typename T, typename TO, bool SAME>
 cudaError_t distill_by_length(const DistillParams& p, int warps, cudaStream_t st) {
     return warps == 1   ? launch_distill<1, T, TO, SAME>(p, st)
-           : warps == 8 ? launch_distill<8, T, TO, SAME>(p, st)
-                        : launch_distill<16, T, TO, SAME>(p, st);
+           : warps == 4 ? launch_distill<4, T, TO, SAME>(p, st)
+                        : launch_distill<8, T, TO, SAME>(p, st);
 }
 
 }  // namespace
@@ -152,8 +150,8 @@ int token_logprobs(const void* logits, int32_t logits_type, int64_t ld_logits, c
     p.padding = padding_idx;
     p.id64 = id_bytes == 8;
     p.top = top_ids || top_logprobs ? top : 0;
-    const bool small = lines <= LG_SMALL && T > WARP_ROWS;
-    p.blocks = small ? 1 : row_blocks(T, lines, SMS * 3);
+    const int warps = row_warps(T, lines);
+    p.blocks = warps < 8 ? 1 : row_blocks(T, lines, SMS * 3);
     p.scan = T <= SCAN_IDS;
     p.scale = scale;
     p.c = (float)((double)scale * 1.4426950408889634);
@@ -165,10 +163,10 @@ int token_logprobs(const void* logits, int32_t logits_type, int64_t ld_logits, c
     const cudaError_t e = with_type(logits_type, [&](auto t) {
         using TZ = decltype(t);
         if (p.top)
-            return entropy ? logprob_by_length<TZ, true, true>(p, small, smem, st)
-                           : logprob_by_length<TZ, false, true>(p, small, smem, st);
-        return entropy ? logprob_by_length<TZ, true, false>(p, small, smem, st)
-                       : logprob_by_length<TZ, false, false>(p, small, smem, st);
+            return entropy ? logprob_by_length<TZ, true, true>(p, warps, smem, st)
+                           : logprob_by_length<TZ, false, true>(p, warps, smem, st);
+        return entropy ? logprob_by_length<TZ, true, false>(p, warps, smem, st)
+                       : logprob_by_length<TZ, false, false>(p, warps, smem, st);
     });
     return e == cudaSuccess ? TOPK_EF_OK : cuda_fail(e);
 }
@@ -275,13 +273,14 @@ int distill_loss(const void* logits, int32_t logits_type, int64_t ld_logits,
     p.id64 = id_bytes == 8;
     p.teacher_type = teacher_type;
     p.K = K;
-    // (with the gradient, rows that shared memory does not hold as a whole take blocks of 16
-    // warps, so that fewer rows are read again out of L2)
-    p.lines = (int32_t)most_lines(logits, ld_logits, V, sz);
-    const int warps = p.lines <= LG_SMALL && T > WARP_ROWS              ? 1
-                      : grad_logits && p.lines > 512 && T >= SMS * 2 ? 16
-                                                                        : 8;
-    p.blocks = warps == 8 ? row_blocks(T, p.lines, SMS * 3) : 1;
+    const bool same = grad_logits && sz == so &&
+                      same_lines(logits, ld_logits, grad_logits, ld_grad_logits, sz);
+    const int64_t lines = most_lines(logits, ld_logits, V, sz);
+    const int warps = row_warps(T, lines);
+    p.blocks = warps < 8 ? 1 : row_blocks(T, lines, SMS * 3);
+    // rows that blocks are at should fit L2 until their gradient is written
+    if (grad_logits && warps == 8)
+        while (p.blocks < 4 && lines * LG_LINE * (SMS * 3 / p.blocks) > GRAD_L2) p.blocks *= 2;
     p.scan = T * std::max(K, 1) <= SCAN_IDS;
     p.scale = scale;
     p.c = (float)((double)scale * 1.4426950408889634);
@@ -289,8 +288,6 @@ int distill_loss(const void* logits, int32_t logits_type, int64_t ld_logits,
         const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(Ctrl), st);
         if (e != cudaSuccess) return cuda_fail(e);
     }
-    const bool same = grad_logits && sz == so &&
-                      same_lines(logits, ld_logits, grad_logits, ld_grad_logits, sz);
     const cudaError_t e = with_type(logits_type, [&](auto t) {
         return with_type(grad_logits ? grad_logits_type : logits_type, [&](auto to) {
             using TZ = decltype(t);
