@@ -739,13 +739,23 @@ def _vector(t, name: str, n: int, device, dtype=None):
     for None."""
     if t is None:
         return None, 0
-    if not isinstance(t, torch.Tensor) or t.get_device() != device.index or t.numel() != n \
-            or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of {n} on {device}")
-    code = _TYPE.get(t.dtype)
-    if code is None or (dtype is not None and t.dtype != dtype):
+    if isinstance(t, torch.Tensor) and t.get_device() == device.index and t.numel() == n \
+            and t.is_contiguous():
+        code = _TYPE.get(t.dtype)
+        if code is not None and (dtype is None or t.dtype is dtype):
+            return t.data_ptr(), code
         raise ValueError(f"{name} must be {dtype or 'float32, bfloat16 or float16'}")
-    return t.data_ptr(), code
+    raise ValueError(f"{name} must be a contiguous tensor of {n} on {device}")
+
+
+def _f32(t, name: str, n: int, device, index: int):
+    """Address of a contiguous float32 [n] tensor on the device; None for None."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.get_device() == index \
+            and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous float32 tensor of {n} on {device}")
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=None, mean=None, rstd=None,
@@ -762,11 +772,11 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=None, me
     T, D = x2.shape
     wp, wt = _vector(weight, "weight", D, dev)
     bp, bt = _vector(bias, "bias", D, dev)
-    _vector(mean, "mean", T, dev, torch.float32)
-    _vector(rstd, "rstd", T, dev, torch.float32)
+    mp = _f32(mean, "mean", T, dev, dev.index)
+    rp = _f32(rstd, "rstd", T, dev, dev.index)
 
     def call(st):
-        o, m, r = out, mean, rstd
+        o, m, r, ma, ra = out, mean, rstd, mp, rp
         if o is None:
             o = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=dev)
         elif out_dtype is not None and o.dtype != out_dtype:
@@ -777,11 +787,12 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=None, me
         if stats:
             if m is None:
                 m = torch.empty(T, dtype=torch.float32, device=dev)
+                ma = m.data_ptr()
             if r is None:
                 r = torch.empty(T, dtype=torch.float32, device=dev)
-        rc = lib().layer_norm(x2.data_ptr(), xt, ldx, wp, wt, bp, bt, T, D, eps, o2.data_ptr(), ot,
-                              ldo, None if m is None else m.data_ptr(),
-                              None if r is None else r.data_ptr(), st)
+                ra = r.data_ptr()
+        rc = (_lib or lib()).layer_norm(x2.data_ptr(), xt, ldx, wp, wt, bp, bt, T, D, eps,
+                                        o2.data_ptr(), ot, ldo, ma, ra, st)
         if rc != OK:
             _check(rc, "layer_norm")
         return o, m, r
@@ -810,8 +821,8 @@ def layer_norm_grad(grad_out, x, mean, rstd, weight=None, affine=True, accumulat
     wp, wt = _vector(weight, "weight", D, dev)
     if mean is None or rstd is None:
         raise ValueError("mean and rstd are needed")
-    mp = _vector(mean, "mean", T, dev, torch.float32)[0]
-    rp = _vector(rstd, "rstd", T, dev, torch.float32)[0]
+    mp = _f32(mean, "mean", T, dev, dev.index)
+    rp = _f32(rstd, "rstd", T, dev, dev.index)
     if affine and accumulate and (grad_weight is None or grad_bias is None):
         raise ValueError("accumulate needs grad_weight and grad_bias")
     _on_device(ws, dev)
@@ -893,18 +904,22 @@ def token_logprobs(logits, ids=None, scale=1.0, top=0, padding_idx=-1, logprob=N
     if top == 0 and (top_ids is not None and top_ids.numel()
                      or top_logprobs is not None and top_logprobs.numel()):
         raise ValueError("top_ids and top_logprobs need top")
-    for t, name in ((logprob, "logprob"), (entropy, "entropy"), (lse, "lse")):
-        _vector(t, name, T, dev, torch.float32)
+    lpp = _f32(logprob, "logprob", T, dev, dev.index)
+    enp = _f32(entropy, "entropy", T, dev, dev.index)
+    lsp = _f32(lse, "lse", T, dev, dev.index)
     _on_device(ws, dev)
 
     def call(st):
-        lp, en, ls, ti, tp = logprob, entropy, lse, top_ids, top_logprobs
+        lp, en, ls, ti, tp, la, ea, sa = logprob, entropy, lse, top_ids, top_logprobs, lpp, enp, lsp
         if lp is None and ids is not None:
             lp = torch.empty(T, dtype=torch.float32, device=dev)
+            la = lp.data_ptr()
         if en is None:
             en = torch.empty(T, dtype=torch.float32, device=dev)
+            ea = en.data_ptr()
         if ls is None:
             ls = torch.empty(T, dtype=torch.float32, device=dev)
+            sa = ls.data_ptr()
         if top > 0:
             if ti is None:
                 ti = torch.empty((T, top), dtype=torch.int32, device=dev)
@@ -913,10 +928,11 @@ def token_logprobs(logits, ids=None, scale=1.0, top=0, padding_idx=-1, logprob=N
             _table(ti, "top_ids", T, top, dev, torch.int32)
             _table(tp, "top_logprobs", T, top, dev, torch.float32)
         w = ws if ws is not None else _workspace(_STATUS_WS, dev, None)
-        rc = lib().token_logprobs(z.data_ptr(), zt, ldz, ip, idb, T, V, scale, int(padding_idx), top,
-                                  None if lp is None else lp.data_ptr(), en.data_ptr(),
-                                  ls.data_ptr(), ti.data_ptr() if top > 0 else None,
-                                  tp.data_ptr() if top > 0 else None, w.data_ptr(), w.nbytes, st)
+        rc = (_lib or lib()).token_logprobs(z.data_ptr(), zt, ldz, ip, idb, T, V, scale,
+                                            int(padding_idx), top, la, ea, sa,
+                                            ti.data_ptr() if top > 0 else None,
+                                            tp.data_ptr() if top > 0 else None, w.data_ptr(),
+                                            w.nbytes, st)
         if rc != OK:
             _check(rc, "token_logprobs")
         return lp, en, ls, ti, tp
@@ -951,10 +967,10 @@ def token_logprobs_grad(logits, ids, lse, grad_logprob=None, entropy=None, grad_
     if lse is None or (grad_entropy is not None and entropy is None) or \
             (grad_logprob is not None and ids is None):
         raise ValueError("lse, ids for grad_logprob and entropy for grad_entropy are needed")
-    sp = _vector(lse, "lse", T, dev, torch.float32)[0]
-    ep = _vector(entropy, "entropy", T, dev, torch.float32)[0]
-    gp = _vector(grad_logprob, "grad_logprob", T, dev, torch.float32)[0]
-    hp = _vector(grad_entropy, "grad_entropy", T, dev, torch.float32)[0]
+    sp = _f32(lse, "lse", T, dev, dev.index)
+    ep = _f32(entropy, "entropy", T, dev, dev.index)
+    gp = _f32(grad_logprob, "grad_logprob", T, dev, dev.index)
+    hp = _f32(grad_entropy, "grad_entropy", T, dev, dev.index)
     _on_device(ws, dev)
 
     def call(st):
@@ -996,20 +1012,22 @@ def distill_loss(logits, teacher_ids, teacher_logits, weight=None, scale=1.0, gr
     tp, tt = _vector(teacher_logits, "teacher_logits", T * K, dev)
     if tp is None:
         raise ValueError("teacher_logits are needed")
-    wp = _vector(weight, "weight", T, dev, torch.float32)[0]
-    _vector(loss, "loss", T, dev, torch.float32)
+    wp = _f32(weight, "weight", T, dev, dev.index)
+    lp = _f32(loss, "loss", T, dev, dev.index)
     _on_device(ws, dev)
 
     def call(st):
-        lo, o, op, ot, ldo = loss, grad_logits, None, 0, V
+        lo, la, o, op, ot, ldo = loss, lp, grad_logits, None, 0, V
         if lo is None:
             lo = torch.empty(T, dtype=torch.float32, device=dev)
+            la = lo.data_ptr()
         if grad or o is not None:
             o, o2, ot, ldo = _grad_rows(o, logits, out_dtype, dev)
             op = o2.data_ptr()
         w = ws if ws is not None else _workspace(_STATUS_WS, dev, None)
-        rc = lib().distill_loss(z.data_ptr(), zt, ldz, teacher_ids.data_ptr(), idb, tp, tt, T, V, K,
-                                scale, wp, lo.data_ptr(), op, ot, ldo, w.data_ptr(), w.nbytes, st)
+        rc = (_lib or lib()).distill_loss(z.data_ptr(), zt, ldz, teacher_ids.data_ptr(), idb, tp, tt,
+                                          T, V, K, scale, wp, la, op, ot, ldo, w.data_ptr(),
+                                          w.nbytes, st)
         if rc != OK:
             _check(rc, "distill_loss")
         return lo, o

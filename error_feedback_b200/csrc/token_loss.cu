@@ -42,10 +42,11 @@ int64_t most_lines(const void* z, int64_t ld, int64_t V, size_t size) {
     return whole ? ceil_div64(V * (int64_t)size, LG_LINE) : (V * (int64_t)size + LG_LINE - 2) / LG_LINE + 1;
 }
 
-// Blocks of a row's cluster: more while the call has fewer than `want`.
-int row_blocks(int64_t T, int64_t lines, int64_t want) {
+// Blocks of a row's cluster: as many as run at once with `most` of the call's (a second round
+// of blocks would take as long as the first: 64 x 32,768 bf16 11.8 us with eight, NN with four).
+int row_blocks(int64_t T, int64_t lines, int64_t most) {
     int c = 1;
-    while (c < 16 && T * c < want && lines / (2 * c) >= LEAST_LINES) c *= 2;
+    while (c < 16 && T * 2 * c <= most && lines / (2 * c) >= LEAST_LINES) c *= 2;
     return c;
 }
 
