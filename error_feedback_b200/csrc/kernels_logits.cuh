@@ -471,7 +471,7 @@ struct TopShared {
     uint32_t count[2 * W];
     uint32_t scan[33];
     uint32_t line[LINES];
-    unsigned long long list[LIST];         // key, then the lower index first
+    __align__(16) unsigned long long list[LIST];   // key, then the lower index first
 };
 
 // Sum of v over the team (every thread gets it); `flip`: not the last call's.
@@ -524,14 +524,6 @@ __device__ __forceinline__ uint32_t bin_of(const uint32_t* hist, uint32_t want, 
     const int at = __ffs(__ballot_sync(0xFFFFFFFFu, in2 >= want)) - 1;
     upto = __shfl_sync(0xFFFFFFFFu, in2, at);
     return (uint32_t)(src * EACH + at);
-}
-
-// A place in a list in shared memory for each lane that wants one.
-__device__ __forceinline__ uint32_t slot(uint32_t* n, bool want) {
-    const uint32_t who = __ballot_sync(0xFFFFFFFFu, want);
-    uint32_t first = 0;
-    if (lane_id() == 0 && who) first = atomicAdd(n, (uint32_t)__popc(who));
-    return __shfl_sync(0xFFFFFFFFu, first, 0) + __popc(who & ((1u << lane_id()) - 1));
 }
 
 // The lists by exact counts, where the bins hold too many: the K-th largest of the lines'
@@ -667,29 +659,32 @@ __device__ __forceinline__ void select_top(const LogprobParams& p, const LineRow
                                                   : __uint_as_float(0x3F800000u + ((bin + 1) << 18));
             const auto within = [&](float z) { return depth(z, c, m) < edge || bin == TL_BINS - 1; };
             if (some) {
-                for (int l0 = 0; l0 < lines; l0 += N) {
-                    const int l = l0 + tid;
-                    const bool in = l < lines && within(tops[l]);
-                    const uint32_t at = slot(&S.lines, in);
-                    if (in) S.line[at] = (uint32_t)l;
-                }
+                for (int l = tid; l < lines; l += N)
+                    if (within(tops[l])) S.line[atomicAdd(&S.lines, 1u)] = (uint32_t)l;
                 Team<W>::sync();
             }
             const int chunks = (some ? (int)S.lines : lines) * 4;
             for (int j = tid; j < chunks; j += N) {
                 const int32_t chunk = (some ? (int32_t)S.line[j >> 2] : j >> 2) * 4 + (j & 3);
+                const int32_t pos = chunk * CHUNK<T>;
                 Chunk<T> q;
                 load_chunk(row, chunk, q);
+                // which are within, then places for all of them at once
+                uint32_t in = 0;
 #pragma unroll
-                for (int e = 0; e < CHUNK<T>; ++e) {
-                    const int32_t pos = chunk * CHUNK<T> + e;
-                    const float z = q.get(e);
-                    if (!within(z) || pos < row.lead || pos >= row.end) continue;
-                    const uint32_t at = atomicAdd(&S.n, 1u);
-                    if (at < LIST)
-                        S.list[at] =
-                            (unsigned long long)order_key(z) << 32 | (uint32_t)(row.end - 1 - pos);
-                }
+                for (int e = 0; e < CHUNK<T>; ++e) in |= (uint32_t)within(q.get(e)) << e;
+                if (pos < row.lead) in &= ~0u << min(row.lead - pos, 31);
+                if (pos + CHUNK<T> > row.end) in &= (1u << max(row.end - pos, 0)) - 1;
+                if (in == 0) continue;
+                uint32_t at = atomicAdd(&S.n, (uint32_t)__popc(in));
+#pragma unroll
+                for (int e = 0; e < CHUNK<T>; ++e)
+                    if (in >> e & 1) {
+                        if (at < LIST)
+                            S.list[at] = (unsigned long long)order_key(q.get(e)) << 32 |
+                                         (uint32_t)(row.end - 1 - pos - e);
+                        ++at;
+                    }
             }
             Team<W>::sync();
             exactly = S.n > LIST;
@@ -702,7 +697,11 @@ __device__ __forceinline__ void select_top(const LogprobParams& p, const LineRow
         const unsigned long long mine = S.list[i];
         uint32_t rank = 0;
 #pragma unroll 4
-        for (uint32_t j = 0; j < n; ++j) rank += S.list[j] > mine;
+        for (uint32_t j = 0; j + 1 < n; j += 2) {
+            const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(S.list + j);
+            rank += (two.x > mine) + (two.y > mine);
+        }
+        if (n & 1) rank += S.list[n - 1] > mine;
         if (rank < (uint32_t)K) {
             const float z = key_value((uint32_t)(mine >> 32));
             const int32_t id = row.end - 1 - (int32_t)(uint32_t)mine - row.lead;
@@ -723,7 +722,7 @@ template <int W, typename T, bool ENTROPY, bool TOP>
 __global__ void __launch_bounds__(Team<W>::BLOCK, LOGPROB_BLOCKS<W, TOP>)
     logprob_kernel(const LogprobParams p) {
     constexpr int N = Team<W>::THREADS, TEAMS = Team<W>::TEAMS;
-    extern __shared__ float s_dyn[];                   // TOP, W > 1: [lines of the row]
+    extern __shared__ __align__(16) float s_dyn[];     // TOP, W > 1: [lines of the row, in fours]
     __shared__ Soft s_soft[W + 1];
     __shared__ TopShared<W> S[TEAMS];
     __shared__ float s_small[TOP && W == 1 ? TEAMS * LG_SMALL : 1];
@@ -761,39 +760,42 @@ __global__ void __launch_bounds__(Team<W>::BLOCK, LOGPROB_BLOCKS<W, TOP>)
     }
     const T* z = static_cast<const T*>(p.z) + r * p.ldz;
     float zt = 0.0f;
-    if (ok && rank == 0 && tid == 0) zt = to_f32(z[id]);
+    if (ok && rank == 0 && tid == N - 32) zt = to_f32(z[id]);
     const LineRow<T> row(z, p.V);
     const int32_t lines = row.lines();
-    const int32_t share = (lines + p.blocks - 1) / p.blocks;
+    const int32_t share = ((lines + p.blocks - 1) / p.blocks + 3) & ~3;
     const int32_t line0 = min(lines, rank * share), line1 = min(lines, line0 + share);
     const Running run = row_sums<W, T, ENTROPY, TOP>(row, line0, line1, p.c, s_tops);
     const RowSoft a = join_softmax<W>(row, line0, line1, p.c, p.blocks, s_soft, run);
-    if (rank == 0 && tid == 0) {
-        if (p.logprob) p.logprob[r] = ok ? a.log_prob(zt, p.c, p.scale) : 0.0f;
-        if (ENTROPY && p.entropy) p.entropy[r] = a.entropy();
-        if (p.lse) p.lse[r] = a.log_sum(p.scale);
-    }
     if (TOP && rank == 0) {
         // the other blocks' lines, several on their way at once
         if (W > 1 && p.blocks > 1) {
-            constexpr int AHEAD = 8;
-            for (int32_t l0 = line1; l0 < lines; l0 += AHEAD * N) {
-                float k[AHEAD];
+            constexpr int AHEAD = 4;
+            for (int32_t l0 = share; l0 < lines; l0 += AHEAD * N * 4) {
+                float4 k[AHEAD];
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) {
-                    const int32_t l = l0 + i * N + tid;
+                    const int32_t l = l0 + (i * N + tid) * 4;      // (of one block: shares of fours)
                     if (l < lines)
-                        asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                     : "=f"(k[i])
+                        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(k[i].x), "=f"(k[i].y), "=f"(k[i].z), "=f"(k[i].w)
                                      : "r"(in_block(smem_u32(s_tops + l), (uint32_t)(l / share))));
                 }
 #pragma unroll
-                for (int i = 0; i < AHEAD; ++i)
-                    if (l0 + i * N + tid < lines) s_tops[l0 + i * N + tid] = k[i];
+                for (int i = 0; i < AHEAD; ++i) {
+                    const int32_t l = l0 + (i * N + tid) * 4;
+                    if (l < lines) *reinterpret_cast<float4*>(s_tops + l) = k[i];
+                }
             }
         }
         Team<W>::sync();
         select_top<W, T>(p, row, r, s_tops, S[Team<W>::team()], a);
+    }
+    // (by the last warp: the first ones rank)
+    if (rank == 0 && tid == N - 32) {
+        if (p.logprob) p.logprob[r] = ok ? a.log_prob(zt, p.c, p.scale) : 0.0f;
+        if (ENTROPY && p.entropy) p.entropy[r] = a.entropy();
+        if (p.lse) p.lse[r] = a.log_sum(p.scale);
     }
     if (W > 1 && p.blocks > 1) cluster_sync();     // no block leaves while its memory is read
 }

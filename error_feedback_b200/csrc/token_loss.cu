@@ -160,7 +160,7 @@ int token_logprobs(const void* logits, int32_t logits_type, int64_t ld_logits, c
         const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(Ctrl), st);
         if (e != cudaSuccess) return cuda_fail(e);
     }
-    const size_t smem = p.top ? (size_t)lines * 4 : 0;
+    const size_t smem = p.top ? ((size_t)lines * 4 + 15) / 16 * 16 : 0;
     const cudaError_t e = with_type(logits_type, [&](auto t) {
         using TZ = decltype(t);
         if (p.top)
