@@ -73,6 +73,13 @@ __device__ __forceinline__ void store8(T* p, const float* x) {
     }
 }
 
+// The larger value; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
 // Two values a register pair, two values an instruction.
 typedef unsigned long long f32x2;
 __device__ __forceinline__ f32x2 pair(float lo, float hi) {

@@ -2,11 +2,12 @@
 //
 //   mean = 1/D sum x,  rstd = (1/D sum (x - mean)^2 + eps)^(-1/2),  y = (x - mean) rstd w + b
 //
-// All sums are fp32, of the row less its first element c: at most sqrt(D) deviations
-// from the mean, so an offset common to a row costs no bits.  The variance
-// is a sum of squares of differences, never a difference of sums: each warp sums the
-// squares of the differences from its own elements' mean, and the warps' (count,
-// sum, squares) are joined by sum n (mean_w - mean)^2.
+// All sums are fp32, and an offset common to a row costs no bits: each warp sums the
+// differences of its elements from their own (rounded) mean m_w, which makes good the
+// rounding, and their squares, and the warps' parts are joined by their distances from the
+// first one's, so the variance is a sum of squares of differences, never a difference of
+// sums, and x - mean is (x - m_w) less a small rest.  The mean that is given out is the
+// plain sum's, unless it is far more than the deviation: then m_0 and the rest are nearer.
 //
 // A row is held in registers by 8 to 1,024 threads, 16 elements each, between the statistics
 // and the result; w and b stay in registers over all rows of a block.  The rows that follow
@@ -299,22 +300,23 @@ __device__ __forceinline__ void read_row(const char* slot, const T* row, int t, 
     }
 }
 
-// Sums over the G threads of a row of (a, b), which each of a warp's lanes holds already summed
-// over its warp; s: two places a warp, `flip` the ones that the last call did not use.
-// Also a barrier of the row.
-template <int G, typename F>
-__device__ __forceinline__ float2 row_parts(float2 v, float2 (*s)[NORM_BLOCK<G> / 32], int& flip, F f) {
+// f(v of the row's warp lane % W, v of its first warp), where v is what each of a warp's lanes
+// has found for its warp; s: two places a warp, `flip` the ones that the last call did not
+// use.  (Rows of one warp: f(v, v).)  Also a barrier of the row.
+template <int G, typename P, typename F>
+__device__ __forceinline__ auto row_parts(P v, P (*s)[NORM_BLOCK<G> / 32], int& flip, F f) {
     constexpr int W = G < 64 ? 1 : G / 32;
-    if (W == 1) {
+    if constexpr (W == 1) {
         __syncwarp();
-        return v;
+        return f(v, v);
+    } else {
+        const int warp = (int)warp_id(), lane = (int)lane_id();
+        if (lane == 0) s[flip][warp] = v;
+        row_sync<G>();
+        const P o = s[flip][warp / W * W + lane % W], first = s[flip][warp / W * W];
+        flip ^= 1;
+        return f(o, first);
     }
-    const int warp = (int)warp_id(), lane = (int)lane_id();
-    if (lane == 0) s[flip][warp] = v;
-    row_sync<G>();
-    const float2 o = s[flip][warp / W * W + lane % W];     // (lanes W apart hold the same)
-    flip ^= 1;
-    return f(o);
 }
 
 // The pair of elements 2 e and 2 e + 1, 0 where the thread has none.
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(NORM_BLOCK<G>, G <= 256 ? 3 : 1) norm_kernel(c
     constexpr int E = NR_ELEMS, ROWS = NORM_BLOCK<G> / G, L = G < 32 ? G : 32, W = G < 64 ? 1 : G / 32;
     constexpr int S = NR_SLOTS<TX, G>, BYTES = NR_BYTES<TX, G, V>;
     extern __shared__ __align__(16) char s_ring[];     // [row of the block][S][BYTES]
-    __shared__ float2 s_part[2][NORM_BLOCK<G> / 32];
+    __shared__ float4 s_part[2][NORM_BLOCK<G> / 32];   // mean, rest, squares, sum of a warp's elements
     pdl_launch();
     const int t = (int)(threadIdx.x % G), D = (int)p.D, lane = (int)lane_id();
     const TX* x = static_cast<const TX*>(p.x);
@@ -350,10 +352,12 @@ __global__ void __launch_bounds__(NORM_BLOCK<G>, G <= 256 ? 3 : 1) norm_kernel(c
         if (r + i * step < p.T) copy_row<TX, G, V>(ring_at + i * BYTES, x + (r + i * step) * p.ldx, t, D);
         copies_commit();
     }
-    TX next_c = r < p.T ? x[r * p.ldx] : from_f32<TX>(0.0f);
+    // (the first element of a 16-bit row that starts within a word is not copied)
+    TX next_first = from_f32<TX>(0.0f);
+    if (V == 1 && sizeof(TX) == 2 && r < p.T) next_first = x[r * p.ldx];
     // elements of this warp's lanes, and of the warp that a lane joins for
     const float n = (float)warp_count<G, V>(t - t % L, D), inv_n = n > 0.0f ? 1.0f / n : 0.0f;
-    const float k = W > 1 ? (float)warp_count<G, V>(lane % W * 32, D) : 0.0f;
+    const float k = W > 1 ? (float)warp_count<G, V>(lane % W * 32, D) : (float)D;
     const uint32_t mask = elems_mask<G, V>(t, D);
     f32x2 w[E / 2], b[E / 2];
     row_weights<G, V>(p.w, p.w_type, t, D, 1.0f, w);
@@ -367,42 +371,44 @@ __global__ void __launch_bounds__(NORM_BLOCK<G>, G <= 256 ? 3 : 1) norm_kernel(c
             copy_row<TX, G, V>(ring_at + free_slot * BYTES, row + (S - 1) * step * p.ldx, t, D);
         copies_commit();
         RowRegs<TX> v;
-        read_row<TX, G, V>(ring + slot * BYTES, row, t, mask, next_c, v);
-        const f32x2 c = both(-to_f32(next_c));
-        if (r + step < p.T) next_c = row[step * p.ldx];
+        read_row<TX, G, V>(ring + slot * BYTES, row, t, mask, next_first, v);
+        if (V == 1 && sizeof(TX) == 2 && r + step < p.T) next_first = row[step * p.ldx];
         free_slot = slot;
         slot = slot + 1 == S ? 0 : slot + 1;
-        // d = x - c, 0 past the row's end
-        f32x2 d[E / 2], sum = 0;
+        f32x2 sum = 0;                                 // (0 past the row's end)
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) d[e] = masked<G, V>(add2(v.two(e), c), mask, e);
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) sum = add2(sum, d[e]);
+        for (int e = 0; e < E / 2; ++e) sum = add2(sum, v.two(e));
         const float2 s = parts(sum);
-        // the mean of the warp's elements, less c, and the squares of the distances from it
-        const float m0 = lanes_sum<L>(s.x + s.y) * inv_n;
-        f32x2 sq2 = 0;
+        const float total = lanes_sum<L>(s.x + s.y), m0 = total * inv_n;
+        f32x2 d[E / 2], sq2 = 0, rest2 = 0;
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) {
-            const f32x2 q = masked<G, V>(add2(d[e], both(-m0)), mask, e);
-            sq2 = fma2(q, q, sq2);
+            d[e] = masked<G, V>(add2(v.two(e), both(-m0)), mask, e);
+            sq2 = fma2(d[e], d[e], sq2);
+            rest2 = add2(rest2, d[e]);
         }
-        const float2 q = parts(sq2);
+        const float2 q = parts(sq2), u = parts(rest2);
+        const float rest = lanes_sum<L>(u.x + u.y) * inv_n, sq = lanes_sum<L>(q.x + q.y);
         copies_wait<S - 2>();                          // (the next row, before the barrier)
-        const float2 tot = row_parts<G>(
-            make_float2(m0, lanes_sum<L>(q.x + q.y)), s_part, flip, [&](float2 o) {
-                const float m = lanes_sum<W>(k * o.x) * p.inv_d, far = o.x - m;
-                return make_float2(m, lanes_sum<W>(fmaf(k * far, far, o.y)));
+        // m_0 of the first warp, the row's mean less that, the squares about the mean, the sum
+        const float4 tot = row_parts<G>(
+            make_float4(m0, rest, sq, total), s_part, flip, [&](float4 o, float4 w0) {
+                const float far = (o.x - w0.x) + o.y;
+                const float m = lanes_sum<W>(k * far) * p.inv_d, off = far - m;
+                const float about = fmaf(k * off, off, fmaf(-k * o.y, o.y, o.z));
+                return make_float4(w0.x, m, lanes_sum<W>(about), lanes_sum<W>(o.w));
             });
-        const float rstd = rsqrtf(fmaf(tot.y, p.inv_d, p.eps));
+        const float var = max_nan(tot.z, 0.0f) * p.inv_d, rstd = rsqrtf(var + p.eps);
+        const f32x2 off = both((m0 - tot.x) - tot.y);
         if (r < p.T) {
             RowRegs<TY> o;
 #pragma unroll
             for (int e = 0; e < E / 2; ++e)
-                o.put_two(e, fma2(mul2(add2(d[e], both(-tot.x)), both(rstd)), w[e], b[e]));
+                o.put_two(e, fma2(mul2(add2(d[e], off), both(rstd)), w[e], b[e]));
             store_row<TY, G, V>(y + r * p.ldy, t, D, o);
             if (t == 0) {
-                if (p.mean) p.mean[r] = tot.x - parts(c).x;
+                const float mean = tot.x + tot.y;
+                if (p.mean) p.mean[r] = mean * mean > 256.0f * var ? mean : tot.w * p.inv_d;
                 if (p.rstd) p.rstd[r] = rstd;
             }
         }
@@ -420,23 +426,25 @@ __global__ void __launch_bounds__(NL_THREADS) norm_long_kernel(const NormParams 
     for (int64_t r = blockIdx.x; r < p.T; r += gridDim.x) {
         const TX* x = static_cast<const TX*>(p.x) + r * p.ldx;
         TY* y = static_cast<TY*>(p.y) + r * p.ldy;
-        const float first = to_f32(x[0]);
         float s = 0.0f;
-        for (int64_t c = threadIdx.x; c < p.D; c += NL_THREADS) s += to_f32(x[c]) - first;
-        const float mean = block_sum(s, s_red) / (float)p.D;       // (less `first`; the syncs in
-        float sq = 0.0f;                                           // block_sum: y may be x)
+        for (int64_t c = threadIdx.x; c < p.D; c += NL_THREADS) s += to_f32(x[c]);
+        const float total = block_sum(s, s_red), m0 = total / (float)p.D;
+        float sq = 0.0f, rest = 0.0f;
         for (int64_t c = threadIdx.x; c < p.D; c += NL_THREADS) {
-            const float d = (to_f32(x[c]) - first) - mean;
+            const float d = to_f32(x[c]) - m0;
             sq = fmaf(d, d, sq);
+            rest += d;
         }
-        const float rstd = rsqrtf(fmaf(block_sum(sq, s_red), p.inv_d, p.eps));
+        rest = block_sum(rest, s_red) / (float)p.D;    // (the barriers in block_sum: y may be x)
+        const float var = max_nan(fmaf(block_sum(sq, s_red), p.inv_d, -rest * rest), 0.0f);
+        const float rstd = rsqrtf(var + p.eps), mean = m0 + rest;
         for (int64_t c = threadIdx.x; c < p.D; c += NL_THREADS) {
             const float w = p.w ? load_as(p.w, p.w_type, c) : 1.0f;
             const float b = p.b ? load_as(p.b, p.b_type, c) : 0.0f;
-            y[c] = from_f32<TY>(fmaf(((to_f32(x[c]) - first) - mean) * rstd, w, b));
+            y[c] = from_f32<TY>(fmaf(((to_f32(x[c]) - m0) - rest) * rstd, w, b));
         }
         if (threadIdx.x == 0) {
-            if (p.mean) p.mean[r] = first + mean;
+            if (p.mean) p.mean[r] = mean * mean > 256.0f * var ? mean : m0;
             if (p.rstd) p.rstd[r] = rstd;
         }
     }

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(NORM_BLOCK<G>, G <= 256 ? 2 : 1)
         const float2 a = parts(s1), b = parts(s2);
         copies_wait<S - 2>();                          // (the next row, before the barrier)
         const float2 tot = row_parts<G>(
-            make_float2(lanes_sum<L>(a.x + a.y), lanes_sum<L>(b.x + b.y)), s_part, flip, [](float2 o) {
+            make_float2(lanes_sum<L>(a.x + a.y), lanes_sum<L>(b.x + b.y)), s_part, flip, [](float2 o, float2) {
                 return make_float2(lanes_sum<W>(o.x), lanes_sum<W>(o.y));
             });
         const float g1 = tot.x * p.inv_d * rstd, g2 = tot.y * p.inv_d * rstd;
