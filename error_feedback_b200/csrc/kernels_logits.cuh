@@ -18,8 +18,8 @@
 //
 // A row is worked on by a team: a warp or four (rows of up to LG_SMALL and LG_MIDDLE lines, where
 // the chain of a row's steps counts: many at once), a block of eight, or a cluster of blocks
-// while there are few rows, each block an equal share of the row's 128-byte lines.  Rows start anywhere; whole
-// lines are read as 32 bytes a thread.
+// while there are few rows, each block an equal share of the row's 128-byte lines.  Rows start
+// anywhere; whole lines are read as 32 bytes a thread.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -70,15 +70,12 @@ struct Team {
             __syncthreads();
         }
     }
-    // Sums over the team; s: 33 words.
+    // Exclusive prefix over the team; s: 33 words.
     static __device__ __forceinline__ uint32_t excl_scan(uint32_t v, uint32_t* s, uint32_t* total) {
         if (W > 1) return block_excl_scan(v, s, total);
         const uint32_t incl = warp_incl_scan(v);
         *total = __shfl_sync(0xFFFFFFFFu, incl, 31);
         return incl - v;
-    }
-    static __device__ __forceinline__ float sum(float v, float* s) {
-        return W > 1 ? block_sum(v, s) : warp_sum(v);
     }
 };
 
@@ -270,12 +267,11 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
-// (BACK: the last batch first, which L2 still holds.)
 // f(FLIGHT chunks, the number of the first, those of the others THREADS apart, end) for the
 // chunks of lines [line0, line1); a chunk from `end` on holds nothing but -inf.  Every thread
-// of a warp makes the same calls.  Batches that lie in the
-// row as a whole are loaded without a check of each chunk, which would take as many
-// instructions as the sums (7.3 instead of 5.5 an element).
+// of a warp makes the same calls.  BACK: the last batch first, which L2 still holds.  Batches
+// that lie in the row as a whole are loaded without a check of each chunk (with it and the
+// check of the running maximum for each chunk: 7.3 instructions an element, without 5.7).
 template <int W, int FLIGHT, bool BACK = false, typename T, typename F>
 __device__ __forceinline__ void for_chunks(const LineRow<T>& row, int32_t line0, int32_t line1, F f) {
     constexpr int N = Team<W>::THREADS;
@@ -962,7 +958,7 @@ __device__ __forceinline__ float2 join_powers(float2 a, float2 b, float c) {
 // Bound by the bytes of z and dz, and for short rows by the chain of a row's steps: so
 // thread k keeps the teacher's k-th entry in registers, its softmax and the loss ride on the
 // barriers that the row's sums and the gradient need anyway (a barrier for each step: 70 us
-// instead of NN for 4,096 rows of 8,192 bf16).  For the gradient the row is read again, out of
+// instead of 65 for 4,096 rows of 8,192 bf16 by eight warps each; 43 by four).  For the gradient the row is read again, out of
 // L2.  (Kept in shared memory instead, with the next row copied behind it, by blocks of 8, 16
 // or 32 warps: 255 to 290 us for 2,048 x 131,072 bf16, 148 for 4,096 x 32,768; read again: 240
 // and 122.  Fewer blocks fit, and they all read or all write at the same time.)

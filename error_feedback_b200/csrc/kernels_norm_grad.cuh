@@ -2,10 +2,13 @@
 //
 //   dx = rstd (g - 1/D sum g - xh 1/D sum (g xh)),  dw = sum_t dy xh,  db = sum_t dy
 //
-// A row is held in registers by 8 to 1,024 threads, 16 elements each (8 of fp32), which keep to
-// their columns over all of a block's rows, so w and the column sums stay in registers.
-// Column sums leave one fp32 row per block, added in a fixed order by a second kernel: no
-// floating-point atomics.  Rows past norm_max_grad_d() columns are read again instead.
+// A row is held in registers by 8 to 1,024 threads, 16 elements each, which keep to their columns
+// over all of a block's rows, so w and the column sums stay in registers, with the rows that
+// follow on their way into a ring of shared memory (kernels_norm.cuh).  Column sums leave one
+// fp32 row per block, added in a fixed order by a second kernel: no floating-point atomics.
+// 1,024 threads (rows past NG_COLS_D) have no registers for the sums: a kernel of its own reads x
+// and dy for them first (2,048 x 16,384 bf16: 125 us with the sums in the same kernel, 80 so).  Rows past
+// NM_MAX_D columns are read again instead of held.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -17,12 +20,11 @@
 
 namespace tke {
 
-// Longest rows that the ring holds, by the bytes of an element of x and one of dy.
-constexpr int norm_max_grad_d(size_t bytes) { return bytes < 8 ? 16384 : 8192; }
+constexpr int NG_COLS_D = 8192;
 
-// Rows of the rings of x and dy.
+// Rows of the rings of x and dy: what 227 KB hold.
 template <typename TX, typename TD, int G>
-constexpr int NG_SLOTS = G >= 1024 ? (sizeof(TX) + sizeof(TD) == 4 ? 3 : 2) : 3;
+constexpr int NG_SLOTS = G < 1024 || sizeof(TX) + sizeof(TD) == 4 ? 3 : sizeof(TX) + sizeof(TD) == 6 ? 2 : 1;
 
 struct NormGradParams {
     const void* dy;
@@ -44,8 +46,9 @@ __global__ void __launch_bounds__(NORM_BLOCK<G>, G <= 256 ? 2 : 1)
     constexpr int E = NR_ELEMS, ROWS = NORM_BLOCK<G> / G, L = G < 32 ? G : 32, W = G < 64 ? 1 : G / 32;
     constexpr int S = NG_SLOTS<TX, TD, G>, BX = NR_BYTES<TX, G, V>, BD = NR_BYTES<TD, G, V>;
     constexpr int BYTES = BX + BD;
-    // (1,024 threads have 64 registers each: w from memory)
-    constexpr bool HOLD = G < 1024;
+    // (1,024 threads have 64 registers each: no column sums, and w from memory beside fp32 rows)
+    constexpr bool HOLD = G < 1024, HOLD_W = HOLD || sizeof(TX) + sizeof(TD) == 4;
+    constexpr int LEFT = S > 1 ? S - 2 : 0;            // groups of copies that need not have landed
     extern __shared__ __align__(16) char s_ring[];     // [row of the block][S][x, dy]
     __shared__ float2 s_part[2][NORM_BLOCK<G> / 32];
     pdl_launch();
@@ -84,15 +87,19 @@ __global__ void __launch_bounds__(NORM_BLOCK<G>, G <= 256 ? 2 : 1)
     };
     fetch(r);
     const uint32_t mask = elems_mask<G, V>(t, D);
-    f32x2 w[E / 2], dw[E / 2], db[E / 2];
-    if (HOLD) row_weights<G, V>(p.w, p.w_type, t, D, 1.0f, w);
+    f32x2 w[E / 2], dw[HOLD ? E / 2 : 1], db[HOLD ? E / 2 : 1];
+    if (HOLD_W) row_weights<G, V>(p.w, p.w_type, t, D, 1.0f, w);
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) dw[i] = db[i] = 0;
-    copies_wait<S - 2>();
+    for (int i = 0; HOLD && i < E / 2; ++i) dw[i] = db[i] = 0;
+    copies_wait<LEFT>();
     row_sync<G>();
-    int flip = 0, slot = 0, free_slot = S - 1;
+    int flip = 0, slot = 0, free_slot = S > 1 ? S - 1 : 0;
     for (int64_t i = 0; i < rounds; ++i, r += step) {
         copy(free_slot, r + (S - 1) * step);
+        if (S == 1) {
+            copies_wait<0>();
+            row_sync<G>();
+        }
         RowRegs<TX> vx;
         RowRegs<TD> vd;
         read_row<TX, G, V>(ring + slot * BYTES, x + r * p.ldx, t, mask, next_x, vx);
@@ -108,25 +115,27 @@ __global__ void __launch_bounds__(NORM_BLOCK<G>, G <= 256 ? 2 : 1)
         slot = slot + 1 == S ? 0 : slot + 1;
         // (dy is 0 past the end, so nothing there counts)
         f32x2 s1 = 0, s2 = 0;
-        if (!HOLD) row_weights<G, V>(p.w, p.w_type, t, D, 1.0f, w);
+        if (!HOLD_W) row_weights<G, V>(p.w, p.w_type, t, D, 1.0f, w);
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) {
             const f32x2 d = vd.two(e), xh = mul2(add2(vx.two(e), both(-mean)), both(rstd));
             const f32x2 g = mul2(d, w[e]);
             s1 = add2(s1, g);
             s2 = fma2(g, xh, s2);
-            dw[e] = fma2(d, xh, dw[e]);
-            db[e] = add2(db[e], d);
+            if constexpr (HOLD) {
+                dw[e] = fma2(d, xh, dw[e]);
+                db[e] = add2(db[e], d);
+            }
         }
         const float2 a = parts(s1), b = parts(s2);
-        copies_wait<S - 2>();                          // (the next row, before the barrier)
+        copies_wait<LEFT>();                          // (the next row, before the barrier)
         const float2 tot = row_parts<G>(
             make_float2(lanes_sum<L>(a.x + a.y), lanes_sum<L>(b.x + b.y)), s_part, flip, [](float2 o, float2) {
                 return make_float2(lanes_sum<W>(o.x), lanes_sum<W>(o.y));
             });
         const float g1 = tot.x * p.inv_d * rstd, g2 = tot.y * p.inv_d * rstd;
         if (r < p.T) {
-            if (!HOLD) row_weights<G, V>(p.w, p.w_type, t, D, 1.0f, w);
+            if (!HOLD_W) row_weights<G, V>(p.w, p.w_type, t, D, 1.0f, w);
             RowRegs<TX> o;
 #pragma unroll
             for (int e = 0; e < E / 2; ++e) {
@@ -137,38 +146,40 @@ __global__ void __launch_bounds__(NORM_BLOCK<G>, G <= 256 ? 2 : 1)
             store_row<TX, G, V>(dx + r * p.lddx, t, D, o);
         }
     }
-    if (!p.part) return;
-    float* s_col = reinterpret_cast<float*>(s_ring);   // (all copies have landed and been read)
-    float* part = p.part + (int64_t)blockIdx.x * 2 * p.D;
-    const int mine = (int)threadIdx.x / G;
+    if constexpr (HOLD) {
+        if (!p.part) return;
+        float* s_col = reinterpret_cast<float*>(s_ring);   // (all copies have landed and been read)
+        float* part = p.part + (int64_t)blockIdx.x * 2 * p.D;
+        const int mine = (int)threadIdx.x / G;
 #pragma unroll
-    for (int k = 0; k < 2; ++k, part += p.D) {
-        f32x2* v = k ? db : dw;
-        // the block's rows, in order
-        for (int i = ROWS - 1; i > 0; --i) {
-            __syncthreads();
-            if (mine == i) {
+        for (int k = 0; k < 2; ++k, part += p.D) {
+            f32x2* v = k ? db : dw;
+            // the block's rows, in order
+            for (int i = ROWS - 1; i > 0; --i) {
+                __syncthreads();
+                if (mine == i) {
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) {
+                        const float2 f = parts(v[e]);
+                        s_col[2 * e * G + t] = f.x;
+                        s_col[(2 * e + 1) * G + t] = f.y;
+                    }
+                }
+                __syncthreads();
+                if (mine == i - 1) {
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e)
+                        v[e] = add2(v[e], pair(s_col[2 * e * G + t], s_col[(2 * e + 1) * G + t]));
+                }
+            }
+            if (mine == 0) {
 #pragma unroll
                 for (int e = 0; e < E / 2; ++e) {
                     const float2 f = parts(v[e]);
-                    s_col[2 * e * G + t] = f.x;
-                    s_col[(2 * e + 1) * G + t] = f.y;
+                    const int c0 = norm_col<G, V>(t, 2 * e), c1 = norm_col<G, V>(t, 2 * e + 1);
+                    if (c0 < D) part[c0] = f.x;
+                    if (c1 < D) part[c1] = f.y;
                 }
-            }
-            __syncthreads();
-            if (mine == i - 1) {
-#pragma unroll
-                for (int e = 0; e < E / 2; ++e)
-                    v[e] = add2(v[e], pair(s_col[2 * e * G + t], s_col[(2 * e + 1) * G + t]));
-            }
-        }
-        if (mine == 0) {
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) {
-                const float2 f = parts(v[e]);
-                const int c0 = norm_col<G, V>(t, 2 * e), c1 = norm_col<G, V>(t, 2 * e + 1);
-                if (c0 < D) part[c0] = f.x;
-                if (c1 < D) part[c1] = f.y;
             }
         }
     }
@@ -201,26 +212,58 @@ __global__ void __launch_bounds__(NL_THREADS) norm_grad_long_kernel(const NormGr
     }
 }
 
-// ... and their column sums, 32 rows of blocks by NL_COLS columns.
-constexpr int NL_COLS = 256, NL_PARTS = 32;
+// The column sums alone: a thread takes V columns, blocks in y take every NL_PARTS-th row, four
+// of them on their way at once.
+constexpr int NL_COLS = 128, NL_PARTS = 64, NL_AHEAD = 4;
 
-template <typename TX, typename TD>
+template <typename TX, typename TD, int V>
 __global__ void __launch_bounds__(NL_COLS) norm_cols_kernel(const NormGradParams p) {
     pdl_launch();
     pdl_wait();
-    const int64_t c = (int64_t)blockIdx.x * NL_COLS + threadIdx.x;
+    const int64_t c = ((int64_t)blockIdx.x * NL_COLS + threadIdx.x) * V;
     if (c >= p.D) return;
     const TX* x = static_cast<const TX*>(p.x) + c;
     const TD* dy = static_cast<const TD*>(p.dy) + c;
-    float dw = 0.0f, db = 0.0f;
-    for (int64_t r = blockIdx.y; r < p.T; r += gridDim.y) {
-        const float d = to_f32(dy[r * p.ldy]);
-        dw = fmaf(d, (to_f32(x[r * p.ldx]) - p.mean[r]) * p.rstd[r], dw);
-        db += d;
+    float dw[V] = {}, db[V] = {};
+    for (int64_t r0 = blockIdx.y; r0 < p.T; r0 += (int64_t)NL_AHEAD * gridDim.y) {
+        TX vx[NL_AHEAD][V];
+        TD vd[NL_AHEAD][V];
+        float mean[NL_AHEAD], rstd[NL_AHEAD];
+#pragma unroll
+        for (int i = 0; i < NL_AHEAD; ++i) {
+            const int64_t r = r0 + (int64_t)i * gridDim.y;
+            if (r >= p.T) continue;
+            mean[i] = p.mean[r];
+            rstd[i] = p.rstd[r];
+            if constexpr (V > 1) {
+#pragma unroll
+                for (int k = 0; k < V * (int)sizeof(TX) / 8; ++k)
+                    reinterpret_cast<uint2*>(vx[i])[k] = reinterpret_cast<const uint2*>(x + r * p.ldx)[k];
+#pragma unroll
+                for (int k = 0; k < V * (int)sizeof(TD) / 8; ++k)
+                    reinterpret_cast<uint2*>(vd[i])[k] = reinterpret_cast<const uint2*>(dy + r * p.ldy)[k];
+            } else {
+                vx[i][0] = x[r * p.ldx];
+                vd[i][0] = dy[r * p.ldy];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NL_AHEAD; ++i) {
+            if (r0 + (int64_t)i * gridDim.y >= p.T) continue;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const float d = to_f32(vd[i][k]);
+                dw[k] = fmaf(d, (to_f32(vx[i][k]) - mean[i]) * rstd[i], dw[k]);
+                db[k] += d;
+            }
+        }
     }
-    float* part = p.part + (int64_t)blockIdx.y * 2 * p.D;
-    part[c] = dw;
-    part[p.D + c] = db;
+    float* part = p.part + (int64_t)blockIdx.y * 2 * p.D + c;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        part[k] = dw[k];
+        part[p.D + k] = db[k];
+    }
 }
 
 // ------------------------------------------------- the blocks' column sums

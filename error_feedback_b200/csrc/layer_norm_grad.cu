@@ -1,6 +1,6 @@
 // Host side of layer_norm_grad (include/topk_ef.h): argument checks, workspace layout,
-// choice of kernel by row length: norm_grad_kernel -> norm_sum_kernel, for rows past
-// norm_max_grad_d() norm_cols_kernel -> norm_grad_long_kernel -> norm_sum_kernel.
+// choice of kernel by row length: norm_grad_kernel -> norm_sum_kernel, for rows past NG_COLS_D
+// norm_cols_kernel -> norm_grad_kernel or norm_grad_long_kernel -> norm_sum_kernel.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -39,6 +39,18 @@ cudaError_t launch_grad(const NormGradParams& p, int32_t& parts, cudaStream_t st
     return e;
 }
 
+// The column sums by themselves.
+template <typename TX, typename TD, int V>
+cudaError_t launch_cols(const NormGradParams& p, int32_t& parts, cudaStream_t st) {
+    parts = (int32_t)std::min<int64_t>(grad_parts(p.T), NL_PARTS);
+    trace_before(st, "norm_cols_kernel");
+    const cudaError_t e =
+        launch_pdl(norm_cols_kernel<TX, TD, V>,
+                   dim3((unsigned)ceil_div64(p.D, NL_COLS * V), (unsigned)parts), NL_COLS, st, p);
+    trace_after(st);
+    return e;
+}
+
 template <typename TX, typename TD, int V>
 cudaError_t grad_by_length(const NormGradParams& p, int32_t& parts, cudaStream_t st) {
     if (p.D <= 128) return launch_grad<TX, TD, 8, V>(p, parts, st);
@@ -48,9 +60,8 @@ cudaError_t grad_by_length(const NormGradParams& p, int32_t& parts, cudaStream_t
     if (p.D <= 2048) return launch_grad<TX, TD, 128, V>(p, parts, st);
     if (p.D <= 4096) return launch_grad<TX, TD, 256, V>(p, parts, st);
     if (p.D <= 8192) return launch_grad<TX, TD, 512, V>(p, parts, st);
-    if constexpr (norm_max_grad_d(sizeof(TX) + sizeof(TD)) > 8192)
-        return launch_grad<TX, TD, 1024, V>(p, parts, st);
-    return cudaErrorInvalidValue;
+    int32_t none = 0;
+    return launch_grad<TX, TD, 1024, V>(p, none, st);
 }
 
 }  // namespace
@@ -114,19 +125,14 @@ int layer_norm_grad(const void* grad_out, int32_t grad_out_type, int64_t ld_grad
             return with_type(grad_out_type, [&](auto td) {
                 using TX = decltype(tx);
                 using TD = decltype(td);
-                if (D <= norm_max_grad_d(sx + sd))
+                // (the sums first: grad_x may be x or grad_out)
+                cudaError_t r = cols && D > NG_COLS_D
+                                    ? vec ? launch_cols<TX, TD, 4>(p, parts, st) : launch_cols<TX, TD, 1>(p, parts, st)
+                                    : cudaSuccess;
+                if (r != cudaSuccess) return r;
+                if (D <= NM_MAX_D)
                     return vec ? grad_by_length<TX, TD, NORM_GROUP<TX, TD>>(p, parts, st)
                                : grad_by_length<TX, TD, 1>(p, parts, st);
-                cudaError_t r = cudaSuccess;
-                if (cols) {      // first: grad_x may be x or grad_out
-                    parts = (int32_t)std::min<int64_t>(grad_parts(T), NL_PARTS);
-                    trace_before(st, "norm_cols_kernel");
-                    r = launch_pdl(norm_cols_kernel<TX, TD>,
-                                   dim3((unsigned)ceil_div64(D, NL_COLS), (unsigned)parts), NL_COLS,
-                                   st, p);
-                    trace_after(st);
-                    if (r != cudaSuccess) return r;
-                }
                 trace_before(st, "norm_grad_long_kernel");
                 r = launch_pdl(norm_grad_long_kernel<TX, TD>, (unsigned)std::min<int64_t>(T, SMS * 4),
                                NL_THREADS, st, p);

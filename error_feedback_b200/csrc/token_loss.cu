@@ -43,7 +43,7 @@ int64_t most_lines(const void* z, int64_t ld, int64_t V, size_t size) {
 }
 
 // Blocks of a row's cluster: as many as run at once with `most` of the call's (a second round
-// of blocks would take as long as the first: 64 x 32,768 bf16 11.8 us with eight, NN with four).
+// of blocks would take as long as the first: 64 x 32,768 bf16 11.8 us with eight, 6.7 with four).
 int row_blocks(int64_t T, int64_t lines, int64_t most) {
     int c = 1;
     while (c < 16 && T * 2 * c <= most && lines / (2 * c) >= LEAST_LINES) c *= 2;
