@@ -348,3 +348,68 @@ def test_binding_refuses():
         ef.layer_norm_grad(x, x, None, rstd)
     with pytest.raises(ef.TopkEfError):
         ef.layer_norm_grad(x, x, mean, rstd, ws=torch.empty(8, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("D", [100, 128, 129, 200, 500, 512, 513, 1000, 1500, 2048, 3001, 4096, 6000, 8191, 8200, 12000, 16383])
+@pytest.mark.parametrize("xt,dt", [("bf16", "bf16"), ("f32", "f32"), ("f16", "f32"), ("f32", "bf16")])
+def test_more_rows_than_run_at_once(D, xt, dt):
+    """Every length class with blocks that walk over several rows, to the last row alone."""
+    T = 148 * 3 * max(1, 4096 // D) + 321 if D < 8192 else 500
+    x = _strided(T, D, TYPES[xt], D, 0, D, 2.0, 0.5)
+    dy = _strided(T, D, TYPES[dt], D, 0, D + 1, 1e-2)
+    w = _strided(1, D, torch.float32, D, 0, 1, 0.3, 1.0)[0].contiguous()
+    b = _strided(1, D, torch.float32, D, 0, 2)[0].contiguous()
+    out, mean, rstd = ef.layer_norm(x, w, b)
+    _check_forward(out, mean, rstd, x, w, b, 1e-5)
+    _check_gradient(dy, x, mean, rstd, w, ef.layer_norm_grad(dy, x, mean, rstd, w))
+    y = x.clone()
+    ef.layer_norm(y, w, b, out=y)
+    assert torch.equal(y, out)
+
+
+@pytest.mark.parametrize("off", [1, 2, 4])
+@pytest.mark.parametrize("wt", ["f32", "bf16"])
+def test_weights_that_start_anywhere(off, wt):
+    x = _strided(9, 1024, torch.bfloat16, 1024, 0, 1)
+    buf = torch.randn(1024 + 8, device="cuda").to(TYPES[wt])
+    w = buf[off:off + 1024]
+    out, mean, rstd = ef.layer_norm(x, w, w)
+    _check_forward(out, mean, rstd, x, w, w, 1e-5)
+    dy = _strided(9, 1024, torch.bfloat16, 1024, 0, 2)
+    gw = torch.full((1024 + 8,), 3.0, device="cuda")
+    got = ef.layer_norm_grad(dy, x, mean, rstd, w, grad_weight=gw[off:off + 1024])
+    _check_gradient(dy, x, mean, rstd, w, got)
+    assert (gw[:off] == 3.0).all() and (gw[off + 1024:] == 3.0).all()
+
+
+def test_one_weight_gradient_alone():
+    """The C call writes either sum without the other."""
+    x, dy = torch.randn(50, 64, device="cuda"), torch.randn(50, 64, device="cuda")
+    _, mean, rstd = ef.layer_norm(x)
+    gx, gw, gb = ef.layer_norm_grad(dy, x, mean, rstd)
+    ws = torch.empty(ef.layer_norm_grad_workspace_bytes(50, 64), dtype=torch.uint8, device="cuda")
+    to, one = torch.empty_like(gx), torch.empty_like(gw)
+    st = torch.cuda.current_stream().cuda_stream
+    for which, want in ((0, gw), (1, gb)):
+        ptrs = [one.data_ptr() if k == which else None for k in range(2)]
+        rc = ef.lib().layer_norm_grad(dy.data_ptr(), 0, 64, x.data_ptr(), 0, 64, mean.data_ptr(), rstd.data_ptr(), None, 0,
+                                      50, 64, to.data_ptr(), 64, ptrs[0], 0, ptrs[1], 0, 0, ws.data_ptr(), ws.numel(), st)
+        assert rc == 0 and torch.equal(one, want) and torch.equal(to, gx)
+
+
+def test_two_calls_at_once():
+    xs = [torch.randn(3000, 1024, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    dys = [torch.randn(3000, 1024, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    want = []
+    for x, dy in zip(xs, dys):
+        y = ef.layer_norm(x)
+        want.append((*y, *ef.layer_norm_grad(dy, x, y[1], y[2])))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for s, x, dy in zip(streams, xs, dys):
+            y = ef.layer_norm(x, stream=s)
+            got.append((*y, *ef.layer_norm_grad(dy, x, y[1], y[2], stream=s)))
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for g, v in zip(got, want) for p, q in zip(g, v))

@@ -274,6 +274,8 @@ def _check_gradient(z, ids, scale, g, h, out=None, out_dtype=None, padding_idx=-
     # p: t is rounded once and its product with log2 e (a constant off by u) twice
     rel = EX2 + 6 * U * (tc.abs() + x.clamp(min=-1e30).abs() * 0 + 1)
     err = scale * (p * size * (rel + 6 * U) + 4 * U * (G.abs()[:, None] * hot))
+    # (p below 2^-126 is 0)
+    err = err + scale * size * 2.0**-126
     want[skip] = 0.0
     err[skip] = 0.0
     assert got.shape == z.shape
@@ -414,6 +416,8 @@ def _check_distill(z, ids, tl, weight, scale, grad=True, out=None, out_dtype=Non
     f = (w * scale)[:, None]
     want = f * (e.p - qv)
     err = f.abs() * (e.p * (e.e_s[:, None] + EX2 + U * (2 * e.round + 8)) + eqv + 4 * U * (e.p + qv))
+    # (2^t below 2^-126 is 0, s at least 1/2: p may lose 2^-125, times f)
+    err = err + f.abs() * 2.0**-125
     want[none] = 0.0
     err[none] = 0.0
     assert (dz[none] == 0).all()
@@ -607,3 +611,74 @@ def test_binding_refuses():
         ef.distill_loss(z, torch.zeros(4, 257, dtype=torch.int32, device="cuda"), torch.zeros(4, 257, device="cuda"))
     with pytest.raises(ef.TopkEfError):
         ef.distill_loss(z, i2, t, scale=-2.0)
+
+
+@pytest.mark.parametrize("V", [1, 33, 500, 2000, 4097, 8192, 16385, 40001])
+@pytest.mark.parametrize("zt", ["f32", "bf16"])
+def test_more_rows_than_run_at_once(V, zt):
+    """Rows of one warp, four and eight."""
+    T = 501
+    z = _logits(T, V, TYPES[zt])
+    z[3] = -INF
+    z[5] = -1e9
+    z[7, ::2] = -INF
+    ids = _ids(T, V)
+    ids[11] = -1
+    _check_forward(z, ids, 1.0, 17)
+    _check_gradient(z, ids, 1.0, torch.randn(T, device="cuda"), torch.randn(T, device="cuda"))
+    tids, tl = _teacher(T, V, 9, distinct=9 <= V)
+    w = torch.rand(T, device="cuda")
+    w[::5] = 0
+    keep = [r for r in range(T) if r not in (3, 7)]       # (a teacher's token at -inf: loss +inf)
+    zk = z[keep].contiguous()
+    tk = [t[keep].contiguous() for t in (tids, tl, w)]
+    _check_distill(zk, *tk[:2], tk[2], 0.7)
+    _check_distill(zk, *tk[:2], None, 0.7, grad=False)
+
+
+@pytest.mark.parametrize("V,zt,top", [(2**19 - 64, "f32", 128), (2**20 - 64, "bf16", 100), (700_001, "f32", 0),
+                                      (3_000_000, "bf16", 0)])
+def test_long_rows(V, zt, top):
+    z = _logits(2, V, TYPES[zt])
+    _check_forward(z, _ids(2, V), 1.0, top)
+    _check_gradient(z, _ids(2, V), 1.0, torch.randn(2, device="cuda"), torch.randn(2, device="cuda"))
+    tids, tl = _teacher(2, V, 20)
+    _check_distill(z, tids, tl, None, 1.0)
+
+
+def test_all_entries_the_same_token():
+    z = _logits(6, 900, torch.float32)
+    ids = torch.full((6, 256), 417, dtype=torch.int64, device="cuda")
+    _check_distill(z, ids, torch.randn(6, 256, device="cuda"), None, 1.0)
+
+
+@pytest.mark.parametrize("scale", [1e-3, 1e-6, 50.0, 1e4])
+@pytest.mark.parametrize("zt", ["f32", "bf16", "f16"])
+def test_scales(scale, zt):
+    """Near uniform and near one-hot rows, forbidden tokens among them."""
+    z = _logits(5, 2100, TYPES[zt], peak=False)
+    z[:, ::7] = -INF
+    scale = float(torch.tensor(scale, dtype=torch.float32))
+    _check_forward(z, _ids(5, 2100), scale, 10)
+    tids, tl = _teacher(5, 2100, 8)
+    tids = tids // 7 * 7 + 1
+    _check_distill(z, tids, tl * 0.1, None, scale)
+
+
+def test_two_calls_at_once():
+    zs = [_logits(700, 9000, torch.bfloat16, seed=s) for s in (1, 2)]
+    ids = [_ids(700, 9000, s) for s in (1, 2)]
+    teach = [_teacher(700, 9000, 16, s) for s in (1, 2)]
+
+    def run(i, s):
+        a = ef.token_logprobs(zs[i], ids[i], top=9, stream=s)
+        b = ef.token_logprobs_grad(zs[i], ids[i], a[2], grad_logprob=a[0], entropy=a[1], grad_entropy=a[1], stream=s)
+        return [*a, b, *ef.distill_loss(zs[i], *teach[i], grad=True, stream=s)]
+
+    want = [run(i, None) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [run(i, s) for i, s in enumerate(streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for g, v in zip(got, want) for p, q in zip(g, v))
