@@ -723,39 +723,75 @@ def muon_update(grad, momentum=None, mu=0.95, nesterov=True, coefficients=MUON_C
 
 # ---------------------------------------------------------------- layer norm
 
-def _rows(t, name: str, D=None, device=None):
-    """_matrix of [..., D] rows: (2-d view, type code, row stride)."""
-    if isinstance(t, torch.Tensor) and t.dim() != 2 and t.dim() > 0:
+# (The checks of these calls ask a tensor for as little as they can: a short call is bound by
+# what the host does, 9 us of which the GPU works 3.)
+
+def _rows(t, name: str, D=None, index=None):
+    """(2-d view, type code, row stride, device index, rows, columns) of [..., D]
+    rows on a CUDA device (`index`, if given) whose elements are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        if t.dim() == 0:
+            raise ValueError(f"{name} must have a dimension")
         n = t.shape[-1]
         t = t.view(-1, n) if t.numel() else t.new_empty((t.shape[:-1].numel(), n))
-    code, ld = _matrix(t, name, device)
-    if D is not None and t.shape[1] != D:
+    at, code = t.get_device(), _TYPE.get(t.dtype)
+    if at < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if code is None:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16")
+    if index is not None and at != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows <= 1:
+        ld = cols
+    elif ld < cols:
+        raise ValueError(f"the rows of {name} overlap")
+    if D is not None and cols != D:
         raise ValueError(f"{name} must have rows of {D}")
-    return t, code, ld
+    return t, code, ld, at, rows, cols
 
 
-def _vector(t, name: str, n: int, device, dtype=None):
+def _vector(t, name: str, n: int, index: int):
     """Address and type code of a contiguous [n] tensor on the device; (None, 0)
     for None."""
     if t is None:
         return None, 0
-    if isinstance(t, torch.Tensor) and t.get_device() == device.index and t.numel() == n \
+    if isinstance(t, torch.Tensor) and t.get_device() == index and t.numel() == n \
             and t.is_contiguous():
         code = _TYPE.get(t.dtype)
-        if code is not None and (dtype is None or t.dtype is dtype):
-            return t.data_ptr(), code
-        raise ValueError(f"{name} must be {dtype or 'float32, bfloat16 or float16'}")
-    raise ValueError(f"{name} must be a contiguous tensor of {n} on {device}")
+        if code is None:
+            raise ValueError(f"{name} must be float32, bfloat16 or float16")
+        return t.data_ptr(), code
+    raise ValueError(f"{name} must be a contiguous tensor of {n} on cuda:{index}")
 
 
-def _f32(t, name: str, n: int, device, index: int):
+def _f32(t, name: str, n: int, index: int):
     """Address of a contiguous float32 [n] tensor on the device; None for None."""
     if t is None:
         return None
     if isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.get_device() == index \
             and t.numel() == n and t.is_contiguous():
         return t.data_ptr()
-    raise ValueError(f"{name} must be a contiguous float32 tensor of {n} on {device}")
+    raise ValueError(f"{name} must be a contiguous float32 tensor of {n} on cuda:{index}")
+
+
+def _workspace_on(ws, index: int):
+    if ws is not None and ws.get_device() != index:
+        raise ValueError(f"ws is on {ws.device}, not on cuda:{index}")
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+
+
+def _at(index: int, stream, call):
+    """_on of a device's index."""
+    if stream is None and index == torch._C._cuda_getDevice():
+        return call(torch._C._cuda_getCurrentRawStream(index))
+    return _on(torch.device("cuda", index), stream, call)
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=None, mean=None, rstd=None,
@@ -767,29 +803,27 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=None, me
     rstd), mean and rstd float32 [rows] for layer_norm_grad (None with
     stats=False and none given).  Autograd records nothing: the gradient is
     layer_norm_grad's."""
-    x2, xt, ldx = _rows(x, "x")
-    dev = x.device
-    T, D = x2.shape
-    wp, wt = _vector(weight, "weight", D, dev)
-    bp, bt = _vector(bias, "bias", D, dev)
-    mp = _f32(mean, "mean", T, dev, dev.index)
-    rp = _f32(rstd, "rstd", T, dev, dev.index)
+    x2, xt, ldx, at, T, D = _rows(x, "x")
+    wp, wt = _vector(weight, "weight", D, at)
+    bp, bt = _vector(bias, "bias", D, at)
+    mp = _f32(mean, "mean", T, at)
+    rp = _f32(rstd, "rstd", T, at)
 
     def call(st):
         o, m, r, ma, ra = out, mean, rstd, mp, rp
         if o is None:
-            o = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=dev)
+            o = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
         elif out_dtype is not None and o.dtype != out_dtype:
             raise ValueError("out and out_dtype differ")
-        o2, ot, ldo = _rows(o, "out", D, dev)
-        if o2.shape[0] != T:
+        o2, ot, ldo, _, rows, _ = _rows(o, "out", D, at)
+        if rows != T:
             raise ValueError(f"out must hold [{T}, {D}] elements")
         if stats:
             if m is None:
-                m = torch.empty(T, dtype=torch.float32, device=dev)
+                m = torch.empty(T, dtype=torch.float32, device=x.device)
                 ma = m.data_ptr()
             if r is None:
-                r = torch.empty(T, dtype=torch.float32, device=dev)
+                r = torch.empty(T, dtype=torch.float32, device=x.device)
                 ra = r.data_ptr()
         rc = (_lib or lib()).layer_norm(x2.data_ptr(), xt, ldx, wp, wt, bp, bt, T, D, eps,
                                         o2.data_ptr(), ot, ldo, ma, ra, st)
@@ -797,7 +831,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=None, me
             _check(rc, "layer_norm")
         return o, m, r
 
-    return _on(dev, stream, call)
+    return _at(at, stream, call)
 
 
 def layer_norm_grad_workspace_bytes(T: int, D: int) -> int:
@@ -812,42 +846,40 @@ def layer_norm_grad(grad_out, x, mean, rstd, weight=None, affine=True, accumulat
     itself; grad_weight, grad_bias: [D] (out_dtype, default float32, the type
     that topk_ef_compress reads), added to what they hold with accumulate; both
     None with affine=False."""
-    x2, xt, ldx = _rows(x, "x")
-    dev = x.device
-    T, D = x2.shape
-    g2, gt, ldg = _rows(grad_out, "grad_out", D, dev)
-    if g2.shape[0] != T:
+    x2, xt, ldx, at, T, D = _rows(x, "x")
+    g2, gt, ldg, _, rows, _ = _rows(grad_out, "grad_out", D, at)
+    if rows != T:
         raise ValueError("grad_out must have x's rows")
-    wp, wt = _vector(weight, "weight", D, dev)
+    wp, wt = _vector(weight, "weight", D, at)
     if mean is None or rstd is None:
         raise ValueError("mean and rstd are needed")
-    mp = _f32(mean, "mean", T, dev, dev.index)
-    rp = _f32(rstd, "rstd", T, dev, dev.index)
+    mp = _f32(mean, "mean", T, at)
+    rp = _f32(rstd, "rstd", T, at)
     if affine and accumulate and (grad_weight is None or grad_bias is None):
         raise ValueError("accumulate needs grad_weight and grad_bias")
-    _on_device(ws, dev)
+    _workspace_on(ws, at)
 
     def call(st):
         gx, gw, gb = grad_x, grad_weight, grad_bias
         if gx is None:
-            gx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        gx2, gxt, ldgx = _rows(gx, "grad_x", D, dev)
-        if gx2.shape[0] != T or gxt != xt:
+            gx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        gx2, gxt, ldgx, _, rows, _ = _rows(gx, "grad_x", D, at)
+        if rows != T or gxt != xt:
             raise ValueError("grad_x must have x's rows and type")
         w = ws
         if affine:
             if gw is None:
-                gw = torch.empty(D, dtype=out_dtype or torch.float32, device=dev)
+                gw = torch.empty(D, dtype=out_dtype or torch.float32, device=x.device)
             if gb is None:
-                gb = torch.empty(D, dtype=out_dtype or torch.float32, device=dev)
+                gb = torch.empty(D, dtype=out_dtype or torch.float32, device=x.device)
             if w is None:
-                w = _own_workspace(layer_norm_grad_workspace_bytes(T, D), dev,
+                w = _own_workspace(layer_norm_grad_workspace_bytes(T, D), x.device,
                                    "layer_norm_grad_workspace_bytes")
         elif gw is not None or gb is not None:
             raise ValueError("affine=False has no grad_weight and grad_bias")
-        gwp, gwt = _vector(gw, "grad_weight", D, dev)
-        gbp, gbt = _vector(gb, "grad_bias", D, dev)
-        rc = lib().layer_norm_grad(g2.data_ptr(), gt, ldg, x2.data_ptr(), xt, ldx, mp, rp, wp, wt,
+        gwp, gwt = _vector(gw, "grad_weight", D, at)
+        gbp, gbt = _vector(gb, "grad_bias", D, at)
+        rc = (_lib or lib()).layer_norm_grad(g2.data_ptr(), gt, ldg, x2.data_ptr(), xt, ldx, mp, rp, wp, wt,
                                    T, D, gx2.data_ptr(), ldgx, gwp, gwt, gbp, gbt,
                                    1 if accumulate else 0, None if w is None else w.data_ptr(),
                                    0 if w is None else w.nbytes, st)
@@ -855,7 +887,7 @@ def layer_norm_grad(grad_out, x, mean, rstd, weight=None, affine=True, accumulat
             _check(rc, "layer_norm_grad")
         return gx, gw, gb
 
-    return _on(dev, stream, call)
+    return _at(at, stream, call)
 
 
 # ------------------------------------------------- losses over a vocabulary
@@ -867,20 +899,23 @@ def token_logprobs_workspace_bytes() -> int:
     return int(lib().token_logprobs_workspace_bytes())
 
 
-def _ids_of(ids, T, device):
-    """Address and size of the T ids of a call, or (None, 8)."""
-    if ids is None:
-        return None, 8
-    idb, n = _token_ids(ids, device)
-    if n != T:
-        raise ValueError("ids must hold one id for each row")
-    return ids.data_ptr(), idb
+def _id_list(ids, name: str, n: int, index: int):
+    """Address of n contiguous int32 or int64 ids on the device, and their size."""
+    if isinstance(ids, torch.Tensor) and ids.get_device() == index and ids.numel() == n \
+            and ids.is_contiguous():
+        if ids.dtype is torch.int64:
+            return ids.data_ptr(), 8
+        if ids.dtype is torch.int32:
+            return ids.data_ptr(), 4
+    raise ValueError(f"{name} must be {n} contiguous int32 or int64 values on cuda:{index}")
 
 
-def _table(t, name: str, rows: int, cols: int, device, dtype):
-    if not isinstance(t, torch.Tensor) or t.get_device() != device.index or t.dtype != dtype \
-            or not t.is_contiguous() or t.numel() != rows * cols:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of [{rows}, {cols}] on {device}")
+def _table(t, name: str, rows: int, cols: int, index: int, dtype):
+    """Address of a contiguous [rows, cols] tensor on the device."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index \
+            and t.numel() == rows * cols and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of [{rows}, {cols}] on cuda:{index}")
 
 
 def token_logprobs(logits, ids=None, scale=1.0, top=0, padding_idx=-1, logprob=None, entropy=None,
@@ -894,59 +929,57 @@ def token_logprobs(logits, ids=None, scale=1.0, top=0, padding_idx=-1, logprob=N
     -inf.  Another id outside [0, V) gives 0 and ERR_BAD_INPUT from
     topk_ef_last_device_status(ws).  Autograd records nothing: the gradient is
     token_logprobs_grad's."""
-    z, zt, ldz = _rows(logits, "logits")
-    dev = z.device
-    T, V = z.shape
-    ip, idb = _ids_of(ids, T, dev)
+    z, zt, ldz, at, T, V = _rows(logits, "logits")
+    ip, idb = (None, 8) if ids is None else _id_list(ids, "ids", T, at)
     top = int(top)
     if ids is None and logprob is not None:
         raise ValueError("logprob needs ids")
     if top == 0 and (top_ids is not None and top_ids.numel()
                      or top_logprobs is not None and top_logprobs.numel()):
         raise ValueError("top_ids and top_logprobs need top")
-    lpp = _f32(logprob, "logprob", T, dev, dev.index)
-    enp = _f32(entropy, "entropy", T, dev, dev.index)
-    lsp = _f32(lse, "lse", T, dev, dev.index)
-    _on_device(ws, dev)
+    lpp = _f32(logprob, "logprob", T, at)
+    enp = _f32(entropy, "entropy", T, at)
+    lsp = _f32(lse, "lse", T, at)
+    _workspace_on(ws, at)
 
     def call(st):
         lp, en, ls, ti, tp, la, ea, sa = logprob, entropy, lse, top_ids, top_logprobs, lpp, enp, lsp
         if lp is None and ids is not None:
-            lp = torch.empty(T, dtype=torch.float32, device=dev)
+            lp = torch.empty(T, dtype=torch.float32, device=z.device)
             la = lp.data_ptr()
         if en is None:
-            en = torch.empty(T, dtype=torch.float32, device=dev)
+            en = torch.empty(T, dtype=torch.float32, device=z.device)
             ea = en.data_ptr()
         if ls is None:
-            ls = torch.empty(T, dtype=torch.float32, device=dev)
+            ls = torch.empty(T, dtype=torch.float32, device=z.device)
             sa = ls.data_ptr()
         if top > 0:
             if ti is None:
-                ti = torch.empty((T, top), dtype=torch.int32, device=dev)
+                ti = torch.empty((T, top), dtype=torch.int32, device=z.device)
             if tp is None:
-                tp = torch.empty((T, top), dtype=torch.float32, device=dev)
-            _table(ti, "top_ids", T, top, dev, torch.int32)
-            _table(tp, "top_logprobs", T, top, dev, torch.float32)
-        w = ws if ws is not None else _workspace(_STATUS_WS, dev, None)
+                tp = torch.empty((T, top), dtype=torch.float32, device=z.device)
+            tia = _table(ti, "top_ids", T, top, at, torch.int32)
+            tpa = _table(tp, "top_logprobs", T, top, at, torch.float32)
+        else:
+            tia = tpa = None
+        w = ws if ws is not None else _workspace(_STATUS_WS, z.device, None)
         rc = (_lib or lib()).token_logprobs(z.data_ptr(), zt, ldz, ip, idb, T, V, scale,
                                             int(padding_idx), top, la, ea, sa,
-                                            ti.data_ptr() if top > 0 else None,
-                                            tp.data_ptr() if top > 0 else None, w.data_ptr(),
-                                            w.nbytes, st)
+                                            tia, tpa, w.data_ptr(), w.nbytes, st)
         if rc != OK:
             _check(rc, "token_logprobs")
         return lp, en, ls, ti, tp
 
-    return _on(dev, stream, call)
+    return _at(at, stream, call)
 
 
-def _grad_rows(out, z, dtype, device):
+def _grad_rows(out, z, dtype, index):
     """(the tensor, 2-d view, type code, row stride) of a gradient of the logits."""
     if out is None:
-        out = torch.empty(z.shape, dtype=dtype or z.dtype, device=device)
+        out = torch.empty(z.shape, dtype=dtype or z.dtype, device=z.device)
     elif dtype is not None and out.dtype != dtype:
         raise ValueError("out and out_dtype differ")
-    o2, ot, ldo = _rows(out, "the logits' gradient", z.shape[-1], device)
+    o2, ot, ldo = _rows(out, "the logits' gradient", z.shape[-1], index)[:3]
     if o2.numel() != z.numel():
         raise ValueError("the logits' gradient must have their shape")
     return out, o2, ot, ldo
@@ -960,30 +993,28 @@ def token_logprobs_grad(logits, ids, lse, grad_logprob=None, entropy=None, grad_
     [rows] or None for 0 (entropy is needed with the latter).  out may be the
     logits.  Rows that are padding or whose gradients are 0 are not read and
     give zeros."""
-    z, zt, ldz = _rows(logits, "logits")
-    dev = z.device
-    T, V = z.shape
-    ip, idb = _ids_of(ids, T, dev)
+    z, zt, ldz, at, T, V = _rows(logits, "logits")
+    ip, idb = (None, 8) if ids is None else _id_list(ids, "ids", T, at)
     if lse is None or (grad_entropy is not None and entropy is None) or \
             (grad_logprob is not None and ids is None):
         raise ValueError("lse, ids for grad_logprob and entropy for grad_entropy are needed")
-    sp = _f32(lse, "lse", T, dev, dev.index)
-    ep = _f32(entropy, "entropy", T, dev, dev.index)
-    gp = _f32(grad_logprob, "grad_logprob", T, dev, dev.index)
-    hp = _f32(grad_entropy, "grad_entropy", T, dev, dev.index)
-    _on_device(ws, dev)
+    sp = _f32(lse, "lse", T, at)
+    ep = _f32(entropy, "entropy", T, at)
+    gp = _f32(grad_logprob, "grad_logprob", T, at)
+    hp = _f32(grad_entropy, "grad_entropy", T, at)
+    _workspace_on(ws, at)
 
     def call(st):
-        o, o2, ot, ldo = _grad_rows(out, logits, out_dtype, dev)
-        w = ws if ws is not None else _workspace(_STATUS_WS, dev, None)
-        rc = lib().token_logprobs_grad(z.data_ptr(), zt, ldz, ip, idb, T, V, scale,
+        o, o2, ot, ldo = _grad_rows(out, logits, out_dtype, at)
+        w = ws if ws is not None else _workspace(_STATUS_WS, z.device, None)
+        rc = (_lib or lib()).token_logprobs_grad(z.data_ptr(), zt, ldz, ip, idb, T, V, scale,
                                        int(padding_idx), sp, ep, gp, hp, o2.data_ptr(), ot, ldo,
                                        w.data_ptr(), w.nbytes, st)
         if rc != OK:
             _check(rc, "token_logprobs_grad")
         return o
 
-    return _on(dev, stream, call)
+    return _at(at, stream, call)
 
 
 def distill_loss_workspace_bytes() -> int:
@@ -1002,37 +1033,35 @@ def distill_loss(logits, teacher_ids, teacher_logits, weight=None, scale=1.0, gr
     entry); teacher_logits: [rows, K]; weight: float32 [rows] or None for 1.  An id
     past V gives ERR_BAD_INPUT from topk_ef_last_device_status(ws) and counts
     nowhere."""
-    z, zt, ldz = _rows(logits, "logits")
-    dev = z.device
-    T, V = z.shape
-    idb, n = _token_ids(teacher_ids, dev)
-    K = int(teacher_ids.shape[-1]) if teacher_ids.dim() else 1
-    if n != T * K:
+    z, zt, ldz, at, T, V = _rows(logits, "logits")
+    if not isinstance(teacher_ids, torch.Tensor) or teacher_ids.dim() == 0:
         raise ValueError("teacher_ids must be [rows, K]")
-    tp, tt = _vector(teacher_logits, "teacher_logits", T * K, dev)
+    K = teacher_ids.shape[-1]
+    ip, idb = _id_list(teacher_ids, "teacher_ids", T * K, at)
+    tp, tt = _vector(teacher_logits, "teacher_logits", T * K, at)
     if tp is None:
         raise ValueError("teacher_logits are needed")
-    wp = _f32(weight, "weight", T, dev, dev.index)
-    lp = _f32(loss, "loss", T, dev, dev.index)
-    _on_device(ws, dev)
+    wp = _f32(weight, "weight", T, at)
+    lp = _f32(loss, "loss", T, at)
+    _workspace_on(ws, at)
 
     def call(st):
         lo, la, o, op, ot, ldo = loss, lp, grad_logits, None, 0, V
         if lo is None:
-            lo = torch.empty(T, dtype=torch.float32, device=dev)
+            lo = torch.empty(T, dtype=torch.float32, device=z.device)
             la = lo.data_ptr()
         if grad or o is not None:
-            o, o2, ot, ldo = _grad_rows(o, logits, out_dtype, dev)
+            o, o2, ot, ldo = _grad_rows(o, logits, out_dtype, at)
             op = o2.data_ptr()
-        w = ws if ws is not None else _workspace(_STATUS_WS, dev, None)
-        rc = (_lib or lib()).distill_loss(z.data_ptr(), zt, ldz, teacher_ids.data_ptr(), idb, tp, tt,
+        w = ws if ws is not None else _workspace(_STATUS_WS, z.device, None)
+        rc = (_lib or lib()).distill_loss(z.data_ptr(), zt, ldz, ip, idb, tp, tt,
                                           T, V, K, scale, wp, la, op, ot, ldo, w.data_ptr(),
                                           w.nbytes, st)
         if rc != OK:
             _check(rc, "distill_loss")
         return lo, o
 
-    return _on(dev, stream, call)
+    return _at(at, stream, call)
 
 
 # -------------------------------------------------------------------- status

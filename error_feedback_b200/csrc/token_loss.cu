@@ -126,7 +126,7 @@ int token_logprobs(const void* logits, int32_t logits_type, int64_t ld_logits, c
         !ws || !aligned(ws, ALIGN))
         return TOPK_EF_ERR_INVALID_ARG;
     const int64_t lines = most_lines(logits, ld_logits, V, sz);
-    if (top > 0 && lines > TL_MAX_LINES) return TOPK_EF_ERR_INVALID_ARG;
+    if (top > 0 && most_lines(nullptr, 1, V, sz) > TL_MAX_LINES) return TOPK_EF_ERR_INVALID_ARG;
     if (ids && ((id_bytes != 4 && id_bytes != 8) || !aligned(ids, id_bytes)))
         return TOPK_EF_ERR_INVALID_ARG;
     if (!ids && logprob) return TOPK_EF_ERR_INVALID_ARG;
