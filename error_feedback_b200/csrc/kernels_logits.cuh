@@ -706,6 +706,9 @@ __device__ __forceinline__ void select_top(const LogprobParams& p, const LineRow
     }
 }
 
+// Bound by the bytes of z without the top (4,096 x 131,072 bf16: 173 us, 6.2 TB/s), by the issue
+// slots that the lines' maxima, their histogram and the ranks take with it (top 64: 220 to 236,
+// top 128: 246).  One row of 131,072 fp32 with its top 20, 16 blocks: 9 us, the chain of its steps.
 template <int W, bool TOP>
 constexpr int LOGPROB_BLOCKS = (TOP ? 3 : 4) * 256 / Team<W>::BLOCK;       // of an SM
 
@@ -812,6 +815,7 @@ constexpr int LD_THREADS = 128, LD_WARPS = LD_THREADS / 32;
 constexpr int LD_LINES = 128;              // lines of a row that one warp takes
 
 // dz_i = scale (g (delta_i,id - p_i) - h p_i (log p_i + entropy)), a warp a part of a row.
+// Bound by the bytes of z and dz: 2,048 x 131,072 bf16 with both gradients in 162 us, 6.5 TB/s.
 // SAME: z's and dz's rows lie alike in their lines.
 template <typename T, typename TO, bool SAME, bool ENTROPY>
 __global__ void __launch_bounds__(LD_THREADS) logprob_grad_kernel(const LogprobGradParams p) {
@@ -958,10 +962,11 @@ __device__ __forceinline__ float2 join_powers(float2 a, float2 b, float c) {
 // Bound by the bytes of z and dz, and for short rows by the chain of a row's steps: so
 // thread k keeps the teacher's k-th entry in registers, its softmax and the loss ride on the
 // barriers that the row's sums and the gradient need anyway (a barrier for each step: 70 us
-// instead of 65 for 4,096 rows of 8,192 bf16 by eight warps each; 43 by four).  For the gradient the row is read again, out of
-// L2.  (Kept in shared memory instead, with the next row copied behind it, by blocks of 8, 16
-// or 32 warps: 255 to 290 us for 2,048 x 131,072 bf16, 148 for 4,096 x 32,768; read again: 240
-// and 122.  Fewer blocks fit, and they all read or all write at the same time.)
+// instead of 65 for 4,096 rows of 8,192 bf16 by eight warps each; 43 by four).  For the
+// gradient the row is read again, out of L2: 228 to 234 us for 2,048 x 131,072 bf16 (4.5 to 4.6
+// TB/s of z and dz), 115 for 4,096 x 32,768.  (Kept in shared memory instead, with the next row
+// copied behind it, by blocks of 8, 16 or 32 warps: 255 to 290, and 148.  Fewer blocks fit, and
+// they all read or all write at the same time.)
 template <int W, typename T, typename TO, bool SAME>
 __global__ void __launch_bounds__(Team<W>::BLOCK, 3 * 256 / Team<W>::BLOCK) distill_kernel(const DistillParams p) {
     constexpr int N = Team<W>::THREADS, TEAMS = Team<W>::TEAMS;

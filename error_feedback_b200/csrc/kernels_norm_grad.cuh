@@ -6,9 +6,9 @@
 // over all of a block's rows, so w and the column sums stay in registers, with the rows that
 // follow on their way into a ring of shared memory (kernels_norm.cuh).  Column sums leave one
 // fp32 row per block, added in a fixed order by a second kernel: no floating-point atomics.
-// 1,024 threads (rows past NG_COLS_D) have no registers for the sums: a kernel of its own reads x
-// and dy for them first (2,048 x 16,384 bf16: 125 us with the sums in the same kernel, 80 so).  Rows past
-// NM_MAX_D columns are read again instead of held.
+// 1,024 threads (rows past NG_COLS_D) have no registers for the sums: a kernel of its own reads
+// x and dy for them first (2,048 x 16,384 bf16: 125 us with the sums in the same kernel, 80 so).
+// Rows past NM_MAX_D columns are read again instead of held.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -39,7 +39,8 @@ struct NormGradParams {
     float inv_d;
 };
 
-// G threads a row.  Bound by the bytes of x, dy and dx.
+// G threads a row.  Bound by the bytes of x, dy and dx: 32,768 x 4,096 bf16 in 142.5 to 147 us
+// with the sum of the parts, 5.5 to 5.65 TB/s.  500 x 1,024 takes 6.8, the latency of two launches.
 template <typename TX, typename TD, int G, int V>
 __global__ void __launch_bounds__(NORM_BLOCK<G>, G <= 256 ? 2 : 1)
     norm_grad_kernel(const NormGradParams p) {

@@ -522,7 +522,8 @@ size_t token_logprobs_workspace_bytes(void);
  *   top_ids, top_logprobs  device, int32 and fp32[T][top], each may be NULL
  *   sizes      0 <= T <= 2^31 - 1; 1 <= V <= 2^24; ld_logits >= V
  *   ws         device workspace of >= token_logprobs_workspace_bytes()
- * -Inf (a forbidden token) has probability 0.  A row of nothing else has lse and
+ * -Inf (a forbidden token) has probability 0, and one below 2^-126 of the largest
+ * logit's counts as 0 in the sums.  A row of nothing else than -Inf has lse and
  * logprob -Inf and entropy 0.  NaN or +Inf makes a row's logprob, entropy, lse
  * and top_logprobs NaN (a token at -Inf keeps -Inf under +Inf), its top_ids
  * follow the order above.  An id outside
@@ -542,7 +543,7 @@ int token_logprobs(const void* logits, int32_t logits_type, int64_t ld_logits,
  * Gradient of token_logprobs' log-probabilities and entropies in the logits:
  *     grad_logits[t][i] = scale * (grad_logprob[t] * ((i == ids[t]) - p_i)
  *                                  - grad_entropy[t] * p_i (log p_i + entropy[t]))
- * in fp32, one rounding to grad_logits_type.
+ * in fp32 (a p_i below 2^-126 counts as 0), one rounding to grad_logits_type.
  *   lse        device, fp32[T], token_logprobs'
  *   entropy    device, fp32[T], token_logprobs'; needed with grad_entropy
  *   grad_logprob, grad_entropy  device, fp32[T]; NULL for 0
@@ -585,7 +586,8 @@ size_t distill_loss_workspace_bytes(void);
  *                   token_logprobs_grad
  *   ws              device workspace of >= distill_loss_workspace_bytes()
  * Rows whose weight is 0 or that have no entry above -Inf give loss 0 and zeros;
- * those of weight 0 are not read.  An id >= V is an empty entry and gives
+ * those of weight 0 are not read.  The loss with and without grad_logits may differ in
+ * its last bits (sums in another order).  An id >= V is an empty entry and gives
  * TOPK_EF_ERR_BAD_INPUT through topk_ef_last_device_status(ws).
  * Infinite and NaN logits, sizes, scale and errors as in token_logprobs; a teacher's
  * token at -Inf makes the loss +Inf.
