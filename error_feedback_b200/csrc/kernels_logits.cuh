@@ -16,9 +16,9 @@
 // -inf (a forbidden token) has p = 0 and counts nowhere.  NaN and +inf make the row
 // NaN.
 //
-// A row is worked on by a team: a warp or four (rows of up to LG_SMALL and LG_MIDDLE lines, where
-// the chain of a row's steps counts: many at once), a block of eight, or a cluster of blocks
-// while there are few rows, each block an equal share of the row's 128-byte lines.  Rows start
+// A row is worked on by a team: a warp or four (many rows, short ones above all: the chain of
+// a row's steps overlaps with other rows' reads), a block of eight, or a cluster of blocks while
+// there are few rows, each block an equal share of the row's 128-byte lines.  Rows start
 // anywhere; whole lines are read as 32 bytes a thread.
 #pragma once
 
@@ -33,7 +33,7 @@
 
 namespace tke {
 
-constexpr int LG_SMALL = 64;               // lines of a row that one warp takes
+constexpr int LG_SMALL = 128;              // lines of a row that one warp takes
 constexpr int LG_MIDDLE = 256;             // ... and that four take
 constexpr int LG_LINE = 128;               // bytes of a line (a group of the top selection)
 constexpr int LG_FLIGHT = 4;               // 32-byte chunks that a thread loads at once
@@ -392,6 +392,11 @@ __device__ __forceinline__ RowSoft join_softmax(const LineRow<T>& row, int32_t l
     return r;
 }
 
+// 32-byte chunks of a group, whose largest value the top selection keeps: a warp's rows are
+// short, and so are their groups (16,384 rows of 8,000 bf16, top 100: 758 us by lines, 157 so).
+template <int W>
+constexpr int GROUP = W == 1 ? 1 : 4;
+
 // The thread's part of the sums of a row, of which a block takes lines [line0, line1); TOP:
 // the largest value of each line in tops[line].
 template <int W, typename T, bool ENTROPY, bool TOP>
@@ -406,6 +411,10 @@ __device__ __forceinline__ Running row_sums(const LineRow<T>& row, int32_t line0
         if (TOP) {
 #pragma unroll
             for (int k = 0; k < LG_FLIGHT; ++k) {
+                if (GROUP<W> == 1) {
+                    if (j + k * N < end) tops[j + k * N] = top[k];
+                    continue;
+                }
                 float line = max_nan(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], 1));
                 line = max_nan(line, __shfl_xor_sync(0xFFFFFFFFu, line, 2));
                 if ((threadIdx.x & 3) == 0 && j + k * N < end) tops[(j + k * N) >> 2] = line;
@@ -451,17 +460,27 @@ __device__ __forceinline__ void scan_ids(const void* ids, int32_t id64, int64_t 
     }
 }
 
+// The groups that hold any of the row's elements.
+template <int W, typename T>
+__device__ __forceinline__ int first_group(const LineRow<T>& row) {
+    return row.lead / (GROUP<W> * CHUNK<T>);
+}
+template <int W, typename T>
+__device__ __forceinline__ int end_group(const LineRow<T>& row) {
+    return (row.end + GROUP<W> * CHUNK<T> - 1) / (GROUP<W> * CHUNK<T>);
+}
+
 constexpr int TL_BINS = 512;               // 32 an octave of 1 + m - c z
 
 template <int W>
 struct TopShared {
-    static constexpr int LINES = W == 1 ? LG_SMALL : 512;  // that are read again
+    static constexpr int GROUPS = W == 1 ? 256 : 512;      // that are read again
     static constexpr int LIST = W == 1 ? 256 : 512;        // candidates that are ranked
     uint32_t hist[TL_BINS];
-    uint32_t lines, n;                     // lengths of the lists
+    uint32_t groups, n;                    // lengths of the lists
     uint32_t count[2 * W];
     uint32_t scan[33];
-    uint32_t line[LINES];
+    uint16_t group[GROUPS];
     __align__(16) unsigned long long list[LIST];   // key, then the lower index first
 };
 
@@ -517,8 +536,8 @@ __device__ __forceinline__ uint32_t bin_of(const uint32_t* hist, uint32_t want, 
     return (uint32_t)(src * EACH + at);
 }
 
-// The lists by exact counts, where the bins hold too many: the K-th largest of the lines'
-// largest values, t; the lines above it and the first of those at it; of their
+// The lists by exact counts, where the bins hold too many: the K-th largest of the groups'
+// largest values, t; the groups above it and the first of those at it; of their
 // elements the ones above the K-th largest of them and the first of those at it.
 template <int W, typename T>
 __device__ __forceinline__ void list_exactly(const LineRow<T>& row, int K, const float* tops,
@@ -528,20 +547,21 @@ __device__ __forceinline__ void list_exactly(const LineRow<T>& row, int K, const
     // (keys whose low bits are set, a negative value's, compare as the value they stand for)
     constexpr uint32_t mask = ~((1u << LOW) - 1);
     const int tid = Team<W>::thread();
-    const int lines = row.lines(), want = min(min(K, lines), TopShared<W>::LINES);
-    const int per = (lines + N - 1) / N;
-    // the thread's lines are neighbours, so that a scan over threads is one over lines
-    const int l0 = min(lines, tid * per), l1 = min(lines, l0 + per);
+    const int g_first = first_group<W>(row), g_end = end_group<W>(row), groups = g_end - g_first;
+    const int want = min(min(K, groups), TopShared<W>::GROUPS);
+    const int per = (groups + N - 1) / N;
+    // the thread's groups are neighbours, so that a scan over threads is one over groups
+    const int g0 = min(g_end, g_first + tid * per), g1 = min(g_end, g0 + per);
     uint32_t t = 0;
-    if (lines > K)
+    if (groups > K)
         t = team_threshold<W, LOW>((uint32_t)K, S.count, [&](uint32_t k) {
             uint32_t n = 0;
-            for (int l = tid; l < lines; l += N) n += order_key(tops[l]) >= k;
+            for (int g = g_first + tid; g < g_end; g += N) n += order_key(tops[g]) >= k;
             return n;
         });
     uint32_t above = 0, equal = 0;
-    for (int l = l0; l < l1; ++l) {
-        const uint32_t k = order_key(tops[l]) & mask;
+    for (int g = g0; g < g1; ++g) {
+        const uint32_t k = order_key(tops[g]) & mask;
         above += k > t;
         equal += k == t;
     }
@@ -550,20 +570,20 @@ __device__ __forceinline__ void list_exactly(const LineRow<T>& row, int K, const
     {
         const uint32_t quota = (uint32_t)want - (tot >> 16);
         uint32_t a = before >> 16, e = before & 0xFFFF;
-        for (int l = l0; l < l1; ++l) {
-            const uint32_t k = order_key(tops[l]) & mask;
-            if (k > t || (k == t && e < quota)) S.line[a + min(e, quota)] = (uint32_t)l;
+        for (int g = g0; g < g1; ++g) {
+            const uint32_t k = order_key(tops[g]) & mask;
+            if (k > t || (k == t && e < quota)) S.group[a + min(e, quota)] = (uint16_t)g;
             a += k > t;
             e += k == t;
         }
     }
     Team<W>::sync();
     // f(key, position) for their elements, in order: the thread's chunks are neighbours too
-    const int chunks = want * 4, each = (chunks + N - 1) / N;
+    const int chunks = want * GROUP<W>, each = (chunks + N - 1) / N;
     const auto elements = [&](auto f) {
 #pragma unroll 1
         for (int j = tid * each; j < min(chunks, tid * each + each); ++j) {
-            const int32_t chunk = (int32_t)S.line[j >> 2] * 4 + (j & 3);
+            const int32_t chunk = S.group[j / GROUP<W>] * GROUP<W> + j % GROUP<W>;
             Chunk<T> q;
             load_chunk(row, chunk, q);
 #pragma unroll
@@ -604,30 +624,32 @@ __device__ __forceinline__ void list_exactly(const LineRow<T>& row, int K, const
 
 // The top K of the row by (value descending, index ascending), one team.
 //
-// The K-th largest value is at least the K-th largest of the lines' largest ones.  A
+// The K-th largest value is at least the K-th largest of the groups' largest ones.  A
 // histogram of those by their distance from the row's largest gives a bin that holds it;
-// the lines up to that bin are read again, and their elements up to it, hardly more than
-// K, are ranked by comparing each with each.  (Exact counts over 16 or 32 bits of the
+// the groups up to that bin are read again, and their elements up to it, hardly more than
+// K, are ranked by comparing each with each.  (While groups are few, a histogram of all
+// elements instead: near K groups have too many elements up to the least of them.)  (Exact counts over 16 or 32 bits of the
 // lines' keys instead of bins: 380 us more for 4,096 rows of 131,072 bf16.)
 template <int W, typename T>
 __device__ __forceinline__ void select_top(const LogprobParams& p, const LineRow<T>& row, int64_t r,
                                            const float* tops, TopShared<W>& S, const RowSoft& soft) {
     constexpr int N = Team<W>::THREADS, LIST = TopShared<W>::LIST;
     const int tid = Team<W>::thread();
-    const int lines = row.lines(), K = p.top;
+    const int g_first = first_group<W>(row), g_end = end_group<W>(row), groups = g_end - g_first;
+    const int K = p.top;
     const float c = p.c, m = soft.m;
     bool exactly = soft.far;                   // (distances mean nothing)
     if (!exactly) {
         for (int i = tid; i < TL_BINS; i += N) S.hist[i] = 0;
-        if (tid == 0) S.lines = S.n = 0;
+        if (tid == 0) S.groups = S.n = 0;
         Team<W>::sync();
-        const bool some = lines > K, binned = some || p.V > LIST;
+        const bool some = groups > (W == 1 ? 2 * K : K), binned = some || p.V > LIST;
         uint32_t bin = TL_BINS - 1;
         if (some) {
-            for (int l = tid; l < lines; l += N)
-                atomicAdd(&S.hist[depth_bin(depth(tops[l], c, m))], 1u);
+            for (int g = g_first + tid; g < g_end; g += N)
+                atomicAdd(&S.hist[depth_bin(depth(tops[g], c, m))], 1u);
         } else if (binned) {
-            for (int j = tid; j < lines * 4; j += N) {
+            for (int j = tid; j < row.lines() * 4; j += N) {
                 Chunk<T> q;
                 load_chunk(row, j, q);
 #pragma unroll
@@ -642,7 +664,7 @@ __device__ __forceinline__ void select_top(const LogprobParams& p, const LineRow
             Team<W>::sync();
             uint32_t upto;
             bin = bin_of(S.hist, (uint32_t)min((int64_t)K, p.V), upto);
-            exactly = upto > (uint32_t)(some ? TopShared<W>::LINES : LIST);
+            exactly = upto > (uint32_t)(some ? TopShared<W>::GROUPS : LIST);
         }
         if (!exactly) {
             // (the last bin has no end)
@@ -650,13 +672,13 @@ __device__ __forceinline__ void select_top(const LogprobParams& p, const LineRow
                                                   : __uint_as_float(0x3F800000u + ((bin + 1) << 18));
             const auto within = [&](float z) { return depth(z, c, m) < edge || bin == TL_BINS - 1; };
             if (some) {
-                for (int l = tid; l < lines; l += N)
-                    if (within(tops[l])) S.line[atomicAdd(&S.lines, 1u)] = (uint32_t)l;
+                for (int g = g_first + tid; g < g_end; g += N)
+                    if (within(tops[g])) S.group[atomicAdd(&S.groups, 1u)] = (uint16_t)g;
                 Team<W>::sync();
             }
-            const int chunks = (some ? (int)S.lines : lines) * 4;
+            const int chunks = some ? (int)S.groups * GROUP<W> : row.lines() * 4;
             for (int j = tid; j < chunks; j += N) {
-                const int32_t chunk = (some ? (int32_t)S.line[j >> 2] : j >> 2) * 4 + (j & 3);
+                const int32_t chunk = some ? S.group[j / GROUP<W>] * GROUP<W> + j % GROUP<W> : j;
                 const int32_t pos = chunk * CHUNK<T>;
                 Chunk<T> q;
                 load_chunk(row, chunk, q);
@@ -706,9 +728,9 @@ __device__ __forceinline__ void select_top(const LogprobParams& p, const LineRow
     }
 }
 
-// Bound by the bytes of z without the top (4,096 x 131,072 bf16: 173 us, 6.2 TB/s), by the issue
-// slots that the lines' maxima, their histogram and the ranks take with it (top 64: 220 to 236,
-// top 128: 246).  One row of 131,072 fp32 with its top 20, 16 blocks: 9 us, the chain of its steps.
+// Bound by the bytes of z without the top (4,096 x 131,072 bf16: 173 to 182 us, 5.9 to 6.2 TB/s),
+// with it by the selection, during which a block reads nothing (top 64: 210 to 223 us, top 128:
+// 250; short rows: 16,384 x 8,000, top 20, 86 us, top 100, 157, most of it the ranks).  One row of 131,072 fp32 with its top 20, 16 blocks: 9 us, the chain of its steps.
 template <int W, bool TOP>
 constexpr int LOGPROB_BLOCKS = (TOP ? 3 : 4) * 256 / Team<W>::BLOCK;       // of an SM
 
@@ -716,10 +738,9 @@ template <int W, typename T, bool ENTROPY, bool TOP>
 __global__ void __launch_bounds__(Team<W>::BLOCK, LOGPROB_BLOCKS<W, TOP>)
     logprob_kernel(const LogprobParams p) {
     constexpr int N = Team<W>::THREADS, TEAMS = Team<W>::TEAMS;
-    extern __shared__ __align__(16) float s_dyn[];     // TOP, W > 1: [lines of the row, in fours]
+    extern __shared__ __align__(16) float s_dyn[];     // TOP: the groups' largest values
     __shared__ Soft s_soft[W + 1];
     __shared__ TopShared<W> S[TEAMS];
-    __shared__ float s_small[TOP && W == 1 ? TEAMS * LG_SMALL : 1];
     pdl_launch();
     pdl_wait();
     const int64_t block = (int64_t)(blockIdx.x / (unsigned)p.blocks) - p.scan;
@@ -730,7 +751,7 @@ __global__ void __launch_bounds__(Team<W>::BLOCK, LOGPROB_BLOCKS<W, TOP>)
     }
     const int64_t r = block * TEAMS + Team<W>::team();
     if (r >= p.T) return;
-    float* s_tops = W == 1 ? s_small + Team<W>::team() * LG_SMALL : s_dyn;
+    float* s_tops = s_dyn + Team<W>::team() * (LG_SMALL * 4);
     int64_t id = -1;
     bool skip = false, ok = false;
     if (p.ids) {

@@ -22,12 +22,24 @@ constexpr int64_t LEAST_LINES = 32;        // lines of a block of a cluster
 // Bytes of logits that L2 holds besides what is written (2,048 x 131,072 bf16, 114 MB: 255 us
 // one block a row, 239 two).
 constexpr int64_t GRAD_L2 = (int64_t)80 << 20;
-// Warps of a row: fewer for short rows once there are more of them than blocks that run at
-// once.  (64 rows of 1,000 bf16, top 20: eight warps each 9.4 us, one 13; 16,384 rows: 280 and
-// 72 us.)
+constexpr int64_t ROUND = SMS * 3;         // blocks of eight warps that run at once
+// Warps of a row: fewer once there are more rows than blocks that run at once, so that more
+// of them overlap.  (1,024 x 1,000 bf16, top 20: one warp 9.5 us, four 14.1; 600 x 1,000: both
+// 9.5; 1,024 x 8,000: 18.2 and 12.6, 2,048 x 8,000: 19.7 and 21.4.  2,048 x 1,000: four 21.3,
+// eight 34.1.)
 int row_warps(int64_t T, int64_t lines) {
-    if (T <= SMS * 3) return 8;
-    return lines <= LG_SMALL ? 1 : lines <= LG_MIDDLE ? 4 : 8;
+    if (T <= ROUND) return 8;
+    if (T > (lines <= 64 ? 2 : 4) * ROUND && lines <= LG_SMALL) return 1;
+    return lines <= 256 ? 4 : 8;
+}
+// token_logprobs' too, whose longer rows gain in their selection, if the last round is as full
+// by four as by eight: 4,096 x 131,072 bf16, top 20, 208.6 us by four and 220.2 by eight, 1,024
+// rows 66.9 and 60.8.  Short of 1,024 lines it need not be (2,048 x 64,000: 66.0 and 69.6); more
+// than 4,608 take shared memory from blocks of four (1,200 x 400,000: 222 and 184).
+int logprob_warps(int64_t T, int64_t lines) {
+    const bool even = ceil_div64(T, 2 * ROUND) * 2 == ceil_div64(T, ROUND);
+    if (T >= 2 * ROUND && lines > 256 && (lines <= 1024 || (lines <= 4608 && even))) return 4;
+    return row_warps(T, lines);
 }
 
 bool sizes_ok(int64_t T, int64_t V) {
@@ -73,12 +85,12 @@ template <int W, typename T, bool ENTROPY, bool TOP>
 cudaError_t launch_logprob(const LogprobParams& p, size_t smem, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     const auto kernel = logprob_kernel<W, T, ENTROPY, TOP>;
-    cudaError_t e = allow(kernel, done, TOP && W > 1 ? TL_MAX_LINES * 4 : 0);
+    cudaError_t e = allow(kernel, done, TOP ? TL_MAX_LINES * 4 : 0);
     if (e != cudaSuccess) return e;
     const int64_t rows = ceil_div64(p.T, Team<W>::TEAMS);
     trace_before(st, "logprob_kernel");
     e = launch_clusters(kernel, (unsigned)((rows + p.scan) * p.blocks), (unsigned)p.blocks,
-                        Team<W>::BLOCK, W > 1 ? smem : 0, st, p);
+                        Team<W>::BLOCK, smem, st, p);
     trace_after(st);
     return e;
 }
@@ -151,8 +163,8 @@ int token_logprobs(const void* logits, int32_t logits_type, int64_t ld_logits, c
     p.padding = padding_idx;
     p.id64 = id_bytes == 8;
     p.top = top_ids || top_logprobs ? top : 0;
-    const int warps = row_warps(T, lines);
-    p.blocks = warps < 8 ? 1 : row_blocks(T, lines, SMS * 3);
+    const int warps = logprob_warps(T, lines);
+    p.blocks = warps < 8 ? 1 : row_blocks(T, lines, ROUND);
     p.scan = T <= SCAN_IDS;
     p.scale = scale;
     p.c = (float)((double)scale * 1.4426950408889634);
@@ -160,7 +172,10 @@ int token_logprobs(const void* logits, int32_t logits_type, int64_t ld_logits, c
         const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(Ctrl), st);
         if (e != cudaSuccess) return cuda_fail(e);
     }
-    const size_t smem = p.top ? ((size_t)lines * 4 + 15) / 16 * 16 : 0;
+    // the groups' largest values: of lines, or of the chunks of a block's rows
+    const size_t smem = !p.top       ? 0
+                        : warps == 1 ? Team<1>::TEAMS * LG_SMALL * 4 * sizeof(float)
+                                     : ((size_t)lines * 4 + 15) / 16 * 16;
     const cudaError_t e = with_type(logits_type, [&](auto t) {
         using TZ = decltype(t);
         if (p.top)
@@ -278,10 +293,10 @@ int distill_loss(const void* logits, int32_t logits_type, int64_t ld_logits,
                       same_lines(logits, ld_logits, grad_logits, ld_grad_logits, sz);
     const int64_t lines = most_lines(logits, ld_logits, V, sz);
     const int warps = row_warps(T, lines);
-    p.blocks = warps < 8 ? 1 : row_blocks(T, lines, SMS * 3);
+    p.blocks = warps < 8 ? 1 : row_blocks(T, lines, ROUND);
     // rows that blocks are at should fit L2 until their gradient is written
     if (grad_logits && warps == 8)
-        while (p.blocks < 4 && lines * LG_LINE * (SMS * 3 / p.blocks) > GRAD_L2) p.blocks *= 2;
+        while (p.blocks < 4 && lines * LG_LINE * (ROUND / p.blocks) > GRAD_L2) p.blocks *= 2;
     p.scan = T * std::max(K, 1) <= SCAN_IDS;
     p.scale = scale;
     p.c = (float)((double)scale * 1.4426950408889634);
