@@ -615,11 +615,11 @@ def test_binding_refuses():
         ef.distill_loss(z, i2, t, scale=-2.0)
 
 
-@pytest.mark.parametrize("V", [1, 33, 500, 2000, 4097, 8192, 16385, 40001])
+@pytest.mark.parametrize("T,V", [(501, V) for V in (1, 33, 500, 2000, 4097, 8192, 16385, 40001)] +
+                         [(900, 1), (900, 33), (900, 500), (900, 2000), (1800, 4000), (1800, 8000)])
 @pytest.mark.parametrize("zt", ["f32", "bf16"])
-def test_more_rows_than_run_at_once(V, zt):
+def test_more_rows_than_run_at_once(T, V, zt):
     """Rows of one warp, four and eight."""
-    T = 501
     z = _logits(T, V, TYPES[zt])
     z[3] = -INF
     z[5] = -1e9
