@@ -58,7 +58,7 @@ constexpr int CHUNK = 32 / (int)sizeof(T);         // elements of 32 bytes
 // W warps: a whole block, or each warp of a block of 8.
 template <int W>
 struct Team {
-    static constexpr int THREADS = W * 32;
+    static constexpr int WARPS = W, THREADS = W * 32;
     static constexpr int BLOCK = W == 1 ? 256 : THREADS;
     static constexpr int TEAMS = BLOCK / THREADS;
     static __device__ __forceinline__ int thread() { return (int)(threadIdx.x % THREADS); }
@@ -830,41 +830,158 @@ struct LogprobGradParams {
     int64_t T, V, ldz, lddz, padding;
     int32_t id64, parts;           // warps of a row
     int32_t scan;                  // the first block checks the ids
-    float scale;
+    float c, scale;
 };
 
 constexpr int LD_THREADS = 128, LD_WARPS = LD_THREADS / 32;
 constexpr int LD_LINES = 128;              // lines of a row that one warp takes
+// Most |lse| whose p = exp(scale z - lse) is kept: an fp32 lse is off by 2^-24 of itself twice
+// (its sum's, its rounding), so p by 2^-16 at most.
+constexpr float LD_LSE = 128.0f;
+
+// The gradient of a row whose lse is too far from 0 to hold log p (or is -inf where the row is
+// not): a team sums the row again, and reads it a third time.  (One team a row, since others'
+// results may lie where it reads.)  2,048 x 131,072 bf16, all rows far: 266 us, none: 165.
+template <int W, typename T, typename TO, bool SAME, bool ENTROPY>
+__device__ __forceinline__ void far_gradient(const T* z, TO* dz, int32_t V, int32_t id, float c, float g,
+                                             float h, float H, Soft* s_soft) {
+    constexpr int N = Team<W>::THREADS;
+    const LineRow<T> row(z, V);
+    const int32_t lines = row.lines();
+    const Running run = row_sums<W, T, false, false>(row, 0, lines, c, nullptr);
+    const RowSoft a = join_softmax<W>(row, 0, lines, c, 1, s_soft, run);
+    const bool none = a.s == 0.0f;                     // (all -inf)
+    // with p = 2^t / s: -p (g + h (log p + H)) = 2^t (k0 + k1 t), and g more at the token
+    const float inv = none ? 0.0f : 1.0f / a.s;
+    const float k1 = ENTROPY && !none ? -h * LN2 * inv : 0.0f;
+    const float k0 = none ? 0.0f : (ENTROPY ? fmaf(-h, H - LN2 * a.log2s, -g) : -g) * inv;
+    const auto values = [&](f32x2 v) {
+        f32x2 t = a.far ? mul2(add2(v, pair(-a.m, -a.m)), pair(c, c))
+                        : fma2(v, pair(c, c), pair(-a.m, -a.m));
+        const f32x2 e = ex2_2(t);
+        if (!ENTROPY) return mul2(e, pair(k0, k0));
+        const float2 f = parts(t);                     // (times e, which is 0 there)
+        t = pair(max_nan(f.x, -1e4f), max_nan(f.y, -1e4f));
+        return mul2(e, fma2(t, pair(k1, k1), pair(k0, k0)));
+    };
+    if (none) g = 0.0f;
+    if (SAME) {
+        const int32_t token = id < 0 ? -1 : id + row.lead;
+        for_chunks<W, 2>(row, 0, lines, [&](const Chunk<T>* q, int32_t j, int32_t end) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k, j += N) {
+                if (j >= end) continue;
+                const int32_t pos = j * CHUNK<T>;
+                Chunk<TO> o;
+#pragma unroll
+                for (int i = 0; i < CHUNK<T> / 2; ++i) {
+                    f32x2 v = values(Pairs<T>::template get<false>(q[k], i, 0.0f));
+                    if (token >> 1 == (pos >> 1) + i)
+                        v = add2(v, pair(token & 1 ? 0.0f : g, token & 1 ? g : 0.0f));
+                    put_pair(o, i, v);
+                }
+                store_chunk(row, dz - row.lead, pos, o);
+            }
+        });
+    } else {
+#pragma unroll 4
+        for (int32_t i = Team<W>::thread(); i < V; i += N) {
+            float v = parts(values(pair(to_f32(z[i]), 0.0f))).x;
+            if (i == id) v += g;
+            dz[i] = from_f32<TO>(v);
+        }
+    }
+}
+
+// What a warp knows of its row.
+template <bool ENTROPY>
+struct GradRow {
+    int64_t r;
+    int32_t part, id;              // id: -1 for none
+    bool there, skip, bad;
+    float lse, g, h, H;
+    __device__ __forceinline__ GradRow(const LogprobGradParams& p, int64_t item) {
+        r = item / p.parts;
+        part = (int)(item - r * p.parts);
+        id = -1;
+        there = r < p.T;
+        skip = !there;
+        bad = false;
+        lse = g = h = H = 0.0f;
+        if (!there) return;
+        if (p.ids) {
+            const int64_t v = load_id(p.ids, p.id64, r);
+            skip = v == p.padding;
+            if (v >= 0 && v < p.V) {
+                id = (int32_t)v;
+            } else {
+                bad = !skip;
+            }
+        }
+        lse = p.lse[r];
+        g = id >= 0 && p.g ? p.scale * p.g[r] : 0.0f;
+        if (ENTROPY) {
+            h = p.scale * p.h[r];
+            H = p.entropy[r];
+        }
+        skip = skip || (g == 0.0f && h == 0.0f);
+    }
+    __device__ __forceinline__ bool far() const { return !skip && fabsf(lse) > LD_LSE; }
+};
+
+// The far rows that the warps of a block have the first part of, by the whole block; of a
+// call whose rows are a warp each, the calling warp's.  (A call, so that it costs the other rows
+// no registers.)
+template <typename T, typename TO, bool SAME, bool ENTROPY>
+__device__ __noinline__ void far_rows(const LogprobGradParams& p) {
+    __shared__ Soft s_soft[LD_WARPS + 1];
+    const int64_t first = ((int64_t)blockIdx.x - p.scan) * LD_WARPS;
+    const auto gradient = [&](auto team, const GradRow<ENTROPY>& at) {
+        far_gradient<decltype(team)::WARPS, T, TO, SAME, ENTROPY>(
+            static_cast<const T*>(p.z) + at.r * p.ldz, static_cast<TO*>(p.dz) + at.r * p.lddz, (int32_t)p.V, at.id,
+            p.c, at.g, at.h, at.H, s_soft);
+    };
+    if (p.parts == 1) {
+        gradient(Team<1>{}, GradRow<ENTROPY>(p, first + warp_id()));
+        return;
+    }
+    for (int i = 0; i < LD_WARPS; ++i) {
+        const GradRow<ENTROPY> at(p, first + i);
+        if (!at.far() || at.part != 0) continue;
+        gradient(Team<LD_WARPS>{}, at);
+        __syncthreads();
+    }
+}
 
 // dz_i = scale (g (delta_i,id - p_i) - h p_i (log p_i + entropy)), a warp a part of a row.
 // Bound by the bytes of z and dz: 2,048 x 131,072 bf16 with both gradients in 162 us, 6.5 TB/s.
 // SAME: z's and dz's rows lie alike in their lines.
 template <typename T, typename TO, bool SAME, bool ENTROPY>
-__global__ void __launch_bounds__(LD_THREADS) logprob_grad_kernel(const LogprobGradParams p) {
+__global__ void __launch_bounds__(LD_THREADS, SAME ? 7 : 16)
+    logprob_grad_kernel(const __grid_constant__ LogprobGradParams p) {
     pdl_launch();
     pdl_wait();
     if (p.scan && blockIdx.x == 0) {
         scan_ids(p.ids, p.id64, p.T, p.V, p.padding, false, p.ctrl);
         return;
     }
+    const int lane = (int)lane_id();
     const int64_t item = ((int64_t)blockIdx.x - p.scan) * LD_WARPS + warp_id();
-    const int64_t r = item / p.parts;
-    const int part = (int)(item - r * p.parts), lane = (int)lane_id();
-    if (r >= p.T) return;
+    GradRow<ENTROPY> at(p, item);
+    // (the row's values are loaded again after the call, so that none is kept over it)
+    if (p.parts == 1 ? at.far() : __syncthreads_or(at.far() && at.part == 0) != 0) {
+        far_rows<T, TO, SAME, ENTROPY>(p);
+        at = GradRow<ENTROPY>(p, item);
+    }
+    if (at.bad && !p.scan && at.part == 0 && lane == 0) atomicOr(&p.ctrl->status, ST_BAD_INPUT);
+    if (!at.there || at.far()) return;
+    const int64_t r = at.r;
+    const int part = at.part;
     const T* z = static_cast<const T*>(p.z) + r * p.ldz;
     TO* dz = static_cast<TO*>(p.dz) + r * p.lddz;
-    int64_t id = -1;
-    bool skip = false, ok = false;
-    if (p.ids) {
-        id = load_id(p.ids, p.id64, r);
-        skip = id == p.padding;
-        ok = id >= 0 && id < p.V;
-        if (!skip && !ok && !p.scan && part == 0 && lane == 0) atomicOr(&p.ctrl->status, ST_BAD_INPUT);
-    }
-    const float lse = p.lse[r];
-    const float g = ok && p.g ? p.scale * p.g[r] : 0.0f;
-    const float h = ENTROPY ? p.scale * p.h[r] : 0.0f, H = ENTROPY ? p.entropy[r] : 0.0f;
-    skip = skip || (g == 0.0f && h == 0.0f) || lse == -CUDART_INF_F;
+    const int32_t id = at.id;
+    const bool skip = at.skip;
+    const float lse = at.lse, g = at.g, h = at.h, H = at.H;
     // -p (g + h (log p + H)), and g more at the token
     const float k0 = fmaf(-h, H, -g);
     auto values = [&](f32x2 v) {
@@ -883,7 +1000,7 @@ __global__ void __launch_bounds__(LD_THREADS) logprob_grad_kernel(const LogprobG
         const int32_t line1 = min(lines, line0 + LD_LINES);
         if (SAME) {
             TO* out = dz - row.lead;
-            const int32_t token = ok ? (int32_t)id + row.lead : -1;
+            const int32_t token = id < 0 ? -1 : id + row.lead;
             if (skip) {
                 const Chunk<TO> zero = {};
                 for (int32_t j = line0 * 4 + lane; j < line1 * 4; j += 32)
@@ -913,7 +1030,7 @@ __global__ void __launch_bounds__(LD_THREADS) logprob_grad_kernel(const LogprobG
                 float v = 0.0f;
                 if (!skip) {
                     v = parts(values(pair(to_f32(z[i]), 0.0f))).x;
-                    if (i == (int32_t)id) v += g;
+                    if (i == id) v += g;
                 }
                 dz[i] = from_f32<TO>(v);
             }

@@ -226,6 +226,7 @@ int token_logprobs_grad(const void* logits, int32_t logits_type, int64_t ld_logi
     p.id64 = id_bytes == 8;
     p.scan = T <= SCAN_IDS;
     p.scale = scale;
+    p.c = (float)((double)scale * 1.4426950408889634);
     p.parts = (int32_t)std::min(ceil_div64(most_lines(logits, ld_logits, V, sz), LD_LINES),
                                 std::max<int64_t>(1, MAX_N / (T + 1)));
     if (!p.scan) {

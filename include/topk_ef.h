@@ -544,6 +544,10 @@ int token_logprobs(const void* logits, int32_t logits_type, int64_t ld_logits,
  *     grad_logits[t][i] = scale * (grad_logprob[t] * ((i == ids[t]) - p_i)
  *                                  - grad_entropy[t] * p_i (log p_i + entropy[t]))
  * in fp32 (a p_i below 2^-126 counts as 0), one rounding to grad_logits_type.
+ * p_i is exp(scale * logits[t][i] - lse[t]) while |lse[t]| <= 128, where lse's own
+ * error leaves it off by 2^-16 at most.  Rows further from 0 (an offset, a small
+ * temperature, nothing left but a mask of finite value) are summed again with exact
+ * differences, which takes about 1.6 times as long.
  *   lse        device, fp32[T], token_logprobs'
  *   entropy    device, fp32[T], token_logprobs'; needed with grad_entropy
  *   grad_logprob, grad_entropy  device, fp32[T]; NULL for 0
@@ -551,8 +555,8 @@ int token_logprobs(const void* logits, int32_t logits_type, int64_t ld_logits,
  *              not written; may be logits itself (same type size and stride),
  *              must not overlap it otherwise.  Rows that lie in their
  *              128-byte lines as logits' do take the vectorised path
- * Rows that are padding, whose gradients are both 0 (an id outside [0, V) makes
- * grad_logprob 0) or whose lse is -Inf are not read and give zeros.
+ * Rows that are padding or whose gradients are both 0 (an id outside [0, V) makes
+ * grad_logprob 0) are not read and give zeros.  So do rows of nothing else than -Inf.
  * Otherwise as token_logprobs.
  */
 int token_logprobs_grad(const void* logits, int32_t logits_type,
