@@ -525,10 +525,10 @@ size_t token_logprobs_workspace_bytes(void);
  * -Inf (a forbidden token) has probability 0, and one below 2^-126 of the largest
  * logit's counts as 0 in the sums.  A row of nothing else than -Inf has lse and
  * logprob -Inf and entropy 0.  NaN or +Inf makes a row's logprob, entropy, lse
- * and top_logprobs NaN (a token at -Inf keeps -Inf under +Inf), its top_ids
- * follow the order above.  An id outside
- * [0, V), other than padding_idx, gives logprob 0 and TOPK_EF_ERR_BAD_INPUT through
- * topk_ef_last_device_status(ws); nothing outside logits is read.
+ * and top_logprobs NaN, those of tokens at -Inf too; its top_ids follow the order
+ * above.  An id outside [0, V), other than padding_idx, gives logprob 0 and
+ * TOPK_EF_ERR_BAD_INPUT through topk_ef_last_device_status(ws); nothing outside
+ * logits is read.
  * Errors: TOPK_EF_ERR_INVALID_ARG (sizes, types, null or misaligned pointers),
  * TOPK_EF_ERR_WORKSPACE, TOPK_EF_ERR_CUDA.
  */

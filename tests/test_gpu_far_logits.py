@@ -178,3 +178,22 @@ def test_far_and_masked_rows_of_every_team(T, V, zt):
     tk = [t[keep].contiguous() for t in (tids, tl, w)]
     calls._check_distill(zk, *tk[:2], tk[2], 0.7)
     calls._check_distill(zk, *tk[:2], None, 0.7, grad=False)
+
+
+@pytest.mark.parametrize("T,V", [(3, 50), (3, 40001), (600, 3000), (2000, 900)])
+def test_minus_inf_beside_inf(T, V):
+    """A row with +inf or NaN is NaN at its tokens of -inf too, as a log softmax is; no other row."""
+    z = calls._logits(T, V, torch.float32)
+    ids = calls._ids(T, V)
+    ids[1] = 4
+    want = ef.token_logprobs(z, ids, top=V if V < 100 else 3)
+    for value in (INF, math.nan):
+        y = z.clone()
+        y[1] = -INF
+        y[1, 7] = value
+        lp, en, ls, ti, tp = got = ef.token_logprobs(y, ids, top=V if V < 100 else 3)
+        assert lp[1].isnan() and en[1].isnan() and ls[1].isnan() and tp[1].isnan().all()
+        assert ti[1, :3].tolist() == [7, 0, 1]
+        assert ef.token_logprobs_grad(y, ids, ls, grad_logprob=torch.ones(T, device="cuda"))[1].isnan().all()
+        others = [r for r in range(T) if r != 1]
+        assert all(torch.equal(a[others], b[others]) for a, b in zip(want, got))
