@@ -7,6 +7,9 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
+#include <utility>
+
 #include "topk_ef.h"
 
 namespace tke {
@@ -21,6 +24,57 @@ inline bool aligned(const void* p, size_t a) { return (uintptr_t)p % a == 0; }
 // Bytes of an element of type t (0: no such type).
 inline size_t type_size(int32_t t) {
     return t == TOPK_EF_F32 ? 4 : t == TOPK_EF_BF16 || t == TOPK_EF_F16 ? 2 : 0;
+}
+
+// What an argument takes of the memory: `rows` of `width` bytes, `ld` bytes apart (ld >= width
+// where there are several).
+struct Region {
+    const void* p;
+    int64_t rows;
+    uint64_t ld, width;
+};
+inline Region vector_of(const void* p, int64_t n, size_t size) { return {p, 1, 0, (uint64_t)n * size}; }
+inline Region rows_of(const void* p, int64_t T, int64_t ld, int64_t n, size_t size) {
+    return {p, T, (uint64_t)ld * size, (uint64_t)n * size};
+}
+
+// Whether two arguments share a byte.  (Columns of one buffer do not.)
+inline bool meet(Region a, Region b) {
+    if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || !a.width || !b.width) return false;
+    if (a.rows > b.rows) std::swap(a, b);
+    uint64_t a0 = (uint64_t)(uintptr_t)a.p, b0 = (uint64_t)(uintptr_t)b.p;
+    if (a0 + (uint64_t)(a.rows - 1) * a.ld + a.width <= b0 || b0 + (uint64_t)(b.rows - 1) * b.ld + b.width <= a0)
+        return false;
+    if (a.rows > 1 && a.ld == b.ld) {
+        // the later one's first row lies in the other's as all of its rows do
+        if (a0 < b0) {
+            std::swap(a, b);
+            std::swap(a0, b0);
+        }
+        const uint64_t k = (a0 - b0) / b.ld, at = (a0 - b0) % b.ld;
+        return at < b.width || ((int64_t)k + 1 < b.rows && at + a.width > b.ld);
+    }
+    for (int64_t i = 0; i < a.rows; ++i) {
+        const uint64_t lo = a0 + (uint64_t)i * a.ld, hi = lo + a.width;
+        // the first of the other's rows that ends after lo
+        uint64_t j = 0;
+        if (lo >= b0 + b.width) j = b.rows == 1 ? 1 : (lo - b0 - b.width) / b.ld + 1;
+        if ((int64_t)j < b.rows && b0 + j * b.ld < hi) return true;
+    }
+    return false;
+}
+// ... and whether any of one list shares one with any of the other, or two of one list.
+inline bool any_meet(std::initializer_list<Region> a, std::initializer_list<Region> b) {
+    for (const Region& x : a)
+        for (const Region& y : b)
+            if (meet(x, y)) return true;
+    return false;
+}
+inline bool any_meet(std::initializer_list<Region> a) {
+    for (auto x = a.begin(); x != a.end(); ++x)
+        for (auto y = x + 1; y != a.end(); ++y)
+            if (meet(*x, *y)) return true;
+    return false;
 }
 
 // Calls f with a value of the C++ type of element type t.

@@ -59,6 +59,11 @@ int layer_norm(const void* x, int32_t x_type, int64_t ld_x, const void* weight,
         return TOPK_EF_ERR_INVALID_ARG;
     if (T > 0 && out == x && (sx != so || ld_x != ld_out)) return TOPK_EF_ERR_INVALID_ARG;
     if (T == 0) return TOPK_EF_OK;
+    const Region rx = rows_of(x, T, ld_x, D, sx), ro = rows_of(out, T, ld_out, D, so);
+    const Region rm = vector_of(mean, T, 4), rr = vector_of(rstd, T, 4);
+    if ((out != x && meet(ro, rx)) || any_meet({rm, rr}, {rx}) || any_meet({ro, rm, rr}) ||
+        any_meet({ro, rm, rr}, {vector_of(weight, D, type_size(weight_type)), vector_of(bias, D, type_size(bias_type))}))
+        return TOPK_EF_ERR_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     NormParams p = {};
     p.x = x;

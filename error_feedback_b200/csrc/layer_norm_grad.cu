@@ -99,6 +99,17 @@ int layer_norm_grad(const void* grad_out, int32_t grad_out_type, int64_t ld_grad
     if (T > 0 && ((grad_x == x && ld_grad_x != ld_x) ||
                   (grad_x == grad_out && (sx != sd || ld_grad_x != ld_grad_out))))
         return TOPK_EF_ERR_INVALID_ARG;
+    // (the column gradients are written after all is read)
+    const Region rx = rows_of(x, T, ld_x, D, sx), rd = rows_of(grad_out, T, ld_grad_out, D, sd);
+    const Region rg = rows_of(grad_x, T, ld_grad_x, D, sx);
+    const Region rw = vector_of(grad_weight, D, type_size(grad_weight_type));
+    const Region rb = vector_of(grad_bias, D, type_size(grad_bias_type));
+    const Region rs = vector_of(cols ? ws : nullptr, 1, need);
+    const Region rm = vector_of(mean, T, 4), rr = vector_of(rstd, T, 4);
+    const Region rk = vector_of(weight, D, type_size(weight_type));
+    if ((grad_x != x && meet(rg, rx)) || (grad_x != grad_out && meet(rg, rd)) ||
+        any_meet({rg, rw, rb, rs}) || any_meet({rg, rs}, {rm, rr, rk}) || any_meet({rs}, {rx, rd}))
+        return TOPK_EF_ERR_INVALID_ARG;
     if (cols && ws_bytes < need) return TOPK_EF_ERR_WORKSPACE;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     NormGradParams p = {};

@@ -146,6 +146,11 @@ int token_logprobs(const void* logits, int32_t logits_type, int64_t ld_logits, c
         !aligned(top_logprobs, 4))
         return TOPK_EF_ERR_INVALID_ARG;
     if (T > 0 && !pointer_ok(logits, sz)) return TOPK_EF_ERR_INVALID_ARG;
+    const std::initializer_list<Region> writes = {
+        vector_of(logprob, T, 4), vector_of(entropy, T, 4), vector_of(lse, T, 4), vector_of(top_ids, T * top, 4),
+        vector_of(top_logprobs, T * top, 4), vector_of(ws, 1, token_logprobs_workspace_bytes())};
+    if (any_meet(writes) || any_meet(writes, {rows_of(logits, T, ld_logits, V, sz), vector_of(ids, T, id_bytes)}))
+        return TOPK_EF_ERR_INVALID_ARG;
     if (ws_bytes < token_logprobs_workspace_bytes()) return TOPK_EF_ERR_WORKSPACE;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     LogprobParams p = {};
@@ -206,6 +211,12 @@ int token_logprobs_grad(const void* logits, int32_t logits_type, int64_t ld_logi
     if (T > 0 && (!pointer_ok(logits, sz) || !pointer_ok(grad_logits, so) || !pointer_ok(lse, 4)))
         return TOPK_EF_ERR_INVALID_ARG;
     if (T > 0 && grad_logits == logits && (sz != so || ld_logits != ld_grad_logits))
+        return TOPK_EF_ERR_INVALID_ARG;
+    const Region rz = rows_of(logits, T, ld_logits, V, sz), rg = rows_of(grad_logits, T, ld_grad_logits, V, so);
+    const Region rs = vector_of(ws, 1, token_logprobs_workspace_bytes());
+    if ((grad_logits != logits && meet(rg, rz)) || meet(rs, rz) || meet(rs, rg) ||
+        any_meet({rg, rs}, {vector_of(ids, T, id_bytes), vector_of(lse, T, 4), vector_of(entropy, T, 4),
+                            vector_of(grad_logprob, T, 4), vector_of(grad_entropy, T, 4)}))
         return TOPK_EF_ERR_INVALID_ARG;
     if (ws_bytes < token_logprobs_workspace_bytes()) return TOPK_EF_ERR_WORKSPACE;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -272,6 +283,15 @@ int distill_loss(const void* logits, int32_t logits_type, int64_t ld_logits,
     if (T > 0 && K > 0 && (!pointer_ok(teacher_ids, id_bytes) || !pointer_ok(teacher_logits, st_)))
         return TOPK_EF_ERR_INVALID_ARG;
     if (T > 0 && grad_logits == logits && (sz != so || ld_logits != ld_grad_logits))
+        return TOPK_EF_ERR_INVALID_ARG;
+    const Region rz = rows_of(logits, T, ld_logits, V, sz);
+    const Region rg = rows_of(grad_logits, T, ld_grad_logits, V, so);
+    const Region rl = vector_of(loss, T, 4), rw = vector_of(weight, T, 4);
+    const Region rs = vector_of(ws, 1, distill_loss_workspace_bytes());
+    // (a row's weight is read before its loss is written)
+    if ((grad_logits != logits && meet(rg, rz)) || (loss != weight && meet(rl, rw)) || any_meet({rg, rl, rs}) ||
+        any_meet({rl, rs}, {rz}) || any_meet({rg, rs}, {rw}) ||
+        any_meet({rg, rl, rs}, {vector_of(teacher_ids, T * K, id_bytes), vector_of(teacher_logits, T * K, st_)}))
         return TOPK_EF_ERR_INVALID_ARG;
     if (ws_bytes < distill_loss_workspace_bytes()) return TOPK_EF_ERR_WORKSPACE;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

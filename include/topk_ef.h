@@ -454,7 +454,8 @@ int muon_update(const void* grad, int32_t grad_type, int64_t ld_grad,
  * Rows on 16-byte boundaries with D a multiple of 8 take the vectorised path,
  * others an elementwise one (same formulas; sums in another order).
  * Infinities and NaNs make their row NaN, no other row.  There is no workspace.
- * Errors: TOPK_EF_ERR_INVALID_ARG (sizes, types, null or misaligned pointers),
+ * Errors: TOPK_EF_ERR_INVALID_ARG (sizes, types, null or misaligned pointers, an
+ * output that shares memory with another argument, but for what is said above),
  * TOPK_EF_ERR_CUDA.
  */
 int layer_norm(const void* x, int32_t x_type, int64_t ld_x, const void* weight,
@@ -481,7 +482,7 @@ size_t layer_norm_grad_workspace_bytes(int64_t T, int64_t D);
  *   grad_x     device, [T][ld_grad_x] of x_type; may be x or grad_out itself
  *              (same type size and stride), must not overlap them otherwise
  *   grad_weight, grad_bias  device, [D] of their types; either or both may be
- *              NULL
+ *              NULL; written after all other arguments are read
  *   ws         device workspace of >= layer_norm_grad_workspace_bytes(T, D);
  *              not used (may be NULL) if grad_weight and grad_bias are NULL
  * Otherwise as layer_norm.
@@ -529,7 +530,8 @@ size_t token_logprobs_workspace_bytes(void);
  * above.  An id outside [0, V), other than padding_idx, gives logprob 0 and
  * TOPK_EF_ERR_BAD_INPUT through topk_ef_last_device_status(ws); nothing outside
  * logits is read.
- * Errors: TOPK_EF_ERR_INVALID_ARG (sizes, types, null or misaligned pointers),
+ * Errors: TOPK_EF_ERR_INVALID_ARG (sizes, types, null or misaligned pointers,
+ * outputs or a workspace that share memory with another argument),
  * TOPK_EF_ERR_WORKSPACE, TOPK_EF_ERR_CUDA.
  */
 int token_logprobs(const void* logits, int32_t logits_type, int64_t ld_logits,
@@ -585,7 +587,7 @@ size_t distill_loss_workspace_bytes(void);
  *   teacher_logits  device, [T][K] of teacher_type; -Inf has q = 0
  *   K               0 .. 256
  *   weight          device, fp32[T], or NULL for 1
- *   loss            device, fp32[T], or NULL
+ *   loss            device, fp32[T], or NULL; may be weight itself
  *   grad_logits     device, [T][ld_grad_logits] of grad_logits_type, or NULL; as in
  *                   token_logprobs_grad
  *   ws              device workspace of >= distill_loss_workspace_bytes()
