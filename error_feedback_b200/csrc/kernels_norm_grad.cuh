@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(NL_THREADS) norm_grad_long_kernel(const NormGr
 
 // The column sums alone: a thread takes V columns, blocks in y take every NL_PARTS-th row, four
 // of them on their way at once.
-constexpr int NL_COLS = 128, NL_PARTS = 64, NL_AHEAD = 4;
+constexpr int NL_COLS = 128, NL_AHEAD = 4;
+constexpr int64_t NL_PARTS = 64;
 
 template <typename TX, typename TD, int V>
 __global__ void __launch_bounds__(NL_COLS) norm_cols_kernel(const NormGradParams p) {

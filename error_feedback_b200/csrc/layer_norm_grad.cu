@@ -14,11 +14,13 @@ using namespace tke;
 
 namespace {
 
-// Most blocks (partial rows of the column sums) of a gradient, and the least rows of each.
-constexpr int64_t NG_MAX_PARTS = SMS * 16, NG_ROWS = 4;
+// Blocks that have at least four rows each.
+int64_t row_parts(int64_t T) { return std::max<int64_t>(1, ceil_div64(T, 4)); }
 
-int64_t grad_parts(int64_t T) {
-    return std::min<int64_t>(NG_MAX_PARTS, std::max<int64_t>(1, ceil_div64(T, NG_ROWS)));
+// Most partial rows of the column sums: as many blocks as run at once, two of 256 threads an SM
+// or one of 512, at 128 registers each; those of the column kernel.
+int64_t grad_parts(int64_t T, int64_t D) {
+    return std::min(row_parts(T), D > NG_COLS_D ? NL_PARTS : D > 4096 ? SMS : (int64_t)2 * SMS);
 }
 
 template <typename TX, typename TD, int G, int V>
@@ -31,7 +33,7 @@ cudaError_t launch_grad(const NormGradParams& p, int32_t& parts, cudaStream_t st
     const int most = resident.get(norm_grad_kernel<TX, TD, G, V>, block, smem);
     if (!most) return cudaErrorLaunchOutOfResources;
     const int64_t rows = ceil_div64(p.T, block / G);
-    parts = (int32_t)std::min(std::min<int64_t>(most, rows), grad_parts(p.T));
+    parts = (int32_t)std::min(std::min<int64_t>(most, rows), G < 1024 ? grad_parts(p.T, p.D) : row_parts(p.T));
     trace_before(st, "norm_grad_kernel");
     const cudaError_t e =
         launch_pdl(norm_grad_kernel<TX, TD, G, V>, (unsigned)parts, block, st, p, smem);
@@ -42,7 +44,7 @@ cudaError_t launch_grad(const NormGradParams& p, int32_t& parts, cudaStream_t st
 // The column sums by themselves.
 template <typename TX, typename TD, int V>
 cudaError_t launch_cols(const NormGradParams& p, int32_t& parts, cudaStream_t st) {
-    parts = (int32_t)std::min<int64_t>(grad_parts(p.T), NL_PARTS);
+    parts = (int32_t)grad_parts(p.T, p.D);
     trace_before(st, "norm_cols_kernel");
     const cudaError_t e =
         launch_pdl(norm_cols_kernel<TX, TD, V>,
@@ -70,7 +72,7 @@ extern "C" {
 
 size_t layer_norm_grad_workspace_bytes(int64_t T, int64_t D) {
     if (!norm_sizes_ok(T, D)) return 0;
-    return align_up(sizeof(Ctrl)) + align_up((size_t)grad_parts(T) * 2 * (size_t)D * 4);
+    return align_up(sizeof(Ctrl)) + align_up((size_t)grad_parts(T, D) * 2 * (size_t)D * 4);
 }
 
 int layer_norm_grad(const void* grad_out, int32_t grad_out_type, int64_t ld_grad_out,
