@@ -913,7 +913,7 @@ def _id_list(ids, name: str, n: int, index: int):
 def _table(t, name: str, rows: int, cols: int, index: int, dtype):
     """Address of a contiguous [rows, cols] tensor on the device."""
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index \
-            and t.numel() == rows * cols and t.is_contiguous():
+            and t.dim() and t.shape[-1] == cols and t.numel() == rows * cols and t.is_contiguous():
         return t.data_ptr()
     raise ValueError(f"{name} must be a contiguous {dtype} tensor of [{rows}, {cols}] on cuda:{index}")
 
@@ -1041,6 +1041,8 @@ def distill_loss(logits, teacher_ids, teacher_logits, weight=None, scale=1.0, gr
     tp, tt = _vector(teacher_logits, "teacher_logits", T * K, at)
     if tp is None:
         raise ValueError("teacher_logits are needed")
+    if teacher_logits.dim() == 0 or teacher_logits.shape[-1] != K:
+        raise ValueError(f"teacher_logits must be [{T}, {K}]")
     wp = _f32(weight, "weight", T, at)
     lp = _f32(loss, "loss", T, at)
     _workspace_on(ws, at)
