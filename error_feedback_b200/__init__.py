@@ -728,14 +728,18 @@ def muon_update(grad, momentum=None, mu=0.95, nesterov=True, coefficients=MUON_C
 
 def _rows(t, name: str, D=None, index=None):
     """(2-d view, type code, row stride, device index, rows, columns) of [..., D]
-    rows on a CUDA device (`index`, if given) whose elements are contiguous."""
+    rows on a CUDA device (`index`, if given), one stride apart, whose elements
+    are contiguous."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() != 2:
         if t.dim() == 0:
             raise ValueError(f"{name} must have a dimension")
         n = t.shape[-1]
-        t = t.view(-1, n) if t.numel() else t.new_empty((t.shape[:-1].numel(), n))
+        try:
+            t = t.view(-1, n) if t.numel() else t.new_empty((t.shape[:-1].numel(), n))
+        except RuntimeError:
+            raise ValueError(f"the rows of {name} must be one stride apart") from None
     at, code = t.get_device(), _TYPE.get(t.dtype)
     if at < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -797,7 +801,7 @@ def _at(index: int, stream, call):
 def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=None, mean=None, rstd=None,
                stats=True, stream=None):
     """out = (x - mean) rstd weight + bias over the last dimension of x
-    ([..., D] with contiguous rows), mean and rstd = (variance + eps)^-1/2 of
+    ([..., D] with contiguous rows one stride apart), mean and rstd = (variance + eps)^-1/2 of
     each row in fp32, the result rounded once.  Types: float32, bfloat16 or
     float16 each (out: x's by default).  out may be x.  Returns (out, mean,
     rstd), mean and rstd float32 [rows] for layer_norm_grad (None with
@@ -920,7 +924,7 @@ def _table(t, name: str, rows: int, cols: int, index: int, dtype):
 
 def token_logprobs(logits, ids=None, scale=1.0, top=0, padding_idx=-1, logprob=None, entropy=None,
                    lse=None, top_ids=None, top_logprobs=None, ws=None, stream=None):
-    """Of each row of logits ([..., V], contiguous rows), with
+    """Of each row of logits ([..., V], contiguous rows one stride apart), with
     p = softmax(scale logits): (log p[ids], the entropy, the log of the sum, the ids
     of the `top` largest logits in descending order, the lower first among
     equal ones, and their log-probabilities).  The outputs are float32 [rows]

@@ -24,3 +24,23 @@ def test_tables_the_wrong_way_round():
     assert torch.equal(ef.distill_loss(z[1], ids[1], t[1])[0], want[1:2])
     got = ef.token_logprobs(z.view(2, 2, 30), top=6, top_ids=ids.view(2, 2, 6), top_logprobs=t.view(2, 2, 6))
     assert torch.equal(got[3].view(4, 6), ef.token_logprobs(z, top=6)[3])
+
+
+def test_rows_of_two_strides():
+    """The first positions of each sequence: rows that no single stride reaches are refused, as a
+    copy or one sequence at a time they work."""
+    z = torch.randn(3, 5, 40, device="cuda")
+    part = z[:, :-1]
+    lse = torch.zeros(12, device="cuda")
+    ids = torch.zeros(12, 2, dtype=torch.int32, device="cuda")
+    for call in (lambda: ef.token_logprobs(part), lambda: ef.layer_norm(part), lambda: ef.layer_norm(z[:, :4].clone(), out=part),
+                 lambda: ef.layer_norm_grad(part, z[:, :4].clone(), lse, lse),
+                 lambda: ef.token_logprobs_grad(part, lse.long(), lse, grad_logprob=lse),
+                 lambda: ef.distill_loss(part, ids, ids.float())):
+        with pytest.raises(ValueError):
+            call()
+    want = ef.token_logprobs(part.contiguous())[2].view(3, 4)
+    assert all(torch.equal(ef.token_logprobs(part[i])[2], want[i]) for i in range(3))
+    # one stride: every second row of each sequence, columns of a wider buffer
+    both = torch.randn(3, 4, 64, device="cuda")[:, ::2, 8:48]
+    assert torch.equal(ef.token_logprobs(both)[2], ef.token_logprobs(both.contiguous())[2])
