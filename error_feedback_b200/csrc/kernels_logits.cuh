@@ -34,7 +34,6 @@
 namespace tke {
 
 constexpr int LG_SMALL = 128;              // lines of a row that one warp takes
-constexpr int LG_MIDDLE = 256;             // ... and that four take
 constexpr int LG_LINE = 128;               // bytes of a line (a group of the top selection)
 constexpr int LG_FLIGHT = 4;               // 32-byte chunks that a thread loads at once
 constexpr float LG_START = -3.402823466e38f;     // m before any value
@@ -1101,7 +1100,8 @@ __device__ __forceinline__ float2 join_powers(float2 a, float2 b, float c) {
 // Bound by the bytes of z and dz, and for short rows by the chain of a row's steps: so
 // thread k keeps the teacher's k-th entry in registers, its softmax and the loss ride on the
 // barriers that the row's sums and the gradient need anyway (a barrier for each step: 70 us
-// instead of 65 for 4,096 rows of 8,192 bf16 by eight warps each; 43 by four).  For the
+// instead of 65 for 4,096 rows of 8,192 bf16 by eight warps each; by four 43, by one, which is what
+// it takes, 46, as rows of 16 KB go: 16,384 of them 153 and 122).  For the
 // gradient the row is read again, out of L2: 228 to 234 us for 2,048 x 131,072 bf16 (4.5 to 4.6
 // TB/s of z and dz), 115 for 4,096 x 32,768.  (Kept in shared memory instead, with the next row
 // copied behind it, by blocks of 8, 16 or 32 warps: 255 to 290, and 148.  Fewer blocks fit, and

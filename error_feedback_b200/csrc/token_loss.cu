@@ -32,14 +32,21 @@ int row_warps(int64_t T, int64_t lines) {
     if (T > (lines <= 64 ? 2 : 4) * ROUND && lines <= LG_SMALL) return 1;
     return lines <= 256 ? 4 : 8;
 }
-// token_logprobs' too, whose longer rows gain in their selection, if the last round is as full
-// by four as by eight: 4,096 x 131,072 bf16, top 20, 208.6 us by four and 220.2 by eight, 1,024
-// rows 66.9 and 60.8.  Short of 1,024 lines it need not be (2,048 x 64,000: 66.0 and 69.6); more
-// than 4,608 take shared memory from blocks of four (1,200 x 400,000: 222 and 184).
-int logprob_warps(int64_t T, int64_t lines) {
-    const bool even = ceil_div64(T, 2 * ROUND) * 2 == ceil_div64(T, ROUND);
-    if (T >= 2 * ROUND && lines > 256 && (lines <= 1024 || (lines <= 4608 && even))) return 4;
-    return row_warps(T, lines);
+// token_logprobs' too, where rows are many.  With a top, since others read while one selects, if
+// the last round is as full by four as by eight: 4,096 x 131,072 bf16, top 20, 209 us by four and
+// 233 by eight, 1,024 rows 68 and 61.  Short of 1,024 lines it need not be (2,048 x 64,000: 65 and
+// 70); more than 4,608 take shared memory from blocks of four (1,776 x 400,000: 288 and 254).
+// Without a top, when four of eight or eight of four run at once on an SM: rows of up to 960 lines
+// (16,384 x 32,000: 189 and 234; 1,333 x 20,000: 16.5 and 19.7; 900 x 30,000 fp32: 21.5 and 22.8),
+// longer ones if they are more than those blocks and the last round is as full (2,048 x 64,000: 50.0
+// and 52.3; 1,400 x 131,072: 72 and 66, 900: 54.5 and 45.6) or one of many (4,096 x 131,072: 178.4
+// and 181.6).
+int logprob_warps(int64_t T, int64_t lines, bool top) {
+    if (T < 2 * ROUND || lines <= 256) return row_warps(T, lines);
+    const int64_t at_once = top ? ROUND : SMS * 4;     // blocks of eight
+    const bool even = ceil_div64(T, 2 * at_once) * 2 == ceil_div64(T, at_once);
+    if (top) return lines <= 1024 || (lines <= 4608 && even) ? 4 : row_warps(T, lines);
+    return lines <= 960 || (T > 2 * at_once && (even || T > 5 * at_once)) ? 4 : row_warps(T, lines);
 }
 
 bool sizes_ok(int64_t T, int64_t V) {
@@ -168,7 +175,7 @@ int token_logprobs(const void* logits, int32_t logits_type, int64_t ld_logits, c
     p.padding = padding_idx;
     p.id64 = id_bytes == 8;
     p.top = top_ids || top_logprobs ? top : 0;
-    const int warps = logprob_warps(T, lines);
+    const int warps = logprob_warps(T, lines, p.top > 0);
     p.blocks = warps < 8 ? 1 : row_blocks(T, lines, ROUND);
     p.scan = T <= SCAN_IDS;
     p.scale = scale;
