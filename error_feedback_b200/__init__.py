@@ -916,9 +916,10 @@ def _id_list(ids, name: str, n: int, index: int):
 
 def _table(t, name: str, rows: int, cols: int, index: int, dtype):
     """Address of a contiguous [rows, cols] tensor on the device."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index \
-            and t.dim() and t.shape[-1] == cols and t.numel() == rows * cols and t.is_contiguous():
-        return t.data_ptr()
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+        s = t.shape
+        if s == (rows, cols) or (s and s[-1] == cols and t.numel() == rows * cols):
+            return t.data_ptr()
     raise ValueError(f"{name} must be a contiguous {dtype} tensor of [{rows}, {cols}] on cuda:{index}")
 
 
@@ -1038,14 +1039,15 @@ def distill_loss(logits, teacher_ids, teacher_logits, weight=None, scale=1.0, gr
     past V gives ERR_BAD_INPUT from topk_ef_last_device_status(ws) and counts
     nowhere."""
     z, zt, ldz, at, T, V = _rows(logits, "logits")
-    if not isinstance(teacher_ids, torch.Tensor) or teacher_ids.dim() == 0:
+    shape = teacher_ids.shape if isinstance(teacher_ids, torch.Tensor) else ()
+    if not shape:
         raise ValueError("teacher_ids must be [rows, K]")
-    K = teacher_ids.shape[-1]
+    K = shape[-1]
     ip, idb = _id_list(teacher_ids, "teacher_ids", T * K, at)
     tp, tt = _vector(teacher_logits, "teacher_logits", T * K, at)
     if tp is None:
         raise ValueError("teacher_logits are needed")
-    if teacher_logits.dim() == 0 or teacher_logits.shape[-1] != K:
+    if teacher_logits.shape != shape and teacher_logits.shape[-1:] != shape[-1:]:
         raise ValueError(f"teacher_logits must be [{T}, {K}]")
     wp = _f32(weight, "weight", T, at)
     lp = _f32(loss, "loss", T, at)

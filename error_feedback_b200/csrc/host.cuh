@@ -27,43 +27,41 @@ inline size_t type_size(int32_t t) {
 }
 
 // What an argument takes of the memory: `rows` of `width` bytes, `ld` bytes apart (ld >= width
-// where there are several).
+// where there are several), from lo to before hi.
 struct Region {
-    const void* p;
-    int64_t rows;
-    uint64_t ld, width;
+    uint64_t lo, hi, rows, ld, width;
+    Region(const void* p, int64_t n, uint64_t apart, uint64_t bytes)
+        : lo(0), hi(0), rows((uint64_t)n), ld(apart), width(bytes) {
+        if (!p || n <= 0 || !bytes) return;
+        lo = (uint64_t)(uintptr_t)p;
+        hi = lo + (rows - 1) * ld + width;
+    }
 };
 inline Region vector_of(const void* p, int64_t n, size_t size) { return {p, 1, 0, (uint64_t)n * size}; }
 inline Region rows_of(const void* p, int64_t T, int64_t ld, int64_t n, size_t size) {
     return {p, T, (uint64_t)ld * size, (uint64_t)n * size};
 }
 
-// Whether two arguments share a byte.  (Columns of one buffer do not.)
-inline bool meet(Region a, Region b) {
-    if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || !a.width || !b.width) return false;
+// Whether two arguments whose ranges overlap share a byte.  (Columns of one buffer do not.)
+inline bool rows_meet(Region a, Region b) {
     if (a.rows > b.rows) std::swap(a, b);
-    uint64_t a0 = (uint64_t)(uintptr_t)a.p, b0 = (uint64_t)(uintptr_t)b.p;
-    if (a0 + (uint64_t)(a.rows - 1) * a.ld + a.width <= b0 || b0 + (uint64_t)(b.rows - 1) * b.ld + b.width <= a0)
-        return false;
     if (a.rows > 1 && a.ld == b.ld) {
         // the later one's first row lies in the other's as all of its rows do
-        if (a0 < b0) {
-            std::swap(a, b);
-            std::swap(a0, b0);
-        }
-        const uint64_t k = (a0 - b0) / b.ld, at = (a0 - b0) % b.ld;
-        return at < b.width || ((int64_t)k + 1 < b.rows && at + a.width > b.ld);
+        if (a.lo < b.lo) std::swap(a, b);
+        const uint64_t k = (a.lo - b.lo) / b.ld, at = (a.lo - b.lo) % b.ld;
+        return at < b.width || (k + 1 < b.rows && at + a.width > b.ld);
     }
-    for (int64_t i = 0; i < a.rows; ++i) {
-        const uint64_t lo = a0 + (uint64_t)i * a.ld, hi = lo + a.width;
+    for (uint64_t i = 0, lo = a.lo; i < a.rows; ++i, lo += a.ld) {
         // the first of the other's rows that ends after lo
         uint64_t j = 0;
-        if (lo >= b0 + b.width) j = b.rows == 1 ? 1 : (lo - b0 - b.width) / b.ld + 1;
-        if ((int64_t)j < b.rows && b0 + j * b.ld < hi) return true;
+        if (lo >= b.lo + b.width) j = b.rows == 1 ? 1 : (lo - b.lo - b.width) / b.ld + 1;
+        if (j < b.rows && b.lo + j * b.ld < lo + a.width) return true;
     }
     return false;
 }
-// ... and whether any of one list shares one with any of the other, or two of one list.
+inline bool meet(const Region& a, const Region& b) { return a.lo < b.hi && b.lo < a.hi && rows_meet(a, b); }
+
+// Whether any of one list shares a byte with any of the other, or two of one list.
 inline bool any_meet(std::initializer_list<Region> a, std::initializer_list<Region> b) {
     for (const Region& x : a)
         for (const Region& y : b)

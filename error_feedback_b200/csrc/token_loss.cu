@@ -295,10 +295,11 @@ int distill_loss(const void* logits, int32_t logits_type, int64_t ld_logits,
     const Region rg = rows_of(grad_logits, T, ld_grad_logits, V, so);
     const Region rl = vector_of(loss, T, 4), rw = vector_of(weight, T, 4);
     const Region rs = vector_of(ws, 1, distill_loss_workspace_bytes());
+    const Region ri = vector_of(teacher_ids, T * K, id_bytes), rt = vector_of(teacher_logits, T * K, st_);
     // (a row's weight is read before its loss is written)
-    if ((grad_logits != logits && meet(rg, rz)) || (loss != weight && meet(rl, rw)) || any_meet({rg, rl, rs}) ||
-        any_meet({rl, rs}, {rz}) || any_meet({rg, rs}, {rw}) ||
-        any_meet({rg, rl, rs}, {vector_of(teacher_ids, T * K, id_bytes), vector_of(teacher_logits, T * K, st_)}))
+    if ((grad_logits != logits && meet(rg, rz)) || (loss != weight && meet(rl, rw)) || meet(rg, rl) || meet(rg, rs) ||
+        meet(rl, rs) || meet(rl, rz) || meet(rs, rz) || meet(rg, rw) || meet(rs, rw) || meet(rg, ri) ||
+        meet(rl, ri) || meet(rs, ri) || meet(rg, rt) || meet(rl, rt) || meet(rs, rt))
         return TOPK_EF_ERR_INVALID_ARG;
     if (ws_bytes < distill_loss_workspace_bytes()) return TOPK_EF_ERR_WORKSPACE;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
