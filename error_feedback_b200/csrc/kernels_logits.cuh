@@ -727,8 +727,8 @@ __device__ __forceinline__ void select_top(const LogprobParams& p, const LineRow
     }
 }
 
-// Bound by the bytes of z without the top (4,096 x 131,072 bf16: 173 to 182 us, 5.9 to 6.2 TB/s),
-// with it by the selection, during which a block reads nothing (top 64: 218 to 225 us, top 128:
+// Bound by the bytes of z without the top (4,096 x 131,072 bf16: 160 to 178 us, 6.0 to 6.7 TB/s),
+// with it by the selection, during which a block reads nothing (top 64: 207 to 226 us, top 128:
 // 250; short rows: 16,384 x 8,000, top 20, 86 us, top 100, 157, most of it the ranks).  One row
 // of 131,072 fp32 with its top 20, 16 blocks: 9 us, the chain of its steps.
 template <int W, bool TOP>

@@ -329,7 +329,7 @@ __device__ __forceinline__ f32x2 masked(f32x2 a, uint32_t mask, int e) {
 }
 
 // G threads a row.  Bound by the bytes of x and y: 16,384 x 4,096 bf16 in 50.5 to 53.5 us, 5.0 to
-// 5.3 TB/s; 30,011 x 1,001 fp32 to bf16, rows that start anywhere, in 44 to 47, 3.9 to 4.1 TB/s.
+// 5.3 TB/s; 30,011 x 1,001 fp32 to bf16, rows that start anywhere, in 44 to 47, 3.8 to 4.1 TB/s.
 template <typename TX, typename TY, int G, int V>
 __global__ void __launch_bounds__(NORM_BLOCK<G>, G <= 256 ? 3 : 1) norm_kernel(const NormParams p) {
     constexpr int E = NR_ELEMS, ROWS = NORM_BLOCK<G> / G, L = G < 32 ? G : 32, W = G < 64 ? 1 : G / 32;

@@ -477,7 +477,8 @@ size_t layer_norm_grad_workspace_bytes(int64_t T, int64_t D);
  * the flat buffer that topk_ef_compress and topk_ef_compress_batched read.
  *   grad_out   device, [T][ld_grad_out] of grad_out_type
  *   x          device, [T][ld_x] of x_type: layer_norm's input
- *   mean, rstd device, fp32[T]: layer_norm's
+ *   mean, rstd device, fp32[T]: layer_norm's (far from 0 the rounding of mean leaves
+ *              xh off by 2^-24 |mean| rstd, as x's own rounding does there)
  *   weight     as in layer_norm
  *   grad_x     device, [T][ld_grad_x] of x_type; may be x or grad_out itself
  *              (same type size and stride), must not overlap them otherwise
