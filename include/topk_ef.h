@@ -550,7 +550,8 @@ int token_logprobs(const void* logits, int32_t logits_type, int64_t ld_logits,
  * p_i is exp(scale * logits[t][i] - lse[t]) while |lse[t]| <= 128, where lse's own
  * error leaves it off by 2^-16 at most.  Rows further from 0 (an offset, a small
  * temperature, nothing left but a mask of finite value) are summed again with exact
- * differences, which takes about 1.6 times as long.
+ * differences by one block each, which takes about 1.6 times as long where rows are
+ * many, three times for one long row.
  *   lse        device, fp32[T], token_logprobs'
  *   entropy    device, fp32[T], token_logprobs'; needed with grad_entropy
  *   grad_logprob, grad_entropy  device, fp32[T]; NULL for 0
